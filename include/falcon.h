@@ -337,6 +337,161 @@ int falcon_chunk_bwd(const falcon_shape_t *shape,
                      falcon_state_t *d_init,
                      void *workspace, size_t workspace_bytes, void *stream);
 
+/* ======================================================================== */
+/* Operators around the mixer                                               */
+/* ======================================================================== */
+/* What stands next to Falcon in a stack of recurrent and attention layers: a
+ * gated linear recurrence with a vector state, the head norm and rotary
+ * positions of queries and keys, and causal softmax attention.  Memory, stream,
+ * error and thread conventions are those of the entry points above; packed
+ * sequences are given by the same device offsets (int32, non-decreasing, first
+ * 0, last at most the given token count; read on the device, not checked there).
+ * Tokens behind the last sequence are not written.  Gradients with
+ * respect to activations have the activations' dtype; those with respect to
+ * parameters and states are fp32.  Sums, states, softmax statistics and norms
+ * are fp32, and results are deterministic.  NaN and infinities propagate as in
+ * the formulas, within their own sequence only. */
+
+/* ---- Gated linear recurrence ---------------------------------------------
+ * Per sequence and channel, with lam_t = exp(log_lambda_t):
+ *   h_t = lam_t h_{t-1} + u_t,  u_t = x_t            (FALCON_SCAN_ADD)
+ *                               u_t = (1 - lam_t) x_t (FALCON_SCAN_MIX)
+ * There is no decay floor: log_lambda = -inf is an exact reset (lam = 0). */
+typedef enum { FALCON_SCAN_ADD = 0, FALCON_SCAN_MIX = 1 } falcon_scan_input_t;
+
+typedef struct {
+  int32_t dtype;   /* falcon_dtype_t of x, log_lambda, h and their gradients */
+  int32_t batch;   /* sequences, >= 1 */
+  int32_t seqlen;  /* steps of every sequence, >= 1; packed: all tokens (>= 1) */
+  int32_t width;   /* channels, a multiple of 8 */
+  int32_t input;   /* falcon_scan_input_t */
+} falcon_scan_shape_t;
+
+#define FALCON_SCAN_CHUNK 256   /* steps between the states the forward keeps */
+
+/* Bytes of workspace of falcon_scan_fwd and falcon_scan_bwd (the same for both);
+ * `packed` is nonzero for calls with cu_seqlens.  0 when the steps fit one chunk
+ * (then workspace may be NULL), and for invalid shapes. */
+size_t falcon_scan_workspace(const falcon_scan_shape_t *shape, int packed);
+
+/* The recurrence over T steps.
+ *   cu_seqlens   NULL: x, log_lambda, h are [B, T, D].  Otherwise [B + 1] offsets
+ *                and the arrays are [T, D], T = all tokens.
+ *   init         [B, D] fp32, or NULL for zeros.
+ *   final_state  [B, D] fp32, or NULL; may alias init.  An empty sequence's is
+ *                its initial state.
+ *   chunk_states [B, ceil(T / FALCON_SCAN_CHUNK), D] fp32 (packed: of the one
+ *                packed time axis, [1, ...]), or NULL: h after every chunk, for
+ *                the backward pass.
+ *   workspace    at least falcon_scan_workspace bytes, else FALCON_ERR_WORKSPACE;
+ *                needs no initialisation; calls sharing one race. */
+int falcon_scan_fwd(const falcon_scan_shape_t *shape, const int32_t *cu_seqlens, const void *x, const void *log_lambda,
+                    const float *init, float *final_state, void *h, float *chunk_states,
+                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradients of <d_h, h> + <d_final, final_state> with respect to x, log_lambda
+ * and init, from the chunk_states the forward wrote for the same arguments.
+ * d_final [B, D] fp32 or NULL (zeros); dx, dg like x; d_init [B, D] fp32 or NULL.
+ * Outputs must not alias inputs. */
+int falcon_scan_bwd(const falcon_scan_shape_t *shape, const int32_t *cu_seqlens, const void *x, const void *log_lambda,
+                    const float *init, const float *chunk_states, const void *d_h, const float *d_final,
+                    void *dx, void *dg, float *d_init, void *workspace, size_t workspace_bytes, void *stream);
+
+/* One step: x, log_lambda, h [B, D]; state [B, D] fp32 is updated in place.
+ * shape->seqlen is ignored. */
+int falcon_scan_step(const falcon_scan_shape_t *shape, const void *x, const void *log_lambda, float *state, void *h,
+                     void *stream);
+
+/* ---- Query / key norm with rotary positions ------------------------------
+ * For every head x (d entries) of q and k of every token:
+ *   z = x w / sqrt(mean(x^2) + eps)   (norm != 0; z = x otherwise)
+ * then the first `rot` entries turn in pairs (a, b) by the angle
+ * position * inv_freq[j], times rot_scale:
+ *   y_a = z_a cos - z_b sin,  y_b = z_b cos + z_a sin
+ * with a = j, b = j + rot / 2 (FALCON_ROPE_HALF) or a = 2 j, b = 2 j + 1
+ * (FALCON_ROPE_INTERLEAVED); the other entries are z.  Longer contexts scale
+ * inv_freq and rot_scale; the angle is formed in 64 bits. */
+typedef enum { FALCON_ROPE_HALF = 0, FALCON_ROPE_INTERLEAVED = 1 } falcon_rope_layout_t;
+
+typedef struct {
+  int32_t dtype;     /* falcon_dtype_t of q, k and the outputs */
+  int32_t tokens;    /* >= 1 */
+  int32_t heads_q;   /* >= 1 */
+  int32_t heads_k;   /* >= 1 */
+  int32_t d;         /* 32, 64 or 128 */
+  int32_t rot;       /* rotated entries: a multiple of 16, 0 .. d */
+  int32_t layout;    /* falcon_rope_layout_t */
+  int32_t norm;      /* 0 or 1 */
+  float eps;         /* finite, >= 0 */
+  float rot_scale;   /* finite */
+  int32_t grad_dtype; /* falcon_dtype_t of the backward's dq_out, dk_out: dtype, or FALCON_F32 */
+} falcon_qk_shape_t;
+
+/* [tokens, heads, d] with dense heads: the elements from one token to the next,
+ * a multiple of 16 bytes and at least heads * d.  So q and k may be views of
+ * one projection's output. */
+typedef struct { const void *data; int64_t token_stride; } falcon_heads_t;
+typedef struct { void *data; int64_t token_stride; } falcon_heads_out_t;
+
+/* q_out, k_out: may be q, k themselves (same pointer and stride), else must not
+ * overlap the inputs.  q_weight, k_weight: [d] fp32, or NULL for ones (ignored
+ * without norm).  positions: [tokens] int32.  inv_freq: [rot / 2] fp64, radians
+ * per position (NULL allowed when rot is 0). */
+int falcon_qk_norm_rope(const falcon_qk_shape_t *shape, falcon_heads_t q, falcon_heads_t k,
+                        const float *q_weight, const float *k_weight, const int32_t *positions,
+                        const double *inv_freq, falcon_heads_out_t q_out, falcon_heads_out_t k_out, void *stream);
+
+/* Bytes of workspace of the backward pass (the workgroups' weight-gradient
+ * sums); 0 without norm and for invalid shapes. */
+size_t falcon_qk_norm_rope_bwd_workspace(const falcon_qk_shape_t *shape);
+
+/* Gradients of <dq_out, q_out> + <dk_out, k_out>: dq, dk in dtype (without norm
+ * q and k are not read and may be {NULL, 0}); dq_weight, dk_weight [d] fp32 or
+ * NULL.  dq, dk may be dq_out, dk_out themselves when the dtypes agree. */
+int falcon_qk_norm_rope_bwd(const falcon_qk_shape_t *shape, falcon_heads_t q, falcon_heads_t k,
+                            const float *q_weight, const float *k_weight, const int32_t *positions,
+                            const double *inv_freq, falcon_heads_t dq_out, falcon_heads_t dk_out,
+                            falcon_heads_out_t dq, falcon_heads_out_t dk, float *dq_weight, float *dk_weight,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- Causal softmax attention --------------------------------------------
+ * The queries of a sequence are the last Lq of its Lk tokens: query i sees keys
+ * j <= i + Lk - Lq.  Query head h reads key head h / (heads_q / heads_k).
+ *   o_i = sum_j softmax_j(scale q_i . k_j) v_j,  lse_i = ln sum_j e^{scale q_i . k_j}
+ * A query that sees no key (Lq > Lk) has o = 0, lse = -inf and no gradients. */
+typedef struct {
+  int32_t dtype;     /* falcon_dtype_t of every array but lse */
+  int32_t batch;     /* sequences, >= 1 */
+  int32_t seqlen_q;  /* query tokens of every sequence, >= 1; packed: all of them */
+  int32_t seqlen_k;  /* key tokens of every sequence, >= 1; packed: all of them */
+  int32_t heads_q;   /* a multiple of heads_k */
+  int32_t heads_k;   /* >= 1 */
+  int32_t d;         /* 32, 64 or 128 */
+  float scale;       /* finite, > 0 */
+} falcon_attn_shape_t;
+
+/* Bytes of workspace of the forward: partial results, where the keys are split
+ * over workgroups because there are few queries; 0 where they are not (then
+ * workspace may be NULL).  `packed`: nonzero for calls with offsets. */
+size_t falcon_attn_fwd_workspace(const falcon_attn_shape_t *shape, int packed);
+
+/* q [tokens, heads_q, d], k, v [tokens, heads_k, d] (token strides as above),
+ * o dense [tokens, heads_q, d], lse [tokens, heads_q] fp32 or NULL.
+ *   cu_q, cu_k  both NULL (batch * seqlen tokens) or both [batch + 1] offsets. */
+int falcon_attn_fwd(const falcon_attn_shape_t *shape, const int32_t *cu_q, const int32_t *cu_k,
+                    falcon_heads_t q, falcon_heads_t k, falcon_heads_t v, void *o, float *lse,
+                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of the backward (one fp32 number per query and head). */
+size_t falcon_attn_bwd_workspace(const falcon_attn_shape_t *shape, int packed);
+
+/* Gradients of <d_o, o> with respect to q, k, v, from the forward's o and lse (o
+ * dense).  Outputs must not alias inputs. */
+int falcon_attn_bwd(const falcon_attn_shape_t *shape, const int32_t *cu_q, const int32_t *cu_k,
+                    falcon_heads_t q, falcon_heads_t k, falcon_heads_t v, const void *o, const float *lse,
+                    falcon_heads_t d_o, falcon_heads_out_t dq, falcon_heads_out_t dk, falcon_heads_out_t dv,
+                    void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

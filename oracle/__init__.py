@@ -33,3 +33,7 @@ from .falcon_oracle import (VARIANTS, recurrent, masked_parallel, chunked,
 
 __all__ = ["VARIANTS", "recurrent", "masked_parallel", "chunked", "decode_step", "phi",
            "recurrent_backward"]
+
+from . import layer_oracle as layer  # noqa: E402
+
+__all__.append("layer")

@@ -20,7 +20,8 @@ LIB = os.path.join(PKG, "libfalcon.so")
 
 SOURCES = ["falcon_abi.cpp", "falcon_fwd.hip", "falcon_fwd_pipe.hip", "falcon_fwd_split.hip", "falcon_fwd_split_win.hip",
            "falcon_fwd3.hip", "falcon_fwd_band.hip",
-           "falcon_step.hip", "falcon_bwd.hip", "falcon_bwd_rows.hip", "falcon_segment.hip", "falcon_static.hip"]
+           "falcon_step.hip", "falcon_bwd.hip", "falcon_bwd_rows.hip", "falcon_segment.hip", "falcon_static.hip",
+           "falcon_layer_abi.cpp", "falcon_scan.hip", "falcon_qk.hip", "falcon_attn.hip", "falcon_attn_bwd.hip"]
 ARCH = "gfx950"
 FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",

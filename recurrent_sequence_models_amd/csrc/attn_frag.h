@@ -1,0 +1,149 @@
+// Tiles and fragments of the attention kernels for gfx950 (wave64).
+//
+// Every product is a 32x32 MFMA tile.  With lane l, c = l % 32, h = l / 32:
+//   result (C-layout)   register i of 16 holds row 8 (i / 4) + 4 h + i % 4, column c
+//   left operand        8 values a lane: row c of the left matrix, 16 summed indices
+//   right operand       8 values a lane: column c of the right matrix, the same 16
+// Which summed index stands in which of the 16 slots (h, j) is free as long as both
+// operands agree, and two assignments are used:
+//   along a row of memory      slot (h, j) = index 8 h + j: 16 contiguous bytes (bf16)
+//   along a result's rows      slot (h, j) = row 4 h + j (j < 4), 8 + 4 h + j - 4 (j >= 4):
+//                              registers 8 b .. 8 b + 7 of a result are, rounded, the
+//                              right operand of a product that sums over its rows.
+// So a product of scores feeds the next product from registers, without LDS; the other
+// operand of that product is read from LDS by columns (transposing reads for bf16).
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include "mfma_frag.h"
+
+namespace falcon {
+
+typedef float f16v __attribute__((ext_vector_type(16)));
+
+template <typename T> struct Frag;
+template <> struct Frag<__bf16> { bf8 v; };
+template <> struct Frag<float> { f4 lo, hi; };
+
+__device__ __forceinline__ void mma(f16v &d, const Frag<__bf16> &a, const Frag<__bf16> &b) {
+  d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.v, b.v, d, 0, 0, 0);
+}
+__device__ __forceinline__ void mma(f16v &d, const Frag<float> &a, const Frag<float> &b) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) d = __builtin_amdgcn_mfma_f32_32x32x2f32(a.lo[j], b.lo[j], d, 0, 0, 0);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) d = __builtin_amdgcn_mfma_f32_32x32x2f32(a.hi[j], b.hi[j], d, 0, 0, 0);
+}
+__device__ __forceinline__ f16v zero16() {
+  f16v z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.f;
+  return z;
+}
+
+// Registers 8 b .. 8 b + 7 of a result as a right operand.  bf16: each value is rounded to
+// nearest even here, as the matrix product takes 8-bit mantissas; sums stay in fp32.
+template <typename T> __device__ __forceinline__ Frag<T> result_frag(const f16v &x, int b);
+template <> __device__ __forceinline__ Frag<__bf16> result_frag<__bf16>(const f16v &x, int b) {
+  Frag<__bf16> f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f.v[j] = (__bf16)x[8 * b + j];
+  return f;
+}
+template <> __device__ __forceinline__ Frag<float> result_frag<float>(const f16v &x, int b) {
+  return Frag<float>{f4{x[8 * b], x[8 * b + 1], x[8 * b + 2], x[8 * b + 3]},
+                     f4{x[8 * b + 4], x[8 * b + 5], x[8 * b + 6], x[8 * b + 7]}};
+}
+
+// 8 values along a row of global memory (this lane's row, 16-entry block b).
+__device__ __forceinline__ Frag<__bf16> global_frag(const __bf16 *row, int b, int h) {
+  return {*reinterpret_cast<const bf8 *>(row + 16 * b + 8 * h)};
+}
+__device__ __forceinline__ Frag<float> global_frag(const float *row, int b, int h) {
+  return {*reinterpret_cast<const f4 *>(row + 16 * b + 8 * h), *reinterpret_cast<const f4 *>(row + 16 * b + 8 * h + 4)};
+}
+__device__ __forceinline__ Frag<__bf16> zero_frag(__bf16) { return {__builtin_bit_cast(bf8, uint4{0, 0, 0, 0})}; }
+__device__ __forceinline__ Frag<float> zero_frag(float) { return {zero4(), zero4()}; }
+
+// A tile of ROWS rows of D entries in LDS, in 16-byte chunks.  Chunk c of a row stands at
+// place c ^ swizzle(row): reads of one chunk of 16 neighbouring rows, and column reads of
+// 4 rows x 4 chunks, then touch all banks evenly (unswizzled, rows of 256 bytes put a
+// column of chunks into one bank group).
+template <typename T, int D> struct Tile {
+  static constexpr int E = 16 / (int)sizeof(T);   // entries per chunk
+  static constexpr int CPR = D / E;               // chunks per row
+  static __device__ __forceinline__ int swizzle(int row) {
+    if constexpr (CPR >= 16) return ((row & 3) << 2) | ((row >> 2) & 3);
+    if constexpr (CPR == 8) return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+    return (row >> 2) & 3;
+  }
+  static __device__ __forceinline__ int place(int row, int chunk) { return row * CPR + (chunk ^ swizzle(row)); }
+
+  // Left operand: rows row0 + c, entries of 16-entry block b.
+  static __device__ __forceinline__ Frag<T> rows(const uint4 *t, int row0, int b, int lane) {
+    const int row = row0 + (lane & 31), h = lane >> 5;
+    if constexpr (sizeof(T) == 2) {
+      return {__builtin_bit_cast(bf8, t[place(row, 2 * b + h)])};
+    } else {
+      return {__builtin_bit_cast(f4, t[place(row, 4 * b + 2 * h)]), __builtin_bit_cast(f4, t[place(row, 4 * b + 2 * h + 1)])};
+    }
+  }
+  // Left operand, transposed: columns col0 + c, rows row0 .. row0 + 15 in the result-row slots.
+  static __device__ __forceinline__ Frag<T> cols(const uint4 *t, int row0, int col0, int lane) {
+    const int h = lane >> 5;
+    if constexpr (sizeof(T) == 2) {
+      // a transposing read: lane j of 16 names 4 entries of row j / 4, and gets column j of the 4 x 16 block
+      const int j = lane & 15, col = col0 + (lane & 16) + 4 * (j & 3);
+      Frag<__bf16> f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int row = row0 + 8 * k + 4 * h + (j >> 2);
+        const __bf16 *p = reinterpret_cast<const __bf16 *>(t + place(row, col / 8)) + (col & 7);
+        const bf4 v = ldtr(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f.v[4 * k + i] = v[i];
+      }
+      return f;
+    } else {
+      const int col = col0 + (lane & 31);
+      const float *p = reinterpret_cast<const float *>(t);
+      Frag<float> f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f.lo[i] = p[4 * place(row0 + 4 * h + i, col / 4) + (col & 3)];
+        f.hi[i] = p[4 * place(row0 + 8 + 4 * h + i, col / 4) + (col & 3)];
+      }
+      return f;
+    }
+  }
+};
+
+// Which sequence and tile a slot of a packed axis is.  Sequence n's tiles of `per` rows
+// (`mul` rows a token) start at slot cu[n] * mul / per + n, which no two sequences share
+// (floor(a) + ceil(b) <= floor(a + b) + 1) and which the device finds from cu alone.
+struct Slot { int n, tile; };
+__device__ __forceinline__ Slot find_slot(const int *cu, int N, int slot, int mul, int per) {
+  int lo = 0, hi = N - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((int)((int64_t)cu[mid] * mul / per) + mid <= slot) lo = mid; else hi = mid - 1;
+  }
+  return Slot{lo, slot - ((int)((int64_t)cu[lo] * mul / per) + lo)};
+}
+
+// max / sum with the lane 32 away.
+__device__ __forceinline__ float max_xor32(float x) { return fmaxf(x, __shfl_xor(x, 32)); }
+__device__ __forceinline__ float sum_xor32(float x) { return x + __shfl_xor(x, 32); }
+
+// 4 consecutive results; bf16: rounded to nearest even.
+__device__ __forceinline__ void store4(__bf16 *p, float a, float b, float c, float d) {
+  *reinterpret_cast<bf4 *>(p) = __builtin_convertvector(f4{a, b, c, d}, bf4);
+}
+__device__ __forceinline__ void store4(float *p, float a, float b, float c, float d) {
+  *reinterpret_cast<f4 *>(p) = f4{a, b, c, d};
+}
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+}  // namespace falcon

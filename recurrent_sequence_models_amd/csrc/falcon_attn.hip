@@ -1,0 +1,272 @@
+// Causal softmax attention with grouped heads over packed sequences, forward, on gfx950.
+//
+// Query i of a sequence sees keys j <= i + Lk - Lq (the queries are the last Lq of its Lk
+// tokens).  Per query head, with s_ij = scale q_i . k_j:
+//   o_i = sum_j e^{s_ij - m} v_j / l,  l = sum_j e^{s_ij - m},  lse_i = m + ln l,
+// in one pass over the keys with the running maximum m and sum l; a query that sees no key
+// gets o = 0 and lse = -inf.
+//
+// The rows of a tile are (token, head of the group) pairs, row r = token r / group, head
+// r % group: the heads that share a key head share its tiles, and a single token still
+// fills `group` rows.  A wave owns 32 rows and keeps their queries and results in
+// registers; tiles of 64 keys and values pass through LDS.  Scores are formed transposed,
+// S^T = K Q^T, so a lane holds 32 scores of one row: the softmax needs one exchange
+// between two lanes, its factors need none, and P^T is the right operand of
+// O^T = V^T P^T as it stands.
+//
+// Bound: MFMA (4 d flops per visible pair and head) for long prompts, with the
+// exponentials close behind; HBM (K and V once) for single tokens.
+#include "attn_frag.h"
+#include "layer_kernels.h"
+
+namespace falcon {
+namespace {
+
+constexpr int THR = 256, TM = 128;   // 4 waves of 32 rows
+
+template <typename T, int D> struct Fwd {
+  // Keys of a tile: 64, or 32 where two pairs of tiles of 64 would take over 64 KB of LDS
+  // (fp32 at d = 128).
+  static constexpr int TN = (sizeof(T) * D > 256) ? 32 : 64;
+  static constexpr int CH = TN * Tile<T, D>::CPR;          // chunks of a tile
+  static constexpr int PER = CH / THR;                     // chunks a thread moves
+  static constexpr int KB = TN / 32;
+  static_assert(PER * THR == CH, "every thread moves whole chunks");
+};
+
+template <typename T, int D> __global__ __launch_bounds__(THR) void attn_fwd(AttnArgs a) {
+  typedef Fwd<T, D> F;
+  typedef Tile<T, D> Ti;
+  constexpr int TN = F::TN, DB = D / 16, CB = D / 32;
+  __shared__ uint4 sk[2][F::CH], sv[2][F::CH];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 31, h = lane >> 5;
+
+  // key head fastest (a head stays on one die where 8 and hk divide one another), then the
+  // split of the keys, then the tiles
+  int id = blockIdx.x;
+  const int head = id % a.hk;
+  id /= a.hk;
+  const int split = id % a.splits;
+  int n, tile, q0, Lq, k0, Lk;
+  if (a.cuq) {
+    const Slot s = find_slot(a.cuq, a.n, id / a.splits, a.group, TM);
+    n = s.n;
+    q0 = a.cuq[n]; Lq = a.cuq[n + 1] - q0;
+    k0 = a.cuk[n]; Lk = a.cuk[n + 1] - k0;
+    tile = s.tile;
+  } else {
+    n = (id / a.splits) % a.n;
+    tile = (id / a.splits) / a.n;
+    q0 = n * a.Tq; Lq = a.Tq;
+    k0 = n * a.Tk; Lk = a.Tk;
+  }
+  const int64_t rows = (int64_t)Lq * a.group;
+  const int tiles = (int)((rows + TM - 1) / TM);
+  if (tile >= tiles) return;
+  tile = tiles - 1 - tile;                      // the tiles with the most keys start first
+
+  const int64_t r = (int64_t)tile * TM + wave * 32 + c;
+  const bool on = r < rows;
+  const int tok = (int)((on ? r : rows - 1) / a.group), hq = head * a.group + (int)((on ? r : rows - 1) % a.group);
+  const int lim = tok + Lk - Lq;                // the last key this row sees
+  const int first_lim = (int)(min((int64_t)tile * TM + wave * 32, rows - 1) / a.group) + Lk - Lq;
+  const int last_lim = (int)(min((int64_t)tile * TM + TM - 1, rows - 1) / a.group) + Lk - Lq;
+  const int keys = max(min(Lk, last_lim + 1), 0), ktiles = (keys + TN - 1) / TN;
+  const int kt0 = (int)((int64_t)ktiles * split / a.splits), kt1 = (int)((int64_t)ktiles * (split + 1) / a.splits);
+
+  const T *qrow = static_cast<const T *>(a.q) + (int64_t)(q0 + tok) * a.ldq + hq * D;
+  Frag<T> qf[DB];
+#pragma unroll
+  for (int b = 0; b < DB; ++b) qf[b] = global_frag(qrow, b, h);
+
+  // staging: rows past the sequence are zeros (their values must not be read: they are
+  // another sequence's or unset, and 0 times an infinity is not 0)
+  const T *kg = static_cast<const T *>(a.k) + (int64_t)k0 * a.ldk + head * D;
+  const T *vg = static_cast<const T *>(a.v) + (int64_t)k0 * a.ldv + head * D;
+  uint4 kr[F::PER], vr[F::PER];
+  auto fetch = [&](int kt) {
+#pragma unroll
+    for (int i = 0; i < F::PER; ++i) {
+      const int e = tid + i * THR, row = e / Ti::CPR, ch = e % Ti::CPR;
+      const int key = kt * TN + row;
+      kr[i] = vr[i] = uint4{0, 0, 0, 0};
+      if (key < Lk) {
+        kr[i] = *reinterpret_cast<const uint4 *>(kg + (int64_t)key * a.ldk + ch * Ti::E);
+        vr[i] = *reinterpret_cast<const uint4 *>(vg + (int64_t)key * a.ldv + ch * Ti::E);
+      }
+    }
+  };
+  auto stage = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < F::PER; ++i) {
+      const int e = tid + i * THR, row = e / Ti::CPR, ch = e % Ti::CPR;
+      sk[buf][Ti::place(row, ch)] = kr[i];
+      sv[buf][Ti::place(row, ch)] = vr[i];
+    }
+  };
+
+  f16v acc[CB];
+#pragma unroll
+  for (int b = 0; b < CB; ++b) acc[b] = zero16();
+  float m = -INFINITY, l = 0.f;                 // maximum in units of the raw scores; this lane's half of the sum
+  const float sc = a.scale * kLog2e;
+
+  if (kt0 < kt1) { fetch(kt0); stage(0); }
+  __syncthreads();
+  for (int kt = kt0; kt < kt1; ++kt) {
+    const int buf = (kt - kt0) & 1;
+    if (kt + 1 < kt1) fetch(kt + 1);
+    f16v s[F::KB];
+#pragma unroll
+    for (int kb = 0; kb < F::KB; ++kb) {
+      s[kb] = zero16();
+#pragma unroll
+      for (int b = 0; b < DB; ++b) mma(s[kb], Ti::rows(sk[buf], kb * 32, b, lane), qf[b]);
+    }
+    if (kt * TN + TN - 1 > first_lim) {         // the same for the whole wave
+#pragma unroll
+      for (int kb = 0; kb < F::KB; ++kb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (kt * TN + kb * 32 + 8 * (i / 4) + 4 * h + (i & 3) > lim) s[kb][i] = -INFINITY;
+    }
+    float top = m;
+#pragma unroll
+    for (int kb = 0; kb < F::KB; ++kb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kb][i]);
+    top = max_xor32(top);
+    const float shift = top == -INFINITY ? 0.f : top * sc;   // nothing seen yet: every weight is e^-inf = 0
+    if (__any(top > m)) {
+      const float f = __builtin_amdgcn_exp2f(m * sc - shift);
+      l *= f;
+#pragma unroll
+      for (int b = 0; b < CB; ++b) acc[b] *= f;
+      m = top;
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int kb = 0; kb < F::KB; ++kb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[kb][i] = __builtin_amdgcn_exp2f(fmaf(s[kb][i], sc, -shift));
+        sum += s[kb][i];
+      }
+    l += sum;
+#pragma unroll
+    for (int kb = 0; kb < F::KB; ++kb)
+#pragma unroll
+      for (int b16 = 0; b16 < 2; ++b16) {
+        const Frag<T> pf = result_frag<T>(s[kb], b16);
+#pragma unroll
+        for (int b = 0; b < CB; ++b) mma(acc[b], Ti::cols(sv[buf], kb * 32 + b16 * 16, b * 32, lane), pf);
+      }
+    if (kt + 1 < kt1) stage(buf ^ 1);
+    __syncthreads();
+  }
+  l = sum_xor32(l);
+  if (!on) return;
+  if (a.splits > 1) {   // unnormalised: [split][row of the packed axis and head][d], then (m, l)
+    const size_t nrow = (size_t)(a.cuq ? a.Tq : a.n * (int64_t)a.Tq) * a.hq;
+    const size_t at = split * nrow + (size_t)(q0 + tok) * a.hq + hq;
+    float *p = a.part + at * D;
+#pragma unroll
+    for (int b = 0; b < CB; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        store4(p + b * 32 + 2 * i + 4 * h, acc[b][i], acc[b][i + 1], acc[b][i + 2], acc[b][i + 3]);
+    if (h == 0) {
+      float *ml = a.part + a.splits * nrow * D + at * 2;
+      ml[0] = m * sc;
+      ml[1] = l;
+    }
+    return;
+  }
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // NaN stays NaN
+  T *out = static_cast<T *>(a.out) + ((int64_t)(q0 + tok) * a.hq + hq) * D;
+#pragma unroll
+  for (int b = 0; b < CB; ++b)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4)
+      store4(out + b * 32 + 2 * i + 4 * h, acc[b][i] * inv, acc[b][i + 1] * inv, acc[b][i + 2] * inv, acc[b][i + 3] * inv);
+  if (h == 0 && a.lse)
+    a.lse[(int64_t)(q0 + tok) * a.hq + hq] = l == 0.f ? -INFINITY : kLn2 * (m * sc + __builtin_amdgcn_logf(l));
+}
+
+// Joins the splits of a row: one thread per 4 entries.
+template <typename T, int D> __global__ __launch_bounds__(THR) void attn_join(AttnArgs a, size_t nrow, int last) {
+  constexpr int L = D / 4;
+  const size_t row = ((size_t)blockIdx.x * THR + threadIdx.x) / L;
+  const int e = (threadIdx.x % L) * 4;
+  if (row >= nrow) return;
+  if (a.cuq && row >= (size_t)a.cuq[last] * a.hq) return;    // behind the last sequence
+  const float *ml = a.part + a.splits * nrow * D;
+  float m = -INFINITY;
+  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, ml[(s * nrow + row) * 2]);
+  f4 o = zero4();
+  float l = 0.f;
+  for (int s = 0; s < a.splits; ++s) {
+    const float ms = ml[(s * nrow + row) * 2], ls = ml[(s * nrow + row) * 2 + 1];
+    if (ms == -INFINITY) continue;                            // nothing seen in this split
+    const float f = __builtin_amdgcn_exp2f(ms - m);
+    const f4 p = *reinterpret_cast<const f4 *>(a.part + (s * nrow + row) * D + e);
+    l = fmaf(f, ls, l);
+    o += f * p;
+  }
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+  store4(static_cast<T *>(a.out) + row * D + e, o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+  if (e == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : kLn2 * (m + __builtin_amdgcn_logf(l));
+}
+
+int64_t query_rows(const AttnArgs &a) { return a.cuq ? (int64_t)a.Tq : (int64_t)a.n * a.Tq; }
+
+// Tiles of the packed row axis, at most; exact without cu.
+int64_t slots_of(const AttnArgs &a) {
+  if (a.cuq) return (int64_t)a.Tq * a.group / TM + a.n;
+  return ((int64_t)a.Tq * a.group + TM - 1) / TM * a.n;
+}
+
+// Splits of the keys: only where the tiles leave compute units idle, and at least 4 tiles
+// of 64 keys (of the average sequence) a split, so that joining stays cheap beside them.
+int splits_of(const AttnArgs &a) {
+  const int64_t blocks = slots_of(a) * a.hk, keys = a.cuq ? a.Tk / a.n : a.Tk;
+  int64_t s = 512 / (blocks > 0 ? blocks : 1);
+  if (s > keys / 256) s = keys / 256;
+  if (s > 64) s = 64;
+  return s < 1 ? 1 : (int)s;
+}
+
+template <typename T, int D> hipError_t run(AttnArgs &a, hipStream_t s) {
+  const int64_t blocks = (int64_t)a.slots * a.hk * a.splits;
+  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((attn_fwd<T, D>), dim3((unsigned)blocks), dim3(THR), 0, s, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  const size_t nrow = (size_t)query_rows(a) * a.hq;
+  const size_t nb = (nrow * (D / 4) + THR - 1) / THR;
+  hipLaunchKernelGGL((attn_join<T, D>), dim3((unsigned)nb), dim3(THR), 0, s, a, nrow, a.n);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t attn_fwd_workspace(bool bf16, int d, const AttnArgs &a) {
+  (void)bf16;
+  const int s = splits_of(a);
+  return s == 1 ? 0 : (size_t)s * query_rows(a) * a.hq * (d + 2) * sizeof(float);
+}
+
+hipError_t launch_attn_fwd(bool bf16, int d, AttnArgs a, void *ws, hipStream_t s) {
+  a.slots = (int)slots_of(a);
+  a.splits = splits_of(a);
+  a.part = static_cast<float *>(ws);
+#define FALCON_ATTN(D_) \
+  if (d == D_) return bf16 ? run<__bf16, D_>(a, s) : run<float, D_>(a, s)
+  FALCON_ATTN(32);
+  FALCON_ATTN(64);
+  FALCON_ATTN(128);
+#undef FALCON_ATTN
+  return hipErrorInvalidValue;
+}
+
+}  // namespace falcon

@@ -23,7 +23,11 @@ WINDOWED = ("F3", "F3A")
 EXPORTS = ("falcon_abi_version", "falcon_status_string", "falcon_chunk_fwd_workspace",
            "falcon_chunk_fwd", "falcon_chunk_fwd_varlen_workspace", "falcon_chunk_fwd_varlen", "falcon_recurrent_step",
            "falcon_chunk_bwd_workspace", "falcon_chunk_bwd",
-           "falcon_chunk_fwd_segmented_workspace", "falcon_chunk_fwd_segmented", "falcon_chunk_fwd_static")
+           "falcon_chunk_fwd_segmented_workspace", "falcon_chunk_fwd_segmented", "falcon_chunk_fwd_static",
+           # the layer operators (layer.py)
+           "falcon_scan_workspace", "falcon_scan_fwd", "falcon_scan_bwd", "falcon_scan_step",
+           "falcon_qk_norm_rope", "falcon_qk_norm_rope_bwd_workspace", "falcon_qk_norm_rope_bwd",
+           "falcon_attn_fwd_workspace", "falcon_attn_fwd", "falcon_attn_bwd_workspace", "falcon_attn_bwd")
 
 
 class Shape(ctypes.Structure):
@@ -37,6 +41,29 @@ class Shape(ctypes.Structure):
 class State(ctypes.Structure):
     _fields_ = [("S", ctypes.c_void_p), ("x_prev", ctypes.c_void_p),
                 ("win_x", ctypes.c_void_p), ("win_v", ctypes.c_void_p)]
+
+
+class ScanShape(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("seqlen", ctypes.c_int32),
+                ("width", ctypes.c_int32), ("input", ctypes.c_int32)]
+
+
+class QkShape(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("tokens", ctypes.c_int32), ("heads_q", ctypes.c_int32),
+                ("heads_k", ctypes.c_int32), ("d", ctypes.c_int32), ("rot", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("norm", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("rot_scale", ctypes.c_float), ("grad_dtype", ctypes.c_int32)]
+
+
+class AttnShape(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("seqlen_q", ctypes.c_int32),
+                ("seqlen_k", ctypes.c_int32), ("heads_q", ctypes.c_int32), ("heads_k", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class Heads(ctypes.Structure):
+    """falcon_heads_t and falcon_heads_out_t: [tokens, heads, d] with a token stride in elements."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64)]
 
 
 class FalconError(RuntimeError):
@@ -83,6 +110,29 @@ def lib() -> ctypes.CDLL:
         L.falcon_chunk_bwd.restype = I
         L.falcon_chunk_bwd.argtypes = [P(Shape), V, V, V, V, V, P(State), V, V, V, V, V, V, V, V, P(State),
                                        V, S, V]
+        L.falcon_scan_workspace.restype = S
+        L.falcon_scan_workspace.argtypes = [P(ScanShape), I]
+        L.falcon_scan_fwd.restype = I
+        L.falcon_scan_fwd.argtypes = [P(ScanShape), V, V, V, V, V, V, V, V, S, V]
+        L.falcon_scan_bwd.restype = I
+        L.falcon_scan_bwd.argtypes = [P(ScanShape), V, V, V, V, V, V, V, V, V, V, V, S, V]
+        L.falcon_scan_step.restype = I
+        L.falcon_scan_step.argtypes = [P(ScanShape), V, V, V, V, V]
+        L.falcon_qk_norm_rope.restype = I
+        L.falcon_qk_norm_rope.argtypes = [P(QkShape), Heads, Heads, V, V, V, V, Heads, Heads, V]
+        L.falcon_qk_norm_rope_bwd_workspace.restype = S
+        L.falcon_qk_norm_rope_bwd_workspace.argtypes = [P(QkShape)]
+        L.falcon_qk_norm_rope_bwd.restype = I
+        L.falcon_qk_norm_rope_bwd.argtypes = [P(QkShape), Heads, Heads, V, V, V, V, Heads, Heads, Heads, Heads, V, V,
+                                              V, S, V]
+        L.falcon_attn_fwd_workspace.restype = S
+        L.falcon_attn_fwd_workspace.argtypes = [P(AttnShape), I]
+        L.falcon_attn_fwd.restype = I
+        L.falcon_attn_fwd.argtypes = [P(AttnShape), V, V, Heads, Heads, Heads, V, V, V, S, V]
+        L.falcon_attn_bwd_workspace.restype = S
+        L.falcon_attn_bwd_workspace.argtypes = [P(AttnShape), I]
+        L.falcon_attn_bwd.restype = I
+        L.falcon_attn_bwd.argtypes = [P(AttnShape), V, V, Heads, Heads, Heads, V, V, Heads, Heads, Heads, Heads, V, S, V]
         _LIB = L
     return _LIB
 

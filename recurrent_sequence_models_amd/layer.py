@@ -1,0 +1,412 @@
+"""Python binding of the layer operators of libfalcon (include/falcon.h): the gated
+linear recurrence, the query / key norm with rotary positions, and causal attention.
+
+Argument marshalling only, as falcon.py: every step of the computation runs in the HIP
+kernels.  A call runs on the device of its tensors; ``stream`` (default: that device's
+current stream) is a torch stream of the same device, and what the call allocates
+belongs to it.
+"""
+
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import math
+
+from .falcon import (DTYPES, OK, AttnShape, FalconError, Heads, QkShape, ScanShape, _check_tensor, _ptr, _stream, lib)
+
+SCAN_CHUNK = 256   # FALCON_SCAN_CHUNK
+LAYOUTS = {"half": 0, "interleaved": 1}
+_HERE = contextlib.nullcontext()
+
+
+def _dtype(name, t):
+    import torch
+    dt = {torch.float32: "fp32", torch.bfloat16: "bf16"}.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{name} must be float32 or bfloat16")
+    return DTYPES[dt]
+
+
+def _device(name, t):
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must live on a GPU")
+    return t.device
+
+
+def _on(dev, stream):
+    """The context of a call: its device current, allocations on the stream it runs on."""
+    import torch
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream: must belong to {dev}")
+        return torch.cuda.stream(stream)
+    return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _done(status, where):
+    if status != OK:
+        raise FalconError(status, where)
+
+
+def _workspace(need, given, dev):
+    """(tensor or None, bytes) of a call that needs ``need`` bytes."""
+    import torch
+    if given is None:
+        return (torch.empty(need, dtype=torch.uint8, device=dev) if need else None), need
+    _check_tensor("workspace", given, torch.uint8, (given.numel(),), dev)
+    return given, given.numel()
+
+
+def _offsets(name, cu, dev):
+    import torch
+    if cu.dim() != 1 or cu.numel() < 2:
+        raise ValueError(f"{name}: shape {tuple(cu.shape)}, expected (sequences + 1,)")
+    _check_tensor(name, cu, torch.int32, tuple(cu.shape), dev)
+    return cu.numel() - 1
+
+
+# ---- Gated linear recurrence ----------------------------------------------------
+
+def _scan_shape(x, log_lambda, cu_seqlens, mix):
+    dt, dev = _dtype("x", x), _device("x", x)
+    if x.dim() != (3 if cu_seqlens is None else 2):
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected " + ("[B, T, D]" if cu_seqlens is None else "[total, D]"))
+    _check_tensor("x", x, x.dtype, x.shape, dev)
+    _check_tensor("log_lambda", log_lambda, x.dtype, x.shape, dev)
+    T, D = x.shape[-2:]
+    n = x.shape[0] if cu_seqlens is None else _offsets("cu_seqlens", cu_seqlens, dev)
+    return ScanShape(dt, n, T, D, 1 if mix else 0), n, T, D, dev
+
+
+def _states_shape(x, cu_seqlens):
+    rows, T = (x.shape[0] if cu_seqlens is None else 1), x.shape[-2]
+    return rows, -(-T // SCAN_CHUNK), x.shape[-1]
+
+
+def gated_scan(x, log_lambda, *, cu_seqlens=None, mix=False, init=None, final=True, chunk_states=False, out=None,
+               workspace=None, stream=None):
+    """falcon_scan_fwd on torch tensors: h_t = lam_t h_{t-1} + u_t per channel, with
+    lam = exp(log_lambda) and u = x, or (1 - lam) x with ``mix``.
+
+    x, log_lambda [B,T,D] (float32 or bfloat16, D a multiple of 8), or [total,D] with
+    ``cu_seqlens``, an int32 device tensor [N+1] of token offsets.  ``init``: None or
+    [N,D] float32.  ``final``: True (allocate), a [N,D] float32 tensor to write (may be
+    ``init``), or False.  ``chunk_states``: whether to keep what gated_scan_bwd needs.
+    Tokens behind cu_seqlens[N] are not written.  Returns (h, final, chunk_states)."""
+    import torch
+    shape, n, T, D, dev = _scan_shape(x, log_lambda, cu_seqlens, mix)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty_like(x)
+        _check_tensor("h", out, x.dtype, x.shape, dev)
+        if final is True:
+            final = torch.empty(n, D, dtype=torch.float32, device=dev)
+        elif final is False:
+            final = None
+        for name, t in (("init", init), ("final", final)):
+            if t is not None:
+                _check_tensor(name, t, torch.float32, (n, D), dev)
+        states = torch.empty(_states_shape(x, cu_seqlens), dtype=torch.float32, device=dev) if chunk_states else None
+        L = lib()
+        ws, nbytes = _workspace(L.falcon_scan_workspace(ctypes.byref(shape), cu_seqlens is not None)
+                                if T > SCAN_CHUNK else 0, workspace, dev)
+        _done(L.falcon_scan_fwd(ctypes.byref(shape), _ptr(cu_seqlens), _ptr(x), _ptr(log_lambda), _ptr(init),
+                                _ptr(final), _ptr(out), _ptr(states), _ptr(ws), nbytes, _stream(stream)),
+              "falcon_scan_fwd")
+    return out, final, states
+
+
+def gated_scan_bwd(x, log_lambda, dh, chunk_states, *, cu_seqlens=None, mix=False, init=None, d_final=None,
+                   d_init=True, out=None, workspace=None, stream=None):
+    """falcon_scan_bwd on torch tensors: gradients of <dh, h> + <d_final, final>.
+
+    ``chunk_states`` is what ``gated_scan(..., chunk_states=True)`` returned for the same
+    arguments.  dh has the dtype and shape of x; ``d_final`` is None or [N,D] float32.
+    ``d_init``: True (allocate), a [N,D] float32 tensor, or False.  ``out``: None or a
+    dict of preallocated dx, dg.  Returns dict(dx, dg, d_init)."""
+    import torch
+    shape, n, T, D, dev = _scan_shape(x, log_lambda, cu_seqlens, mix)
+    _check_tensor("dh", dh, x.dtype, x.shape, dev)
+    _check_tensor("chunk_states", chunk_states, torch.float32, _states_shape(x, cu_seqlens), dev)
+    with _on(dev, stream):
+        if out is None:
+            out = dict(dx=torch.empty_like(x), dg=torch.empty_like(x))
+        for name in ("dx", "dg"):
+            _check_tensor(name, out[name], x.dtype, x.shape, dev)
+        if d_init is True:
+            d_init = torch.empty(n, D, dtype=torch.float32, device=dev)
+        elif d_init is False:
+            d_init = None
+        for name, t in (("init", init), ("d_final", d_final), ("d_init", d_init)):
+            if t is not None:
+                _check_tensor(name, t, torch.float32, (n, D), dev)
+        L = lib()
+        ws, nbytes = _workspace(L.falcon_scan_workspace(ctypes.byref(shape), cu_seqlens is not None)
+                                if T > SCAN_CHUNK else 0, workspace, dev)
+        _done(L.falcon_scan_bwd(ctypes.byref(shape), _ptr(cu_seqlens), _ptr(x), _ptr(log_lambda), _ptr(init),
+                                _ptr(chunk_states), _ptr(dh), _ptr(d_final), _ptr(out["dx"]), _ptr(out["dg"]),
+                                _ptr(d_init), _ptr(ws), nbytes, _stream(stream)), "falcon_scan_bwd")
+    return dict(dx=out["dx"], dg=out["dg"], d_init=d_init)
+
+
+def gated_scan_step(x, log_lambda, state, *, mix=False, out=None, stream=None):
+    """falcon_scan_step: one token; x, log_lambda [B,D], ``state`` [B,D] float32 updated
+    in place.  Returns h [B,D] in the dtype of x."""
+    import torch
+    dt, dev = _dtype("x", x), _device("x", x)
+    if x.dim() != 2:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected [B, D]")
+    B, D = x.shape
+    _check_tensor("x", x, x.dtype, (B, D), dev)
+    _check_tensor("log_lambda", log_lambda, x.dtype, (B, D), dev)
+    _check_tensor("state", state, torch.float32, (B, D), dev)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty_like(x)
+        _check_tensor("h", out, x.dtype, (B, D), dev)
+        shape = ScanShape(dt, B, 1, D, 1 if mix else 0)
+        _done(lib().falcon_scan_step(ctypes.byref(shape), _ptr(x), _ptr(log_lambda), _ptr(state), _ptr(out),
+                                     _stream(stream)), "falcon_scan_step")
+    return out
+
+
+# ---- Heads ------------------------------------------------------------------------
+
+def _heads(name, t, dtype, dev, lead=None, heads=None, d=None):
+    """falcon_heads_t of t [..., heads, d]: dense heads, tokens one stride apart (views
+    of a wider projection are taken as they are)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.dim() < 3:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [..., heads, d]")
+    if lead is not None and tuple(t.shape) != (*lead, heads, d):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(*lead, heads, d)}")
+    if t.device != dev:
+        raise ValueError(f"{name}: must live on {dev}")
+    *sizes, H, D = t.shape
+    *strides, sh, sd = t.stride()
+    step = H * D                       # the distance of two tokens, if there are two
+    want = None
+    ok = (sd == 1 or D == 1) and (sh == D or H == 1)
+    for n, s in zip(reversed(sizes), reversed(strides)):
+        if n == 1:
+            continue
+        if want is None:
+            step = s
+            want = s
+        ok = ok and s == want
+        want = want * n
+    if not ok or step < H * D:
+        raise ValueError(f"{name}: heads must be dense and tokens one stride apart")
+    if (step * t.element_size()) % 16:
+        raise ValueError(f"{name}: the distance of two tokens must be a multiple of 16 bytes")
+    return Heads(t.data_ptr(), step)
+
+
+# ---- Query / key norm with rotary positions -----------------------------------------
+
+def rope_frequencies(rot, base=10000.0, *, scaling=None, factor=1.0, original_length=None, beta_fast=32.0,
+                     beta_slow=1.0, device=None):
+    """(inv_freq, rot_scale) of a rotation of ``rot`` entries: inv_freq [rot / 2] float64
+    radians per position, base^(-2 j / rot), scaled for contexts ``factor`` times as long:
+
+    - None: as they are;
+    - "linear": positions interpolated, every frequency divided by the factor;
+    - "ntk": the base raised to base factor^(rot / (rot - 2)), which leaves the fastest
+      pair as it is and divides the slowest by the factor;
+    - "parts": pairs that turn more than ``beta_fast`` times in ``original_length`` tokens
+      are kept, those that turn less than ``beta_slow`` times are divided by the factor,
+      with a ramp over the pairs between; the rotated part is scaled by
+      0.1 ln(factor) + 1 (a factor of at most 1: by 1)."""
+    import torch
+    if rot < 2 or rot % 2:
+        raise ValueError(f"rot: {rot}, expected a positive even number")
+    if not base > 0 or not factor > 0:
+        raise ValueError("base and factor must be positive")
+    j = torch.arange(rot // 2, dtype=torch.float64)
+    scale = 1.0
+    if scaling == "ntk":
+        if rot == 2:
+            raise ValueError("scaling 'ntk' needs rot > 2")
+        base = base * factor ** (rot / (rot - 2))
+    freq = base ** (-2.0 * j / rot)
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "parts":
+        if not original_length or base == 1:
+            raise ValueError("scaling 'parts' needs original_length and a base other than 1")
+
+        def pair(turns):   # the (fractional) pair that turns so often in original_length tokens
+            return rot * math.log(original_length / (2 * math.pi * turns)) / (2 * math.log(base))
+
+        low = min(max(math.floor(pair(beta_fast)), 0), rot // 2 - 1)
+        high = min(max(math.ceil(pair(beta_slow)), 0), rot // 2 - 1)
+        ramp = ((j - low) / max(high - low, 1e-3)).clamp(0, 1)
+        freq = freq * (1 - ramp) + freq / factor * ramp
+        scale = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+    elif scaling not in (None, "ntk"):
+        raise ValueError(f"scaling: {scaling!r}, expected None, 'linear', 'ntk' or 'parts'")
+    return freq.to(device) if device is not None else freq, scale
+
+
+def _qk_shape(q, k, positions, inv_freq, q_weight, k_weight, norm, eps, layout, rot_scale, grad_dtype):
+    import torch
+    if q.dim() < 3 or k.dim() < 3 or q.shape[:-2] != k.shape[:-2] or q.shape[-1] != k.shape[-1]:
+        raise ValueError(f"q, k: shapes {tuple(q.shape)}, {tuple(k.shape)}, expected [..., heads, d] of the same tokens")
+    if layout not in LAYOUTS:
+        raise ValueError(f"layout: {layout!r}, expected 'half' or 'interleaved'")
+    dt, dev = _dtype("q", q), _device("q", q)
+    lead, d = q.shape[:-2], q.shape[-1]
+    tokens = math.prod(lead)
+    _check_tensor("positions", positions, torch.int32, lead, dev)
+    rot = 0
+    if inv_freq is not None:
+        _check_tensor("inv_freq", inv_freq, torch.float64, (inv_freq.numel(),), dev)
+        rot = 2 * inv_freq.numel()
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            if not norm:
+                raise ValueError(f"{name}: weights belong to the norm")
+            _check_tensor(name, w, torch.float32, (d,), dev)
+    shape = QkShape(dt, tokens, q.shape[-2], k.shape[-2], d, rot, LAYOUTS[layout], 1 if norm else 0, eps, rot_scale,
+                    dt if grad_dtype is None else grad_dtype)
+    return shape, lead, d, dev
+
+
+def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, norm=True, eps=1e-6, layout="half",
+                 rot_scale=1.0, out=None, stream=None):
+    """falcon_qk_norm_rope on torch tensors: every head of q and k divided by its root
+    mean square (``norm``; times its weight), then its first 2 * len(inv_freq) entries
+    turned by positions * inv_freq.
+
+    q [..., Hq, d], k [..., Hk, d] (float32 or bfloat16; views of a projection's output
+    with dense heads will do), positions [...] int32, inv_freq [rot / 2] float64 (None:
+    no rotation), weights [d] float32.  ``layout``: "half" (pairs j, j + rot / 2) or
+    "interleaved" (2 j, 2 j + 1).  ``out``: None or (q_out, k_out), which may be q and k.
+    Returns (q_out, k_out)."""
+    import torch
+    shape, lead, d, dev = _qk_shape(q, k, positions, inv_freq, q_weight, k_weight, norm, eps, layout, rot_scale, None)
+    hq, hk = _heads("q", q, q.dtype, dev), _heads("k", k, q.dtype, dev)
+    with _on(dev, stream):
+        if out is None:
+            out = (torch.empty(q.shape, dtype=q.dtype, device=dev), torch.empty(k.shape, dtype=q.dtype, device=dev))
+        oq = _heads("q_out", out[0], q.dtype, dev, lead, q.shape[-2], d)
+        ok = _heads("k_out", out[1], q.dtype, dev, lead, k.shape[-2], d)
+        _done(lib().falcon_qk_norm_rope(ctypes.byref(shape), hq, hk, _ptr(q_weight), _ptr(k_weight), _ptr(positions),
+                                        _ptr(inv_freq), oq, ok, _stream(stream)), "falcon_qk_norm_rope")
+    return out[0], out[1]
+
+
+def qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, *, q_weight=None, k_weight=None, norm=True, eps=1e-6,
+                     layout="half", rot_scale=1.0, out=None, workspace=None, stream=None):
+    """falcon_qk_norm_rope_bwd on torch tensors: gradients of <dq_out, q_out> +
+    <dk_out, k_out> for ``qk_norm_rope`` of the same arguments.
+
+    dq_out, dk_out are both in the dtype of q or both float32 (as chunk_bwd gives them).
+    ``out``: None or a dict of preallocated dq, dk.  Returns dict(dq, dk, dq_weight,
+    dk_weight): dq, dk in the dtype of q, the weights' gradients [d] float32 (None where
+    no weight was given)."""
+    import torch
+    grad = _dtype("dq_out", dq_out)
+    shape, lead, d, dev = _qk_shape(q, k, positions, inv_freq, q_weight, k_weight, norm, eps, layout, rot_scale, grad)
+    hq, hk = _heads("q", q, q.dtype, dev), _heads("k", k, q.dtype, dev)
+    gq = _heads("dq_out", dq_out, dq_out.dtype, dev, lead, q.shape[-2], d)
+    gk = _heads("dk_out", dk_out, dq_out.dtype, dev, lead, k.shape[-2], d)
+    with _on(dev, stream):
+        if out is None:
+            out = dict(dq=torch.empty(q.shape, dtype=q.dtype, device=dev),
+                       dk=torch.empty(k.shape, dtype=q.dtype, device=dev))
+        oq = _heads("dq", out["dq"], q.dtype, dev, lead, q.shape[-2], d)
+        ok = _heads("dk", out["dk"], q.dtype, dev, lead, k.shape[-2], d)
+        dwq = torch.empty(d, dtype=torch.float32, device=dev) if q_weight is not None else None
+        dwk = torch.empty(d, dtype=torch.float32, device=dev) if k_weight is not None else None
+        L = lib()
+        some = dwq is not None or dwk is not None
+        ws, nbytes = _workspace(L.falcon_qk_norm_rope_bwd_workspace(ctypes.byref(shape)) if some else 0, workspace, dev)
+        _done(L.falcon_qk_norm_rope_bwd(ctypes.byref(shape), hq, hk, _ptr(q_weight), _ptr(k_weight), _ptr(positions),
+                                        _ptr(inv_freq), gq, gk, oq, ok, _ptr(dwq), _ptr(dwk), _ptr(ws), nbytes,
+                                        _stream(stream)), "falcon_qk_norm_rope_bwd")
+    return dict(dq=out["dq"], dk=out["dk"], dq_weight=dwq, dk_weight=dwk)
+
+
+# ---- Causal attention -----------------------------------------------------------------
+
+def _attn_shape(q, k, v, cu_seqlens, cu_seqlens_k, scale):
+    dt, dev = _dtype("q", q), _device("q", q)
+    dims = 4 if cu_seqlens is None else 3
+    if cu_seqlens is None and cu_seqlens_k is not None:
+        raise ValueError("cu_seqlens_k: given without cu_seqlens")
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t.dim() != dims:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected " +
+                             ("[B, T, heads, d]" if cu_seqlens is None else "[total, heads, d]"))
+    d = q.shape[-1]
+    if cu_seqlens is None:
+        n, tq, tk = q.shape[0], q.shape[1], k.shape[1]
+        klead = (n, tk)
+    else:
+        if cu_seqlens_k is None:
+            cu_seqlens_k = cu_seqlens
+            if k.shape[0] != q.shape[0]:
+                raise ValueError(f"k: {k.shape[0]} tokens, expected {q.shape[0]} (without cu_seqlens_k)")
+        n = _offsets("cu_seqlens", cu_seqlens, dev)
+        if _offsets("cu_seqlens_k", cu_seqlens_k, dev) != n:
+            raise ValueError("cu_seqlens and cu_seqlens_k differ in length")
+        tq, tk = q.shape[0], k.shape[0]
+        klead = (tk,)
+    hq = _heads("q", q, q.dtype, dev)
+    hk = _heads("k", k, q.dtype, dev, klead, k.shape[-2], d)
+    hv = _heads("v", v, q.dtype, dev, klead, k.shape[-2], d)
+    shape = AttnShape(dt, n, tq, tk, q.shape[-2], k.shape[-2], d, d ** -0.5 if scale is None else scale)
+    return shape, cu_seqlens_k, hq, hk, hv, dev
+
+
+def attention_fwd(q, k, v, *, cu_seqlens=None, cu_seqlens_k=None, scale=None, lse=True, out=None, workspace=None,
+                  stream=None):
+    """falcon_attn_fwd on torch tensors: causal softmax attention with grouped heads.
+
+    q [B,Tq,Hq,d], k, v [B,Tk,Hk,d] (float32 or bfloat16, Hq a multiple of Hk; views with
+    dense heads will do), or packed [total,H,d] with ``cu_seqlens`` (and ``cu_seqlens_k``
+    where a sequence's keys are more than its queries, which are then its last tokens),
+    int32 device tensors [N+1].  ``scale``: default d^-1/2.  ``lse``: whether to return
+    the log-sum-exp of every row (attention_bwd needs it).
+    Returns (o, lse): o like q and dense, lse [..., Hq] float32 or None."""
+    import torch
+    shape, cuk, hq, hk, hv, dev = _attn_shape(q, k, v, cu_seqlens, cu_seqlens_k, scale)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        _check_tensor("o", out, q.dtype, q.shape, dev)
+        rows = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev) if lse else None
+        L = lib()
+        ws, nbytes = _workspace(L.falcon_attn_fwd_workspace(ctypes.byref(shape), cuk is not None), workspace, dev)
+        _done(L.falcon_attn_fwd(ctypes.byref(shape), _ptr(cu_seqlens), _ptr(cuk), hq, hk, hv, _ptr(out), _ptr(rows),
+                                _ptr(ws), nbytes, _stream(stream)), "falcon_attn_fwd")
+    return out, rows
+
+
+def attention_bwd(q, k, v, o, lse, do, *, cu_seqlens=None, cu_seqlens_k=None, scale=None, out=None, workspace=None,
+                  stream=None):
+    """falcon_attn_bwd on torch tensors: gradients of <do, o> for ``attention_fwd`` of the
+    same arguments, which gave o and lse.  ``out``: None or a dict of preallocated dq, dk,
+    dv (views with dense heads will do).  Returns dict(dq, dk, dv) in the dtype of q."""
+    import torch
+    shape, cuk, hq, hk, hv, dev = _attn_shape(q, k, v, cu_seqlens, cu_seqlens_k, scale)
+    _check_tensor("o", o, q.dtype, q.shape, dev)
+    _check_tensor("lse", lse, torch.float32, q.shape[:-1], dev)
+    lq, lk, H, G, d = q.shape[:-2], k.shape[:-2], q.shape[-2], k.shape[-2], q.shape[-1]
+    hdo = _heads("do", do, q.dtype, dev, lq, H, d)
+    with _on(dev, stream):
+        if out is None:
+            out = dict(dq=torch.empty(q.shape, dtype=q.dtype, device=dev),
+                       dk=torch.empty(k.shape, dtype=q.dtype, device=dev),
+                       dv=torch.empty(k.shape, dtype=q.dtype, device=dev))
+        hdq = _heads("dq", out["dq"], q.dtype, dev, lq, H, d)
+        hdk = _heads("dk", out["dk"], q.dtype, dev, lk, G, d)
+        hdv = _heads("dv", out["dv"], q.dtype, dev, lk, G, d)
+        L = lib()
+        ws, nbytes = _workspace(L.falcon_attn_bwd_workspace(ctypes.byref(shape), cuk is not None), workspace, dev)
+        _done(L.falcon_attn_bwd(ctypes.byref(shape), _ptr(cu_seqlens), _ptr(cuk), hq, hk, hv, _ptr(o), _ptr(lse), hdo,
+                                hdq, hdk, hdv, _ptr(ws), nbytes, _stream(stream)), "falcon_attn_bwd")
+    return dict(dq=out["dq"], dk=out["dk"], dv=out["dv"])

@@ -1,0 +1,189 @@
+"""GPU parity of causal attention (falcon_attn_fwd, falcon_attn_bwd) against the fp64
+oracle, elementwise, with the bounds of layer_helpers.attention_bounds."""
+
+import numpy as np
+import pytest
+
+from layer_helpers import attention_bounds, check, f64, offsets, rand
+from oracle import layer as L
+
+pytestmark = pytest.mark.gpu
+
+
+def run_case(dtype, ql, kl, hq, hk, d, packed=True, scale=None, seed=1, back=True, behind=0, spread=1.0):
+    import torch
+    from recurrent_sequence_models_amd import attention_bwd, attention_fwd
+    nq, nk = sum(ql) + behind, sum(kl) + behind
+    q, do = rand(seed, nq, hq, d, dtype=dtype, scale=spread), rand(seed + 3, nq, hq, d, dtype=dtype)
+    k, v = rand(seed + 1, nk, hk, d, dtype=dtype, scale=spread), rand(seed + 2, nk, hk, d, dtype=dtype)
+    if packed:
+        kw = dict(cu_seqlens=offsets(ql), cu_seqlens_k=offsets(kl), scale=scale)
+        args = (q, k, v)
+    else:
+        kw = dict(scale=scale)
+        args = (q.view(len(ql), ql[0], hq, d), k.view(len(kl), kl[0], hk, d), v.view(len(kl), kl[0], hk, d))
+    out = torch.full_like(args[0], 7.0)
+    o, lse = attention_fwd(*args, out=out, **kw)
+    grads = None
+    if back:
+        grads = attention_bwd(*args, o, lse, do.view(o.shape), **kw,
+                              out=dict(dq=torch.full_like(args[0], 7.0), dk=torch.full_like(args[1], 7.0),
+                                       dv=torch.full_like(args[2], 7.0)))
+        grads = {n: f64(t).reshape(-1, *t.shape[-2:]) for n, t in grads.items()}
+    torch.cuda.synchronize()
+    O, LSE = f64(o).reshape(nq, hq, d), f64(lse).reshape(nq, hq)
+    Q, K, V, DO = f64(q), f64(k), f64(v), f64(do)
+    sc = float(np.float32(d ** -0.5 if scale is None else scale))
+    for i, ((a, b), (c, e)) in enumerate(zip(L.ranges(ql), L.ranges(kl))):
+        if b == a and e == c:
+            continue
+        ref = attention_bounds(Q[a:b], K[c:e], V[c:e], sc, dtype, DO[a:b] if back else None)
+        check(f"o[{i}]", O[a:b], ref["o"], ref["bo"])
+        none = np.isneginf(ref["lse"])
+        assert np.all(np.isneginf(LSE[a:b]) == none) and np.all(O[a:b][none] == 0), i
+        check(f"lse[{i}]", np.where(none, 0, LSE[a:b]), np.where(none, 0, ref["lse"]), ref["bl"])
+        if back:
+            for n, lo, hi, bn in (("dq", a, b, "bq"), ("dk", c, e, "bk"), ("dv", c, e, "bv")):
+                check(f"{n}[{i}]", grads[n][lo:hi], ref[n], ref[bn] * 1.01)
+    if behind:
+        assert np.all(O[-behind:] == 7.0)
+        if back:
+            assert all(np.all(g[-behind:] == 7.0) for g in grads.values())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("T", [1, 31, 32, 33, 64, 129])
+def test_lengths(dtype, d, T):
+    run_case(dtype, [T, T], [T, T], 2, 2, d, packed=False, seed=T + d)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("hq,hk", [(1, 1), (3, 1), (4, 2), (8, 1), (5, 5), (12, 2), (40, 1)])
+def test_groups(dtype, hq, hk):
+    """Groups that do and do not divide a tile's rows."""
+    run_case(dtype, [50, 7], [50, 7], hq, hk, 64, seed=hq)
+
+
+PACKED = [([1], [1]), ([5, 0, 70, 1, 1], [5, 0, 70, 1, 1]), ([3, 40, 1, 0], [90, 40, 130, 6]),
+          ([1, 1, 1, 1], [200, 1, 64, 65]), ([10, 5], [4, 0]), ([64, 128, 1], [64, 128, 1]), ([0, 0, 9], [3, 0, 9])]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("lens", PACKED, ids=lambda p: "q" + "-".join(map(str, p[0])))
+@pytest.mark.parametrize("hq,hk,d", [(4, 2, 64), (3, 3, 128)])
+def test_packed(dtype, lens, hq, hk, d):
+    """Ragged and empty sequences, keys before the queries, more queries than keys (rows
+    that see nothing: o = 0, lse = -inf, no gradients)."""
+    run_case(dtype, *lens, hq, hk, d, seed=sum(lens[0]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_packed_leaves_the_rest(dtype):
+    run_case(dtype, [40, 0, 33], [40, 0, 33], 4, 2, 64, behind=9)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("lens", [([1], [1500]), ([1, 1, 0, 1], [3000, 1, 5, 700]), ([2, 3], [1111, 2048]),
+                                  ([40], [1300])], ids=["one", "ragged", "few", "rows"])
+@pytest.mark.parametrize("hq,hk,d", [(4, 1, 128), (2, 2, 64), (6, 2, 32), (40, 1, 64)])
+def test_split_keys(dtype, lens, hq, hk, d):
+    """Few queries against many keys: the keys are split over workgroups and joined."""
+    run_case(dtype, *lens, hq, hk, d, back=False, seed=hq + d)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_large_scores_and_scale(dtype):
+    """Peaked rows (scores of several hundred) and a scale of the caller's."""
+    run_case(dtype, [70], [70], 2, 1, 64, scale=0.5, spread=3.0, seed=3)
+
+
+def test_longer_prompt():
+    """A few thousand tokens: running maxima over many tiles, several row and key tiles."""
+    run_case("bf16", [1100], [1100], 2, 1, 64, seed=4)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_views_and_other_sequences(dtype):
+    """q, k, v as views of one projection; NaN in the sequences beside and behind one do not
+    reach it; gradients into views leave the rest."""
+    import torch
+    from recurrent_sequence_models_amd import attention_bwd, attention_fwd
+    hq, hk, d, lens = 4, 2, 64, [30, 45, 20]
+    qkv = rand(1, sum(lens) + 3, hq + 2 * hk, d, dtype=dtype)
+    do = rand(2, sum(lens) + 3, hq, d, dtype=dtype)
+    cu = offsets(lens)
+    cut = lambda t: (t[:, :hq], t[:, hq:hq + hk], t[:, hq + hk:])  # noqa: E731
+    dense = [t.contiguous() for t in cut(qkv)]
+    o, lse = attention_fwd(*dense, cu_seqlens=cu)
+    g = attention_bwd(*dense, o, lse, do, cu_seqlens=cu)
+    bad = qkv.clone()
+    bad[:30], bad[75:] = float("nan"), float("inf")
+    bad_do = do.clone()
+    bad_do[:30], bad_do[75:] = float("inf"), float("nan")
+    o2, lse2 = attention_fwd(*cut(bad), cu_seqlens=cu)
+    grad = torch.full_like(qkv, 3.0)
+    attention_bwd(*cut(bad), o2, lse2, bad_do, cu_seqlens=cu, out=dict(zip(("dq", "dk", "dv"), cut(grad))))
+    s = slice(30, 75)
+    assert torch.equal(o[s], o2[s]) and torch.equal(lse[s], lse2[s])
+    for n, t in zip(("dq", "dk", "dv"), cut(grad)):
+        assert torch.equal(g[n][s], t[s])
+    assert torch.all(grad[-3:] == 3.0)
+
+
+def test_streams_and_graph():
+    """Another stream, and a captured forward and backward (split keys too), replayed."""
+    import torch
+    from recurrent_sequence_models_amd import attention_bwd, attention_fwd
+    q, k, v = (rand(i, 2, 150, h, 64, dtype="bf16") for i, h in ((1, 4), (2, 2), (3, 2)))
+    t, kk, vv = rand(4, 2, 1, 4, 64, dtype="bf16"), rand(5, 2, 2000, 2, 64, dtype="bf16"), rand(6, 2, 2000, 2, 64, dtype="bf16")
+
+    def call(**kw):
+        o, lse = attention_fwd(q, k, v, **kw)
+        g = attention_bwd(q, k, v, o, lse, o, **kw)
+        return [o, lse, g["dq"], g["dk"], g["dv"], *attention_fwd(t, kk, vv, **kw)]
+
+    want = call()
+    torch.cuda.synchronize()
+    got = call(stream=torch.cuda.Stream())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call()
+    for _ in range(3):
+        for x in got:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_refusals():
+    import torch
+    from recurrent_sequence_models_amd import FalconError, attention_bwd, attention_fwd
+    q, k = rand(1, 2, 16, 4, 64), rand(2, 2, 16, 2, 64)
+    o, lse = attention_fwd(q, k, k)
+    bad = [
+        (TypeError, lambda: attention_fwd(q.half(), k.half(), k.half())),
+        (TypeError, lambda: attention_fwd(q, k, k.bfloat16())),
+        (ValueError, lambda: attention_fwd(q, k, k[:, :8])),
+        (ValueError, lambda: attention_fwd(q[0], k[0], k[0])),
+        (ValueError, lambda: attention_fwd(q, k, k, cu_seqlens=offsets([16, 16]))),
+        (ValueError, lambda: attention_fwd(q[0], k[0], k[0], cu_seqlens=offsets([16]), cu_seqlens_k=offsets([8, 8]))),
+        (ValueError, lambda: attention_fwd(q[0], k[0, :8], k[0, :8], cu_seqlens=offsets([16]))),
+        (ValueError, lambda: attention_fwd(q.transpose(1, 2), k.transpose(1, 2), k.transpose(1, 2))),
+        (FalconError, lambda: attention_fwd(q[:, :, :3].contiguous(), k, k)),          # 3 heads over 2
+        (FalconError, lambda: attention_fwd(q[..., :48].contiguous(), k[..., :48].contiguous(), k[..., :48].contiguous())),
+        (FalconError, lambda: attention_fwd(q, k, k, scale=0.0)),
+        (FalconError, lambda: attention_fwd(q, k, k, scale=float("inf"))),
+        (FalconError, lambda: attention_fwd(rand(1, 1, 1, 1, 64), rand(2, 1, 4000, 1, 64), rand(3, 1, 4000, 1, 64),
+                                            workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))),
+        (ValueError, lambda: attention_bwd(q, k, k, o, lse[:, :8], o)),
+        (TypeError, lambda: attention_bwd(q, k, k, o, lse, o.bfloat16())),
+        (ValueError, lambda: attention_fwd(q.cpu(), k.cpu(), k.cpu())),
+    ]
+    for i, (err, f_) in enumerate(bad):
+        with pytest.raises(err):
+            f_()
+            raise AssertionError(f"call {i} was taken")
