@@ -363,7 +363,7 @@ typedef struct {
   int32_t dtype;   /* falcon_dtype_t of x, log_lambda, h and their gradients */
   int32_t batch;   /* sequences, >= 1 */
   int32_t seqlen;  /* steps of every sequence, >= 1; packed: all tokens (>= 1) */
-  int32_t width;   /* channels, a multiple of 8 */
+  int32_t width;   /* channels, a multiple of 8, at most 2^20 */
   int32_t input;   /* falcon_scan_input_t */
 } falcon_scan_shape_t;
 

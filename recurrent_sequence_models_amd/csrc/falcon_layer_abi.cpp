@@ -44,7 +44,7 @@ int check_scan(const falcon_scan_shape_t *s, bool packed, bool step) {
   if (!s || !dtype_ok(s->dtype)) return FALCON_ERR_INVALID_ARG;
   if (s->input != FALCON_SCAN_ADD && s->input != FALCON_SCAN_MIX) return FALCON_ERR_INVALID_ARG;
   if (s->batch < 1 || s->width < 1 || (!step && s->seqlen < 1)) return FALCON_ERR_INVALID_ARG;
-  if (s->width % 8 != 0) return FALCON_ERR_UNSUPPORTED;
+  if (s->width % 8 != 0 || s->width > (1 << 20)) return FALCON_ERR_UNSUPPORTED;
   if (step) return FALCON_OK;
   // step numbers are ints, chunk rounding included; so are workgroup numbers
   if (s->seqlen > INT32_MAX - FALCON_SCAN_CHUNK) return FALCON_ERR_UNSUPPORTED;

@@ -215,21 +215,22 @@ template <typename T, typename G, int D> __global__ __launch_bounds__(THR) void 
   }
 }
 
-// Sums the workgroups' weight gradients, in a fixed order: block k = tensor, 1024 threads
-// = 1024 / D slices of the workgroups for each entry.
-template <int D> __global__ __launch_bounds__(1024) void qk_weight_sum(QkArgs a, int blocks) {
-  constexpr int SL = 1024 / D;
-  __shared__ float sum[SL][D];
-  const int k = blockIdx.x, e = threadIdx.x % D, sl = threadIdx.x / D;
+// Sums the workgroups' weight gradients, in a fixed order: block (16 entries, tensor), 64
+// slices of the workgroups for each entry.
+constexpr int SUM_E = 16, SUM_S = 1024 / SUM_E;
+__global__ __launch_bounds__(1024) void qk_weight_sum(QkArgs a, int d, int blocks) {
+  __shared__ float sum[SUM_S][SUM_E];
+  const int k = blockIdx.y, e = threadIdx.x % SUM_E, sl = threadIdx.x / SUM_E, col = blockIdx.x * SUM_E + e;
   float s = 0.f;
 #pragma unroll 4
-  for (int i = sl; i < blocks; i += SL) s += a.part[((size_t)i * 2 + k) * D + e];
+  for (int i = sl; i < blocks; i += SUM_S) s += a.part[((size_t)i * 2 + k) * d + col];
   sum[sl][e] = s;
   __syncthreads();
-  if (threadIdx.x < D && a.dw[k]) {
+  if (threadIdx.x < SUM_E && a.dw[k]) {
     s = 0.f;
-    for (int i = 0; i < SL; ++i) s += sum[i][e];
-    a.dw[k][e] = s;
+#pragma unroll 8
+    for (int i = 0; i < SUM_S; ++i) s += sum[i][e];
+    a.dw[k][col] = s;
   }
 }
 
@@ -278,7 +279,7 @@ hipError_t launch_qk_bwd(bool bf16, bool dy_f32, int d, QkArgs a, void *ws, hipS
     else hipLaunchKernelGGL((qk_bwd<__bf16, __bf16, D_>), dim3(blocks), dim3(THR), lds, s, a);                   \
     const hipError_t e = hipGetLastError();                                                                      \
     if (e != hipSuccess || !weights) return e;                                                                   \
-    hipLaunchKernelGGL((qk_weight_sum<D_>), dim3(2), dim3(1024), 0, s, a, blocks);                               \
+    hipLaunchKernelGGL(qk_weight_sum, dim3(D_ / SUM_E, 2), dim3(1024), 0, s, a, D_, blocks);                     \
     return hipGetLastError();                                                                                    \
   }
   FALCON_QK(32)

@@ -41,31 +41,32 @@ constexpr int LPR = 8;        // lanes side by side in a 128-byte column
 constexpr int GROUP = 16;     // chunks whose maps a workgroup applies itself
 constexpr unsigned long long EMPTY = ~0ull;
 
+typedef unsigned int u4 __attribute__((ext_vector_type(4)));   // 16 bytes of channels, in registers
+
 template <typename T> constexpr int CPT = 16 / (int)sizeof(T);   // channels per thread
 template <typename T> constexpr int TC = LPR * CPT<T>;           // channels per column
 
 // ---- 16 bytes of channels ----------------------------------------------------
-__device__ __forceinline__ void unpack16(const uint4 &u, float (&o)[8]) {
-  const unsigned w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ void unpack16(const u4 &u, float (&o)[8]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    o[2 * j] = __uint_as_float(w[j] << 16);
-    o[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    o[2 * j] = __uint_as_float(u[j] << 16);
+    o[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
   }
 }
-__device__ __forceinline__ void unpack16(const uint4 &u, float (&o)[4]) {
-  o[0] = __uint_as_float(u.x); o[1] = __uint_as_float(u.y);
-  o[2] = __uint_as_float(u.z); o[3] = __uint_as_float(u.w);
+__device__ __forceinline__ void unpack16(const u4 &u, float (&o)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o[j] = __uint_as_float(u[j]);
 }
 // Rounded to nearest even: the one rounding of a result held in bf16.
-__device__ __forceinline__ uint4 pack16(const float (&v)[8]) {
+__device__ __forceinline__ u4 pack16(const float (&v)[8]) {
   bf8 b;
 #pragma unroll
   for (int j = 0; j < 8; ++j) b[j] = (__bf16)v[j];
-  return __builtin_bit_cast(uint4, b);
+  return __builtin_bit_cast(u4, b);
 }
-__device__ __forceinline__ uint4 pack16(const float (&v)[4]) {
-  return uint4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+__device__ __forceinline__ u4 pack16(const float (&v)[4]) {
+  return u4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
 }
 template <int N> __device__ __forceinline__ void load_f32(const float *p, float (&o)[N]) {
 #pragma unroll
@@ -83,16 +84,15 @@ template <int N> __device__ __forceinline__ void store_f32(float *p, const float
 // grows where the decay itself has become negligible against 1.
 __device__ __forceinline__ float decay(float g) { return __builtin_amdgcn_exp2f(g * 1.44269504088896f); }
 
-// 1 - e^g: the series -(g + g^2/2! + ... + g^7/7!) near 0, where 1 - lam would cancel
-// (|g| <= 1/4: the next term is below 2^-28 of the result), else 1 - lam.
+// 1 - e^g: the series -g (1 + g / 2! + ... + g^5 / 6!) near 0, where 1 - lam would cancel
+// (|g| <= 1/8: the next term is 2^-30 of the result), else 1 - lam (off by 2^-22 at most).
 __device__ __forceinline__ float one_minus_decay(float g, float lam) {
-  float p = 1.f + g * (1.f / 7.f);
-  p = 1.f + g * (1.f / 6.f) * p;
-  p = 1.f + g * (1.f / 5.f) * p;
-  p = 1.f + g * (1.f / 4.f) * p;
-  p = 1.f + g * (1.f / 3.f) * p;
-  p = 1.f + g * (1.f / 2.f) * p;
-  return fabsf(g) <= 0.25f ? -g * p : 1.f - lam;
+  float p = fmaf(g, 1.f / 720.f, 1.f / 120.f);
+  p = fmaf(p, g, 1.f / 24.f);
+  p = fmaf(p, g, 1.f / 6.f);
+  p = fmaf(p, g, 0.5f);
+  p = fmaf(p, g, 1.f);
+  return fabsf(g) <= 0.125f ? -g * p : 1.f - lam;
 }
 
 // y after the map (A, H); a set sign of A cuts the carry off.
@@ -113,37 +113,8 @@ __device__ __forceinline__ unsigned long long peek(const unsigned long long *p) 
   return __hip_atomic_load(const_cast<unsigned long long *>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// The value carried into the chunk of rank `rank` (its place in the column's chain) for
-// one channel: the group's carry, then the maps of the group's earlier chunks in order.
-__device__ __forceinline__ float carry_in(const unsigned long long *agg, const unsigned long long *pre, int rank,
-                                          int tc) {
-  const int g0 = rank & ~(GROUP - 1), j = rank - g0;
-  unsigned long long w[GROUP];
-  unsigned long long c = 0;
-  bool wait;
-  do {   // ends: every word waited for belongs to a chunk whose ticket was drawn earlier
-    wait = false;
-    if (g0) {
-      c = peek(pre + (size_t)(rank / GROUP) * tc);
-      wait |= c == EMPTY;
-    }
-#pragma unroll
-    for (int i = 0; i < GROUP - 1; ++i)
-      if (i < j) {
-        w[i] = peek(agg + (size_t)(g0 + i) * tc);
-        wait |= w[i] == EMPTY;
-      }
-    if (wait) __builtin_amdgcn_s_sleep(1);
-  } while (wait);
-  float y = g0 ? __uint_as_float((unsigned)c) : 0.f;
-#pragma unroll
-  for (int i = 0; i < GROUP - 1; ++i)
-    if (i < j) y = apply(__uint_as_float((unsigned)(w[i] >> 32)), __uint_as_float((unsigned)w[i]), y);
-  return y;
-}
-
 // ---- Sequences ---------------------------------------------------------------
-// The sequence that holds token t: the largest n < N with cu[n] <= t (cu[0] if none).
+// The sequence that holds token t: the largest n < N with cu[n] <= t (0 if none).
 __device__ __forceinline__ int seq_of(const int *cu, int N, int t) {
   int lo = 0, hi = N - 1;
   while (lo < hi) {
@@ -153,22 +124,30 @@ __device__ __forceinline__ int seq_of(const int *cu, int N, int t) {
   return lo;
 }
 
-// Which of a thread's steps t0 .. t0 + SEG - 1 are the first or last of a sequence, and
-// how many are inside one (the rest are behind the last sequence or the time axis).
-struct Marks { unsigned first, last; int valid; };
-
-template <int SEG> __device__ __forceinline__ Marks marks_of(const ScanArgs &a, int t0) {
-  Marks m{0, 0, 0};
-  if (!a.cu) {
-    m.valid = min(max(a.T - t0, 0), SEG);
-    if (t0 == 0) m.first = 1;
-    if (a.T - 1 >= t0 && a.T - 1 < t0 + SEG) m.last = 1u << (a.T - 1 - t0);
-    return m;
+// The same for a token that the whole wave asks for: 64 places at a time, one round trip to
+// memory for up to 64 sequences, two for 4096.
+__device__ __forceinline__ int wave_seq_of(const int *cu, int N, int t) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, len = N;
+  while (len > 1) {
+    const int step = (len + 63) / 64, at = lane * step;
+    const int before = __popcll(__ballot(at < len && cu[lo + min(at, len - 1)] <= t));
+    const int skip = max(before - 1, 0) * step;
+    lo += skip;
+    len = min(step, len - skip);
   }
-  const int end = min(a.cu[a.nseq], a.T);
-  m.valid = min(max(end - t0, 0), SEG);
-  if (m.valid == 0) return m;
-  int n = seq_of(a.cu, a.nseq, t0);
+  return lo;
+}
+
+// Which of a thread's steps t0 .. t0 + SEG - 1 are the first or last of a packed sequence.
+// (Batch rows begin and end with the chain: the carry of rank 0 and the chain's result.)
+struct Marks { unsigned first, last; };
+
+template <int SEG> __device__ __forceinline__ Marks marks_of(const ScanArgs &a, int t0, int end) {
+  Marks m{0, 0};
+  int n = wave_seq_of(a.cu, a.nseq, __builtin_amdgcn_readfirstlane(t0));   // of the wave's first step
+  if (t0 >= end) return m;
+  while (n + 1 < a.nseq && a.cu[n + 1] <= t0) ++n;
   if (a.cu[n] == t0) m.first = 1;
   for (; n < a.nseq; ++n) {      // walk the sequence ends inside the steps
     const int e = a.cu[n + 1];
@@ -180,9 +159,28 @@ template <int SEG> __device__ __forceinline__ Marks marks_of(const ScanArgs &a, 
   }
   return m;
 }
-// The sequence of step t of this row (batch rows are their own sequences).
-__device__ __forceinline__ int seq_at(const ScanArgs &a, int row, int t) {
-  return a.cu ? seq_of(a.cu, a.nseq, t) : row;
+// Row `seq` of a [nseq, D] array for the packed sequence of token t; zeros without the array.
+template <int N>
+__device__ __forceinline__ void load_seq(const ScanArgs &a, const float *p, int t, int ch, float (&o)[N]) {
+#pragma unroll
+  for (int c = 0; c < N; ++c) o[c] = 0.f;
+  if (p) load_f32<N>(p + (size_t)seq_of(a.cu, a.nseq, t) * a.D + ch, o);
+}
+template <int N>
+__device__ __forceinline__ void store_seq(const ScanArgs &a, float *p, int t, int ch, const float (&v)[N]) {
+  if (p) store_f32<N>(p + (size_t)seq_of(a.cu, a.nseq, t) * a.D + ch, v);
+}
+// An empty sequence ends where it began: its rows are copied (zeros without a source).
+template <int N>
+__device__ __forceinline__ void copy_empty(const ScanArgs &a, const float *from, float *to, int rank, int grp, int ngrp,
+                                           int ch) {
+  if (!to || ch >= a.D) return;
+  for (int n = rank * ngrp + grp; n < a.nseq; n += a.NC * ngrp) {
+    if (a.cu[n] != a.cu[n + 1]) continue;
+    float v[N] = {};
+    if (from) load_f32<N>(from + (size_t)n * a.D + ch, v);
+    store_f32<N>(to + (size_t)n * a.D + ch, v);
+  }
 }
 
 struct Place { int row, rank, c0; size_t col; };
@@ -208,194 +206,312 @@ template <typename T> __device__ __forceinline__ Place place(const ScanArgs &a) 
   return p;
 }
 
-// An empty sequence ends where it began: its rows are copied (zeros without a source).
-template <int N>
-__device__ __forceinline__ void copy_empty(const ScanArgs &a, const float *from, float *to, int rank, int grp, int ngrp,
-                                           int ch) {
-  if (!a.cu || !to || ch >= a.D) return;
-  for (int n = rank * ngrp + grp; n < a.nseq; n += a.NC * ngrp) {
-    if (a.cu[n] != a.cu[n + 1]) continue;
-    float v[N] = {};
-    if (from) load_f32<N>(from + (size_t)n * a.D + ch, v);
-    store_f32<N>(to + (size_t)n * a.D + ch, v);
+// A thread's steps: 16 bytes of channels at each of SEG tokens from t0.  Tokens past `end`
+// and channels past D read another place of the same array and become zeros, which as x
+// (dh) and log decay are the identity map.  The loads are unconditional, so that all of
+// them are in flight at once.
+// Addresses are the chunk's (scalar) plus 32 bits a thread: a chunk of the widest rows,
+// 2^20 channels, is 2^30 bytes.
+template <typename T, int SEG> struct Steps {
+  size_t base;         // the chunk's first element
+  int t, most, n;      // the thread's first step and the last one of the array, counted in the chunk; its valid steps
+  unsigned D, c;
+  __device__ __forceinline__ Steps(const ScanArgs &a, int row, int chunk, int grp, int end, int ch) {
+    base = ((size_t)row * a.T + (size_t)chunk * CHUNK) * a.D;
+    t = grp * SEG;
+    most = a.T - 1 - chunk * CHUNK;
+    n = ch < a.D ? end - chunk * CHUNK - t : 0;
+    D = a.D;
+    c = min(ch, a.D - CPT<T>);
+  }
+  __device__ __forceinline__ unsigned at(int i) const { return (unsigned)min(t + i, most) * D + c; }
+  __device__ __forceinline__ void load(const void *p, u4 (&v)[SEG]) const {
+    const T *q = static_cast<const T *>(p) + base;
+#pragma unroll
+    for (int i = 0; i < SEG; ++i) v[i] = *reinterpret_cast<const u4 *>(q + at(i));
+  }
+  __device__ __forceinline__ void store(void *p, int i, const u4 &v) const {
+    if (i < n) *reinterpret_cast<u4 *>(static_cast<T *>(p) + base + at(i)) = v;
+  }
+  __device__ __forceinline__ void mask(u4 (&v)[SEG]) const {
+#pragma unroll
+    for (int i = 0; i < SEG; ++i) v[i] = i < n ? v[i] : u4{0, 0, 0, 0};
+  }
+};
+
+// Makes raw inputs opaque to the compiler, which otherwise keeps every step's decay and input
+// in fp32 from one pass over the steps to the next (4 times the registers of the bf16 inputs).
+template <int N> __device__ __forceinline__ void forget(u4 (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+v"(v[i]));
+}
+
+// lam and u of one step's channels.
+template <bool MIX, int C>
+__device__ __forceinline__ void step_of(const u4 &x, const u4 &g, float (&lam)[C], float (&u)[C]) {
+  float gv[C];
+  unpack16(x, u);
+  unpack16(g, gv);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    lam[c] = decay(gv[c]);
+    if (MIX) u[c] *= one_minus_decay(gv[c], lam[c]);
   }
 }
 
-// ---- Forward -----------------------------------------------------------------
-// 256 threads: 32 groups of 8 lanes, each group 8 steps.
-constexpr int FSEG = 8, FGRP = CHUNK / FSEG, FTHR = FGRP * LPR;
+// ---- A chunk's scan -----------------------------------------------------------
+// 512 threads: 64 groups of 8 lanes, each group 4 steps; a wave's 8 groups are neighbours
+// in time.  Groups, waves and chunks are scanned in turn, 8, 8 and at most 15 maps one
+// after the other (a single wave over all 64 groups took 0.8 us of every workgroup's time,
+// twice).
+constexpr int SEG = 4, GRPS = CHUNK / SEG, THR = GRPS * LPR, WAVES = THR / 64, GPW = GRPS / WAVES;
 
-template <typename T, bool MIX> __global__ __launch_bounds__(FTHR) void scan_fwd(ScanArgs a) {
-  constexpr int C = CPT<T>, W = TC<T>;
-  __shared__ __align__(16) float sA[FGRP][W], sH[FGRP][W];   // group maps; sH then holds the groups' carries
-  const Place p = place<T>(a);
-  const int tid = threadIdx.x, grp = tid / LPR, cl = (tid % LPR) * C, ch = p.c0 + cl;
-  const int t0 = p.rank * CHUNK + grp * FSEG;
-  const bool on = ch < a.D;
-  Marks m = marks_of<FSEG>(a, t0);
-  if (!on) m = Marks{0, 0, 0};
-  const T *x = static_cast<const T *>(a.x) + ((size_t)p.row * a.T + t0) * a.D + ch;
-  const T *g = static_cast<const T *>(a.g) + ((size_t)p.row * a.T + t0) * a.D + ch;
-  uint4 xr[FSEG], gr[FSEG];
+template <int W> struct Lds {
+  float A[GRPS][W], H[GRPS][W];          // the groups' maps; H then holds the values carried into them
+  float wA[WAVES][W], wH[WAVES][W];      // the waves' maps
+  unsigned long long words[GROUP][W];    // words read from the column's chain
+};
+
+// The values carried into the groups (to s.H), from the groups' maps, in time order or (REV)
+// against it.  Without CHAIN, *first is the value carried into the chunk.  With it the
+// chunk is number `rank` of its column's chain and *first the value carried into rank 0: it
+// is read by rank 0 alone, which passes it on as it does its map, since its memory may be
+// where the chain's result goes.  Returns, in lanes < W of every wave, the value that leaves
+// the chunk.  Every thread of the workgroup calls it; the maps are the calling wave's own.
+template <int W, bool REV, bool CHAIN>
+__device__ __forceinline__ float scan_chunk(const ScanArgs &a, Lds<W> &s, size_t col, int rank, const float *first) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const bool on = lane < W;
+  const int ng = (a.NC + GROUP - 1) / GROUP, grp = rank / GROUP, g0 = grp * GROUP, j = rank - g0;
+  unsigned long long *agg = nullptr, *pre = nullptr;
+  if (CHAIN && a.NC > 1) {
+    agg = a.agg + col * a.NC * W + lane;
+    pre = a.pre + col * ng * W + lane;
+  }
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the wave's maps are in LDS
+  if (on) {
+    float A = 1.f, H = 0.f;
 #pragma unroll
-  for (int i = 0; i < FSEG; ++i) {   // steps outside are x = 0, g = 0: the identity map
-    xr[i] = gr[i] = uint4{0, 0, 0, 0};
-    if (i < m.valid) {
-      xr[i] = *reinterpret_cast<const uint4 *>(x + (size_t)i * a.D);
-      gr[i] = *reinterpret_cast<const uint4 *>(g + (size_t)i * a.D);
+    for (int i = 0; i < GPW; ++i) {
+      const int q = wave * GPW + (REV ? GPW - 1 - i : i);
+      H = apply(s.A[q][lane], s.H[q][lane], H);
+      A *= s.A[q][lane];
+    }
+    s.wA[wave][lane] = A;
+    s.wH[wave][lane] = H;
+  }
+  __syncthreads();
+  float At = 1.f, Ht = 0.f, y = 0.f;
+  if (on) {
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) {
+      const int w = REV ? WAVES - 1 - i : i;
+      Ht = apply(s.wA[w][lane], s.wH[w][lane], Ht);
+      At *= s.wA[w][lane];
     }
   }
-  copy_empty<C>(a, a.init, a.final_state, p.rank, grp, FGRP, ch);
+  if (!CHAIN || a.NC == 1) {
+    if (on && first) y = first[lane];
+  } else {
+    // one wave publishes, and each reads two words of the chain: the value carried into the
+    // group of chunks (word 15) and the maps of the group's chunks before this one
+    if (on && wave == 0) {
+      if (rank + 1 < a.NC) publish(agg + (size_t)rank * W, word(At, Ht));
+      if (rank == 0) publish(pre, word(0.f, first ? first[lane] : 0.f));
+    }
+    if (on) {
+#pragma unroll
+      for (int k = 2 * wave; k < 2 * wave + 2; ++k) {
+        if (k >= j && k < GROUP - 1) continue;
+        const unsigned long long *p = k == GROUP - 1 ? pre + (size_t)grp * W : agg + (size_t)(g0 + k) * W;
+        unsigned long long v;
+        // ends: the word is published by a chunk whose ticket was drawn earlier (or, word 15
+        // of rank 0's group, by rank 0 itself above)
+        while ((v = peek(p)) == EMPTY) __builtin_amdgcn_s_sleep(1);
+        s.words[k][lane] = v;
+      }
+    }
+    __syncthreads();
+    if (on) {
+      y = __uint_as_float((unsigned)s.words[GROUP - 1][lane]);
+      for (int i = 0; i < j; ++i) {
+        const unsigned long long v = s.words[i][lane];
+        y = apply(__uint_as_float((unsigned)(v >> 32)), __uint_as_float((unsigned)v), y);
+      }
+      if (wave == 0 && j == GROUP - 1 && rank + 1 < a.NC) publish(pre + (size_t)(grp + 1) * W, word(0.f, apply(At, Ht, y)));
+    }
+  }
+  const float out = apply(At, Ht, y);
+  if (on) {
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) {
+      const int w = REV ? WAVES - 1 - i : i;
+      const float z = apply(s.wA[w][lane], s.wH[w][lane], y);
+      if (REV ? w > wave : w < wave) y = z;
+    }
+#pragma unroll
+    for (int i = 0; i < GPW; ++i) {
+      const int q = wave * GPW + (REV ? GPW - 1 - i : i);
+      const float H = s.H[q][lane];
+      s.H[q][lane] = y;
+      y = apply(s.A[q][lane], H, y);
+    }
+  }
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the wave's carries are in LDS
+  return out;
+}
+
+// ---- Forward -----------------------------------------------------------------
+// A thread keeps its steps' decays and inputs in fp32 for the replay (64 registers for bf16;
+// computing them again made that kernel bound by the vector unit).
+template <typename T, bool MIX, bool PACKED> __global__ __launch_bounds__(THR, 4) void scan_fwd(ScanArgs a) {
+  constexpr int C = CPT<T>, W = TC<T>;
+  __shared__ __align__(16) Lds<W> s;
+  const Place p = place<T>(a);
+  const int tid = threadIdx.x, grp = tid / LPR, cl = (tid % LPR) * C, ch = p.c0 + cl;
+  const int t0 = p.rank * CHUNK + grp * SEG;
+  const int end = PACKED ? min(a.cu[a.nseq], a.T) : a.T;
+  const Steps<T, SEG> st(a, p.row, p.rank, grp, end, ch);
+  u4 xr[SEG], gr[SEG];
+  st.load(a.x, xr);
+  st.load(a.g, gr);
+  Marks m{0, 0};
+  if (PACKED) {
+    m = marks_of<SEG>(a, t0, end);
+    if (ch >= a.D) m = Marks{0, 0};
+    copy_empty<C>(a, a.init, a.final_state, p.rank, grp, GRPS, ch);
+  }
+  st.mask(xr);
+  st.mask(gr);
 
   // this thread's map; h0 keeps the initial state of the last sequence that starts here (another
   // workgroup may write its final state, which may be the same memory, before the replay below)
-  float A[C], H[C], h0[C] = {};
+  float A[C], H[C], h0[C] = {}, lam[SEG][C], u[SEG][C];
 #pragma unroll
   for (int c = 0; c < C; ++c) { A[c] = 1.f; H[c] = 0.f; }
 #pragma unroll
-  for (int i = 0; i < FSEG; ++i) {
-    if ((m.first >> i) & 1) {
-      if (a.init) load_f32<C>(a.init + (size_t)seq_at(a, p.row, t0 + i) * a.D + ch, h0);
+  for (int i = 0; i < SEG; ++i) {
+    if (PACKED && ((m.first >> i) & 1)) {
+      load_seq<C>(a, a.init, t0 + i, ch, h0);
 #pragma unroll
       for (int c = 0; c < C; ++c) { A[c] = -0.f; H[c] = h0[c]; }
     }
-    float xv[C], gv[C];
-    unpack16(xr[i], xv);
-    unpack16(gr[i], gv);
+    step_of<MIX, C>(xr[i], gr[i], lam[i], u[i]);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const float lam = decay(gv[c]);
-      const float u = MIX ? one_minus_decay(gv[c], lam) * xv[c] : xv[c];
-      A[c] *= lam;
-      H[c] = fmaf(lam, H[c], u);
+      A[c] *= lam[i][c];
+      H[c] = fmaf(lam[i][c], H[c], u[i][c]);
     }
   }
-  store_f32<C>(&sA[grp][cl], A);
-  store_f32<C>(&sH[grp][cl], H);
-  __syncthreads();
-  if (tid < W) {   // one lane a channel: the chunk's map, the carry, the groups' carries
-    float At = 1.f, Ht = 0.f;
-#pragma unroll 8
-    for (int q = 0; q < FGRP; ++q) {
-      Ht = apply(sA[q][tid], sH[q][tid], Ht);
-      At *= sA[q][tid];
-    }
-    float y = 0.f;
-    if (a.NC > 1) {
-      const int ng = (a.NC + GROUP - 1) / GROUP;
-      unsigned long long *agg = a.agg + p.col * a.NC * W + tid, *pre = a.pre + p.col * ng * W + tid;
-      if (p.rank + 1 < a.NC) publish(agg + (size_t)p.rank * W, word(At, Ht));
-      y = carry_in(agg, pre, p.rank, W);
-      if (p.rank % GROUP == GROUP - 1 && p.rank + 1 < a.NC)
-        publish(pre + (size_t)(p.rank / GROUP + 1) * W, word(0.f, apply(At, Ht, y)));
-    }
-    if (a.states && p.c0 + tid < a.D)
-      a.states[((size_t)p.row * a.NC + p.rank) * a.D + p.c0 + tid] = apply(At, Ht, y);
-#pragma unroll 8
-    for (int q = 0; q < FGRP; ++q) {
-      const float Hq = sH[q][tid];
-      sH[q][tid] = y;
-      y = apply(sA[q][tid], Hq, y);
-    }
+  store_f32<C>(&s.A[grp][cl], A);
+  store_f32<C>(&s.H[grp][cl], H);
+  const float *first = !PACKED && a.init && p.c0 + (tid & 63) < a.D ? a.init + (size_t)p.row * a.D + p.c0 : nullptr;
+  const float out = scan_chunk<W, false, true>(a, s, p.col, p.rank, first);
+  if (tid < W && p.c0 + tid < a.D) {
+    if (a.states) a.states[((size_t)p.row * a.NC + p.rank) * a.D + p.c0 + tid] = out;
+    if (!PACKED && a.final_state && p.rank == a.NC - 1) a.final_state[(size_t)p.row * a.D + p.c0 + tid] = out;
   }
-  __syncthreads();
   float h[C];
-  load_f32<C>(&sH[grp][cl], h);
-  T *out = static_cast<T *>(a.h) + ((size_t)p.row * a.T + t0) * a.D + ch;
+  load_f32<C>(&s.H[grp][cl], h);
 #pragma unroll
-  for (int i = 0; i < FSEG; ++i) {
-    if (i >= m.valid) break;
-    if ((m.first >> i) & 1) {
+  for (int i = 0; i < SEG; ++i) {
+    if (PACKED && ((m.first >> i) & 1)) {
       if (m.first >> (i + 1)) {   // a sequence inside these steps: read again, this thread alone writes its end
-#pragma unroll
-        for (int c = 0; c < C; ++c) h[c] = 0.f;
-        if (a.init) load_f32<C>(a.init + (size_t)seq_at(a, p.row, t0 + i) * a.D + ch, h);
+        load_seq<C>(a, a.init, t0 + i, ch, h);
       } else {
 #pragma unroll
         for (int c = 0; c < C; ++c) h[c] = h0[c];
       }
     }
-    float xv[C], gv[C];
-    unpack16(xr[i], xv);
-    unpack16(gr[i], gv);
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const float lam = decay(gv[c]);
-      const float u = MIX ? one_minus_decay(gv[c], lam) * xv[c] : xv[c];
-      h[c] = fmaf(lam, h[c], u);
-    }
-    *reinterpret_cast<uint4 *>(out + (size_t)i * a.D) = pack16(h);
-    if (((m.last >> i) & 1) && a.final_state)
-      store_f32<C>(a.final_state + (size_t)seq_at(a, p.row, t0 + i) * a.D + ch, h);
+    for (int c = 0; c < C; ++c) h[c] = fmaf(lam[i][c], h[c], u[i][c]);
+    st.store(a.h, i, pack16(h));
+    if (PACKED && ((m.last >> i) & 1)) store_seq<C>(a, a.final_state, t0 + i, ch, h);
   }
 }
 
 // ---- Backward ----------------------------------------------------------------
-// 512 threads: 64 groups of 8 lanes, each group 4 steps (a step has three inputs, and its
-// incoming state is kept from the forward replay: half the forward's steps per thread).
-// The states of the forward's chunks give the state entering a chunk; only the reverse
-// direction is chained.
-constexpr int BSEG = 4, BGRP = CHUNK / BSEG, BTHR = BGRP * LPR;
-
-template <typename T, bool MIX> __global__ __launch_bounds__(BTHR) void scan_bwd(ScanArgs a) {
+// The states of the forward's chunks give the state entering a chunk, so only the reverse
+// direction is chained (rank 0 is the last chunk).
+template <typename T, bool MIX, bool PACKED> __global__ __launch_bounds__(THR, 4) void scan_bwd(ScanArgs a) {
   constexpr int C = CPT<T>, W = TC<T>;
-  __shared__ __align__(16) float sA[BGRP][W], sH[BGRP][W];   // forward maps
-  __shared__ __align__(16) float sR[BGRP][W], sQ[BGRP][W];   // reverse maps
+  __shared__ __align__(16) Lds<W> s;
   const Place p = place<T>(a);
   const int chunk = a.NC - 1 - p.rank;
   const int tid = threadIdx.x, grp = tid / LPR, cl = (tid % LPR) * C, ch = p.c0 + cl;
-  const int t0 = chunk * CHUNK + grp * BSEG;
-  const bool on = ch < a.D;
-  Marks m = marks_of<BSEG>(a, t0);
-  if (!on) m = Marks{0, 0, 0};
-  const size_t at = ((size_t)p.row * a.T + t0) * a.D + ch;
-  const T *x = static_cast<const T *>(a.x) + at, *g = static_cast<const T *>(a.g) + at;
-  const T *dh = static_cast<const T *>(a.dh) + at;
-  uint4 xr[BSEG], gr[BSEG], dr[BSEG];
-#pragma unroll
-  for (int i = 0; i < BSEG; ++i) {
-    xr[i] = gr[i] = dr[i] = uint4{0, 0, 0, 0};
-    if (i < m.valid) {
-      xr[i] = *reinterpret_cast<const uint4 *>(x + (size_t)i * a.D);
-      gr[i] = *reinterpret_cast<const uint4 *>(g + (size_t)i * a.D);
-      dr[i] = *reinterpret_cast<const uint4 *>(dh + (size_t)i * a.D);
-    }
+  const int t0 = chunk * CHUNK + grp * SEG;
+  const int end = PACKED ? min(a.cu[a.nseq], a.T) : a.T;
+  const Steps<T, SEG> st(a, p.row, chunk, grp, end, ch);
+  u4 xr[SEG], gr[SEG], dr[SEG];
+  st.load(a.x, xr);
+  st.load(a.g, gr);
+  st.load(a.dh, dr);
+  Marks m{0, 0};
+  if (PACKED) {
+    m = marks_of<SEG>(a, t0, end);
+    if (ch >= a.D) m = Marks{0, 0};
+    copy_empty<C>(a, a.d_final, a.d_init, p.rank, grp, GRPS, ch);
   }
-  copy_empty<C>(a, a.d_final, a.d_init, p.rank, grp, BGRP, ch);
+  st.mask(xr);
+  st.mask(gr);
+  st.mask(dr);
 
   float A[C], H[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) { A[c] = 1.f; H[c] = 0.f; }
 #pragma unroll
-  for (int i = 0; i < BSEG; ++i) {
-    if ((m.first >> i) & 1) {
-      float h0[C] = {};
-      if (a.init) load_f32<C>(a.init + (size_t)seq_at(a, p.row, t0 + i) * a.D + ch, h0);
+  for (int i = 0; i < SEG; ++i) {
+    if (PACKED && ((m.first >> i) & 1)) {
+      load_seq<C>(a, a.init, t0 + i, ch, H);
 #pragma unroll
-      for (int c = 0; c < C; ++c) { A[c] = -0.f; H[c] = h0[c]; }
+      for (int c = 0; c < C; ++c) A[c] = -0.f;
     }
-    float xv[C], gv[C];
-    unpack16(xr[i], xv);
-    unpack16(gr[i], gv);
+    float lam[C], u[C];
+    step_of<MIX, C>(xr[i], gr[i], lam, u);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const float lam = decay(gv[c]);
-      A[c] *= lam;
-      H[c] = fmaf(lam, H[c], MIX ? one_minus_decay(gv[c], lam) * xv[c] : xv[c]);
+      A[c] *= lam[c];
+      H[c] = fmaf(lam[c], H[c], u[c]);
     }
   }
-  store_f32<C>(&sA[grp][cl], A);
-  store_f32<C>(&sH[grp][cl], H);
+  store_f32<C>(&s.A[grp][cl], A);
+  store_f32<C>(&s.H[grp][cl], H);
+  const bool on = p.c0 + (tid & 63) < a.D;
+  const size_t c0 = (size_t)p.row * a.D + p.c0;
+  const float *first = nullptr;
+  if (on && chunk > 0) first = a.states + ((size_t)p.row * a.NC + chunk - 1) * a.D + p.c0;
+  else if (on && !PACKED && a.init) first = a.init + c0;
+  scan_chunk<W, false, false>(a, s, p.col, p.rank, first);
+  forget(xr);
+  forget(gr);
+  float h[C], e[SEG][C];                  // e: what dlam multiplies, h_{t-1} (mix: h_{t-1} - x_t)
+  load_f32<C>(&s.H[grp][cl], h);
+#pragma unroll
+  for (int i = 0; i < SEG; ++i) {
+    if (PACKED && ((m.first >> i) & 1)) load_seq<C>(a, a.init, t0 + i, ch, h);
+    float lam[C], u[C], xv[C];
+    step_of<MIX, C>(xr[i], gr[i], lam, u);
+    unpack16(xr[i], xv);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      e[i][c] = MIX ? h[c] - xv[c] : h[c];
+      h[c] = fmaf(lam[c], h[c], u[c]);
+    }
+    // formed here and now: left to itself, the compiler keeps what e is made of instead
+#pragma unroll
+    for (int c = 0; c < C; ++c) asm volatile("" : "+v"(e[i][c]), "+v"(h[c]));
+  }
+  forget(gr);
+  forget(dr);
   // the reverse map of these steps: r_{t+1} of the last to r_t of the first
 #pragma unroll
   for (int c = 0; c < C; ++c) { A[c] = 1.f; H[c] = 0.f; }
 #pragma unroll
-  for (int i = BSEG - 1; i >= 0; --i) {
-    if ((m.last >> i) & 1) {
-      float d0[C] = {};
-      if (a.d_final) load_f32<C>(a.d_final + (size_t)seq_at(a, p.row, t0 + i) * a.D + ch, d0);
+  for (int i = SEG - 1; i >= 0; --i) {
+    if (PACKED && ((m.last >> i) & 1)) {
+      load_seq<C>(a, a.d_final, t0 + i, ch, H);
 #pragma unroll
-      for (int c = 0; c < C; ++c) { A[c] = -0.f; H[c] = d0[c]; }
+      for (int c = 0; c < C; ++c) A[c] = -0.f;
     }
     float gv[C], dv[C];
     unpack16(gr[i], gv);
@@ -407,76 +523,20 @@ template <typename T, bool MIX> __global__ __launch_bounds__(BTHR) void scan_bwd
       H[c] = lam * (dv[c] + H[c]);
     }
   }
-  store_f32<C>(&sR[grp][cl], A);
-  store_f32<C>(&sQ[grp][cl], H);
-  __syncthreads();
-  if (tid < W) {                          // one wave: the reverse chain
-    float At = 1.f, Ht = 0.f;
-#pragma unroll 8
-    for (int q = BGRP - 1; q >= 0; --q) {
-      Ht = apply(sR[q][tid], sQ[q][tid], Ht);
-      At *= sR[q][tid];
-    }
-    float y = 0.f;
-    if (a.NC > 1) {
-      const int ng = (a.NC + GROUP - 1) / GROUP;
-      unsigned long long *agg = a.agg + p.col * a.NC * W + tid, *pre = a.pre + p.col * ng * W + tid;
-      if (p.rank + 1 < a.NC) publish(agg + (size_t)p.rank * W, word(At, Ht));
-      y = carry_in(agg, pre, p.rank, W);
-      if (p.rank % GROUP == GROUP - 1 && p.rank + 1 < a.NC)
-        publish(pre + (size_t)(p.rank / GROUP + 1) * W, word(0.f, apply(At, Ht, y)));
-    }
-#pragma unroll 8
-    for (int q = BGRP - 1; q >= 0; --q) {
-      const float Hq = sQ[q][tid];
-      sQ[q][tid] = y;
-      y = apply(sR[q][tid], Hq, y);
-    }
-  } else if (tid >= 64 && tid < 64 + W) {  // another wave: the states entering the groups
-    const int l = tid - 64;
-    float y = 0.f;
-    if (chunk > 0 && p.c0 + l < a.D) y = a.states[((size_t)p.row * a.NC + chunk - 1) * a.D + p.c0 + l];
-#pragma unroll 8
-    for (int q = 0; q < BGRP; ++q) {
-      const float Hq = sH[q][l];
-      sH[q][l] = y;
-      y = apply(sA[q][l], Hq, y);
-    }
-  }
-  __syncthreads();
-  if (m.valid == 0) return;
-  float h[C], hp[BSEG][C];                // hp: the state entering each step
-  load_f32<C>(&sH[grp][cl], h);
-#pragma unroll
-  for (int i = 0; i < BSEG; ++i) {
-    if ((m.first >> i) & 1) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) h[c] = 0.f;
-      if (a.init) load_f32<C>(a.init + (size_t)seq_at(a, p.row, t0 + i) * a.D + ch, h);
-    }
-    float xv[C], gv[C];
-    unpack16(xr[i], xv);
-    unpack16(gr[i], gv);
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const float lam = decay(gv[c]);
-      hp[i][c] = h[c];
-      h[c] = fmaf(lam, h[c], MIX ? one_minus_decay(gv[c], lam) * xv[c] : xv[c]);
-    }
-  }
+  __syncthreads();                        // every wave is done with the waves' forward maps
+  store_f32<C>(&s.A[grp][cl], A);
+  store_f32<C>(&s.H[grp][cl], H);
+  first = on && !PACKED && a.d_final ? a.d_final + c0 : nullptr;
+  const float out = scan_chunk<W, true, true>(a, s, p.col, p.rank, first);
+  if (tid < W && on && !PACKED && a.d_init && chunk == 0) a.d_init[c0 + tid] = out;
+  forget(dr);
+  forget(gr);
   float r[C];
-  load_f32<C>(&sQ[grp][cl], r);
-  T *dx = static_cast<T *>(a.dx) + at, *dg = static_cast<T *>(a.dg) + at;
+  load_f32<C>(&s.H[grp][cl], r);
 #pragma unroll
-  for (int i = BSEG - 1; i >= 0; --i) {
-    if (i >= m.valid) continue;
-    if ((m.last >> i) & 1) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) r[c] = 0.f;
-      if (a.d_final) load_f32<C>(a.d_final + (size_t)seq_at(a, p.row, t0 + i) * a.D + ch, r);
-    }
-    float xv[C], gv[C], dv[C], ox[C], og[C];
-    unpack16(xr[i], xv);
+  for (int i = SEG - 1; i >= 0; --i) {
+    if (PACKED && ((m.last >> i) & 1)) load_seq<C>(a, a.d_final, t0 + i, ch, r);
+    float gv[C], dv[C], ox[C], og[C];
     unpack16(gr[i], gv);
     unpack16(dr[i], dv);
 #pragma unroll
@@ -485,12 +545,11 @@ template <typename T, bool MIX> __global__ __launch_bounds__(BTHR) void scan_bwd
       const float delta = dv[c] + r[c];
       r[c] = lam * delta;
       ox[c] = MIX ? one_minus_decay(gv[c], lam) * delta : delta;
-      og[c] = r[c] * (MIX ? hp[i][c] - xv[c] : hp[i][c]);
+      og[c] = r[c] * e[i][c];
     }
-    *reinterpret_cast<uint4 *>(dx + (size_t)i * a.D) = pack16(ox);
-    *reinterpret_cast<uint4 *>(dg + (size_t)i * a.D) = pack16(og);
-    if (((m.first >> i) & 1) && a.d_init)
-      store_f32<C>(a.d_init + (size_t)seq_at(a, p.row, t0 + i) * a.D + ch, r);
+    st.store(a.dx, i, pack16(ox));
+    st.store(a.dg, i, pack16(og));
+    if (PACKED && ((m.first >> i) & 1)) store_seq<C>(a, a.d_init, t0 + i, ch, r);
   }
 }
 
@@ -502,8 +561,8 @@ __global__ __launch_bounds__(256) void scan_step(const T *x, const T *g, float *
   const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * C;
   if (i >= n) return;
   float xv[C], gv[C], s[C];
-  unpack16(*reinterpret_cast<const uint4 *>(x + i), xv);
-  unpack16(*reinterpret_cast<const uint4 *>(g + i), gv);
+  unpack16(*reinterpret_cast<const u4 *>(x + i), xv);
+  unpack16(*reinterpret_cast<const u4 *>(g + i), gv);
   load_f32<C>(state + i, s);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
@@ -511,7 +570,7 @@ __global__ __launch_bounds__(256) void scan_step(const T *x, const T *g, float *
     s[c] = fmaf(lam, s[c], MIX ? one_minus_decay(gv[c], lam) * xv[c] : xv[c]);
   }
   store_f32<C>(state + i, s);
-  *reinterpret_cast<uint4 *>(h + i) = pack16(s);
+  *reinterpret_cast<u4 *>(h + i) = pack16(s);
 }
 
 __global__ __launch_bounds__(256) void fill_ones(uint4 *p, size_t n) {
@@ -556,21 +615,27 @@ size_t scan_workspace(bool bf16, int rows, int T, int D) {
   return l.ticket + l.agg + l.pre;
 }
 
-#define FALCON_SCAN_LAUNCH(KERNEL, THREADS)                                                                \
-  unsigned grid = 0;                                                                                       \
-  const hipError_t e = prepare(bf16, a, ws, grid, s);                                                      \
-  if (e != hipSuccess) return e;                                                                           \
-  if (bf16 && mix) hipLaunchKernelGGL((KERNEL<__bf16, true>), dim3(grid), dim3(THREADS), 0, s, a);         \
-  else if (bf16) hipLaunchKernelGGL((KERNEL<__bf16, false>), dim3(grid), dim3(THREADS), 0, s, a);          \
-  else if (mix) hipLaunchKernelGGL((KERNEL<float, true>), dim3(grid), dim3(THREADS), 0, s, a);             \
-  else hipLaunchKernelGGL((KERNEL<float, false>), dim3(grid), dim3(THREADS), 0, s, a);                     \
+#define FALCON_SCAN_LAUNCH(KERNEL)                                                                              \
+  unsigned grid = 0;                                                                                            \
+  const hipError_t e = prepare(bf16, a, ws, grid, s);                                                           \
+  if (e != hipSuccess) return e;                                                                                \
+  switch ((bf16 ? 4 : 0) + (mix ? 2 : 0) + (a.cu ? 1 : 0)) {                                                    \
+    case 0: hipLaunchKernelGGL((KERNEL<float, false, false>), dim3(grid), dim3(THR)    , 0, s, a); break;       \
+    case 1: hipLaunchKernelGGL((KERNEL<float, false, true>), dim3(grid), dim3(THR)    , 0, s, a); break;        \
+    case 2: hipLaunchKernelGGL((KERNEL<float, true, false>), dim3(grid), dim3(THR)    , 0, s, a); break;        \
+    case 3: hipLaunchKernelGGL((KERNEL<float, true, true>), dim3(grid), dim3(THR)    , 0, s, a); break;         \
+    case 4: hipLaunchKernelGGL((KERNEL<__bf16, false, false>), dim3(grid), dim3(THR)    , 0, s, a); break;      \
+    case 5: hipLaunchKernelGGL((KERNEL<__bf16, false, true>), dim3(grid), dim3(THR)    , 0, s, a); break;       \
+    case 6: hipLaunchKernelGGL((KERNEL<__bf16, true, false>), dim3(grid), dim3(THR)    , 0, s, a); break;       \
+    default: hipLaunchKernelGGL((KERNEL<__bf16, true, true>), dim3(grid), dim3(THR)    , 0, s, a);              \
+  }                                                                                                             \
   return hipGetLastError();
 
 hipError_t launch_scan_fwd(bool bf16, bool mix, ScanArgs a, void *ws, hipStream_t s) {
-  FALCON_SCAN_LAUNCH(scan_fwd, FTHR)
+  FALCON_SCAN_LAUNCH(scan_fwd)
 }
 hipError_t launch_scan_bwd(bool bf16, bool mix, ScanArgs a, void *ws, hipStream_t s) {
-  FALCON_SCAN_LAUNCH(scan_bwd, BTHR)
+  FALCON_SCAN_LAUNCH(scan_bwd)
 }
 #undef FALCON_SCAN_LAUNCH
 

@@ -11,27 +11,47 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 
-from .falcon import (DTYPES, OK, AttnShape, FalconError, Heads, QkShape, ScanShape, _check_tensor, _ptr, _stream, lib)
+from .falcon import OK, AttnShape, FalconError, Heads, QkShape, ScanShape, _check_tensor, lib
 
 SCAN_CHUNK = 256   # FALCON_SCAN_CHUNK
 LAYOUTS = {"half": 0, "interleaved": 1}
 _HERE = contextlib.nullcontext()
 
+# A small call's time is this module's: checks are written to pass quickly (the long ones in
+# falcon.py run only to say what is wrong), and what follows from sizes alone (the C structs,
+# the workspace sizes) is kept by sizes.
+
+
+@functools.lru_cache(maxsize=None)
+def _types():
+    import torch
+    return {torch.float32: 0, torch.bfloat16: 1}
+
 
 def _dtype(name, t):
-    import torch
-    dt = {torch.float32: "fp32", torch.bfloat16: "bf16"}.get(t.dtype)
+    dt = _types().get(t.dtype)
     if dt is None:
         raise TypeError(f"{name} must be float32 or bfloat16")
-    return DTYPES[dt]
+    return dt
 
 
 def _device(name, t):
     if not t.is_cuda:
         raise ValueError(f"{name}: must live on a GPU")
     return t.device
+
+
+def _check(name, t, dtype, shape, dev):
+    """_check_tensor, quick where the tensor is as it should be."""
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        _check_tensor(name, t, dtype, shape, dev)
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
 
 
 def _on(dev, stream):
@@ -42,6 +62,20 @@ def _on(dev, stream):
             raise ValueError(f"stream: must belong to {dev}")
         return torch.cuda.stream(stream)
     return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+@functools.lru_cache(maxsize=None)
+def _raw_stream():
+    """device index -> its current HIP stream; by the short way where this torch has one
+    (making a stream object takes 2 us)."""
+    import torch
+    return getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _current(dev):
+    """The HIP stream of a call, inside its context."""
+    return _raw_stream()(dev.index)
 
 
 def _done(status, where):
@@ -62,21 +96,30 @@ def _offsets(name, cu, dev):
     import torch
     if cu.dim() != 1 or cu.numel() < 2:
         raise ValueError(f"{name}: shape {tuple(cu.shape)}, expected (sequences + 1,)")
-    _check_tensor(name, cu, torch.int32, tuple(cu.shape), dev)
+    _check(name, cu, torch.int32, cu.shape, dev)
     return cu.numel() - 1
 
 
 # ---- Gated linear recurrence ----------------------------------------------------
 
+@functools.lru_cache(maxsize=1024)
+def _scan_plan(dtype, n, T, D, mix, packed):
+    """(pointer to the C shape, workspace bytes)."""
+    shape = ScanShape(dtype, n, T, D, 1 if mix else 0)
+    return ctypes.pointer(shape), lib().falcon_scan_workspace(ctypes.byref(shape), packed)
+
+
 def _scan_shape(x, log_lambda, cu_seqlens, mix):
     dt, dev = _dtype("x", x), _device("x", x)
-    if x.dim() != (3 if cu_seqlens is None else 2):
-        raise ValueError(f"x: shape {tuple(x.shape)}, expected " + ("[B, T, D]" if cu_seqlens is None else "[total, D]"))
-    _check_tensor("x", x, x.dtype, x.shape, dev)
-    _check_tensor("log_lambda", log_lambda, x.dtype, x.shape, dev)
+    packed = cu_seqlens is not None
+    if x.dim() != (2 if packed else 3):
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected " + ("[total, D]" if packed else "[B, T, D]"))
+    _check("x", x, x.dtype, x.shape, dev)
+    _check("log_lambda", log_lambda, x.dtype, x.shape, dev)
     T, D = x.shape[-2:]
-    n = x.shape[0] if cu_seqlens is None else _offsets("cu_seqlens", cu_seqlens, dev)
-    return ScanShape(dt, n, T, D, 1 if mix else 0), n, T, D, dev
+    n = _offsets("cu_seqlens", cu_seqlens, dev) if packed else x.shape[0]
+    shape, need = _scan_plan(dt, n, T, D, bool(mix), packed)
+    return shape, need, n, D, dev
 
 
 def _states_shape(x, cu_seqlens):
@@ -95,25 +138,22 @@ def gated_scan(x, log_lambda, *, cu_seqlens=None, mix=False, init=None, final=Tr
     ``init``), or False.  ``chunk_states``: whether to keep what gated_scan_bwd needs.
     Tokens behind cu_seqlens[N] are not written.  Returns (h, final, chunk_states)."""
     import torch
-    shape, n, T, D, dev = _scan_shape(x, log_lambda, cu_seqlens, mix)
+    shape, need, n, D, dev = _scan_shape(x, log_lambda, cu_seqlens, mix)
     with _on(dev, stream):
         if out is None:
             out = torch.empty_like(x)
-        _check_tensor("h", out, x.dtype, x.shape, dev)
+        _check("h", out, x.dtype, x.shape, dev)
         if final is True:
             final = torch.empty(n, D, dtype=torch.float32, device=dev)
         elif final is False:
             final = None
         for name, t in (("init", init), ("final", final)):
             if t is not None:
-                _check_tensor(name, t, torch.float32, (n, D), dev)
+                _check(name, t, torch.float32, (n, D), dev)
         states = torch.empty(_states_shape(x, cu_seqlens), dtype=torch.float32, device=dev) if chunk_states else None
-        L = lib()
-        ws, nbytes = _workspace(L.falcon_scan_workspace(ctypes.byref(shape), cu_seqlens is not None)
-                                if T > SCAN_CHUNK else 0, workspace, dev)
-        _done(L.falcon_scan_fwd(ctypes.byref(shape), _ptr(cu_seqlens), _ptr(x), _ptr(log_lambda), _ptr(init),
-                                _ptr(final), _ptr(out), _ptr(states), _ptr(ws), nbytes, _stream(stream)),
-              "falcon_scan_fwd")
+        ws, nbytes = _workspace(need, workspace, dev)
+        _done(lib().falcon_scan_fwd(shape, _p(cu_seqlens), _p(x), _p(log_lambda), _p(init), _p(final), _p(out),
+                                    _p(states), _p(ws), nbytes, _current(dev)), "falcon_scan_fwd")
     return out, final, states
 
 
@@ -126,27 +166,25 @@ def gated_scan_bwd(x, log_lambda, dh, chunk_states, *, cu_seqlens=None, mix=Fals
     ``d_init``: True (allocate), a [N,D] float32 tensor, or False.  ``out``: None or a
     dict of preallocated dx, dg.  Returns dict(dx, dg, d_init)."""
     import torch
-    shape, n, T, D, dev = _scan_shape(x, log_lambda, cu_seqlens, mix)
-    _check_tensor("dh", dh, x.dtype, x.shape, dev)
-    _check_tensor("chunk_states", chunk_states, torch.float32, _states_shape(x, cu_seqlens), dev)
+    shape, need, n, D, dev = _scan_shape(x, log_lambda, cu_seqlens, mix)
+    _check("dh", dh, x.dtype, x.shape, dev)
+    _check("chunk_states", chunk_states, torch.float32, _states_shape(x, cu_seqlens), dev)
     with _on(dev, stream):
         if out is None:
             out = dict(dx=torch.empty_like(x), dg=torch.empty_like(x))
         for name in ("dx", "dg"):
-            _check_tensor(name, out[name], x.dtype, x.shape, dev)
+            _check(name, out[name], x.dtype, x.shape, dev)
         if d_init is True:
             d_init = torch.empty(n, D, dtype=torch.float32, device=dev)
         elif d_init is False:
             d_init = None
         for name, t in (("init", init), ("d_final", d_final), ("d_init", d_init)):
             if t is not None:
-                _check_tensor(name, t, torch.float32, (n, D), dev)
-        L = lib()
-        ws, nbytes = _workspace(L.falcon_scan_workspace(ctypes.byref(shape), cu_seqlens is not None)
-                                if T > SCAN_CHUNK else 0, workspace, dev)
-        _done(L.falcon_scan_bwd(ctypes.byref(shape), _ptr(cu_seqlens), _ptr(x), _ptr(log_lambda), _ptr(init),
-                                _ptr(chunk_states), _ptr(dh), _ptr(d_final), _ptr(out["dx"]), _ptr(out["dg"]),
-                                _ptr(d_init), _ptr(ws), nbytes, _stream(stream)), "falcon_scan_bwd")
+                _check(name, t, torch.float32, (n, D), dev)
+        ws, nbytes = _workspace(need, workspace, dev)
+        _done(lib().falcon_scan_bwd(shape, _p(cu_seqlens), _p(x), _p(log_lambda), _p(init), _p(chunk_states), _p(dh),
+                                    _p(d_final), _p(out["dx"]), _p(out["dg"]), _p(d_init), _p(ws), nbytes,
+                                    _current(dev)), "falcon_scan_bwd")
     return dict(dx=out["dx"], dg=out["dg"], d_init=d_init)
 
 
@@ -158,50 +196,56 @@ def gated_scan_step(x, log_lambda, state, *, mix=False, out=None, stream=None):
     if x.dim() != 2:
         raise ValueError(f"x: shape {tuple(x.shape)}, expected [B, D]")
     B, D = x.shape
-    _check_tensor("x", x, x.dtype, (B, D), dev)
-    _check_tensor("log_lambda", log_lambda, x.dtype, (B, D), dev)
-    _check_tensor("state", state, torch.float32, (B, D), dev)
+    _check("x", x, x.dtype, (B, D), dev)
+    _check("log_lambda", log_lambda, x.dtype, (B, D), dev)
+    _check("state", state, torch.float32, (B, D), dev)
     with _on(dev, stream):
         if out is None:
             out = torch.empty_like(x)
-        _check_tensor("h", out, x.dtype, (B, D), dev)
-        shape = ScanShape(dt, B, 1, D, 1 if mix else 0)
-        _done(lib().falcon_scan_step(ctypes.byref(shape), _ptr(x), _ptr(log_lambda), _ptr(state), _ptr(out),
-                                     _stream(stream)), "falcon_scan_step")
+        _check("h", out, x.dtype, (B, D), dev)
+        shape, _ = _scan_plan(dt, B, 1, D, bool(mix), False)
+        _done(lib().falcon_scan_step(shape, _p(x), _p(log_lambda), _p(state), _p(out), _current(dev)),
+              "falcon_scan_step")
     return out
 
 
 # ---- Heads ------------------------------------------------------------------------
 
-def _heads(name, t, dtype, dev, lead=None, heads=None, d=None):
-    """falcon_heads_t of t [..., heads, d]: dense heads, tokens one stride apart (views
-    of a wider projection are taken as they are)."""
-    if t.dtype != dtype:
+def _heads(name, t, dtype, dev, shape=None):
+    """falcon_heads_t of t [..., heads, d] (of this shape, if given): dense heads, tokens
+    one stride apart (views of a wider projection are taken as they are)."""
+    size = t.shape
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.dim() < 3:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [..., heads, d]")
-    if lead is not None and tuple(t.shape) != (*lead, heads, d):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(*lead, heads, d)}")
+    if len(size) < 3 or (shape is not None and size != shape):
+        raise ValueError(f"{name}: shape {tuple(size)}, expected {'[..., heads, d]' if shape is None else tuple(shape)}")
     if t.device != dev:
         raise ValueError(f"{name}: must live on {dev}")
-    *sizes, H, D = t.shape
-    *strides, sh, sd = t.stride()
+    *sizes, H, D = size
     step = H * D                       # the distance of two tokens, if there are two
-    want = None
-    ok = (sd == 1 or D == 1) and (sh == D or H == 1)
-    for n, s in zip(reversed(sizes), reversed(strides)):
-        if n == 1:
-            continue
-        if want is None:
-            step = s
-            want = s
-        ok = ok and s == want
-        want = want * n
-    if not ok or step < H * D:
-        raise ValueError(f"{name}: heads must be dense and tokens one stride apart")
+    if not t.is_contiguous():
+        *strides, sh, sd = t.stride()
+        want = None
+        ok = (sd == 1 or D == 1) and (sh == D or H == 1)
+        for n, s in zip(reversed(sizes), reversed(strides)):
+            if n == 1:
+                continue
+            if want is None:
+                step = want = s
+            ok = ok and s == want
+            want = want * n
+        if not ok or step < H * D:
+            raise ValueError(f"{name}: heads must be dense and tokens one stride apart")
     if (step * t.element_size()) % 16:
         raise ValueError(f"{name}: the distance of two tokens must be a multiple of 16 bytes")
     return Heads(t.data_ptr(), step)
+
+
+def _dense(t):
+    """A new dense tensor like t, and its falcon_heads_t."""
+    import torch
+    o = torch.empty_like(t, memory_format=torch.contiguous_format)
+    return o, Heads(o.data_ptr(), t.shape[-1] * t.shape[-2])
 
 
 # ---- Query / key norm with rotary positions -----------------------------------------
@@ -250,6 +294,13 @@ def rope_frequencies(rot, base=10000.0, *, scaling=None, factor=1.0, original_le
     return freq.to(device) if device is not None else freq, scale
 
 
+@functools.lru_cache(maxsize=1024)
+def _qk_plan(*sizes):
+    """(pointer to the C shape, workspace bytes of the backward)."""
+    shape = QkShape(*sizes)
+    return ctypes.pointer(shape), lib().falcon_qk_norm_rope_bwd_workspace(ctypes.byref(shape))
+
+
 def _qk_shape(q, k, positions, inv_freq, q_weight, k_weight, norm, eps, layout, rot_scale, grad_dtype):
     import torch
     if q.dim() < 3 or k.dim() < 3 or q.shape[:-2] != k.shape[:-2] or q.shape[-1] != k.shape[-1]:
@@ -258,20 +309,20 @@ def _qk_shape(q, k, positions, inv_freq, q_weight, k_weight, norm, eps, layout, 
         raise ValueError(f"layout: {layout!r}, expected 'half' or 'interleaved'")
     dt, dev = _dtype("q", q), _device("q", q)
     lead, d = q.shape[:-2], q.shape[-1]
-    tokens = math.prod(lead)
-    _check_tensor("positions", positions, torch.int32, lead, dev)
+    _check("positions", positions, torch.int32, lead, dev)
+    tokens = positions.numel()
     rot = 0
     if inv_freq is not None:
-        _check_tensor("inv_freq", inv_freq, torch.float64, (inv_freq.numel(),), dev)
+        _check("inv_freq", inv_freq, torch.float64, (inv_freq.numel(),), dev)
         rot = 2 * inv_freq.numel()
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None:
             if not norm:
                 raise ValueError(f"{name}: weights belong to the norm")
-            _check_tensor(name, w, torch.float32, (d,), dev)
-    shape = QkShape(dt, tokens, q.shape[-2], k.shape[-2], d, rot, LAYOUTS[layout], 1 if norm else 0, eps, rot_scale,
-                    dt if grad_dtype is None else grad_dtype)
-    return shape, lead, d, dev
+            _check(name, w, torch.float32, (d,), dev)
+    shape, need = _qk_plan(dt, tokens, q.shape[-2], k.shape[-2], d, rot, LAYOUTS[layout], 1 if norm else 0, eps, rot_scale,
+                           dt if grad_dtype is None else grad_dtype)
+    return shape, need, d, dev
 
 
 def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, norm=True, eps=1e-6, layout="half",
@@ -285,17 +336,17 @@ def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, nor
     no rotation), weights [d] float32.  ``layout``: "half" (pairs j, j + rot / 2) or
     "interleaved" (2 j, 2 j + 1).  ``out``: None or (q_out, k_out), which may be q and k.
     Returns (q_out, k_out)."""
-    import torch
-    shape, lead, d, dev = _qk_shape(q, k, positions, inv_freq, q_weight, k_weight, norm, eps, layout, rot_scale, None)
+    shape, _, _, dev = _qk_shape(q, k, positions, inv_freq, q_weight, k_weight, norm, eps, layout, rot_scale, None)
     hq, hk = _heads("q", q, q.dtype, dev), _heads("k", k, q.dtype, dev)
     with _on(dev, stream):
         if out is None:
-            out = (torch.empty(q.shape, dtype=q.dtype, device=dev), torch.empty(k.shape, dtype=q.dtype, device=dev))
-        oq = _heads("q_out", out[0], q.dtype, dev, lead, q.shape[-2], d)
-        ok = _heads("k_out", out[1], q.dtype, dev, lead, k.shape[-2], d)
-        _done(lib().falcon_qk_norm_rope(ctypes.byref(shape), hq, hk, _ptr(q_weight), _ptr(k_weight), _ptr(positions),
-                                        _ptr(inv_freq), oq, ok, _stream(stream)), "falcon_qk_norm_rope")
-    return out[0], out[1]
+            (yq, oq), (yk, ok) = _dense(q), _dense(k)
+        else:
+            yq, yk = out
+            oq, ok = _heads("q_out", yq, q.dtype, dev, q.shape), _heads("k_out", yk, q.dtype, dev, k.shape)
+        _done(lib().falcon_qk_norm_rope(shape, hq, hk, _p(q_weight), _p(k_weight), _p(positions), _p(inv_freq), oq, ok,
+                                        _current(dev)), "falcon_qk_norm_rope")
+    return yq, yk
 
 
 def qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, *, q_weight=None, k_weight=None, norm=True, eps=1e-6,
@@ -309,28 +360,35 @@ def qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, *, q_weight=None
     no weight was given)."""
     import torch
     grad = _dtype("dq_out", dq_out)
-    shape, lead, d, dev = _qk_shape(q, k, positions, inv_freq, q_weight, k_weight, norm, eps, layout, rot_scale, grad)
+    shape, need, d, dev = _qk_shape(q, k, positions, inv_freq, q_weight, k_weight, norm, eps, layout, rot_scale, grad)
     hq, hk = _heads("q", q, q.dtype, dev), _heads("k", k, q.dtype, dev)
-    gq = _heads("dq_out", dq_out, dq_out.dtype, dev, lead, q.shape[-2], d)
-    gk = _heads("dk_out", dk_out, dq_out.dtype, dev, lead, k.shape[-2], d)
+    gq = _heads("dq_out", dq_out, dq_out.dtype, dev, q.shape)
+    gk = _heads("dk_out", dk_out, dq_out.dtype, dev, k.shape)
     with _on(dev, stream):
         if out is None:
-            out = dict(dq=torch.empty(q.shape, dtype=q.dtype, device=dev),
-                       dk=torch.empty(k.shape, dtype=q.dtype, device=dev))
-        oq = _heads("dq", out["dq"], q.dtype, dev, lead, q.shape[-2], d)
-        ok = _heads("dk", out["dk"], q.dtype, dev, lead, k.shape[-2], d)
+            (dq, oq), (dk, ok) = _dense(q), _dense(k)
+        else:
+            dq, dk = out["dq"], out["dk"]
+            oq, ok = _heads("dq", dq, q.dtype, dev, q.shape), _heads("dk", dk, q.dtype, dev, k.shape)
         dwq = torch.empty(d, dtype=torch.float32, device=dev) if q_weight is not None else None
         dwk = torch.empty(d, dtype=torch.float32, device=dev) if k_weight is not None else None
-        L = lib()
-        some = dwq is not None or dwk is not None
-        ws, nbytes = _workspace(L.falcon_qk_norm_rope_bwd_workspace(ctypes.byref(shape)) if some else 0, workspace, dev)
-        _done(L.falcon_qk_norm_rope_bwd(ctypes.byref(shape), hq, hk, _ptr(q_weight), _ptr(k_weight), _ptr(positions),
-                                        _ptr(inv_freq), gq, gk, oq, ok, _ptr(dwq), _ptr(dwk), _ptr(ws), nbytes,
-                                        _stream(stream)), "falcon_qk_norm_rope_bwd")
-    return dict(dq=out["dq"], dk=out["dk"], dq_weight=dwq, dk_weight=dwk)
+        ws, nbytes = _workspace(need if dwq is not None or dwk is not None else 0, workspace, dev)
+        _done(lib().falcon_qk_norm_rope_bwd(shape, hq, hk, _p(q_weight), _p(k_weight), _p(positions), _p(inv_freq), gq,
+                                            gk, oq, ok, _p(dwq), _p(dwk), _p(ws), nbytes, _current(dev)),
+              "falcon_qk_norm_rope_bwd")
+    return dict(dq=dq, dk=dk, dq_weight=dwq, dk_weight=dwk)
 
 
 # ---- Causal attention -----------------------------------------------------------------
+
+@functools.lru_cache(maxsize=1024)
+def _attn_plan(packed, *sizes):
+    """(pointer to the C shape, workspace bytes of the forward, of the backward)."""
+    shape = AttnShape(*sizes)
+    L = lib()
+    return (ctypes.pointer(shape), L.falcon_attn_fwd_workspace(ctypes.byref(shape), packed),
+            L.falcon_attn_bwd_workspace(ctypes.byref(shape), packed))
+
 
 def _attn_shape(q, k, v, cu_seqlens, cu_seqlens_k, scale):
     dt, dev = _dtype("q", q), _device("q", q)
@@ -341,25 +399,24 @@ def _attn_shape(q, k, v, cu_seqlens, cu_seqlens_k, scale):
         if t.dim() != dims:
             raise ValueError(f"{name}: shape {tuple(t.shape)}, expected " +
                              ("[B, T, heads, d]" if cu_seqlens is None else "[total, heads, d]"))
-    d = q.shape[-1]
-    if cu_seqlens is None:
+    (H, d), G = q.shape[-2:], k.shape[-2]
+    packed = cu_seqlens is not None
+    if not packed:
         n, tq, tk = q.shape[0], q.shape[1], k.shape[1]
-        klead = (n, tk)
     else:
         if cu_seqlens_k is None:
             cu_seqlens_k = cu_seqlens
             if k.shape[0] != q.shape[0]:
                 raise ValueError(f"k: {k.shape[0]} tokens, expected {q.shape[0]} (without cu_seqlens_k)")
         n = _offsets("cu_seqlens", cu_seqlens, dev)
-        if _offsets("cu_seqlens_k", cu_seqlens_k, dev) != n:
+        if cu_seqlens_k is not cu_seqlens and _offsets("cu_seqlens_k", cu_seqlens_k, dev) != n:
             raise ValueError("cu_seqlens and cu_seqlens_k differ in length")
         tq, tk = q.shape[0], k.shape[0]
-        klead = (tk,)
     hq = _heads("q", q, q.dtype, dev)
-    hk = _heads("k", k, q.dtype, dev, klead, k.shape[-2], d)
-    hv = _heads("v", v, q.dtype, dev, klead, k.shape[-2], d)
-    shape = AttnShape(dt, n, tq, tk, q.shape[-2], k.shape[-2], d, d ** -0.5 if scale is None else scale)
-    return shape, cu_seqlens_k, hq, hk, hv, dev
+    hk = _heads("k", k, q.dtype, dev, (tk, G, d) if packed else (n, tk, G, d))
+    hv = _heads("v", v, q.dtype, dev, k.shape)
+    plan = _attn_plan(packed, dt, n, tq, tk, H, G, d, d ** -0.5 if scale is None else float(scale))
+    return plan, cu_seqlens_k, hq, hk, hv, dev
 
 
 def attention_fwd(q, k, v, *, cu_seqlens=None, cu_seqlens_k=None, scale=None, lse=True, out=None, workspace=None,
@@ -373,16 +430,15 @@ def attention_fwd(q, k, v, *, cu_seqlens=None, cu_seqlens_k=None, scale=None, ls
     the log-sum-exp of every row (attention_bwd needs it).
     Returns (o, lse): o like q and dense, lse [..., Hq] float32 or None."""
     import torch
-    shape, cuk, hq, hk, hv, dev = _attn_shape(q, k, v, cu_seqlens, cu_seqlens_k, scale)
+    (shape, fwd_bytes, _), cuk, hq, hk, hv, dev = _attn_shape(q, k, v, cu_seqlens, cu_seqlens_k, scale)
     with _on(dev, stream):
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        _check_tensor("o", out, q.dtype, q.shape, dev)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        _check("o", out, q.dtype, q.shape, dev)
         rows = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev) if lse else None
-        L = lib()
-        ws, nbytes = _workspace(L.falcon_attn_fwd_workspace(ctypes.byref(shape), cuk is not None), workspace, dev)
-        _done(L.falcon_attn_fwd(ctypes.byref(shape), _ptr(cu_seqlens), _ptr(cuk), hq, hk, hv, _ptr(out), _ptr(rows),
-                                _ptr(ws), nbytes, _stream(stream)), "falcon_attn_fwd")
+        ws, nbytes = _workspace(fwd_bytes, workspace, dev)
+        _done(lib().falcon_attn_fwd(shape, _p(cu_seqlens), _p(cuk), hq, hk, hv, _p(out), _p(rows),
+                                _p(ws), nbytes, _current(dev)), "falcon_attn_fwd")
     return out, rows
 
 
@@ -392,21 +448,19 @@ def attention_bwd(q, k, v, o, lse, do, *, cu_seqlens=None, cu_seqlens_k=None, sc
     same arguments, which gave o and lse.  ``out``: None or a dict of preallocated dq, dk,
     dv (views with dense heads will do).  Returns dict(dq, dk, dv) in the dtype of q."""
     import torch
-    shape, cuk, hq, hk, hv, dev = _attn_shape(q, k, v, cu_seqlens, cu_seqlens_k, scale)
-    _check_tensor("o", o, q.dtype, q.shape, dev)
-    _check_tensor("lse", lse, torch.float32, q.shape[:-1], dev)
-    lq, lk, H, G, d = q.shape[:-2], k.shape[:-2], q.shape[-2], k.shape[-2], q.shape[-1]
-    hdo = _heads("do", do, q.dtype, dev, lq, H, d)
+    (shape, _, bwd_bytes), cuk, hq, hk, hv, dev = _attn_shape(q, k, v, cu_seqlens, cu_seqlens_k, scale)
+    _check("o", o, q.dtype, q.shape, dev)
+    _check("lse", lse, torch.float32, q.shape[:-1], dev)
+    hdo = _heads("do", do, q.dtype, dev, q.shape)
     with _on(dev, stream):
         if out is None:
-            out = dict(dq=torch.empty(q.shape, dtype=q.dtype, device=dev),
-                       dk=torch.empty(k.shape, dtype=q.dtype, device=dev),
-                       dv=torch.empty(k.shape, dtype=q.dtype, device=dev))
-        hdq = _heads("dq", out["dq"], q.dtype, dev, lq, H, d)
-        hdk = _heads("dk", out["dk"], q.dtype, dev, lk, G, d)
-        hdv = _heads("dv", out["dv"], q.dtype, dev, lk, G, d)
-        L = lib()
-        ws, nbytes = _workspace(L.falcon_attn_bwd_workspace(ctypes.byref(shape), cuk is not None), workspace, dev)
-        _done(L.falcon_attn_bwd(ctypes.byref(shape), _ptr(cu_seqlens), _ptr(cuk), hq, hk, hv, _ptr(o), _ptr(lse), hdo,
-                                hdq, hdk, hdv, _ptr(ws), nbytes, _stream(stream)), "falcon_attn_bwd")
-    return dict(dq=out["dq"], dk=out["dk"], dv=out["dv"])
+            (dq, hdq), (dk, hdk), (dv, hdv) = _dense(q), _dense(k), _dense(v)
+        else:
+            dq, dk, dv = out["dq"], out["dk"], out["dv"]
+            hdq = _heads("dq", dq, q.dtype, dev, q.shape)
+            hdk = _heads("dk", dk, q.dtype, dev, k.shape)
+            hdv = _heads("dv", dv, q.dtype, dev, k.shape)
+        ws, nbytes = _workspace(bwd_bytes, workspace, dev)
+        _done(lib().falcon_attn_bwd(shape, _p(cu_seqlens), _p(cuk), hq, hk, hv, _p(o), _p(lse), hdo,
+                                hdq, hdk, hdv, _p(ws), nbytes, _current(dev)), "falcon_attn_bwd")
+    return dict(dq=dq, dk=dk, dv=dv)
