@@ -15,11 +15,13 @@
 #pragma once
 #include <hip/hip_runtime.h>
 
+#include "layer_kernels.h"
 #include "mfma_frag.h"
 
 namespace falcon {
 
 typedef float f16v __attribute__((ext_vector_type(16)));
+typedef unsigned int uint4v __attribute__((ext_vector_type(4)));
 
 template <typename T> struct Frag;
 template <> struct Frag<__bf16> { bf8 v; };
@@ -129,6 +131,51 @@ __device__ __forceinline__ Slot find_slot(const int *cu, int N, int slot, int mu
     if ((int)((int64_t)cu[mid] * mul / per) + mid <= slot) lo = mid; else hi = mid - 1;
   }
   return Slot{lo, slot - ((int)((int64_t)cu[lo] * mul / per) + lo)};
+}
+
+// 16 bytes a lane from global memory (a scalar base plus 32 bits a lane) straight into LDS, lane
+// l's to lds + 16 l.  The compiler does not count these: copies_done() before the barrier that
+// hands the tile over.
+__device__ __forceinline__ void copy_to_lds(const void *base, unsigned offset, unsigned lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(offset), "s"(base), "s"(lds)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ unsigned lds_address(const void *p) {
+  return (unsigned)(size_t)(__attribute__((address_space(3))) const void *)p;
+}
+
+// The share of one thread of 256 in copying tiles of ROWS rows of D entries: PER pieces of 16
+// bytes, piece i of wave w being the tile's places 64 (4 i + w) .. + 63.
+template <typename T, int D, int ROWS> struct Copy {
+  typedef Tile<T, D> Ti;
+  static constexpr int CH = ROWS * Ti::CPR, PER = (CH + 255) / 256;
+  static constexpr bool ALL = CH % 256 == 0;     // else the last waves have nothing to copy
+  static __device__ __forceinline__ bool has(int i, int wave) { return ALL || 64 * (4 * i + wave) < CH; }
+  static __device__ __forceinline__ int row(int i, int tid) { return (256 * i + tid) / Ti::CPR; }
+  // bytes of the piece within its row: the chunk whose place this is
+  static __device__ __forceinline__ unsigned byte(int i, int tid) {
+    return (((256 * i + tid) % Ti::CPR) ^ Ti::swizzle(row(i, tid))) * 16;
+  }
+  static __device__ __forceinline__ unsigned to(const uint4 *tile, int i, int wave) {
+    return lds_address(tile + 64 * (4 * i + wave));
+  }
+};
+
+// A sequence's token ranges, kept inside the arrays whatever the offsets hold.
+struct Seq { int q0, Lq, k0, Lk; };
+__device__ __forceinline__ void clamp_range(const int *cu, int n, int total, int &begin, int &length) {
+  begin = min(max(cu[n], 0), total);
+  length = max(min(cu[n + 1], total) - begin, 0);
+}
+__device__ __forceinline__ Seq seq_of(const AttnArgs &a, int n) {
+  if (!a.cuq) return Seq{n * a.Tq, a.Tq, n * a.Tk, a.Tk};
+  Seq s;
+  clamp_range(a.cuq, n, a.Tq, s.q0, s.Lq);
+  clamp_range(a.cuk, n, a.Tk, s.k0, s.Lk);
+  return s;
 }
 
 // max / sum with the lane 32 away.

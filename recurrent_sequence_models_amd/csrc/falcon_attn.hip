@@ -29,93 +29,95 @@ template <typename T, int D> struct Fwd {
   // (fp32 at d = 128).
   static constexpr int TN = (sizeof(T) * D > 256) ? 32 : 64;
   static constexpr int CH = TN * Tile<T, D>::CPR;          // chunks of a tile
-  static constexpr int PER = CH / THR;                     // chunks a thread moves
   static constexpr int KB = TN / 32;
-  static_assert(PER * THR == CH, "every thread moves whole chunks");
 };
 
-template <typename T, int D> __global__ __launch_bounds__(THR) void attn_fwd(AttnArgs a) {
+template <typename T, int D> __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_fwd(AttnArgs a) {
   typedef Fwd<T, D> F;
   typedef Tile<T, D> Ti;
   constexpr int TN = F::TN, DB = D / 16, CB = D / 32;
   __shared__ uint4 sk[2][F::CH], sv[2][F::CH];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 31, h = lane >> 5;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 31, h = lane >> 5;
 
   // key head fastest (a head stays on one die where 8 and hk divide one another), then the
   // split of the keys, then the tiles
-  int id = blockIdx.x;
-  const int head = id % a.hk;
-  id /= a.hk;
-  const int split = id % a.splits;
-  int n, tile, q0, Lq, k0, Lk;
+  unsigned id = blockIdx.x;
+  const int head = id % (unsigned)a.hk;
+  id /= (unsigned)a.hk;
+  const int split = id % (unsigned)a.splits;
+  id /= (unsigned)a.splits;
+  int n, tile;
   if (a.cuq) {
-    const Slot s = find_slot(a.cuq, a.n, id / a.splits, a.group, TM);
+    const Slot s = find_slot(a.cuq, a.n, id, a.group, TM);
     n = s.n;
-    q0 = a.cuq[n]; Lq = a.cuq[n + 1] - q0;
-    k0 = a.cuk[n]; Lk = a.cuk[n + 1] - k0;
     tile = s.tile;
   } else {
-    n = (id / a.splits) % a.n;
-    tile = (id / a.splits) / a.n;
-    q0 = n * a.Tq; Lq = a.Tq;
-    k0 = n * a.Tk; Lk = a.Tk;
+    n = id % (unsigned)a.n;
+    tile = id / (unsigned)a.n;
   }
-  const int64_t rows = (int64_t)Lq * a.group;
-  const int tiles = (int)((rows + TM - 1) / TM);
+  const Seq q = seq_of(a, n);
+  const int rows = q.Lq * a.group, tiles = (rows + TM - 1) / TM;
   if (tile >= tiles) return;
   tile = tiles - 1 - tile;                      // the tiles with the most keys start first
 
-  const int64_t r = (int64_t)tile * TM + wave * 32 + c;
-  const bool on = r < rows;
-  const int tok = (int)((on ? r : rows - 1) / a.group), hq = head * a.group + (int)((on ? r : rows - 1) % a.group);
-  const int lim = tok + Lk - Lq;                // the last key this row sees
-  const int first_lim = (int)(min((int64_t)tile * TM + wave * 32, rows - 1) / a.group) + Lk - Lq;
-  const int last_lim = (int)(min((int64_t)tile * TM + TM - 1, rows - 1) / a.group) + Lk - Lq;
-  const int keys = max(min(Lk, last_lim + 1), 0), ktiles = (keys + TN - 1) / TN;
+  const int off = q.Lk - q.Lq, r0 = tile * TM + wave * 32;
+  const int r = min(r0 + c, rows - 1);
+  const bool on = r0 + c < rows;
+  const int tok = r / (unsigned)a.group, hq = head * a.group + (r - tok * a.group);
+  const int lim = tok + off;                    // the last key this row sees
+  const int first_lim = (int)((unsigned)min(r0, rows - 1) / (unsigned)a.group) + off;
+  const int wave_lim = (int)((unsigned)min(r0 + 31, rows - 1) / (unsigned)a.group) + off;
+  const int last_lim = (int)((unsigned)min(tile * TM + TM - 1, rows - 1) / (unsigned)a.group) + off;
+  const int keys = max(min(q.Lk, last_lim + 1), 0), ktiles = (keys + TN - 1) / TN;
   const int kt0 = (int)((int64_t)ktiles * split / a.splits), kt1 = (int)((int64_t)ktiles * (split + 1) / a.splits);
 
-  const T *qrow = static_cast<const T *>(a.q) + (int64_t)(q0 + tok) * a.ldq + hq * D;
+  const T *qrow = static_cast<const T *>(a.q) + (int64_t)(q.q0 + tok) * a.ldq + hq * D;
   Frag<T> qf[DB];
 #pragma unroll
   for (int b = 0; b < DB; ++b) qf[b] = global_frag(qrow, b, h);
 
-  // staging: rows past the sequence are zeros (their values must not be read: they are
-  // another sequence's or unset, and 0 times an infinity is not 0)
-  const T *kg = static_cast<const T *>(a.k) + (int64_t)k0 * a.ldk + head * D;
-  const T *vg = static_cast<const T *>(a.v) + (int64_t)k0 * a.ldv + head * D;
-  uint4 kr[F::PER], vr[F::PER];
-  auto fetch = [&](int kt) {
+  // Copying tiles.  Rows past the sequence's keys repeat its last one: no row of another
+  // sequence is read, and their weights are 0.
+  typedef Copy<T, D, TN> Cp;
+  const T *kg = static_cast<const T *>(a.k) + (int64_t)q.k0 * a.ldk + head * D;
+  const T *vg = static_cast<const T *>(a.v) + (int64_t)q.k0 * a.ldv + head * D;
+  const unsigned kstep = (unsigned)a.ldk * sizeof(T), vstep = (unsigned)a.ldv * sizeof(T);
+  unsigned ko[Cp::PER], vo[Cp::PER];
 #pragma unroll
-    for (int i = 0; i < F::PER; ++i) {
-      const int e = tid + i * THR, row = e / Ti::CPR, ch = e % Ti::CPR;
-      const int key = kt * TN + row;
-      kr[i] = vr[i] = uint4{0, 0, 0, 0};
-      if (key < Lk) {
-        kr[i] = *reinterpret_cast<const uint4 *>(kg + (int64_t)key * a.ldk + ch * Ti::E);
-        vr[i] = *reinterpret_cast<const uint4 *>(vg + (int64_t)key * a.ldv + ch * Ti::E);
+  for (int i = 0; i < Cp::PER; ++i) {
+    ko[i] = Cp::row(i, tid) * kstep + Cp::byte(i, tid);
+    vo[i] = Cp::row(i, tid) * vstep + Cp::byte(i, tid);
+  }
+  auto copy = [&](int kt, int buf) {
+    const T *kp = kg + (int64_t)kt * TN * a.ldk, *vp = vg + (int64_t)kt * TN * a.ldv;
+    const int last = q.Lk - 1 - kt * TN;
+#pragma unroll
+    for (int i = 0; i < Cp::PER; ++i) {
+      if (!Cp::has(i, wave)) continue;
+      unsigned kb = ko[i], vb = vo[i];
+      if (last < TN - 1) {                      // the sequence's last tile
+        const int row = min(Cp::row(i, tid), last);
+        kb = row * kstep + Cp::byte(i, tid);
+        vb = row * vstep + Cp::byte(i, tid);
       }
-    }
-  };
-  auto stage = [&](int buf) {
-#pragma unroll
-    for (int i = 0; i < F::PER; ++i) {
-      const int e = tid + i * THR, row = e / Ti::CPR, ch = e % Ti::CPR;
-      sk[buf][Ti::place(row, ch)] = kr[i];
-      sv[buf][Ti::place(row, ch)] = vr[i];
+      copy_to_lds(kp, kb, Cp::to(sk[buf], i, wave));
+      copy_to_lds(vp, vb, Cp::to(sv[buf], i, wave));
     }
   };
 
   f16v acc[CB];
 #pragma unroll
   for (int b = 0; b < CB; ++b) acc[b] = zero16();
-  float m = -INFINITY, l = 0.f;                 // maximum in units of the raw scores; this lane's half of the sum
+  float m = -INFINITY, l = 0.f;                 // the weights' reference score; this lane's half of the sum
   const float sc = a.scale * kLog2e;
 
-  if (kt0 < kt1) { fetch(kt0); stage(0); }
+  if (kt0 < kt1) copy(kt0, 0);
+  copies_done();
   __syncthreads();
   for (int kt = kt0; kt < kt1; ++kt) {
     const int buf = (kt - kt0) & 1;
-    if (kt + 1 < kt1) fetch(kt + 1);
+    if (kt + 1 < kt1) copy(kt + 1, buf ^ 1);    // its last readers are behind the barrier
+    if (kt * TN <= wave_lim) {                  // else no row of this wave sees a key of the tile
     f16v s[F::KB];
 #pragma unroll
     for (int kb = 0; kb < F::KB; ++kb) {
@@ -124,26 +126,30 @@ template <typename T, int D> __global__ __launch_bounds__(THR) void attn_fwd(Att
       for (int b = 0; b < DB; ++b) mma(s[kb], Ti::rows(sk[buf], kb * 32, b, lane), qf[b]);
     }
     if (kt * TN + TN - 1 > first_lim) {         // the same for the whole wave
+      const int left = lim - kt * TN - 4 * h;   // key 8 (i / 4) + 4 h + i % 4 of the tile is seen up to here
 #pragma unroll
       for (int kb = 0; kb < F::KB; ++kb)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (kt * TN + kb * 32 + 8 * (i / 4) + 4 * h + (i & 3) > lim) s[kb][i] = -INFINITY;
+          if (kb * 32 + 8 * (i / 4) + (i & 3) > left) s[kb][i] = -INFINITY;
     }
-    float top = m;
+    float top = s[0][0];
 #pragma unroll
     for (int kb = 0; kb < F::KB; ++kb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kb][i]);
     top = max_xor32(top);
-    const float shift = top == -INFINITY ? 0.f : top * sc;   // nothing seen yet: every weight is e^-inf = 0
-    if (__any(top > m)) {
-      const float f = __builtin_amdgcn_exp2f(m * sc - shift);
+    // The reference follows the maximum when that has grown by over 8 (base 2): weights stay
+    // below 2^8, and most tiles rescale nothing.  (-inf: nothing seen yet, any weight is 0.)
+    if (__any(top * sc > m * sc + 8.f)) {
+      const float now = fmaxf(top, m);
+      const float f = now == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - now) * sc);
       l *= f;
 #pragma unroll
       for (int b = 0; b < CB; ++b) acc[b] *= f;
-      m = top;
+      m = now;
     }
+    const float shift = m == -INFINITY ? 0.f : m * sc;
     float sum = 0.f;
 #pragma unroll
     for (int kb = 0; kb < F::KB; ++kb)
@@ -161,36 +167,36 @@ template <typename T, int D> __global__ __launch_bounds__(THR) void attn_fwd(Att
 #pragma unroll
         for (int b = 0; b < CB; ++b) mma(acc[b], Ti::cols(sv[buf], kb * 32 + b16 * 16, b * 32, lane), pf);
       }
-    if (kt + 1 < kt1) stage(buf ^ 1);
+    }
+    copies_done();
     __syncthreads();
   }
   l = sum_xor32(l);
   if (!on) return;
+  const size_t at = (size_t)(q.q0 + tok) * a.hq + hq;
   if (a.splits > 1) {   // unnormalised: [split][row of the packed axis and head][d], then (m, l)
-    const size_t nrow = (size_t)(a.cuq ? a.Tq : a.n * (int64_t)a.Tq) * a.hq;
-    const size_t at = split * nrow + (size_t)(q0 + tok) * a.hq + hq;
-    float *p = a.part + at * D;
+    const size_t nrow = (size_t)(a.cuq ? a.Tq : a.n * (int64_t)a.Tq) * a.hq, ps = split * nrow + at;
+    float *p = a.part + ps * D;
 #pragma unroll
     for (int b = 0; b < CB; ++b)
 #pragma unroll
       for (int i = 0; i < 16; i += 4)
         store4(p + b * 32 + 2 * i + 4 * h, acc[b][i], acc[b][i + 1], acc[b][i + 2], acc[b][i + 3]);
     if (h == 0) {
-      float *ml = a.part + a.splits * nrow * D + at * 2;
+      float *ml = a.part + a.splits * nrow * D + ps * 2;
       ml[0] = m * sc;
       ml[1] = l;
     }
     return;
   }
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // NaN stays NaN
-  T *out = static_cast<T *>(a.out) + ((int64_t)(q0 + tok) * a.hq + hq) * D;
+  T *out = static_cast<T *>(a.out) + at * D;
 #pragma unroll
   for (int b = 0; b < CB; ++b)
 #pragma unroll
     for (int i = 0; i < 16; i += 4)
       store4(out + b * 32 + 2 * i + 4 * h, acc[b][i] * inv, acc[b][i + 1] * inv, acc[b][i + 2] * inv, acc[b][i + 3] * inv);
-  if (h == 0 && a.lse)
-    a.lse[(int64_t)(q0 + tok) * a.hq + hq] = l == 0.f ? -INFINITY : kLn2 * (m * sc + __builtin_amdgcn_logf(l));
+  if (h == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : kLn2 * (m * sc + __builtin_amdgcn_logf(l));
 }
 
 // Joins the splits of a row: one thread per 4 entries.

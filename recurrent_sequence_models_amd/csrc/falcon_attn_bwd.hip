@@ -40,126 +40,123 @@ template <typename T, int D> __global__ __launch_bounds__(THR) void attn_delta(A
   if (row < nrow && e == 0) a.delta[row] = s;
 }
 
-struct Seq { int q0, Lq, k0, Lk; };
-__device__ __forceinline__ Seq seq_of(const AttnArgs &a, int n) {
-  if (a.cuq) return Seq{a.cuq[n], a.cuq[n + 1] - a.cuq[n], a.cuk[n], a.cuk[n + 1] - a.cuk[n]};
-  return Seq{n * a.Tq, a.Tq, n * a.Tk, a.Tk};
-}
-
 // ---- dk, dv ------------------------------------------------------------------
-template <typename T, int D> __global__ __launch_bounds__(THR, 1) void attn_bwd_kv(AttnArgs a) {
+template <typename T, int D>
+__global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_kv(AttnArgs a) {
   typedef Tile<T, D> Ti;
-  constexpr int TQ = 32, CH = TQ * Ti::CPR, PER = (CH + THR - 1) / THR, DB = D / 16, CB = D / 32;
-  __shared__ uint4 sq[2][CH], sg[2][CH];
+  constexpr int TQ = 32, DB = D / 16, CB = D / 32;
+  typedef Copy<T, D, TQ> Cp;
+  __shared__ uint4 sq[2][Cp::CH], sg[2][Cp::CH];
   __shared__ __align__(16) float sL[2][TQ], sD[2][TQ];   // lse (base 2) and D of the rows
   __shared__ __align__(16) int sM[2][TQ];                // the last key each row sees
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 31, h = lane >> 5;
-  const int head = blockIdx.x % a.hk, slot = blockIdx.x / a.hk;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 31, h = lane >> 5;
+  const int head = blockIdx.x % (unsigned)a.hk, slot = blockIdx.x / (unsigned)a.hk;
   int n, tile;
   if (a.cuk) {
     const Slot s = find_slot(a.cuk, a.n, slot, 1, TR);
     n = s.n; tile = s.tile;
   } else {
-    n = slot % a.n; tile = slot / a.n;
+    n = slot % (unsigned)a.n; tile = slot / (unsigned)a.n;
   }
   const Seq q = seq_of(a, n);
   if (tile >= (q.Lk + TR - 1) / TR) return;               // tile 0, which most rows see, starts first
-  const int key0 = tile * TR, key = key0 + wave * 32 + c;
+  const int key0 = tile * TR, wkey = key0 + wave * 32, key = wkey + c;
   const bool on = key < q.Lk;
-  const int64_t rows = (int64_t)q.Lq * a.group;
-  const int off = q.Lk - q.Lq;
+  const int rows = q.Lq * a.group, off = q.Lk - q.Lq;
   // the first row that sees a key of this tile, down to a whole tile of rows
-  const int64_t r_first = min((int64_t)max(key0 - off, 0) * a.group, rows) / TQ * TQ;
-  const int tiles = (int)((rows - r_first + TQ - 1) / TQ);
+  const int r_first = min(max(key0 - off, 0), q.Lq) * a.group / TQ * TQ;
+  const int tiles = (rows - r_first + TQ - 1) / TQ;
 
   Frag<T> kf[DB], vf[DB];
   {
-    const T *kp = static_cast<const T *>(a.k) + (int64_t)(q.k0 + key) * a.ldk + head * D;
-    const T *vp = static_cast<const T *>(a.v) + (int64_t)(q.k0 + key) * a.ldv + head * D;
+    const T *kp = static_cast<const T *>(a.k) + (int64_t)(q.k0 + min(key, q.Lk - 1)) * a.ldk + head * D;
+    const T *vp = static_cast<const T *>(a.v) + (int64_t)(q.k0 + min(key, q.Lk - 1)) * a.ldv + head * D;
 #pragma unroll
     for (int b = 0; b < DB; ++b) {
-      kf[b] = vf[b] = zero_frag(T());
-      if (on) { kf[b] = global_frag(kp, b, h); vf[b] = global_frag(vp, b, h); }
+      kf[b] = global_frag(kp, b, h);
+      vf[b] = global_frag(vp, b, h);
     }
   }
-  uint4 qr[PER], gr[PER];
+  // Copying tiles of rows: rows past the sequence's repeat its last one, and their weights are
+  // 0 (lse = inf).  A row's token is its number over the group, by a multiplication: exact for
+  // the numbers up to group + 31 left when the tile's first token is taken off.
+  const T *qg = static_cast<const T *>(a.q) + (int64_t)q.q0 * a.ldq + head * a.group * D;
+  const T *gg = static_cast<const T *>(a.d_o) + (int64_t)q.q0 * a.lddo + head * a.group * D;
+  const float inv = 1.f / a.group;
+  auto token = [&](int rel) { return (int)((rel + 0.5f) * inv); };
   float rl = 0.f, rd = 0.f;
   int rm = 0;
-  auto fetch = [&](int t) {
-    const int64_t rt = r_first + (int64_t)t * TQ;
+  auto copy = [&](int t, int buf) {
+    const int rt = r_first + t * TQ, tb = rt / (unsigned)a.group, r0 = tb * a.group;
+    const T *qp = qg + (int64_t)tb * a.ldq, *gp = gg + (int64_t)tb * a.lddo;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = tid + i * THR, row = e / Ti::CPR, ch = e % Ti::CPR;
-      const int64_t r = rt + row;
-      qr[i] = gr[i] = uint4{0, 0, 0, 0};
-      if (e < CH && r < rows) {
-        const int tok = (int)(r / a.group), hq = head * a.group + (int)(r - (int64_t)tok * a.group);
-        qr[i] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) + (int64_t)(q.q0 + tok) * a.ldq + hq * D + ch * Ti::E);
-        gr[i] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.d_o) + (int64_t)(q.q0 + tok) * a.lddo + hq * D + ch * Ti::E);
-      }
+    for (int i = 0; i < Cp::PER; ++i) {
+      if (!Cp::has(i, wave)) continue;
+      const int rel = min(rt + Cp::row(i, tid), rows - 1) - r0, tok = token(rel), hh = rel - tok * a.group;
+      const unsigned in = hh * D * sizeof(T) + Cp::byte(i, tid);
+      copy_to_lds(qp, tok * (unsigned)a.ldq * sizeof(T) + in, Cp::to(sq[buf], i, wave));
+      copy_to_lds(gp, tok * (unsigned)a.lddo * sizeof(T) + in, Cp::to(sg[buf], i, wave));
     }
     if (tid < TQ) {
-      const int64_t r = rt + tid;
-      rl = INFINITY; rd = 0.f; rm = -1;                    // rows outside: P = e^-inf = 0
-      if (r < rows) {
-        const int tok = (int)(r / a.group), hq = head * a.group + (int)(r - (int64_t)tok * a.group);
-        const int64_t at = (int64_t)(q.q0 + tok) * a.hq + hq;
+      rl = INFINITY; rd = 0.f; rm = -1;
+      if (rt + tid < rows) {
+        const int rel = rt + tid - r0, tok = token(rel), hh = rel - tok * a.group;
+        const int64_t at = (int64_t)(q.q0 + tb + tok) * a.hq + head * a.group + hh;
         const float lse = a.lse_in[at];
         rl = lse == -INFINITY ? INFINITY : lse * kLog2e;   // a row that sees nothing
         rd = a.delta[at];
-        rm = tok + off;
+        rm = tb + tok + off;
       }
     }
   };
-  auto stage = [&](int buf) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = tid + i * THR, row = e / Ti::CPR, ch = e % Ti::CPR;
-      if (e < CH) {
-        sq[buf][Ti::place(row, ch)] = qr[i];
-        sg[buf][Ti::place(row, ch)] = gr[i];
-      }
-    }
+  auto hand_over = [&](int buf) {
     if (tid < TQ) { sL[buf][tid] = rl; sD[buf][tid] = rd; sM[buf][tid] = rm; }
+    copies_done();
+    __syncthreads();
   };
   f16v dk[CB], dv[CB];
 #pragma unroll
   for (int b = 0; b < CB; ++b) dk[b] = dv[b] = zero16();
   const float sc = a.scale * kLog2e;
-  if (tiles > 0) { fetch(0); stage(0); }
-  __syncthreads();
+  if (tiles > 0) copy(0, 0);
+  hand_over(0);
   for (int t = 0; t < tiles; ++t) {
-    const int buf = t & 1;
-    if (t + 1 < tiles) fetch(t + 1);
-    f16v s = zero16(), g = zero16();
+    const int buf = t & 1, rt = r_first + t * TQ;
+    if (t + 1 < tiles) copy(t + 1, buf ^ 1);               // its last readers are behind the barrier
+    const int first_lim = (int)(rt / (unsigned)a.group) + off;
+    const int last_lim = (int)(min(rt + TQ - 1, rows - 1) / (unsigned)a.group) + off;
+    if (wkey <= last_lim) {                                // else no row of the tile sees a key of this wave
+      f16v s = zero16(), g = zero16();
 #pragma unroll
-    for (int b = 0; b < DB; ++b) mma(s, Ti::rows(sq[buf], 0, b, lane), kf[b]);
+      for (int b = 0; b < DB; ++b) mma(s, Ti::rows(sq[buf], 0, b, lane), kf[b]);
 #pragma unroll
-    for (int b = 0; b < DB; ++b) mma(g, Ti::rows(sg[buf], 0, b, lane), vf[b]);
+      for (int b = 0; b < DB; ++b) mma(g, Ti::rows(sg[buf], 0, b, lane), vf[b]);
+      const bool masked = wkey + 31 > first_lim;
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const f4 L = *reinterpret_cast<const f4 *>(&sL[buf][8 * b + 4 * h]);
-      const f4 Dr = *reinterpret_cast<const f4 *>(&sD[buf][8 * b + 4 * h]);
-      const int4 M = *reinterpret_cast<const int4 *>(&sM[buf][8 * b + 4 * h]);
-      const int lim[4] = {M.x, M.y, M.z, M.w};
+      for (int b = 0; b < 4; ++b) {
+        const f4 L = *reinterpret_cast<const f4 *>(&sL[buf][8 * b + 4 * h]);
+        const f4 Dr = *reinterpret_cast<const f4 *>(&sD[buf][8 * b + 4 * h]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float p = __builtin_amdgcn_exp2f(fmaf(s[4 * b + i], sc, -L[i]));
-        if (key > lim[i]) p = 0.f;
-        s[4 * b + i] = p;
-        g[4 * b + i] = p * (g[4 * b + i] - Dr[i]);
+        for (int i = 0; i < 4; ++i) s[4 * b + i] = __builtin_amdgcn_exp2f(fmaf(s[4 * b + i], sc, -L[i]));
+        if (masked) {
+          const int4 M = *reinterpret_cast<const int4 *>(&sM[buf][8 * b + 4 * h]);
+          const int lim[4] = {M.x, M.y, M.z, M.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[4 * b + i] = key > lim[i] ? 0.f : s[4 * b + i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) g[4 * b + i] = s[4 * b + i] * (g[4 * b + i] - Dr[i]);
+      }
+#pragma unroll
+      for (int b16 = 0; b16 < 2; ++b16) {
+        const Frag<T> pf = result_frag<T>(s, b16), gf = result_frag<T>(g, b16);
+#pragma unroll
+        for (int b = 0; b < CB; ++b) mma(dv[b], Ti::cols(sg[buf], b16 * 16, b * 32, lane), pf);
+#pragma unroll
+        for (int b = 0; b < CB; ++b) mma(dk[b], Ti::cols(sq[buf], b16 * 16, b * 32, lane), gf);
       }
     }
-#pragma unroll
-    for (int b16 = 0; b16 < 2; ++b16) {
-      const Frag<T> pf = result_frag<T>(s, b16), gf = result_frag<T>(g, b16);
-#pragma unroll
-      for (int b = 0; b < CB; ++b) mma(dv[b], Ti::cols(sg[buf], b16 * 16, b * 32, lane), pf);
-#pragma unroll
-      for (int b = 0; b < CB; ++b) mma(dk[b], Ti::cols(sq[buf], b16 * 16, b * 32, lane), gf);
-    }
-    if (t + 1 < tiles) stage(buf ^ 1);
-    __syncthreads();
+    hand_over(buf ^ 1);
   }
   if (!on) return;
   T *pk = static_cast<T *>(a.dk) + (int64_t)(q.k0 + key) * a.lddk + head * D;
@@ -175,30 +172,32 @@ template <typename T, int D> __global__ __launch_bounds__(THR, 1) void attn_bwd_
 }
 
 // ---- dq ----------------------------------------------------------------------
-template <typename T, int D> __global__ __launch_bounds__(THR, 1) void attn_bwd_q(AttnArgs a) {
+template <typename T, int D>
+__global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_q(AttnArgs a) {
   typedef Tile<T, D> Ti;
-  constexpr int TN = 32, CH = TN * Ti::CPR, PER = (CH + THR - 1) / THR, DB = D / 16, CB = D / 32;
-  __shared__ uint4 sk[2][CH], sv[2][CH];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 31, h = lane >> 5;
-  const int head = blockIdx.x % a.hk, slot = blockIdx.x / a.hk;
+  constexpr int TN = 32, DB = D / 16, CB = D / 32;
+  typedef Copy<T, D, TN> Cp;
+  __shared__ uint4 sk[2][Cp::CH], sv[2][Cp::CH];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 31, h = lane >> 5;
+  const int head = blockIdx.x % (unsigned)a.hk, slot = blockIdx.x / (unsigned)a.hk;
   int n, tile;
   if (a.cuq) {
     const Slot s = find_slot(a.cuq, a.n, slot, a.group, TR);
     n = s.n; tile = s.tile;
   } else {
-    n = slot % a.n; tile = slot / a.n;
+    n = slot % (unsigned)a.n; tile = slot / (unsigned)a.n;
   }
   const Seq q = seq_of(a, n);
-  const int64_t rows = (int64_t)q.Lq * a.group;
-  const int tiles = (int)((rows + TR - 1) / TR);
+  const int rows = q.Lq * a.group, tiles = (rows + TR - 1) / TR;
   if (tile >= tiles) return;
   tile = tiles - 1 - tile;
-  const int off = q.Lk - q.Lq;
-  const int64_t r = (int64_t)tile * TR + wave * 32 + c;
-  const bool on = r < rows;
-  const int tok = (int)((on ? r : rows - 1) / a.group), hq = head * a.group + (int)((on ? r : rows - 1) % a.group);
+  const int off = q.Lk - q.Lq, r0 = tile * TR + wave * 32, r = min(r0 + c, rows - 1);
+  const bool on = r0 + c < rows;
+  const int tok = r / (unsigned)a.group, hq = head * a.group + (r - tok * a.group);
   const int lim = tok + off;
-  const int last_lim = (int)(min((int64_t)tile * TR + TR - 1, rows - 1) / a.group) + off;
+  const int first_lim = (int)((unsigned)min(r0, rows - 1) / (unsigned)a.group) + off;
+  const int wave_lim = (int)((unsigned)min(r0 + 31, rows - 1) / (unsigned)a.group) + off;
+  const int last_lim = (int)((unsigned)min(tile * TR + TR - 1, rows - 1) / (unsigned)a.group) + off;
   const int keys = max(min(q.Lk, last_lim + 1), 0), ktiles = (keys + TN - 1) / TN;
 
   const T *qp = static_cast<const T *>(a.q) + (int64_t)(q.q0 + tok) * a.ldq + hq * D;
@@ -213,57 +212,51 @@ template <typename T, int D> __global__ __launch_bounds__(THR, 1) void attn_bwd_
 
   const T *kg = static_cast<const T *>(a.k) + (int64_t)q.k0 * a.ldk + head * D;
   const T *vg = static_cast<const T *>(a.v) + (int64_t)q.k0 * a.ldv + head * D;
-  uint4 kr[PER], vr[PER];
-  auto fetch = [&](int kt) {
+  const unsigned kstep = (unsigned)a.ldk * sizeof(T), vstep = (unsigned)a.ldv * sizeof(T);
+  auto copy = [&](int kt, int buf) {            // rows past the sequence's keys repeat its last one
+    const T *kp = kg + (int64_t)kt * TN * a.ldk, *vp = vg + (int64_t)kt * TN * a.ldv;
+    const int last = q.Lk - 1 - kt * TN;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = tid + i * THR, row = e / Ti::CPR, ch = e % Ti::CPR;
-      const int key = kt * TN + row;
-      kr[i] = vr[i] = uint4{0, 0, 0, 0};
-      if (e < CH && key < q.Lk) {
-        kr[i] = *reinterpret_cast<const uint4 *>(kg + (int64_t)key * a.ldk + ch * Ti::E);
-        vr[i] = *reinterpret_cast<const uint4 *>(vg + (int64_t)key * a.ldv + ch * Ti::E);
-      }
-    }
-  };
-  auto stage = [&](int buf) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = tid + i * THR, row = e / Ti::CPR, ch = e % Ti::CPR;
-      if (e < CH) {
-        sk[buf][Ti::place(row, ch)] = kr[i];
-        sv[buf][Ti::place(row, ch)] = vr[i];
-      }
+    for (int i = 0; i < Cp::PER; ++i) {
+      if (!Cp::has(i, wave)) continue;
+      const int row = min(Cp::row(i, tid), last);
+      copy_to_lds(kp, row * kstep + Cp::byte(i, tid), Cp::to(sk[buf], i, wave));
+      copy_to_lds(vp, row * vstep + Cp::byte(i, tid), Cp::to(sv[buf], i, wave));
     }
   };
   f16v dq[CB];
 #pragma unroll
   for (int b = 0; b < CB; ++b) dq[b] = zero16();
   const float sc = a.scale * kLog2e;
-  if (ktiles > 0) { fetch(0); stage(0); }
+  if (ktiles > 0) copy(0, 0);
+  copies_done();
   __syncthreads();
   for (int kt = 0; kt < ktiles; ++kt) {
     const int buf = kt & 1;
-    if (kt + 1 < ktiles) fetch(kt + 1);
-    f16v s = zero16(), g = zero16();
+    if (kt + 1 < ktiles) copy(kt + 1, buf ^ 1);            // its last readers are behind the barrier
+    if (kt * TN <= wave_lim) {
+      f16v s = zero16(), g = zero16();
 #pragma unroll
-    for (int b = 0; b < DB; ++b) mma(s, Ti::rows(sk[buf], 0, b, lane), qf[b]);
+      for (int b = 0; b < DB; ++b) mma(s, Ti::rows(sk[buf], 0, b, lane), qf[b]);
 #pragma unroll
-    for (int b = 0; b < DB; ++b) mma(g, Ti::rows(sv[buf], 0, b, lane), gf[b]);
+      for (int b = 0; b < DB; ++b) mma(g, Ti::rows(sv[buf], 0, b, lane), gf[b]);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int key = kt * TN + 8 * (i / 4) + 4 * h + (i & 3);
-      float p = __builtin_amdgcn_exp2f(fmaf(s[i], sc, -L));
-      if (key > lim) p = 0.f;
-      s[i] = p * (g[i] - Dr);
+      for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], sc, -L));
+      if (kt * TN + TN - 1 > first_lim) {
+        const int left = lim - kt * TN - 4 * h;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = 8 * (i / 4) + (i & 3) > left ? 0.f : s[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i] *= g[i] - Dr;
+#pragma unroll
+      for (int b16 = 0; b16 < 2; ++b16) {
+        const Frag<T> sf = result_frag<T>(s, b16);
+#pragma unroll
+        for (int b = 0; b < CB; ++b) mma(dq[b], Ti::cols(sk[buf], b16 * 16, b * 32, lane), sf);
+      }
     }
-#pragma unroll
-    for (int b16 = 0; b16 < 2; ++b16) {
-      const Frag<T> sf = result_frag<T>(s, b16);
-#pragma unroll
-      for (int b = 0; b < CB; ++b) mma(dq[b], Ti::cols(sk[buf], b16 * 16, b * 32, lane), sf);
-    }
-    if (kt + 1 < ktiles) stage(buf ^ 1);
+    copies_done();
     __syncthreads();
   }
   if (!on) return;

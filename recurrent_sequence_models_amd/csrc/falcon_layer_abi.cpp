@@ -270,7 +270,8 @@ int check_attn(const falcon_attn_shape_t *s, bool packed) {
   // token, row and workgroup numbers are ints (128 rows or keys a workgroup; the split of the
   // keys only happens where there are few of them)
   const int64_t tq = attn_tokens_q(s, packed), tk = attn_tokens_k(s, packed);
-  if (tq > INT32_MAX - 4096 || tk > INT32_MAX - 4096) return FALCON_ERR_UNSUPPORTED;
+  if (tq > INT32_MAX - 4096 || tk > INT32_MAX - 4096 || s->heads_q > (1 << 20)) return FALCON_ERR_UNSUPPORTED;
+  if (tq * (s->heads_q / s->heads_k) > INT32_MAX - 4096) return FALCON_ERR_UNSUPPORTED;
   if ((tq * s->heads_q / 128 + (int64_t)(s->batch + 1) * s->heads_k) > INT32_MAX / 2) return FALCON_ERR_UNSUPPORTED;
   if ((tk / 128 + s->batch + 1) * s->heads_k > INT32_MAX / 2) return FALCON_ERR_UNSUPPORTED;
   return FALCON_OK;
@@ -301,6 +302,9 @@ int check_attn_in(const falcon_attn_shape_t *s, const int32_t *cu_q, const int32
   FALCON_TRY(check_heads(q.data, q.token_stride, attn_tokens_q(s, packed), s->heads_q, s->d, e));
   FALCON_TRY(check_heads(k.data, k.token_stride, attn_tokens_k(s, packed), s->heads_k, s->d, e));
   FALCON_TRY(check_heads(v.data, v.token_stride, attn_tokens_k(s, packed), s->heads_k, s->d, e));
+  // a tile's rows are 32 bits of bytes apart
+  if (q.token_stride > (1 << 24) || k.token_stride > (1 << 24) || v.token_stride > (1 << 24))
+    return FALCON_ERR_UNSUPPORTED;
   return need(o, 16);
 }
 
@@ -347,6 +351,7 @@ int falcon_attn_bwd(const falcon_attn_shape_t *s, const int32_t *cu_q, const int
   const int64_t tq = attn_tokens_q(s, packed), tk = attn_tokens_k(s, packed);
   const int e = esize(s->dtype);
   FALCON_TRY(check_heads(d_o.data, d_o.token_stride, tq, s->heads_q, s->d, e));
+  if (d_o.token_stride > (1 << 24)) return FALCON_ERR_UNSUPPORTED;
   FALCON_TRY(check_heads(dq.data, dq.token_stride, tq, s->heads_q, s->d, e));
   FALCON_TRY(check_heads(dk.data, dk.token_stride, tk, s->heads_k, s->d, e));
   FALCON_TRY(check_heads(dv.data, dv.token_stride, tk, s->heads_k, s->d, e));
