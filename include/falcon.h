@@ -482,7 +482,8 @@ int falcon_attn_fwd(const falcon_attn_shape_t *shape, const int32_t *cu_q, const
                     falcon_heads_t q, falcon_heads_t k, falcon_heads_t v, void *o, float *lse,
                     void *workspace, size_t workspace_bytes, void *stream);
 
-/* Bytes of workspace of the backward (one fp32 number per query and head). */
+/* Bytes of workspace of the backward: two fp32 numbers per query and head, and, where
+ * few key tiles meet many queries, partial sums of dk and dv. */
 size_t falcon_attn_bwd_workspace(const falcon_attn_shape_t *shape, int packed);
 
 /* Gradients of <d_o, o> with respect to q, k, v, from the forward's o and lse (o

@@ -136,8 +136,24 @@ __device__ __forceinline__ Slot find_slot(const int *cu, int N, int slot, int mu
 // 16 bytes a lane from global memory (a scalar base plus 32 bits a lane) straight into LDS, lane
 // l's to lds + 16 l.  The compiler does not count these: copies_done() before the barrier that
 // hands the tile over.
+__device__ __forceinline__ const void *scalar(const void *base) {   // the same in every lane; the compiler may not know
+  const uint64_t p = reinterpret_cast<uint64_t>(base);
+  return reinterpret_cast<const void *>((uint64_t)(unsigned)__builtin_amdgcn_readfirstlane((int)p) |
+                                        (uint64_t)(unsigned)__builtin_amdgcn_readfirstlane((int)(p >> 32)) << 32);
+}
 __device__ __forceinline__ void copy_to_lds(const void *base, unsigned offset, unsigned lds) {
+  base = scalar(base);
+  lds = __builtin_amdgcn_readfirstlane((int)lds);
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(offset), "s"(base), "s"(lds)
+               : "memory", "m0");
+}
+// The same for 4 bytes a lane, lane l's to lds + 4 l.
+__device__ __forceinline__ void copy4_to_lds(const void *base, unsigned offset, unsigned lds) {
+  base = scalar(base);
+  lds = __builtin_amdgcn_readfirstlane((int)lds);
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
                :
                : "v"(offset), "s"(base), "s"(lds)
                : "memory", "m0");
@@ -163,6 +179,14 @@ template <typename T, int D, int ROWS> struct Copy {
     return lds_address(tile + 64 * (4 * i + wave));
   }
 };
+
+// Tokens of the packed axes, or of all sequences.
+__host__ __device__ __forceinline__ int64_t query_tokens(const AttnArgs &a) {
+  return a.cuq ? (int64_t)a.Tq : (int64_t)a.n * a.Tq;
+}
+__host__ __device__ __forceinline__ int64_t key_tokens(const AttnArgs &a) {
+  return a.cuk ? (int64_t)a.Tk : (int64_t)a.n * a.Tk;
+}
 
 // A sequence's token ranges, kept inside the arrays whatever the offsets hold.
 struct Seq { int q0, Lq, k0, Lk; };

@@ -175,7 +175,7 @@ template <typename T, int D> __global__ __launch_bounds__(THR, sizeof(T) * D > 2
   if (!on) return;
   const size_t at = (size_t)(q.q0 + tok) * a.hq + hq;
   if (a.splits > 1) {   // unnormalised: [split][row of the packed axis and head][d], then (m, l)
-    const size_t nrow = (size_t)(a.cuq ? a.Tq : a.n * (int64_t)a.Tq) * a.hq, ps = split * nrow + at;
+    const size_t nrow = (size_t)query_tokens(a) * a.hq, ps = split * nrow + at;
     float *p = a.part + ps * D;
 #pragma unroll
     for (int b = 0; b < CB; ++b)
@@ -205,7 +205,7 @@ template <typename T, int D> __global__ __launch_bounds__(THR) void attn_join(At
   const size_t row = ((size_t)blockIdx.x * THR + threadIdx.x) / L;
   const int e = (threadIdx.x % L) * 4;
   if (row >= nrow) return;
-  if (a.cuq && row >= (size_t)a.cuq[last] * a.hq) return;    // behind the last sequence
+  if (a.cuq && row >= (size_t)max(a.cuq[last], 0) * a.hq) return;    // behind the last sequence
   const float *ml = a.part + a.splits * nrow * D;
   float m = -INFINITY;
   for (int s = 0; s < a.splits; ++s) m = fmaxf(m, ml[(s * nrow + row) * 2]);
@@ -223,8 +223,6 @@ template <typename T, int D> __global__ __launch_bounds__(THR) void attn_join(At
   store4(static_cast<T *>(a.out) + row * D + e, o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
   if (e == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : kLn2 * (m + __builtin_amdgcn_logf(l));
 }
-
-int64_t query_rows(const AttnArgs &a) { return a.cuq ? (int64_t)a.Tq : (int64_t)a.n * a.Tq; }
 
 // Tiles of the packed row axis, at most; exact without cu.
 int64_t slots_of(const AttnArgs &a) {
@@ -248,7 +246,7 @@ template <typename T, int D> hipError_t run(AttnArgs &a, hipStream_t s) {
   hipLaunchKernelGGL((attn_fwd<T, D>), dim3((unsigned)blocks), dim3(THR), 0, s, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  const size_t nrow = (size_t)query_rows(a) * a.hq;
+  const size_t nrow = (size_t)query_tokens(a) * a.hq;
   const size_t nb = (nrow * (D / 4) + THR - 1) / THR;
   hipLaunchKernelGGL((attn_join<T, D>), dim3((unsigned)nb), dim3(THR), 0, s, a, nrow, a.n);
   return hipGetLastError();
@@ -259,7 +257,7 @@ template <typename T, int D> hipError_t run(AttnArgs &a, hipStream_t s) {
 size_t attn_fwd_workspace(bool bf16, int d, const AttnArgs &a) {
   (void)bf16;
   const int s = splits_of(a);
-  return s == 1 ? 0 : (size_t)s * query_rows(a) * a.hq * (d + 2) * sizeof(float);
+  return s == 1 ? 0 : (size_t)s * query_tokens(a) * a.hq * (d + 2) * sizeof(float);
 }
 
 hipError_t launch_attn_fwd(bool bf16, int d, AttnArgs a, void *ws, hipStream_t s) {

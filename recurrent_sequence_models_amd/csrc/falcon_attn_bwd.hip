@@ -23,6 +23,8 @@ namespace {
 
 constexpr int THR = 256, TR = 128;   // 4 waves of 32 rows (or keys)
 
+// Per row (query token and head): D = do . o, and lse in base 2, +inf where the row sees
+// nothing, so that all its weights e^{s - lse} come out 0.
 template <typename T, int D> __global__ __launch_bounds__(THR) void attn_delta(AttnArgs a, size_t nrow) {
   constexpr int E = 16 / (int)sizeof(T), L = D / E;
   const size_t row = ((size_t)blockIdx.x * THR + threadIdx.x) / L;
@@ -37,20 +39,41 @@ template <typename T, int D> __global__ __launch_bounds__(THR) void attn_delta(A
   }
   s = lane_sum<(L < 16 ? L : 16)>(s);
   if constexpr (L == 32) s = add_xor16(s);
-  if (row < nrow && e == 0) a.delta[row] = s;
+  if (row < nrow && e == 0) {
+    const float lse = a.lse_in[row];
+    a.delta[row] = s;
+    a.lse2[row] = lse == -INFINITY ? INFINITY : lse * kLog2e;
+  }
 }
 
 // ---- dk, dv ------------------------------------------------------------------
+// Rows of a tile: 64 (half the barriers and address work of 32), or 32 where two pairs of
+// tiles of 64 would leave one workgroup a compute unit (fp32 at d = 128).
+template <typename T, int D> constexpr int TQ_OF = sizeof(T) * D > 128 ? 32 : 64;
+// Where rows are longer than 128 bytes, the values wait in LDS instead of registers: with both
+// operands and both sums in registers (bf16 at d = 128: 192 of the 256 that leave two waves a
+// SIMD) the compiler spills, and every reload waits for the copies in flight as well.
+template <typename T, int D> constexpr bool V_IN_LDS = sizeof(T) * D > 128;
+// The same for 2 of a lane's 8 key fragments at bf16, d = 128: none is spilled then, and two
+// workgroups' LDS still fits a compute unit.
+template <typename T, int D> constexpr int KEYS_IN_LDS = sizeof(T) == 2 && D == 128 ? 2 : 0;
+
 template <typename T, int D>
 __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_kv(AttnArgs a) {
   typedef Tile<T, D> Ti;
-  constexpr int TQ = 32, DB = D / 16, CB = D / 32;
+  constexpr int TQ = TQ_OF<T, D>, DB = D / 16, CB = D / 32;
+  constexpr bool VL = V_IN_LDS<T, D>;
   typedef Copy<T, D, TQ> Cp;
-  __shared__ uint4 sq[2][Cp::CH], sg[2][Cp::CH];
-  __shared__ __align__(16) float sL[2][TQ], sD[2][TQ];   // lse (base 2) and D of the rows
-  __shared__ __align__(16) int sM[2][TQ];                // the last key each row sees
+  typedef Copy<T, D, TR> CpV;
+  constexpr int KR = DB - KEYS_IN_LDS<T, D>;
+  __shared__ uint4 sq[2][Cp::CH], sg[2][Cp::CH], sv[VL ? CpV::CH : 1];
+  __shared__ Frag<T> sk[DB > KR ? DB - KR : 1][THR];
+  __shared__ __align__(16) float sL[2][64], sD[2][64];   // lse (base 2) and D of the rows
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 31, h = lane >> 5;
-  const int head = blockIdx.x % (unsigned)a.hk, slot = blockIdx.x / (unsigned)a.hk;
+  unsigned id = blockIdx.x;
+  const int head = id % (unsigned)a.hk;
+  id /= (unsigned)a.hk;
+  const int split = id % (unsigned)a.splits, slot = id / (unsigned)a.splits;
   int n, tile;
   if (a.cuk) {
     const Slot s = find_slot(a.cuk, a.n, slot, 1, TR);
@@ -63,31 +86,49 @@ __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_kv(
   const int key0 = tile * TR, wkey = key0 + wave * 32, key = wkey + c;
   const bool on = key < q.Lk;
   const int rows = q.Lq * a.group, off = q.Lk - q.Lq;
-  // the first row that sees a key of this tile, down to a whole tile of rows
-  const int r_first = min(max(key0 - off, 0), q.Lq) * a.group / TQ * TQ;
-  const int tiles = (rows - r_first + TQ - 1) / TQ;
+  // The first row that sees a key: of this lane's, of any of this wave's, of all of them, and,
+  // down to a whole tile of rows, of any of this tile's; then this split's share of the tiles.
+  auto first_row = [&](int k) { return max(min(k, q.Lk - 1) - off, 0) * a.group; };
+  const int see = first_row(key), wave_see = first_row(wkey), wave_all = first_row(wkey + 31);
+  const int r_first = first_row(key0) / TQ * TQ;
+  const int64_t all = (rows - r_first + TQ - 1) / TQ;
+  const int t0 = __builtin_amdgcn_readfirstlane((int)(all * split / a.splits));
+  const int t1 = __builtin_amdgcn_readfirstlane((int)(all * (split + 1) / a.splits));
 
-  Frag<T> kf[DB], vf[DB];
+  Frag<T> kf[KR], vf[VL ? 1 : DB];
   {
     const T *kp = static_cast<const T *>(a.k) + (int64_t)(q.k0 + min(key, q.Lk - 1)) * a.ldk + head * D;
     const T *vp = static_cast<const T *>(a.v) + (int64_t)(q.k0 + min(key, q.Lk - 1)) * a.ldv + head * D;
 #pragma unroll
     for (int b = 0; b < DB; ++b) {
-      kf[b] = global_frag(kp, b, h);
-      vf[b] = global_frag(vp, b, h);
+      if (b < KR) kf[b < KR ? b : 0] = global_frag(kp, b, h);
+      else sk[b < KR ? 0 : b - KR][tid] = global_frag(kp, b, h);
+      if (!VL) vf[VL ? 0 : b] = global_frag(vp, b, h);
     }
   }
+  if (VL) {
+    const T *vg = static_cast<const T *>(a.v) + (int64_t)(q.k0 + key0) * a.ldv + head * D;
+#pragma unroll
+    for (int i = 0; i < CpV::PER; ++i) {
+      const int row = min(CpV::row(i, tid), q.Lk - 1 - key0);
+      copy_to_lds(vg, row * (unsigned)a.ldv * sizeof(T) + CpV::byte(i, tid), CpV::to(sv, i, wave));
+    }
+  }
+  auto keys = [&](int b) { return b < KR ? kf[b < KR ? b : 0] : sk[b < KR ? 0 : b - KR][tid]; };
+  auto value = [&](int b) { return VL ? Ti::rows(sv, wave * 32, b, lane) : vf[VL ? 0 : b]; };
   // Copying tiles of rows: rows past the sequence's repeat its last one, and their weights are
-  // 0 (lse = inf).  A row's token is its number over the group, by a multiplication: exact for
-  // the numbers up to group + 31 left when the tile's first token is taken off.
+  // masked.  A row's token is its number over the group, by a multiplication: in 64 bits it is
+  // exact for any row number, in 32 for the numbers up to group + 63 left when the tile's first
+  // token is taken off.
   const T *qg = static_cast<const T *>(a.q) + (int64_t)q.q0 * a.ldq + head * a.group * D;
   const T *gg = static_cast<const T *>(a.d_o) + (int64_t)q.q0 * a.lddo + head * a.group * D;
-  const float inv = 1.f / a.group;
+  const int64_t row0 = (int64_t)q.q0 * a.hq + head * a.group;
+  const double inv64 = 1.0 / a.group;
+  const float inv = (float)inv64;
+  auto token64 = [&](int row) { return __builtin_amdgcn_readfirstlane((int)((row + 0.5) * inv64)); };
   auto token = [&](int rel) { return (int)((rel + 0.5f) * inv); };
-  float rl = 0.f, rd = 0.f;
-  int rm = 0;
   auto copy = [&](int t, int buf) {
-    const int rt = r_first + t * TQ, tb = rt / (unsigned)a.group, r0 = tb * a.group;
+    const int rt = r_first + t * TQ, tb = token64(rt), r0 = tb * a.group;
     const T *qp = qg + (int64_t)tb * a.ldq, *gp = gg + (int64_t)tb * a.lddo;
 #pragma unroll
     for (int i = 0; i < Cp::PER; ++i) {
@@ -97,68 +138,80 @@ __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_kv(
       copy_to_lds(qp, tok * (unsigned)a.ldq * sizeof(T) + in, Cp::to(sq[buf], i, wave));
       copy_to_lds(gp, tok * (unsigned)a.lddo * sizeof(T) + in, Cp::to(sg[buf], i, wave));
     }
-    if (tid < TQ) {
-      rl = INFINITY; rd = 0.f; rm = -1;
-      if (rt + tid < rows) {
-        const int rel = rt + tid - r0, tok = token(rel), hh = rel - tok * a.group;
-        const int64_t at = (int64_t)(q.q0 + tb + tok) * a.hq + head * a.group + hh;
-        const float lse = a.lse_in[at];
-        rl = lse == -INFINITY ? INFINITY : lse * kLog2e;   // a row that sees nothing
-        rd = a.delta[at];
-        rm = tb + tok + off;
-      }
+    if (wave < 2) {
+      const int rel = min(rt + lane, rows - 1) - r0, tok = token(rel), hh = rel - tok * a.group;
+      const int64_t at = row0 + (int64_t)tb * a.hq;
+      copy4_to_lds((wave ? a.delta : a.lse2) + at, (tok * (unsigned)a.hq + hh) * 4, lds_address(wave ? sD[buf] : sL[buf]));
     }
-  };
-  auto hand_over = [&](int buf) {
-    if (tid < TQ) { sL[buf][tid] = rl; sD[buf][tid] = rd; sM[buf][tid] = rm; }
-    copies_done();
-    __syncthreads();
   };
   f16v dk[CB], dv[CB];
 #pragma unroll
   for (int b = 0; b < CB; ++b) dk[b] = dv[b] = zero16();
   const float sc = a.scale * kLog2e;
-  if (tiles > 0) copy(0, 0);
-  hand_over(0);
-  for (int t = 0; t < tiles; ++t) {
-    const int buf = t & 1, rt = r_first + t * TQ;
-    if (t + 1 < tiles) copy(t + 1, buf ^ 1);               // its last readers are behind the barrier
-    const int first_lim = (int)(rt / (unsigned)a.group) + off;
-    const int last_lim = (int)(min(rt + TQ - 1, rows - 1) / (unsigned)a.group) + off;
-    if (wkey <= last_lim) {                                // else no row of the tile sees a key of this wave
+  if (t0 < t1) copy(t0, 0);
+  copies_done();
+  __syncthreads();
+  for (int t = t0; t < t1; ++t) {
+    const int buf = (t - t0) & 1;
+    if (t + 1 < t1) copy(t + 1, buf ^ 1);                  // its last readers are behind the barrier
+    // what the tile's first and last rows see
+    const int rt = r_first + t * TQ;
+    const int lo = see - rt - 4 * h, hi = rows - rt - 4 * h;   // the rows of the tile that see this lane's key
+    const bool masked = rt < wave_all || rt + TQ > rows;
+    if (rt + TQ > wave_see)                                // else no row of the tile sees a key of this wave
+#pragma unroll
+    for (int rb = 0; rb < TQ; rb += 32) {
+      if (rt + rb >= rows) break;
       f16v s = zero16(), g = zero16();
 #pragma unroll
-      for (int b = 0; b < DB; ++b) mma(s, Ti::rows(sq[buf], 0, b, lane), kf[b]);
+      for (int b = 0; b < DB; ++b) mma(s, Ti::rows(sq[buf], rb, b, lane), keys(b));
 #pragma unroll
-      for (int b = 0; b < DB; ++b) mma(g, Ti::rows(sg[buf], 0, b, lane), vf[b]);
-      const bool masked = wkey + 31 > first_lim;
+      for (int b = 0; b < DB; ++b) mma(g, Ti::rows(sg[buf], rb, b, lane), value(b));
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const f4 L = *reinterpret_cast<const f4 *>(&sL[buf][8 * b + 4 * h]);
-        const f4 Dr = *reinterpret_cast<const f4 *>(&sD[buf][8 * b + 4 * h]);
+        const f4 L = *reinterpret_cast<const f4 *>(&sL[buf][rb + 8 * b + 4 * h]);
+        const f4 Dr = *reinterpret_cast<const f4 *>(&sD[buf][rb + 8 * b + 4 * h]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[4 * b + i] = __builtin_amdgcn_exp2f(fmaf(s[4 * b + i], sc, -L[i]));
-        if (masked) {
-          const int4 M = *reinterpret_cast<const int4 *>(&sM[buf][8 * b + 4 * h]);
-          const int lim[4] = {M.x, M.y, M.z, M.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[4 * b + i] = key > lim[i] ? 0.f : s[4 * b + i];
+        for (int i = 0; i < 4; ++i) {
+          s[4 * b + i] = __builtin_amdgcn_exp2f(fmaf(s[4 * b + i], sc, -L[i]));
+          g[4 * b + i] -= Dr[i];
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) g[4 * b + i] = s[4 * b + i] * (g[4 * b + i] - Dr[i]);
       }
+      if (masked) {   // the same for the whole wave; once, so that what is around it stays in two pieces
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int e = rb + 8 * (i / 4) + (i & 3);
+          s[i] = e >= lo && e < hi ? s[i] : 0.f;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) g[i] *= s[i];
 #pragma unroll
       for (int b16 = 0; b16 < 2; ++b16) {
         const Frag<T> pf = result_frag<T>(s, b16), gf = result_frag<T>(g, b16);
 #pragma unroll
-        for (int b = 0; b < CB; ++b) mma(dv[b], Ti::cols(sg[buf], b16 * 16, b * 32, lane), pf);
+        for (int b = 0; b < CB; ++b) mma(dv[b], Ti::cols(sg[buf], rb + b16 * 16, b * 32, lane), pf);
 #pragma unroll
-        for (int b = 0; b < CB; ++b) mma(dk[b], Ti::cols(sq[buf], b16 * 16, b * 32, lane), gf);
+        for (int b = 0; b < CB; ++b) mma(dk[b], Ti::cols(sq[buf], rb + b16 * 16, b * 32, lane), gf);
       }
     }
-    hand_over(buf ^ 1);
+    copies_done();
+    __syncthreads();
   }
   if (!on) return;
+  if (a.splits > 1) {   // [split][dk, dv][key token, head][d]
+    const size_t nkey = (size_t)key_tokens(a) * a.hk, at = (size_t)(q.k0 + key) * a.hk + head;
+    float *pk = a.part + ((size_t)split * 2 * nkey + at) * D, *pv = pk + nkey * D;
+#pragma unroll
+    for (int b = 0; b < CB; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const int e = b * 32 + 2 * i + 4 * h;
+        store4(pk + e, dk[b][i], dk[b][i + 1], dk[b][i + 2], dk[b][i + 3]);
+        store4(pv + e, dv[b][i], dv[b][i + 1], dv[b][i + 2], dv[b][i + 3]);
+      }
+    return;
+  }
   T *pk = static_cast<T *>(a.dk) + (int64_t)(q.k0 + key) * a.lddk + head * D;
   T *pv = static_cast<T *>(a.dv) + (int64_t)(q.k0 + key) * a.lddv + head * D;
 #pragma unroll
@@ -169,6 +222,26 @@ __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_kv(
       store4(pk + e, dk[b][i] * a.scale, dk[b][i + 1] * a.scale, dk[b][i + 2] * a.scale, dk[b][i + 3] * a.scale);
       store4(pv + e, dv[b][i], dv[b][i + 1], dv[b][i + 2], dv[b][i + 3]);
     }
+}
+
+// Adds the splits of dk and dv in order: one thread per 4 entries.
+template <typename T, int D> __global__ __launch_bounds__(THR) void attn_bwd_sum(AttnArgs a, size_t nkey) {
+  constexpr int L = D / 4;
+  const size_t at = ((size_t)blockIdx.x * THR + threadIdx.x) / L;
+  const int e = (threadIdx.x % L) * 4;
+  if (at >= nkey) return;
+  const size_t tok = at / a.hk;
+  const int head = (int)(at - tok * a.hk);
+  if (a.cuk && tok >= (size_t)max(a.cuk[a.n], 0)) return;      // behind the last sequence
+  f4 dk = zero4(), dv = zero4();
+  for (int s = 0; s < a.splits; ++s) {
+    const float *p = a.part + ((size_t)s * 2 * nkey + at) * D + e;
+    dk += *reinterpret_cast<const f4 *>(p);
+    dv += *reinterpret_cast<const f4 *>(p + nkey * D);
+  }
+  dk *= a.scale;
+  store4(static_cast<T *>(a.dk) + (int64_t)tok * a.lddk + head * D + e, dk[0], dk[1], dk[2], dk[3]);
+  store4(static_cast<T *>(a.dv) + (int64_t)tok * a.lddv + head * D + e, dv[0], dv[1], dv[2], dv[3]);
 }
 
 // ---- dq ----------------------------------------------------------------------
@@ -206,9 +279,7 @@ __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_q(A
 #pragma unroll
   for (int b = 0; b < DB; ++b) { qf[b] = global_frag(qp, b, h); gf[b] = global_frag(gp, b, h); }
   const int64_t at = (int64_t)(q.q0 + tok) * a.hq + hq;
-  float L = a.lse_in[at];
-  L = L == -INFINITY ? INFINITY : L * kLog2e;
-  const float Dr = a.delta[at];
+  const float L = a.lse2[at], Dr = a.delta[at];
 
   const T *kg = static_cast<const T *>(a.k) + (int64_t)q.k0 * a.ldk + head * D;
   const T *vg = static_cast<const T *>(a.v) + (int64_t)q.k0 * a.ldv + head * D;
@@ -269,30 +340,61 @@ __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_q(A
              dq[b][i + 3] * a.scale);
 }
 
-int64_t query_rows(const AttnArgs &a) { return a.cuq ? (int64_t)a.Tq : (int64_t)a.n * a.Tq; }
+int64_t key_slots(const AttnArgs &a) {
+  return a.cuk ? (int64_t)a.Tk / TR + a.n : ((int64_t)a.Tk + TR - 1) / TR * a.n;
+}
+
+// Splits of the rows between workgroups of one key tile.  Tile 0 meets every row and the last
+// tile 128 of them, so at two workgroups a compute unit one round of workgroups would take
+// twice the average one; with 1024 of them the short ones fill in.  At least 512 rows (of the
+// average sequence) a split, so that writing and adding the parts stays small beside them.
+int bwd_splits(const AttnArgs &a) {
+  const int64_t blocks = key_slots(a) * a.hk;
+  const int64_t rows = (a.cuq ? a.Tq / a.n : a.Tq) * (int64_t)a.group;
+  int64_t s = (1024 + blocks - 1) / blocks;
+  if (s > rows / 512) s = rows / 512;
+  if (s > 16) s = 16;
+  return s < 1 ? 1 : (int)s;
+}
 
 template <typename T, int D> hipError_t run(AttnArgs &a, hipStream_t s) {
-  const size_t nrow = (size_t)query_rows(a) * a.hq;
+  const size_t nrow = (size_t)query_tokens(a) * a.hq, nkey = (size_t)key_tokens(a) * a.hk;
   constexpr int L = D * (int)sizeof(T) / 16;
-  const int64_t kslots = a.cuk ? (int64_t)a.Tk / TR + a.n : ((int64_t)a.Tk + TR - 1) / TR * a.n;
+  const int64_t kblocks = key_slots(a) * a.hk * a.splits;
   const int64_t qslots = a.cuq ? (int64_t)a.Tq * a.group / TR + a.n : ((int64_t)a.Tq * a.group + TR - 1) / TR * a.n;
-  const size_t nb = (nrow * L + THR - 1) / THR;
-  if (nb > 0x7fffffff || kslots * a.hk > 0x7fffffff || qslots * a.hk > 0x7fffffff) return hipErrorInvalidValue;
+  const size_t nb = (nrow * L + THR - 1) / THR, ns = (nkey * (D / 4) + THR - 1) / THR;
+  if (nb > 0x7fffffff || ns > 0x7fffffff || kblocks > 0x7fffffff || qslots * a.hk > 0x7fffffff)
+    return hipErrorInvalidValue;
   hipLaunchKernelGGL((attn_delta<T, D>), dim3((unsigned)nb), dim3(THR), 0, s, a, nrow);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attn_bwd_kv<T, D>), dim3((unsigned)(kslots * a.hk)), dim3(THR), 0, s, a);
+  hipLaunchKernelGGL((attn_bwd_kv<T, D>), dim3((unsigned)kblocks), dim3(THR), 0, s, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (a.splits > 1) {
+    hipLaunchKernelGGL((attn_bwd_sum<T, D>), dim3((unsigned)ns), dim3(THR), 0, s, a, nkey);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
   hipLaunchKernelGGL((attn_bwd_q<T, D>), dim3((unsigned)(qslots * a.hk)), dim3(THR), 0, s, a);
   return hipGetLastError();
 }
 
+// One fp32 number per query and head, in whole 16 bytes.
+size_t row_bytes(const AttnArgs &a) { return ((size_t)query_tokens(a) * a.hq * sizeof(float) + 15) & ~(size_t)15; }
+
 }  // namespace
 
-size_t attn_bwd_workspace(const AttnArgs &a) { return (size_t)query_rows(a) * a.hq * sizeof(float); }
+size_t attn_bwd_workspace(int d, const AttnArgs &a) {
+  const int s = bwd_splits(a);
+  const size_t part = s == 1 ? 0 : (size_t)s * 2 * key_tokens(a) * a.hk * d * sizeof(float);
+  return 2 * row_bytes(a) + part;
+}
 
 hipError_t launch_attn_bwd(bool bf16, int d, AttnArgs a, void *ws, hipStream_t s) {
-  a.delta = static_cast<float *>(ws);
+  unsigned char *p = static_cast<unsigned char *>(ws);
+  a.splits = bwd_splits(a);
+  a.delta = reinterpret_cast<float *>(p);
+  a.lse2 = reinterpret_cast<float *>(p + row_bytes(a));
+  a.part = reinterpret_cast<float *>(p + 2 * row_bytes(a));
 #define FALCON_ATTN(D_) \
   if (d == D_) return bf16 ? run<__bf16, D_>(a, s) : run<float, D_>(a, s)
   FALCON_ATTN(32);

@@ -338,7 +338,7 @@ int falcon_attn_fwd(const falcon_attn_shape_t *s, const int32_t *cu_q, const int
 
 size_t falcon_attn_bwd_workspace(const falcon_attn_shape_t *s, int packed) {
   if (check_attn(s, packed != 0) != FALCON_OK) return 0;
-  return falcon::attn_bwd_workspace(size_args(s, packed != 0));
+  return falcon::attn_bwd_workspace(s->d, size_args(s, packed != 0));
 }
 
 int falcon_attn_bwd(const falcon_attn_shape_t *s, const int32_t *cu_q, const int32_t *cu_k, falcon_heads_t q,

@@ -60,7 +60,8 @@ struct AttnArgs {
   void *out, *dq, *dk, *dv;
   float *lse;                    // [query tokens, hq]
   const int *cuq, *cuk;          // [n + 1] or null
-  float *part, *delta;           // workspace: forward partial results; backward row sums of do o
+  float *part;                   // workspace: partial results of splits
+  float *delta, *lse2;           // backward workspace: row sums of do o, lse in base 2
   int64_t ldq, ldk, ldv, ldo, lddo, lddq, lddk, lddv;
   int n, Tq, Tk;                 // packed: Tq, Tk are the totals
   int hq, hk, group;             // group = hq / hk
@@ -69,7 +70,7 @@ struct AttnArgs {
 };
 size_t attn_fwd_workspace(bool bf16, int d, const AttnArgs &a);
 hipError_t launch_attn_fwd(bool bf16, int d, AttnArgs a, void *ws, hipStream_t s);
-size_t attn_bwd_workspace(const AttnArgs &a);
+size_t attn_bwd_workspace(int d, const AttnArgs &a);
 hipError_t launch_attn_bwd(bool bf16, int d, AttnArgs a, void *ws, hipStream_t s);
 
 }  // namespace falcon

@@ -158,7 +158,7 @@ def test_attention_refusals():
         assert attn_fwd(s, **kw) == INVALID and attn_bwd(s, **kw) == INVALID, kw
     for kw in (dict(lse=None), dict(do=H(None)), dict(dq=H(P + 8)), dict(dk=H(P, 64)), dict(dv=H(None))):
         assert attn_bwd(s, **kw) == INVALID, kw
-    assert attn_bwd(s, n=2 * 100 * 4 * 4 - 1) == WORKSPACE and attn_bwd(s, ws=None) == WORKSPACE
+    assert attn_bwd(s, n=2 * 2 * 100 * 4 * 4 - 1) == WORKSPACE and attn_bwd(s, ws=None) == WORKSPACE
     assert attn_bwd(s, ws=P + 8) == INVALID
     few = attn_shape(seqlen_q=1, seqlen_k=4096)
     need = F.lib().falcon_attn_fwd_workspace(ref(few), 0)
@@ -167,10 +167,10 @@ def test_attention_refusals():
 
 
 def test_attention_workspace():
-    """Partial results only where few rows meet many keys; one number a row in the backward."""
+    """Partial results only where few rows meet many keys; two numbers a row in the backward."""
     L = F.lib()
     assert L.falcon_attn_fwd_workspace(ref(attn_shape()), 0) == 0
     assert L.falcon_attn_fwd_workspace(ref(attn_shape(seqlen_q=1 << 15, seqlen_k=1 << 15)), 0) == 0
     assert L.falcon_attn_fwd_workspace(ref(attn_shape(seqlen_q=2, seqlen_k=1 << 14)), 1) > 0
-    assert L.falcon_attn_bwd_workspace(ref(attn_shape()), 0) == 2 * 100 * 4 * 4
-    assert L.falcon_attn_bwd_workspace(ref(attn_shape()), 1) == 100 * 4 * 4
+    assert L.falcon_attn_bwd_workspace(ref(attn_shape()), 0) == 2 * 2 * 100 * 4 * 4
+    assert L.falcon_attn_bwd_workspace(ref(attn_shape()), 1) == 2 * 100 * 4 * 4
