@@ -159,6 +159,11 @@ __device__ __forceinline__ void copy4_to_lds(const void *base, unsigned offset, 
                : "memory", "m0");
 }
 __device__ __forceinline__ void copies_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// All but the last N of this wave's copies; N at most 63, and only copies outstanding.
+template <int N> __device__ __forceinline__ void copies_done_but() {
+  static_assert(N <= 63, "the counter's range");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ unsigned lds_address(const void *p) {
   return (unsigned)(size_t)(__attribute__((address_space(3))) const void *)p;
 }

@@ -32,6 +32,69 @@ template <typename T, int D> struct Fwd {
   static constexpr int KB = TN / 32;
 };
 
+// One tile's softmax: s becomes the weights e^{scale s - reference}; the reference m (in raw
+// scores), this lane's half of the sum and the results follow.
+template <int KB, int CB>
+__device__ __forceinline__ void weigh(f16v (&s)[KB], float sc, float &m, float &l, f16v (&acc)[CB]) {
+  float top = s[0][0];
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kb][i]);
+  top = max_xor32(top);
+  // The reference follows the maximum when that has grown by over 8 (base 2): weights stay
+  // below 2^8, and most tiles rescale nothing.  (-inf: nothing seen yet, any weight is 0.)
+  if (__any(top * sc > m * sc + 8.f)) {
+    const float now = fmaxf(top, m);
+    const float f = now == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - now) * sc);
+    l *= f;
+#pragma unroll
+    for (int b = 0; b < CB; ++b) acc[b] *= f;
+    m = now;
+  }
+  const float shift = m == -INFINITY ? 0.f : m * sc;
+  float sum = 0.f;
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      s[kb][i] = __builtin_amdgcn_exp2f(fmaf(s[kb][i], sc, -shift));
+      sum += s[kb][i];
+    }
+  l += sum;
+}
+
+// A lane's row: the result and lse, or, of one of several splits, the unnormalised sum [split]
+// [row of the packed axis and head][d], then (reference in base 2, sum of weights).
+template <typename T, int D>
+__device__ __forceinline__ void finish(const AttnArgs &a, size_t at, int split, int h, float m, float l,
+                                       const f16v (&acc)[D / 32]) {
+  const float sc = a.scale * kLog2e;
+  if (a.splits > 1) {
+    const size_t nrow = (size_t)query_tokens(a) * a.hq, ps = split * nrow + at;
+    float *p = a.part + ps * D;
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        store4(p + b * 32 + 2 * i + 4 * h, acc[b][i], acc[b][i + 1], acc[b][i + 2], acc[b][i + 3]);
+    if (h == 0) {
+      float *ml = a.part + a.splits * nrow * D + ps * 2;
+      ml[0] = m * sc;
+      ml[1] = l;
+    }
+    return;
+  }
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // NaN stays NaN
+  T *out = static_cast<T *>(a.out) + at * D;
+#pragma unroll
+  for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4)
+      store4(out + b * 32 + 2 * i + 4 * h, acc[b][i] * inv, acc[b][i + 1] * inv, acc[b][i + 2] * inv, acc[b][i + 3] * inv);
+  if (h == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : kLn2 * (m * sc + __builtin_amdgcn_logf(l));
+}
+
 template <typename T, int D> __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_fwd(AttnArgs a) {
   typedef Fwd<T, D> F;
   typedef Tile<T, D> Ti;
@@ -133,32 +196,7 @@ template <typename T, int D> __global__ __launch_bounds__(THR, sizeof(T) * D > 2
         for (int i = 0; i < 16; ++i)
           if (kb * 32 + 8 * (i / 4) + (i & 3) > left) s[kb][i] = -INFINITY;
     }
-    float top = s[0][0];
-#pragma unroll
-    for (int kb = 0; kb < F::KB; ++kb)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kb][i]);
-    top = max_xor32(top);
-    // The reference follows the maximum when that has grown by over 8 (base 2): weights stay
-    // below 2^8, and most tiles rescale nothing.  (-inf: nothing seen yet, any weight is 0.)
-    if (__any(top * sc > m * sc + 8.f)) {
-      const float now = fmaxf(top, m);
-      const float f = now == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - now) * sc);
-      l *= f;
-#pragma unroll
-      for (int b = 0; b < CB; ++b) acc[b] *= f;
-      m = now;
-    }
-    const float shift = m == -INFINITY ? 0.f : m * sc;
-    float sum = 0.f;
-#pragma unroll
-    for (int kb = 0; kb < F::KB; ++kb)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[kb][i] = __builtin_amdgcn_exp2f(fmaf(s[kb][i], sc, -shift));
-        sum += s[kb][i];
-      }
-    l += sum;
+    weigh<F::KB, CB>(s, sc, m, l, acc);
 #pragma unroll
     for (int kb = 0; kb < F::KB; ++kb)
 #pragma unroll
@@ -172,69 +210,160 @@ template <typename T, int D> __global__ __launch_bounds__(THR, sizeof(T) * D > 2
     __syncthreads();
   }
   l = sum_xor32(l);
-  if (!on) return;
-  const size_t at = (size_t)(q.q0 + tok) * a.hq + hq;
-  if (a.splits > 1) {   // unnormalised: [split][row of the packed axis and head][d], then (m, l)
-    const size_t nrow = (size_t)query_tokens(a) * a.hq, ps = split * nrow + at;
-    float *p = a.part + ps * D;
-#pragma unroll
-    for (int b = 0; b < CB; ++b)
-#pragma unroll
-      for (int i = 0; i < 16; i += 4)
-        store4(p + b * 32 + 2 * i + 4 * h, acc[b][i], acc[b][i + 1], acc[b][i + 2], acc[b][i + 3]);
-    if (h == 0) {
-      float *ml = a.part + a.splits * nrow * D + ps * 2;
-      ml[0] = m * sc;
-      ml[1] = l;
-    }
-    return;
-  }
-  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // NaN stays NaN
-  T *out = static_cast<T *>(a.out) + at * D;
-#pragma unroll
-  for (int b = 0; b < CB; ++b)
-#pragma unroll
-    for (int i = 0; i < 16; i += 4)
-      store4(out + b * 32 + 2 * i + 4 * h, acc[b][i] * inv, acc[b][i + 1] * inv, acc[b][i + 2] * inv, acc[b][i + 3] * inv);
-  if (h == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : kLn2 * (m * sc + __builtin_amdgcn_logf(l));
+  if (on) finish<T, D>(a, (size_t)(q.q0 + tok) * a.hq + hq, split, h, m, l, acc);
 }
 
-// Joins the splits of a row: one thread per 4 entries.
-template <typename T, int D> __global__ __launch_bounds__(THR) void attn_join(AttnArgs a, size_t nrow, int last) {
-  constexpr int L = D / 4;
-  const size_t row = ((size_t)blockIdx.x * THR + threadIdx.x) / L;
-  const int e = (threadIdx.x % L) * 4;
-  if (row >= nrow) return;
-  if (a.cuq && row >= (size_t)max(a.cuq[last], 0) * a.hq) return;    // behind the last sequence
+// ---- Few rows ------------------------------------------------------------------
+// Single tokens and the like: at most 32 rows (of the average sequence and key head) meet long
+// keys, and the time is that of reading K and V once.  A workgroup is one wave with its own 32
+// rows, one split of the keys, tiles of 32 keys and its own part of LDS, so nothing waits at a
+// barrier: tile t + 1 is on its way while tile t is used.
+constexpr int FEW = 32;
+
+template <typename T, int D> __global__ __launch_bounds__(64) void attn_few(AttnArgs a) {
+  typedef Tile<T, D> Ti;
+  constexpr int TN = 32, CH = TN * Ti::CPR, PER = CH / 64, DB = D / 16, CB = D / 32;
+  __shared__ uint4 sk[2][CH], sv[2][CH];
+  const int lane = threadIdx.x, c = lane & 31, h = lane >> 5;
+  unsigned id = blockIdx.x;
+  const int head = id % (unsigned)a.hk;
+  id /= (unsigned)a.hk;
+  const int split = id % (unsigned)a.splits;
+  id /= (unsigned)a.splits;
+  int n, tile;
+  if (a.cuq) {
+    const Slot s = find_slot(a.cuq, a.n, id, a.group, FEW);
+    n = s.n;
+    tile = s.tile;
+  } else {
+    n = id % (unsigned)a.n;
+    tile = id / (unsigned)a.n;
+  }
+  const Seq q = seq_of(a, n);
+  const int rows = q.Lq * a.group;
+  if (tile >= (rows + FEW - 1) / FEW) return;
+  const int off = q.Lk - q.Lq, r0 = tile * FEW, r = min(r0 + c, rows - 1);
+  const int tok = r / (unsigned)a.group, hq = head * a.group + (r - tok * a.group);
+  const int lim = tok + off;
+  const int first_lim = (int)((unsigned)r0 / (unsigned)a.group) + off;
+  const int last_lim = (int)((unsigned)min(r0 + FEW - 1, rows - 1) / (unsigned)a.group) + off;
+  const int keys = max(min(q.Lk, last_lim + 1), 0), ktiles = (keys + TN - 1) / TN;
+  const int kt0 = __builtin_amdgcn_readfirstlane((int)((int64_t)ktiles * split / a.splits));
+  const int kt1 = __builtin_amdgcn_readfirstlane((int)((int64_t)ktiles * (split + 1) / a.splits));
+
+  const T *qrow = static_cast<const T *>(a.q) + (int64_t)(q.q0 + tok) * a.ldq + hq * D;
+  Frag<T> qf[DB];
+#pragma unroll
+  for (int b = 0; b < DB; ++b) qf[b] = global_frag(qrow, b, h);
+  const T *kg = static_cast<const T *>(a.k) + (int64_t)q.k0 * a.ldk + head * D;
+  const T *vg = static_cast<const T *>(a.v) + (int64_t)q.k0 * a.ldv + head * D;
+  const unsigned kstep = (unsigned)a.ldk * sizeof(T), vstep = (unsigned)a.ldv * sizeof(T);
+  auto copy = [&](int kt, int buf) {            // rows past the sequence's keys repeat its last one
+    const T *kp = kg + (int64_t)kt * TN * a.ldk, *vp = vg + (int64_t)kt * TN * a.ldv;
+    const int last = q.Lk - 1 - kt * TN;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = i * 64 + lane, row = e / Ti::CPR;
+      const unsigned in = ((e % Ti::CPR) ^ Ti::swizzle(row)) * 16;
+      copy_to_lds(kp, min(row, last) * kstep + in, lds_address(sk[buf] + i * 64));
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = i * 64 + lane, row = e / Ti::CPR;
+      const unsigned in = ((e % Ti::CPR) ^ Ti::swizzle(row)) * 16;
+      copy_to_lds(vp, min(row, last) * vstep + in, lds_address(sv[buf] + i * 64));
+    }
+  };
+  f16v acc[CB];
+#pragma unroll
+  for (int b = 0; b < CB; ++b) acc[b] = zero16();
+  float m = -INFINITY, l = 0.f;
+  const float sc = a.scale * kLog2e;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");         // from here on only copies are counted
+  if (kt0 < kt1) copy(kt0, 0);
+  for (int kt = kt0; kt < kt1; ++kt) {
+    const int buf = (kt - kt0) & 1;
+    if (kt + 1 < kt1) {
+      copy(kt + 1, buf ^ 1);
+      copies_done_but<2 * PER>();                          // this tile's are there
+    } else {
+      copies_done();
+    }
+    f16v s[1] = {zero16()};
+#pragma unroll
+    for (int b = 0; b < DB; ++b) mma(s[0], Ti::rows(sk[buf], 0, b, lane), qf[b]);
+    if (kt * TN + TN - 1 > first_lim) {
+      const int left = lim - kt * TN - 4 * h;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (8 * (i / 4) + (i & 3) > left) s[0][i] = -INFINITY;
+    }
+    weigh<1, CB>(s, sc, m, l, acc);
+#pragma unroll
+    for (int b16 = 0; b16 < 2; ++b16) {
+      const Frag<T> pf = result_frag<T>(s[0], b16);
+#pragma unroll
+      for (int b = 0; b < CB; ++b) mma(acc[b], Ti::cols(sv[buf], b16 * 16, b * 32, lane), pf);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");     // the buffer is read; the next copy may fill it
+  }
+  l = sum_xor32(l);
+  if (r0 + c < rows) finish<T, D>(a, (size_t)(q.q0 + tok) * a.hq + hq, split, h, m, l, acc);
+}
+
+// Joins the splits of a row: one workgroup a row, D / 4 threads side by side, the splits dealt
+// to the threads' groups and the groups added in order.
+template <typename T, int D> __global__ __launch_bounds__(THR) void attn_join(AttnArgs a, size_t nrow) {
+  constexpr int L = D / 4, GR = THR / L;
+  __shared__ float sl[GR];
+  __shared__ f4 so[GR][L];
+  const size_t row = blockIdx.x;
+  if (a.cuq && row >= (size_t)max(a.cuq[a.n], 0) * a.hq) return;    // behind the last sequence
+  const int g = threadIdx.x / L, e = threadIdx.x % L;
   const float *ml = a.part + a.splits * nrow * D;
   float m = -INFINITY;
   for (int s = 0; s < a.splits; ++s) m = fmaxf(m, ml[(s * nrow + row) * 2]);
   f4 o = zero4();
   float l = 0.f;
-  for (int s = 0; s < a.splits; ++s) {
+#pragma unroll 4
+  for (int s = g; s < a.splits; s += GR) {
     const float ms = ml[(s * nrow + row) * 2], ls = ml[(s * nrow + row) * 2 + 1];
-    if (ms == -INFINITY) continue;                            // nothing seen in this split
-    const float f = __builtin_amdgcn_exp2f(ms - m);
-    const f4 p = *reinterpret_cast<const f4 *>(a.part + (s * nrow + row) * D + e);
+    const f4 p = *reinterpret_cast<const f4 *>(a.part + (s * nrow + row) * D + e * 4);
+    const float f = ms == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ms - m);   // nothing seen in this split
     l = fmaf(f, ls, l);
     o += f * p;
   }
+  so[g][e] = o;
+  if (e == 0) sl[g] = l;
+  __syncthreads();
+  if (g) return;
+  for (int i = 1; i < GR; ++i) {
+    o += so[i][e];
+    l += sl[i];
+  }
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-  store4(static_cast<T *>(a.out) + row * D + e, o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+  store4(static_cast<T *>(a.out) + row * D + e * 4, o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
   if (e == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : kLn2 * (m + __builtin_amdgcn_logf(l));
 }
 
+// Whether a sequence's rows (the average's) fit a single wave.
+bool few_rows(const AttnArgs &a) { return (a.cuq ? (int64_t)a.Tq : (int64_t)a.n * a.Tq) * a.group <= (int64_t)FEW * a.n; }
+
 // Tiles of the packed row axis, at most; exact without cu.
 int64_t slots_of(const AttnArgs &a) {
-  if (a.cuq) return (int64_t)a.Tq * a.group / TM + a.n;
-  return ((int64_t)a.Tq * a.group + TM - 1) / TM * a.n;
+  const int tm = few_rows(a) ? FEW : TM;
+  if (a.cuq) return (int64_t)a.Tq * a.group / tm + a.n;
+  return ((int64_t)a.Tq * a.group + tm - 1) / tm * a.n;
 }
 
-// Splits of the keys: only where the tiles leave compute units idle, and at least 4 tiles
-// of 64 keys (of the average sequence) a split, so that joining stays cheap beside them.
+// Splits of the keys: only where the tiles leave compute units idle, and at least 256 keys (of
+// the average sequence) a split, so that joining stays cheap beside them.  Workgroups of few
+// rows are dealt twice over (5 of them stand on a compute unit): 16 sequences of up to 16 384
+// keys, 4 key heads of 128, took 98 us at 640 workgroups, 80 us at 1280 and 2560; of equal
+// lengths 117, 139 and 125 us.
 int splits_of(const AttnArgs &a) {
   const int64_t blocks = slots_of(a) * a.hk, keys = a.cuq ? a.Tk / a.n : a.Tk;
-  int64_t s = 512 / (blocks > 0 ? blocks : 1);
+  int64_t s = (few_rows(a) ? 2560 : 512) / (blocks > 0 ? blocks : 1);
   if (s > keys / 256) s = keys / 256;
   if (s > 64) s = 64;
   return s < 1 ? 1 : (int)s;
@@ -242,13 +371,13 @@ int splits_of(const AttnArgs &a) {
 
 template <typename T, int D> hipError_t run(AttnArgs &a, hipStream_t s) {
   const int64_t blocks = (int64_t)a.slots * a.hk * a.splits;
-  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((attn_fwd<T, D>), dim3((unsigned)blocks), dim3(THR), 0, s, a);
+  const size_t nrow = (size_t)query_tokens(a) * a.hq;
+  if (blocks > 0x7fffffff || (a.splits > 1 && nrow > 0x7fffffff)) return hipErrorInvalidValue;
+  if (few_rows(a)) hipLaunchKernelGGL((attn_few<T, D>), dim3((unsigned)blocks), dim3(64), 0, s, a);
+  else hipLaunchKernelGGL((attn_fwd<T, D>), dim3((unsigned)blocks), dim3(THR), 0, s, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  const size_t nrow = (size_t)query_tokens(a) * a.hq;
-  const size_t nb = (nrow * (D / 4) + THR - 1) / THR;
-  hipLaunchKernelGGL((attn_join<T, D>), dim3((unsigned)nb), dim3(THR), 0, s, a, nrow, a.n);
+  hipLaunchKernelGGL((attn_join<T, D>), dim3((unsigned)nrow), dim3(THR), 0, s, a, nrow);
   return hipGetLastError();
 }
 
