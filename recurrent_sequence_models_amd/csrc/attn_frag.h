@@ -15,6 +15,7 @@
 #pragma once
 #include <hip/hip_runtime.h>
 
+#include "lane_ops.h"
 #include "layer_kernels.h"
 #include "mfma_frag.h"
 
@@ -207,9 +208,12 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs &a, int n) {
   return s;
 }
 
-// max / sum with the lane 32 away.
-__device__ __forceinline__ float max_xor32(float x) { return fmaxf(x, __shfl_xor(x, 32)); }
-__device__ __forceinline__ float sum_xor32(float x) { return x + __shfl_xor(x, 32); }
+// max with the lane 32 away, by the lane swap of lane_ops.h.  Every lane of the wave calls it.
+__device__ __forceinline__ float max_xor32(float x) {
+  float a = x, b = x;
+  asm volatile("s_nop 1\n\tv_permlane32_swap_b32 %0, %1\n\ts_nop 1" : "+v"(a), "+v"(b));
+  return fmaxf(a, b);
+}
 
 // 4 consecutive results; bf16: rounded to nearest even.
 __device__ __forceinline__ void store4(__bf16 *p, float a, float b, float c, float d) {

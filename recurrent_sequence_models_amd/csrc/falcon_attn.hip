@@ -209,7 +209,7 @@ template <typename T, int D> __global__ __launch_bounds__(THR, sizeof(T) * D > 2
     copies_done();
     __syncthreads();
   }
-  l = sum_xor32(l);
+  l = add_xor32(l);
   if (on) finish<T, D>(a, (size_t)(q.q0 + tok) * a.hq + hq, split, h, m, l, acc);
 }
 
@@ -307,7 +307,7 @@ template <typename T, int D> __global__ __launch_bounds__(64) void attn_few(Attn
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");     // the buffer is read; the next copy may fill it
   }
-  l = sum_xor32(l);
+  l = add_xor32(l);
   if (r0 + c < rows) finish<T, D>(a, (size_t)(q.q0 + tok) * a.hq + hq, split, h, m, l, acc);
 }
 

@@ -23,7 +23,7 @@ namespace {
 
 constexpr int THR = 256, TR = 128;   // 4 waves of 32 rows (or keys)
 
-// Per row (query token and head): D = do . o, and lse in base 2, +inf where the row sees
+// Per row (query token and head): -D = -do . o, where the products do . v start from, and lse in base 2, +inf where the row sees
 // nothing, so that all its weights e^{s - lse} come out 0.
 template <typename T, int D> __global__ __launch_bounds__(THR) void attn_delta(AttnArgs a, size_t nrow) {
   constexpr int E = 16 / (int)sizeof(T), L = D / E;
@@ -41,7 +41,7 @@ template <typename T, int D> __global__ __launch_bounds__(THR) void attn_delta(A
   if constexpr (L == 32) s = add_xor16(s);
   if (row < nrow && e == 0) {
     const float lse = a.lse_in[row];
-    a.delta[row] = s;
+    a.delta[row] = -s;
     a.lse2[row] = lse == -INFINITY ? INFINITY : lse * kLog2e;
   }
 }
@@ -68,7 +68,7 @@ __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_kv(
   constexpr int KR = DB - KEYS_IN_LDS<T, D>;
   __shared__ uint4 sq[2][Cp::CH], sg[2][Cp::CH], sv[VL ? CpV::CH : 1];
   __shared__ Frag<T> sk[DB > KR ? DB - KR : 1][THR];
-  __shared__ __align__(16) float sL[2][64], sD[2][64];   // lse (base 2) and D of the rows
+  __shared__ __align__(16) float sL[2][64], sD[2][64];   // lse (base 2) and -D of the rows
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 31, h = lane >> 5;
   unsigned id = blockIdx.x;
   const int head = id % (unsigned)a.hk;
@@ -162,20 +162,22 @@ __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_kv(
 #pragma unroll
     for (int rb = 0; rb < TQ; rb += 32) {
       if (rt + rb >= rows) break;
-      f16v s = zero16(), g = zero16();
+      f16v s = zero16(), g;
 #pragma unroll
       for (int b = 0; b < DB; ++b) mma(s, Ti::rows(sq[buf], rb, b, lane), keys(b));
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const f4 Dr = *reinterpret_cast<const f4 *>(&sD[buf][rb + 8 * b + 4 * h]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) g[4 * b + i] = Dr[i];
+      }
 #pragma unroll
       for (int b = 0; b < DB; ++b) mma(g, Ti::rows(sg[buf], rb, b, lane), value(b));
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         const f4 L = *reinterpret_cast<const f4 *>(&sL[buf][rb + 8 * b + 4 * h]);
-        const f4 Dr = *reinterpret_cast<const f4 *>(&sD[buf][rb + 8 * b + 4 * h]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[4 * b + i] = __builtin_amdgcn_exp2f(fmaf(s[4 * b + i], sc, -L[i]));
-          g[4 * b + i] -= Dr[i];
-        }
+        for (int i = 0; i < 4; ++i) s[4 * b + i] = __builtin_amdgcn_exp2f(fmaf(s[4 * b + i], sc, -L[i]));
       }
       if (masked) {   // the same for the whole wave; once, so that what is around it stays in two pieces
 #pragma unroll
@@ -306,7 +308,9 @@ __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_q(A
     const int buf = kt & 1;
     if (kt + 1 < ktiles) copy(kt + 1, buf ^ 1);            // its last readers are behind the barrier
     if (kt * TN <= wave_lim) {
-      f16v s = zero16(), g = zero16();
+      f16v s = zero16(), g;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) g[i] = Dr;
 #pragma unroll
       for (int b = 0; b < DB; ++b) mma(s, Ti::rows(sk[buf], 0, b, lane), qf[b]);
 #pragma unroll
@@ -319,7 +323,7 @@ __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_q(A
         for (int i = 0; i < 16; ++i) s[i] = 8 * (i / 4) + (i & 3) > left ? 0.f : s[i];
       }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[i] *= g[i] - Dr;
+      for (int i = 0; i < 16; ++i) s[i] *= g[i];
 #pragma unroll
       for (int b16 = 0; b16 < 2; ++b16) {
         const Frag<T> sf = result_frag<T>(s, b16);
