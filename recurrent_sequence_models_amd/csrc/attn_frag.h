@@ -215,6 +215,35 @@ __device__ __forceinline__ float max_xor32(float x) {
   return fmaxf(a, b);
 }
 
+// Whether any of 16 bytes of entries is infinite or NaN (exponent all ones).
+__device__ __forceinline__ bool nonfinite(const uint4v &u, __bf16) {
+  unsigned r = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r |= (u[j] & 0x7fff7fffu) + 0x00800080u;
+  return (r & 0x80008000u) != 0;
+}
+__device__ __forceinline__ bool nonfinite(const uint4v &u, float) {
+  unsigned r = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r |= (u[j] & 0x7fffffffu) + 0x00800000u;
+  return (r & 0x80000000u) != 0;
+}
+
+// The same 16 bytes with zeros in their place.
+__device__ __forceinline__ uint4v only_finite(uint4v u, __bf16) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const unsigned top = ((u[j] & 0x7fff7fffu) + 0x00800080u) & 0x80008000u;   // the top bit of a half that goes
+    u[j] &= ~((top >> 15) * 0xffffu);
+  }
+  return u;
+}
+__device__ __forceinline__ uint4v only_finite(uint4v u, float) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) u[j] = (u[j] & 0x7fffffffu) + 0x00800000u >= 0x80000000u ? 0u : u[j];
+  return u;
+}
+
 // 4 consecutive results; bf16: rounded to nearest even.
 __device__ __forceinline__ void store4(__bf16 *p, float a, float b, float c, float d) {
   *reinterpret_cast<bf4 *>(p) = __builtin_convertvector(f4{a, b, c, d}, bf4);

@@ -64,6 +64,45 @@ __device__ __forceinline__ void weigh(f16v (&s)[KB], float sc, float &m, float &
   l += sum;
 }
 
+// acc += V^T P^T for one tile of KB * 32 keys.
+template <typename T, int D, int KB>
+__device__ __forceinline__ void add_values(f16v (&acc)[D / 32], const f16v (&s)[KB], const uint4 *sv, int lane) {
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+    for (int b16 = 0; b16 < 2; ++b16) {
+      const Frag<T> pf = result_frag<T>(s[kb], b16);
+#pragma unroll
+      for (int b = 0; b < D / 32; ++b) mma(acc[b], Tile<T, D>::cols(sv, kb * 32 + b16 * 16, b * 32, lane), pf);
+    }
+}
+
+// Infinite and NaN values behind the mask.  A weight of 0 times one of them is not 0, so in a
+// tile with keys that some rows do not see they are set to 0 in LDS, and added afterwards, as
+// they are, to the results of the rows that do see them: by the lane that wrote them (which
+// reads its own writes; the sums are no longer in registers, so that this path costs the loop
+// none), keys j0 .. j1 - 1.
+template <typename T> __device__ __forceinline__ bool clean16(uint4 *p) {
+  uint4v u = *reinterpret_cast<const uint4v *>(p);
+  if (!nonfinite(u, T())) return false;
+  *reinterpret_cast<uint4v *>(p) = only_finite(u, T());
+  return true;
+}
+template <typename T, typename O, int D>
+__device__ __forceinline__ void add_nonfinite(O *out, const T *v, int64_t ld, int j0, int j1, int h) {
+#pragma unroll 1
+  for (int j = j0; j < j1; ++j)
+#pragma unroll 1
+    for (int e = 4 * h; e < D; e += 8) {
+      const f4 x = to_f4(ld4(v + j * ld + e));
+      f4 o = to_f4(ld4(out + e));
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (!(fabsf(x[i]) < INFINITY)) o[i] += x[i];
+      store4(out + e, o[0], o[1], o[2], o[3]);
+    }
+}
+
 // A lane's row: the result and lse, or, of one of several splits, the unnormalised sum [split]
 // [row of the packed axis and head][d], then (reference in base 2, sum of weights).
 template <typename T, int D>
@@ -95,11 +134,18 @@ __device__ __forceinline__ void finish(const AttnArgs &a, size_t at, int split, 
   if (h == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : kLn2 * (m * sc + __builtin_amdgcn_logf(l));
 }
 
-template <typename T, int D> __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_fwd(AttnArgs a) {
+template <typename T, int D>
+__device__ __forceinline__ void restore(const AttnArgs &a, size_t at, int split, const T *v, int j0, int j1, int h) {
+  if (a.splits > 1) add_nonfinite<T, float, D>(a.part + (split * (size_t)query_tokens(a) * a.hq + at) * D, v, a.ldv, j0, j1, h);
+  else add_nonfinite<T, T, D>(static_cast<T *>(a.out) + at * D, v, a.ldv, j0, j1, h);
+}
+
+template <typename T, int D> __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : sizeof(T) * D > 128 ? 2 : 4) void attn_fwd(AttnArgs a) {
   typedef Fwd<T, D> F;
   typedef Tile<T, D> Ti;
   constexpr int TN = F::TN, DB = D / 16, CB = D / 32;
   __shared__ uint4 sk[2][F::CH], sv[2][F::CH];
+  __shared__ int sbad;                          // a value was cleaned
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 31, h = lane >> 5;
 
   // key head fastest (a head stays on one die where 8 and hk divide one another), then the
@@ -129,6 +175,7 @@ template <typename T, int D> __global__ __launch_bounds__(THR, sizeof(T) * D > 2
   const int tok = r / (unsigned)a.group, hq = head * a.group + (r - tok * a.group);
   const int lim = tok + off;                    // the last key this row sees
   const int first_lim = (int)((unsigned)min(r0, rows - 1) / (unsigned)a.group) + off;
+  const int tile_lim = (int)((unsigned)(tile * TM) / (unsigned)a.group) + off;
   const int wave_lim = (int)((unsigned)min(r0 + 31, rows - 1) / (unsigned)a.group) + off;
   const int last_lim = (int)((unsigned)min(tile * TM + TM - 1, rows - 1) / (unsigned)a.group) + off;
   const int keys = max(min(q.Lk, last_lim + 1), 0), ktiles = (keys + TN - 1) / TN;
@@ -142,6 +189,8 @@ template <typename T, int D> __global__ __launch_bounds__(THR, sizeof(T) * D > 2
   // Copying tiles.  Rows past the sequence's keys repeat its last one: no row of another
   // sequence is read, and their weights are 0.
   typedef Copy<T, D, TN> Cp;
+  if (tid == 0) sbad = 0;
+  __syncthreads();                              // before any wave sets it
   const T *kg = static_cast<const T *>(a.k) + (int64_t)q.k0 * a.ldk + head * D;
   const T *vg = static_cast<const T *>(a.v) + (int64_t)q.k0 * a.ldv + head * D;
   const unsigned kstep = (unsigned)a.ldk * sizeof(T), vstep = (unsigned)a.ldv * sizeof(T);
@@ -168,14 +217,26 @@ template <typename T, int D> __global__ __launch_bounds__(THR, sizeof(T) * D > 2
     }
   };
 
+  // From tile hidden0 on, tiles have keys of the sequence that some row of this tile does not see;
+  // every wave cleans the values that it copied, before the barrier that hands the tile over.
+  const int hidden0 = tile_lim + 1 < q.Lk ? max(tile_lim + 1, 0) / TN : kt1;
+  auto clean = [&](int kt, int buf) {
+    if (kt < hidden0) return;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < Cp::PER; ++i)
+      if (Cp::has(i, wave)) bad |= clean16<T>(&sv[buf][256 * i + tid]);
+    if (__any(bad) && lane == 0) sbad = 1;
+  };
+
+  const float sc = a.scale * kLog2e;
   f16v acc[CB];
+  float m = -INFINITY, l = 0.f;                 // the weights' reference score; this lane's half of the sum
 #pragma unroll
   for (int b = 0; b < CB; ++b) acc[b] = zero16();
-  float m = -INFINITY, l = 0.f;                 // the weights' reference score; this lane's half of the sum
-  const float sc = a.scale * kLog2e;
-
   if (kt0 < kt1) copy(kt0, 0);
   copies_done();
+  if (kt0 < kt1) clean(kt0, 0);
   __syncthreads();
   for (int kt = kt0; kt < kt1; ++kt) {
     const int buf = (kt - kt0) & 1;
@@ -197,20 +258,17 @@ template <typename T, int D> __global__ __launch_bounds__(THR, sizeof(T) * D > 2
           if (kb * 32 + 8 * (i / 4) + (i & 3) > left) s[kb][i] = -INFINITY;
     }
     weigh<F::KB, CB>(s, sc, m, l, acc);
-#pragma unroll
-    for (int kb = 0; kb < F::KB; ++kb)
-#pragma unroll
-      for (int b16 = 0; b16 < 2; ++b16) {
-        const Frag<T> pf = result_frag<T>(s[kb], b16);
-#pragma unroll
-        for (int b = 0; b < CB; ++b) mma(acc[b], Ti::cols(sv[buf], kb * 32 + b16 * 16, b * 32, lane), pf);
-      }
+    add_values<T, D, F::KB>(acc, s, sv[buf], lane);
     }
     copies_done();
+    if (kt + 1 < kt1) clean(kt + 1, buf ^ 1);
     __syncthreads();
   }
   l = add_xor32(l);
-  if (on) finish<T, D>(a, (size_t)(q.q0 + tok) * a.hq + hq, split, h, m, l, acc);
+  if (!on) return;
+  const size_t at = (size_t)(q.q0 + tok) * a.hq + hq;
+  finish<T, D>(a, at, split, h, m, l, acc);
+  if (sbad) restore<T, D>(a, at, split, vg, max(kt0, hidden0) * TN, min(lim + 1, kt1 * TN), h);
 }
 
 // ---- Few rows ------------------------------------------------------------------
@@ -220,7 +278,7 @@ template <typename T, int D> __global__ __launch_bounds__(THR, sizeof(T) * D > 2
 // barrier: tile t + 1 is on its way while tile t is used.
 constexpr int FEW = 32;
 
-template <typename T, int D> __global__ __launch_bounds__(64) void attn_few(AttnArgs a) {
+template <typename T, int D> __global__ __launch_bounds__(64, sizeof(T) * D > 256 ? 1 : 2) void attn_few(AttnArgs a) {
   typedef Tile<T, D> Ti;
   constexpr int TN = 32, CH = TN * Ti::CPR, PER = CH / 64, DB = D / 16, CB = D / 32;
   __shared__ uint4 sk[2][CH], sv[2][CH];
@@ -274,12 +332,14 @@ template <typename T, int D> __global__ __launch_bounds__(64) void attn_few(Attn
       copy_to_lds(vp, min(row, last) * vstep + in, lds_address(sv[buf] + i * 64));
     }
   };
+  const float sc = a.scale * kLog2e;
   f16v acc[CB];
+  float m = -INFINITY, l = 0.f;
+  bool bad = false;                                        // a value was cleaned
+  const int hidden0 = first_lim + 1 < q.Lk ? max(first_lim + 1, 0) / TN : kt1;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");         // from here on only copies are counted
 #pragma unroll
   for (int b = 0; b < CB; ++b) acc[b] = zero16();
-  float m = -INFINITY, l = 0.f;
-  const float sc = a.scale * kLog2e;
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");         // from here on only copies are counted
   if (kt0 < kt1) copy(kt0, 0);
   for (int kt = kt0; kt < kt1; ++kt) {
     const int buf = (kt - kt0) & 1;
@@ -288,6 +348,11 @@ template <typename T, int D> __global__ __launch_bounds__(64) void attn_few(Attn
       copies_done_but<2 * PER>();                          // this tile's are there
     } else {
       copies_done();
+    }
+    if (kt >= hidden0) {                                   // keys that some row does not see
+#pragma unroll
+      for (int i = 0; i < PER; ++i) bad |= clean16<T>(&sv[buf][64 * i + lane]);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
     f16v s[1] = {zero16()};
 #pragma unroll
@@ -299,16 +364,15 @@ template <typename T, int D> __global__ __launch_bounds__(64) void attn_few(Attn
         if (8 * (i / 4) + (i & 3) > left) s[0][i] = -INFINITY;
     }
     weigh<1, CB>(s, sc, m, l, acc);
-#pragma unroll
-    for (int b16 = 0; b16 < 2; ++b16) {
-      const Frag<T> pf = result_frag<T>(s[0], b16);
-#pragma unroll
-      for (int b = 0; b < CB; ++b) mma(acc[b], Ti::cols(sv[buf], b16 * 16, b * 32, lane), pf);
-    }
+    add_values<T, D, 1>(acc, s, sv[buf], lane);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");     // the buffer is read; the next copy may fill it
   }
   l = add_xor32(l);
-  if (r0 + c < rows) finish<T, D>(a, (size_t)(q.q0 + tok) * a.hq + hq, split, h, m, l, acc);
+  const bool cleaned = __any(bad);
+  if (r0 + c >= rows) return;
+  const size_t at = (size_t)(q.q0 + tok) * a.hq + hq;
+  finish<T, D>(a, at, split, h, m, l, acc);
+  if (cleaned) restore<T, D>(a, at, split, vg, max(kt0, hidden0) * TN, min(lim + 1, kt1 * TN), h);
 }
 
 // Joins the splits of a row: one workgroup a row, D / 4 threads side by side, the splits dealt

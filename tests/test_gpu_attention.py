@@ -187,3 +187,39 @@ def test_refusals():
         with pytest.raises(err):
             f_()
             raise AssertionError(f"call {i} was taken")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("ql,kl,hq,hk,d", [([200], [200], 2, 2, 64), ([130], [170], 4, 1, 128), ([40], [40], 3, 1, 32),
+                                           ([4], [90], 2, 1, 64), ([3], [1500], 4, 2, 128), ([70, 60], [70, 61], 2, 1, 64)])
+def test_keys_behind_the_mask(dtype, ql, kl, hq, hk, d):
+    """Infinite and NaN keys and values do not reach the queries that do not see them, and do
+    reach those that see them (split keys too)."""
+    import torch
+    from recurrent_sequence_models_amd import attention_fwd
+    q, k, v = rand(1, sum(ql), hq, d, dtype=dtype), rand(2, sum(kl), hk, d, dtype=dtype), rand(3, sum(kl), hk, d, dtype=dtype)
+    kw = dict(cu_seqlens=offsets(ql), cu_seqlens_k=offsets(kl))
+    o, lse = attention_fwd(q, k, v, **kw)
+    for back in (1, 2, min(ql[0] - 1, 37)):                # the bad key: so many from the first sequence's end
+        j = kl[0] - back
+        i = ql[0] - back                                   # the first query that sees it
+        for name, bad in (("nan", (float("nan"),) * d), ("inf", (float("inf"), -float("inf")) * (d // 2))):
+            v2 = v.clone()
+            v2[j, :] = torch.tensor(bad, device="cuda").to(v.dtype)
+            o2, lse2 = attention_fwd(q, k, v2, **kw)
+            keep = torch.ones(sum(ql), dtype=torch.bool, device="cuda")
+            keep[i:ql[0]] = False
+            assert torch.equal(o2[keep], o[keep]) and torch.equal(lse2, lse), (name, back)
+            seen = o2[~keep].float()
+            assert torch.isnan(seen).all() if name == "nan" else torch.equal(seen, v2[j].float().repeat_interleave(
+                hq // hk, 0).expand_as(seen)), (name, back)
+        k2 = k.clone()
+        k2[j] = float("nan")
+        o2, lse2 = attention_fwd(q, k2, v, **kw)
+        assert torch.equal(o2[keep], o[keep]) and torch.equal(lse2[keep], lse[keep])
+        assert torch.isnan(o2[~keep].float()).all() and torch.isnan(lse2[~keep]).all()
+        v2[j], v2[j - 1] = float("inf"), -float("inf")     # both: NaN where both are seen
+        o2, _ = attention_fwd(q, k, v2, **kw)
+        assert torch.isnan(o2[i:ql[0]].float()).all()
+        if i > 0:
+            assert torch.all(o2[i - 1].float() == -float("inf"))
