@@ -124,42 +124,61 @@ __device__ __forceinline__ int seq_of(const int *cu, int N, int t) {
   return lo;
 }
 
-// The same for a token that the whole wave asks for: 64 places at a time, one round trip to
-// memory for up to 64 sequences, two for 4096.
-__device__ __forceinline__ int wave_seq_of(const int *cu, int N, int t) {
-  const int lane = threadIdx.x & 63;
-  int lo = 0, len = N;
-  while (len > 1) {
-    const int step = (len + 63) / 64, at = lane * step;
-    const int before = __popcll(__ballot(at < len && cu[lo + min(at, len - 1)] <= t));
-    const int skip = max(before - 1, 0) * step;
-    lo += skip;
-    len = min(step, len - skip);
+// The offsets as a wave reads them while it places its steps: up to 63 sequences in one register
+// (lane i holds cu[i], loaded before anything else is waited for), more from memory.  Every
+// lane of the wave calls them.
+struct Offsets {
+  const int *cu;
+  int N, reg;
+  __device__ __forceinline__ Offsets(const ScanArgs &a) : cu(a.cu), N(a.nseq), reg(0) {
+    if (cu && N < 64) reg = cu[min((int)(threadIdx.x & 63), N)];
   }
-  return lo;
-}
+  __device__ __forceinline__ int at(int i) const { return N < 64 ? __shfl(reg, i) : cu[i]; }
+  __device__ __forceinline__ int last() const { return N < 64 ? __builtin_amdgcn_readlane(reg, N) : cu[N]; }
+  // the sequence that holds token t, the same t in every lane: 64 places at a time
+  __device__ __forceinline__ int seq_of(int t) const {
+    const int lane = threadIdx.x & 63;
+    if (N < 64) return max((int)__popcll(__ballot(lane < N && reg <= t)) - 1, 0);
+    int lo = 0, len = N;
+    while (len > 1) {
+      const int step = (len + 63) / 64, at = lane * step;
+      const int before = __popcll(__ballot(at < len && cu[lo + min(at, len - 1)] <= t));
+      const int skip = max(before - 1, 0) * step;
+      lo += skip;
+      len = min(step, len - skip);
+    }
+    return lo;
+  }
+};
 
 // Which of a thread's steps t0 .. t0 + SEG - 1 are the first or last of a packed sequence.
 // (Batch rows begin and end with the chain: the carry of rank 0 and the chain's result.)
 struct Marks { unsigned first, last; };
 
-template <int SEG> __device__ __forceinline__ Marks marks_of(const ScanArgs &a, int t0, int end) {
+template <int SEG> __device__ __forceinline__ Marks marks_of(const Offsets &cu, int t0, int end) {
   Marks m{0, 0};
-  int n = wave_seq_of(a.cu, a.nseq, __builtin_amdgcn_readfirstlane(t0));   // of the wave's first step
-  if (t0 >= end) return m;
-  while (n + 1 < a.nseq && a.cu[n + 1] <= t0) ++n;
-  if (a.cu[n] == t0) m.first = 1;
-  for (; n < a.nseq; ++n) {      // walk the sequence ends inside the steps
-    const int e = a.cu[n + 1];
-    if (e > t0 + SEG) break;
-    if (e > t0) {
+  int n = cu.seq_of(__builtin_amdgcn_readfirstlane(t0));   // of the wave's first step, then of this thread's
+  bool more = true;
+  while (__any(more)) {
+    const int e = cu.at(min(n + 1, cu.N));
+    more = n + 1 < cu.N && e <= t0;
+    n += more;
+  }
+  const bool in = t0 < end;
+  if (cu.at(n) == t0 && in) m.first = 1;
+  more = in;
+  while (__any(more)) {          // the sequence ends inside the steps
+    const int e = cu.at(min(n + 1, cu.N));
+    more = more && n < cu.N && e <= t0 + SEG;
+    if (more && e > t0) {
       m.last |= 1u << (e - 1 - t0);
       if (e < end && e < t0 + SEG) m.first |= 1u << (e - t0);
     }
+    n += more;
   }
   return m;
 }
-// Row `seq` of a [nseq, D] array for the packed sequence of token t; zeros without the array.
+// The row of a [nseq, D] array of the packed sequence of token t; zeros without the array.
 template <int N>
 __device__ __forceinline__ void load_seq(const ScanArgs &a, const float *p, int t, int ch, float (&o)[N]) {
 #pragma unroll
@@ -367,17 +386,18 @@ __device__ __forceinline__ float scan_chunk(const ScanArgs &a, Lds<W> &s, size_t
 template <typename T, bool MIX, bool PACKED> __global__ __launch_bounds__(THR, 4) void scan_fwd(ScanArgs a) {
   constexpr int C = CPT<T>, W = TC<T>;
   __shared__ __align__(16) Lds<W> s;
+  const Offsets offs(a);
   const Place p = place<T>(a);
   const int tid = threadIdx.x, grp = tid / LPR, cl = (tid % LPR) * C, ch = p.c0 + cl;
   const int t0 = p.rank * CHUNK + grp * SEG;
-  const int end = PACKED ? min(a.cu[a.nseq], a.T) : a.T;
+  const int end = PACKED ? min(offs.last(), a.T) : a.T;
   const Steps<T, SEG> st(a, p.row, p.rank, grp, end, ch);
   u4 xr[SEG], gr[SEG];
   st.load(a.x, xr);
   st.load(a.g, gr);
   Marks m{0, 0};
   if (PACKED) {
-    m = marks_of<SEG>(a, t0, end);
+    m = marks_of<SEG>(offs, t0, end);
     if (ch >= a.D) m = Marks{0, 0};
     copy_empty<C>(a, a.init, a.final_state, p.rank, grp, GRPS, ch);
   }
@@ -436,11 +456,12 @@ template <typename T, bool MIX, bool PACKED> __global__ __launch_bounds__(THR, 4
 template <typename T, bool MIX, bool PACKED> __global__ __launch_bounds__(THR, 4) void scan_bwd(ScanArgs a) {
   constexpr int C = CPT<T>, W = TC<T>;
   __shared__ __align__(16) Lds<W> s;
+  const Offsets offs(a);
   const Place p = place<T>(a);
   const int chunk = a.NC - 1 - p.rank;
   const int tid = threadIdx.x, grp = tid / LPR, cl = (tid % LPR) * C, ch = p.c0 + cl;
   const int t0 = chunk * CHUNK + grp * SEG;
-  const int end = PACKED ? min(a.cu[a.nseq], a.T) : a.T;
+  const int end = PACKED ? min(offs.last(), a.T) : a.T;
   const Steps<T, SEG> st(a, p.row, chunk, grp, end, ch);
   u4 xr[SEG], gr[SEG], dr[SEG];
   st.load(a.x, xr);
@@ -448,7 +469,7 @@ template <typename T, bool MIX, bool PACKED> __global__ __launch_bounds__(THR, 4
   st.load(a.dh, dr);
   Marks m{0, 0};
   if (PACKED) {
-    m = marks_of<SEG>(a, t0, end);
+    m = marks_of<SEG>(offs, t0, end);
     if (ch >= a.D) m = Marks{0, 0};
     copy_empty<C>(a, a.d_final, a.d_init, p.rank, grp, GRPS, ch);
   }

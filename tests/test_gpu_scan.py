@@ -38,6 +38,8 @@ def run_case(dtype, shape, mix, lens=None, init=True, kind="slow", seed=1, back=
     """Forward and backward of one batch, every sequence against the oracle."""
     import torch
     from recurrent_sequence_models_amd import gated_scan, gated_scan_bwd
+    if lens is not None:
+        shape = (sum(lens) + behind, shape[-1])
     n, D = (len(lens) if lens is not None else shape[0]), shape[-1]
     x, dh = rand(seed, *shape, dtype=dtype), rand(seed + 1, *shape, dtype=dtype)
     g = gates(seed + 2, *shape, dtype=dtype, kind=kind)
@@ -118,6 +120,13 @@ PACKED = [[1], [5, 0, 0, 3], [1] * 40, [3, 1, 1, 2, 900, 1, 0, 255, 256, 1, 257]
 @pytest.mark.parametrize("mix,init", [(False, True), (True, False)])
 def test_packed(dtype, lens, mix, init):
     run_case(dtype, (sum(lens), 40), mix, lens=lens, init=init, seed=len(lens))
+
+
+@pytest.mark.parametrize("n", [62, 63, 64, 65, 400, 4200])
+def test_many_sequences(n):
+    """More sequences than one register of offsets holds, and more than 64 x 64; some empty."""
+    r = np.random.Generator(np.random.PCG64(n))
+    run_case("fp32", (0, 8), True, lens=[int(x) for x in r.integers(0, 9 if n < 1000 else 3, size=n)], seed=n)
 
 
 @pytest.mark.parametrize("behind", [1, 300])
