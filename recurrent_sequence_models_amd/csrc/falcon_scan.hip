@@ -285,83 +285,48 @@ __device__ __forceinline__ void step_of(const u4 &x, const u4 &g, float (&lam)[C
 // twice).
 constexpr int SEG = 4, GRPS = CHUNK / SEG, THR = GRPS * LPR, WAVES = THR / 64, GPW = GRPS / WAVES;
 
-template <int W> struct Lds {
+template <int W> struct Maps {
   float A[GRPS][W], H[GRPS][W];          // the groups' maps; H then holds the values carried into them
   float wA[WAVES][W], wH[WAVES][W];      // the waves' maps
-  unsigned long long words[GROUP][W];    // words read from the column's chain
 };
+struct Map { float A, H; };
+template <int W> using Words = unsigned long long[GROUP][W];   // words read from the column's chain
 
-// The values carried into the groups (to s.H), from the groups' maps, in time order or (REV)
-// against it.  Without CHAIN, *first is the value carried into the chunk.  With it the
-// chunk is number `rank` of its column's chain and *first the value carried into rank 0: it
-// is read by rank 0 alone, which passes it on as it does its map, since its memory may be
-// where the chain's result goes.  Returns, in lanes < W of every wave, the value that leaves
-// the chunk.  Every thread of the workgroup calls it; the maps are the calling wave's own.
-template <int W, bool REV, bool CHAIN>
-__device__ __forceinline__ float scan_chunk(const ScanArgs &a, Lds<W> &s, size_t col, int rank, const float *first) {
+// All of these run one lane a channel (lanes < W), in time order or (REV) against it; every
+// thread of the workgroup calls them.
+
+// The map of this wave's groups, from the groups' maps that its lanes wrote.
+template <int W, bool REV> __device__ __forceinline__ void wave_map(Maps<W> &s) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const bool on = lane < W;
-  const int ng = (a.NC + GROUP - 1) / GROUP, grp = rank / GROUP, g0 = grp * GROUP, j = rank - g0;
-  unsigned long long *agg = nullptr, *pre = nullptr;
-  if (CHAIN && a.NC > 1) {
-    agg = a.agg + col * a.NC * W + lane;
-    pre = a.pre + col * ng * W + lane;
-  }
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the wave's maps are in LDS
-  if (on) {
-    float A = 1.f, H = 0.f;
+  if (lane >= W) return;
+  float A = 1.f, H = 0.f;
 #pragma unroll
-    for (int i = 0; i < GPW; ++i) {
-      const int q = wave * GPW + (REV ? GPW - 1 - i : i);
-      H = apply(s.A[q][lane], s.H[q][lane], H);
-      A *= s.A[q][lane];
-    }
-    s.wA[wave][lane] = A;
-    s.wH[wave][lane] = H;
+  for (int i = 0; i < GPW; ++i) {
+    const int q = wave * GPW + (REV ? GPW - 1 - i : i);
+    H = apply(s.A[q][lane], s.H[q][lane], H);
+    A *= s.A[q][lane];
   }
-  __syncthreads();
-  float At = 1.f, Ht = 0.f, y = 0.f;
-  if (on) {
+  s.wA[wave][lane] = A;
+  s.wH[wave][lane] = H;
+}
+// (A barrier later:) the chunk's map.
+template <int W, bool REV> __device__ __forceinline__ Map chunk_map(const Maps<W> &s) {
+  const int lane = threadIdx.x & 63;
+  Map m{1.f, 0.f};
+  if (lane < W)
 #pragma unroll
     for (int i = 0; i < WAVES; ++i) {
       const int w = REV ? WAVES - 1 - i : i;
-      Ht = apply(s.wA[w][lane], s.wH[w][lane], Ht);
-      At *= s.wA[w][lane];
+      m.H = apply(s.wA[w][lane], s.wH[w][lane], m.H);
+      m.A *= s.wA[w][lane];
     }
-  }
-  if (!CHAIN || a.NC == 1) {
-    if (on && first) y = first[lane];
-  } else {
-    // one wave publishes, and each reads two words of the chain: the value carried into the
-    // group of chunks (word 15) and the maps of the group's chunks before this one
-    if (on && wave == 0) {
-      if (rank + 1 < a.NC) publish(agg + (size_t)rank * W, word(At, Ht));
-      if (rank == 0) publish(pre, word(0.f, first ? first[lane] : 0.f));
-    }
-    if (on) {
-#pragma unroll
-      for (int k = 2 * wave; k < 2 * wave + 2; ++k) {
-        if (k >= j && k < GROUP - 1) continue;
-        const unsigned long long *p = k == GROUP - 1 ? pre + (size_t)grp * W : agg + (size_t)(g0 + k) * W;
-        unsigned long long v;
-        // ends: the word is published by a chunk whose ticket was drawn earlier (or, word 15
-        // of rank 0's group, by rank 0 itself above)
-        while ((v = peek(p)) == EMPTY) __builtin_amdgcn_s_sleep(1);
-        s.words[k][lane] = v;
-      }
-    }
-    __syncthreads();
-    if (on) {
-      y = __uint_as_float((unsigned)s.words[GROUP - 1][lane]);
-      for (int i = 0; i < j; ++i) {
-        const unsigned long long v = s.words[i][lane];
-        y = apply(__uint_as_float((unsigned)(v >> 32)), __uint_as_float((unsigned)v), y);
-      }
-      if (wave == 0 && j == GROUP - 1 && rank + 1 < a.NC) publish(pre + (size_t)(grp + 1) * W, word(0.f, apply(At, Ht, y)));
-    }
-  }
-  const float out = apply(At, Ht, y);
-  if (on) {
+  return m;
+}
+// The values carried into the groups (to s.H), from the one carried into the chunk.
+template <int W, bool REV> __device__ __forceinline__ void spread(Maps<W> &s, float y) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  if (lane < W) {
 #pragma unroll
     for (int i = 0; i < WAVES; ++i) {
       const int w = REV ? WAVES - 1 - i : i;
@@ -377,15 +342,66 @@ __device__ __forceinline__ float scan_chunk(const ScanArgs &a, Lds<W> &s, size_t
     }
   }
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the wave's carries are in LDS
-  return out;
 }
+
+// The chain of a column's chunks (NC > 1).  The chunk of rank `rank` publishes its map; rank 0
+// also publishes *first, the value carried into it, which it alone reads, since its memory may
+// be where the chain's result goes.
+template <int W> struct Chain {
+  unsigned long long *agg, *pre;         // this lane's channel: the chunks' maps, the groups' carries
+  int rank, grp, j, NC;                  // j: place in the group of chunks
+  __device__ __forceinline__ Chain(const ScanArgs &a, size_t col, int rank) : rank(rank), NC(a.NC) {
+    const int lane = threadIdx.x & 63, ng = (a.NC + GROUP - 1) / GROUP;
+    grp = rank / GROUP;
+    j = rank % GROUP;
+    agg = a.agg + col * a.NC * W + lane;
+    pre = a.pre + col * ng * W + lane;
+  }
+  __device__ __forceinline__ void give(const Map &m, const float *first) const {
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    if (wave || lane >= W) return;
+    if (rank + 1 < NC) publish(agg + (size_t)rank * W, word(m.A, m.H));
+    if (rank == 0) publish(pre, word(0.f, first ? first[lane] : 0.f));
+  }
+  // Every wave reads two words: the maps of the group's chunks before this one, and (word 15) the
+  // value carried into the group.
+  __device__ __forceinline__ void take(Words<W> &words) const {
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    if (lane >= W) return;
+#pragma unroll
+    for (int k = 2 * wave; k < 2 * wave + 2; ++k) {
+      if (k >= j && k < GROUP - 1) continue;
+      const unsigned long long *p = k == GROUP - 1 ? pre + (size_t)grp * W : agg + (size_t)(grp * GROUP + k) * W;
+      unsigned long long v;
+      // ends: the word is published by a chunk whose ticket was drawn earlier (or, word 15 of
+      // rank 0's group, by rank 0 itself before it comes here)
+      while ((v = peek(p)) == EMPTY) __builtin_amdgcn_s_sleep(1);
+      words[k][lane] = v;
+    }
+  }
+  // (A barrier later:) the value carried into this chunk; the last chunk of a group passes its
+  // result on.
+  __device__ __forceinline__ float carry(const Words<W> &words, const Map &m) const {
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    if (lane >= W) return 0.f;
+    float y = __uint_as_float((unsigned)words[GROUP - 1][lane]);
+    for (int i = 0; i < j; ++i) {
+      const unsigned long long v = words[i][lane];
+      y = apply(__uint_as_float((unsigned)(v >> 32)), __uint_as_float((unsigned)v), y);
+    }
+    if (wave == 0 && j == GROUP - 1 && rank + 1 < NC)
+      publish(pre + (size_t)(grp + 1) * W, word(0.f, apply(m.A, m.H, y)));
+    return y;
+  }
+};
 
 // ---- Forward -----------------------------------------------------------------
 // A thread keeps its steps' decays and inputs in fp32 for the replay (64 registers for bf16;
 // computing them again made that kernel bound by the vector unit).
 template <typename T, bool MIX, bool PACKED> __global__ __launch_bounds__(THR, 4) void scan_fwd(ScanArgs a) {
   constexpr int C = CPT<T>, W = TC<T>;
-  __shared__ __align__(16) Lds<W> s;
+  __shared__ __align__(16) Maps<W> s;
+  __shared__ Words<W> words;
   const Offsets offs(a);
   const Place p = place<T>(a);
   const int tid = threadIdx.x, grp = tid / LPR, cl = (tid % LPR) * C, ch = p.c0 + cl;
@@ -426,7 +442,20 @@ template <typename T, bool MIX, bool PACKED> __global__ __launch_bounds__(THR, 4
   store_f32<C>(&s.A[grp][cl], A);
   store_f32<C>(&s.H[grp][cl], H);
   const float *first = !PACKED && a.init && p.c0 + (tid & 63) < a.D ? a.init + (size_t)p.row * a.D + p.c0 : nullptr;
-  const float out = scan_chunk<W, false, true>(a, s, p.col, p.rank, first);
+  wave_map<W, false>(s);
+  // a lone chunk: every wave reads it before the barrier, as wave 0 may write its memory after
+  float y = a.NC == 1 && first && (tid & 63) < W ? first[tid & 63] : 0.f;
+  __syncthreads();
+  const Map m0 = chunk_map<W, false>(s);
+  if (a.NC > 1) {
+    const Chain<W> chain(a, p.col, p.rank);
+    chain.give(m0, first);
+    chain.take(words);
+    __syncthreads();
+    y = chain.carry(words, m0);
+  }
+  spread<W, false>(s, y);
+  const float out = apply(m0.A, m0.H, y);
   if (tid < W && p.c0 + tid < a.D) {
     if (a.states) a.states[((size_t)p.row * a.NC + p.rank) * a.D + p.c0 + tid] = out;
     if (!PACKED && a.final_state && p.rank == a.NC - 1) a.final_state[(size_t)p.row * a.D + p.c0 + tid] = out;
@@ -455,7 +484,8 @@ template <typename T, bool MIX, bool PACKED> __global__ __launch_bounds__(THR, 4
 // direction is chained (rank 0 is the last chunk).
 template <typename T, bool MIX, bool PACKED> __global__ __launch_bounds__(THR, 4) void scan_bwd(ScanArgs a) {
   constexpr int C = CPT<T>, W = TC<T>;
-  __shared__ __align__(16) Lds<W> s;
+  __shared__ __align__(16) union { Maps<W> s; Words<W> words; } f;   // forward maps; done with, the chain's words
+  __shared__ __align__(16) Maps<W> s;                                 // reverse maps
   const Offsets offs(a);
   const Place p = place<T>(a);
   const int chunk = a.NC - 1 - p.rank;
@@ -464,67 +494,21 @@ template <typename T, bool MIX, bool PACKED> __global__ __launch_bounds__(THR, 4
   const int end = PACKED ? min(offs.last(), a.T) : a.T;
   const Steps<T, SEG> st(a, p.row, chunk, grp, end, ch);
   u4 xr[SEG], gr[SEG], dr[SEG];
-  st.load(a.x, xr);
-  st.load(a.g, gr);
   st.load(a.dh, dr);
+  st.load(a.g, gr);
+  st.load(a.x, xr);
   Marks m{0, 0};
   if (PACKED) {
     m = marks_of<SEG>(offs, t0, end);
     if (ch >= a.D) m = Marks{0, 0};
     copy_empty<C>(a, a.d_final, a.d_init, p.rank, grp, GRPS, ch);
   }
-  st.mask(xr);
-  st.mask(gr);
   st.mask(dr);
+  st.mask(gr);
 
+  // The reverse map of these steps first, r_{t+1} of the last to r_t of the first: others wait
+  // for this chunk's, while the forward direction needs nobody.
   float A[C], H[C];
-#pragma unroll
-  for (int c = 0; c < C; ++c) { A[c] = 1.f; H[c] = 0.f; }
-#pragma unroll
-  for (int i = 0; i < SEG; ++i) {
-    if (PACKED && ((m.first >> i) & 1)) {
-      load_seq<C>(a, a.init, t0 + i, ch, H);
-#pragma unroll
-      for (int c = 0; c < C; ++c) A[c] = -0.f;
-    }
-    float lam[C], u[C];
-    step_of<MIX, C>(xr[i], gr[i], lam, u);
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      A[c] *= lam[c];
-      H[c] = fmaf(lam[c], H[c], u[c]);
-    }
-  }
-  store_f32<C>(&s.A[grp][cl], A);
-  store_f32<C>(&s.H[grp][cl], H);
-  const bool on = p.c0 + (tid & 63) < a.D;
-  const size_t c0 = (size_t)p.row * a.D + p.c0;
-  const float *first = nullptr;
-  if (on && chunk > 0) first = a.states + ((size_t)p.row * a.NC + chunk - 1) * a.D + p.c0;
-  else if (on && !PACKED && a.init) first = a.init + c0;
-  scan_chunk<W, false, false>(a, s, p.col, p.rank, first);
-  forget(xr);
-  forget(gr);
-  float h[C], e[SEG][C];                  // e: what dlam multiplies, h_{t-1} (mix: h_{t-1} - x_t)
-  load_f32<C>(&s.H[grp][cl], h);
-#pragma unroll
-  for (int i = 0; i < SEG; ++i) {
-    if (PACKED && ((m.first >> i) & 1)) load_seq<C>(a, a.init, t0 + i, ch, h);
-    float lam[C], u[C], xv[C];
-    step_of<MIX, C>(xr[i], gr[i], lam, u);
-    unpack16(xr[i], xv);
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      e[i][c] = MIX ? h[c] - xv[c] : h[c];
-      h[c] = fmaf(lam[c], h[c], u[c]);
-    }
-    // formed here and now: left to itself, the compiler keeps what e is made of instead
-#pragma unroll
-    for (int c = 0; c < C; ++c) asm volatile("" : "+v"(e[i][c]), "+v"(h[c]));
-  }
-  forget(gr);
-  forget(dr);
-  // the reverse map of these steps: r_{t+1} of the last to r_t of the first
 #pragma unroll
   for (int c = 0; c < C; ++c) { A[c] = 1.f; H[c] = 0.f; }
 #pragma unroll
@@ -544,14 +528,77 @@ template <typename T, bool MIX, bool PACKED> __global__ __launch_bounds__(THR, 4
       H[c] = lam * (dv[c] + H[c]);
     }
   }
-  __syncthreads();                        // every wave is done with the waves' forward maps
   store_f32<C>(&s.A[grp][cl], A);
   store_f32<C>(&s.H[grp][cl], H);
-  first = on && !PACKED && a.d_final ? a.d_final + c0 : nullptr;
-  const float out = scan_chunk<W, true, true>(a, s, p.col, p.rank, first);
-  if (tid < W && on && !PACKED && a.d_init && chunk == 0) a.d_init[c0 + tid] = out;
-  forget(dr);
+  wave_map<W, true>(s);
   forget(gr);
+  forget(dr);
+  st.mask(xr);
+#pragma unroll
+  for (int c = 0; c < C; ++c) { A[c] = 1.f; H[c] = 0.f; }
+#pragma unroll
+  for (int i = 0; i < SEG; ++i) {
+    if (PACKED && ((m.first >> i) & 1)) {
+      load_seq<C>(a, a.init, t0 + i, ch, H);
+#pragma unroll
+      for (int c = 0; c < C; ++c) A[c] = -0.f;
+    }
+    float lam[C], u[C];
+    step_of<MIX, C>(xr[i], gr[i], lam, u);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      A[c] *= lam[c];
+      H[c] = fmaf(lam[c], H[c], u[c]);
+    }
+  }
+  store_f32<C>(&f.s.A[grp][cl], A);
+  store_f32<C>(&f.s.H[grp][cl], H);
+  wave_map<W, false>(f.s);
+  const bool on = p.c0 + (tid & 63) < a.D;
+  const size_t c0 = (size_t)p.row * a.D + p.c0;
+  const float *last = on && !PACKED && a.d_final ? a.d_final + c0 : nullptr;
+  __syncthreads();
+  const Map mr = chunk_map<W, true>(s);
+  const Chain<W> chain(a, p.col, p.rank);
+  if (a.NC > 1) chain.give(mr, last);
+  float y = 0.f;
+  if (on && (tid & 63) < W) {
+    if (chunk > 0) y = a.states[((size_t)p.row * a.NC + chunk - 1) * a.D + p.c0 + (tid & 63)];
+    else if (!PACKED && a.init) y = a.init[c0 + (tid & 63)];
+  }
+  spread<W, false>(f.s, y);
+  forget(xr);
+  forget(gr);
+  float h[C], e[SEG][C];                  // e: what dlam multiplies, h_{t-1} (mix: h_{t-1} - x_t)
+  load_f32<C>(&f.s.H[grp][cl], h);
+#pragma unroll
+  for (int i = 0; i < SEG; ++i) {
+    if (PACKED && ((m.first >> i) & 1)) load_seq<C>(a, a.init, t0 + i, ch, h);
+    float lam[C], u[C], xv[C];
+    step_of<MIX, C>(xr[i], gr[i], lam, u);
+    unpack16(xr[i], xv);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      e[i][c] = MIX ? h[c] - xv[c] : h[c];
+      h[c] = fmaf(lam[c], h[c], u[c]);
+    }
+    // formed here and now: left to itself, the compiler keeps what e is made of instead
+#pragma unroll
+    for (int c = 0; c < C; ++c) asm volatile("" : "+v"(e[i][c]), "+v"(h[c]));
+  }
+  y = 0.f;
+  if (a.NC > 1) {
+    __syncthreads();                      // every wave is done with the forward maps, whose place the words take
+    chain.take(f.words);
+    __syncthreads();
+    y = chain.carry(f.words, mr);
+  } else if (last && (tid & 63) < W) {
+    y = last[tid & 63];
+  }
+  spread<W, true>(s, y);
+  if (tid < W && on && !PACKED && a.d_init && chunk == 0) a.d_init[c0 + tid] = apply(mr.A, mr.H, y);
+  forget(gr);
+  forget(dr);
   float r[C];
   load_f32<C>(&s.H[grp][cl], r);
 #pragma unroll
