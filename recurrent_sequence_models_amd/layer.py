@@ -142,15 +142,16 @@ def gated_scan(x, log_lambda, *, cu_seqlens=None, mix=False, init=None, final=Tr
     with _on(dev, stream):
         if out is None:
             out = torch.empty_like(x)
-        _check("h", out, x.dtype, x.shape, dev)
+        else:
+            _check("h", out, x.dtype, x.shape, dev)
         if final is True:
-            final = torch.empty(n, D, dtype=torch.float32, device=dev)
+            final = x.new_empty((n, D), dtype=torch.float32)
         elif final is False:
             final = None
         for name, t in (("init", init), ("final", final)):
             if t is not None:
                 _check(name, t, torch.float32, (n, D), dev)
-        states = torch.empty(_states_shape(x, cu_seqlens), dtype=torch.float32, device=dev) if chunk_states else None
+        states = x.new_empty(_states_shape(x, cu_seqlens), dtype=torch.float32) if chunk_states else None
         ws, nbytes = _workspace(need, workspace, dev)
         _done(lib().falcon_scan_fwd(shape, _p(cu_seqlens), _p(x), _p(log_lambda), _p(init), _p(final), _p(out),
                                     _p(states), _p(ws), nbytes, _current(dev)), "falcon_scan_fwd")
@@ -175,7 +176,7 @@ def gated_scan_bwd(x, log_lambda, dh, chunk_states, *, cu_seqlens=None, mix=Fals
         for name in ("dx", "dg"):
             _check(name, out[name], x.dtype, x.shape, dev)
         if d_init is True:
-            d_init = torch.empty(n, D, dtype=torch.float32, device=dev)
+            d_init = x.new_empty((n, D), dtype=torch.float32)
         elif d_init is False:
             d_init = None
         for name, t in (("init", init), ("d_final", d_final), ("d_init", d_init)):
@@ -202,7 +203,8 @@ def gated_scan_step(x, log_lambda, state, *, mix=False, out=None, stream=None):
     with _on(dev, stream):
         if out is None:
             out = torch.empty_like(x)
-        _check("h", out, x.dtype, (B, D), dev)
+        else:
+            _check("h", out, x.dtype, (B, D), dev)
         shape, _ = _scan_plan(dt, B, 1, D, bool(mix), False)
         _done(lib().falcon_scan_step(shape, _p(x), _p(log_lambda), _p(state), _p(out), _current(dev)),
               "falcon_scan_step")
@@ -370,8 +372,8 @@ def qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, *, q_weight=None
         else:
             dq, dk = out["dq"], out["dk"]
             oq, ok = _heads("dq", dq, q.dtype, dev, q.shape), _heads("dk", dk, q.dtype, dev, k.shape)
-        dwq = torch.empty(d, dtype=torch.float32, device=dev) if q_weight is not None else None
-        dwk = torch.empty(d, dtype=torch.float32, device=dev) if k_weight is not None else None
+        dwq = q.new_empty((d,), dtype=torch.float32) if q_weight is not None else None
+        dwk = q.new_empty((d,), dtype=torch.float32) if k_weight is not None else None
         ws, nbytes = _workspace(need if dwq is not None or dwk is not None else 0, workspace, dev)
         _done(lib().falcon_qk_norm_rope_bwd(shape, hq, hk, _p(q_weight), _p(k_weight), _p(positions), _p(inv_freq), gq,
                                             gk, oq, ok, _p(dwq), _p(dwk), _p(ws), nbytes, _current(dev)),
@@ -434,8 +436,9 @@ def attention_fwd(q, k, v, *, cu_seqlens=None, cu_seqlens_k=None, scale=None, ls
     with _on(dev, stream):
         if out is None:
             out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        _check("o", out, q.dtype, q.shape, dev)
-        rows = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev) if lse else None
+        else:
+            _check("o", out, q.dtype, q.shape, dev)
+        rows = q.new_empty(q.shape[:-1], dtype=torch.float32) if lse else None
         ws, nbytes = _workspace(fwd_bytes, workspace, dev)
         _done(lib().falcon_attn_fwd(shape, _p(cu_seqlens), _p(cuk), hq, hk, hv, _p(out), _p(rows),
                                 _p(ws), nbytes, _current(dev)), "falcon_attn_fwd")
