@@ -25,8 +25,8 @@
 //
 // Sequence starts.  The first step of a sequence does not see the carry: its map has
 // A = -0, and a map with the sign bit set is applied as y -> H, not as 0 y + H, so an
-// infinite or NaN state of one sequence does not reach the next.  Products of decays
-// keep the sign: -0 times a decay >= 0 is -0.
+// infinite or NaN state of one sequence does not reach the next.  Products with decays
+// (>= 0) keep the sign, and joining maps sets it where either map's is.
 //
 // Bound: HBM.  Algorithmic bytes: forward 3, backward 5 elements of the input type per
 // step and channel.
@@ -95,6 +95,10 @@ __device__ __forceinline__ float one_minus_decay(float g, float lam) {
   return fabsf(g) <= 0.125f ? -g * p : 1.f - lam;
 }
 
+// The product of two maps' factors; the sign is set where either's is (-0 times -0 would clear it).
+__device__ __forceinline__ float join(float A, float B) {
+  return __uint_as_float(__float_as_uint(A * B) | ((__float_as_uint(A) | __float_as_uint(B)) & 0x80000000u));
+}
 // y after the map (A, H); a set sign of A cuts the carry off.
 __device__ __forceinline__ float apply(float A, float H, float y) {
   return (__float_as_uint(A) >> 31) ? H : fmaf(A, y, H);
@@ -305,7 +309,7 @@ template <int W, bool REV> __device__ __forceinline__ void wave_map(Maps<W> &s) 
   for (int i = 0; i < GPW; ++i) {
     const int q = wave * GPW + (REV ? GPW - 1 - i : i);
     H = apply(s.A[q][lane], s.H[q][lane], H);
-    A *= s.A[q][lane];
+    A = join(A, s.A[q][lane]);
   }
   s.wA[wave][lane] = A;
   s.wH[wave][lane] = H;
@@ -319,7 +323,7 @@ template <int W, bool REV> __device__ __forceinline__ Map chunk_map(const Maps<W
     for (int i = 0; i < WAVES; ++i) {
       const int w = REV ? WAVES - 1 - i : i;
       m.H = apply(s.wA[w][lane], s.wH[w][lane], m.H);
-      m.A *= s.wA[w][lane];
+      m.A = join(m.A, s.wA[w][lane]);
     }
   return m;
 }

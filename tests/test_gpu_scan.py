@@ -157,6 +157,33 @@ def test_one_sequence_does_not_reach_the_next():
     assert not torch.isfinite(b["dx"][300:321]).any()
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("lens", [[40, 8, 252, 4, 4, 192, 300], [20, 12, 12, 12, 12, 700, 12, 12, 300, 9, 9],
+                                  [300] + [5] * 130 + [600]], ids=["few", "waves", "many"])
+def test_several_starts_behind_a_nonfinite_sequence(dtype, lens):
+    """However many sequences begin in a stretch of steps, none of them sees what is before the
+    stretch (forward) or behind it (backward)."""
+    import torch
+    from recurrent_sequence_models_amd import gated_scan, gated_scan_bwd
+    T, D, cu = sum(lens), 64, offsets(lens)
+    first, last = lens[0], T - lens[-1]
+    x, dh = rand(41, T, D, dtype=dtype), rand(42, T, D, dtype=dtype)
+    g = gates(43, T, D, dtype=dtype)
+    bad, dbad = x.clone(), dh.clone()
+    bad[:first, ::2], bad[:first, 1::2] = float("nan"), float("inf")
+    dbad[last:, ::2], dbad[last:, 1::2] = float("nan"), float("inf")
+    h0, fin0, states0 = gated_scan(x, g, cu_seqlens=cu, chunk_states=True)
+    h1, fin1, _ = gated_scan(bad, g, cu_seqlens=cu)
+    assert torch.equal(h0[first:], h1[first:]) and torch.equal(fin0[1:], fin1[1:])
+    assert not h1[:first].isfinite().any() and not fin1[0].isfinite().any()
+    r0 = gated_scan_bwd(x, g, dh, states0, cu_seqlens=cu)
+    r1 = gated_scan_bwd(x, g, dbad, states0, cu_seqlens=cu)
+    for k in ("dx", "dg"):
+        assert torch.equal(r0[k][:last], r1[k][:last]), k
+    assert torch.equal(r0["d_init"][:-1], r1["d_init"][:-1])
+    assert not r1["dx"][last:].isfinite().any()
+
+
 @pytest.mark.parametrize("packed", [False, True])
 def test_in_place_state_and_continuation(packed):
     """final may be init; two halves in a row equal the whole."""
