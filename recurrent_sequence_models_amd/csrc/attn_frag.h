@@ -65,8 +65,6 @@ __device__ __forceinline__ Frag<__bf16> global_frag(const __bf16 *row, int b, in
 __device__ __forceinline__ Frag<float> global_frag(const float *row, int b, int h) {
   return {*reinterpret_cast<const f4 *>(row + 16 * b + 8 * h), *reinterpret_cast<const f4 *>(row + 16 * b + 8 * h + 4)};
 }
-__device__ __forceinline__ Frag<__bf16> zero_frag(__bf16) { return {__builtin_bit_cast(bf8, uint4{0, 0, 0, 0})}; }
-__device__ __forceinline__ Frag<float> zero_frag(float) { return {zero4(), zero4()}; }
 
 // A tile of ROWS rows of D entries in LDS, in 16-byte chunks.  Chunk c of a row stands at
 // place c ^ swizzle(row): reads of one chunk of 16 neighbouring rows, and column reads of

@@ -166,7 +166,7 @@ template <typename T, int D> __global__ __launch_bounds__(THR, sizeof(T) * D > 2
   }
   const Seq q = seq_of(a, n);
   const int rows = q.Lq * a.group, tiles = (rows + TM - 1) / TM;
-  if (tile >= tiles) return;
+  if ((unsigned)tile >= (unsigned)tiles) return;
   tile = tiles - 1 - tile;                      // the tiles with the most keys start first
 
   const int off = q.Lk - q.Lq, r0 = tile * TM + wave * 32;
@@ -299,7 +299,7 @@ template <typename T, int D> __global__ __launch_bounds__(64, sizeof(T) * D > 25
   }
   const Seq q = seq_of(a, n);
   const int rows = q.Lq * a.group;
-  if (tile >= (rows + FEW - 1) / FEW) return;
+  if ((unsigned)tile >= (unsigned)((rows + FEW - 1) / FEW)) return;
   const int off = q.Lk - q.Lq, r0 = tile * FEW, r = min(r0 + c, rows - 1);
   const int tok = r / (unsigned)a.group, hq = head * a.group + (r - tok * a.group);
   const int lim = tok + off;
@@ -434,9 +434,8 @@ int splits_of(const AttnArgs &a) {
 }
 
 template <typename T, int D> hipError_t run(AttnArgs &a, hipStream_t s) {
-  const int64_t blocks = (int64_t)a.slots * a.hk * a.splits;
+  const int64_t blocks = slots_of(a) * a.hk * a.splits;
   const size_t nrow = (size_t)query_tokens(a) * a.hq;
-  if (blocks > 0x7fffffff || (a.splits > 1 && nrow > 0x7fffffff)) return hipErrorInvalidValue;
   if (few_rows(a)) hipLaunchKernelGGL((attn_few<T, D>), dim3((unsigned)blocks), dim3(64), 0, s, a);
   else hipLaunchKernelGGL((attn_fwd<T, D>), dim3((unsigned)blocks), dim3(THR), 0, s, a);
   const hipError_t e = hipGetLastError();
@@ -447,14 +446,16 @@ template <typename T, int D> hipError_t run(AttnArgs &a, hipStream_t s) {
 
 }  // namespace
 
-size_t attn_fwd_workspace(bool bf16, int d, const AttnArgs &a) {
-  (void)bf16;
+bool attn_fwd_fits(const AttnArgs &a) {   // the join too: splits only come with few rows
+  return grid_fits(slots_of(a) * a.hk * splits_of(a), few_rows(a) ? 64 : THR);
+}
+
+size_t attn_fwd_workspace(int d, const AttnArgs &a) {
   const int s = splits_of(a);
   return s == 1 ? 0 : (size_t)s * query_tokens(a) * a.hq * (d + 2) * sizeof(float);
 }
 
 hipError_t launch_attn_fwd(bool bf16, int d, AttnArgs a, void *ws, hipStream_t s) {
-  a.slots = (int)slots_of(a);
   a.splits = splits_of(a);
   a.part = static_cast<float *>(ws);
 #define FALCON_ATTN(D_) \

@@ -82,7 +82,7 @@ __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_kv(
     n = slot % (unsigned)a.n; tile = slot / (unsigned)a.n;
   }
   const Seq q = seq_of(a, n);
-  if (tile >= (q.Lk + TR - 1) / TR) return;               // tile 0, which most rows see, starts first
+  if ((unsigned)tile >= (unsigned)((q.Lk + TR - 1) / TR)) return;   // tile 0, which most rows see, starts first
   const int key0 = tile * TR, wkey = key0 + wave * 32, key = wkey + c;
   const bool on = key < q.Lk;
   const int rows = q.Lq * a.group, off = q.Lk - q.Lq;
@@ -264,7 +264,7 @@ __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_q(A
   }
   const Seq q = seq_of(a, n);
   const int rows = q.Lq * a.group, tiles = (rows + TR - 1) / TR;
-  if (tile >= tiles) return;
+  if ((unsigned)tile >= (unsigned)tiles) return;
   tile = tiles - 1 - tile;
   const int off = q.Lk - q.Lq, r0 = tile * TR + wave * 32, r = min(r0 + c, rows - 1);
   const bool on = r0 + c < rows;
@@ -347,6 +347,12 @@ __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_q(A
 int64_t key_slots(const AttnArgs &a) {
   return a.cuk ? (int64_t)a.Tk / TR + a.n : ((int64_t)a.Tk + TR - 1) / TR * a.n;
 }
+int64_t row_slots(const AttnArgs &a) {
+  return a.cuq ? (int64_t)a.Tq * a.group / TR + a.n : ((int64_t)a.Tq * a.group + TR - 1) / TR * a.n;
+}
+// Workgroups of the two kernels over all rows or keys.
+int64_t delta_blocks(const AttnArgs &a, int L) { return (query_tokens(a) * a.hq * L + THR - 1) / THR; }
+int64_t sum_blocks(const AttnArgs &a, int d) { return (key_tokens(a) * a.hk * (d / 4) + THR - 1) / THR; }
 
 // Splits of the rows between workgroups of one key tile.  Tile 0 meets every row and the last
 // tile 128 of them, so at two workgroups a compute unit one round of workgroups would take
@@ -363,22 +369,18 @@ int bwd_splits(const AttnArgs &a) {
 
 template <typename T, int D> hipError_t run(AttnArgs &a, hipStream_t s) {
   const size_t nrow = (size_t)query_tokens(a) * a.hq, nkey = (size_t)key_tokens(a) * a.hk;
-  constexpr int L = D * (int)sizeof(T) / 16;
-  const int64_t kblocks = key_slots(a) * a.hk * a.splits;
-  const int64_t qslots = a.cuq ? (int64_t)a.Tq * a.group / TR + a.n : ((int64_t)a.Tq * a.group + TR - 1) / TR * a.n;
-  const size_t nb = (nrow * L + THR - 1) / THR, ns = (nkey * (D / 4) + THR - 1) / THR;
-  if (nb > 0x7fffffff || ns > 0x7fffffff || kblocks > 0x7fffffff || qslots * a.hk > 0x7fffffff)
-    return hipErrorInvalidValue;
-  hipLaunchKernelGGL((attn_delta<T, D>), dim3((unsigned)nb), dim3(THR), 0, s, a, nrow);
+  const unsigned nd = (unsigned)delta_blocks(a, D * (int)sizeof(T) / 16), ns = (unsigned)sum_blocks(a, D);
+  const unsigned nk = (unsigned)(key_slots(a) * a.hk * a.splits), nq = (unsigned)(row_slots(a) * a.hk);
+  hipLaunchKernelGGL((attn_delta<T, D>), dim3(nd), dim3(THR), 0, s, a, nrow);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attn_bwd_kv<T, D>), dim3((unsigned)kblocks), dim3(THR), 0, s, a);
+  hipLaunchKernelGGL((attn_bwd_kv<T, D>), dim3(nk), dim3(THR), 0, s, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   if (a.splits > 1) {
-    hipLaunchKernelGGL((attn_bwd_sum<T, D>), dim3((unsigned)ns), dim3(THR), 0, s, a, nkey);
+    hipLaunchKernelGGL((attn_bwd_sum<T, D>), dim3(ns), dim3(THR), 0, s, a, nkey);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((attn_bwd_q<T, D>), dim3((unsigned)(qslots * a.hk)), dim3(THR), 0, s, a);
+  hipLaunchKernelGGL((attn_bwd_q<T, D>), dim3(nq), dim3(THR), 0, s, a);
   return hipGetLastError();
 }
 
@@ -386,6 +388,12 @@ template <typename T, int D> hipError_t run(AttnArgs &a, hipStream_t s) {
 size_t row_bytes(const AttnArgs &a) { return ((size_t)query_tokens(a) * a.hq * sizeof(float) + 15) & ~(size_t)15; }
 
 }  // namespace
+
+bool attn_bwd_fits(bool bf16, int d, const AttnArgs &a) {
+  const int splits = bwd_splits(a);
+  return grid_fits(delta_blocks(a, d * (bf16 ? 2 : 4) / 16), THR) && grid_fits(key_slots(a) * a.hk * splits, THR) &&
+         (splits == 1 || grid_fits(sum_blocks(a, d), THR)) && grid_fits(row_slots(a) * a.hk, THR);
+}
 
 size_t attn_bwd_workspace(int d, const AttnArgs &a) {
   const int s = bwd_splits(a);

@@ -46,12 +46,9 @@ int check_scan(const falcon_scan_shape_t *s, bool packed, bool step) {
   if (s->batch < 1 || s->width < 1 || (!step && s->seqlen < 1)) return FALCON_ERR_INVALID_ARG;
   if (s->width % 8 != 0 || s->width > (1 << 20)) return FALCON_ERR_UNSUPPORTED;
   if (step) return FALCON_OK;
-  // step numbers are ints, chunk rounding included; so are workgroup numbers
-  if (s->seqlen > INT32_MAX - FALCON_SCAN_CHUNK) return FALCON_ERR_UNSUPPORTED;
-  const int64_t tc = 128 / esize(s->dtype);
-  const int64_t cols = (packed ? 1 : (int64_t)s->batch) * ((s->width + tc - 1) / tc);
-  const int64_t chunks = ((int64_t)s->seqlen + FALCON_SCAN_CHUNK - 1) / FALCON_SCAN_CHUNK;
-  if (cols > INT32_MAX / chunks) return FALCON_ERR_UNSUPPORTED;
+  // step and sequence numbers are ints, with a chunk or a stride over the sequences added
+  if (s->seqlen > INT32_MAX - FALCON_SCAN_CHUNK || s->batch > (1 << 30)) return FALCON_ERR_UNSUPPORTED;
+  if (!falcon::scan_fits(s->dtype == FALCON_BF16, packed ? 1 : s->batch, s->seqlen, s->width)) return FALCON_ERR_UNSUPPORTED;
   return FALCON_OK;
 }
 
@@ -260,23 +257,6 @@ int64_t attn_tokens_k(const falcon_attn_shape_t *s, bool packed) {
   return packed ? s->seqlen_k : (int64_t)s->batch * s->seqlen_k;
 }
 
-int check_attn(const falcon_attn_shape_t *s, bool packed) {
-  if (!s || !dtype_ok(s->dtype)) return FALCON_ERR_INVALID_ARG;
-  if (s->batch < 1 || s->seqlen_q < 1 || s->seqlen_k < 1 || s->heads_q < 1 || s->heads_k < 1 || s->d < 1)
-    return FALCON_ERR_INVALID_ARG;
-  if (s->heads_q % s->heads_k != 0) return FALCON_ERR_INVALID_ARG;
-  if (!std::isfinite(s->scale) || !(s->scale > 0.f)) return FALCON_ERR_INVALID_ARG;
-  FALCON_TRY(check_d(s->d));
-  // token, row and workgroup numbers are ints (128 rows or keys a workgroup; the split of the
-  // keys only happens where there are few of them)
-  const int64_t tq = attn_tokens_q(s, packed), tk = attn_tokens_k(s, packed);
-  if (tq > INT32_MAX - 4096 || tk > INT32_MAX - 4096 || s->heads_q > (1 << 20)) return FALCON_ERR_UNSUPPORTED;
-  if (tq * (s->heads_q / s->heads_k) > INT32_MAX - 4096) return FALCON_ERR_UNSUPPORTED;
-  if ((tq * s->heads_q / 128 + (int64_t)(s->batch + 1) * s->heads_k) > INT32_MAX / 2) return FALCON_ERR_UNSUPPORTED;
-  if ((tk / 128 + s->batch + 1) * s->heads_k > INT32_MAX / 2) return FALCON_ERR_UNSUPPORTED;
-  return FALCON_OK;
-}
-
 falcon::AttnArgs attn_args(const falcon_attn_shape_t *s, const int32_t *cu_q, const int32_t *cu_k) {
   falcon::AttnArgs a{};
   a.cuq = cu_q;
@@ -291,6 +271,38 @@ falcon::AttnArgs attn_args(const falcon_attn_shape_t *s, const int32_t *cu_q, co
   return a;
 }
 
+// The fields that sizes depend on, for the workspace queries (any non-null offsets mark a packed call).
+falcon::AttnArgs size_args(const falcon_attn_shape_t *s, bool packed) {
+  static const int32_t mark = 0;
+  return attn_args(s, packed ? &mark : nullptr, packed ? &mark : nullptr);
+}
+
+int check_attn(const falcon_attn_shape_t *s, bool packed) {
+  if (!s || !dtype_ok(s->dtype)) return FALCON_ERR_INVALID_ARG;
+  if (s->batch < 1 || s->seqlen_q < 1 || s->seqlen_k < 1 || s->heads_q < 1 || s->heads_k < 1 || s->d < 1)
+    return FALCON_ERR_INVALID_ARG;
+  if (s->heads_q % s->heads_k != 0) return FALCON_ERR_INVALID_ARG;
+  if (!std::isfinite(s->scale) || !(s->scale > 0.f)) return FALCON_ERR_INVALID_ARG;
+  FALCON_TRY(check_d(s->d));
+  // token, row and sequence numbers are ints, with a tile added
+  const int64_t tq = attn_tokens_q(s, packed), tk = attn_tokens_k(s, packed);
+  if (tq > INT32_MAX - 4096 || tk > INT32_MAX - 4096 || s->heads_q > (1 << 20)) return FALCON_ERR_UNSUPPORTED;
+  if (tq * (s->heads_q / s->heads_k) > INT32_MAX - 4096 || s->batch > (1 << 30)) return FALCON_ERR_UNSUPPORTED;
+  return FALCON_OK;
+}
+
+// Of one direction: its launches too.
+int check_attn_fwd(const falcon_attn_shape_t *s, bool packed) {
+  FALCON_TRY(check_attn(s, packed));
+  return falcon::attn_fwd_fits(size_args(s, packed)) ? FALCON_OK : FALCON_ERR_UNSUPPORTED;
+}
+int check_attn_bwd(const falcon_attn_shape_t *s, bool packed) {
+  FALCON_TRY(check_attn(s, packed));
+  return falcon::attn_bwd_fits(s->dtype == FALCON_BF16, s->d, size_args(s, packed)) ? FALCON_OK : FALCON_ERR_UNSUPPORTED;
+}
+
+constexpr int64_t MOST_STEP = 1 << 25;   // bytes between two tokens
+
 int check_attn_in(const falcon_attn_shape_t *s, const int32_t *cu_q, const int32_t *cu_k, falcon_heads_t q,
                   falcon_heads_t k, falcon_heads_t v, const void *o) {
   if ((cu_q == nullptr) != (cu_k == nullptr)) return FALCON_ERR_INVALID_ARG;
@@ -302,16 +314,10 @@ int check_attn_in(const falcon_attn_shape_t *s, const int32_t *cu_q, const int32
   FALCON_TRY(check_heads(q.data, q.token_stride, attn_tokens_q(s, packed), s->heads_q, s->d, e));
   FALCON_TRY(check_heads(k.data, k.token_stride, attn_tokens_k(s, packed), s->heads_k, s->d, e));
   FALCON_TRY(check_heads(v.data, v.token_stride, attn_tokens_k(s, packed), s->heads_k, s->d, e));
-  // a tile's rows are 32 bits of bytes apart
-  if (q.token_stride > (1 << 24) || k.token_stride > (1 << 24) || v.token_stride > (1 << 24))
-    return FALCON_ERR_UNSUPPORTED;
+  // the rows of a tile, at most 128, are 32 bits of bytes apart
+  for (const int64_t stride : {q.token_stride, k.token_stride, v.token_stride})
+    if (stride > MOST_STEP / e) return FALCON_ERR_UNSUPPORTED;
   return need(o, 16);
-}
-
-// The fields that sizes depend on, for the workspace queries (any non-null offsets mark a packed call).
-falcon::AttnArgs size_args(const falcon_attn_shape_t *s, bool packed) {
-  static const int32_t mark = 0;
-  return attn_args(s, packed ? &mark : nullptr, packed ? &mark : nullptr);
 }
 
 }  // namespace
@@ -319,13 +325,14 @@ falcon::AttnArgs size_args(const falcon_attn_shape_t *s, bool packed) {
 extern "C" {
 
 size_t falcon_attn_fwd_workspace(const falcon_attn_shape_t *s, int packed) {
-  if (check_attn(s, packed != 0) != FALCON_OK) return 0;
-  return falcon::attn_fwd_workspace(s->dtype == FALCON_BF16, s->d, size_args(s, packed != 0));
+  if (check_attn_fwd(s, packed != 0) != FALCON_OK) return 0;
+  return falcon::attn_fwd_workspace(s->d, size_args(s, packed != 0));
 }
 
 int falcon_attn_fwd(const falcon_attn_shape_t *s, const int32_t *cu_q, const int32_t *cu_k, falcon_heads_t q,
                     falcon_heads_t k, falcon_heads_t v, void *o, float *lse, void *ws, size_t ws_bytes, void *stream) {
   FALCON_TRY(check_attn_in(s, cu_q, cu_k, q, k, v, o));
+  FALCON_TRY(check_attn_fwd(s, cu_q != nullptr));
   FALCON_TRY(maybe(lse, 4));
   FALCON_TRY(check_workspace(ws, ws_bytes, falcon_attn_fwd_workspace(s, cu_q != nullptr)));
   falcon::AttnArgs a = attn_args(s, cu_q, cu_k);
@@ -337,7 +344,7 @@ int falcon_attn_fwd(const falcon_attn_shape_t *s, const int32_t *cu_q, const int
 }
 
 size_t falcon_attn_bwd_workspace(const falcon_attn_shape_t *s, int packed) {
-  if (check_attn(s, packed != 0) != FALCON_OK) return 0;
+  if (check_attn_bwd(s, packed != 0) != FALCON_OK) return 0;
   return falcon::attn_bwd_workspace(s->d, size_args(s, packed != 0));
 }
 
@@ -346,12 +353,13 @@ int falcon_attn_bwd(const falcon_attn_shape_t *s, const int32_t *cu_q, const int
                     falcon_heads_out_t dq, falcon_heads_out_t dk, falcon_heads_out_t dv, void *ws, size_t ws_bytes,
                     void *stream) {
   FALCON_TRY(check_attn_in(s, cu_q, cu_k, q, k, v, o));
-  FALCON_TRY(need(lse, 4));
   const bool packed = cu_q != nullptr;
+  FALCON_TRY(check_attn_bwd(s, packed));
+  FALCON_TRY(need(lse, 4));
   const int64_t tq = attn_tokens_q(s, packed), tk = attn_tokens_k(s, packed);
   const int e = esize(s->dtype);
   FALCON_TRY(check_heads(d_o.data, d_o.token_stride, tq, s->heads_q, s->d, e));
-  if (d_o.token_stride > (1 << 24)) return FALCON_ERR_UNSUPPORTED;
+  if (d_o.token_stride > MOST_STEP / e) return FALCON_ERR_UNSUPPORTED;
   FALCON_TRY(check_heads(dq.data, dq.token_stride, tq, s->heads_q, s->d, e));
   FALCON_TRY(check_heads(dk.data, dk.token_stride, tk, s->heads_k, s->d, e));
   FALCON_TRY(check_heads(dv.data, dv.token_stride, tk, s->heads_k, s->d, e));

@@ -22,7 +22,8 @@ namespace falcon {
 namespace {
 
 constexpr int THR = 256;
-constexpr int BWD_BLOCKS = 1024;   // workgroups of the backward pass: four a compute unit
+constexpr int FWD_BLOCKS = 1 << 18;   // workgroups of the forward pass, at most: a launch holds less than 2^32 threads
+constexpr int BWD_BLOCKS = 1024;      // of the backward pass: four a compute unit, each with its sum for the weights
 
 template <typename T> constexpr int EPL = 16 / (int)sizeof(T);   // entries per lane
 
@@ -120,34 +121,36 @@ template <int E> __device__ __forceinline__ void load_weight(const float *w, int
 template <typename T, int D> __global__ __launch_bounds__(THR) void qk_fwd(QkArgs a) {
   constexpr int E = EPL<T>, L = D / E, ROWS = THR / L;
   extern __shared__ __align__(16) float2 tab[];
-  const int t0 = blockIdx.x * a.tok, nt = min(a.tok, a.tokens - t0), H = a.hq + a.hk;
-  const int e0 = (threadIdx.x % L) * E;
+  const int H = a.hq + a.hk, e0 = (threadIdx.x % L) * E;
   const Turn turn = turn_of<T, D>(a);
   float w[2][E];
   load_weight<E>(a.w[0], e0, w[0]);
   load_weight<E>(a.w[1], e0, w[1]);
-  fill_table(a, t0, nt, tab);
-  __syncthreads();
-  const int rows = nt * H;
-  for (int base = 0; base < rows; base += ROWS) {   // the same count for every wave: rotate() needs whole waves
-    const int row = base + threadIdx.x / L;
-    const bool on = row < rows;
-    const int t = on ? row / H : 0, hh = on ? row - t * H : 0;
-    const bool isk = hh >= a.hq;
-    const int64_t head = (int64_t)(isk ? hh - a.hq : hh) * D + e0;
-    const QkTensor &xs = a.x[isk], &ys = a.y[isk];
-    float z[E];
-    load_row(static_cast<const T *>(xs.p) + (t0 + t) * xs.ld + head, z);
-    if (a.norm) {
-      float ss = 0.f;
+  for (int t0 = blockIdx.x * a.tok; t0 < a.tokens; t0 += gridDim.x * a.tok) {
+    const int nt = min(a.tok, a.tokens - t0), rows = nt * H;
+    if (t0 >= (int)gridDim.x * a.tok) __syncthreads();   // the table of the tokens before is read no more
+    fill_table(a, t0, nt, tab);
+    __syncthreads();
+    for (int base = 0; base < rows; base += ROWS) {   // the same count for every wave: rotate() needs whole waves
+      const int row = base + threadIdx.x / L;
+      const bool on = row < rows;
+      const int t = on ? row / H : 0, hh = on ? row - t * H : 0;
+      const bool isk = hh >= a.hq;
+      const int64_t head = (int64_t)(isk ? hh - a.hq : hh) * D + e0;
+      const QkTensor &xs = a.x[isk], &ys = a.y[isk];
+      float z[E];
+      load_row(static_cast<const T *>(xs.p) + (t0 + t) * xs.ld + head, z);
+      if (a.norm) {
+        float ss = 0.f;
 #pragma unroll
-      for (int j = 0; j < E; ++j) ss = fmaf(z[j], z[j], ss);
-      const float r = rsqrtf(row_sum<L>(ss) * (1.f / D) + a.eps);
+        for (int j = 0; j < E; ++j) ss = fmaf(z[j], z[j], ss);
+        const float r = rsqrtf(row_sum<L>(ss) * (1.f / D) + a.eps);
 #pragma unroll
-      for (int j = 0; j < E; ++j) z[j] *= r * (isk ? w[1][j] : w[0][j]);
+        for (int j = 0; j < E; ++j) z[j] *= r * (isk ? w[1][j] : w[0][j]);
+      }
+      rotate<false, E>(z, turn, tab + t * (a.rot / 2), a.interleaved);
+      if (on) store_row(static_cast<T *>(const_cast<void *>(ys.p)) + (t0 + t) * ys.ld + head, z);
     }
-    rotate<false, E>(z, turn, tab + t * (a.rot / 2), a.interleaved);
-    if (on) store_row(static_cast<T *>(const_cast<void *>(ys.p)) + (t0 + t) * ys.ld + head, z);
   }
 }
 
@@ -234,24 +237,28 @@ __global__ __launch_bounds__(1024) void qk_weight_sum(QkArgs a, int d, int block
   }
 }
 
-int bwd_blocks(int tokens, int tok) {
+int blocks_of(int tokens, int tok, int most) {
   const int n = (tokens + tok - 1) / tok;
-  return n < BWD_BLOCKS ? n : BWD_BLOCKS;
+  return n < most ? n : most;
 }
 
-// Tokens of a workgroup: enough rows to keep its lanes busy a few times over (the table
-// and the barrier are shared by them), one token where there are few tokens.
-int tokens_per_block(int tokens) { return tokens >= 4096 ? 4 : 1; }
+// Tokens of a workgroup: they share the table's work and the barrier, and fewer tokens leave
+// more workgroups.  1 / 2 / 4 tokens a workgroup took, forward, 12 + 12 heads of 64, bf16:
+//   512 and fewer do not fill the chip: 64 tokens 2.8 / 3.4 / 4.1 us
+//   1024 tokens 3.9 / 4.1 / 4.6 us (16 + 4 heads of 128: 6.1 / 5.4 / 6.4; backward 12.2 / 10.2 / 11.1)
+//   2048 tokens 5.6 / 5.7 / 5.7 us (16 + 4 heads of 128: 9.9 / 8.7 / 8.5; fp32, 12 + 12 of 64: 7.2 / 6.9 / 8.2)
+//   4096 tokens 9.3 / 8.7 / 7.8 us (16 + 4 heads of 128: 15.2 / 13.2 / 11.8), 32768 tokens 60 / 48 / 39 us
+int tokens_per_block(int tokens) { return tokens >= 4096 ? 4 : tokens >= 1024 ? 2 : 1; }
 
 }  // namespace
 
 size_t qk_bwd_workspace(int tokens, int d) {
-  return (size_t)bwd_blocks(tokens, tokens_per_block(tokens)) * 2 * d * sizeof(float);
+  return (size_t)blocks_of(tokens, tokens_per_block(tokens), BWD_BLOCKS) * 2 * d * sizeof(float);
 }
 
 hipError_t launch_qk_fwd(bool bf16, int d, QkArgs a, hipStream_t s) {
   a.tok = tokens_per_block(a.tokens);
-  const unsigned grid = (a.tokens + a.tok - 1) / a.tok;
+  const int grid = blocks_of(a.tokens, a.tok, FWD_BLOCKS);
   const unsigned lds = a.tok * (a.rot / 2) * sizeof(float2);
 #define FALCON_QK(D_)                                                                                        \
   if (d == D_) {                                                                                             \
@@ -270,7 +277,7 @@ hipError_t launch_qk_bwd(bool bf16, bool dy_f32, int d, QkArgs a, void *ws, hipS
   a.tok = tokens_per_block(a.tokens);
   const bool weights = a.norm && (a.dw[0] || a.dw[1]);
   a.part = weights ? static_cast<float *>(ws) : nullptr;
-  const int blocks = bwd_blocks(a.tokens, a.tok);
+  const int blocks = blocks_of(a.tokens, a.tok, BWD_BLOCKS);
   const unsigned lds = a.tok * (a.rot / 2) * sizeof(float2);
 #define FALCON_QK(D_)                                                                                            \
   if (d == D_) {                                                                                                 \

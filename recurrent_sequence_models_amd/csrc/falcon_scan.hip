@@ -661,13 +661,15 @@ Layout layout(bool bf16, int rows, int T, int D) {
   return Layout{up16(cols * 4), cols * nc * tc * 8, cols * ((nc + GROUP - 1) / GROUP) * tc * 8};
 }
 
-// Lays the workspace out, fills it, and gives the grid size (0: more workgroups than a grid holds).
-hipError_t prepare(bool bf16, ScanArgs &a, void *ws, unsigned &grid, hipStream_t s) {
+int64_t blocks_of(bool bf16, int rows, int T, int D) {
   const int tc = bf16 ? TC<__bf16> : TC<float>;
+  return (int64_t)rows * ((D + tc - 1) / tc) * (((int64_t)T + CHUNK - 1) / CHUNK);
+}
+
+// Lays the workspace out, fills it, and gives the grid size.
+hipError_t prepare(bool bf16, ScanArgs &a, void *ws, unsigned &grid, hipStream_t s) {
   a.NC = (a.T + CHUNK - 1) / CHUNK;
-  const size_t blocks = (size_t)a.rows * ((a.D + tc - 1) / tc) * a.NC;
-  if (blocks > 0x7fffffffu) return hipErrorInvalidValue;
-  grid = (unsigned)blocks;
+  grid = (unsigned)blocks_of(bf16, a.rows, a.T, a.D);
   if (a.NC == 1) return hipSuccess;
   const Layout l = layout(bf16, a.rows, a.T, a.D);
   unsigned char *p = static_cast<unsigned char *>(ws);
@@ -682,6 +684,8 @@ hipError_t prepare(bool bf16, ScanArgs &a, void *ws, unsigned &grid, hipStream_t
 
 }  // namespace
 
+bool scan_fits(bool bf16, int rows, int T, int D) { return grid_fits(blocks_of(bf16, rows, T, D), THR); }
+
 size_t scan_workspace(bool bf16, int rows, int T, int D) {
   const Layout l = layout(bf16, rows, T, D);
   return l.ticket + l.agg + l.pre;
@@ -692,14 +696,14 @@ size_t scan_workspace(bool bf16, int rows, int T, int D) {
   const hipError_t e = prepare(bf16, a, ws, grid, s);                                                           \
   if (e != hipSuccess) return e;                                                                                \
   switch ((bf16 ? 4 : 0) + (mix ? 2 : 0) + (a.cu ? 1 : 0)) {                                                    \
-    case 0: hipLaunchKernelGGL((KERNEL<float, false, false>), dim3(grid), dim3(THR)    , 0, s, a); break;       \
-    case 1: hipLaunchKernelGGL((KERNEL<float, false, true>), dim3(grid), dim3(THR)    , 0, s, a); break;        \
-    case 2: hipLaunchKernelGGL((KERNEL<float, true, false>), dim3(grid), dim3(THR)    , 0, s, a); break;        \
-    case 3: hipLaunchKernelGGL((KERNEL<float, true, true>), dim3(grid), dim3(THR)    , 0, s, a); break;         \
-    case 4: hipLaunchKernelGGL((KERNEL<__bf16, false, false>), dim3(grid), dim3(THR)    , 0, s, a); break;      \
-    case 5: hipLaunchKernelGGL((KERNEL<__bf16, false, true>), dim3(grid), dim3(THR)    , 0, s, a); break;       \
-    case 6: hipLaunchKernelGGL((KERNEL<__bf16, true, false>), dim3(grid), dim3(THR)    , 0, s, a); break;       \
-    default: hipLaunchKernelGGL((KERNEL<__bf16, true, true>), dim3(grid), dim3(THR)    , 0, s, a);              \
+    case 0: hipLaunchKernelGGL((KERNEL<float, false, false>), dim3(grid), dim3(THR), 0, s, a); break;           \
+    case 1: hipLaunchKernelGGL((KERNEL<float, false, true>), dim3(grid), dim3(THR), 0, s, a); break;            \
+    case 2: hipLaunchKernelGGL((KERNEL<float, true, false>), dim3(grid), dim3(THR), 0, s, a); break;            \
+    case 3: hipLaunchKernelGGL((KERNEL<float, true, true>), dim3(grid), dim3(THR), 0, s, a); break;             \
+    case 4: hipLaunchKernelGGL((KERNEL<__bf16, false, false>), dim3(grid), dim3(THR), 0, s, a); break;          \
+    case 5: hipLaunchKernelGGL((KERNEL<__bf16, false, true>), dim3(grid), dim3(THR), 0, s, a); break;           \
+    case 6: hipLaunchKernelGGL((KERNEL<__bf16, true, false>), dim3(grid), dim3(THR), 0, s, a); break;           \
+    default: hipLaunchKernelGGL((KERNEL<__bf16, true, true>), dim3(grid), dim3(THR), 0, s, a);                  \
   }                                                                                                             \
   return hipGetLastError();
 
@@ -714,7 +718,6 @@ hipError_t launch_scan_bwd(bool bf16, bool mix, ScanArgs a, void *ws, hipStream_
 hipError_t launch_scan_step(bool bf16, bool mix, const void *x, const void *g, float *state, void *h, size_t n,
                             hipStream_t s) {
   const size_t blocks = (n / (bf16 ? 8 : 4) + 255) / 256;
-  if (blocks > 0x7fffffffu) return hipErrorInvalidValue;
 #define FALCON_STEP1(T_, M_)                                                                                    \
   hipLaunchKernelGGL((scan_step<T_, M_>), dim3((unsigned)blocks), dim3(256), 0, s, static_cast<const T_ *>(x),   \
                      static_cast<const T_ *>(g), state, static_cast<T_ *>(h), n)

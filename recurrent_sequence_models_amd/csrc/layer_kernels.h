@@ -8,6 +8,9 @@
 
 namespace falcon {
 
+// A launch holds less than 2^32 threads.
+inline bool grid_fits(int64_t blocks, int threads) { return blocks >= 0 && blocks <= UINT32_MAX / threads; }
+
 // Gated linear recurrence.  Packed calls (cu != null) have rows = 1 and T = the
 // packed length; nseq sequences.  Otherwise rows = nseq sequences of T steps.
 struct ScanArgs {
@@ -26,6 +29,7 @@ struct ScanArgs {
   unsigned long long *pre;       // one carry per (column, group of chunks, channel)
   int rows, T, D, nseq, NC;
 };
+bool scan_fits(bool bf16, int rows, int T, int D);          // within a launch
 size_t scan_workspace(bool bf16, int rows, int T, int D);
 hipError_t launch_scan_fwd(bool bf16, bool mix, ScanArgs a, void *ws, hipStream_t s);
 hipError_t launch_scan_bwd(bool bf16, bool mix, ScanArgs a, void *ws, hipStream_t s);
@@ -65,10 +69,12 @@ struct AttnArgs {
   int64_t ldq, ldk, ldv, ldo, lddo, lddq, lddk, lddv;
   int n, Tq, Tk;                 // packed: Tq, Tk are the totals
   int hq, hk, group;             // group = hq / hk
-  int slots, splits;             // filled at launch
+  int splits;                    // filled at launch
   float scale;
 };
-size_t attn_fwd_workspace(bool bf16, int d, const AttnArgs &a);
+bool attn_fwd_fits(const AttnArgs &a);                      // within a launch
+bool attn_bwd_fits(bool bf16, int d, const AttnArgs &a);
+size_t attn_fwd_workspace(int d, const AttnArgs &a);
 hipError_t launch_attn_fwd(bool bf16, int d, AttnArgs a, void *ws, hipStream_t s);
 size_t attn_bwd_workspace(int d, const AttnArgs &a);
 hipError_t launch_attn_bwd(bool bf16, int d, AttnArgs a, void *ws, hipStream_t s);

@@ -100,12 +100,19 @@ def _offsets(name, cu, dev):
     return cu.numel() - 1
 
 
+def _ints(*sizes):
+    """The sizes, which the C structs hold in 32 bits (ctypes would drop the rest)."""
+    if max(sizes) > 2 ** 31 - 1:
+        raise ValueError(f"sizes {sizes}: at most 2^31 - 1")
+    return sizes
+
+
 # ---- Gated linear recurrence ----------------------------------------------------
 
 @functools.lru_cache(maxsize=1024)
 def _scan_plan(dtype, n, T, D, mix, packed):
     """(pointer to the C shape, workspace bytes)."""
-    shape = ScanShape(dtype, n, T, D, 1 if mix else 0)
+    shape = ScanShape(dtype, *_ints(n, T, D), 1 if mix else 0)
     return ctypes.pointer(shape), lib().falcon_scan_workspace(ctypes.byref(shape), packed)
 
 
@@ -297,9 +304,9 @@ def rope_frequencies(rot, base=10000.0, *, scaling=None, factor=1.0, original_le
 
 
 @functools.lru_cache(maxsize=1024)
-def _qk_plan(*sizes):
+def _qk_plan(dtype, tokens, hq, hk, d, *rest):
     """(pointer to the C shape, workspace bytes of the backward)."""
-    shape = QkShape(*sizes)
+    shape = QkShape(dtype, *_ints(tokens, hq, hk, d), *rest)
     return ctypes.pointer(shape), lib().falcon_qk_norm_rope_bwd_workspace(ctypes.byref(shape))
 
 
@@ -322,8 +329,8 @@ def _qk_shape(q, k, positions, inv_freq, q_weight, k_weight, norm, eps, layout, 
             if not norm:
                 raise ValueError(f"{name}: weights belong to the norm")
             _check(name, w, torch.float32, (d,), dev)
-    shape, need = _qk_plan(dt, tokens, q.shape[-2], k.shape[-2], d, rot, LAYOUTS[layout], 1 if norm else 0, eps, rot_scale,
-                           dt if grad_dtype is None else grad_dtype)
+    shape, need = _qk_plan(dt, tokens, q.shape[-2], k.shape[-2], d, rot, LAYOUTS[layout], 1 if norm else 0, float(eps),
+                           float(rot_scale), dt if grad_dtype is None else grad_dtype)
     return shape, need, d, dev
 
 
@@ -384,9 +391,9 @@ def qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, *, q_weight=None
 # ---- Causal attention -----------------------------------------------------------------
 
 @functools.lru_cache(maxsize=1024)
-def _attn_plan(packed, *sizes):
+def _attn_plan(packed, dtype, n, tq, tk, hq, hk, d, scale):
     """(pointer to the C shape, workspace bytes of the forward, of the backward)."""
-    shape = AttnShape(*sizes)
+    shape = AttnShape(dtype, *_ints(n, tq, tk, hq, hk, d), scale)
     L = lib()
     return (ctypes.pointer(shape), L.falcon_attn_fwd_workspace(ctypes.byref(shape), packed),
             L.falcon_attn_bwd_workspace(ctypes.byref(shape), packed))

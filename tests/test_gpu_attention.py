@@ -223,3 +223,27 @@ def test_keys_behind_the_mask(dtype, ql, kl, hq, hk, d):
         assert torch.isnan(o2[i:ql[0]].float()).all()
         if i > 0:
             assert torch.all(o2[i - 1].float() == -float("inf"))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_widest_strides(d):
+    """Tokens 2^25 bytes apart, the widest there are."""
+    import torch
+    from recurrent_sequence_models_amd import attention_bwd, attention_fwd
+    T, step = 131, 1 << 23
+    wide = torch.empty(T, step, device="cuda")
+    parts = [rand(i, T, 2, d) for i in range(4)]
+    views = []
+    for i, t in enumerate(parts):
+        v = wide[:, i * step // 4:][:, :2 * d].unflatten(1, (2, d))
+        v.copy_(t)
+        views.append(v)
+    cu = offsets([T])
+    (q, k, v, do), (wq, wk, wv, wdo) = parts, views
+    o, lse = attention_fwd(q, k, v, cu_seqlens=cu)
+    o2, lse2 = attention_fwd(wq, wk, wv, cu_seqlens=cu)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    want = attention_bwd(q, k, v, o, lse, do, cu_seqlens=cu)
+    got = attention_bwd(wq, wk, wv, o, lse, wdo, cu_seqlens=cu, out=None)
+    for n in ("dq", "dk", "dv"):
+        assert torch.equal(want[n], got[n]), n

@@ -204,3 +204,37 @@ def test_refusals():
         with pytest.raises((err, ValueError) if err is FalconError else err):
             f_()
             raise AssertionError(f"call {i} was taken")
+
+
+def test_more_tokens_than_a_launch_of_one_group_each():
+    """2^26 tokens and some: workgroups come round again, and the last tokens are as in a short call."""
+    import torch
+    from recurrent_sequence_models_amd import qk_norm_rope, rope_frequencies
+    n, tail, d = (1 << 26) + 5, 4099, 32
+    freq, _ = rope_frequencies(d, device="cuda")
+    q = torch.zeros(n, 1, d, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros_like(q)
+    at = [slice(0, tail), slice((1 << 20) - 7, (1 << 20) + tail), slice(n - tail, n)]   # 2^18 groups of 4 tokens in a round
+    for i, s in enumerate(at):
+        q[s] = rand(2 * i, s.stop - s.start, 1, d, dtype="bf16")
+        k[s] = rand(2 * i + 1, s.stop - s.start, 1, d, dtype="bf16")
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    want = [qk_norm_rope(q[s], k[s], pos[s], freq) for s in at]
+    qk_norm_rope(q, k, pos, freq, out=(q, k))
+    for s, (wq, wk) in zip(at, want):
+        assert torch.equal(q[s], wq) and torch.equal(k[s], wk)
+    assert not q[tail:(1 << 20) - 7].any()
+
+
+def test_numbers_in_changing_tensors():
+    """eps and the scale are taken by their value at the call, whatever object holds them."""
+    import torch
+    from recurrent_sequence_models_amd import qk_norm_rope, rope_frequencies
+    q, pos = rand(1, 9, 2, 64), torch.arange(9, dtype=torch.int32, device="cuda")
+    freq, _ = rope_frequencies(64, device="cuda")
+    eps, scale = torch.tensor(1e-6), torch.tensor(1.0)
+    a = qk_norm_rope(q, q, pos, freq, eps=eps, rot_scale=scale)[0]
+    eps.fill_(0.5), scale.fill_(2.0)
+    b = qk_norm_rope(q, q, pos, freq, eps=eps, rot_scale=scale)[0]
+    assert torch.equal(a, qk_norm_rope(q, q, pos, freq)[0])
+    assert torch.equal(b, qk_norm_rope(q, q, pos, freq, eps=0.5, rot_scale=2.0)[0])

@@ -174,3 +174,42 @@ def test_attention_workspace():
     assert L.falcon_attn_fwd_workspace(ref(attn_shape(seqlen_q=2, seqlen_k=1 << 14)), 1) > 0
     assert L.falcon_attn_bwd_workspace(ref(attn_shape()), 0) == 2 * 2 * 100 * 4 * 4
     assert L.falcon_attn_bwd_workspace(ref(attn_shape()), 1) == 2 * 100 * 4 * 4
+
+
+@cpu_only
+def test_sizes_past_a_launch_or_an_index():
+    """Sizes whose workgroups, numbers or addresses would pass what a launch or an index holds are
+    refused, the largest that fit are not (they get as far as the workspace)."""
+    L = F.lib()
+    big = 1 << 62
+    for kw, packed in ((dict(batch=1 << 23, seqlen=1, width=64), 0), (dict(batch=1 << 22, seqlen=257, width=64), 0),
+                       (dict(batch=1, seqlen=1 << 26, width=1 << 12), 1), (dict(batch=(1 << 30) + 1, seqlen=1000), 1)):
+        s, cu = scan_shape(**kw), P if packed else None
+        assert scan_fwd(s, cu=cu, n=big) == UNSUPPORTED and scan_bwd(s, cu=cu, n=big) == UNSUPPORTED, kw
+        assert L.falcon_scan_workspace(ref(s), packed) == 0
+    for kw, packed in ((dict(batch=(1 << 22) - 1, seqlen=257, width=64), 0), (dict(batch=1 << 30, seqlen=1000), 1)):
+        s, cu = scan_shape(**kw), P if packed else None
+        assert scan_fwd(s, cu=cu, n=16) == WORKSPACE and scan_bwd(s, cu=cu, n=16) == WORKSPACE, kw
+    for kw in (dict(batch=1 << 24, seqlen_q=1, seqlen_k=1, heads_q=8, heads_k=8),
+               dict(batch=1 << 12, seqlen_q=1 << 12, seqlen_k=1 << 12, heads_q=256, heads_k=128)):
+        s = attn_shape(**kw)
+        t = H(P, kw["heads_q"] * 64)
+        assert attn_fwd(s, q=t, k=t, v=t, n=big) == UNSUPPORTED, kw
+        assert attn_bwd(s, q=t, k=t, v=t, do=t, dq=t, dk=t, dv=t, n=big) == UNSUPPORTED, kw
+    assert attn_bwd(attn_shape(batch=1 << 10, seqlen_q=1 << 10, seqlen_k=1), n=16) == WORKSPACE
+    for dtype, most in ((1, 1 << 24), (0, 1 << 23)):   # 2^25 bytes between tokens
+        s = attn_shape(dtype=dtype)
+        for name in ("q", "k", "v"):
+            assert attn_fwd(s, **{name: H(P, most + 8)}) == UNSUPPORTED, (dtype, name)
+            assert attn_bwd(s, n=16, **{name: H(P, most)}) == WORKSPACE, (dtype, name)
+        assert attn_bwd(s, do=H(P, most + 8)) == UNSUPPORTED
+
+
+def test_sizes_past_32_bits():
+    """The binding refuses sizes that the C structs would hold only in part."""
+    from recurrent_sequence_models_amd import layer
+    for call, sizes in ((layer._scan_plan, (1, 1, 2 ** 32 + 5, 8, False, False)),
+                        (layer._qk_plan, (1, 2 ** 32 + 1, 4, 4, 64, 64, 0, 1, 1e-6, 1.0, 1)),
+                        (layer._attn_plan, (False, 1, 1, 2 ** 31, 5, 4, 4, 64, 0.125))):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call(*sizes)
