@@ -131,3 +131,42 @@ def test_single_tokens_continue_a_prompt(dtype):
         for i in range(len(lens)):
             want = f64(whole[int(ends[i]) - more + t])
             assert rel_l2(f64(o[i]), want) <= TOL[dtype] / 2, (t, i)
+
+
+def test_graphs_that_share_a_workspace():
+    """Two captured graphs whose calls were given the same workspaces, replayed in turn with eager
+    calls on them between."""
+    import torch
+    from recurrent_sequence_models_amd import (attention_bwd, attention_fwd, gated_scan, gated_scan_bwd, qk_norm_rope_bwd,
+                                               rope_frequencies)
+    x, g, dh = (rand(i, 2, 1500, 72, dtype="bf16") for i in (1, 2, 3))
+    g = -g.abs()
+    q, k, v, do = (rand(i, 700, h, 64, dtype="bf16") for i, h in ((4, 4), (5, 2), (6, 2), (7, 4)))
+    one, cu, cuk = rand(8, 1, 4, 64, dtype="bf16"), offsets([1]), offsets([700])
+    pos, freq = torch.arange(700, dtype=torch.int32, device="cuda"), rope_frequencies(64, device="cuda")[0]
+    w = rand(9, 64)
+    ws = [torch.empty(1 << 24, dtype=torch.uint8, device="cuda") for _ in range(4)]
+
+    def call(sign):
+        h, _, st = gated_scan(x, g, mix=sign, chunk_states=True, workspace=ws[0])
+        b = gated_scan_bwd(x, g, dh, st, mix=sign, workspace=ws[0])
+        o, lse = attention_fwd(q, k, v, scale=0.1 + 0.1 * sign, cu_seqlens=cuk, workspace=ws[1])
+        t, _ = attention_fwd(one, k, v, scale=0.1 + 0.1 * sign, cu_seqlens=cu, cu_seqlens_k=cuk, workspace=ws[1])
+        a = attention_bwd(q, k, v, o, lse, do, scale=0.1 + 0.1 * sign, cu_seqlens=cuk, workspace=ws[2])
+        n = qk_norm_rope_bwd(q, k, pos, freq, do, k, q_weight=w, k_weight=w, rot_scale=1.0 + sign, workspace=ws[3])
+        return [h, st, *b.values(), o, t, *a.values(), *n.values()]
+
+    want = [call(False), call(True)]
+    torch.cuda.synchronize()
+    graphs, got = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], [None, None]
+    for i in (0, 1):
+        with torch.cuda.graph(graphs[i]):
+            got[i] = call(bool(i))
+    for turn in (0, 1, 1, 0, 1):
+        for t in got[turn]:
+            t.zero_()
+        graphs[turn].replay()
+        eager = call(not turn)
+        torch.cuda.synchronize()
+        for a, b, c, d in zip(got[turn], want[turn], eager, want[not turn]):
+            assert torch.equal(a, b) and torch.equal(c, d)

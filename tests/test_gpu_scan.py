@@ -318,3 +318,24 @@ def test_refusals():
         gated_scan_step(x[:, 0].contiguous(), x[:, 0].contiguous(), torch.zeros(2, 32, device="cuda"))
     with pytest.raises(ValueError):
         gated_scan(x.cpu(), x.cpu())
+
+
+def test_past_32_bits_of_elements():
+    """Arrays of over 2^31 elements: the steps behind that place are as in a short call."""
+    import torch
+    from recurrent_sequence_models_amd import gated_scan, gated_scan_bwd
+    D, T, tail = 2048, (1 << 20) + 512 + 5, 517     # the tail begins with a chunk, and with a reset
+    cut = slice(T - tail, T)
+    x, g, dh = (torch.zeros(1, T, D, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    x[:, cut], dh[:, cut] = rand(1, 1, tail, D, dtype="bf16"), rand(2, 1, tail, D, dtype="bf16")
+    g[:, cut] = gates(3, 1, tail, D, dtype="bf16")
+    g[:, T - tail] = float("-inf")
+    h, fin, st = gated_scan(x, g, chunk_states=True)
+    b = gated_scan_bwd(x, g, dh, st)
+    X, G, DH = (t[:, cut].contiguous() for t in (x, g, dh))
+    h2, fin2, st2 = gated_scan(X, G, chunk_states=True)
+    b2 = gated_scan_bwd(X, G, DH, st2)
+    assert torch.equal(h[:, cut], h2) and torch.equal(fin, fin2) and torch.equal(st[:, -3:], st2)
+    assert not h[:, :T - tail].any()
+    for n in ("dx", "dg"):
+        assert torch.equal(b[n][:, cut], b2[n]) and not b[n][:, :T - tail].any(), n
