@@ -66,6 +66,12 @@ __device__ __forceinline__ Frag<float> global_frag(const float *row, int b, int 
   return {*reinterpret_cast<const f4 *>(row + 16 * b + 8 * h), *reinterpret_cast<const f4 *>(row + 16 * b + 8 * h + 4)};
 }
 
+// Makes a fragment's loads arrive here.  The compiler waits for them at their first use, and where
+// that is in a loop it waits there every time, for the loop's copies (below) as well, which it
+// does not know of: the next tile's copies would be awaited as soon as they are issued.
+__device__ __forceinline__ void arrived(Frag<__bf16> &f) { asm volatile("" : "+v"(f.v)); }
+__device__ __forceinline__ void arrived(Frag<float> &f) { asm volatile("" : "+v"(f.lo), "+v"(f.hi)); }
+
 // A tile of ROWS rows of D entries in LDS, in 16-byte chunks.  Chunk c of a row stands at
 // place c ^ swizzle(row): reads of one chunk of 16 neighbouring rows, and column reads of
 // 4 rows x 4 chunks, then touch all banks evenly (unswizzled, rows of 256 bytes put a

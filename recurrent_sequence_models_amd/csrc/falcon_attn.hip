@@ -32,36 +32,38 @@ template <typename T, int D> struct Fwd {
   static constexpr int KB = TN / 32;
 };
 
-// One tile's softmax: s becomes the weights e^{scale s - reference}; the reference m (in raw
-// scores), this lane's half of the sum and the results follow.
+// Softmax state of a lane's row: the score, in base 2, that weights are relative to (-inf: nothing
+// seen yet), and this lane's half of the sum of weights.
+struct Row { float base = -INFINITY, l = 0.f; };
+
+// One tile's softmax: s becomes the weights 2^{scale log2(e) s - base}.  The base follows the
+// maximum when that has grown by over 8: weights stay below 2^8, and most tiles neither exchange
+// maxima between the row's two lanes nor rescale.
 template <int KB, int CB>
-__device__ __forceinline__ void weigh(f16v (&s)[KB], float sc, float &m, float &l, f16v (&acc)[CB]) {
+__device__ __forceinline__ void weigh(f16v (&s)[KB], float sc, Row &r, f16v (&acc)[CB]) {
   float top = s[0][0];
 #pragma unroll
   for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
     for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kb][i]);
-  top = max_xor32(top);
-  // The reference follows the maximum when that has grown by over 8 (base 2): weights stay
-  // below 2^8, and most tiles rescale nothing.  (-inf: nothing seen yet, any weight is 0.)
-  if (__any(top * sc > m * sc + 8.f)) {
-    const float now = fmaxf(top, m);
-    const float f = now == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - now) * sc);
-    l *= f;
+  if (__any(fmaf(top, sc, -r.base) > 8.f)) {
+    const float now = fmaxf(max_xor32(top) * sc, r.base);
+    const float f = now == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(r.base - now);
+    r.l *= f;
 #pragma unroll
     for (int b = 0; b < CB; ++b) acc[b] *= f;
-    m = now;
+    r.base = now;
   }
-  const float shift = m == -INFINITY ? 0.f : m * sc;
+  const float base = r.base == -INFINITY ? 0.f : r.base;
   float sum = 0.f;
 #pragma unroll
   for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      s[kb][i] = __builtin_amdgcn_exp2f(fmaf(s[kb][i], sc, -shift));
+      s[kb][i] = __builtin_amdgcn_exp2f(fmaf(s[kb][i], sc, -base));
       sum += s[kb][i];
     }
-  l += sum;
+  r.l += sum;
 }
 
 // acc += V^T P^T for one tile of KB * 32 keys.
@@ -106,9 +108,8 @@ __device__ __forceinline__ void add_nonfinite(O *out, const T *v, int64_t ld, in
 // A lane's row: the result and lse, or, of one of several splits, the unnormalised sum [split]
 // [row of the packed axis and head][d], then (reference in base 2, sum of weights).
 template <typename T, int D>
-__device__ __forceinline__ void finish(const AttnArgs &a, size_t at, int split, int h, float m, float l,
+__device__ __forceinline__ void finish(const AttnArgs &a, size_t at, int split, int h, float base, float l,
                                        const f16v (&acc)[D / 32]) {
-  const float sc = a.scale * kLog2e;
   if (a.splits > 1) {
     const size_t nrow = (size_t)query_tokens(a) * a.hq, ps = split * nrow + at;
     float *p = a.part + ps * D;
@@ -119,7 +120,7 @@ __device__ __forceinline__ void finish(const AttnArgs &a, size_t at, int split, 
         store4(p + b * 32 + 2 * i + 4 * h, acc[b][i], acc[b][i + 1], acc[b][i + 2], acc[b][i + 3]);
     if (h == 0) {
       float *ml = a.part + a.splits * nrow * D + ps * 2;
-      ml[0] = m * sc;
+      ml[0] = base;
       ml[1] = l;
     }
     return;
@@ -131,7 +132,7 @@ __device__ __forceinline__ void finish(const AttnArgs &a, size_t at, int split, 
 #pragma unroll
     for (int i = 0; i < 16; i += 4)
       store4(out + b * 32 + 2 * i + 4 * h, acc[b][i] * inv, acc[b][i + 1] * inv, acc[b][i + 2] * inv, acc[b][i + 3] * inv);
-  if (h == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : kLn2 * (m * sc + __builtin_amdgcn_logf(l));
+  if (h == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : kLn2 * (base + __builtin_amdgcn_logf(l));
 }
 
 template <typename T, int D>
@@ -231,11 +232,13 @@ template <typename T, int D> __global__ __launch_bounds__(THR, sizeof(T) * D > 2
 
   const float sc = a.scale * kLog2e;
   f16v acc[CB];
-  float m = -INFINITY, l = 0.f;                 // the weights' reference score; this lane's half of the sum
+  Row row;
 #pragma unroll
   for (int b = 0; b < CB; ++b) acc[b] = zero16();
   if (kt0 < kt1) copy(kt0, 0);
   copies_done();
+#pragma unroll
+  for (int b = 0; b < DB; ++b) arrived(qf[b]);
   if (kt0 < kt1) clean(kt0, 0);
   __syncthreads();
   for (int kt = kt0; kt < kt1; ++kt) {
@@ -257,17 +260,17 @@ template <typename T, int D> __global__ __launch_bounds__(THR, sizeof(T) * D > 2
         for (int i = 0; i < 16; ++i)
           if (kb * 32 + 8 * (i / 4) + (i & 3) > left) s[kb][i] = -INFINITY;
     }
-    weigh<F::KB, CB>(s, sc, m, l, acc);
+    weigh<F::KB, CB>(s, sc, row, acc);
     add_values<T, D, F::KB>(acc, s, sv[buf], lane);
     }
     copies_done();
     if (kt + 1 < kt1) clean(kt + 1, buf ^ 1);
     __syncthreads();
   }
-  l = add_xor32(l);
+  const float l = add_xor32(row.l);
   if (!on) return;
   const size_t at = (size_t)(q.q0 + tok) * a.hq + hq;
-  finish<T, D>(a, at, split, h, m, l, acc);
+  finish<T, D>(a, at, split, h, row.base, l, acc);
   if (sbad) restore<T, D>(a, at, split, vg, max(kt0, hidden0) * TN, min(lim + 1, kt1 * TN), h);
 }
 
@@ -334,10 +337,12 @@ template <typename T, int D> __global__ __launch_bounds__(64, sizeof(T) * D > 25
   };
   const float sc = a.scale * kLog2e;
   f16v acc[CB];
-  float m = -INFINITY, l = 0.f;
+  Row row;
   bool bad = false;                                        // a value was cleaned
   const int hidden0 = first_lim + 1 < q.Lk ? max(first_lim + 1, 0) / TN : kt1;
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");         // from here on only copies are counted
+#pragma unroll
+  for (int b = 0; b < DB; ++b) arrived(qf[b]);
 #pragma unroll
   for (int b = 0; b < CB; ++b) acc[b] = zero16();
   if (kt0 < kt1) copy(kt0, 0);
@@ -363,15 +368,15 @@ template <typename T, int D> __global__ __launch_bounds__(64, sizeof(T) * D > 25
       for (int i = 0; i < 16; ++i)
         if (8 * (i / 4) + (i & 3) > left) s[0][i] = -INFINITY;
     }
-    weigh<1, CB>(s, sc, m, l, acc);
+    weigh<1, CB>(s, sc, row, acc);
     add_values<T, D, 1>(acc, s, sv[buf], lane);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");     // the buffer is read; the next copy may fill it
   }
-  l = add_xor32(l);
+  const float l = add_xor32(row.l);
   const bool cleaned = __any(bad);
   if (r0 + c >= rows) return;
   const size_t at = (size_t)(q.q0 + tok) * a.hq + hq;
-  finish<T, D>(a, at, split, h, m, l, acc);
+  finish<T, D>(a, at, split, h, row.base, l, acc);
   if (cleaned) restore<T, D>(a, at, split, vg, max(kt0, hidden0) * TN, min(lim + 1, kt1 * TN), h);
 }
 

@@ -150,6 +150,10 @@ __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_kv(
   const float sc = a.scale * kLog2e;
   if (t0 < t1) copy(t0, 0);
   copies_done();
+#pragma unroll
+  for (int b = 0; b < KR; ++b) arrived(kf[b]);
+#pragma unroll
+  for (int b = 0; b < (VL ? 0 : DB); ++b) arrived(vf[b]);
   __syncthreads();
   for (int t = t0; t < t1; ++t) {
     const int buf = (t - t0) & 1;
@@ -303,6 +307,8 @@ __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_q(A
   const float sc = a.scale * kLog2e;
   if (ktiles > 0) copy(0, 0);
   copies_done();
+#pragma unroll
+  for (int b = 0; b < DB; ++b) { arrived(qf[b]); arrived(gf[b]); }
   __syncthreads();
   for (int kt = 0; kt < ktiles; ++kt) {
     const int buf = kt & 1;
