@@ -349,19 +349,24 @@ int falcon_chunk_bwd(const falcon_shape_t *shape,
  * Tokens behind the last sequence are not written.  Gradients with
  * respect to activations have the activations' dtype; those with respect to
  * parameters and states are fp32.  Sums, states, softmax statistics and norms
- * are fp32, and results are deterministic.  NaN and infinities propagate as in
- * the formulas, within their own sequence only. */
+ * are fp32, and results are deterministic.  NaN and infinities stay in their own
+ * sequence.  A workspace needs no initialisation and serves one call at a time.
+ * Sizes past the limits given here, or past a launch (2^32 threads), are
+ * FALCON_ERR_UNSUPPORTED. */
 
 /* ---- Gated linear recurrence ---------------------------------------------
  * Per sequence and channel, with lam_t = exp(log_lambda_t):
  *   h_t = lam_t h_{t-1} + u_t,  u_t = x_t            (FALCON_SCAN_ADD)
  *                               u_t = (1 - lam_t) x_t (FALCON_SCAN_MIX)
- * There is no decay floor: log_lambda = -inf is an exact reset (lam = 0). */
+ * There is no decay floor: log_lambda = -inf is an exact reset (lam = 0).
+ * log_lambda > 0 grows the state; the product of the lam of FALCON_SCAN_CHUNK
+ * steps then has to stay in fp32's range.  (Steps are composed before they are
+ * applied: behind an infinite state a later one may be NaN.) */
 typedef enum { FALCON_SCAN_ADD = 0, FALCON_SCAN_MIX = 1 } falcon_scan_input_t;
 
 typedef struct {
   int32_t dtype;   /* falcon_dtype_t of x, log_lambda, h and their gradients */
-  int32_t batch;   /* sequences, >= 1 */
+  int32_t batch;   /* sequences, 1 .. 2^30 */
   int32_t seqlen;  /* steps of every sequence, >= 1; packed: all tokens (>= 1) */
   int32_t width;   /* channels, a multiple of 8, at most 2^20 */
   int32_t input;   /* falcon_scan_input_t */
@@ -383,8 +388,8 @@ size_t falcon_scan_workspace(const falcon_scan_shape_t *shape, int packed);
  *   chunk_states [B, ceil(T / FALCON_SCAN_CHUNK), D] fp32 (packed: of the one
  *                packed time axis, [1, ...]), or NULL: h after every chunk, for
  *                the backward pass.
- *   workspace    at least falcon_scan_workspace bytes, else FALCON_ERR_WORKSPACE;
- *                needs no initialisation; calls sharing one race. */
+ *   workspace    at least falcon_scan_workspace bytes, else FALCON_ERR_WORKSPACE.
+ * Outputs must not overlap inputs otherwise. */
 int falcon_scan_fwd(const falcon_scan_shape_t *shape, const int32_t *cu_seqlens, const void *x, const void *log_lambda,
                     const float *init, float *final_state, void *h, float *chunk_states,
                     void *workspace, size_t workspace_bytes, void *stream);
@@ -410,14 +415,15 @@ int falcon_scan_step(const falcon_scan_shape_t *shape, const void *x, const void
  *   y_a = z_a cos - z_b sin,  y_b = z_b cos + z_a sin
  * with a = j, b = j + rot / 2 (FALCON_ROPE_HALF) or a = 2 j, b = 2 j + 1
  * (FALCON_ROPE_INTERLEAVED); the other entries are z.  Longer contexts scale
- * inv_freq and rot_scale; the angle is formed in 64 bits. */
+ * inv_freq and rot_scale; the angle is formed in 64 bits, the mean of squares in
+ * 32 (entries over 2^63 overflow it: z = 0). */
 typedef enum { FALCON_ROPE_HALF = 0, FALCON_ROPE_INTERLEAVED = 1 } falcon_rope_layout_t;
 
 typedef struct {
   int32_t dtype;     /* falcon_dtype_t of q, k and the outputs */
-  int32_t tokens;    /* >= 1 */
+  int32_t tokens;    /* 1 .. 2^31 - 1 - 2^20 */
   int32_t heads_q;   /* >= 1 */
-  int32_t heads_k;   /* >= 1 */
+  int32_t heads_k;   /* >= 1; both together at most 2^20 */
   int32_t d;         /* 32, 64 or 128 */
   int32_t rot;       /* rotated entries: a multiple of 16, 0 .. d */
   int32_t layout;    /* falcon_rope_layout_t */
@@ -458,14 +464,16 @@ int falcon_qk_norm_rope_bwd(const falcon_qk_shape_t *shape, falcon_heads_t q, fa
  * The queries of a sequence are the last Lq of its Lk tokens: query i sees keys
  * j <= i + Lk - Lq.  Query head h reads key head h / (heads_q / heads_k).
  *   o_i = sum_j softmax_j(scale q_i . k_j) v_j,  lse_i = ln sum_j e^{scale q_i . k_j}
- * A query that sees no key (Lq > Lk) has o = 0, lse = -inf and no gradients. */
+ * A query that sees no key (Lq > Lk) has o = 0, lse = -inf and no gradients.
+ * Infinite or NaN keys and values do not reach o and lse of the queries that do
+ * not see them; any gradient of a sequence that holds some may be NaN. */
 typedef struct {
   int32_t dtype;     /* falcon_dtype_t of every array but lse */
-  int32_t batch;     /* sequences, >= 1 */
+  int32_t batch;     /* sequences, 1 .. 2^30 */
   int32_t seqlen_q;  /* query tokens of every sequence, >= 1; packed: all of them */
   int32_t seqlen_k;  /* key tokens of every sequence, >= 1; packed: all of them */
-  int32_t heads_q;   /* a multiple of heads_k */
-  int32_t heads_k;   /* >= 1 */
+  int32_t heads_q;   /* a multiple of heads_k, at most 2^20 */
+  int32_t heads_k;   /* >= 1; query tokens * heads_q / heads_k at most 2^31 - 4097 */
   int32_t d;         /* 32, 64 or 128 */
   float scale;       /* finite, > 0 */
 } falcon_attn_shape_t;
@@ -475,8 +483,9 @@ typedef struct {
  * workspace may be NULL).  `packed`: nonzero for calls with offsets. */
 size_t falcon_attn_fwd_workspace(const falcon_attn_shape_t *shape, int packed);
 
-/* q [tokens, heads_q, d], k, v [tokens, heads_k, d] (token strides as above),
- * o dense [tokens, heads_q, d], lse [tokens, heads_q] fp32 or NULL.
+/* q [tokens, heads_q, d], k, v [tokens, heads_k, d] (token strides as above, at
+ * most 2^25 bytes), o dense [tokens, heads_q, d], lse [tokens, heads_q] fp32 or
+ * NULL; they must not overlap the inputs.
  *   cu_q, cu_k  both NULL (batch * seqlen tokens) or both [batch + 1] offsets. */
 int falcon_attn_fwd(const falcon_attn_shape_t *shape, const int32_t *cu_q, const int32_t *cu_k,
                     falcon_heads_t q, falcon_heads_t k, falcon_heads_t v, void *o, float *lse,
@@ -487,7 +496,7 @@ int falcon_attn_fwd(const falcon_attn_shape_t *shape, const int32_t *cu_q, const
 size_t falcon_attn_bwd_workspace(const falcon_attn_shape_t *shape, int packed);
 
 /* Gradients of <d_o, o> with respect to q, k, v, from the forward's o and lse (o
- * dense).  Outputs must not alias inputs. */
+ * dense; the stride of d_o at most 2^25 bytes).  Outputs must not alias inputs. */
 int falcon_attn_bwd(const falcon_attn_shape_t *shape, const int32_t *cu_q, const int32_t *cu_k,
                     falcon_heads_t q, falcon_heads_t k, falcon_heads_t v, const void *o, const float *lse,
                     falcon_heads_t d_o, falcon_heads_out_t dq, falcon_heads_out_t dk, falcon_heads_out_t dv,

@@ -45,7 +45,10 @@ int check_scan(const falcon_scan_shape_t *s, bool packed, bool step) {
   if (s->input != FALCON_SCAN_ADD && s->input != FALCON_SCAN_MIX) return FALCON_ERR_INVALID_ARG;
   if (s->batch < 1 || s->width < 1 || (!step && s->seqlen < 1)) return FALCON_ERR_INVALID_ARG;
   if (s->width % 8 != 0 || s->width > (1 << 20)) return FALCON_ERR_UNSUPPORTED;
-  if (step) return FALCON_OK;
+  if (step) {
+    const int64_t threads = (int64_t)s->batch * s->width * esize(s->dtype) / 16;
+    return falcon::grid_fits((threads + 255) / 256, 256) ? FALCON_OK : FALCON_ERR_UNSUPPORTED;
+  }
   // step and sequence numbers are ints, with a chunk or a stride over the sequences added
   if (s->seqlen > INT32_MAX - FALCON_SCAN_CHUNK || s->batch > (1 << 30)) return FALCON_ERR_UNSUPPORTED;
   if (!falcon::scan_fits(s->dtype == FALCON_BF16, packed ? 1 : s->batch, s->seqlen, s->width)) return FALCON_ERR_UNSUPPORTED;

@@ -190,6 +190,7 @@ def test_sizes_past_a_launch_or_an_index():
     for kw, packed in ((dict(batch=(1 << 22) - 1, seqlen=257, width=64), 0), (dict(batch=1 << 30, seqlen=1000), 1)):
         s, cu = scan_shape(**kw), P if packed else None
         assert scan_fwd(s, cu=cu, n=16) == WORKSPACE and scan_bwd(s, cu=cu, n=16) == WORKSPACE, kw
+    assert L.falcon_scan_step(ref(scan_shape(batch=1 << 30, width=1 << 5)), P, P, P, P, None) == UNSUPPORTED
     for kw in (dict(batch=1 << 24, seqlen_q=1, seqlen_k=1, heads_q=8, heads_k=8),
                dict(batch=1 << 12, seqlen_q=1 << 12, seqlen_k=1 << 12, heads_q=256, heads_k=128)):
         s = attn_shape(**kw)
