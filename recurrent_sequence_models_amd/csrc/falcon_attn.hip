@@ -14,8 +14,15 @@
 // between two lanes, its factors need none, and P^T is the right operand of
 // O^T = V^T P^T as it stands.
 //
-// Bound: MFMA (4 d flops per visible pair and head) for long prompts, with the
-// exponentials close behind; HBM (K and V once) for single tokens.
+// Bound: for prompts the matrix unit (4 d flops per visible pair and head), with the
+// exponentials close behind, and power: with operands of zeros the same launches take 20 %
+// less, as the clock then stays up.  HBM (K and V once) for single tokens.  Measured, where an
+// 8192^3 bf16 matrix product reaches 1.21 PFLOP/s:
+//   1 x 16384, 16 / 4 heads of 128, bf16: 1.00 ms, 1.10 PFLOP/s (matrix unit busy 57 %, vector unit 54 %)
+//   8 x 2048, 12 / 12 heads of 64, bf16: 76 us, 0.68 PFLOP/s (35 and 64 %), 92 us in a long run
+//   2 x 2048, 12 / 12 heads of 64, fp32: 192 us, 67 TFLOP/s (384 workgroups; an fp32 product: 154)
+// Issuing the next tile's scores between this one's exponentials, in one wave, was slower (80 us
+// and 1.06 ms): the waves of a SIMD overlap the two by themselves, without its registers.
 #include "attn_frag.h"
 #include "layer_kernels.h"
 
@@ -131,23 +138,28 @@ __device__ __forceinline__ void finish(const AttnArgs &a, size_t at, int split, 
   for (int b = 0; b < D / 32; ++b)
 #pragma unroll
     for (int i = 0; i < 16; i += 4)
-      store4(out + b * 32 + 2 * i + 4 * h, acc[b][i] * inv, acc[b][i + 1] * inv, acc[b][i + 2] * inv, acc[b][i + 3] * inv);
+      store4(out + b * 32 + 2 * i + 4 * h, acc[b][i] * inv, acc[b][i + 1] * inv, acc[b][i + 2] * inv,
+             acc[b][i + 3] * inv);
   if (h == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : kLn2 * (base + __builtin_amdgcn_logf(l));
 }
 
 template <typename T, int D>
 __device__ __forceinline__ void restore(const AttnArgs &a, size_t at, int split, const T *v, int j0, int j1, int h) {
-  if (a.splits > 1) add_nonfinite<T, float, D>(a.part + (split * (size_t)query_tokens(a) * a.hq + at) * D, v, a.ldv, j0, j1, h);
-  else add_nonfinite<T, T, D>(static_cast<T *>(a.out) + at * D, v, a.ldv, j0, j1, h);
+  if (a.splits > 1)
+    add_nonfinite<T, float, D>(a.part + (split * (size_t)query_tokens(a) * a.hq + at) * D, v, a.ldv, j0, j1, h);
+  else
+    add_nonfinite<T, T, D>(static_cast<T *>(a.out) + at * D, v, a.ldv, j0, j1, h);
 }
 
-template <typename T, int D> __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : sizeof(T) * D > 128 ? 2 : 4) void attn_fwd(AttnArgs a) {
+template <typename T, int D>
+__global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : sizeof(T) * D > 128 ? 2 : 4) void attn_fwd(AttnArgs a) {
   typedef Fwd<T, D> F;
   typedef Tile<T, D> Ti;
   constexpr int TN = F::TN, DB = D / 16, CB = D / 32;
   __shared__ uint4 sk[2][F::CH], sv[2][F::CH];
   __shared__ int sbad;                          // a value was cleaned
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 31, h = lane >> 5;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = tid & 63, c = lane & 31, h = lane >> 5;
 
   // key head fastest (a head stays on one die where 8 and hk divide one another), then the
   // split of the keys, then the tiles
@@ -245,23 +257,23 @@ template <typename T, int D> __global__ __launch_bounds__(THR, sizeof(T) * D > 2
     const int buf = (kt - kt0) & 1;
     if (kt + 1 < kt1) copy(kt + 1, buf ^ 1);    // its last readers are behind the barrier
     if (kt * TN <= wave_lim) {                  // else no row of this wave sees a key of the tile
-    f16v s[F::KB];
+      f16v s[F::KB];
 #pragma unroll
-    for (int kb = 0; kb < F::KB; ++kb) {
-      s[kb] = zero16();
+      for (int kb = 0; kb < F::KB; ++kb) {
+        s[kb] = zero16();
 #pragma unroll
-      for (int b = 0; b < DB; ++b) mma(s[kb], Ti::rows(sk[buf], kb * 32, b, lane), qf[b]);
-    }
-    if (kt * TN + TN - 1 > first_lim) {         // the same for the whole wave
-      const int left = lim - kt * TN - 4 * h;   // key 8 (i / 4) + 4 h + i % 4 of the tile is seen up to here
+        for (int b = 0; b < DB; ++b) mma(s[kb], Ti::rows(sk[buf], kb * 32, b, lane), qf[b]);
+      }
+      if (kt * TN + TN - 1 > first_lim) {       // the same for the whole wave
+        const int left = lim - kt * TN - 4 * h; // key 8 (i / 4) + 4 h + i % 4 of the tile is seen up to here
 #pragma unroll
-      for (int kb = 0; kb < F::KB; ++kb)
+        for (int kb = 0; kb < F::KB; ++kb)
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (kb * 32 + 8 * (i / 4) + (i & 3) > left) s[kb][i] = -INFINITY;
-    }
-    weigh<F::KB, CB>(s, sc, row, acc);
-    add_values<T, D, F::KB>(acc, s, sv[buf], lane);
+          for (int i = 0; i < 16; ++i)
+            if (kb * 32 + 8 * (i / 4) + (i & 3) > left) s[kb][i] = -INFINITY;
+      }
+      weigh<F::KB, CB>(s, sc, row, acc);
+      add_values<T, D, F::KB>(acc, s, sv[buf], lane);
     }
     copies_done();
     if (kt + 1 < kt1) clean(kt + 1, buf ^ 1);
@@ -279,6 +291,8 @@ template <typename T, int D> __global__ __launch_bounds__(THR, sizeof(T) * D > 2
 // keys, and the time is that of reading K and V once.  A workgroup is one wave with its own 32
 // rows, one split of the keys, tiles of 32 keys and its own part of LDS, so nothing waits at a
 // barrier: tile t + 1 is on its way while tile t is used.
+// 16 sequences of up to 16384 keys, 16 / 4 heads of 128, single tokens: 67 us for 329 MB (4.9 TB/s), and
+// 5 us for the join.
 constexpr int FEW = 32;
 
 template <typename T, int D> __global__ __launch_bounds__(64, sizeof(T) * D > 256 ? 1 : 2) void attn_few(AttnArgs a) {
@@ -380,43 +394,89 @@ template <typename T, int D> __global__ __launch_bounds__(64, sizeof(T) * D > 25
   if (cleaned) restore<T, D>(a, at, split, vg, max(kt0, hidden0) * TN, min(lim + 1, kt1 * TN), h);
 }
 
-// Joins the splits of a row: one workgroup a row, D / 4 threads side by side, the splits dealt
-// to the threads' groups and the groups added in order.
+// Joins the splits of a row, one workgroup a row: a thread forms the factor of one split (of at most
+// THR; one thread after the other over 64 splits took 20 us), then
+// D / 4 threads side by side add every GR-th split's sums, and the groups are added in order.
 template <typename T, int D> __global__ __launch_bounds__(THR) void attn_join(AttnArgs a, size_t nrow) {
-  constexpr int L = D / 4, GR = THR / L;
-  __shared__ float sl[GR];
+  constexpr int L = D / 4, GR = THR / L, WAVES = THR / 64;
+  __shared__ float sm[WAVES], sl[WAVES], sf[THR];
   __shared__ f4 so[GR][L];
   const size_t row = blockIdx.x;
   if (a.cuq && row >= (size_t)max(a.cuq[a.n], 0) * a.hq) return;    // behind the last sequence
-  const int g = threadIdx.x / L, e = threadIdx.x % L;
+  const int t = threadIdx.x, wave = t >> 6, g = t / L, e = t % L;
   const float *ml = a.part + a.splits * nrow * D;
-  float m = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, ml[(s * nrow + row) * 2]);
-  f4 o = zero4();
-  float l = 0.f;
-#pragma unroll 4
-  for (int s = g; s < a.splits; s += GR) {
-    const float ms = ml[(s * nrow + row) * 2], ls = ml[(s * nrow + row) * 2 + 1];
-    const f4 p = *reinterpret_cast<const f4 *>(a.part + (s * nrow + row) * D + e * 4);
-    const float f = ms == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ms - m);   // nothing seen in this split
-    l = fmaf(f, ls, l);
-    o += f * p;
+  float ms = -INFINITY, l = 0.f;
+  if (t < a.splits) {
+    ms = ml[(t * nrow + row) * 2];
+    l = ml[(t * nrow + row) * 2 + 1];
   }
+  float m = ms;
+#pragma unroll
+  for (int i = 32; i > 0; i /= 2) m = fmaxf(m, __shfl_xor(m, i));
+  if ((t & 63) == 0) sm[wave] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) m = fmaxf(m, sm[w]);
+  const float f = ms == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ms - m);   // nothing seen in this split
+  sf[t] = f;
+  l *= f;
+#pragma unroll
+  for (int i = 32; i > 0; i /= 2) l += __shfl_xor(l, i);
+  if ((t & 63) == 0) sl[wave] = l;
+  __syncthreads();
+  f4 o = zero4();
+#pragma unroll 8
+  for (int s = g; s < a.splits; s += GR)
+    o += sf[s] * *reinterpret_cast<const f4 *>(a.part + (s * nrow + row) * D + e * 4);
   so[g][e] = o;
-  if (e == 0) sl[g] = l;
   __syncthreads();
   if (g) return;
-  for (int i = 1; i < GR; ++i) {
-    o += so[i][e];
-    l += sl[i];
+  for (int i = 1; i < GR; ++i) o += so[i][e];
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) l += sl[w];
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+  store4(static_cast<T *>(a.out) + row * D + e * 4, o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+  if (e == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : kLn2 * (m + __builtin_amdgcn_logf(l));
+}
+
+// The same where a row has few splits: D / 4 threads a row add them one after the other (3 splits
+// of 64 x 32 x 16 rows: 46 us for the call, 60 with a workgroup a row).
+constexpr int FEW_SPLITS = 8;
+template <typename T, int D> __global__ __launch_bounds__(THR) void attn_join_few(AttnArgs a, size_t nrow) {
+  constexpr int L = D / 4, GR = THR / L;
+  const size_t row = (size_t)blockIdx.x * GR + threadIdx.x / L;
+  const int e = threadIdx.x % L;
+  if (row >= nrow || (a.cuq && row >= (size_t)max(a.cuq[a.n], 0) * a.hq)) return;
+  const float *ml = a.part + a.splits * nrow * D;
+  float m = -INFINITY, l = 0.f;
+  float ms[FEW_SPLITS], ls[FEW_SPLITS];
+  f4 p[FEW_SPLITS], o = zero4();
+#pragma unroll
+  for (int s = 0; s < FEW_SPLITS; ++s) {
+    const bool on = s < a.splits;
+    const size_t at = (on ? s : 0) * nrow + row;
+    ms[s] = on ? ml[at * 2] : -INFINITY;
+    ls[s] = on ? ml[at * 2 + 1] : 0.f;
+    p[s] = on ? *reinterpret_cast<const f4 *>(a.part + at * D + e * 4) : zero4();
+  }
+#pragma unroll
+  for (int s = 0; s < FEW_SPLITS; ++s) m = fmaxf(m, ms[s]);
+#pragma unroll
+  for (int s = 0; s < FEW_SPLITS; ++s) {
+    const float f = ms[s] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ms[s] - m);
+    l = fmaf(f, ls[s], l);
+    o += f * p[s];
   }
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
   store4(static_cast<T *>(a.out) + row * D + e * 4, o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
   if (e == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : kLn2 * (m + __builtin_amdgcn_logf(l));
 }
 
-// Whether a sequence's rows (the average's) fit a single wave.
-bool few_rows(const AttnArgs &a) { return (a.cuq ? (int64_t)a.Tq : (int64_t)a.n * a.Tq) * a.group <= (int64_t)FEW * a.n; }
+// Whether a sequence's rows (the average's) fit a single wave.  16 sequences of up to 16384 keys, 4
+// rows: 67 us this way, 75 by attn_fwd; 8 x 2048 keys, 12 heads of 64, 1 and 32 rows: 13.8 and 16.7
+// against 17.3 and 18.4.  64 rows, two waves that read the keys each: 119 us against 62 (16 x 8192).
+bool few_rows(const AttnArgs &a) { return query_tokens(a) * a.group <= (int64_t)FEW * a.n; }
 
 // Tiles of the packed row axis, at most; exact without cu.
 int64_t slots_of(const AttnArgs &a) {
@@ -426,15 +486,25 @@ int64_t slots_of(const AttnArgs &a) {
 }
 
 // Splits of the keys: only where the tiles leave compute units idle, and at least 256 keys (of
-// the average sequence) a split, so that joining stays cheap beside them.  Workgroups of few
-// rows are dealt twice over (5 of them stand on a compute unit): 16 sequences of up to 16 384
-// keys, 4 key heads of 128, took 98 us at 640 workgroups, 80 us at 1280 and 2560; of equal
-// lengths 117, 139 and 125 us.
+// the average sequence) a split, so that joining stays cheap beside them.
+// Few rows: one wave a workgroup, so 2560 of them (5 stand on a compute unit, dealt twice over:
+// 16 sequences of up to 16384 keys, 4 key heads of 128, took 98 us at 640 workgroups, 80 us at
+// 1280 and 2560), or, where the rows' partial sums would be over a sixteenth of the keys and values,
+// as many splits as that allows, down to 512 workgroups (32 rows on 16 x 8192 keys: 32 splits 77 us,
+// 8 splits 58 us; 8 rows on 8 x 2048 keys of 12 heads: 8 splits 16 us, 2 splits 29 us).  At most
+// 128: a single sequence of 65536 keys, 4 heads, took 35 us with 64 splits, 28 with 128 or 256.
+constexpr int MOST_SPLITS = 128;
 int splits_of(const AttnArgs &a) {
-  const int64_t blocks = slots_of(a) * a.hk, keys = a.cuq ? a.Tk / a.n : a.Tk;
-  int64_t s = (few_rows(a) ? 2560 : 512) / (blocks > 0 ? blocks : 1);
+  const bool few = few_rows(a);
+  const int64_t blocks = (few ? a.n : slots_of(a)) * a.hk, keys = a.cuq ? a.Tk / a.n : a.Tk;
+  int64_t s = (few ? 2560 : 512) / blocks;
+  if (few) {
+    const int64_t rows = query_tokens(a) * a.group / a.n, least = 512 / blocks;
+    const int64_t small = keys / (32 * (rows < 1 ? 1 : rows));
+    if (s > small) s = small > least ? small : least;
+  }
   if (s > keys / 256) s = keys / 256;
-  if (s > 64) s = 64;
+  if (s > MOST_SPLITS) s = MOST_SPLITS;
   return s < 1 ? 1 : (int)s;
 }
 
@@ -445,7 +515,11 @@ template <typename T, int D> hipError_t run(AttnArgs &a, hipStream_t s) {
   else hipLaunchKernelGGL((attn_fwd<T, D>), dim3((unsigned)blocks), dim3(THR), 0, s, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  hipLaunchKernelGGL((attn_join<T, D>), dim3((unsigned)nrow), dim3(THR), 0, s, a, nrow);
+  constexpr int GR = THR / (D / 4);
+  if (a.splits <= FEW_SPLITS)
+    hipLaunchKernelGGL((attn_join_few<T, D>), dim3((unsigned)((nrow + GR - 1) / GR)), dim3(THR), 0, s, a, nrow);
+  else
+    hipLaunchKernelGGL((attn_join<T, D>), dim3((unsigned)nrow), dim3(THR), 0, s, a, nrow);
   return hipGetLastError();
 }
 

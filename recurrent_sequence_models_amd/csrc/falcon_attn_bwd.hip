@@ -13,7 +13,12 @@
 // are right operands of dV^T = dO^T P and dK^T = Q^T dS; in the row kernel a wave owns 32
 // rows and forms the transposes.
 //
-// Bound: MFMA, 14 d flops executed per visible pair and head (10 d needed).
+// Bound: the matrix unit, 14 d flops executed per visible pair and head (10 d needed), and power
+// (operands of zeros: 20 % less time).  Measured, as useful flops (10 d), where an 8192^3 bf16
+// matrix product reaches 1.21 PFLOP/s:
+//   4 x 4096, 16 / 4 heads of 128, bf16: 0.96 ms, 715 TFLOP/s (keys 565 us, their sum 26, rows 354, D 16)
+//   8 x 2048, 12 / 12 heads of 64, bf16: 228 us, 565 TFLOP/s (keys 136 us, rows 88, D 7), 252 us in a long run
+//   2 x 2048, 12 / 12 heads of 64, fp32: 530 us, 61 TFLOP/s
 #include "attn_frag.h"
 #include "layer_kernels.h"
 #include "lane_ops.h"
@@ -23,8 +28,8 @@ namespace {
 
 constexpr int THR = 256, TR = 128;   // 4 waves of 32 rows (or keys)
 
-// Per row (query token and head): -D = -do . o, where the products do . v start from, and lse in base 2, +inf where the row sees
-// nothing, so that all its weights e^{s - lse} come out 0.
+// Per row (query token and head): -D = -do . o, where the products do . v start from, and lse in
+// base 2, +inf where the row sees nothing, so that all its weights e^{s - lse} come out 0.
 template <typename T, int D> __global__ __launch_bounds__(THR) void attn_delta(AttnArgs a, size_t nrow) {
   constexpr int E = 16 / (int)sizeof(T), L = D / E;
   const size_t row = ((size_t)blockIdx.x * THR + threadIdx.x) / L;
@@ -47,15 +52,16 @@ template <typename T, int D> __global__ __launch_bounds__(THR) void attn_delta(A
 }
 
 // ---- dk, dv ------------------------------------------------------------------
-// Rows of a tile: 64 (half the barriers and address work of 32), or 32 where two pairs of
-// tiles of 64 would leave one workgroup a compute unit (fp32 at d = 128).
+// Rows of a tile: 64 (half the barriers and address work of 32: 8 x 2048, 12 heads of 64, bf16,
+// 228 us for the whole backward against 237), or 32 where two pairs of tiles of 64 would leave one
+// workgroup a compute unit.
 template <typename T, int D> constexpr int TQ_OF = sizeof(T) * D > 128 ? 32 : 64;
-// Where rows are longer than 128 bytes, the values wait in LDS instead of registers: with both
-// operands and both sums in registers (bf16 at d = 128: 192 of the 256 that leave two waves a
-// SIMD) the compiler spills, and every reload waits for the copies in flight as well.
+// Where rows are longer than 128 bytes, the values wait in LDS instead of registers, and at bf16,
+// d = 128, 2 of a lane's 8 key fragments: with both operands and both sums in registers (192 of
+// the 256 that leave two waves a SIMD) the compiler spills, and every reload waits for the copies
+// in flight as well.  4 x 4096, 16 / 4 heads of 128: 0.96 ms, with the keys in registers 1.05, with
+// the values too 1.46; fp32 rows of 64, which fit either way, the same.  Two workgroups' LDS still fit.
 template <typename T, int D> constexpr bool V_IN_LDS = sizeof(T) * D > 128;
-// The same for 2 of a lane's 8 key fragments at bf16, d = 128: none is spilled then, and two
-// workgroups' LDS still fits a compute unit.
 template <typename T, int D> constexpr int KEYS_IN_LDS = sizeof(T) == 2 && D == 128 ? 2 : 0;
 
 template <typename T, int D>
@@ -69,7 +75,8 @@ __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_kv(
   __shared__ uint4 sq[2][Cp::CH], sg[2][Cp::CH], sv[VL ? CpV::CH : 1];
   __shared__ Frag<T> sk[DB > KR ? DB - KR : 1][THR];
   __shared__ __align__(16) float sL[2][64], sD[2][64];   // lse (base 2) and -D of the rows
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 31, h = lane >> 5;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = tid & 63, c = lane & 31, h = lane >> 5;
   unsigned id = blockIdx.x;
   const int head = id % (unsigned)a.hk;
   id /= (unsigned)a.hk;
@@ -141,7 +148,8 @@ __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_kv(
     if (wave < 2) {
       const int rel = min(rt + lane, rows - 1) - r0, tok = token(rel), hh = rel - tok * a.group;
       const int64_t at = row0 + (int64_t)tb * a.hq;
-      copy4_to_lds((wave ? a.delta : a.lse2) + at, (tok * (unsigned)a.hq + hh) * 4, lds_address(wave ? sD[buf] : sL[buf]));
+      copy4_to_lds((wave ? a.delta : a.lse2) + at, (tok * (unsigned)a.hq + hh) * 4,
+                   lds_address(wave ? sD[buf] : sL[buf]));
     }
   };
   f16v dk[CB], dv[CB];
@@ -257,7 +265,8 @@ __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_q(A
   constexpr int TN = 32, DB = D / 16, CB = D / 32;
   typedef Copy<T, D, TN> Cp;
   __shared__ uint4 sk[2][Cp::CH], sv[2][Cp::CH];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 31, h = lane >> 5;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = tid & 63, c = lane & 31, h = lane >> 5;
   const int head = blockIdx.x % (unsigned)a.hk, slot = blockIdx.x / (unsigned)a.hk;
   int n, tile;
   if (a.cuq) {
@@ -364,6 +373,8 @@ int64_t sum_blocks(const AttnArgs &a, int d) { return (key_tokens(a) * a.hk * (d
 // tile 128 of them, so at two workgroups a compute unit one round of workgroups would take
 // twice the average one; with 1024 of them the short ones fill in.  At least 512 rows (of the
 // average sequence) a split, so that writing and adding the parts stays small beside them.
+// 1 x 4096, 16 / 4 heads of 128: 0.30 ms, unsplit 0.83, for 512 workgroups 0.34, for 2048 0.34;
+// 4 x 4096: 0.96, 1.14, 1.14, 0.99; 8 x 2048, 12 / 12 heads of 64, is not split: 228 us, 293 in two.
 int bwd_splits(const AttnArgs &a) {
   const int64_t blocks = key_slots(a) * a.hk;
   const int64_t rows = (a.cuq ? a.Tq / a.n : a.Tq) * (int64_t)a.group;

@@ -51,8 +51,8 @@ int check_scan(const falcon_scan_shape_t *s, bool packed, bool step) {
   }
   // step and sequence numbers are ints, with a chunk or a stride over the sequences added
   if (s->seqlen > INT32_MAX - FALCON_SCAN_CHUNK || s->batch > (1 << 30)) return FALCON_ERR_UNSUPPORTED;
-  if (!falcon::scan_fits(s->dtype == FALCON_BF16, packed ? 1 : s->batch, s->seqlen, s->width)) return FALCON_ERR_UNSUPPORTED;
-  return FALCON_OK;
+  return falcon::scan_fits(s->dtype == FALCON_BF16, packed ? 1 : s->batch, s->seqlen, s->width) ? FALCON_OK
+                                                                                                : FALCON_ERR_UNSUPPORTED;
 }
 
 falcon::ScanArgs scan_args(const falcon_scan_shape_t *s, const int32_t *cu, const void *x, const void *g,

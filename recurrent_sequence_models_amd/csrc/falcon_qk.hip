@@ -14,6 +14,9 @@
 // read them there (per row they would cost more instructions than everything else).
 // pos * freq is reduced to a fraction of a turn in 64 bits: at position 10^6 a 32-bit
 // product would be off by 2^-5 radians.
+// Measured, where a plain copy moves 5.1 TB/s: forward, 16384 tokens, 12 + 12 heads of 64, bf16:
+// 18.8 us (101 MB at 5.4 TB/s); backward, 16387 tokens, 16 + 4 heads of 128, bf16 with fp32
+// incoming gradients: 68 us (336 MB at 4.9 TB/s) and 4.7 us to add the weights' gradients.
 #include "layer_kernels.h"
 #include "lane_ops.h"
 #include "mfma_frag.h"

@@ -28,8 +28,17 @@
 // infinite or NaN state of one sequence does not reach the next.  Products with decays
 // (>= 0) keep the sign, and joining maps sets it where either map's is.
 //
-// Bound: HBM.  Algorithmic bytes: forward 3, backward 5 elements of the input type per
-// step and channel.
+// Bound: HBM, with algorithmic bytes of 3 (forward) and 5 (backward) elements of the input type
+// per step and channel, and for bf16 the vector unit close behind.  Measured, where a plain
+// copy moves 5.1 TB/s:
+//   64 x 256 x 2048 bf16, one chunk a sequence: forward 39.8 us (5.1 TB/s), backward 75 us (4.5)
+//   65536 x 2048 bf16: forward 183 us (4.4 TB/s); 9001 x 2048 fp32, 13 sequences: 54.5 us (4.1)
+//   8 x 2048 x 768 bf16, mix: forward 19.5 us (3.9 TB/s), and 2 us to clear the workspace
+//   4 x 4096 x 768 bf16, mix: backward 35 us (3.6 TB/s; vector unit 83 % busy: the decay and
+//   1 - lam are formed again in the passes over a thread's steps, as the registers to keep them
+//   are the second workgroup's of a compute unit: 45 us then, or spilled for no gain)
+// A chunk waits for those before it: with few chunks a column (the 768-wide cases) that
+// latency is the rest.
 #include "layer_kernels.h"
 #include "mfma_frag.h"
 
@@ -286,7 +295,7 @@ __device__ __forceinline__ void step_of(const u4 &x, const u4 &g, float (&lam)[C
 // 512 threads: 64 groups of 8 lanes, each group 4 steps; a wave's 8 groups are neighbours
 // in time.  Groups, waves and chunks are scanned in turn, 8, 8 and at most 15 maps one
 // after the other (a single wave over all 64 groups took 0.8 us of every workgroup's time,
-// twice).
+// twice).  2 or 8 steps a thread, and chunks of 128, were no faster.
 constexpr int SEG = 4, GRPS = CHUNK / SEG, THR = GRPS * LPR, WAVES = THR / 64, GPW = GRPS / WAVES;
 
 template <int W> struct Maps {

@@ -247,3 +247,11 @@ def test_widest_strides(d):
     got = attention_bwd(wq, wk, wv, o, lse, wdo, cu_seqlens=cu, out=None)
     for n in ("dq", "dk", "dv"):
         assert torch.equal(want[n], got[n]), n
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("lens", [([1], [20000]), ([1, 1], [40000, 3]), ([1, 0, 2, 3], [9000, 7, 1, 20001]),
+                                  ([5] * 40, [1100] * 40)], ids=["one", "uneven", "mixed", "few"])
+def test_many_splits(dtype, lens):
+    """Up to 128 splits of the keys, most of them empty for the short sequences; and few, of many rows."""
+    run_case(dtype, *lens, 4, 1, 64, back=False)
