@@ -485,25 +485,31 @@ int64_t slots_of(const AttnArgs &a) {
   return ((int64_t)a.Tq * a.group + tm - 1) / tm * a.n;
 }
 
-// Splits of the keys: only where the tiles leave compute units idle, and at least 256 keys (of
-// the average sequence) a split, so that joining stays cheap beside them.
+// Splits of the keys: only where the tiles leave compute units idle, and at least so many keys (of
+// the average sequence) a split that joining stays cheap beside them.
 // Few rows: one wave a workgroup, so 2560 of them (5 stand on a compute unit, dealt twice over:
 // 16 sequences of up to 16384 keys, 4 key heads of 128, took 98 us at 640 workgroups, 80 us at
 // 1280 and 2560), or, where the rows' partial sums would be over a sixteenth of the keys and values,
 // as many splits as that allows, down to 512 workgroups (32 rows on 16 x 8192 keys: 32 splits 77 us,
 // 8 splits 58 us; 8 rows on 8 x 2048 keys of 12 heads: 8 splits 16 us, 2 splits 29 us).  At most
 // 128: a single sequence of 65536 keys, 4 heads, took 35 us with 64 splits, 28 with 128 or 256.
+// Other rows, bf16: a workgroup a compute unit and 512 keys (64 tokens on 4 x 8192 keys, 16 / 4 heads
+// of 128: 35 us, at two workgroups a unit 41, unsplit 149; 4 x 512, 12 / 12 of 64, where 256
+// keys a split would be two: 13 us unsplit, 20 split).  fp32, whose products take 8 times as long
+// beside the same partial sums: two a unit and 256 keys (1 x 2048, 16 / 4 of 128: 187 us, at one
+// a unit 311; 1 x 1024, 12 / 12 of 64: 40 us, with 512 keys 48, with 1024 80).
 constexpr int MOST_SPLITS = 128;
-int splits_of(const AttnArgs &a) {
+int splits_of(bool bf16, const AttnArgs &a) {
   const bool few = few_rows(a);
   const int64_t blocks = (few ? a.n : slots_of(a)) * a.hk, keys = a.cuq ? a.Tk / a.n : a.Tk;
-  int64_t s = (few ? 2560 : 512) / blocks;
+  int64_t s = few ? 2560 / blocks : bf16 ? (256 + blocks - 1) / blocks : 512 / blocks;
   if (few) {
     const int64_t rows = query_tokens(a) * a.group / a.n, least = 512 / blocks;
     const int64_t small = keys / (32 * (rows < 1 ? 1 : rows));
     if (s > small) s = small > least ? small : least;
   }
-  if (s > keys / 256) s = keys / 256;
+  const int64_t most = keys / (few || !bf16 ? 256 : 512);
+  if (s > most) s = most;
   if (s > MOST_SPLITS) s = MOST_SPLITS;
   return s < 1 ? 1 : (int)s;
 }
@@ -525,17 +531,17 @@ template <typename T, int D> hipError_t run(AttnArgs &a, hipStream_t s) {
 
 }  // namespace
 
-bool attn_fwd_fits(const AttnArgs &a) {   // the join too: splits only come with few rows
-  return grid_fits(slots_of(a) * a.hk * splits_of(a), few_rows(a) ? 64 : THR);
+bool attn_fwd_fits(bool bf16, const AttnArgs &a) {   // the join too: splits only come with few rows
+  return grid_fits(slots_of(a) * a.hk * splits_of(bf16, a), few_rows(a) ? 64 : THR);
 }
 
-size_t attn_fwd_workspace(int d, const AttnArgs &a) {
-  const int s = splits_of(a);
+size_t attn_fwd_workspace(bool bf16, int d, const AttnArgs &a) {
+  const int s = splits_of(bf16, a);
   return s == 1 ? 0 : (size_t)s * query_tokens(a) * a.hq * (d + 2) * sizeof(float);
 }
 
 hipError_t launch_attn_fwd(bool bf16, int d, AttnArgs a, void *ws, hipStream_t s) {
-  a.splits = splits_of(a);
+  a.splits = splits_of(bf16, a);
   a.part = static_cast<float *>(ws);
 #define FALCON_ATTN(D_) \
   if (d == D_) return bf16 ? run<__bf16, D_>(a, s) : run<float, D_>(a, s)

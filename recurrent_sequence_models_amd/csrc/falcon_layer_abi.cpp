@@ -297,7 +297,7 @@ int check_attn(const falcon_attn_shape_t *s, bool packed) {
 // Of one direction: its launches too.
 int check_attn_fwd(const falcon_attn_shape_t *s, bool packed) {
   FALCON_TRY(check_attn(s, packed));
-  return falcon::attn_fwd_fits(size_args(s, packed)) ? FALCON_OK : FALCON_ERR_UNSUPPORTED;
+  return falcon::attn_fwd_fits(s->dtype == FALCON_BF16, size_args(s, packed)) ? FALCON_OK : FALCON_ERR_UNSUPPORTED;
 }
 int check_attn_bwd(const falcon_attn_shape_t *s, bool packed) {
   FALCON_TRY(check_attn(s, packed));
@@ -329,7 +329,7 @@ extern "C" {
 
 size_t falcon_attn_fwd_workspace(const falcon_attn_shape_t *s, int packed) {
   if (check_attn_fwd(s, packed != 0) != FALCON_OK) return 0;
-  return falcon::attn_fwd_workspace(s->d, size_args(s, packed != 0));
+  return falcon::attn_fwd_workspace(s->dtype == FALCON_BF16, s->d, size_args(s, packed != 0));
 }
 
 int falcon_attn_fwd(const falcon_attn_shape_t *s, const int32_t *cu_q, const int32_t *cu_k, falcon_heads_t q,

@@ -72,9 +72,9 @@ struct AttnArgs {
   int splits;                    // filled at launch
   float scale;
 };
-bool attn_fwd_fits(const AttnArgs &a);                      // within a launch
+bool attn_fwd_fits(bool bf16, const AttnArgs &a);           // within a launch
 bool attn_bwd_fits(bool bf16, int d, const AttnArgs &a);
-size_t attn_fwd_workspace(int d, const AttnArgs &a);
+size_t attn_fwd_workspace(bool bf16, int d, const AttnArgs &a);
 hipError_t launch_attn_fwd(bool bf16, int d, AttnArgs a, void *ws, hipStream_t s);
 size_t attn_bwd_workspace(int d, const AttnArgs &a);
 hipError_t launch_attn_bwd(bool bf16, int d, AttnArgs a, void *ws, hipStream_t s);
