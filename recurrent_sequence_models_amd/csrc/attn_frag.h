@@ -66,6 +66,21 @@ __device__ __forceinline__ Frag<float> global_frag(const float *row, int b, int 
   return {*reinterpret_cast<const f4 *>(row + 16 * b + 8 * h), *reinterpret_cast<const f4 *>(row + 16 * b + 8 * h + 4)};
 }
 
+__device__ __forceinline__ float dot(const Frag<__bf16> &a, const Frag<__bf16> &b) {
+  float s = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s = fmaf((float)a.v[j], (float)b.v[j], s);
+  return s;
+}
+__device__ __forceinline__ float dot(const Frag<float> &a, const Frag<float> &b) {
+  float s = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) s = fmaf(a.lo[j], b.lo[j], s);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) s = fmaf(a.hi[j], b.hi[j], s);
+  return s;
+}
+
 // Makes a fragment's loads arrive here.  The compiler waits for them at their first use, and where
 // that is in a loop it waits there every time, for the loop's copies (below) as well, which it
 // does not know of: the next tile's copies would be awaited as soon as they are issued.

@@ -3,8 +3,7 @@
 // With P = e^{s - lse} (recomputed), D_i = do_i . o_i:
 //   dv_j = sum_i P_ij do_i,  dS_ij = P_ij (do_i . v_j - D_i),
 //   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i  (over the group's heads).
-// Three kernels: the row sums D; one over key tiles for dk and dv; one over row tiles for
-// dq.  The scores and do . v are formed twice (7 products of the size of the scores where
+// Two kernels: one over row tiles for D and dq, one over key tiles for dk and dv.  The scores and do . v are formed twice (7 products of the size of the scores where
 // 5 would do), and in return every sum is one wave's own, in a fixed order: no atomics, no
 // fp32 copy of dq in memory, and equal inputs give equal bits.
 //
@@ -16,9 +15,9 @@
 // Bound: the matrix unit, 14 d flops executed per visible pair and head (10 d needed), and power
 // (operands of zeros: 20 % less time).  Measured, as useful flops (10 d), where an 8192^3 bf16
 // matrix product reaches 1.21 PFLOP/s:
-//   4 x 4096, 16 / 4 heads of 128, bf16: 0.96 ms, 715 TFLOP/s (keys 565 us, their sum 26, rows 354, D 16)
-//   8 x 2048, 12 / 12 heads of 64, bf16: 228 us, 565 TFLOP/s (keys 136 us, rows 88, D 7), 252 us in a long run
-//   2 x 2048, 12 / 12 heads of 64, fp32: 530 us, 61 TFLOP/s
+//   4 x 4096, 16 / 4 heads of 128, bf16: 0.95 ms, 725 TFLOP/s (rows 360 us, keys 565, their sum 26)
+//   8 x 2048, 12 / 12 heads of 64, bf16: 222 us, 580 TFLOP/s (rows 89 us, keys 136), 246 us in a long run
+//   2 x 2048, 12 / 12 heads of 64, fp32: 525 us, 61 TFLOP/s
 #include "attn_frag.h"
 #include "layer_kernels.h"
 #include "lane_ops.h"
@@ -28,27 +27,117 @@ namespace {
 
 constexpr int THR = 256, TR = 128;   // 4 waves of 32 rows (or keys)
 
-// Per row (query token and head): -D = -do . o, where the products do . v start from, and lse in
-// base 2, +inf where the row sees nothing, so that all its weights e^{s - lse} come out 0.
-template <typename T, int D> __global__ __launch_bounds__(THR) void attn_delta(AttnArgs a, size_t nrow) {
-  constexpr int E = 16 / (int)sizeof(T), L = D / E;
-  const size_t row = ((size_t)blockIdx.x * THR + threadIdx.x) / L;
-  const int e = (threadIdx.x % L) * E;
-  float s = 0.f;
-  if (row < nrow) {
-    const size_t tok = row / a.hq, hq = row - tok * a.hq;
-    const T *o = static_cast<const T *>(a.o) + tok * a.ldo + hq * D + e;
-    const T *g = static_cast<const T *>(a.d_o) + tok * a.lddo + hq * D + e;
+// ---- dq ----------------------------------------------------------------------
+template <typename T, int D>
+__global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_q(AttnArgs a) {
+  typedef Tile<T, D> Ti;
+  constexpr int TN = 32, DB = D / 16, CB = D / 32;
+  typedef Copy<T, D, TN> Cp;
+  __shared__ uint4 sk[2][Cp::CH], sv[2][Cp::CH];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = tid & 63, c = lane & 31, h = lane >> 5;
+  const int head = blockIdx.x % (unsigned)a.hk, slot = blockIdx.x / (unsigned)a.hk;
+  int n, tile;
+  if (a.cuq) {
+    const Slot s = find_slot(a.cuq, a.n, slot, a.group, TR);
+    n = s.n; tile = s.tile;
+  } else {
+    n = slot % (unsigned)a.n; tile = slot / (unsigned)a.n;
+  }
+  const Seq q = seq_of(a, n);
+  const int rows = q.Lq * a.group, tiles = (rows + TR - 1) / TR;
+  if ((unsigned)tile >= (unsigned)tiles) return;
+  tile = tiles - 1 - tile;
+  const int off = q.Lk - q.Lq, r0 = tile * TR + wave * 32, r = min(r0 + c, rows - 1);
+  const bool on = r0 + c < rows;
+  const int tok = r / (unsigned)a.group, hq = head * a.group + (r - tok * a.group);
+  const int lim = tok + off;
+  const int first_lim = (int)((unsigned)min(r0, rows - 1) / (unsigned)a.group) + off;
+  const int wave_lim = (int)((unsigned)min(r0 + 31, rows - 1) / (unsigned)a.group) + off;
+  const int last_lim = (int)((unsigned)min(tile * TR + TR - 1, rows - 1) / (unsigned)a.group) + off;
+  const int keys = max(min(q.Lk, last_lim + 1), 0), ktiles = (keys + TN - 1) / TN;
+
+  const T *qp = static_cast<const T *>(a.q) + (int64_t)(q.q0 + tok) * a.ldq + hq * D;
+  const T *gp = static_cast<const T *>(a.d_o) + (int64_t)(q.q0 + tok) * a.lddo + hq * D;
+  Frag<T> qf[DB], gf[DB];
 #pragma unroll
-    for (int i = 0; i < E; ++i) s = fmaf((float)o[i], (float)g[i], s);
+  for (int b = 0; b < DB; ++b) { qf[b] = global_frag(qp, b, h); gf[b] = global_frag(gp, b, h); }
+  // For these rows and, through memory, the key kernel: -D = -do . o, where the products do . v
+  // start from, and lse in base 2, +inf where the row sees nothing, so that all its weights
+  // e^{s - lse} come out 0.
+  const int64_t at = (int64_t)(q.q0 + tok) * a.hq + hq;
+  const T *op = static_cast<const T *>(a.o) + at * D;
+  float Dr = 0.f;
+#pragma unroll
+  for (int b = 0; b < DB; ++b) Dr -= dot(global_frag(op, b, h), gf[b]);
+  Dr = add_xor32(Dr);
+  const float lse = a.lse_in[at], L = lse == -INFINITY ? INFINITY : lse * kLog2e;
+  if (on && h == 0) {
+    a.delta[at] = Dr;
+    a.lse2[at] = L;
   }
-  s = lane_sum<(L < 16 ? L : 16)>(s);
-  if constexpr (L == 32) s = add_xor16(s);
-  if (row < nrow && e == 0) {
-    const float lse = a.lse_in[row];
-    a.delta[row] = -s;
-    a.lse2[row] = lse == -INFINITY ? INFINITY : lse * kLog2e;
+
+  const T *kg = static_cast<const T *>(a.k) + (int64_t)q.k0 * a.ldk + head * D;
+  const T *vg = static_cast<const T *>(a.v) + (int64_t)q.k0 * a.ldv + head * D;
+  const unsigned kstep = (unsigned)a.ldk * sizeof(T), vstep = (unsigned)a.ldv * sizeof(T);
+  auto copy = [&](int kt, int buf) {            // rows past the sequence's keys repeat its last one
+    const T *kp = kg + (int64_t)kt * TN * a.ldk, *vp = vg + (int64_t)kt * TN * a.ldv;
+    const int last = q.Lk - 1 - kt * TN;
+#pragma unroll
+    for (int i = 0; i < Cp::PER; ++i) {
+      if (!Cp::has(i, wave)) continue;
+      const int row = min(Cp::row(i, tid), last);
+      copy_to_lds(kp, row * kstep + Cp::byte(i, tid), Cp::to(sk[buf], i, wave));
+      copy_to_lds(vp, row * vstep + Cp::byte(i, tid), Cp::to(sv[buf], i, wave));
+    }
+  };
+  f16v dq[CB];
+#pragma unroll
+  for (int b = 0; b < CB; ++b) dq[b] = zero16();
+  const float sc = a.scale * kLog2e;
+  if (ktiles > 0) copy(0, 0);
+  copies_done();
+#pragma unroll
+  for (int b = 0; b < DB; ++b) { arrived(qf[b]); arrived(gf[b]); }
+  __syncthreads();
+  for (int kt = 0; kt < ktiles; ++kt) {
+    const int buf = kt & 1;
+    if (kt + 1 < ktiles) copy(kt + 1, buf ^ 1);            // its last readers are behind the barrier
+    if (kt * TN <= wave_lim) {
+      f16v s = zero16(), g;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) g[i] = Dr;
+#pragma unroll
+      for (int b = 0; b < DB; ++b) mma(s, Ti::rows(sk[buf], 0, b, lane), qf[b]);
+#pragma unroll
+      for (int b = 0; b < DB; ++b) mma(g, Ti::rows(sv[buf], 0, b, lane), gf[b]);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], sc, -L));
+      if (kt * TN + TN - 1 > first_lim) {
+        const int left = lim - kt * TN - 4 * h;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = 8 * (i / 4) + (i & 3) > left ? 0.f : s[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i] *= g[i];
+#pragma unroll
+      for (int b16 = 0; b16 < 2; ++b16) {
+        const Frag<T> sf = result_frag<T>(s, b16);
+#pragma unroll
+        for (int b = 0; b < CB; ++b) mma(dq[b], Ti::cols(sk[buf], b16 * 16, b * 32, lane), sf);
+      }
+    }
+    copies_done();
+    __syncthreads();
   }
+  if (!on) return;
+  T *pq = static_cast<T *>(a.dq) + (int64_t)(q.q0 + tok) * a.lddq + hq * D;
+#pragma unroll
+  for (int b = 0; b < CB; ++b)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4)
+      store4(pq + b * 32 + 2 * i + 4 * h, dq[b][i] * a.scale, dq[b][i + 1] * a.scale, dq[b][i + 2] * a.scale,
+             dq[b][i + 3] * a.scale);
 }
 
 // ---- dk, dv ------------------------------------------------------------------
@@ -258,115 +347,12 @@ template <typename T, int D> __global__ __launch_bounds__(THR) void attn_bwd_sum
   store4(static_cast<T *>(a.dv) + (int64_t)tok * a.lddv + head * D + e, dv[0], dv[1], dv[2], dv[3]);
 }
 
-// ---- dq ----------------------------------------------------------------------
-template <typename T, int D>
-__global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_q(AttnArgs a) {
-  typedef Tile<T, D> Ti;
-  constexpr int TN = 32, DB = D / 16, CB = D / 32;
-  typedef Copy<T, D, TN> Cp;
-  __shared__ uint4 sk[2][Cp::CH], sv[2][Cp::CH];
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int lane = tid & 63, c = lane & 31, h = lane >> 5;
-  const int head = blockIdx.x % (unsigned)a.hk, slot = blockIdx.x / (unsigned)a.hk;
-  int n, tile;
-  if (a.cuq) {
-    const Slot s = find_slot(a.cuq, a.n, slot, a.group, TR);
-    n = s.n; tile = s.tile;
-  } else {
-    n = slot % (unsigned)a.n; tile = slot / (unsigned)a.n;
-  }
-  const Seq q = seq_of(a, n);
-  const int rows = q.Lq * a.group, tiles = (rows + TR - 1) / TR;
-  if ((unsigned)tile >= (unsigned)tiles) return;
-  tile = tiles - 1 - tile;
-  const int off = q.Lk - q.Lq, r0 = tile * TR + wave * 32, r = min(r0 + c, rows - 1);
-  const bool on = r0 + c < rows;
-  const int tok = r / (unsigned)a.group, hq = head * a.group + (r - tok * a.group);
-  const int lim = tok + off;
-  const int first_lim = (int)((unsigned)min(r0, rows - 1) / (unsigned)a.group) + off;
-  const int wave_lim = (int)((unsigned)min(r0 + 31, rows - 1) / (unsigned)a.group) + off;
-  const int last_lim = (int)((unsigned)min(tile * TR + TR - 1, rows - 1) / (unsigned)a.group) + off;
-  const int keys = max(min(q.Lk, last_lim + 1), 0), ktiles = (keys + TN - 1) / TN;
-
-  const T *qp = static_cast<const T *>(a.q) + (int64_t)(q.q0 + tok) * a.ldq + hq * D;
-  const T *gp = static_cast<const T *>(a.d_o) + (int64_t)(q.q0 + tok) * a.lddo + hq * D;
-  Frag<T> qf[DB], gf[DB];
-#pragma unroll
-  for (int b = 0; b < DB; ++b) { qf[b] = global_frag(qp, b, h); gf[b] = global_frag(gp, b, h); }
-  const int64_t at = (int64_t)(q.q0 + tok) * a.hq + hq;
-  const float L = a.lse2[at], Dr = a.delta[at];
-
-  const T *kg = static_cast<const T *>(a.k) + (int64_t)q.k0 * a.ldk + head * D;
-  const T *vg = static_cast<const T *>(a.v) + (int64_t)q.k0 * a.ldv + head * D;
-  const unsigned kstep = (unsigned)a.ldk * sizeof(T), vstep = (unsigned)a.ldv * sizeof(T);
-  auto copy = [&](int kt, int buf) {            // rows past the sequence's keys repeat its last one
-    const T *kp = kg + (int64_t)kt * TN * a.ldk, *vp = vg + (int64_t)kt * TN * a.ldv;
-    const int last = q.Lk - 1 - kt * TN;
-#pragma unroll
-    for (int i = 0; i < Cp::PER; ++i) {
-      if (!Cp::has(i, wave)) continue;
-      const int row = min(Cp::row(i, tid), last);
-      copy_to_lds(kp, row * kstep + Cp::byte(i, tid), Cp::to(sk[buf], i, wave));
-      copy_to_lds(vp, row * vstep + Cp::byte(i, tid), Cp::to(sv[buf], i, wave));
-    }
-  };
-  f16v dq[CB];
-#pragma unroll
-  for (int b = 0; b < CB; ++b) dq[b] = zero16();
-  const float sc = a.scale * kLog2e;
-  if (ktiles > 0) copy(0, 0);
-  copies_done();
-#pragma unroll
-  for (int b = 0; b < DB; ++b) { arrived(qf[b]); arrived(gf[b]); }
-  __syncthreads();
-  for (int kt = 0; kt < ktiles; ++kt) {
-    const int buf = kt & 1;
-    if (kt + 1 < ktiles) copy(kt + 1, buf ^ 1);            // its last readers are behind the barrier
-    if (kt * TN <= wave_lim) {
-      f16v s = zero16(), g;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) g[i] = Dr;
-#pragma unroll
-      for (int b = 0; b < DB; ++b) mma(s, Ti::rows(sk[buf], 0, b, lane), qf[b]);
-#pragma unroll
-      for (int b = 0; b < DB; ++b) mma(g, Ti::rows(sv[buf], 0, b, lane), gf[b]);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], sc, -L));
-      if (kt * TN + TN - 1 > first_lim) {
-        const int left = lim - kt * TN - 4 * h;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = 8 * (i / 4) + (i & 3) > left ? 0.f : s[i];
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) s[i] *= g[i];
-#pragma unroll
-      for (int b16 = 0; b16 < 2; ++b16) {
-        const Frag<T> sf = result_frag<T>(s, b16);
-#pragma unroll
-        for (int b = 0; b < CB; ++b) mma(dq[b], Ti::cols(sk[buf], b16 * 16, b * 32, lane), sf);
-      }
-    }
-    copies_done();
-    __syncthreads();
-  }
-  if (!on) return;
-  T *pq = static_cast<T *>(a.dq) + (int64_t)(q.q0 + tok) * a.lddq + hq * D;
-#pragma unroll
-  for (int b = 0; b < CB; ++b)
-#pragma unroll
-    for (int i = 0; i < 16; i += 4)
-      store4(pq + b * 32 + 2 * i + 4 * h, dq[b][i] * a.scale, dq[b][i + 1] * a.scale, dq[b][i + 2] * a.scale,
-             dq[b][i + 3] * a.scale);
-}
-
 int64_t key_slots(const AttnArgs &a) {
   return a.cuk ? (int64_t)a.Tk / TR + a.n : ((int64_t)a.Tk + TR - 1) / TR * a.n;
 }
 int64_t row_slots(const AttnArgs &a) {
   return a.cuq ? (int64_t)a.Tq * a.group / TR + a.n : ((int64_t)a.Tq * a.group + TR - 1) / TR * a.n;
 }
-// Workgroups of the two kernels over all rows or keys.
-int64_t delta_blocks(const AttnArgs &a, int L) { return (query_tokens(a) * a.hq * L + THR - 1) / THR; }
 int64_t sum_blocks(const AttnArgs &a, int d) { return (key_tokens(a) * a.hk * (d / 4) + THR - 1) / THR; }
 
 // Splits of the rows between workgroups of one key tile.  Tile 0 meets every row and the last
@@ -385,19 +371,15 @@ int bwd_splits(const AttnArgs &a) {
 }
 
 template <typename T, int D> hipError_t run(AttnArgs &a, hipStream_t s) {
-  const size_t nrow = (size_t)query_tokens(a) * a.hq, nkey = (size_t)key_tokens(a) * a.hk;
-  const unsigned nd = (unsigned)delta_blocks(a, D * (int)sizeof(T) / 16), ns = (unsigned)sum_blocks(a, D);
+  const size_t nkey = (size_t)key_tokens(a) * a.hk;
   const unsigned nk = (unsigned)(key_slots(a) * a.hk * a.splits), nq = (unsigned)(row_slots(a) * a.hk);
-  hipLaunchKernelGGL((attn_delta<T, D>), dim3(nd), dim3(THR), 0, s, a, nrow);
+  hipLaunchKernelGGL((attn_bwd_q<T, D>), dim3(nq), dim3(THR), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((attn_bwd_kv<T, D>), dim3(nk), dim3(THR), 0, s, a);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  if (a.splits > 1) {
-    hipLaunchKernelGGL((attn_bwd_sum<T, D>), dim3(ns), dim3(THR), 0, s, a, nkey);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
-  hipLaunchKernelGGL((attn_bwd_q<T, D>), dim3(nq), dim3(THR), 0, s, a);
+  e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  hipLaunchKernelGGL((attn_bwd_sum<T, D>), dim3((unsigned)sum_blocks(a, D)), dim3(THR), 0, s, a, nkey);
   return hipGetLastError();
 }
 
@@ -406,10 +388,10 @@ size_t row_bytes(const AttnArgs &a) { return ((size_t)query_tokens(a) * a.hq * s
 
 }  // namespace
 
-bool attn_bwd_fits(bool bf16, int d, const AttnArgs &a) {
+bool attn_bwd_fits(int d, const AttnArgs &a) {
   const int splits = bwd_splits(a);
-  return grid_fits(delta_blocks(a, d * (bf16 ? 2 : 4) / 16), THR) && grid_fits(key_slots(a) * a.hk * splits, THR) &&
-         (splits == 1 || grid_fits(sum_blocks(a, d), THR)) && grid_fits(row_slots(a) * a.hk, THR);
+  return grid_fits(row_slots(a) * a.hk, THR) && grid_fits(key_slots(a) * a.hk * splits, THR) &&
+         (splits == 1 || grid_fits(sum_blocks(a, d), THR));
 }
 
 size_t attn_bwd_workspace(int d, const AttnArgs &a) {

@@ -301,7 +301,7 @@ int check_attn_fwd(const falcon_attn_shape_t *s, bool packed) {
 }
 int check_attn_bwd(const falcon_attn_shape_t *s, bool packed) {
   FALCON_TRY(check_attn(s, packed));
-  return falcon::attn_bwd_fits(s->dtype == FALCON_BF16, s->d, size_args(s, packed)) ? FALCON_OK : FALCON_ERR_UNSUPPORTED;
+  return falcon::attn_bwd_fits(s->d, size_args(s, packed)) ? FALCON_OK : FALCON_ERR_UNSUPPORTED;
 }
 
 constexpr int64_t MOST_STEP = 1 << 25;   // bytes between two tokens
@@ -371,7 +371,6 @@ int falcon_attn_bwd(const falcon_attn_shape_t *s, const int32_t *cu_q, const int
   a.q = q.data; a.k = k.data; a.v = v.data;
   a.ldq = q.token_stride; a.ldk = k.token_stride; a.ldv = v.token_stride;
   a.o = o;
-  a.ldo = (int64_t)s->heads_q * s->d;
   a.lse_in = lse;
   a.d_o = d_o.data;
   a.lddo = d_o.token_stride;

@@ -65,15 +65,15 @@ struct AttnArgs {
   float *lse;                    // [query tokens, hq]
   const int *cuq, *cuk;          // [n + 1] or null
   float *part;                   // workspace: partial results of splits
-  float *delta, *lse2;           // backward workspace: row sums of do o, lse in base 2
-  int64_t ldq, ldk, ldv, ldo, lddo, lddq, lddk, lddv;
+  float *delta, *lse2;           // backward workspace: -do . o and lse in base 2 of every row
+  int64_t ldq, ldk, ldv, lddo, lddq, lddk, lddv;
   int n, Tq, Tk;                 // packed: Tq, Tk are the totals
   int hq, hk, group;             // group = hq / hk
   int splits;                    // filled at launch
   float scale;
 };
 bool attn_fwd_fits(bool bf16, const AttnArgs &a);           // within a launch
-bool attn_bwd_fits(bool bf16, int d, const AttnArgs &a);
+bool attn_bwd_fits(int d, const AttnArgs &a);
 size_t attn_fwd_workspace(bool bf16, int d, const AttnArgs &a);
 hipError_t launch_attn_fwd(bool bf16, int d, AttnArgs a, void *ws, hipStream_t s);
 size_t attn_bwd_workspace(int d, const AttnArgs &a);
