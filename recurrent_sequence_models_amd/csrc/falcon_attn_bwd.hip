@@ -3,9 +3,10 @@
 // With P = e^{s - lse} (recomputed), D_i = do_i . o_i:
 //   dv_j = sum_i P_ij do_i,  dS_ij = P_ij (do_i . v_j - D_i),
 //   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i  (over the group's heads).
-// Two kernels: one over row tiles for D and dq, one over key tiles for dk and dv.  The scores and do . v are formed twice (7 products of the size of the scores where
-// 5 would do), and in return every sum is one wave's own, in a fixed order: no atomics, no
-// fp32 copy of dq in memory, and equal inputs give equal bits.
+// Two kernels: one over row tiles for D and dq, one over key tiles for dk and dv.  The scores
+// and do . v are formed twice (7 products of the size of the scores where 5 would do), and in
+// return every sum is one wave's own, in a fixed order: no atomics, no fp32 copy of dq in
+// memory, and equal inputs give equal bits.
 //
 // Rows are (token, head of the group) pairs as in the forward pass.  In the key kernel a
 // wave owns 32 keys with their k and v in registers and forms S = Q K^T, so that P and dS
@@ -15,9 +16,9 @@
 // Bound: the matrix unit, 14 d flops executed per visible pair and head (10 d needed), and power
 // (operands of zeros: 20 % less time).  Measured, as useful flops (10 d), where an 8192^3 bf16
 // matrix product reaches 1.21 PFLOP/s:
-//   4 x 4096, 16 / 4 heads of 128, bf16: 0.95 ms, 725 TFLOP/s (rows 360 us, keys 565, their sum 26)
-//   8 x 2048, 12 / 12 heads of 64, bf16: 222 us, 580 TFLOP/s (rows 89 us, keys 136), 246 us in a long run
-//   2 x 2048, 12 / 12 heads of 64, fp32: 525 us, 61 TFLOP/s
+//   4 x 4096, 16 / 4 heads of 128, bf16: 0.94 ms, 730 TFLOP/s (rows 350 us, keys 565, their sum 26)
+//   8 x 2048, 12 / 12 heads of 64, bf16: 218 us, 590 TFLOP/s (rows 85 us, keys 136), 244 us in a long run
+//   2 x 2048, 12 / 12 heads of 64, fp32: 521 us, 62 TFLOP/s
 #include "attn_frag.h"
 #include "layer_kernels.h"
 #include "lane_ops.h"
@@ -31,7 +32,7 @@ constexpr int THR = 256, TR = 128;   // 4 waves of 32 rows (or keys)
 template <typename T, int D>
 __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_q(AttnArgs a) {
   typedef Tile<T, D> Ti;
-  constexpr int TN = 32, DB = D / 16, CB = D / 32;
+  constexpr int TN = 64, DB = D / 16, CB = D / 32;   // keys of a tile (32: 1 to 2 % more time)
   typedef Copy<T, D, TN> Cp;
   __shared__ uint4 sk[2][Cp::CH], sv[2][Cp::CH];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -103,18 +104,21 @@ __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_q(A
   for (int kt = 0; kt < ktiles; ++kt) {
     const int buf = kt & 1;
     if (kt + 1 < ktiles) copy(kt + 1, buf ^ 1);            // its last readers are behind the barrier
-    if (kt * TN <= wave_lim) {
+#pragma unroll
+    for (int kb = 0; kb < TN; kb += 32) {
+      const int key0 = kt * TN + kb;
+      if (key0 > wave_lim) break;               // no row of this wave sees the keys from here on
       f16v s = zero16(), g;
 #pragma unroll
       for (int i = 0; i < 16; ++i) g[i] = Dr;
 #pragma unroll
-      for (int b = 0; b < DB; ++b) mma(s, Ti::rows(sk[buf], 0, b, lane), qf[b]);
+      for (int b = 0; b < DB; ++b) mma(s, Ti::rows(sk[buf], kb, b, lane), qf[b]);
 #pragma unroll
-      for (int b = 0; b < DB; ++b) mma(g, Ti::rows(sv[buf], 0, b, lane), gf[b]);
+      for (int b = 0; b < DB; ++b) mma(g, Ti::rows(sv[buf], kb, b, lane), gf[b]);
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], sc, -L));
-      if (kt * TN + TN - 1 > first_lim) {
-        const int left = lim - kt * TN - 4 * h;
+      if (key0 + 31 > first_lim) {
+        const int left = lim - key0 - 4 * h;
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[i] = 8 * (i / 4) + (i & 3) > left ? 0.f : s[i];
       }
@@ -124,7 +128,7 @@ __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_q(A
       for (int b16 = 0; b16 < 2; ++b16) {
         const Frag<T> sf = result_frag<T>(s, b16);
 #pragma unroll
-        for (int b = 0; b < CB; ++b) mma(dq[b], Ti::cols(sk[buf], b16 * 16, b * 32, lane), sf);
+        for (int b = 0; b < CB; ++b) mma(dq[b], Ti::cols(sk[buf], kb + b16 * 16, b * 32, lane), sf);
       }
     }
     copies_done();
