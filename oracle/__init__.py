@@ -26,6 +26,10 @@ forms, reductions and invariants).  The absolute values of the constants
 eps_phi, eps_eta, the zero first key of a fresh sequence and the window divisor
 at the start of a sequence are readings, not values the pages fix: for them the
 parity is unpinned by the pages and fixed only by the readings.
+
+:mod:`oracle.layer_oracle` (``oracle.layer``) holds the operators around the mixer, from
+their formulas: the gated linear recurrence, the query / key norm with rotary
+positions and causal attention, pinned in ``tests/test_layer_oracle_pins.py``.
 """
 
 from .falcon_oracle import (VARIANTS, recurrent, masked_parallel, chunked,
