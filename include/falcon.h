@@ -464,7 +464,8 @@ int falcon_qk_norm_rope_bwd(const falcon_qk_shape_t *shape, falcon_heads_t q, fa
  * The queries of a sequence are the last Lq of its Lk tokens: query i sees keys
  * j <= i + Lk - Lq.  Query head h reads key head h / (heads_q / heads_k).
  *   o_i = sum_j softmax_j(scale q_i . k_j) v_j,  lse_i = ln sum_j e^{scale q_i . k_j}
- * A query that sees no key (Lq > Lk) has o = 0, lse = -inf and no gradients.
+ * A query that sees no key (Lq > Lk), or whose scores are all -inf, has o = 0,
+ * lse = -inf and no gradients.
  * Infinite or NaN keys and values do not reach o and lse of the queries that do
  * not see them; any gradient of a sequence that holds some may be NaN. */
 typedef struct {

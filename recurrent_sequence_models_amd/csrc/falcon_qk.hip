@@ -25,8 +25,11 @@ namespace falcon {
 namespace {
 
 constexpr int THR = 256;
-constexpr int FWD_BLOCKS = 1 << 18;   // workgroups of the forward pass, at most: a launch holds less than 2^32 threads
-constexpr int BWD_BLOCKS = 1024;      // of the backward pass: four a compute unit, each with its sum for the weights
+// workgroups of the forward pass, at most (a launch holds less than 2^32 threads), and
+constexpr int FWD_BLOCKS = 1 << 18;
+// of the backward pass: four a compute unit, each with its sum for the weights (16387 tokens, 16 + 4
+// heads of 128: 73 us; 768 workgroups 86, 2048 77)
+constexpr int BWD_BLOCKS = 1024;
 
 template <typename T> constexpr int EPL = 16 / (int)sizeof(T);   // entries per lane
 
