@@ -34,9 +34,9 @@
 //   64 x 256 x 2048 bf16, one chunk a sequence: forward 39.8 us (5.1 TB/s), backward 75 us (4.5)
 //   65536 x 2048 bf16: forward 183 us (4.4 TB/s); 9001 x 2048 fp32, 13 sequences: 54.5 us (4.1)
 //   8 x 2048 x 768 bf16, mix: forward 19.5 us (3.9 TB/s), and 2 us to clear the workspace
-//   4 x 4096 x 768 bf16, mix: backward 35 us (3.6 TB/s; vector unit 83 % busy: the decay and
-//   1 - lam are formed again in the passes over a thread's steps, as the registers to keep them
-//   are the second workgroup's of a compute unit: 45 us then, or spilled for no gain)
+//   4 x 4096 x 768 bf16, mix: backward 33 us (3.9 TB/s; the vector unit is busy with the decay and
+//   1 - lam, formed again where the registers to keep them are the second workgroup's of a
+//   compute unit: 45 us without that one)
 // A chunk waits for those before it: with few chunks a column (the 768-wide cases) that
 // latency is the rest.
 #include "layer_kernels.h"
@@ -495,8 +495,10 @@ template <typename T, bool MIX, bool PACKED> __global__ __launch_bounds__(THR, 4
 // ---- Backward ----------------------------------------------------------------
 // The states of the forward's chunks give the state entering a chunk, so only the reverse
 // direction is chained (rank 0 is the last chunk).
+// KEEP: the last steps whose 1 - lam is kept from the forward replay to the reverse one, as many as
+// registers hold: bf16, 4 x 4096 x 768: none 37.6 us, 1 37.2, 2 37.0, 3 36.1, 4 (6 spilled) 39.2.
 template <typename T, bool MIX, bool PACKED> __global__ __launch_bounds__(THR, 4) void scan_bwd(ScanArgs a) {
-  constexpr int C = CPT<T>, W = TC<T>;
+  constexpr int C = CPT<T>, W = TC<T>, KEEP = sizeof(T) == 4 ? SEG : PACKED ? 1 : 3;
   __shared__ __align__(16) union { Maps<W> s; Words<W> words; } f;   // forward maps; done with, the chain's words
   __shared__ __align__(16) Maps<W> s;                                 // reverse maps
   const Offsets offs(a);
@@ -521,7 +523,7 @@ template <typename T, bool MIX, bool PACKED> __global__ __launch_bounds__(THR, 4
 
   // The reverse map of these steps first, r_{t+1} of the last to r_t of the first: others wait
   // for this chunk's, while the forward direction needs nobody.
-  float A[C], H[C];
+  float A[C], H[C], lam[SEG][C];
 #pragma unroll
   for (int c = 0; c < C; ++c) { A[c] = 1.f; H[c] = 0.f; }
 #pragma unroll
@@ -536,15 +538,15 @@ template <typename T, bool MIX, bool PACKED> __global__ __launch_bounds__(THR, 4
     unpack16(dr[i], dv);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const float lam = decay(gv[c]);
-      A[c] *= lam;
-      H[c] = lam * (dv[c] + H[c]);
+      lam[i][c] = decay(gv[c]);
+      A[c] *= lam[i][c];
+      H[c] = lam[i][c] * (dv[c] + H[c]);
     }
   }
   store_f32<C>(&s.A[grp][cl], A);
   store_f32<C>(&s.H[grp][cl], H);
   wave_map<W, true>(s);
-  forget(gr);
+  if (MIX) forget(gr);
   forget(dr);
   st.mask(xr);
 #pragma unroll
@@ -556,12 +558,14 @@ template <typename T, bool MIX, bool PACKED> __global__ __launch_bounds__(THR, 4
 #pragma unroll
       for (int c = 0; c < C; ++c) A[c] = -0.f;
     }
-    float lam[C], u[C];
-    step_of<MIX, C>(xr[i], gr[i], lam, u);
+    float gv[C], u[C];
+    unpack16(gr[i], gv);
+    unpack16(xr[i], u);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      A[c] *= lam[c];
-      H[c] = fmaf(lam[c], H[c], u[c]);
+      if (MIX) u[c] *= one_minus_decay(gv[c], lam[i][c]);
+      A[c] *= lam[i][c];
+      H[c] = fmaf(lam[i][c], H[c], u[c]);
     }
   }
   store_f32<C>(&f.s.A[grp][cl], A);
@@ -582,22 +586,27 @@ template <typename T, bool MIX, bool PACKED> __global__ __launch_bounds__(THR, 4
   spread<W, false>(f.s, y);
   forget(xr);
   forget(gr);
-  float h[C], e[SEG][C];                  // e: what dlam multiplies, h_{t-1} (mix: h_{t-1} - x_t)
+  float h[C], e[SEG][C], w[KEEP][C];      // e: what dlam multiplies, h_{t-1} (mix: h_{t-1} - x_t); w (mix): 1 - lam
   load_f32<C>(&f.s.H[grp][cl], h);
 #pragma unroll
   for (int i = 0; i < SEG; ++i) {
     if (PACKED && ((m.first >> i) & 1)) load_seq<C>(a, a.init, t0 + i, ch, h);
-    float lam[C], u[C], xv[C];
-    step_of<MIX, C>(xr[i], gr[i], lam, u);
+    float gv[C], xv[C];
+    unpack16(gr[i], gv);
     unpack16(xr[i], xv);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
+      const float lam = decay(gv[c]), omd = MIX ? one_minus_decay(gv[c], lam) : 1.f;
+      if (MIX && i >= SEG - KEEP) w[i - (SEG - KEEP)][c] = omd;
       e[i][c] = MIX ? h[c] - xv[c] : h[c];
-      h[c] = fmaf(lam[c], h[c], u[c]);
+      h[c] = fmaf(lam, h[c], MIX ? omd * xv[c] : xv[c]);
     }
-    // formed here and now: left to itself, the compiler keeps what e is made of instead
+    // formed here and now: left to itself, the compiler keeps what they are made of instead
 #pragma unroll
-    for (int c = 0; c < C; ++c) asm volatile("" : "+v"(e[i][c]), "+v"(h[c]));
+    for (int c = 0; c < C; ++c) {
+      asm volatile("" : "+v"(e[i][c]), "+v"(h[c]));
+      if (MIX && i >= SEG - KEEP) asm volatile("" : "+v"(w[i - (SEG - KEEP)][c]));
+    }
   }
   y = 0.f;
   if (a.NC > 1) {
@@ -625,7 +634,7 @@ template <typename T, bool MIX, bool PACKED> __global__ __launch_bounds__(THR, 4
       const float lam = decay(gv[c]);
       const float delta = dv[c] + r[c];
       r[c] = lam * delta;
-      ox[c] = MIX ? one_minus_decay(gv[c], lam) * delta : delta;
+      ox[c] = MIX ? (i >= SEG - KEEP ? w[i - (SEG - KEEP)][c] : one_minus_decay(gv[c], lam)) * delta : delta;
       og[c] = r[c] * e[i][c];
     }
     st.store(a.dx, i, pack16(ox));
