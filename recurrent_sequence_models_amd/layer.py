@@ -268,10 +268,10 @@ def rope_frequencies(rot, base=10000.0, *, scaling=None, factor=1.0, original_le
     - "linear": positions interpolated, every frequency divided by the factor;
     - "ntk": the base raised to base factor^(rot / (rot - 2)), which leaves the fastest
       pair as it is and divides the slowest by the factor;
-    - "parts": pairs that turn more than ``beta_fast`` times in ``original_length`` tokens
-      are kept, those that turn less than ``beta_slow`` times are divided by the factor,
-      with a ramp over the pairs between; the rotated part is scaled by
-      0.1 ln(factor) + 1 (a factor of at most 1: by 1)."""
+    - "parts": the by-parts interpolation of YaRN (Peng et al., 2023): pairs that turn more
+      than ``beta_fast`` times in ``original_length`` tokens are kept, those that turn less
+      than ``beta_slow`` times are divided by the factor, with a ramp over the pairs between;
+      the rotated part is scaled by 0.1 ln(factor) + 1 (a factor of at most 1: by 1)."""
     import torch
     if rot < 2 or rot % 2:
         raise ValueError(f"rot: {rot}, expected a positive even number")
@@ -293,8 +293,10 @@ def rope_frequencies(rot, base=10000.0, *, scaling=None, factor=1.0, original_le
         def pair(turns):   # the (fractional) pair that turns so often in original_length tokens
             return rot * math.log(original_length / (2 * math.pi * turns)) / (2 * math.log(base))
 
-        low = min(max(math.floor(pair(beta_fast)), 0), rot // 2 - 1)
-        high = min(max(math.ceil(pair(beta_slow)), 0), rot // 2 - 1)
+        # the ramp may end past the last pair (long original contexts, where the slowest pair still
+        # turns more than beta_slow times); the method limits its end by rot - 1
+        low = max(math.floor(pair(beta_fast)), 0)
+        high = min(max(math.ceil(pair(beta_slow)), 0), rot - 1)
         ramp = ((j - low) / max(high - low, 1e-3)).clamp(0, 1)
         freq = freq * (1 - ramp) + freq / factor * ramp
         scale = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0

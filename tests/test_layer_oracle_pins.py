@@ -131,6 +131,25 @@ def test_rope_frequencies():
             rf(**bad)
 
 
+@pytest.mark.parametrize("base", [1e4, 5e5])
+@pytest.mark.parametrize("rot,factor", [(128, 4.0), (64, 8.0), (16, 2.0)])
+@pytest.mark.parametrize("length", [100, 4096, 65536, 131072, 10 ** 7, 10 ** 12])
+def test_rope_frequencies_by_parts_pair_for_pair(base, rot, factor, length):
+    """Every pair from how often it turns: the ramp begins at the last pair that turns at least
+    beta_fast = 32 times and ends at the first that turns at most beta_slow = 1 times, counted on
+    past the last pair (up to rot - 1) where the slowest still turns more often."""
+    from recurrent_sequence_models_amd import rope_frequencies as rf
+    f = rf(rot, base)[0].numpy()
+    turns = length / (2 * math.pi) * base ** (-2.0 * np.arange(-1, 4 * rot) / rot)
+    low = max(int(np.sum(turns >= 32.0)) - 2, 0)
+    high = min(int(np.sum(turns > 1.0)) - 1, rot - 1)
+    want = [f[j] if j <= low else f[j] / factor if j >= high else
+            f[j] * (1 + (1 / factor - 1) * (j - low) / (high - low)) for j in range(rot // 2)]
+    got, scale = rf(rot, base, scaling="parts", factor=factor, original_length=length)
+    assert np.allclose(got.numpy(), want, rtol=1e-12, atol=0)
+    assert scale == pytest.approx(0.1 * math.log(factor) + 1)
+
+
 # ---- Attention ----------------------------------------------------------------------------
 
 def test_attention_closed_forms():
