@@ -87,7 +87,8 @@ __device__ __forceinline__ void add_values(f16v (&acc)[D / 32], const f16v (&s)[
 }
 
 // Infinite and NaN values behind the mask.  A weight of 0 times one of them is not 0, so in a
-// tile with keys that some rows do not see they are set to 0 in LDS, and added afterwards, as
+// tile with keys that some rows do not see, or that ends behind the sequence's last key (which
+// then stands there again, with weights of 0), they are set to 0 in LDS, and added afterwards, as
 // they are, to the results of the rows that do see them: by the lane that wrote them (which
 // reads its own writes; the sums are no longer in registers, so that this path costs the loop
 // none), keys j0 .. j1 - 1.
@@ -230,9 +231,10 @@ __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : sizeof(T) * D > 128 
     }
   };
 
-  // From tile hidden0 on, tiles have keys of the sequence that some row of this tile does not see;
-  // every wave cleans the values that it copied, before the barrier that hands the tile over.
-  const int hidden0 = tile_lim + 1 < q.Lk ? max(tile_lim + 1, 0) / TN : kt1;
+  // From tile hidden0 on, tiles have keys that some row of this tile does not see, or that stand in
+  // for keys past the sequence's last; every wave cleans the values that it copied, before the
+  // barrier that hands the tile over.
+  const int hidden0 = max(tile_lim + 1, 0) / TN;
   auto clean = [&](int kt, int buf) {
     if (kt < hidden0) return;
     bool bad = false;
@@ -353,7 +355,7 @@ template <typename T, int D> __global__ __launch_bounds__(64, sizeof(T) * D > 25
   f16v acc[CB];
   Row row;
   bool bad = false;                                        // a value was cleaned
-  const int hidden0 = first_lim + 1 < q.Lk ? max(first_lim + 1, 0) / TN : kt1;
+  const int hidden0 = max(first_lim + 1, 0) / TN;
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");         // from here on only copies are counted
 #pragma unroll
   for (int b = 0; b < DB; ++b) arrived(qf[b]);
@@ -368,7 +370,7 @@ template <typename T, int D> __global__ __launch_bounds__(64, sizeof(T) * D > 25
     } else {
       copies_done();
     }
-    if (kt >= hidden0) {                                   // keys that some row does not see
+    if (kt >= hidden0) {                                   // keys that some row does not see, or past the last
 #pragma unroll
       for (int i = 0; i < PER; ++i) bad |= clean16<T>(&sv[buf][64 * i + lane]);
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");

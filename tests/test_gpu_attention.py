@@ -255,3 +255,26 @@ def test_widest_strides(d):
 def test_many_splits(dtype, lens):
     """Up to 128 splits of the keys, most of them empty for the short sequences; and few, of many rows."""
     run_case(dtype, *lens, 4, 1, 64, back=False)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("ql,kl,hq,hk,d", [([1], [1], 2, 2, 64), ([1], [33], 2, 1, 128), ([1, 1], [33, 40], 4, 1, 32),
+                                           ([1], [1500], 4, 2, 64), ([1, 1], [20001, 70], 4, 1, 128),
+                                           ([129], [129], 2, 2, 64), ([129, 1], [129, 1], 1, 1, 128), ([257], [300], 1, 1, 32)])
+def test_infinite_value_at_the_end(dtype, ql, kl, hq, hk, d):
+    """An infinite value of the last key, where a tile of keys ends behind it: inf for the query
+    that sees it (the last one), however many keys there are, and nothing for the others."""
+    import torch
+    from recurrent_sequence_models_amd import attention_fwd
+    q, k, v = rand(1, sum(ql), hq, d, dtype=dtype), rand(2, sum(kl), hk, d, dtype=dtype), rand(3, sum(kl), hk, d, dtype=dtype)
+    kw = dict(cu_seqlens=offsets(ql), cu_seqlens_k=offsets(kl))
+    o, lse = attention_fwd(q, k, v, **kw)
+    v2 = v.clone()
+    j, i = kl[0] - 1, ql[0] - 1
+    v2[j, :, ::2], v2[j, :, 1::4] = float("inf"), -float("inf")     # every fourth entry stays as it is
+    o2, lse2 = attention_fwd(q, k, v2, **kw)
+    keep = torch.ones(sum(ql), dtype=torch.bool, device="cuda")
+    keep[i] = False
+    assert torch.equal(o2[keep], o[keep]) and torch.equal(lse2, lse)
+    want = torch.where(torch.isfinite(v2[j]), torch.zeros_like(v2[j]), v2[j]).repeat_interleave(hq // hk, 0)
+    assert torch.equal(o2[i], o[i] + want)
