@@ -116,7 +116,7 @@ __device__ __forceinline__ float apply(float A, float H, float y) {
 // ---- Published words ---------------------------------------------------------
 __device__ __forceinline__ unsigned long long word(float A, float H) {
   unsigned a = __float_as_uint(A);
-  if (a == 0xffffffffu) a = 0x7fc00000u;   // a NaN map must not look like an empty word
+  if (a == 0xffffffffu) a = 0xffc00000u;   // a NaN map must not look like an empty word; its sign still cuts the carry off
   return ((unsigned long long)a << 32) | __float_as_uint(H);
 }
 __device__ __forceinline__ void publish(unsigned long long *p, unsigned long long v) {

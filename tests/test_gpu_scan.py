@@ -339,3 +339,32 @@ def test_past_32_bits_of_elements():
     assert not h[:, :T - tail].any()
     for n in ("dx", "dg"):
         assert torch.equal(b[n][:, cut], b2[n]) and not b[n][:, :T - tail].any(), n
+
+
+@pytest.mark.parametrize("mix", [False, True])
+@pytest.mark.parametrize("bits", [0x7fc00000, 0x7fffffff, -1, 0x7f800000])
+def test_nonfinite_decay_stays_in_its_sequence(bits, mix):
+    """Log decays that are NaN (of any payload: memory of all ones too) or +inf make their own
+    sequence's states non-finite, not those of a sequence that begins later in the same chunk and
+    goes on into the next ones; and so against time."""
+    import torch
+    from recurrent_sequence_models_amd import gated_scan, gated_scan_bwd
+    lens, D = [100, 700, 90, 600], 64
+    T, cu = sum(lens), offsets(lens)
+    x, dh, g, init = rand(1, T, D), rand(2, T, D), gates(3, T, D, dtype="fp32"), rand(4, 4, D)
+    bad = g.clone()
+    bad.view(torch.int32)[50], bad.view(torch.int32)[850] = bits, bits      # sequences 0 and 2
+    kw = dict(cu_seqlens=cu, mix=mix, init=init)
+    h, fin, st = gated_scan(x, g, chunk_states=True, **kw)
+    h2, fin2, st2 = gated_scan(x, bad, chunk_states=True, **kw)
+    a, b = gated_scan_bwd(x, g, dh, st, **kw), gated_scan_bwd(x, bad, dh, st2, **kw)
+    for n, (lo, hi) in enumerate(L.ranges(lens)):
+        if n % 2:
+            assert torch.equal(h[lo:hi], h2[lo:hi]) and torch.equal(fin[n], fin2[n]), n
+            for k in ("dx", "dg"):
+                assert torch.equal(a[k][lo:hi], b[k][lo:hi]), (k, n)
+            assert torch.equal(a["d_init"][n], b["d_init"][n]), n
+        else:
+            at = 50 if n == 0 else 850
+            assert not h2[at:hi].isfinite().any() and not fin2[n].isfinite().any()
+            assert not b["dx"][lo:at].isfinite().any() and not b["d_init"][n].isfinite().any()
