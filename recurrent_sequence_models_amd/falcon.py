@@ -82,6 +82,9 @@ def lib() -> ctypes.CDLL:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"{LIB_PATH} is missing: run __graft_entry__.build() (the HIP "
                                "library is required; there is no fallback)")
+        # torch first: its HIP runtime is then the one that libfalcon finds loaded.  The other way
+        # round there would be two in the process, and torch's streams are nothing to the second.
+        import torch  # noqa: F401
         L = ctypes.CDLL(LIB_PATH)
         P, I, V, S = ctypes.POINTER, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
         L.falcon_abi_version.restype = I

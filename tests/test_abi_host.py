@@ -388,3 +388,14 @@ def test_bench_reference_counts():
     assert bench.ref_flops(c5, "F1A") / 1e9 == pytest.approx(103.08, abs=0.01)
     # Falcon-3 with one pair per step is Falcon-1
     assert bench.ref_flops(c4, "F3", 1) == bench.ref_flops(c4, "F1")
+
+
+def test_one_hip_runtime():
+    """Whatever a program loads first, the library works on torch's HIP runtime: one copy of it in
+    the process."""
+    import subprocess
+    import sys
+    code = ("import recurrent_sequence_models_amd as rsm; rsm.lib(); import torch; "
+            "print(len({l.split()[-1] for l in open('/proc/self/maps') if 'libamdhip64' in l}))")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.split() == ["1"], (r.stdout, r.stderr[-500:])
