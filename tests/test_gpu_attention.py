@@ -278,3 +278,89 @@ def test_infinite_value_at_the_end(dtype, ql, kl, hq, hk, d):
     assert torch.equal(o2[keep], o[keep]) and torch.equal(lse2, lse)
     want = torch.where(torch.isfinite(v2[j]), torch.zeros_like(v2[j]), v2[j]).repeat_interleave(hq // hk, 0)
     assert torch.equal(o2[i], o[i] + want)
+
+
+def splits(nq, nk, n, hq, hk, d, dtype, back, packed=True):
+    """How many workgroups share the keys of a forward (the rows of a backward) of nq query and
+    nk key tokens, from the partial results that its workspace holds."""
+    import ctypes
+    from recurrent_sequence_models_amd.falcon import AttnShape, lib
+    tq, tk = (nq, nk) if packed else (nq // n, nk // n)
+    s = AttnShape(1 if dtype == "bf16" else 0, n, tq, tk, hq, hk, d, 1.0)
+    if not back:
+        return max(lib().falcon_attn_fwd_workspace(ctypes.byref(s), packed) // (nq * hq * (d + 2) * 4), 1)
+    rows = 2 * (-(-nq * hq * 4 // 16) * 16)
+    return max((lib().falcon_attn_bwd_workspace(ctypes.byref(s), packed) - rows) // (2 * nk * hk * d * 4), 1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("ql,kl,least,behind", [([1], [20000], 65, 0), ([1, 0, 1, 2], [9000, 5, 12000, 1], 9, 3),
+                                                ([1, 3, 1], [1700, 900, 2], 2, 5)], ids=["most", "many", "few"])
+def test_joined_splits(dtype, d, ql, kl, least, behind):
+    """Both ways of joining the splits of a row, at each head size, with tokens behind."""
+    n = splits(sum(ql) + behind, sum(kl) + behind, len(ql), 3, 1, d, dtype, False)
+    assert n >= least and (least > 8 or n <= 8), n
+    run_case(dtype, ql, kl, 3, 1, d, back=False, behind=behind, seed=d)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("ql,kl,hq,hk,behind,packed", [([900, 0, 1301], [900, 7, 1301], 2, 1, 6, True),
+                                                       ([700, 20], [811, 3], 3, 1, 0, True),
+                                                       ([1027, 1027], [1027, 1027], 2, 2, 0, False)],
+                         ids=["ragged", "groups", "batch"])
+def test_split_backward(dtype, d, ql, kl, hq, hk, behind, packed):
+    """The rows of a key tile split between workgroups and added: each head size and type,
+    several sequences, an empty one, keys before the queries, more queries than keys, tokens
+    behind, the batched form."""
+    assert splits(sum(ql) + behind, sum(kl) + behind, len(ql), hq, hk, d, dtype, True, packed) > 1
+    run_case(dtype, ql, kl, hq, hk, d, packed=packed, behind=behind, seed=d)
+
+
+def test_arrays_past_31_bits():
+    """More than 2^31 elements of q, k, v, o and the gradients; the sequences at both ends are
+    what they are by themselves."""
+    import torch
+    from recurrent_sequence_models_amd import attention_bwd, attention_fwd
+    H, d, each, n = 64, 128, 64, (1 << 12) + 2
+    assert n * each * H * d > 2 ** 31
+    gen = torch.Generator("cuda").manual_seed(1)
+    q, k, v, do = (torch.randn(n * each, H, d, generator=gen, device="cuda", dtype=torch.bfloat16) for _ in range(4))
+    cu = torch.arange(n + 1, device="cuda", dtype=torch.int32) * each
+    o, lse = attention_fwd(q, k, v, cu_seqlens=cu)
+    g = attention_bwd(q, k, v, o, lse, do, cu_seqlens=cu)
+    for i in (0, n // 2, n - 1):
+        s = slice(i * each, (i + 1) * each)
+        o1, lse1 = attention_fwd(q[s], k[s], v[s], cu_seqlens=offsets([each]))
+        g1 = attention_bwd(q[s], k[s], v[s], o1, lse1, do[s], cu_seqlens=offsets([each]))
+        assert torch.equal(o[s], o1) and torch.equal(lse[s], lse1), i
+        for name in ("dq", "dk", "dv"):
+            assert torch.equal(g[name][s], g1[name]), (name, i)
+
+
+@pytest.mark.parametrize("d", [32, 128])
+def test_strides_past_31_bits(d):
+    """Tokens as far apart as is allowed: the last ones lie 2^31 elements and more from the first,
+    in the inputs, the incoming gradients and the gradients; prompts and a single token."""
+    import torch
+    from recurrent_sequence_models_amd import attention_bwd, attention_fwd
+    T, step = 150, 1 << 24
+    assert (T - 1) * step > 2 ** 31
+    wide = torch.empty(T, step, device="cuda", dtype=torch.bfloat16)
+    parts = [rand(i, T, 2, d, dtype="bf16") for i in range(4)]
+    at = lambda i: wide[:, i * step // 8:][:, :2 * d].unflatten(1, (2, d))  # noqa: E731
+    for i, t in enumerate(parts):
+        at(i).copy_(t)
+    (q, k, v, do), (wq, wk, wv, wdo, wdq, wdk, wdv) = parts, [at(i) for i in range(7)]
+    cu, one = offsets([T]), offsets([1])
+    o, lse = attention_fwd(q, k, v, cu_seqlens=cu)
+    o2, lse2 = attention_fwd(wq, wk, wv, cu_seqlens=cu)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    want = attention_bwd(q, k, v, o, lse, do, cu_seqlens=cu)
+    got = attention_bwd(wq, wk, wv, o, lse, wdo, cu_seqlens=cu, out=dict(dq=wdq, dk=wdk, dv=wdv))
+    for n in ("dq", "dk", "dv"):
+        assert torch.equal(want[n], got[n]), n
+    o, _ = attention_fwd(q[-1:], k, v, cu_seqlens=one, cu_seqlens_k=cu)
+    o2, _ = attention_fwd(wq[-1:], wk, wv, cu_seqlens=one, cu_seqlens_k=cu)
+    assert torch.equal(o, o2)
