@@ -10,8 +10,11 @@
 //
 // Roundings, for bf16: P and dS as operands of the products that sum over them (8-bit mantissas are
 // what the matrix unit takes at this rate; each adds 0.16 % of a gradient's norm to the 0.17 % of its
-// own rounding), and D from o as the caller holds it, rounded (0.2 % at 64 tokens, 0.07 % at 2048).
-// Sums are fp32.
+// own rounding: 0.23 to 0.25 % in all).  D is fp32, although o is rounded, in dk and in the dq of rows
+// that see 128 keys at most (with D from the rounded o: 0.79 % at 2 tokens, 0.27 % at 64).  Over more
+// keys dq takes it from o, which adds less than 0.02 % where a row's weight is spread; where it lies on
+// few of 2048 keys (scores of standard deviation 2.5) dq is off by 0.41 %: one more product over all
+// keys, a tenth of the time, would be the price of the rest.  Sums are fp32.
 //
 // Rows are (token, head of the group) pairs as in the forward pass.  In the key kernel a
 // wave owns 32 keys with their k and v in registers and forms S = Q K^T, so that P and dS
@@ -34,8 +37,9 @@ namespace {
 constexpr int THR = 256, TR = 128;   // 4 waves of 32 rows (or keys)
 
 // ---- dq ----------------------------------------------------------------------
+// Three waves a SIMD where rows are 128 bytes at most (167 registers at bf16, d = 64).
 template <typename T, int D>
-__global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_q(AttnArgs a) {
+__global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : sizeof(T) * D > 128 ? 2 : 3) void attn_bwd_q(AttnArgs a) {
   typedef Tile<T, D> Ti;
   constexpr int TN = 64, DB = D / 16, CB = D / 32;   // keys of a tile (32: 1 to 2 % more time)
   typedef Copy<T, D, TN> Cp;
@@ -68,9 +72,15 @@ __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_q(A
   Frag<T> qf[DB], gf[DB];
 #pragma unroll
   for (int b = 0; b < DB; ++b) { qf[b] = global_frag(qp, b, h); gf[b] = global_frag(gp, b, h); }
-  // For these rows and, through memory, the key kernel: -D = -do . o, where the products do . v
-  // start from, and lse in base 2, +inf where the row sees nothing, so that all its weights
-  // e^{s - lse} come out 0.
+  // -D = -do . o, where the products do . v start from, and lse in base 2, +inf where the row sees
+  // nothing, so that all its weights e^{s - lse} come out 0.
+  // o is rounded, and what D is off by is the same in all do . v - D of a row: for bf16 the largest
+  // error there is in rows whose weight lies on few keys.  As the weights add up to 1, the sum over
+  // the keys of P (do . v - D) is what D lacks.  It is summed beside the products, so that the key
+  // kernel gets a D of fp32 throughout; rows that see two tiles of keys at most, which both stand in
+  // LDS, form it first, so that dq has it as well.  8 x 2048, 12 / 12 heads of 64: 209 us without
+  // the sum, 213 with it; 16 x 128: 17.7 and 19.2 us.
+  constexpr bool SUMS = sizeof(T) == 2;
   const int64_t at = (int64_t)(q.q0 + tok) * a.hq + hq;
   const T *op = static_cast<const T *>(a.o) + at * D;
   float Dr = 0.f;
@@ -78,10 +88,7 @@ __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_q(A
   for (int b = 0; b < DB; ++b) Dr -= dot(global_frag(op, b, h), gf[b]);
   Dr = add_xor32(Dr);
   const float lse = a.lse_in[at], L = lse == -INFINITY ? INFINITY : lse * kLog2e;
-  if (on && h == 0) {
-    a.delta[at] = Dr;
-    a.lse2[at] = L;
-  }
+  if (on && h == 0) a.lse2[at] = L;             // for the key kernel, as -D below
 
   const T *kg = static_cast<const T *>(a.k) + (int64_t)q.k0 * a.ldk + head * D;
   const T *vg = static_cast<const T *>(a.v) + (int64_t)q.k0 * a.ldv + head * D;
@@ -97,38 +104,59 @@ __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_q(A
       copy_to_lds(vp, row * vstep + Cp::byte(i, tid), Cp::to(sv[buf], i, wave));
     }
   };
-  f16v dq[CB];
-#pragma unroll
-  for (int b = 0; b < CB; ++b) dq[b] = zero16();
   const float sc = a.scale * kLog2e;
+  // P, and do . v - D, of the 32 keys from key0 (kb of the tile in buf)
+  auto products = [&](int buf, int kb, int key0, f16v &s, f16v &g) {
+    s = zero16();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) g[i] = Dr;
+#pragma unroll
+    for (int b = 0; b < DB; ++b) mma(s, Ti::rows(sk[buf], kb, b, lane), qf[b]);
+#pragma unroll
+    for (int b = 0; b < DB; ++b) mma(g, Ti::rows(sv[buf], kb, b, lane), gf[b]);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], sc, -L));
+    if (key0 + 31 > first_lim) {
+      const int left = lim - key0 - 4 * h;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i] = 8 * (i / 4) + (i & 3) > left ? 0.f : s[i];
+    }
+  };
+  const bool refine = SUMS && ktiles <= 2;
   if (ktiles > 0) copy(0, 0);
+  if (refine && ktiles == 2) copy(1, 1);
   copies_done();
 #pragma unroll
   for (int b = 0; b < DB; ++b) { arrived(qf[b]); arrived(gf[b]); }
   __syncthreads();
+  float rest = 0.f;                             // the sum over the keys of P (do . v - D), 0 but for D's error
+  if (refine) {
+    for (int key0 = 0; key0 < ktiles * TN && key0 <= wave_lim; key0 += 32) {
+      f16v s, g;
+      products(key0 / TN, key0 % TN, key0, s, g);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) rest = fmaf(s[i], g[i], rest);
+    }
+    Dr -= add_xor32(rest);
+    rest = 0.f;
+  }
+  f16v dq[CB];
+#pragma unroll
+  for (int b = 0; b < CB; ++b) dq[b] = zero16();
   for (int kt = 0; kt < ktiles; ++kt) {
     const int buf = kt & 1;
-    if (kt + 1 < ktiles) copy(kt + 1, buf ^ 1);            // its last readers are behind the barrier
+    if (kt + 1 < ktiles && !refine) copy(kt + 1, buf ^ 1);  // its last readers are behind the barrier
 #pragma unroll
     for (int kb = 0; kb < TN; kb += 32) {
       const int key0 = kt * TN + kb;
       if (key0 > wave_lim) break;               // no row of this wave sees the keys from here on
-      f16v s = zero16(), g;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) g[i] = Dr;
-#pragma unroll
-      for (int b = 0; b < DB; ++b) mma(s, Ti::rows(sk[buf], kb, b, lane), qf[b]);
-#pragma unroll
-      for (int b = 0; b < DB; ++b) mma(g, Ti::rows(sv[buf], kb, b, lane), gf[b]);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], sc, -L));
-      if (key0 + 31 > first_lim) {
-        const int left = lim - key0 - 4 * h;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = 8 * (i / 4) + (i & 3) > left ? 0.f : s[i];
-      }
+      f16v s, g;
+      products(buf, kb, key0, s, g);
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[i] *= g[i];
+      if (SUMS)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) rest += s[i];
 #pragma unroll
       for (int b16 = 0; b16 < 2; ++b16) {
         const Frag<T> sf = result_frag<T>(s, b16);
@@ -139,7 +167,9 @@ __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : 2) void attn_bwd_q(A
     copies_done();
     __syncthreads();
   }
+  if (SUMS) Dr -= add_xor32(rest);
   if (!on) return;
+  if (h == 0) a.delta[at] = Dr;                 // for the key kernel
   T *pq = static_cast<T *>(a.dq) + (int64_t)(q.q0 + tok) * a.lddq + hq * D;
 #pragma unroll
   for (int b = 0; b < CB; ++b)

@@ -364,3 +364,79 @@ def test_strides_past_31_bits(d):
     o, _ = attention_fwd(q[-1:], k, v, cu_seqlens=one, cu_seqlens_k=cu)
     o2, _ = attention_fwd(wq[-1:], wk, wv, cu_seqlens=one, cu_seqlens_k=cu)
     assert torch.equal(o, o2)
+
+
+@pytest.mark.parametrize("lens,hq,hk,d,spread", [([1], 2, 2, 64, 1.0), ([2, 1, 9], 4, 1, 128, 1.0), ([64, 3], 2, 2, 32, 2.0),
+                                                 ([128], 3, 1, 64, 1.0), ([300], 4, 2, 128, 2.5), ([700, 129], 2, 1, 64, 2.5),
+                                                 ([1400], 2, 1, 128, 2.0)])
+def test_rounded_results_do_not_reach_the_gradients(lens, hq, hk, d, spread):
+    """bf16: D = do . o, which all weights of a row share, is held to fp32 although o is rounded:
+    in dk of every length, and in dq of the rows that see 128 keys at most.
+
+    D is formed as D' + sum_j P_ij (do_i . v_j - D'), D' from the rounded o.  With dp_ij the sum of
+    absolute values of do_i . v_j and Da that of D: each difference is off by (d + 4) u (dp + Da),
+    the weights by ep relatively (and their sum from 1 by ep, which multiplies D'), the sum over
+    the keys by (Lk + 16) u."""
+    import torch
+    from layer_helpers import TINY, U, half
+    from recurrent_sequence_models_amd import attention_bwd, attention_fwd
+    total = sum(lens)
+    q, do = rand(1, total, hq, d, dtype="bf16", scale=spread), rand(4, total, hq, d, dtype="bf16")
+    k, v = rand(2, total, hk, d, dtype="bf16"), rand(3, total, hk, d, dtype="bf16")
+    cu = offsets(lens)
+    o, lse = attention_fwd(q, k, v, cu_seqlens=cu)
+    g = attention_bwd(q, k, v, o, lse, do, cu_seqlens=cu)
+    torch.cuda.synchronize()
+    Q, K, V, DO, DQ, DK = (f64(t) for t in (q, k, v, do, g["dq"], g["dk"]))
+    h, sc = half("bf16"), float(np.float32(d ** -0.5))
+    for n, (a, b) in enumerate(L.ranges(lens)):
+        T, grp = b - a, hq // hk
+        f, r = L.attention(Q[a:b], K[a:b], V[a:b], sc), L.attention_backward(Q[a:b], K[a:b], V[a:b], DO[a:b], sc)
+        bq, bk = np.zeros_like(Q[a:b]), np.zeros_like(K[a:b])
+        for i in range(hq):
+            kv = i // grp
+            A = sc * (np.abs(Q[a:b, i]) @ np.abs(K[a:b, kv]).T)
+            ep = 2 * ((d + 4) * U * A.max() + U * (A.max() + 4) * 2) + (T + 16) * U
+            p, go = f["p"][i], np.abs(DO[a:b, i])
+            dp, Da = go @ np.abs(V[a:b, kv]).T, np.sum(go * np.abs(f["o"][:, i]), -1, keepdims=True)
+            eD = np.sum(p * ((d + 4) * U + ep + (T + 16) * U) * (dp + Da), -1, keepdims=True) + ep * Da
+            eds = p * ((d + 4) * U * (dp + Da) + eD + (ep + 2 * U) * (dp + Da)) + (h + (T * grp + 2) * U) * np.abs(r["ds"][i])
+            eds = eds * (1 + h) + TINY
+            bq[:, i] = sc * eds @ np.abs(K[a:b, kv])
+            bk[:, kv] += sc * eds.T @ np.abs(Q[a:b, i])
+        few = min(T, 128)
+        check(f"dq[{n}]", DQ[a:a + few], r["dq"][:few], (bq * (1 + h) + h * np.abs(r["dq"]) + TINY)[:few])
+        check(f"dk[{n}]", DK[a:b], r["dk"], bk * (1 + h) + h * np.abs(r["dk"]) + TINY)
+
+
+@pytest.mark.parametrize("lens,hq,hk,d,spread,names", [([2] * 40, 4, 2, 64, 1.0, ("dq", "dk")), ([3, 2, 4] * 9, 2, 2, 128, 1.0, ("dq", "dk")),
+                                                       ([128] * 2, 2, 1, 32, 2.0, ("dq", "dk")), ([1500], 4, 1, 128, 2.5, ("dk",))])
+def test_gradients_are_as_good_as_their_roundings(lens, hq, hk, d, spread, names):
+    """The norm of the error of dq and dk in bf16 is that of the roundings of dS and of the result.
+
+    A rounding of x is off by at most 2^-8 |x| and, over evenly spread remainders, by 2^-8 / sqrt(3)
+    |x| in the mean square.  They are independent, so their squares add: over the result's entries,
+    and over the terms scale dS_ij k_j (dS_ij q_i) of its sum."""
+    import torch
+    from recurrent_sequence_models_amd import attention_bwd, attention_fwd
+    total, grp, sc = sum(lens), hq // hk, d ** -0.5
+    q, do = rand(1, total, hq, d, dtype="bf16", scale=spread), rand(4, total, hq, d, dtype="bf16")
+    k, v = rand(2, total, hk, d, dtype="bf16"), rand(3, total, hk, d, dtype="bf16")
+    cu = offsets(lens)
+    o, lse = attention_fwd(q, k, v, cu_seqlens=cu)
+    g = attention_bwd(q, k, v, o, lse, do, cu_seqlens=cu)
+    torch.cuda.synchronize()
+    Q, K, V, DO = (f64(t) for t in (q, k, v, do))
+    err, terms = dict.fromkeys(names, 0.0), dict.fromkeys(names, 0.0)
+    for a, b in L.ranges(lens):
+        r = L.attention_backward(Q[a:b], K[a:b], V[a:b], DO[a:b], sc)
+        for n in names:
+            err[n] += np.sum((f64(g[n])[a:b] - r[n]) ** 2)
+            terms[n] += np.sum(r[n] ** 2)
+        for h in range(hq):
+            ds2 = (sc * r["ds"][h]) ** 2
+            for n, w in (("dq", ds2 @ np.sum(K[a:b, h // grp] ** 2, -1)), ("dk", ds2.T @ np.sum(Q[a:b, h] ** 2, -1))):
+                if n in names:
+                    terms[n] += np.sum(w)
+    for n in names:
+        assert err[n] <= terms[n] * 2.0 ** -16 / 3, (n, np.sqrt(err[n] / terms[n]) / 2.0 ** -8)
