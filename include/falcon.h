@@ -416,7 +416,8 @@ int falcon_scan_step(const falcon_scan_shape_t *shape, const void *x, const void
  * with a = j, b = j + rot / 2 (FALCON_ROPE_HALF) or a = 2 j, b = 2 j + 1
  * (FALCON_ROPE_INTERLEAVED); the other entries are z.  Longer contexts scale
  * inv_freq and rot_scale; the angle is formed in 64 bits, the mean of squares in
- * 32 (entries over 2^63 overflow it: z = 0). */
+ * 32 (entries over 2^63 overflow it: z = 0; with eps = 0, z of a row of zeros, or
+ * of entries under 2^-75, is not finite). */
 typedef enum { FALCON_ROPE_HALF = 0, FALCON_ROPE_INTERLEAVED = 1 } falcon_rope_layout_t;
 
 typedef struct {
@@ -487,7 +488,9 @@ size_t falcon_attn_fwd_workspace(const falcon_attn_shape_t *shape, int packed);
 /* q [tokens, heads_q, d], k, v [tokens, heads_k, d] (token strides as above, at
  * most 2^25 bytes), o dense [tokens, heads_q, d], lse [tokens, heads_q] fp32 or
  * NULL; they must not overlap the inputs.
- *   cu_q, cu_k  both NULL (batch * seqlen tokens) or both [batch + 1] offsets. */
+ *   cu_q, cu_k  both NULL (batch * seqlen tokens) or both [batch + 1] offsets.
+ * Either way the tokens of a sequence follow those of the one before: there is no
+ * form for keys kept with room to grow between the sequences. */
 int falcon_attn_fwd(const falcon_attn_shape_t *shape, const int32_t *cu_q, const int32_t *cu_k,
                     falcon_heads_t q, falcon_heads_t k, falcon_heads_t v, void *o, float *lse,
                     void *workspace, size_t workspace_bytes, void *stream);

@@ -24,9 +24,10 @@
 // Bound: the matrix unit, 14 d flops executed per visible pair and head (10 d needed), and power
 // (operands of zeros: 20 % less time).  Measured, as useful flops (10 d), where an 8192^3 bf16
 // matrix product reaches 1.21 PFLOP/s:
-//   4 x 4096, 16 / 4 heads of 128, bf16: 0.94 ms, 730 TFLOP/s (rows 350 us, keys 565, their sum 26)
-//   8 x 2048, 12 / 12 heads of 64, bf16: 218 us, 590 TFLOP/s (rows 85 us, keys 136), 244 us in a long run
-//   2 x 2048, 12 / 12 heads of 64, fp32: 521 us, 62 TFLOP/s
+//   4 x 4096, 16 / 4 heads of 128, bf16: 0.98 ms, 700 TFLOP/s (in a long run 1.11: rows 399 us, keys
+//     687, their sum 27)
+//   8 x 2048, 12 / 12 heads of 64, bf16: 213 us, 605 TFLOP/s (in a long run 260: rows 115 us, keys 144)
+//   2 x 2048, 12 / 12 heads of 64, fp32: 526 us, 61 TFLOP/s
 #include "attn_frag.h"
 #include "layer_kernels.h"
 #include "lane_ops.h"
@@ -78,8 +79,8 @@ __global__ __launch_bounds__(THR, sizeof(T) * D > 256 ? 1 : sizeof(T) * D > 128 
   // error there is in rows whose weight lies on few keys.  As the weights add up to 1, the sum over
   // the keys of P (do . v - D) is what D lacks.  It is summed beside the products, so that the key
   // kernel gets a D of fp32 throughout; rows that see two tiles of keys at most, which both stand in
-  // LDS, form it first, so that dq has it as well.  8 x 2048, 12 / 12 heads of 64: 209 us without
-  // the sum, 213 with it; 16 x 128: 17.7 and 19.2 us.
+  // LDS, form it first, so that dq has it as well.  Forward and backward of 8 x 2048, 12 / 12 heads of
+  // 64, in a long run: 281 us without the sum, 287 with it; of 16 x 128 the same 30 us.
   constexpr bool SUMS = sizeof(T) == 2;
   const int64_t at = (int64_t)(q.q0 + tok) * a.hq + hq;
   const T *op = static_cast<const T *>(a.o) + at * D;

@@ -32,9 +32,9 @@
 // per step and channel, and for bf16 the vector unit close behind.  Measured, where a plain
 // copy moves 5.1 TB/s:
 //   64 x 256 x 2048 bf16, one chunk a sequence: forward 39.8 us (5.1 TB/s), backward 75 us (4.5)
-//   65536 x 2048 bf16: forward 183 us (4.4 TB/s); 9001 x 2048 fp32, 13 sequences: 54.5 us (4.1)
+//   65536 x 2048 bf16: forward 183 us (4.4 TB/s); 9001 x 2048 fp32, 13 sequences: 55 to 60 us (3.7 to 4.1)
 //   8 x 2048 x 768 bf16, mix: forward 19.5 us (3.9 TB/s), and 2 us to clear the workspace
-//   4 x 4096 x 768 bf16, mix: backward 33 us (3.9 TB/s; the vector unit is busy with the decay and
+//   4 x 4096 x 768 bf16, mix: backward 33 us (3.8 TB/s; the vector unit is busy with the decay and
 //   1 - lam, formed again where the registers to keep them are the second workgroup's of a
 //   compute unit: 45 us without that one)
 // A chunk waits for those before it: with few chunks a column (the 768-wide cases) that
@@ -497,6 +497,7 @@ template <typename T, bool MIX, bool PACKED> __global__ __launch_bounds__(THR, 4
 // direction is chained (rank 0 is the last chunk).
 // KEEP: the last steps whose 1 - lam is kept from the forward replay to the reverse one, as many as
 // registers hold: bf16, 4 x 4096 x 768: none 37.6 us, 1 37.2, 2 37.0, 3 36.1, 4 (6 spilled) 39.2.
+// Packed, where 6 registers are spilled with 1 and 8 with 3: 45.6 us each (16384 x 768, 13 sequences).
 template <typename T, bool MIX, bool PACKED> __global__ __launch_bounds__(THR, 4) void scan_bwd(ScanArgs a) {
   constexpr int C = CPT<T>, W = TC<T>, KEEP = sizeof(T) == 4 ? SEG : PACKED ? 1 : 3;
   __shared__ __align__(16) union { Maps<W> s; Words<W> words; } f;   // forward maps; done with, the chain's words

@@ -437,7 +437,8 @@ def attention_fwd(q, k, v, *, cu_seqlens=None, cu_seqlens_k=None, scale=None, ls
     q [B,Tq,Hq,d], k, v [B,Tk,Hk,d] (float32 or bfloat16, Hq a multiple of Hk; views with
     dense heads will do), or packed [total,H,d] with ``cu_seqlens`` (and ``cu_seqlens_k``
     where a sequence's keys are more than its queries, which are then its last tokens),
-    int32 device tensors [N+1].  ``scale``: default d^-1/2.  ``lse``: whether to return
+    int32 device tensors [N+1].  Sequences follow one another without room between them (a
+    view of a longer cache is taken for one sequence only).  ``scale``: default d^-1/2.  ``lse``: whether to return
     the log-sum-exp of every row (attention_bwd needs it).
     Returns (o, lse): o like q and dense, lse [..., Hq] float32 or None."""
     import torch
