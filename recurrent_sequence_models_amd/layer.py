@@ -275,8 +275,8 @@ def rope_frequencies(rot, base=10000.0, *, scaling=None, factor=1.0, original_le
     import torch
     if rot < 2 or rot % 2:
         raise ValueError(f"rot: {rot}, expected a positive even number")
-    if not base > 0 or not factor > 0:
-        raise ValueError("base and factor must be positive")
+    if not 0 < base < math.inf or not 0 < factor < math.inf:
+        raise ValueError("base and factor must be positive and finite")
     j = torch.arange(rot // 2, dtype=torch.float64)
     scale = 1.0
     if scaling == "ntk":
@@ -287,8 +287,8 @@ def rope_frequencies(rot, base=10000.0, *, scaling=None, factor=1.0, original_le
     if scaling == "linear":
         freq = freq / factor
     elif scaling == "parts":
-        if not original_length or base == 1:
-            raise ValueError("scaling 'parts' needs original_length and a base other than 1")
+        if not original_length or not original_length > 0 or not base > 1 or not beta_fast >= beta_slow > 0:
+            raise ValueError("scaling 'parts' needs original_length, a base over 1, and beta_fast >= beta_slow > 0")
 
         def pair(turns):   # the (fractional) pair that turns so often in original_length tokens
             return rot * math.log(original_length / (2 * math.pi * turns)) / (2 * math.log(base))

@@ -150,6 +150,16 @@ def test_rope_frequencies_by_parts_pair_for_pair(base, rot, factor, length):
     assert scale == pytest.approx(0.1 * math.log(factor) + 1)
 
 
+@pytest.mark.parametrize("bad", [dict(base=0.5), dict(base=1.0), dict(beta_fast=1.0, beta_slow=32.0), dict(beta_slow=0.0),
+                                 dict(original_length=-5), dict(original_length=0), dict(factor=float("inf")),
+                                 dict(factor=float("nan")), dict(base=float("inf"))])
+def test_rope_frequencies_by_parts_refusals(bad):
+    """What has no ramp from the pairs that turn often to those that turn rarely is refused."""
+    from recurrent_sequence_models_amd import rope_frequencies as rf
+    with pytest.raises(ValueError, match="parts|finite"):
+        rf(64, **{**dict(scaling="parts", factor=4.0, original_length=4096), **bad})
+
+
 # ---- Attention ----------------------------------------------------------------------------
 
 def test_attention_closed_forms():
