@@ -76,7 +76,8 @@ typedef enum {
   FALCON_3A = 6   /* window of Bw pairs, averaged additive write  */
 } falcon_variant_t;
 
-typedef enum { FALCON_F32 = 0, FALCON_BF16 = 1 } falcon_dtype_t;  /* of q, k, v, o */
+typedef enum { FALCON_F32 = 0, FALCON_BF16 = 1, FALCON_E4M3 = 2 } falcon_dtype_t;  /* of q, k, v, o: F32 or BF16;
+ E4M3 (8 bits, largest number 448, no infinities): only where an entry point names it */
 
 /* Which key the pair written at step t carries ([P1] 本质; [P2] 一个被忽略的时间差):
  * the prefix pair (phi(k_{t-1}), v_t), the method's alignment, or the same-step
@@ -505,6 +506,96 @@ int falcon_attn_bwd(const falcon_attn_shape_t *shape, const int32_t *cu_q, const
                     falcon_heads_t q, falcon_heads_t k, falcon_heads_t v, const void *o, const float *lse,
                     falcon_heads_t d_o, falcon_heads_out_t dq, falcon_heads_out_t dk, falcon_heads_out_t dv,
                     void *workspace, size_t workspace_bytes, void *stream);
+
+/* ======================================================================== */
+/* Operators of a state-space block                                         */
+/* ======================================================================== */
+/* What a block of a recurrent model is made of besides its mixer: the norm of the
+ * residual stream, the projections, the short causal convolution, and the
+ * selective state-space scan.  Conventions as for the operators around the mixer
+ * (packed sequences, gradients' types, determinism, workspaces, refusals).
+ * Arrays are dense unless given as falcon_heads_t, with one head of the array's
+ * width: then tokens may be further apart, as in a view of a wider projection. */
+
+typedef enum { FALCON_ACT_NONE = 0, FALCON_ACT_SILU = 1, FALCON_ACT_GELU = 2 } falcon_activation_t;
+/* silu(p) = p / (1 + e^-p);  gelu(p) = p (1 + erf(p / sqrt 2)) / 2 */
+
+/* ---- Norm of the residual stream ------------------------------------------
+ * Per token, of `width` entries:
+ *   s = x + residual, rounded to dtype          (residual NULL: s = x)
+ *   y = s w / sqrt(mean(s^2) + eps)             (norm = 0: y = s w)
+ * The norm is of the rounded stream, which the backward pass differentiates.
+ * out = FALCON_E4M3: y in 8 bits, y = q scale with one fp32 scale a token,
+ *   scale = max(max |y|, 1e-30) / 448, q = y / scale rounded to nearest even
+ * (from the unrounded y; with norm = 0 and no weight this quantises x's rows).  A
+ * row with a NaN has a NaN scale; one with an infinity (norm = 0) an infinite one.
+ * The mean of squares is formed in fp32: as in the query / key norm, entries over
+ * 2^63 overflow it, and with eps = 0 a row of zeros is not finite. */
+typedef struct {
+  int32_t dtype;   /* falcon_dtype_t of x, residual and the stream: F32 or BF16 */
+  int32_t tokens;  /* 1 .. 2^31 - 1 - 2^20 */
+  int32_t width;   /* a multiple of 8; at most 32768 (BF16) or 16384 (F32) */
+  int32_t norm;    /* 0 or 1 */
+  int32_t out;     /* falcon_dtype_t of y: dtype or E4M3 */
+  float eps;       /* finite, >= 0 */
+} falcon_norm_shape_t;
+
+/* weight [width] fp32 or NULL (ones).  stream: receives s; may be NULL, and may be
+ * x or residual itself; not written without residual.  y may be x or residual
+ * itself if it has their type and is not the stream.  scale: [tokens] fp32, for E4M3. */
+int falcon_rms_norm(const falcon_norm_shape_t *shape, const void *x, const void *residual, const float *weight,
+                    void *stream_out, void *y, float *scale, void *stream);
+
+/* Bytes of workspace of the backward pass (the workgroups' sums for the weight's
+ * gradient); 0 for invalid shapes. */
+size_t falcon_rms_norm_bwd_workspace(const falcon_norm_shape_t *shape);
+
+/* The gradient dx, which is x's and the residual's alike, of <d_y, y> + <d_stream, s>,
+ * from the stream s (x itself where there was no residual).  shape->norm must be 1, and
+ * out is ignored: d_y, d_stream (NULL: zeros) and dx have dtype.  dweight [width] fp32 or
+ * NULL (then workspace may be NULL).  dx may be d_y or d_stream itself. */
+int falcon_rms_norm_bwd(const falcon_norm_shape_t *shape, const void *s, const float *weight, const void *d_y,
+                        const void *d_stream, void *dx, float *dweight, void *workspace, size_t workspace_bytes,
+                        void *stream);
+
+/* ---- Short causal convolution ----------------------------------------------
+ * Per sequence and channel, with one filter of `taps` weights a channel:
+ *   y_t = act(bias + sum_j w_j x_{t - taps + 1 + j}),  j = 0 .. taps - 1
+ * The inputs before a sequence's first token are its initial state (oldest first),
+ * its last taps - 1 inputs (those of the initial state included) its final one. */
+typedef struct {
+  int32_t dtype;       /* falcon_dtype_t of x, y, the states and their gradients: F32 or BF16 */
+  int32_t batch;       /* sequences, >= 1 */
+  int32_t seqlen;      /* tokens of every sequence, >= 1; packed: all tokens.  At most 2^31 - 1 - 4096 in all */
+  int32_t width;       /* channels, a multiple of 8, at most 2^20 */
+  int32_t taps;        /* 2, 3 or 4 */
+  int32_t activation;  /* FALCON_ACT_NONE or FALCON_ACT_SILU */
+} falcon_conv_shape_t;
+
+/*   cu_seqlens   NULL: x, y are [B, T, D].  Otherwise [B + 1] offsets, and they are [T, D].
+ *   weight       [D, taps] fp32;  bias [D] fp32 or NULL.
+ *   init         [B, taps - 1, D] in dtype, or NULL for zeros.
+ *   final_state  the same, or NULL.  An empty sequence's is its initial state.
+ * Outputs must not overlap inputs. */
+int falcon_conv_fwd(const falcon_conv_shape_t *shape, const int32_t *cu_seqlens, falcon_heads_t x, const float *weight,
+                    const float *bias, const void *init, void *final_state, void *y, void *stream);
+
+/* Bytes of workspace of the backward pass; `packed` is nonzero for calls with
+ * cu_seqlens.  0 for invalid shapes. */
+size_t falcon_conv_bwd_workspace(const falcon_conv_shape_t *shape, int packed);
+
+/* Gradients of <d_y, y> + <d_final, final_state>: dx, d_init (or NULL) in dtype, the sums
+ * rounded once; dweight [D, taps], dbias [D] fp32, or NULL (both NULL: workspace may be
+ * NULL).  d_final as the final state, or NULL.  Outputs must not alias inputs. */
+int falcon_conv_bwd(const falcon_conv_shape_t *shape, const int32_t *cu_seqlens, falcon_heads_t x, const float *weight,
+                    const float *bias, const void *init, const void *d_y, const void *d_final, falcon_heads_out_t dx,
+                    float *dweight, float *dbias, void *d_init, void *workspace, size_t workspace_bytes, void *stream);
+
+/* One token of every sequence: x [B, D] (batch the tokens), y [B, D]; state
+ * [B, taps - 1, D] in dtype, state_out the same (may be state itself).  shape->seqlen is
+ * ignored. */
+int falcon_conv_step(const falcon_conv_shape_t *shape, falcon_heads_t x, const float *weight, const float *bias,
+                     const void *state, void *state_out, void *y, void *stream);
 
 #ifdef __cplusplus
 }

@@ -30,6 +30,8 @@ parity is unpinned by the pages and fixed only by the readings.
 :mod:`oracle.layer_oracle` (``oracle.layer``) holds the operators around the mixer, from
 their formulas: the gated linear recurrence, the query / key norm with rotary
 positions and causal attention, pinned in ``tests/test_layer_oracle_pins.py``.
+:mod:`oracle.block_oracle` (``oracle.block``) holds those of a state-space block, pinned in
+``tests/test_block_oracle_pins.py``.
 """
 
 from .falcon_oracle import (VARIANTS, recurrent, masked_parallel, chunked,
@@ -40,4 +42,6 @@ __all__ = ["VARIANTS", "recurrent", "masked_parallel", "chunked", "decode_step",
 
 from . import layer_oracle as layer  # noqa: E402
 
-__all__.append("layer")
+from . import block_oracle as block  # noqa: E402
+
+__all__ += ["layer", "block"]

@@ -1,0 +1,72 @@
+// Internal launch interface of the operators of a state-space block (norm of the residual stream,
+// short causal convolution, selective state-space scan, projections): between the C ABI
+// (falcon_block_abi.cpp) and their kernels.  Not part of the public ABI.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "layer_kernels.h"
+
+namespace falcon {
+
+// out[c] = sum over i < rows of part[i][c], c < cols, in a fixed order; columns from `split` on go to
+// out2[c - split].  Either output may be null.
+hipError_t launch_column_sum(const float *part, int rows, int64_t cols, float *out, int64_t split, float *out2,
+                             hipStream_t s);
+
+// Norm of the residual stream.  Dense rows of `width` entries.
+struct NormArgs {
+  const void *x, *residual;      // forward: input, what it is added to or null; backward: x is the stream
+  const float *w;                // [width] or null (ones)
+  void *s, *y;                   // forward: stream or null, result; backward: y is dx
+  float *scale;                  // [tokens], 8-bit results
+  const void *dy, *ds;           // backward: incoming gradients of the result and (or null) of the stream
+  float *part;                   // backward workspace: per-workgroup weight-gradient sums [blocks, width]
+  int tokens, width, norm;
+  float eps, inv_width;
+};
+size_t norm_bwd_workspace(bool bf16, int tokens, int width);
+hipError_t launch_norm_fwd(bool bf16, bool q8, NormArgs a, hipStream_t s);
+hipError_t launch_norm_bwd(bool bf16, NormArgs a, float *dw, void *ws, hipStream_t s);
+
+// The sequences of a call: n of T tokens each, or (cu != null) packed on one axis of T tokens.
+struct SeqMap {
+  const int *cu;
+  int n, T;
+  __host__ __device__ int tokens() const { return cu ? T : n * T; }
+  // token ranges, kept inside the arrays whatever the offsets hold
+  __host__ __device__ int inside(int t) const { return t < 0 ? 0 : t > T ? T : t; }
+  __host__ __device__ int begin(int i) const { return cu ? inside(cu[i]) : i * T; }
+  __host__ __device__ int end(int i) const { return cu ? inside(cu[i + 1]) : (i + 1) * T; }
+  // the largest i < n that begins at or before token t (0 if none)
+  __host__ __device__ int of(int t) const {
+    if (!cu) return t / T;
+    int lo = 0, len = n;
+    while (len > 1) {
+      const int half = len >> 1;
+      if (cu[lo + half] <= t) { lo += half; len -= half; } else { len = half; }
+    }
+    return lo;
+  }
+};
+
+// Short causal convolution.  x may have a token stride; the rest is dense.
+struct ConvArgs {
+  const void *x, *dy;            // [tokens, D]
+  void *y, *dx;
+  const float *w, *bias;         // [D, taps]; [D] or null
+  const void *init, *d_final;    // [n, taps - 1, D] or null (zeros)
+  void *final_state, *d_init;    // [n, taps - 1, D] or null
+  float *part;                   // backward workspace: sums for the weights [blocks, D taps + D]
+  SeqMap seq;
+  int64_t ldx, lddx;
+  int D, silu, run;              // run: tokens of a thread
+};
+bool conv_fits(bool bf16, SeqMap seq, int D);
+size_t conv_bwd_workspace(bool bf16, int taps, SeqMap seq, int D);
+hipError_t launch_conv_fwd(bool bf16, int taps, ConvArgs a, hipStream_t s);
+hipError_t launch_conv_bwd(bool bf16, int taps, ConvArgs a, float *dw, float *db, void *ws, hipStream_t s);
+hipError_t launch_conv_step(bool bf16, int taps, ConvArgs a, hipStream_t s);
+
+}  // namespace falcon

@@ -1,0 +1,204 @@
+// C ABI of the operators of a state-space block (declared in include/falcon.h): the norm of
+// the residual stream, the short causal convolution, the selective state-space scan and the
+// projections.
+//
+// Host side only, as falcon_layer_abi.cpp: every argument is validated before the first HIP
+// call.
+#include "abi_checks.h"
+#include "block_kernels.h"
+
+using namespace falcon::abi;
+
+// ---- Norm of the residual stream -------------------------------------------------
+namespace {
+
+int check_norm(const falcon_norm_shape_t *s) {
+  if (!s || !float_dtype(s->dtype)) return FALCON_ERR_INVALID_ARG;
+  if (s->tokens < 1 || s->width < 1 || (s->norm != 0 && s->norm != 1)) return FALCON_ERR_INVALID_ARG;
+  if (!std::isfinite(s->eps) || s->eps < 0.f) return FALCON_ERR_INVALID_ARG;
+  if (s->width % 8 != 0 || s->width > 65536 / esize(s->dtype)) return FALCON_ERR_UNSUPPORTED;
+  return s->tokens > INT32_MAX - (1 << 20) ? FALCON_ERR_UNSUPPORTED : FALCON_OK;
+}
+
+falcon::NormArgs norm_args(const falcon_norm_shape_t *s, const float *w) {
+  falcon::NormArgs a{};
+  a.w = w;
+  a.tokens = s->tokens;
+  a.width = s->width;
+  a.norm = s->norm;
+  a.eps = s->eps;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+int falcon_rms_norm(const falcon_norm_shape_t *s, const void *x, const void *residual, const float *weight,
+                    void *stream_out, void *y, float *scale, void *stream) {
+  FALCON_TRY(check_norm(s));
+  const bool q8 = s->out == FALCON_E4M3;
+  if (!q8 && !float_dtype(s->out)) return FALCON_ERR_INVALID_ARG;
+  if (!q8 && s->out != s->dtype) return FALCON_ERR_UNSUPPORTED;
+  FALCON_TRY(need(x, 16));
+  FALCON_TRY(maybe(residual, 16));
+  FALCON_TRY(maybe(weight, 16));
+  FALCON_TRY(maybe(stream_out, 16));
+  FALCON_TRY(need(y, 16));
+  FALCON_TRY(q8 ? need(scale, 4) : maybe(scale, 4));
+  if (residual && y == stream_out) return FALCON_ERR_INVALID_ARG;
+  falcon::NormArgs a = norm_args(s, weight);
+  a.x = x;
+  a.residual = residual;
+  a.s = stream_out;
+  a.y = y;
+  a.scale = scale;
+  return status_of(falcon::launch_norm_fwd(s->dtype == FALCON_BF16, q8, a, static_cast<hipStream_t>(stream)));
+}
+
+size_t falcon_rms_norm_bwd_workspace(const falcon_norm_shape_t *s) {
+  if (check_norm(s) != FALCON_OK) return 0;
+  return falcon::norm_bwd_workspace(s->dtype == FALCON_BF16, s->tokens, s->width);
+}
+
+int falcon_rms_norm_bwd(const falcon_norm_shape_t *s, const void *stream_in, const float *weight, const void *d_y,
+                        const void *d_stream, void *dx, float *dweight, void *ws, size_t ws_bytes, void *stream) {
+  FALCON_TRY(check_norm(s));
+  if (!s->norm) return FALCON_ERR_UNSUPPORTED;
+  FALCON_TRY(need(stream_in, 16));
+  FALCON_TRY(maybe(weight, 16));
+  FALCON_TRY(need(d_y, 16));
+  FALCON_TRY(maybe(d_stream, 16));
+  FALCON_TRY(need(dx, 16));
+  FALCON_TRY(maybe(dweight, 4));
+  if (dweight) FALCON_TRY(check_workspace(ws, ws_bytes, falcon_rms_norm_bwd_workspace(s)));
+  falcon::NormArgs a = norm_args(s, weight);
+  a.x = stream_in;
+  a.dy = d_y;
+  a.ds = d_stream;
+  a.y = dx;
+  return status_of(falcon::launch_norm_bwd(s->dtype == FALCON_BF16, a, dweight, ws, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// ---- Short causal convolution ------------------------------------------------------
+namespace {
+
+int check_seq(int64_t batch, int64_t seqlen, bool packed) {
+  if (batch < 1 || seqlen < 1) return FALCON_ERR_INVALID_ARG;
+  // token and sequence numbers are ints, with a workgroup's tokens added
+  if (batch > (1 << 30) || seqlen > INT32_MAX - 4096 || (!packed && batch * seqlen > INT32_MAX - 4096))
+    return FALCON_ERR_UNSUPPORTED;
+  return FALCON_OK;
+}
+
+falcon::SeqMap seq_map(int batch, int seqlen, const int32_t *cu) { return falcon::SeqMap{cu, batch, seqlen}; }
+
+// The same for queries of sizes, where any non-null offsets mark a packed call.
+falcon::SeqMap seq_sizes(int batch, int seqlen, bool packed) {
+  static const int32_t mark = 0;
+  return falcon::SeqMap{packed ? &mark : nullptr, batch, seqlen};
+}
+
+int check_conv(const falcon_conv_shape_t *s, bool packed, bool step) {
+  if (!s || !float_dtype(s->dtype)) return FALCON_ERR_INVALID_ARG;
+  if (s->activation < FALCON_ACT_NONE || s->activation > FALCON_ACT_GELU) return FALCON_ERR_INVALID_ARG;
+  if (s->width < 1 || s->taps < 1) return FALCON_ERR_INVALID_ARG;
+  FALCON_TRY(check_seq(s->batch, step ? 1 : s->seqlen, packed));
+  if (s->activation == FALCON_ACT_GELU || s->taps < 2 || s->taps > 4) return FALCON_ERR_UNSUPPORTED;
+  if (s->width % 8 != 0 || s->width > (1 << 20)) return FALCON_ERR_UNSUPPORTED;
+  const bool bf16 = s->dtype == FALCON_BF16;
+  if (step) {
+    const int64_t threads = (int64_t)s->batch * s->width * esize(s->dtype) / 16;
+    return falcon::grid_fits((threads + 255) / 256, 256) ? FALCON_OK : FALCON_ERR_UNSUPPORTED;
+  }
+  return falcon::conv_fits(bf16, seq_sizes(s->batch, s->seqlen, packed), s->width) ? FALCON_OK : FALCON_ERR_UNSUPPORTED;
+}
+
+falcon::ConvArgs conv_args(const falcon_conv_shape_t *s, const int32_t *cu, falcon_heads_t x, const float *w,
+                           const float *bias) {
+  falcon::ConvArgs a{};
+  a.seq = seq_map(s->batch, s->seqlen, cu);
+  a.x = x.data;
+  a.ldx = x.token_stride;
+  a.w = w;
+  a.bias = bias;
+  a.D = s->width;
+  a.silu = s->activation == FALCON_ACT_SILU;
+  return a;
+}
+
+int check_conv_in(const falcon_conv_shape_t *s, int64_t tokens, falcon_heads_t x, const float *w, const float *bias) {
+  FALCON_TRY(check_rows(x.data, x.token_stride, tokens, s->width, esize(s->dtype)));
+  FALCON_TRY(need(w, 4));
+  return maybe(bias, 4);
+}
+
+int64_t seq_tokens(int64_t batch, int64_t seqlen, bool packed) { return packed ? seqlen : batch * seqlen; }
+
+}  // namespace
+
+extern "C" {
+
+int falcon_conv_fwd(const falcon_conv_shape_t *s, const int32_t *cu, falcon_heads_t x, const float *w, const float *bias,
+                    const void *init, void *final_state, void *y, void *stream) {
+  FALCON_TRY(check_conv(s, cu != nullptr, false));
+  FALCON_TRY(maybe(cu, 4));
+  FALCON_TRY(check_conv_in(s, seq_tokens(s->batch, s->seqlen, cu), x, w, bias));
+  FALCON_TRY(maybe(init, 16));
+  FALCON_TRY(maybe(final_state, 16));
+  FALCON_TRY(need(y, 16));
+  falcon::ConvArgs a = conv_args(s, cu, x, w, bias);
+  a.init = init;
+  a.final_state = final_state;
+  a.y = y;
+  return status_of(falcon::launch_conv_fwd(s->dtype == FALCON_BF16, s->taps, a, static_cast<hipStream_t>(stream)));
+}
+
+size_t falcon_conv_bwd_workspace(const falcon_conv_shape_t *s, int packed) {
+  if (check_conv(s, packed != 0, false) != FALCON_OK) return 0;
+  return falcon::conv_bwd_workspace(s->dtype == FALCON_BF16, s->taps, seq_sizes(s->batch, s->seqlen, packed != 0), s->width);
+}
+
+int falcon_conv_bwd(const falcon_conv_shape_t *s, const int32_t *cu, falcon_heads_t x, const float *w, const float *bias,
+                    const void *init, const void *d_y, const void *d_final, falcon_heads_out_t dx, float *dw, float *db,
+                    void *d_init, void *ws, size_t ws_bytes, void *stream) {
+  FALCON_TRY(check_conv(s, cu != nullptr, false));
+  FALCON_TRY(maybe(cu, 4));
+  const int64_t tokens = seq_tokens(s->batch, s->seqlen, cu);
+  FALCON_TRY(check_conv_in(s, tokens, x, w, bias));
+  FALCON_TRY(maybe(init, 16));
+  FALCON_TRY(need(d_y, 16));
+  FALCON_TRY(maybe(d_final, 16));
+  FALCON_TRY(check_rows(dx.data, dx.token_stride, tokens, s->width, esize(s->dtype)));
+  FALCON_TRY(maybe(dw, 4));
+  FALCON_TRY(maybe(db, 4));
+  FALCON_TRY(maybe(d_init, 16));
+  if (dw || db) FALCON_TRY(check_workspace(ws, ws_bytes, falcon_conv_bwd_workspace(s, cu != nullptr)));
+  falcon::ConvArgs a = conv_args(s, cu, x, w, bias);
+  a.init = init;
+  a.dy = d_y;
+  a.d_final = d_final;
+  a.dx = dx.data;
+  a.lddx = dx.token_stride;
+  a.d_init = d_init;
+  return status_of(falcon::launch_conv_bwd(s->dtype == FALCON_BF16, s->taps, a, dw, db, ws,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+int falcon_conv_step(const falcon_conv_shape_t *s, falcon_heads_t x, const float *w, const float *bias, const void *state,
+                     void *state_out, void *y, void *stream) {
+  FALCON_TRY(check_conv(s, false, true));
+  FALCON_TRY(check_conv_in(s, s->batch, x, w, bias));
+  FALCON_TRY(need(state, 16));
+  FALCON_TRY(need(state_out, 16));
+  FALCON_TRY(need(y, 16));
+  falcon::ConvArgs a = conv_args(s, nullptr, x, w, bias);
+  a.init = state;
+  a.final_state = state_out;
+  a.y = y;
+  return status_of(falcon::launch_conv_step(s->dtype == FALCON_BF16, s->taps, a, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

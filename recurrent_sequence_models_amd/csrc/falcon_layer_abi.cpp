@@ -4,44 +4,15 @@
 // Host side only, as falcon_abi.cpp: every argument is validated before the first HIP
 // call.  The kernels live in falcon_scan.hip, falcon_qk.hip, falcon_attn.hip and
 // falcon_attn_bwd.hip.
-#include "falcon.h"
+#include "abi_checks.h"
 
-#include <cmath>
-#include <cstdint>
-
-#include "layer_kernels.h"
-
-namespace {
-
-bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-bool dtype_ok(int d) { return d == FALCON_F32 || d == FALCON_BF16; }
-int esize(int dtype) { return dtype == FALCON_BF16 ? 2 : 4; }
-
-// A required (or, if null, optional) pointer with its alignment.
-int need(const void *p, unsigned align) { return p && aligned(p, align) ? FALCON_OK : FALCON_ERR_INVALID_ARG; }
-int maybe(const void *p, unsigned align) { return aligned(p, align) ? FALCON_OK : FALCON_ERR_INVALID_ARG; }
-
-int status_of(hipError_t e) { return e == hipSuccess ? FALCON_OK : FALCON_ERR_HIP; }
-
-int check_workspace(const void *ws, size_t have, size_t want) {
-  if (want == 0) return FALCON_OK;
-  if (!ws || have < want) return FALCON_ERR_WORKSPACE;
-  return maybe(ws, 16);
-}
-
-}  // namespace
-
-#define FALCON_TRY(x)                        \
-  do {                                       \
-    const int st_ = (x);                     \
-    if (st_ != FALCON_OK) return st_;        \
-  } while (0)
+using namespace falcon::abi;
 
 // ---- Gated linear recurrence ---------------------------------------------------
 namespace {
 
 int check_scan(const falcon_scan_shape_t *s, bool packed, bool step) {
-  if (!s || !dtype_ok(s->dtype)) return FALCON_ERR_INVALID_ARG;
+  if (!s || !float_dtype(s->dtype)) return FALCON_ERR_INVALID_ARG;
   if (s->input != FALCON_SCAN_ADD && s->input != FALCON_SCAN_MIX) return FALCON_ERR_INVALID_ARG;
   if (s->batch < 1 || s->width < 1 || (!step && s->seqlen < 1)) return FALCON_ERR_INVALID_ARG;
   if (s->width % 8 != 0 || s->width > (1 << 20)) return FALCON_ERR_UNSUPPORTED;
@@ -149,7 +120,7 @@ int check_d(int d) { return d == 32 || d == 64 || d == 128 ? FALCON_OK : FALCON_
 
 // ---- Query / key norm with rotary positions --------------------------------------
 int check_qk(const falcon_qk_shape_t *s) {
-  if (!s || !dtype_ok(s->dtype) || !dtype_ok(s->grad_dtype)) return FALCON_ERR_INVALID_ARG;
+  if (!s || !float_dtype(s->dtype) || !float_dtype(s->grad_dtype)) return FALCON_ERR_INVALID_ARG;
   if (s->tokens < 1 || s->heads_q < 1 || s->heads_k < 1 || s->d < 1) return FALCON_ERR_INVALID_ARG;
   if (s->layout != FALCON_ROPE_HALF && s->layout != FALCON_ROPE_INTERLEAVED) return FALCON_ERR_INVALID_ARG;
   if (s->norm != 0 && s->norm != 1) return FALCON_ERR_INVALID_ARG;
@@ -281,7 +252,7 @@ falcon::AttnArgs size_args(const falcon_attn_shape_t *s, bool packed) {
 }
 
 int check_attn(const falcon_attn_shape_t *s, bool packed) {
-  if (!s || !dtype_ok(s->dtype)) return FALCON_ERR_INVALID_ARG;
+  if (!s || !float_dtype(s->dtype)) return FALCON_ERR_INVALID_ARG;
   if (s->batch < 1 || s->seqlen_q < 1 || s->seqlen_k < 1 || s->heads_q < 1 || s->heads_k < 1 || s->d < 1)
     return FALCON_ERR_INVALID_ARG;
   if (s->heads_q % s->heads_k != 0) return FALCON_ERR_INVALID_ARG;

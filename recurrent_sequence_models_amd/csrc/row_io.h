@@ -1,0 +1,64 @@
+// Rows of bf16 or fp32 entries, 16 bytes a lane, as the block operators read and write them.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include "lane_ops.h"
+#include "mfma_frag.h"
+
+namespace falcon {
+
+typedef unsigned int u4 __attribute__((ext_vector_type(4)));   // 16 bytes of entries, in registers
+
+template <typename T> constexpr int PER16 = 16 / (int)sizeof(T);   // entries in 16 bytes
+
+__device__ __forceinline__ void widen(const u4 &u, float (&o)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    o[2 * j] = __uint_as_float(u[j] << 16);
+    o[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void widen(const u4 &u, float (&o)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o[j] = __uint_as_float(u[j]);
+}
+// Rounded to nearest even: the one rounding of a result held in bf16.
+__device__ __forceinline__ u4 narrow(const float (&v)[8]) {
+  bf8 b;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) b[j] = (__bf16)v[j];
+  return __builtin_bit_cast(u4, b);
+}
+__device__ __forceinline__ u4 narrow(const float (&v)[4]) {
+  return u4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+}
+template <typename T> __device__ __forceinline__ u4 load16(const T *p) { return *reinterpret_cast<const u4 *>(p); }
+template <typename T> __device__ __forceinline__ void store16(T *p, const u4 &v) { *reinterpret_cast<u4 *>(p) = v; }
+template <int N> __device__ __forceinline__ void load_f32(const float *p, float (&o)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; j += 4) {
+    const f4 v = *reinterpret_cast<const f4 *>(p + j);
+    o[j] = v[0]; o[j + 1] = v[1]; o[j + 2] = v[2]; o[j + 3] = v[3];
+  }
+}
+template <int N> __device__ __forceinline__ void store_f32(float *p, const float (&v)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; j += 4) *reinterpret_cast<f4 *>(p + j) = f4{v[j], v[j + 1], v[j + 2], v[j + 3]};
+}
+
+// Sum over the 64 lanes of a wave, in each of them.
+__device__ __forceinline__ float wave_sum(float x) { return add_xor32(add_xor16(lane_sum<16>(x))); }
+// The largest of 64 lanes' unsigned values, in each of them.
+__device__ __forceinline__ unsigned wave_max(unsigned x) {
+#pragma unroll
+  for (int k = 1; k < 64; k *= 2) x = max(x, (unsigned)__shfl_xor((int)x, k));
+  return x;
+}
+
+// 1 / (1 + e^-v) by the hardware's exp2 and reciprocal (each within one step): exact 0 and 1 at the ends, as
+// e^-v becomes infinite or 0 there.
+__device__ __forceinline__ float sigmoid(float v) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -1.44269504088896f));
+}
+
+}  // namespace falcon

@@ -27,7 +27,10 @@ EXPORTS = ("falcon_abi_version", "falcon_status_string", "falcon_chunk_fwd_works
            # the layer operators (layer.py)
            "falcon_scan_workspace", "falcon_scan_fwd", "falcon_scan_bwd", "falcon_scan_step",
            "falcon_qk_norm_rope", "falcon_qk_norm_rope_bwd_workspace", "falcon_qk_norm_rope_bwd",
-           "falcon_attn_fwd_workspace", "falcon_attn_fwd", "falcon_attn_bwd_workspace", "falcon_attn_bwd")
+           "falcon_attn_fwd_workspace", "falcon_attn_fwd", "falcon_attn_bwd_workspace", "falcon_attn_bwd",
+           # the operators of a state-space block (block.py)
+           "falcon_rms_norm", "falcon_rms_norm_bwd_workspace", "falcon_rms_norm_bwd",
+           "falcon_conv_fwd", "falcon_conv_bwd_workspace", "falcon_conv_bwd", "falcon_conv_step")
 
 
 class Shape(ctypes.Structure):
@@ -59,6 +62,16 @@ class AttnShape(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("seqlen_q", ctypes.c_int32),
                 ("seqlen_k", ctypes.c_int32), ("heads_q", ctypes.c_int32), ("heads_k", ctypes.c_int32),
                 ("d", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class NormShape(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("tokens", ctypes.c_int32), ("width", ctypes.c_int32),
+                ("norm", ctypes.c_int32), ("out", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class ConvShape(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("seqlen", ctypes.c_int32),
+                ("width", ctypes.c_int32), ("taps", ctypes.c_int32), ("activation", ctypes.c_int32)]
 
 
 class Heads(ctypes.Structure):
@@ -136,6 +149,20 @@ def lib() -> ctypes.CDLL:
         L.falcon_attn_bwd_workspace.argtypes = [P(AttnShape), I]
         L.falcon_attn_bwd.restype = I
         L.falcon_attn_bwd.argtypes = [P(AttnShape), V, V, Heads, Heads, Heads, V, V, Heads, Heads, Heads, Heads, V, S, V]
+        L.falcon_rms_norm.restype = I
+        L.falcon_rms_norm.argtypes = [P(NormShape), V, V, V, V, V, V, V]
+        L.falcon_rms_norm_bwd_workspace.restype = S
+        L.falcon_rms_norm_bwd_workspace.argtypes = [P(NormShape)]
+        L.falcon_rms_norm_bwd.restype = I
+        L.falcon_rms_norm_bwd.argtypes = [P(NormShape), V, V, V, V, V, V, V, S, V]
+        L.falcon_conv_fwd.restype = I
+        L.falcon_conv_fwd.argtypes = [P(ConvShape), V, Heads, V, V, V, V, V, V]
+        L.falcon_conv_bwd_workspace.restype = S
+        L.falcon_conv_bwd_workspace.argtypes = [P(ConvShape), I]
+        L.falcon_conv_bwd.restype = I
+        L.falcon_conv_bwd.argtypes = [P(ConvShape), V, Heads, V, V, V, V, V, Heads, V, V, V, V, S, V]
+        L.falcon_conv_step.restype = I
+        L.falcon_conv_step.argtypes = [P(ConvShape), Heads, V, V, V, V, V, V]
         _LIB = L
     return _LIB
 
