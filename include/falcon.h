@@ -597,6 +597,55 @@ int falcon_conv_bwd(const falcon_conv_shape_t *shape, const int32_t *cu_seqlens,
 int falcon_conv_step(const falcon_conv_shape_t *shape, falcon_heads_t x, const float *weight, const float *bias,
                      const void *state, void *state_out, void *y, void *stream);
 
+/* ---- Selective state-space scan --------------------------------------------
+ * Per sequence, channel d and state n, with delta_t = softplus(dt_t + dt_bias)
+ * (softplus = 0: delta_t = dt_t + dt_bias):
+ *   h_t = exp(delta_t A[d][n]) h_{t-1} + delta_t x_t B_t[n]
+ *   y_t = (sum_n C_t[n] h_t[n] + D[d] x_t) silu(z_t)         (z NULL: no gate)
+ * B_t and C_t are shared by the channels.  A is finite; where delta_t A > 0 the state
+ * grows, and its growth over FALCON_SSM_CHUNK steps (a long sequence: over all of them)
+ * has to stay in fp32's range.  States, sums and delta are fp32. */
+typedef struct {
+  int32_t dtype;     /* falcon_dtype_t of x, dt, B, C, z, y and their gradients: F32 or BF16 */
+  int32_t batch;     /* sequences, >= 1 */
+  int32_t seqlen;    /* tokens of every sequence, >= 1; packed: all tokens.  At most 2^31 - 1 - 4096 in all */
+  int32_t width;     /* channels, a multiple of 8, at most 2^20 */
+  int32_t state;     /* N: 16, 32 or 64 */
+  int32_t softplus;  /* 0 or 1 */
+} falcon_ssm_shape_t;
+
+#define FALCON_SSM_CHUNK 64   /* steps between the states the forward keeps */
+
+/* Bytes of workspace of the forward: the maps of segments, where few long sequences are
+ * cut to run in parallel; 0 where none may be (then workspace may be NULL), and for invalid
+ * shapes.  `packed` is nonzero for calls with cu_seqlens. */
+size_t falcon_ssm_fwd_workspace(const falcon_ssm_shape_t *shape, int packed);
+
+/* Chunks that the forward keeps a state of: batch ceil(T / FALCON_SSM_CHUNK), or packed
+ * floor(T / FALCON_SSM_CHUNK) + batch (chunk c of sequence n, which begins at token s, is
+ * number floor(s / FALCON_SSM_CHUNK) + n + c; some stay unused).  0 for invalid shapes. */
+int32_t falcon_ssm_chunks(const falcon_ssm_shape_t *shape, int packed);
+
+/*   cu_seqlens   NULL: x, dt, z, y are [B, T, D] and Bm, Cm [B, T, N].  Otherwise [B + 1] offsets,
+ *                and they are [T, ...].
+ *   A            [D, N] fp32;  D, dt_bias  [D] fp32, or NULL (zeros).
+ *   z            {NULL, 0}: no gate.
+ *   init         [B, D, N] fp32, or NULL for zeros.
+ *   final_state  [B, D, N] fp32, or NULL.  An empty sequence's is its initial state.
+ *   chunk_states [falcon_ssm_chunks, D, N] fp32, or NULL: h before every chunk of a sequence,
+ *                for the backward pass.
+ * Outputs must not overlap inputs (final_state may not be init). */
+int falcon_ssm_fwd(const falcon_ssm_shape_t *shape, const int32_t *cu_seqlens, falcon_heads_t x, falcon_heads_t dt,
+                   const float *A, falcon_heads_t Bm, falcon_heads_t Cm, const float *D, falcon_heads_t z,
+                   const float *dt_bias, const float *init, float *final_state, void *y, float *chunk_states,
+                   void *workspace, size_t workspace_bytes, void *stream);
+
+/* One step of every sequence: x, dt, z, y [B, D], Bm, Cm [B, N]; state, state_out [B, D, N] fp32
+ * (state_out may be state itself).  shape->seqlen is ignored. */
+int falcon_ssm_step(const falcon_ssm_shape_t *shape, falcon_heads_t x, falcon_heads_t dt, const float *A,
+                    falcon_heads_t Bm, falcon_heads_t Cm, const float *D, falcon_heads_t z, const float *dt_bias,
+                    const float *state, float *state_out, void *y, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -11,10 +11,11 @@ from __future__ import annotations
 import ctypes
 import functools
 
-from .falcon import ConvShape, Heads, NormShape, lib
+from .falcon import ConvShape, Heads, NormShape, SsmShape, lib
 from .layer import _check, _current, _device, _done, _dtype, _ints, _offsets, _on, _p, _workspace
 
-E4M3 = 2   # FALCON_E4M3
+E4M3 = 2         # FALCON_E4M3
+SSM_CHUNK = 64   # FALCON_SSM_CHUNK
 ACTIVATIONS = {None: 0, "silu": 1, "gelu": 2}
 
 
@@ -270,4 +271,92 @@ def causal_conv_step(x, weight, state, *, bias=None, activation=None, state_out=
         shape, _ = _conv_plan(dt, B, 1, D, taps, _activation(activation), False)
         _done(lib().falcon_conv_step(shape, hx, _p(weight), _p(bias), _p(state), _p(state_out), _p(out), _current(dev)),
               "falcon_conv_step")
+    return out
+
+
+# ---- Selective state-space scan ------------------------------------------------------------
+
+_NO_ROWS = Heads(None, 0)
+
+
+@functools.lru_cache(maxsize=1024)
+def _ssm_plan(dtype, n, T, D, N, softplus, packed):
+    """(pointer to the C shape, chunks, workspace bytes of the forward)."""
+    shape = SsmShape(dtype, *_ints(n, T, D, N), softplus)
+    L, ref = lib(), ctypes.byref(shape)
+    return ctypes.pointer(shape), L.falcon_ssm_chunks(ref, packed), L.falcon_ssm_fwd_workspace(ref, packed)
+
+
+def _ssm_args(x, dt, A, B, C, D, z, dt_bias):
+    """The checked arguments as the C calls take them, (x, dt, A, B, C, D, z, dt_bias)."""
+    import torch
+    dev, lead, width = x.device, x.shape[:-1], x.shape[-1]
+    if A.dim() != 2:
+        raise ValueError(f"A: shape {tuple(A.shape)}, expected [D, N]")
+    N = A.shape[1]
+    _check("A", A, torch.float32, (width, N), dev)
+    _maybe("D", D, torch.float32, (width,), dev)
+    _maybe("dt_bias", dt_bias, torch.float32, (width,), dev)
+    kind, states = x.dtype, lead + (N,)
+    return (_rows("x", x, kind, dev), _rows("dt", dt, kind, dev, x.shape), _p(A), _rows("B", B, kind, dev, states),
+            _rows("C", C, kind, dev, states), _p(D), _NO_ROWS if z is None else _rows("z", z, kind, dev, x.shape), _p(dt_bias))
+
+
+def selective_scan(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, softplus=True, cu_seqlens=None, init=None, final=True,
+                   chunk_states=False, out=None, workspace=None, stream=None):
+    """falcon_ssm_fwd on torch tensors: per channel d and state n, with delta =
+    softplus(dt + dt_bias) (or dt + dt_bias without ``softplus``),
+    h_t = exp(delta_t A[d,n]) h_{t-1} + delta_t x_t B_t[n] and
+    y_t = (sum_n C_t[n] h_t + D[d] x_t) silu(z_t).
+
+    x, dt, z [B,T,D] and B, C [B,T,N] (float32 or bfloat16, D a multiple of 8, N 16, 32 or
+    64; views of a wider projection will do), or [total,...] with ``cu_seqlens``, an int32
+    device tensor [N+1] of token offsets.  A [D,N], D, dt_bias [D] float32; D, z and
+    dt_bias may be None.  ``init``: None or [N,D,N] float32.  ``final``: True (allocate),
+    such a tensor to write, or False.  ``chunk_states``: whether to keep what
+    selective_scan_bwd needs.  Tokens behind cu_seqlens[N] are not written.
+    Returns (y, final, chunk_states)."""
+    import torch
+    kind, dev = _dtype("x", x), _device("x", x)
+    n, T = _sequences(x, cu_seqlens)
+    args = _ssm_args(x, dt, A, B, C, D, z, dt_bias)
+    width, N = A.shape
+    shape, chunks, need = _ssm_plan(kind, n, T, width, N, 1 if softplus else 0, cu_seqlens is not None)
+    _maybe("init", init, torch.float32, (n, width, N), dev)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        else:
+            _check("y", out, x.dtype, x.shape, dev)
+        final = x.new_empty((n, width, N), dtype=torch.float32) if final is True else None if final is False else final
+        _maybe("final", final, torch.float32, (n, width, N), dev)
+        states = x.new_empty((chunks, width, N), dtype=torch.float32) if chunk_states else None
+        ws, nbytes = _workspace(need, workspace, dev)
+        _done(lib().falcon_ssm_fwd(shape, _p(cu_seqlens), *args, _p(init), _p(final), _p(out), _p(states), _p(ws), nbytes,
+                                   _current(dev)), "falcon_ssm_fwd")
+    return out, final, states
+
+
+def selective_scan_step(x, dt, A, B, C, state, *, D=None, z=None, dt_bias=None, softplus=True, state_out=None, out=None,
+                        stream=None):
+    """falcon_ssm_step: one token of every sequence; x, dt, z [B,D], B, C [B,N], ``state``
+    [B,D,N] float32 updated in place, or left as it is with ``state_out``, a tensor for
+    the new state.  Returns y [B,D] in the dtype of x."""
+    import torch
+    kind, dev = _dtype("x", x), _device("x", x)
+    if x.dim() != 2:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected [B, D]")
+    args = _ssm_args(x, dt, A, B, C, D, z, dt_bias)
+    n, (width, N) = x.shape[0], A.shape
+    if state_out is None:
+        state_out = state
+    for name, t in (("state", state), ("state_out", state_out)):
+        _check(name, t, torch.float32, (n, width, N), dev)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((n, width), dtype=x.dtype, device=dev)
+        else:
+            _check("y", out, x.dtype, x.shape, dev)
+        shape, _, _ = _ssm_plan(kind, n, 1, width, N, 1 if softplus else 0, False)
+        _done(lib().falcon_ssm_step(shape, *args, _p(state), _p(state_out), _p(out), _current(dev)), "falcon_ssm_step")
     return out

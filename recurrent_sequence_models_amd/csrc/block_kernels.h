@@ -69,4 +69,22 @@ hipError_t launch_conv_fwd(bool bf16, int taps, ConvArgs a, hipStream_t s);
 hipError_t launch_conv_bwd(bool bf16, int taps, ConvArgs a, float *dw, float *db, void *ws, hipStream_t s);
 hipError_t launch_conv_step(bool bf16, int taps, ConvArgs a, hipStream_t s);
 
+// Selective state-space scan.  x, dt, z [tokens, D] and B, C [tokens, N] may have token strides.
+struct SsmArgs {
+  const void *x, *dt, *z, *B, *C;   // z may be null
+  const float *A, *skip, *bias;     // [D, N]; [D] or null; [D] or null
+  const float *init;                // [n, D, N] or null (zeros); single tokens: the state
+  float *final_state;               // [n, D, N] or null; single tokens: the new state
+  void *y;                          // [tokens, D]
+  float *states;                    // [chunks, D, N]: the state before every chunk, or null
+  float *seg_map, *seg_state, *seg_sum;   // workspace, by segment: end state from zero, first state, sum of delta
+  SeqMap seq;
+  int64_t ldx, lddt, ldz, ldB, ldC;
+  int D, softplus, seg;             // seg: tokens of a segment
+};
+bool ssm_fits(SeqMap seq, int D);
+size_t ssm_fwd_workspace(SeqMap seq, int D, int N);
+hipError_t launch_ssm_fwd(bool bf16, int N, SsmArgs a, void *ws, hipStream_t s);
+hipError_t launch_ssm_step(bool bf16, int N, SsmArgs a, hipStream_t s);
+
 }  // namespace falcon

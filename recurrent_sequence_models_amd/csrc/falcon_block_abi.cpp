@@ -202,3 +202,101 @@ int falcon_conv_step(const falcon_conv_shape_t *s, falcon_heads_t x, const float
 }
 
 }  // extern "C"
+
+// ---- Selective state-space scan ------------------------------------------------------
+namespace {
+
+int check_ssm(const falcon_ssm_shape_t *s, bool packed, bool step) {
+  if (!s || !float_dtype(s->dtype)) return FALCON_ERR_INVALID_ARG;
+  if (s->width < 1 || s->state < 1 || (s->softplus != 0 && s->softplus != 1)) return FALCON_ERR_INVALID_ARG;
+  FALCON_TRY(check_seq(s->batch, step ? 1 : s->seqlen, packed));
+  if (s->state != 16 && s->state != 32 && s->state != 64) return FALCON_ERR_UNSUPPORTED;
+  if (s->width % 8 != 0 || s->width > (1 << 20)) return FALCON_ERR_UNSUPPORTED;
+  if (step) {
+    const int64_t threads = (int64_t)s->batch * s->width * (s->state / 4);
+    return falcon::grid_fits((threads + 255) / 256, 256) ? FALCON_OK : FALCON_ERR_UNSUPPORTED;
+  }
+  return falcon::ssm_fits(seq_sizes(s->batch, s->seqlen, packed), s->width) ? FALCON_OK : FALCON_ERR_UNSUPPORTED;
+}
+
+int check_ssm_in(const falcon_ssm_shape_t *s, int64_t tokens, falcon_heads_t x, falcon_heads_t dt, const float *A,
+                 falcon_heads_t B, falcon_heads_t C, const float *D, falcon_heads_t z, const float *bias) {
+  const int e = esize(s->dtype);
+  FALCON_TRY(check_rows(x.data, x.token_stride, tokens, s->width, e));
+  FALCON_TRY(check_rows(dt.data, dt.token_stride, tokens, s->width, e));
+  FALCON_TRY(need(A, 16));
+  FALCON_TRY(check_rows(B.data, B.token_stride, tokens, s->state, e));
+  FALCON_TRY(check_rows(C.data, C.token_stride, tokens, s->state, e));
+  FALCON_TRY(maybe(D, 4));
+  if (z.data) FALCON_TRY(check_rows(z.data, z.token_stride, tokens, s->width, e));
+  return maybe(bias, 4);
+}
+
+falcon::SsmArgs ssm_args(const falcon_ssm_shape_t *s, const int32_t *cu, falcon_heads_t x, falcon_heads_t dt,
+                         const float *A, falcon_heads_t B, falcon_heads_t C, const float *D, falcon_heads_t z,
+                         const float *bias) {
+  falcon::SsmArgs a{};
+  a.seq = seq_map(s->batch, s->seqlen, cu);
+  a.x = x.data; a.dt = dt.data; a.z = z.data; a.B = B.data; a.C = C.data;
+  a.ldx = x.token_stride; a.lddt = dt.token_stride; a.ldz = z.token_stride;
+  a.ldB = B.token_stride; a.ldC = C.token_stride;
+  a.A = A;
+  a.skip = D;
+  a.bias = bias;
+  a.D = s->width;
+  a.softplus = s->softplus;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t falcon_ssm_fwd_workspace(const falcon_ssm_shape_t *s, int packed) {
+  if (check_ssm(s, packed != 0, false) != FALCON_OK) return 0;
+  return falcon::ssm_fwd_workspace(seq_sizes(s->batch, s->seqlen, packed != 0), s->width, s->state);
+}
+
+int32_t falcon_ssm_chunks(const falcon_ssm_shape_t *s, int packed) {
+  if (check_ssm(s, packed != 0, false) != FALCON_OK) return 0;
+  if (packed) return s->seqlen / FALCON_SSM_CHUNK + s->batch;
+  return s->batch * ((s->seqlen + FALCON_SSM_CHUNK - 1) / FALCON_SSM_CHUNK);
+}
+
+int falcon_ssm_fwd(const falcon_ssm_shape_t *s, const int32_t *cu, falcon_heads_t x, falcon_heads_t dt, const float *A,
+                   falcon_heads_t B, falcon_heads_t C, const float *D, falcon_heads_t z, const float *bias,
+                   const float *init, float *final_state, void *y, float *chunk_states, void *ws, size_t ws_bytes,
+                   void *stream) {
+  FALCON_TRY(check_ssm(s, cu != nullptr, false));
+  FALCON_TRY(maybe(cu, 4));
+  FALCON_TRY(check_ssm_in(s, seq_tokens(s->batch, s->seqlen, cu), x, dt, A, B, C, D, z, bias));
+  FALCON_TRY(maybe(init, 16));
+  FALCON_TRY(maybe(final_state, 16));
+  FALCON_TRY(need(y, 16));
+  FALCON_TRY(maybe(chunk_states, 16));
+  FALCON_TRY(check_workspace(ws, ws_bytes, falcon_ssm_fwd_workspace(s, cu != nullptr)));
+  falcon::SsmArgs a = ssm_args(s, cu, x, dt, A, B, C, D, z, bias);
+  a.init = init;
+  a.final_state = final_state;
+  a.y = y;
+  a.states = chunk_states;
+  return status_of(falcon::launch_ssm_fwd(s->dtype == FALCON_BF16, s->state, a, ws, static_cast<hipStream_t>(stream)));
+}
+
+int falcon_ssm_step(const falcon_ssm_shape_t *s, falcon_heads_t x, falcon_heads_t dt, const float *A, falcon_heads_t B,
+                    falcon_heads_t C, const float *D, falcon_heads_t z, const float *bias, const float *state,
+                    float *state_out, void *y, void *stream) {
+  FALCON_TRY(check_ssm(s, false, true));
+  FALCON_TRY(check_ssm_in(s, s->batch, x, dt, A, B, C, D, z, bias));
+  FALCON_TRY(need(state, 16));
+  FALCON_TRY(need(state_out, 16));
+  FALCON_TRY(need(y, 16));
+  falcon::SsmArgs a = ssm_args(s, nullptr, x, dt, A, B, C, D, z, bias);
+  a.seq.T = 1;
+  a.init = state;
+  a.final_state = state_out;
+  a.y = y;
+  return status_of(falcon::launch_ssm_step(s->dtype == FALCON_BF16, s->state, a, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

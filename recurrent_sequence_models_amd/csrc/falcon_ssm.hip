@@ -1,0 +1,312 @@
+// Selective state-space scan on gfx950, forward and for single tokens.
+//
+// Per sequence, channel d and state n, with delta_t = softplus(dt_t + bias) (or dt_t + bias):
+//   h_t = exp(delta_t A_dn) h_{t-1} + delta_t x_t B_tn
+//   y_t = (sum_n C_tn h_t + D_d x_t) silu(z_t)
+//
+// A tile's steps pass through LDS once: (delta, delta x) of its channels, B and C.  The waves of a
+// workgroup that lie behind each other in time each compose their 16 steps first, h -> P h + H
+// with P = exp(A sum of delta), keeping the 64 decays of a lane in registers; then every wave
+// joins the maps before its own to the tile's first state and runs its steps again from there,
+// without an exponential.  So a workgroup has 4 times as many steps in flight as a plain recurrence
+// and pays 12 instructions for 4 states and a step where that pays 12 less an exchange of maps.
+//
+// Few long sequences: they are cut into segments, whose maps a pass of its own forms, and which then
+// run in parallel.
+//
+// Bound: the vector unit: per state and step one exponential and 6 multiplications and additions.
+#include "ssm_common.h"
+
+namespace falcon {
+namespace {
+
+// What a thread loads of a tile: VEC channels of one step, and two entries of B and C.
+template <typename T, int N> struct Loaded {
+  static constexpr int V = SsmTile<N>::VEC;
+  float x[V], dt[V], z[V], B[2], C[2];
+};
+
+// MAPS: only the segment's map (end state from zero, sum of delta) is formed.
+template <typename T, int N, bool MAPS> __global__ __launch_bounds__(SSM_THR, 4) void ssm_fwd(SsmArgs a) {
+  typedef SsmTile<N> L;
+  constexpr int V = L::VEC;
+  __shared__ __align__(16) float2 step[L::TS][SSM_CH];        // (delta, delta x); then (y, -)
+  __shared__ __align__(16) float sB[L::TS][N], sC[L::TS][N];
+  __shared__ __align__(16) float mapP[L::TW][SSM_CH][N], mapH[L::TW][SSM_CH][N];
+  __shared__ float sumd[L::TW][SSM_CH];
+  const int groups = (a.D + SSM_CH - 1) / SSM_CH;
+  const int slots = slots_of(a.seq, a.seg), id = dealt(groups * slots);
+  if (id >= groups * slots) return;
+  const Segment g = find_segment(a.seq, a.seg, id / groups);
+  const int c0 = (id % groups) * SSM_CH;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tw = wave / L::WIDE, ch = (wave % L::WIDE) * L::CW + lane / L::P, p4 = (lane % L::P) * 4;
+  const int c = c0 + ch;                      // this lane's channel
+  const bool on = c < a.D;
+  // an empty sequence has one slot, in which it ends where it began
+  if (!g.any && !(g.s == g.e && g.slot == first_slot(a.seq, g.n, a.seg))) return;
+  const bool first = g.t0 == g.s, lastseg = g.t1 == g.e;
+  if constexpr (MAPS) { if (lastseg) return; }      // nobody starts from its end
+  f4 A2{0.f, 0.f, 0.f, 0.f}, h{0.f, 0.f, 0.f, 0.f};
+  if (on) {
+    A2 = *reinterpret_cast<const f4 *>(a.A + (size_t)c * N + p4) * SSM_LOG2E;
+    if constexpr (!MAPS) {
+      if (!first) h = *reinterpret_cast<const f4 *>(a.seg_state + ((size_t)g.slot * a.D + c) * N + p4);
+      else if (a.init) h = *reinterpret_cast<const f4 *>(a.init + ((size_t)g.n * a.D + c) * N + p4);
+    }
+  }
+  // the part of a tile that this thread loads, and of y that it stores
+  const int ls = tid / (SSM_CH / V), lc = (tid % (SSM_CH / V)) * V, lcc = c0 + lc;
+  const bool lon = lcc < a.D;
+  const int bs = tid / (N / 2), bn = (tid % (N / 2)) * 2;
+  float bias[V] = {}, skip[V] = {};
+  if (lon) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if (a.bias) bias[j] = a.bias[lcc + j];
+      if (a.skip) skip[j] = a.skip[lcc + j];
+    }
+  }
+  const int chunk0 = MAPS ? 0 : first_slot(a.seq, g.n, SSM_CHUNK);
+  Loaded<T, N> in;
+  auto load = [&](int t) {
+    const int q = min(t + ls, g.t1 - 1), qb = min(t + bs, g.t1 - 1), cc = lon ? lcc : 0;
+    load_few<V>(static_cast<const T *>(a.x) + (int64_t)q * a.ldx + cc, in.x);
+    load_few<V>(static_cast<const T *>(a.dt) + (int64_t)q * a.lddt + cc, in.dt);
+    if (!MAPS && a.z) load_few<V>(static_cast<const T *>(a.z) + (int64_t)q * a.ldz + cc, in.z);
+    load_few<2>(static_cast<const T *>(a.B) + (int64_t)qb * a.ldB + bn, in.B);
+    if (!MAPS) load_few<2>(static_cast<const T *>(a.C) + (int64_t)qb * a.ldC + bn, in.C);
+  };
+  float total = 0.f;                          // MAPS: the sum of delta of this lane's channel
+  if (g.any) load(g.t0);
+  for (int t = g.t0; t < g.t1; t += L::TS) {
+    float x[V], z[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      x[j] = in.x[j];
+      z[j] = in.z[j];
+      float d = in.dt[j] + bias[j];
+      if (a.softplus) d = softplus(d);
+      const bool valid = lon && t + ls < g.t1;      // steps behind the end change nothing: delta = 0
+      step[ls][lc + j] = valid ? float2{d, d * x[j]} : float2{0.f, 0.f};
+    }
+    *reinterpret_cast<float2 *>(&sB[bs][bn]) = float2{in.B[0], in.B[1]};
+    if constexpr (!MAPS) *reinterpret_cast<float2 *>(&sC[bs][bn]) = float2{in.C[0], in.C[1]};
+    __syncthreads();
+    if (t + L::TS < g.t1) load(t + L::TS);
+    if constexpr (!MAPS) {
+      if (a.states && tw == 0 && on && (t - g.s) % SSM_CHUNK == 0)
+        *reinterpret_cast<f4 *>(a.states + ((size_t)(chunk0 + (t - g.s) / SSM_CHUNK) * a.D + c) * N + p4) = h;
+    }
+    const int s0 = tw * SSM_STEPS;
+    f4 dec[SSM_STEPS];
+    if constexpr (L::TW > 1 || MAPS) {
+      f4 H{0.f, 0.f, 0.f, 0.f};
+      float sd = 0.f;
+#pragma unroll
+      for (int s = 0; s < SSM_STEPS; ++s) {
+        const float2 du = step[s0 + s][ch];
+        const f4 b = *reinterpret_cast<const f4 *>(&sB[s0 + s][p4]);
+        sd += du.x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          dec[s][j] = __builtin_amdgcn_exp2f(du.x * A2[j]);
+          H[j] = fmaf(dec[s][j], H[j], du.y * b[j]);
+        }
+      }
+      f4 Pm;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) Pm[j] = __builtin_amdgcn_exp2f(sd * A2[j]);
+      *reinterpret_cast<f4 *>(&mapP[tw][ch][p4]) = Pm;
+      *reinterpret_cast<f4 *>(&mapH[tw][ch][p4]) = H;
+      if (MAPS && p4 == 0) sumd[tw][ch] = sd;
+      __syncthreads();
+    }
+    // the state before this wave's steps, and before the next tile
+    f4 run = h;
+    if constexpr (L::TW > 1 || MAPS) {
+      f4 mine = h;
+#pragma unroll
+      for (int w = 0; w < L::TW; ++w) {
+        if (w == tw) mine = run;
+        const f4 Pm = *reinterpret_cast<const f4 *>(&mapP[w][ch][p4]), H = *reinterpret_cast<const f4 *>(&mapH[w][ch][p4]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) run[j] = fmaf(Pm[j], run[j], H[j]);
+        if (MAPS) total += sumd[w][ch];
+      }
+      h = run;
+      run = mine;
+    }
+    if constexpr (!MAPS) {
+#pragma unroll
+      for (int s = 0; s < SSM_STEPS; ++s) {
+        const float2 du = step[s0 + s][ch];
+        const f4 b = *reinterpret_cast<const f4 *>(&sB[s0 + s][p4]), cv = *reinterpret_cast<const f4 *>(&sC[s0 + s][p4]);
+        float y = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float e = L::TW > 1 ? dec[s][j] : __builtin_amdgcn_exp2f(du.x * A2[j]);
+          run[j] = fmaf(e, run[j], du.y * b[j]);
+          y = fmaf(cv[j], run[j], y);
+        }
+        y = lane_sum<L::P>(y);
+        if (p4 == 0) step[s0 + s][ch].x = y;
+      }
+      if constexpr (L::TW == 1) h = run;
+    }
+    __syncthreads();
+    if constexpr (!MAPS) {
+      if (lon && t + ls < g.t1) {
+        float y[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          y[j] = fmaf(skip[j], x[j], step[ls][lc + j].x);
+          if (a.z) y[j] *= z[j] * sigmoid(z[j]);
+        }
+        store_few<V>(static_cast<T *>(a.y) + (size_t)(t + ls) * a.D + lcc, y);
+      }
+    }
+  }
+  if (tw != 0 || !on) return;
+  if constexpr (MAPS) {
+    *reinterpret_cast<f4 *>(a.seg_map + ((size_t)g.slot * a.D + c) * N + p4) = h;
+    if (p4 == 0) a.seg_sum[(size_t)g.slot * a.D + c] = total;
+  } else if (lastseg && a.final_state) {
+    *reinterpret_cast<f4 *>(a.final_state + ((size_t)g.n * a.D + c) * N + p4) = h;
+  }
+}
+
+// The states that the segments of a sequence start from, in order: thread per (channel, 4 states).
+template <int N> __global__ __launch_bounds__(256) void ssm_chain(SsmArgs a) {
+  const int per = a.D * (N / 4), i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= per) return;
+  const int c = i / (N / 4), p4 = (i % (N / 4)) * 4;
+  const f4 A2 = *reinterpret_cast<const f4 *>(a.A + (size_t)c * N + p4) * SSM_LOG2E;
+  for (int n = blockIdx.y; n < a.seq.n; n += gridDim.y) {
+    const int s = a.seq.begin(n), e = a.seq.end(n), slot = first_slot(a.seq, n, a.seg);
+    f4 h{0.f, 0.f, 0.f, 0.f};
+    if (a.init) h = *reinterpret_cast<const f4 *>(a.init + ((size_t)n * a.D + c) * N + p4);
+    for (int k = 0; (int64_t)s + (int64_t)(k + 1) * a.seg < e; ++k) {
+      const size_t at = ((size_t)(slot + k) * a.D + c) * N + p4;
+      const float sd = a.seg_sum[(size_t)(slot + k) * a.D + c];
+      const f4 H = *reinterpret_cast<const f4 *>(a.seg_map + at);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = fmaf(__builtin_amdgcn_exp2f(sd * A2[j]), h[j], H[j]);
+      *reinterpret_cast<f4 *>(a.seg_state + at + (size_t)a.D * N) = h;
+    }
+  }
+}
+
+template <typename T, int N> __global__ __launch_bounds__(256) void ssm_step(SsmArgs a) {
+  constexpr int P = N / 4;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, rows = (int64_t)a.seq.n * a.D;
+  const int64_t row = min(i / P, rows - 1);           // whole waves stay for the sum over lanes
+  const int n = (int)(row / a.D), c = (int)(row - (int64_t)n * a.D), p4 = (int)(i % P) * 4;
+  const size_t at = (size_t)row * N + p4;
+  const f4 h0 = *reinterpret_cast<const f4 *>(a.init + at);
+  const f4 A = *reinterpret_cast<const f4 *>(a.A + (size_t)c * N + p4);
+  float B[4], C[4], x[1], dt[1], z[1] = {0.f};
+  load_few<4>(static_cast<const T *>(a.B) + (int64_t)n * a.ldB + p4, B);
+  load_few<4>(static_cast<const T *>(a.C) + (int64_t)n * a.ldC + p4, C);
+  load_few<1>(static_cast<const T *>(a.x) + (int64_t)n * a.ldx + c, x);
+  load_few<1>(static_cast<const T *>(a.dt) + (int64_t)n * a.lddt + c, dt);
+  if (a.z) load_few<1>(static_cast<const T *>(a.z) + (int64_t)n * a.ldz + c, z);
+  float d = dt[0] + (a.bias ? a.bias[c] : 0.f);
+  if (a.softplus) d = softplus(d);
+  f4 h;
+  float y = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    h[j] = fmaf(__builtin_amdgcn_exp2f(d * (A[j] * SSM_LOG2E)), h0[j], d * x[0] * B[j]);
+    y = fmaf(C[j], h[j], y);
+  }
+  y = lane_sum<P>(y);
+  if (i / P >= rows) return;
+  *reinterpret_cast<f4 *>(a.final_state + at) = h;
+  if (p4) return;
+  if (a.skip) y = fmaf(a.skip[c], x[0], y);
+  if (a.z) y *= z[0] * sigmoid(z[0]);
+  static_cast<T *>(a.y)[row] = (T)y;
+}
+
+// Tokens of a segment: as many segments as give every compute unit two workgroups, where whole
+// sequences do not; a whole number of chunks.
+int segment_of(const SeqMap &q, int D) {
+  const int64_t groups = (D + SSM_CH - 1) / SSM_CH, want = 512;
+  int64_t len;
+  if (q.cu) {
+    len = ((int64_t)q.T * groups + want - 1) / want;
+  } else {
+    const int64_t parts = want / (q.n * groups);
+    if (parts < 2) return (q.T + SSM_CHUNK - 1) / SSM_CHUNK * SSM_CHUNK;
+    len = (q.T + parts - 1) / parts;
+  }
+  len = (len + SSM_CHUNK - 1) / SSM_CHUNK * SSM_CHUNK;
+  return (int)(len < 256 ? 256 : len);
+}
+// Whether any sequence has more than one segment (packed: may have).
+bool segmented(const SeqMap &q, int seg) { return q.T > seg; }
+
+size_t align16(size_t n) { return (n + 15) / 16 * 16; }
+
+}  // namespace
+
+bool ssm_fits(SeqMap seq, int D) {
+  const int64_t groups = (D + SSM_CH - 1) / SSM_CH;
+  const int64_t seg = segment_of(seq, D);
+  const int64_t slots = seq.cu ? seq.T / seg + seq.n : (int64_t)seq.n * ((seq.T + seg - 1) / seg);
+  return slots * groups <= INT32_MAX - 64 && grid_fits(slots * groups + 8, SSM_THR);
+}
+
+size_t ssm_fwd_workspace(SeqMap seq, int D, int N) {
+  const int seg = segment_of(seq, D);
+  if (!segmented(seq, seg)) return 0;
+  const size_t slots = slots_of(seq, seg) + 1;
+  return 2 * align16(slots * D * N * sizeof(float)) + align16(slots * D * sizeof(float));
+}
+
+template <typename T, int N> static hipError_t fwd(SsmArgs a, void *ws, hipStream_t s) {
+  a.seg = segment_of(a.seq, a.D);
+  const int64_t groups = (a.D + SSM_CH - 1) / SSM_CH;
+  const unsigned grid = dealt_grid(groups * slots_of(a.seq, a.seg));
+  if (segmented(a.seq, a.seg)) {
+    const size_t states = align16((size_t)(slots_of(a.seq, a.seg) + 1) * a.D * N * sizeof(float));
+    a.seg_map = static_cast<float *>(ws);
+    a.seg_state = reinterpret_cast<float *>(static_cast<char *>(ws) + states);
+    a.seg_sum = reinterpret_cast<float *>(static_cast<char *>(ws) + 2 * states);
+    hipLaunchKernelGGL((ssm_fwd<T, N, true>), dim3(grid), dim3(SSM_THR), 0, s, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int rows = a.seq.n < 65535 ? a.seq.n : 65535;
+    hipLaunchKernelGGL((ssm_chain<N>), dim3((a.D * (N / 4) + 255) / 256, rows), dim3(256), 0, s, a);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((ssm_fwd<T, N, false>), dim3(grid), dim3(SSM_THR), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_ssm_fwd(bool bf16, int N, SsmArgs a, void *ws, hipStream_t s) {
+  if (N == 16) return bf16 ? fwd<__bf16, 16>(a, ws, s) : fwd<float, 16>(a, ws, s);
+  if (N == 32) return bf16 ? fwd<__bf16, 32>(a, ws, s) : fwd<float, 32>(a, ws, s);
+  if (N == 64) return bf16 ? fwd<__bf16, 64>(a, ws, s) : fwd<float, 64>(a, ws, s);
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_ssm_step(bool bf16, int N, SsmArgs a, hipStream_t s) {
+  const int64_t threads = (int64_t)a.seq.n * a.D * (N / 4);
+  const dim3 grid((unsigned)((threads + 255) / 256));
+#define FALCON_STEP(N_)                                                                              \
+  if (N == N_) {                                                                                     \
+    if (bf16) hipLaunchKernelGGL((ssm_step<__bf16, N_>), grid, dim3(256), 0, s, a);                  \
+    else hipLaunchKernelGGL((ssm_step<float, N_>), grid, dim3(256), 0, s, a);                        \
+    return hipGetLastError();                                                                        \
+  }
+  FALCON_STEP(16)
+  FALCON_STEP(32)
+  FALCON_STEP(64)
+#undef FALCON_STEP
+  return hipErrorInvalidValue;
+}
+
+}  // namespace falcon

@@ -1,0 +1,110 @@
+// What the selective state-space scan's kernels share: the layout of a tile, its steps, and the
+// slots of a call's segments and chunks.
+//
+// A wave's lane holds 4 states of one channel: P = N / 4 lanes beside each other make a channel, so a
+// sum over the states is one over 4 registers and P neighbouring lanes.  A workgroup of 8 waves
+// owns CH = 32 channels: WIDE waves lie side by side over them and TW behind each other in time, each
+// with STEPS = 16 consecutive steps of a tile of TS = 16 TW.
+#pragma once
+#include "block_kernels.h"
+#include "row_io.h"
+
+namespace falcon {
+
+constexpr int SSM_THR = 512, SSM_CH = 32, SSM_STEPS = 16;
+constexpr int SSM_CHUNK = 64;      // steps between the states that the forward keeps (FALCON_SSM_CHUNK)
+constexpr float SSM_LOG2E = 1.44269504088896340736f;
+
+template <int N> struct SsmTile {
+  static constexpr int P = N / 4, CW = 64 / P, WIDE = SSM_CH / CW, TW = 8 / WIDE, TS = TW * SSM_STEPS;
+  static constexpr int VEC = TS * SSM_CH / SSM_THR;     // channels of a step that a thread loads: 4, 2 or 1
+  static_assert(SSM_CHUNK % TS == 0, "chunks begin with a tile");
+};
+
+// V consecutive entries as floats; the address is a multiple of their size together.
+template <int V> __device__ __forceinline__ void load_few(const float *p, float (&o)[V]) {
+  if constexpr (V == 4) { const f4 v = *reinterpret_cast<const f4 *>(p); o[0] = v[0]; o[1] = v[1]; o[2] = v[2]; o[3] = v[3]; }
+  else if constexpr (V == 2) { const float2 v = *reinterpret_cast<const float2 *>(p); o[0] = v.x; o[1] = v.y; }
+  else o[0] = *p;
+}
+template <int V> __device__ __forceinline__ void load_few(const __bf16 *p, float (&o)[V]) {
+  if constexpr (V == 4) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    o[0] = __uint_as_float(v.x << 16); o[1] = __uint_as_float(v.x & 0xffff0000u);
+    o[2] = __uint_as_float(v.y << 16); o[3] = __uint_as_float(v.y & 0xffff0000u);
+  } else if constexpr (V == 2) {
+    const unsigned v = *reinterpret_cast<const unsigned *>(p);
+    o[0] = __uint_as_float(v << 16); o[1] = __uint_as_float(v & 0xffff0000u);
+  } else o[0] = (float)*p;
+}
+template <int V> __device__ __forceinline__ void store_few(float *p, const float (&v)[V]) {
+  if constexpr (V == 4) *reinterpret_cast<f4 *>(p) = f4{v[0], v[1], v[2], v[3]};
+  else if constexpr (V == 2) *reinterpret_cast<float2 *>(p) = float2{v[0], v[1]};
+  else *p = v[0];
+}
+// rounded to nearest even: the one rounding of a result held in bf16
+template <int V> __device__ __forceinline__ void store_few(__bf16 *p, const float (&v)[V]) {
+  if constexpr (V == 4) *reinterpret_cast<bf4 *>(p) = __builtin_convertvector(f4{v[0], v[1], v[2], v[3]}, bf4);
+  else if constexpr (V == 2) {
+    typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+    *reinterpret_cast<bf2 *>(p) = bf2{(__bf16)v[0], (__bf16)v[1]};
+  } else *p = (__bf16)v[0];
+}
+
+// softplus(v) = max(v, 0) + ln(1 + e), e = e^-|v| in (0, 1]; ln(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3, by
+// its series to s^15 (the next term is 2^-28 of the result): relative precision however small e is.
+__device__ __forceinline__ float softplus(float v) {
+  const float e = __builtin_amdgcn_exp2f(-fabsf(v) * SSM_LOG2E);
+  const float s = e * __builtin_amdgcn_rcpf(2.f + e), q = s * s;
+  float p = fmaf(q, 1.f / 15.f, 1.f / 13.f);
+  p = fmaf(p, q, 1.f / 11.f);
+  p = fmaf(p, q, 1.f / 9.f);
+  p = fmaf(p, q, 1.f / 7.f);
+  p = fmaf(p, q, 1.f / 5.f);
+  p = fmaf(p, q, 1.f / 3.f);
+  return fmaxf(v, 0.f) + 2.f * fmaf(p * q, s, s);
+}
+
+// A sequence's part that one workgroup runs over: tokens t0 .. t1 - 1 of sequence n, which begins at s
+// and ends at e; `slot` names it among the call's.  Sequence n's segments of `len` tokens
+// start at slot begin(n) / len + n, which no two sequences share (floor(a) + ceil(b) <= floor(a + b) + 1);
+// sequences of the same length have ceil(T / len) each.
+struct Segment { int n, slot, s, e, t0, t1; bool any; };
+
+__host__ __device__ inline int slots_of(const SeqMap &q, int len) {
+  return q.cu ? q.T / len + q.n : q.n * ((q.T + len - 1) / len);
+}
+__device__ __forceinline__ int first_slot(const SeqMap &q, int n, int len) {
+  return q.cu ? q.begin(n) / len + n : n * ((q.T + len - 1) / len);
+}
+__device__ __forceinline__ Segment find_segment(const SeqMap &q, int len, int slot) {
+  Segment g;
+  g.slot = slot;
+  if (!q.cu) {
+    g.n = slot / ((q.T + len - 1) / len);
+  } else {
+    int lo = 0, more = q.n;
+    while (more > 1) {
+      const int half = more >> 1;
+      if (first_slot(q, lo + half, len) <= slot) { lo += half; more -= half; } else { more = half; }
+    }
+    g.n = lo;
+  }
+  g.s = q.begin(g.n);
+  g.e = max(q.end(g.n), g.s);
+  const int64_t at = g.s + (int64_t)(slot - first_slot(q, g.n, len)) * len;
+  g.t0 = (int)(at < g.e ? at : g.e);
+  g.t1 = (int)(at + len < g.e ? at + len : g.e);
+  g.any = at >= g.s && at < g.e;
+  return g;
+}
+
+// The workgroup's place in a grid that is dealt to the 8 dies in turn: neighbours in (segment,
+// channels) run on one die, whose cache they share lines of x and the tiles of B and C in.
+__device__ __forceinline__ int dealt(int total) {
+  const int per = (total + 7) / 8;
+  return (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
+}
+inline unsigned dealt_grid(int64_t total) { return (unsigned)((total + 7) / 8 * 8); }
+
+}  // namespace falcon

@@ -30,7 +30,8 @@ EXPORTS = ("falcon_abi_version", "falcon_status_string", "falcon_chunk_fwd_works
            "falcon_attn_fwd_workspace", "falcon_attn_fwd", "falcon_attn_bwd_workspace", "falcon_attn_bwd",
            # the operators of a state-space block (block.py)
            "falcon_rms_norm", "falcon_rms_norm_bwd_workspace", "falcon_rms_norm_bwd",
-           "falcon_conv_fwd", "falcon_conv_bwd_workspace", "falcon_conv_bwd", "falcon_conv_step")
+           "falcon_conv_fwd", "falcon_conv_bwd_workspace", "falcon_conv_bwd", "falcon_conv_step",
+           "falcon_ssm_fwd_workspace", "falcon_ssm_chunks", "falcon_ssm_fwd", "falcon_ssm_step")
 
 
 class Shape(ctypes.Structure):
@@ -72,6 +73,11 @@ class NormShape(ctypes.Structure):
 class ConvShape(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("seqlen", ctypes.c_int32),
                 ("width", ctypes.c_int32), ("taps", ctypes.c_int32), ("activation", ctypes.c_int32)]
+
+
+class SsmShape(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("seqlen", ctypes.c_int32),
+                ("width", ctypes.c_int32), ("state", ctypes.c_int32), ("softplus", ctypes.c_int32)]
 
 
 class Heads(ctypes.Structure):
@@ -163,6 +169,14 @@ def lib() -> ctypes.CDLL:
         L.falcon_conv_bwd.argtypes = [P(ConvShape), V, Heads, V, V, V, V, V, Heads, V, V, V, V, S, V]
         L.falcon_conv_step.restype = I
         L.falcon_conv_step.argtypes = [P(ConvShape), Heads, V, V, V, V, V, V]
+        L.falcon_ssm_fwd_workspace.restype = S
+        L.falcon_ssm_fwd_workspace.argtypes = [P(SsmShape), I]
+        L.falcon_ssm_chunks.restype = ctypes.c_int32
+        L.falcon_ssm_chunks.argtypes = [P(SsmShape), I]
+        L.falcon_ssm_fwd.restype = I
+        L.falcon_ssm_fwd.argtypes = [P(SsmShape), V, Heads, Heads, V, Heads, Heads, V, Heads, V, V, V, V, V, V, S, V]
+        L.falcon_ssm_step.restype = I
+        L.falcon_ssm_step.argtypes = [P(SsmShape), Heads, Heads, V, Heads, Heads, V, Heads, V, V, V, V, V]
         _LIB = L
     return _LIB
 
