@@ -603,8 +603,8 @@ int falcon_conv_step(const falcon_conv_shape_t *shape, falcon_heads_t x, const f
  *   h_t = exp(delta_t A[d][n]) h_{t-1} + delta_t x_t B_t[n]
  *   y_t = (sum_n C_t[n] h_t[n] + D[d] x_t) silu(z_t)         (z NULL: no gate)
  * B_t and C_t are shared by the channels.  A is finite; where delta_t A > 0 the state
- * grows, and its growth over FALCON_SSM_CHUNK steps (a long sequence: over all of them)
- * has to stay in fp32's range.  States, sums and delta are fp32. */
+ * grows, and its growth over 64 steps (where sequences are cut into segments, over a
+ * segment) has to stay in fp32's range.  States, sums and delta are fp32. */
 typedef struct {
   int32_t dtype;     /* falcon_dtype_t of x, dt, B, C, z, y and their gradients: F32 or BF16 */
   int32_t batch;     /* sequences, >= 1 */
@@ -614,16 +614,16 @@ typedef struct {
   int32_t softplus;  /* 0 or 1 */
 } falcon_ssm_shape_t;
 
-#define FALCON_SSM_CHUNK 64   /* steps between the states the forward keeps */
+#define FALCON_SSM_CHUNK(state) (1024 / (state))   /* steps between the states the forward keeps */
 
 /* Bytes of workspace of the forward: the maps of segments, where few long sequences are
  * cut to run in parallel; 0 where none may be (then workspace may be NULL), and for invalid
  * shapes.  `packed` is nonzero for calls with cu_seqlens. */
 size_t falcon_ssm_fwd_workspace(const falcon_ssm_shape_t *shape, int packed);
 
-/* Chunks that the forward keeps a state of: batch ceil(T / FALCON_SSM_CHUNK), or packed
- * floor(T / FALCON_SSM_CHUNK) + batch (chunk c of sequence n, which begins at token s, is
- * number floor(s / FALCON_SSM_CHUNK) + n + c; some stay unused).  0 for invalid shapes. */
+/* Chunks of K = FALCON_SSM_CHUNK(N) steps that the forward keeps a state of: batch ceil(T / K),
+ * or packed floor(T / K) + batch (chunk c of sequence n, which begins at token s, is number
+ * floor(s / K) + n + c; some stay unused).  0 for invalid shapes. */
 int32_t falcon_ssm_chunks(const falcon_ssm_shape_t *shape, int packed);
 
 /*   cu_seqlens   NULL: x, dt, z, y are [B, T, D] and Bm, Cm [B, T, N].  Otherwise [B + 1] offsets,
@@ -638,6 +638,22 @@ int32_t falcon_ssm_chunks(const falcon_ssm_shape_t *shape, int packed);
 int falcon_ssm_fwd(const falcon_ssm_shape_t *shape, const int32_t *cu_seqlens, falcon_heads_t x, falcon_heads_t dt,
                    const float *A, falcon_heads_t Bm, falcon_heads_t Cm, const float *D, falcon_heads_t z,
                    const float *dt_bias, const float *init, float *final_state, void *y, float *chunk_states,
+                   void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of the backward: partial sums of dB and dC for every 32 channels, and of
+ * the parameters' gradients. */
+size_t falcon_ssm_bwd_workspace(const falcon_ssm_shape_t *shape, int packed);
+
+/* Gradients of <d_y, y> + <d_final, final_state>, from the chunk_states the forward wrote for
+ * the same arguments (the initial state among them).  d_y [.., D] dense in dtype; d_final
+ * [B, D, N] fp32 or NULL (zeros).  dx, ddt, dz (ignored without z), dB, dC in dtype; dA [D, N],
+ * dD, ddt_bias [D] fp32 (dD, ddt_bias may be NULL); d_init [B, D, N] fp32 or NULL.  Outputs must
+ * not alias inputs. */
+int falcon_ssm_bwd(const falcon_ssm_shape_t *shape, const int32_t *cu_seqlens, falcon_heads_t x, falcon_heads_t dt,
+                   const float *A, falcon_heads_t Bm, falcon_heads_t Cm, const float *D, falcon_heads_t z,
+                   const float *dt_bias, const float *chunk_states, const void *d_y, const float *d_final,
+                   falcon_heads_out_t dx, falcon_heads_out_t ddt, float *dA, falcon_heads_out_t dB,
+                   falcon_heads_out_t dC, float *dD, falcon_heads_out_t dz, float *ddt_bias, float *d_init,
                    void *workspace, size_t workspace_bytes, void *stream);
 
 /* One step of every sequence: x, dt, z, y [B, D], Bm, Cm [B, N]; state, state_out [B, D, N] fp32

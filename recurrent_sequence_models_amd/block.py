@@ -14,8 +14,7 @@ import functools
 from .falcon import ConvShape, Heads, NormShape, SsmShape, lib
 from .layer import _check, _current, _device, _done, _dtype, _ints, _offsets, _on, _p, _workspace
 
-E4M3 = 2         # FALCON_E4M3
-SSM_CHUNK = 64   # FALCON_SSM_CHUNK
+E4M3 = 2   # FALCON_E4M3
 ACTIVATIONS = {None: 0, "silu": 1, "gelu": 2}
 
 
@@ -281,10 +280,11 @@ _NO_ROWS = Heads(None, 0)
 
 @functools.lru_cache(maxsize=1024)
 def _ssm_plan(dtype, n, T, D, N, softplus, packed):
-    """(pointer to the C shape, chunks, workspace bytes of the forward)."""
+    """(pointer to the C shape, chunks, workspace bytes of the forward, of the backward)."""
     shape = SsmShape(dtype, *_ints(n, T, D, N), softplus)
     L, ref = lib(), ctypes.byref(shape)
-    return ctypes.pointer(shape), L.falcon_ssm_chunks(ref, packed), L.falcon_ssm_fwd_workspace(ref, packed)
+    return (ctypes.pointer(shape), L.falcon_ssm_chunks(ref, packed), L.falcon_ssm_fwd_workspace(ref, packed),
+            L.falcon_ssm_bwd_workspace(ref, packed))
 
 
 def _ssm_args(x, dt, A, B, C, D, z, dt_bias):
@@ -321,7 +321,7 @@ def selective_scan(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, softplus=Tru
     n, T = _sequences(x, cu_seqlens)
     args = _ssm_args(x, dt, A, B, C, D, z, dt_bias)
     width, N = A.shape
-    shape, chunks, need = _ssm_plan(kind, n, T, width, N, 1 if softplus else 0, cu_seqlens is not None)
+    shape, chunks, need, _ = _ssm_plan(kind, n, T, width, N, 1 if softplus else 0, cu_seqlens is not None)
     _maybe("init", init, torch.float32, (n, width, N), dev)
     with _on(dev, stream):
         if out is None:
@@ -335,6 +335,45 @@ def selective_scan(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, softplus=Tru
         _done(lib().falcon_ssm_fwd(shape, _p(cu_seqlens), *args, _p(init), _p(final), _p(out), _p(states), _p(ws), nbytes,
                                    _current(dev)), "falcon_ssm_fwd")
     return out, final, states
+
+
+def selective_scan_bwd(x, dt, A, B, C, dy, chunk_states, *, D=None, z=None, dt_bias=None, softplus=True, cu_seqlens=None,
+                       init=None, d_final=None, d_init=True, out=None, workspace=None, stream=None):
+    """falcon_ssm_bwd on torch tensors: gradients of <dy, y> + <d_final, final> for
+    ``selective_scan`` of the same arguments.
+
+    ``chunk_states`` is what ``selective_scan(..., chunk_states=True)`` returned (``init``
+    is in it).  dy has the dtype and shape of x; d_final is None or [N,D,N] float32.
+    ``d_init``: True (allocate), a [N,D,N] float32 tensor, or False.  ``out``: None or a
+    dict of preallocated dx, ddt, dB, dC and, with z, dz (views with dense rows will do).
+    Returns dict(dx, ddt, dA, dB, dC, dD, dz, ddt_bias, d_init): dA [D,N], dD, ddt_bias [D]
+    float32, None for what was not given."""
+    import torch
+    kind, dev = _dtype("x", x), _device("x", x)
+    n, T = _sequences(x, cu_seqlens)
+    args = _ssm_args(x, dt, A, B, C, D, z, dt_bias)
+    width, N = A.shape
+    shape, chunks, _, need = _ssm_plan(kind, n, T, width, N, 1 if softplus else 0, cu_seqlens is not None)
+    states = (n, width, N)
+    _check("dy", dy, x.dtype, x.shape, dev)
+    _check("chunk_states", chunk_states, torch.float32, (chunks, width, N), dev)
+    for name, t in (("init", init), ("d_final", d_final)):
+        _maybe(name, t, torch.float32, states, dev)
+    with _on(dev, stream):
+        like = dict(dx=x, ddt=dt, dB=B, dC=C, dz=z)
+        if out is None:
+            out = {k: torch.empty(t.shape, dtype=x.dtype, device=dev) for k, t in like.items() if t is not None}
+        rows = {k: _NO_ROWS if t is None else _rows(k, out[k], x.dtype, dev, t.shape) for k, t in like.items()}
+        d_init = x.new_empty(states, dtype=torch.float32) if d_init is True else None if d_init is False else d_init
+        _maybe("d_init", d_init, torch.float32, states, dev)
+        dA = torch.empty_like(A)
+        dD, db = (None if t is None else torch.empty_like(t) for t in (D, dt_bias))
+        ws, nbytes = _workspace(need, workspace, dev)
+        _done(lib().falcon_ssm_bwd(shape, _p(cu_seqlens), *args, _p(chunk_states), _p(dy), _p(d_final), rows["dx"], rows["ddt"],
+                                   _p(dA), rows["dB"], rows["dC"], _p(dD), rows["dz"], _p(db), _p(d_init), _p(ws), nbytes,
+                                   _current(dev)), "falcon_ssm_bwd")
+    return dict(dx=out["dx"], ddt=out["ddt"], dA=dA, dB=out["dB"], dC=out["dC"], dD=dD, dz=None if z is None else out["dz"],
+                ddt_bias=db, d_init=d_init)
 
 
 def selective_scan_step(x, dt, A, B, C, state, *, D=None, z=None, dt_bias=None, softplus=True, state_out=None, out=None,
@@ -357,6 +396,6 @@ def selective_scan_step(x, dt, A, B, C, state, *, D=None, z=None, dt_bias=None, 
             out = torch.empty((n, width), dtype=x.dtype, device=dev)
         else:
             _check("y", out, x.dtype, x.shape, dev)
-        shape, _, _ = _ssm_plan(kind, n, 1, width, N, 1 if softplus else 0, False)
+        shape, *_ = _ssm_plan(kind, n, 1, width, N, 1 if softplus else 0, False)
         _done(lib().falcon_ssm_step(shape, *args, _p(state), _p(state_out), _p(out), _current(dev)), "falcon_ssm_step")
     return out

@@ -81,10 +81,23 @@ struct SsmArgs {
   SeqMap seq;
   int64_t ldx, lddt, ldz, ldB, ldC;
   int D, softplus, seg;             // seg: tokens of a segment
+  // backward: states is read; gradients of x, dt, z [tokens, D] and B, C [tokens, N], with token strides
+  const void *dy;                   // [tokens, D]
+  const float *d_final;             // [n, D, N] or null (zeros)
+  void *dx, *ddt, *dz, *dB, *dC;
+  float *d_init;                    // [n, D, N] or null
+  float *part_bc, *part_A, *part_D; // workspace: sums by group of channels, by segment, by segment
+  int64_t lddx, ldddt, lddz, lddB, lddC;
 };
+struct SsmGrads { float *dA, *dD, *dbias; };   // [D, N]; [D] or null; [D] or null
+int ssm_chunk(int N);                             // steps between the states that the forward keeps
+int ssm_segment(const SeqMap &seq, int D);        // tokens of a segment
+bool ssm_segmented(const SeqMap &seq, int segment);   // whether a sequence has more than one (packed: may have)
 bool ssm_fits(SeqMap seq, int D);
 size_t ssm_fwd_workspace(SeqMap seq, int D, int N);
 hipError_t launch_ssm_fwd(bool bf16, int N, SsmArgs a, void *ws, hipStream_t s);
+size_t ssm_bwd_workspace(SeqMap seq, int D, int N);
+hipError_t launch_ssm_bwd(bool bf16, int N, SsmArgs a, SsmGrads o, void *ws, hipStream_t s);
 hipError_t launch_ssm_step(bool bf16, int N, SsmArgs a, hipStream_t s);
 
 }  // namespace falcon

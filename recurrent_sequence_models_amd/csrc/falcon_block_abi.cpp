@@ -259,8 +259,9 @@ size_t falcon_ssm_fwd_workspace(const falcon_ssm_shape_t *s, int packed) {
 
 int32_t falcon_ssm_chunks(const falcon_ssm_shape_t *s, int packed) {
   if (check_ssm(s, packed != 0, false) != FALCON_OK) return 0;
-  if (packed) return s->seqlen / FALCON_SSM_CHUNK + s->batch;
-  return s->batch * ((s->seqlen + FALCON_SSM_CHUNK - 1) / FALCON_SSM_CHUNK);
+  const int K = falcon::ssm_chunk(s->state);
+  if (packed) return s->seqlen / K + s->batch;
+  return s->batch * ((s->seqlen + K - 1) / K);
 }
 
 int falcon_ssm_fwd(const falcon_ssm_shape_t *s, const int32_t *cu, falcon_heads_t x, falcon_heads_t dt, const float *A,
@@ -281,6 +282,54 @@ int falcon_ssm_fwd(const falcon_ssm_shape_t *s, const int32_t *cu, falcon_heads_
   a.y = y;
   a.states = chunk_states;
   return status_of(falcon::launch_ssm_fwd(s->dtype == FALCON_BF16, s->state, a, ws, static_cast<hipStream_t>(stream)));
+}
+
+// Of the backward: its launches for the sums over workgroups too.
+static int check_ssm_bwd(const falcon_ssm_shape_t *s, bool packed) {
+  FALCON_TRY(check_ssm(s, packed, false));
+  const int64_t sums = seq_tokens(s->batch, s->seqlen, packed) * s->state / 2;
+  return falcon::grid_fits((sums + 255) / 256, 256) && falcon::grid_fits((int64_t)s->width * s->state / 16, 1024)
+             ? FALCON_OK : FALCON_ERR_UNSUPPORTED;
+}
+
+size_t falcon_ssm_bwd_workspace(const falcon_ssm_shape_t *s, int packed) {
+  if (check_ssm_bwd(s, packed != 0) != FALCON_OK) return 0;
+  return falcon::ssm_bwd_workspace(seq_sizes(s->batch, s->seqlen, packed != 0), s->width, s->state);
+}
+
+int falcon_ssm_bwd(const falcon_ssm_shape_t *s, const int32_t *cu, falcon_heads_t x, falcon_heads_t dt, const float *A,
+                   falcon_heads_t B, falcon_heads_t C, const float *D, falcon_heads_t z, const float *bias,
+                   const float *chunk_states, const void *d_y, const float *d_final, falcon_heads_out_t dx,
+                   falcon_heads_out_t ddt, float *dA, falcon_heads_out_t dB, falcon_heads_out_t dC, float *dD,
+                   falcon_heads_out_t dz, float *ddt_bias, float *d_init, void *ws, size_t ws_bytes, void *stream) {
+  FALCON_TRY(check_ssm_bwd(s, cu != nullptr));
+  FALCON_TRY(maybe(cu, 4));
+  const int64_t tokens = seq_tokens(s->batch, s->seqlen, cu);
+  FALCON_TRY(check_ssm_in(s, tokens, x, dt, A, B, C, D, z, bias));
+  FALCON_TRY(need(chunk_states, 16));
+  FALCON_TRY(need(d_y, 16));
+  FALCON_TRY(maybe(d_final, 16));
+  const int e = esize(s->dtype);
+  FALCON_TRY(check_rows(dx.data, dx.token_stride, tokens, s->width, e));
+  FALCON_TRY(check_rows(ddt.data, ddt.token_stride, tokens, s->width, e));
+  FALCON_TRY(check_rows(dB.data, dB.token_stride, tokens, s->state, e));
+  FALCON_TRY(check_rows(dC.data, dC.token_stride, tokens, s->state, e));
+  if (z.data) FALCON_TRY(check_rows(dz.data, dz.token_stride, tokens, s->width, e));
+  FALCON_TRY(need(dA, 4));
+  FALCON_TRY(maybe(dD, 4));
+  FALCON_TRY(maybe(ddt_bias, 4));
+  FALCON_TRY(maybe(d_init, 16));
+  FALCON_TRY(check_workspace(ws, ws_bytes, falcon_ssm_bwd_workspace(s, cu != nullptr)));
+  falcon::SsmArgs a = ssm_args(s, cu, x, dt, A, B, C, D, z, bias);
+  a.states = const_cast<float *>(chunk_states);
+  a.dy = d_y;
+  a.d_final = d_final;
+  a.dx = dx.data; a.ddt = ddt.data; a.dz = dz.data; a.dB = dB.data; a.dC = dC.data;
+  a.lddx = dx.token_stride; a.ldddt = ddt.token_stride; a.lddz = dz.token_stride;
+  a.lddB = dB.token_stride; a.lddC = dC.token_stride;
+  a.d_init = d_init;
+  return status_of(falcon::launch_ssm_bwd(s->dtype == FALCON_BF16, s->state, a, falcon::SsmGrads{dA, dD, ddt_bias}, ws,
+                                          static_cast<hipStream_t>(stream)));
 }
 
 int falcon_ssm_step(const falcon_ssm_shape_t *s, falcon_heads_t x, falcon_heads_t dt, const float *A, falcon_heads_t B,

@@ -67,7 +67,7 @@ template <typename T, int N, bool MAPS> __global__ __launch_bounds__(SSM_THR, 4)
       if (a.skip) skip[j] = a.skip[lcc + j];
     }
   }
-  const int chunk0 = MAPS ? 0 : first_slot(a.seq, g.n, SSM_CHUNK);
+  const int chunk0 = MAPS ? 0 : first_slot(a.seq, g.n, L::TS);
   Loaded<T, N> in;
   auto load = [&](int t) {
     const int q = min(t + ls, g.t1 - 1), qb = min(t + bs, g.t1 - 1), cc = lon ? lcc : 0;
@@ -95,8 +95,8 @@ template <typename T, int N, bool MAPS> __global__ __launch_bounds__(SSM_THR, 4)
     __syncthreads();
     if (t + L::TS < g.t1) load(t + L::TS);
     if constexpr (!MAPS) {
-      if (a.states && tw == 0 && on && (t - g.s) % SSM_CHUNK == 0)
-        *reinterpret_cast<f4 *>(a.states + ((size_t)(chunk0 + (t - g.s) / SSM_CHUNK) * a.D + c) * N + p4) = h;
+      if (a.states && tw == 0 && on)
+        *reinterpret_cast<f4 *>(a.states + ((size_t)(chunk0 + (t - g.s) / L::TS) * a.D + c) * N + p4) = h;
     }
     const int s0 = tw * SSM_STEPS;
     f4 dec[SSM_STEPS];
@@ -229,47 +229,49 @@ template <typename T, int N> __global__ __launch_bounds__(256) void ssm_step(Ssm
   static_cast<T *>(a.y)[row] = (T)y;
 }
 
+size_t align16(size_t n) { return (n + 15) / 16 * 16; }
+
+}  // namespace
+
 // Tokens of a segment: as many segments as give every compute unit two workgroups, where whole
 // sequences do not; a whole number of chunks.
-int segment_of(const SeqMap &q, int D) {
+int ssm_segment(const SeqMap &q, int D) {
   const int64_t groups = (D + SSM_CH - 1) / SSM_CH, want = 512;
   int64_t len;
   if (q.cu) {
     len = ((int64_t)q.T * groups + want - 1) / want;
   } else {
     const int64_t parts = want / (q.n * groups);
-    if (parts < 2) return (q.T + SSM_CHUNK - 1) / SSM_CHUNK * SSM_CHUNK;
+    if (parts < 2) return (q.T + SSM_ALIGN - 1) / SSM_ALIGN * SSM_ALIGN;
     len = (q.T + parts - 1) / parts;
   }
-  len = (len + SSM_CHUNK - 1) / SSM_CHUNK * SSM_CHUNK;
+  len = (len + SSM_ALIGN - 1) / SSM_ALIGN * SSM_ALIGN;
   return (int)(len < 256 ? 256 : len);
 }
 // Whether any sequence has more than one segment (packed: may have).
-bool segmented(const SeqMap &q, int seg) { return q.T > seg; }
+bool ssm_segmented(const SeqMap &q, int seg) { return q.T > seg; }
 
-size_t align16(size_t n) { return (n + 15) / 16 * 16; }
-
-}  // namespace
+int ssm_chunk(int N) { return 1024 / N; }
 
 bool ssm_fits(SeqMap seq, int D) {
   const int64_t groups = (D + SSM_CH - 1) / SSM_CH;
-  const int64_t seg = segment_of(seq, D);
+  const int64_t seg = ssm_segment(seq, D);
   const int64_t slots = seq.cu ? seq.T / seg + seq.n : (int64_t)seq.n * ((seq.T + seg - 1) / seg);
   return slots * groups <= INT32_MAX - 64 && grid_fits(slots * groups + 8, SSM_THR);
 }
 
 size_t ssm_fwd_workspace(SeqMap seq, int D, int N) {
-  const int seg = segment_of(seq, D);
-  if (!segmented(seq, seg)) return 0;
+  const int seg = ssm_segment(seq, D);
+  if (!ssm_segmented(seq, seg)) return 0;
   const size_t slots = slots_of(seq, seg) + 1;
   return 2 * align16(slots * D * N * sizeof(float)) + align16(slots * D * sizeof(float));
 }
 
 template <typename T, int N> static hipError_t fwd(SsmArgs a, void *ws, hipStream_t s) {
-  a.seg = segment_of(a.seq, a.D);
+  a.seg = ssm_segment(a.seq, a.D);
   const int64_t groups = (a.D + SSM_CH - 1) / SSM_CH;
   const unsigned grid = dealt_grid(groups * slots_of(a.seq, a.seg));
-  if (segmented(a.seq, a.seg)) {
+  if (ssm_segmented(a.seq, a.seg)) {
     const size_t states = align16((size_t)(slots_of(a.seq, a.seg) + 1) * a.D * N * sizeof(float));
     a.seg_map = static_cast<float *>(ws);
     a.seg_state = reinterpret_cast<float *>(static_cast<char *>(ws) + states);

@@ -1,0 +1,385 @@
+// Selective state-space scan on gfx950, backward.
+//
+// With gy_t = dy_t silu(z_t), a_t = exp(delta_t A), against time:
+//   g_t = gy_t C_t + r_{t+1},  r_t = a_t g_t           (r behind the last step: d_final)
+//   dC_t = sum_d gy_t h_t,  dB_t = sum_d g_t delta_t x_t
+//   dx_t = delta_t sum_n g_t B_t + D gy_t
+//   ddelta_t = sum_n (r_t h_{t-1} A + g_t B_t x_t),  ddt_t = ddelta_t softplus'
+//   dA = sum_t r_t h_{t-1} delta_t,  dD = sum_t gy_t x_t,  dbias = sum_t ddt_t
+//   dz_t = dy_t (sum_n C_t h_t + D x_t) silu'(z_t),  d init = r at the first step.
+//
+// The layout of the forward, its tiles taken from the last to the first.  A tile starts from the state
+// that the forward kept; its waves compose their 16 steps in both directions (the maps share their
+// factor exp(A sum of delta)), join the maps, run forward again to have the states before their steps in
+// registers beside the decays, and then back.  Sums over the states are over 4 registers and N / 4
+// lanes; those over the channels, for dB and dC, go by exchanges that halve the number of values with the
+// number of lanes (16 instructions for 8 sums over 16 lanes), over the waves in LDS, and over
+// workgroups in a pass of their own, in order.
+//
+// Bound: the vector unit.
+#include "ssm_common.h"
+
+namespace falcon {
+namespace {
+
+// v_permlane16_swap / v_permlane32_swap of the pairs (a0, b0), (a1, b1), then their sums: rows (halves) of
+// even number get the sum of two rows of a, odd ones that of b.  Every lane of the wave calls it.
+__device__ __forceinline__ void halve16(float a0, float b0, float a1, float b1, float &x0, float &x1) {
+  asm volatile("s_nop 1\n\tv_permlane16_swap_b32 %0, %1\n\tv_permlane16_swap_b32 %2, %3\n\ts_nop 1"
+               : "+v"(a0), "+v"(b0), "+v"(a1), "+v"(b1));
+  x0 = a0 + b0;
+  x1 = a1 + b1;
+}
+__device__ __forceinline__ void halve32(float a0, float b0, float a1, float b1, float &x0, float &x1) {
+  asm volatile("s_nop 1\n\tv_permlane32_swap_b32 %0, %1\n\tv_permlane32_swap_b32 %2, %3\n\ts_nop 1"
+               : "+v"(a0), "+v"(b0), "+v"(a1), "+v"(b1));
+  x0 = a0 + b0;
+  x1 = a1 + b1;
+}
+// Sums over the channels of a wave: u = b[r], v = c[r] of row r = lane / 16, in each lane of its part of the states.
+template <int P> __device__ __forceinline__ void channel_sums(const f4 &b, const f4 &c, float &u, float &v) {
+  float q0, q1, q2, q3;
+  halve16(b[0], b[1], b[2], b[3], q0, q1);
+  halve16(c[0], c[1], c[2], c[3], q2, q3);
+  halve32(q0, q1, q2, q3, u, v);
+  if constexpr (P <= 4) { u += dpp_mov<0x124>(u); v += dpp_mov<0x124>(v); }    // row_ror:4
+  if constexpr (P <= 8) { u += dpp_mov<0x128>(u); v += dpp_mov<0x128>(v); }    // row_ror:8
+}
+
+// MAPS: only the segment's map (r at its start from zero behind its end, sum of delta) is formed.
+template <typename T, int N, bool MAPS> __global__ __launch_bounds__(SSM_THR, MAPS ? 4 : 2) void ssm_bwd(SsmArgs a) {
+  typedef SsmTile<N> L;
+  constexpr int V = L::VEC;
+  __shared__ __align__(16) float2 step[L::TS][SSM_CH];       // (delta, delta x); then (sum g B, sum r h A)
+  __shared__ float sgy[L::TS][SSM_CH];                       // gy; then sum C h
+  __shared__ __align__(16) float sB[L::TS][N], sC[L::TS][N];
+  __shared__ __align__(16) float mapP[L::TW][SSM_CH][N], mapG[L::TW][SSM_CH][N], mapH[MAPS ? 1 : L::TW][SSM_CH][N];
+  __shared__ __align__(16) float red[MAPS ? 1 : L::WIDE][L::TS][2 * N];
+  __shared__ float sumd[L::TW][SSM_CH];
+  const int groups = (a.D + SSM_CH - 1) / SSM_CH;
+  const int slots = slots_of(a.seq, a.seg), id = dealt(groups * slots);
+  if (id >= groups * slots) return;
+  const Segment g = find_segment(a.seq, a.seg, id / groups);
+  const int group = id % groups, c0 = group * SSM_CH;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tw = wave / L::WIDE, wide = wave % L::WIDE, ch = wide * L::CW + lane / L::P, p4 = (lane % L::P) * 4;
+  const int c = c0 + ch;
+  const bool on = c < a.D;
+  const int ls = tid / (SSM_CH / V), lc = (tid % (SSM_CH / V)) * V, lcc = c0 + lc;
+  const bool lon = lcc < a.D;
+  const bool empty = g.s == g.e && g.slot == first_slot(a.seq, g.n, a.seg);
+  const bool first = g.t0 == g.s, lastseg = g.t1 == g.e;
+  if constexpr (MAPS) {
+    if (!g.any || first) return;        // nobody starts from its end
+  }
+  f4 A{0.f, 0.f, 0.f, 0.f}, r{0.f, 0.f, 0.f, 0.f};
+  if (on) {
+    A = *reinterpret_cast<const f4 *>(a.A + (size_t)c * N + p4);
+    if constexpr (!MAPS) {
+      if (g.any && !lastseg) r = *reinterpret_cast<const f4 *>(a.seg_state + ((size_t)g.slot * a.D + c) * N + p4);
+      else if ((g.any || empty) && a.d_final) r = *reinterpret_cast<const f4 *>(a.d_final + ((size_t)g.n * a.D + c) * N + p4);
+    }
+  }
+  const f4 A2 = A * SSM_LOG2E;
+  const int bs = tid / (N / 2), bn = (tid % (N / 2)) * 2;
+  float bias[V] = {}, skip[V] = {};
+  if (lon) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if (a.bias) bias[j] = a.bias[lcc + j];
+      if (a.skip) skip[j] = a.skip[lcc + j];
+    }
+  }
+  const int chunk0 = MAPS ? 0 : first_slot(a.seq, g.n, L::TS);
+  f4 dA{0.f, 0.f, 0.f, 0.f};
+  float dD[V] = {}, dbias[V] = {}, total = 0.f;
+  const int64_t tokens = a.seq.tokens();
+  for (int t = g.any ? g.t0 + (g.t1 - g.t0 - 1) / L::TS * L::TS : g.t0 - 1; t >= g.t0; t -= L::TS) {
+    const int q = min(t + ls, g.t1 - 1), qb = min(t + bs, g.t1 - 1), cc = lon ? lcc : 0;
+    const bool valid = lon && t + ls < g.t1;     // steps behind the end change nothing: delta = gy = 0
+    float x[V], d[V], z[V] = {}, dy[V], gy[V], slope[V], b2[2], c2[2];
+    load_few<V>(static_cast<const T *>(a.x) + (int64_t)q * a.ldx + cc, x);
+    load_few<V>(static_cast<const T *>(a.dt) + (int64_t)q * a.lddt + cc, d);
+    if (a.z) load_few<V>(static_cast<const T *>(a.z) + (int64_t)q * a.ldz + cc, z);
+    load_few<V>(static_cast<const T *>(a.dy) + (size_t)q * a.D + cc, dy);
+    load_few<2>(static_cast<const T *>(a.B) + (int64_t)qb * a.ldB + bn, b2);
+    load_few<2>(static_cast<const T *>(a.C) + (int64_t)qb * a.ldC + bn, c2);
+    f4 hv{0.f, 0.f, 0.f, 0.f};                   // the tile's first state, then this wave's
+    if constexpr (!MAPS) {
+      if (on) hv = *reinterpret_cast<const f4 *>(a.states + ((size_t)(chunk0 + (t - g.s) / L::TS) * a.D + c) * N + p4);
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      d[j] += bias[j];
+      slope[j] = 1.f;
+      if (a.softplus) { slope[j] = sigmoid(d[j]); d[j] = softplus(d[j]); }
+      gy[j] = a.z ? dy[j] * (z[j] * sigmoid(z[j])) : dy[j];
+      step[ls][lc + j] = valid ? float2{d[j], d[j] * x[j]} : float2{0.f, 0.f};
+      sgy[ls][lc + j] = valid ? gy[j] : 0.f;
+    }
+    *reinterpret_cast<float2 *>(&sB[bs][bn]) = float2{b2[0], b2[1]};
+    *reinterpret_cast<float2 *>(&sC[bs][bn]) = float2{c2[0], c2[1]};
+    __syncthreads();
+    const int s0 = tw * SSM_STEPS;
+    f4 dec[SSM_STEPS];
+    float sd = 0.f;
+    f4 H{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < SSM_STEPS; ++s) {
+      const float2 du = step[s0 + s][ch];
+      sd += du.x;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) dec[s][j] = __builtin_amdgcn_exp2f(du.x * A2[j]);
+      if constexpr (L::TW > 1 && !MAPS) {
+        const f4 b = *reinterpret_cast<const f4 *>(&sB[s0 + s][p4]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) H[j] = fmaf(dec[s][j], H[j], du.y * b[j]);
+      }
+    }
+    f4 mine = r;                                 // r behind this wave's steps
+    if constexpr (L::TW > 1 || MAPS) {
+      f4 G{0.f, 0.f, 0.f, 0.f}, Pm;
+#pragma unroll
+      for (int s = SSM_STEPS - 1; s >= 0; --s) {
+        const float gv = sgy[s0 + s][ch];
+        const f4 cv = *reinterpret_cast<const f4 *>(&sC[s0 + s][p4]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) G[j] = dec[s][j] * fmaf(gv, cv[j], G[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) Pm[j] = __builtin_amdgcn_exp2f(sd * A2[j]);
+      *reinterpret_cast<f4 *>(&mapP[tw][ch][p4]) = Pm;
+      *reinterpret_cast<f4 *>(&mapG[tw][ch][p4]) = G;
+      if constexpr (!MAPS) *reinterpret_cast<f4 *>(&mapH[tw][ch][p4]) = H;
+      if (MAPS && p4 == 0) sumd[tw][ch] = sd;
+      __syncthreads();
+      f4 run = r;
+#pragma unroll
+      for (int w = L::TW - 1; w >= 0; --w) {
+        if (w == tw) mine = run;
+        const f4 Pw = *reinterpret_cast<const f4 *>(&mapP[w][ch][p4]), Gw = *reinterpret_cast<const f4 *>(&mapG[w][ch][p4]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) run[j] = fmaf(Pw[j], run[j], Gw[j]);
+        if (MAPS) total += sumd[w][ch];
+      }
+      r = run;
+      if constexpr (!MAPS) {
+#pragma unroll
+        for (int w = 0; w < L::TW - 1; ++w) {
+          if (w < tw) {
+            const f4 Pw = *reinterpret_cast<const f4 *>(&mapP[w][ch][p4]), Hw = *reinterpret_cast<const f4 *>(&mapH[w][ch][p4]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) hv[j] = fmaf(Pw[j], hv[j], Hw[j]);
+          }
+        }
+      }
+    }
+    if constexpr (!MAPS) {
+      f4 hp[SSM_STEPS + 1];                      // the state before every step
+      hp[0] = hv;
+#pragma unroll
+      for (int s = 0; s < SSM_STEPS; ++s) {
+        const float2 du = step[s0 + s][ch];
+        const f4 b = *reinterpret_cast<const f4 *>(&sB[s0 + s][p4]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) hp[s + 1][j] = fmaf(dec[s][j], hp[s][j], du.y * b[j]);
+      }
+#pragma unroll
+      for (int s = SSM_STEPS - 1; s >= 0; --s) {
+        const float2 du = step[s0 + s][ch];
+        const float gv = sgy[s0 + s][ch];
+        const f4 b = *reinterpret_cast<const f4 *>(&sB[s0 + s][p4]), cv = *reinterpret_cast<const f4 *>(&sC[s0 + s][p4]);
+        f4 gb, gc;
+        float sum_b = 0.f, sum_a = 0.f, read = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float gj = fmaf(gv, cv[j], mine[j]);
+          gb[j] = gj * du.y;
+          gc[j] = gv * hp[s + 1][j];
+          sum_b = fmaf(gj, b[j], sum_b);
+          read = fmaf(cv[j], hp[s + 1][j], read);
+          mine[j] = dec[s][j] * gj;
+          const float w = mine[j] * hp[s][j];
+          sum_a = fmaf(w, A[j], sum_a);
+          dA[j] = fmaf(w, du.x, dA[j]);
+        }
+        sum_b = lane_sum<L::P>(sum_b);
+        sum_a = lane_sum<L::P>(sum_a);
+        read = lane_sum<L::P>(read);
+        float u, v;
+        channel_sums<L::P>(gb, gc, u, v);
+        if ((lane & 15) < L::P) {
+          red[wide][s0 + s][p4 + (lane >> 4)] = u;
+          red[wide][s0 + s][N + p4 + (lane >> 4)] = v;
+        }
+        if (p4 == 0) {
+          step[s0 + s][ch] = float2{sum_b, sum_a};
+          sgy[s0 + s][ch] = read;
+        }
+      }
+      if constexpr (L::TW == 1) r = mine;
+    }
+    __syncthreads();
+    if constexpr (!MAPS) {
+      if (valid) {
+        float dx[V], ddt[V], dz[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float2 s2 = step[ls][lc + j];
+          dx[j] = fmaf(s2.x, d[j], skip[j] * gy[j]);
+          ddt[j] = fmaf(s2.x, x[j], s2.y) * slope[j];
+          dD[j] = fmaf(gy[j], x[j], dD[j]);
+          dbias[j] += ddt[j];
+          if (a.z) {
+            const float sg = sigmoid(z[j]);
+            dz[j] = dy[j] * fmaf(skip[j], x[j], sgy[ls][lc + j]) * (sg * fmaf(z[j], 1.f - sg, 1.f));
+          }
+        }
+        store_few<V>(static_cast<T *>(a.dx) + (int64_t)q * a.lddx + lcc, dx);
+        store_few<V>(static_cast<T *>(a.ddt) + (int64_t)q * a.ldddt + lcc, ddt);
+        if (a.z) store_few<V>(static_cast<T *>(a.dz) + (int64_t)q * a.lddz + lcc, dz);
+      }
+      float *out = a.part_bc + ((size_t)group * tokens + t) * (2 * N);
+      for (int i = tid; i < L::TS * 2 * N; i += SSM_THR) {
+        if (t + i / (2 * N) >= g.t1) continue;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < L::WIDE; ++w) v += (&red[w][0][0])[i];
+        out[i] = v;
+      }
+    }
+  }
+  if constexpr (MAPS) {
+    if (tw == 0 && on) {
+      *reinterpret_cast<f4 *>(a.seg_map + ((size_t)g.slot * a.D + c) * N + p4) = r;
+      if (p4 == 0) a.seg_sum[(size_t)g.slot * a.D + c] = total;
+    }
+  } else {
+    if (tw == 0 && on && a.d_init && (empty || (g.any && first)))
+      *reinterpret_cast<f4 *>(a.d_init + ((size_t)g.n * a.D + c) * N + p4) = r;
+    // the segment's sums for A, D and the bias, over its waves (steps) in order; zeros without any
+    __syncthreads();
+    *reinterpret_cast<f4 *>(&mapH[tw][ch][p4]) = dA;
+    float(*sums)[SSM_CH] = &sgy[0];               // dD over the steps, then dbias
+    constexpr int ROWS = L::TS;
+#pragma unroll
+    for (int j = 0; j < V; ++j) sums[ls][lc + j] = dD[j];
+    __syncthreads();
+    if (on && tw == 0) {
+#pragma unroll
+      for (int w = 1; w < L::TW; ++w) dA += *reinterpret_cast<const f4 *>(&mapH[w][ch][p4]);
+      *reinterpret_cast<f4 *>(a.part_A + ((size_t)g.slot * a.D + c) * N + p4) = dA;
+    }
+    float *out = a.part_D + (size_t)g.slot * 2 * a.D;
+    if (tid < SSM_CH && c0 + tid < a.D) {
+      float v = 0.f;
+      for (int i = 0; i < ROWS; ++i) v += sums[i][tid];
+      out[c0 + tid] = v;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < V; ++j) sums[ls][lc + j] = dbias[j];
+    __syncthreads();
+    if (tid < SSM_CH && c0 + tid < a.D) {
+      float v = 0.f;
+      for (int i = 0; i < ROWS; ++i) v += sums[i][tid];
+      out[a.D + c0 + tid] = v;
+    }
+  }
+}
+
+// r behind every segment of a sequence but its last, in reverse order.
+template <int N> __global__ __launch_bounds__(256) void ssm_chain_bwd(SsmArgs a) {
+  const int per = a.D * (N / 4), i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= per) return;
+  const int c = i / (N / 4), p4 = (i % (N / 4)) * 4;
+  const f4 A2 = *reinterpret_cast<const f4 *>(a.A + (size_t)c * N + p4) * SSM_LOG2E;
+  for (int n = blockIdx.y; n < a.seq.n; n += gridDim.y) {
+    const int s = a.seq.begin(n), e = a.seq.end(n), slot = first_slot(a.seq, n, a.seg);
+    f4 r{0.f, 0.f, 0.f, 0.f};
+    if (a.d_final) r = *reinterpret_cast<const f4 *>(a.d_final + ((size_t)n * a.D + c) * N + p4);
+    for (int k = e > s ? (e - s - 1) / a.seg : 0; k > 0; --k) {
+      const size_t at = ((size_t)(slot + k) * a.D + c) * N + p4;
+      const float sd = a.seg_sum[(size_t)(slot + k) * a.D + c];
+      const f4 G = *reinterpret_cast<const f4 *>(a.seg_map + at);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r[j] = fmaf(__builtin_amdgcn_exp2f(sd * A2[j]), r[j], G[j]);
+      *reinterpret_cast<f4 *>(a.seg_state + at - (size_t)a.D * N) = r;
+    }
+  }
+}
+
+// dB and dC: the sums over the groups of channels, in order.
+template <typename T, int N> __global__ __launch_bounds__(256) void ssm_sum_bc(SsmArgs a, int groups) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, tokens = a.seq.tokens();
+  if (i >= tokens * 2 * N) return;
+  const int64_t t = i / (2 * N);
+  const int n = (int)(i % (2 * N));
+  if (a.seq.cu && (t >= a.seq.end(a.seq.n - 1) || t < a.seq.begin(0))) return;      // tokens of no sequence
+  f4 s{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int k = 0; k < groups; ++k) s += *reinterpret_cast<const f4 *>(a.part_bc + (size_t)k * tokens * (2 * N) + i);
+  const float v[4] = {s[0], s[1], s[2], s[3]};
+  if (n < N) store_few<4>(static_cast<T *>(a.dB) + t * a.lddB + n, v);
+  else store_few<4>(static_cast<T *>(a.dC) + t * a.lddC + n - N, v);
+}
+
+size_t align16(size_t n) { return (n + 15) / 16 * 16; }
+
+struct Parts { size_t bc, A, D, map, sum, total; };
+Parts parts_of(const SeqMap &q, int D, int N) {
+  const int seg = ssm_segment(q, D);
+  const size_t groups = (D + SSM_CH - 1) / SSM_CH, slots = slots_of(q, seg);
+  Parts p;
+  p.bc = align16(groups * q.tokens() * 2 * N * sizeof(float));
+  p.A = align16(slots * D * N * sizeof(float));
+  p.D = align16(slots * 2 * D * sizeof(float));
+  const bool cut = ssm_segmented(q, seg);
+  p.map = cut ? align16((slots + 1) * D * N * sizeof(float)) : 0;
+  p.sum = cut ? align16((slots + 1) * D * sizeof(float)) : 0;
+  p.total = p.bc + p.A + p.D + 2 * p.map + p.sum;
+  return p;
+}
+
+}  // namespace
+
+size_t ssm_bwd_workspace(SeqMap seq, int D, int N) { return parts_of(seq, D, N).total; }
+
+template <typename T, int N> static hipError_t bwd(SsmArgs a, const SsmGrads &o, void *ws, hipStream_t s) {
+  const Parts p = parts_of(a.seq, a.D, N);
+  char *at = static_cast<char *>(ws);
+  a.part_bc = reinterpret_cast<float *>(at);
+  a.part_A = reinterpret_cast<float *>(at += p.bc);
+  a.part_D = reinterpret_cast<float *>(at += p.A);
+  a.seg_map = reinterpret_cast<float *>(at += p.D);
+  a.seg_state = reinterpret_cast<float *>(at += p.map);
+  a.seg_sum = reinterpret_cast<float *>(at += p.map);
+  a.seg = ssm_segment(a.seq, a.D);
+  const int groups = (a.D + SSM_CH - 1) / SSM_CH, slots = slots_of(a.seq, a.seg);
+  const unsigned grid = dealt_grid((int64_t)groups * slots);
+  hipError_t e;
+  if (ssm_segmented(a.seq, a.seg)) {
+    hipLaunchKernelGGL((ssm_bwd<T, N, true>), dim3(grid), dim3(SSM_THR), 0, s, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    const int rows = a.seq.n < 65535 ? a.seq.n : 65535;
+    hipLaunchKernelGGL((ssm_chain_bwd<N>), dim3((a.D * (N / 4) + 255) / 256, rows), dim3(256), 0, s, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((ssm_bwd<T, N, false>), dim3(grid), dim3(SSM_THR), 0, s, a);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  const int64_t sums = (int64_t)a.seq.tokens() * 2 * N / 4;
+  hipLaunchKernelGGL((ssm_sum_bc<T, N>), dim3((unsigned)((sums + 255) / 256)), dim3(256), 0, s, a, groups);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  e = launch_column_sum(a.part_A, slots, (int64_t)a.D * N, o.dA, (int64_t)a.D * N, nullptr, s);
+  if (e != hipSuccess || (!o.dD && !o.dbias)) return e;
+  return launch_column_sum(a.part_D, slots, 2 * (int64_t)a.D, o.dD, a.D, o.dbias, s);
+}
+
+hipError_t launch_ssm_bwd(bool bf16, int N, SsmArgs a, SsmGrads o, void *ws, hipStream_t s) {
+  if (N == 16) return bf16 ? bwd<__bf16, 16>(a, o, ws, s) : bwd<float, 16>(a, o, ws, s);
+  if (N == 32) return bf16 ? bwd<__bf16, 32>(a, o, ws, s) : bwd<float, 32>(a, o, ws, s);
+  if (N == 64) return bf16 ? bwd<__bf16, 64>(a, o, ws, s) : bwd<float, 64>(a, o, ws, s);
+  return hipErrorInvalidValue;
+}
+
+}  // namespace falcon

@@ -12,13 +12,13 @@
 namespace falcon {
 
 constexpr int SSM_THR = 512, SSM_CH = 32, SSM_STEPS = 16;
-constexpr int SSM_CHUNK = 64;      // steps between the states that the forward keeps (FALCON_SSM_CHUNK)
+constexpr int SSM_ALIGN = 64;      // segments are a multiple of this long: whole tiles of every N
 constexpr float SSM_LOG2E = 1.44269504088896340736f;
 
 template <int N> struct SsmTile {
   static constexpr int P = N / 4, CW = 64 / P, WIDE = SSM_CH / CW, TW = 8 / WIDE, TS = TW * SSM_STEPS;
   static constexpr int VEC = TS * SSM_CH / SSM_THR;     // channels of a step that a thread loads: 4, 2 or 1
-  static_assert(SSM_CHUNK % TS == 0, "chunks begin with a tile");
+  static_assert(SSM_ALIGN % TS == 0 && TS * N == 1024, "segments are whole tiles");
 };
 
 // V consecutive entries as floats; the address is a multiple of their size together.

@@ -31,7 +31,8 @@ EXPORTS = ("falcon_abi_version", "falcon_status_string", "falcon_chunk_fwd_works
            # the operators of a state-space block (block.py)
            "falcon_rms_norm", "falcon_rms_norm_bwd_workspace", "falcon_rms_norm_bwd",
            "falcon_conv_fwd", "falcon_conv_bwd_workspace", "falcon_conv_bwd", "falcon_conv_step",
-           "falcon_ssm_fwd_workspace", "falcon_ssm_chunks", "falcon_ssm_fwd", "falcon_ssm_step")
+           "falcon_ssm_fwd_workspace", "falcon_ssm_chunks", "falcon_ssm_fwd", "falcon_ssm_bwd_workspace",
+           "falcon_ssm_bwd", "falcon_ssm_step")
 
 
 class Shape(ctypes.Structure):
@@ -175,6 +176,11 @@ def lib() -> ctypes.CDLL:
         L.falcon_ssm_chunks.argtypes = [P(SsmShape), I]
         L.falcon_ssm_fwd.restype = I
         L.falcon_ssm_fwd.argtypes = [P(SsmShape), V, Heads, Heads, V, Heads, Heads, V, Heads, V, V, V, V, V, V, S, V]
+        L.falcon_ssm_bwd_workspace.restype = S
+        L.falcon_ssm_bwd_workspace.argtypes = [P(SsmShape), I]
+        L.falcon_ssm_bwd.restype = I
+        L.falcon_ssm_bwd.argtypes = [P(SsmShape), V, Heads, Heads, V, Heads, Heads, V, Heads, V, V, V, V, Heads, Heads, V,
+                                     Heads, Heads, V, Heads, V, V, V, S, V]
         L.falcon_ssm_step.restype = I
         L.falcon_ssm_step.argtypes = [P(SsmShape), Heads, Heads, V, Heads, Heads, V, Heads, V, V, V, V, V]
         _LIB = L
