@@ -662,6 +662,46 @@ int falcon_ssm_step(const falcon_ssm_shape_t *shape, falcon_heads_t x, falcon_he
                     falcon_heads_t Bm, falcon_heads_t Cm, const float *D, falcon_heads_t z, const float *dt_bias,
                     const float *state, float *state_out, void *y, void *stream);
 
+/* ---- Projections -----------------------------------------------------------
+ *   p = x W^T (x_scale, weight_scale) + bias,  y = act(p) + residual
+ * with x [tokens, in] and W [out, in] in dtype.  E4M3: entry (t, o) of the product is scaled by
+ * x_scale[t] weight_scale[o], as falcon_rms_norm and its form without norm leave rows.  Sums
+ * are fp32 and y is rounded once. */
+typedef struct {
+  int32_t dtype;       /* falcon_dtype_t of x and W: F32, BF16 or E4M3 */
+  int32_t tokens;      /* 1 .. 2^31 - 4097 */
+  int32_t in;          /* a multiple of 16, at most 2^20 */
+  int32_t out;         /* a multiple of 8, at most 2^20 */
+  int32_t activation;  /* falcon_activation_t */
+  int32_t out_dtype;   /* falcon_dtype_t of y and residual: dtype; for E4M3 F32 or BF16 */
+} falcon_linear_shape_t;
+
+/* Bytes of workspace of the forward: the sums of workgroups that split `in`, where there are
+ * few tokens but more than 64; 0 elsewhere (then workspace may be NULL) and for invalid shapes. */
+size_t falcon_linear_fwd_workspace(const falcon_linear_shape_t *shape);
+
+/*   x             token stride at most 2^23 bytes;  weight dense.
+ *   x_scale, weight_scale  [tokens], [out] fp32 for E4M3, else NULL.
+ *   bias          [out] fp32, or NULL;  residual [tokens, out] in out_dtype, or NULL.
+ *   y             [tokens, out]; may be the residual itself.
+ *   pre           [tokens, out] fp32: receives p, for the backward pass of an activation; or
+ *                 NULL.  Outputs must not overlap inputs otherwise. */
+int falcon_linear_fwd(const falcon_linear_shape_t *shape, falcon_heads_t x, const void *weight, const float *x_scale,
+                      const float *weight_scale, const float *bias, const void *residual, void *y, float *pre,
+                      void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of the backward: the gradient of p, and partial sums. */
+size_t falcon_linear_bwd_workspace(const falcon_linear_shape_t *shape);
+
+/* Gradients of <d_y, y> (the residual's is d_y itself), for F32 and BF16: with
+ * d = d_y act'(pre), dx = d W and dweight = d^T x in dtype, dbias = the sum of d over tokens, fp32;
+ * any may be NULL (dx: {NULL, 0}).  For BF16 with an activation the products take d rounded to
+ * BF16 (dbias the unrounded d).  pre as the forward wrote it (without an activation it is
+ * ignored).  Strides of x and d_y at most 2^23 bytes.  Outputs must not alias inputs. */
+int falcon_linear_bwd(const falcon_linear_shape_t *shape, falcon_heads_t x, const void *weight, const float *pre,
+                      falcon_heads_t d_y, falcon_heads_out_t dx, void *dweight, float *dbias,
+                      void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -11,5 +11,5 @@ from .falcon import (VARIANTS, FalconError, ForwardCall, chunk_fwd, chunk_fwd_va
                      segmented_workspace_bytes)
 from .layer import (SCAN_CHUNK, attention_bwd, attention_fwd, gated_scan, gated_scan_bwd, gated_scan_step,  # noqa: F401
                     qk_norm_rope, qk_norm_rope_bwd, rope_frequencies)
-from .block import (causal_conv, causal_conv_bwd, causal_conv_step, quantize_rows, rms_norm,  # noqa: F401
+from .block import (causal_conv, causal_conv_bwd, causal_conv_step, linear, linear_bwd, quantize_rows, rms_norm,  # noqa: F401
                     rms_norm_bwd, selective_scan, selective_scan_bwd, selective_scan_step)

@@ -11,7 +11,7 @@ from __future__ import annotations
 import ctypes
 import functools
 
-from .falcon import ConvShape, Heads, NormShape, SsmShape, lib
+from .falcon import ConvShape, Heads, LinearShape, NormShape, SsmShape, lib
 from .layer import _check, _current, _device, _done, _dtype, _ints, _offsets, _on, _p, _workspace
 
 E4M3 = 2   # FALCON_E4M3
@@ -399,3 +399,100 @@ def selective_scan_step(x, dt, A, B, C, state, *, D=None, z=None, dt_bias=None, 
         shape, *_ = _ssm_plan(kind, n, 1, width, N, 1 if softplus else 0, False)
         _done(lib().falcon_ssm_step(shape, *args, _p(state), _p(state_out), _p(out), _current(dev)), "falcon_ssm_step")
     return out
+
+
+# ---- Projections --------------------------------------------------------------------------------
+
+@functools.lru_cache(maxsize=1024)
+def _linear_plan(dtype, tokens, K, N, act, out):
+    """(pointer to the C shape, workspace bytes of the forward, of the backward)."""
+    shape = LinearShape(dtype, *_ints(tokens, K, N), act, out)
+    L, ref = lib(), ctypes.byref(shape)
+    return ctypes.pointer(shape), L.falcon_linear_fwd_workspace(ref), L.falcon_linear_bwd_workspace(ref)
+
+
+def _linear_shape(x, weight, activation, out_dtype):
+    import torch
+    dev = _device("x", x)
+    f8 = x.dtype is _f8()
+    kind = E4M3 if f8 else _dtype("x", x)
+    if weight.dim() != 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
+        raise ValueError(f"x, weight: shapes {tuple(x.shape)}, {tuple(weight.shape)}, expected [..., in], [out, in]")
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if f8 else x.dtype
+    if not f8 and out_dtype is not x.dtype:
+        raise TypeError(f"out_dtype: {out_dtype}, expected {x.dtype} (only 8-bit operands have another)")
+    N, K = weight.shape
+    _check("weight", weight, x.dtype, (N, K), dev)
+    out = {torch.float32: 0, torch.bfloat16: 1}.get(out_dtype)
+    if out is None:
+        raise TypeError("out_dtype must be float32 or bfloat16")
+    lead = x.shape[:-1]
+    plan = _linear_plan(kind, x.numel() // max(K, 1), K, N, _activation(activation), out)
+    return *plan, lead, out_dtype, f8, dev
+
+
+def linear(x, weight, *, bias=None, activation=None, residual=None, x_scale=None, weight_scale=None, pre=False,
+           out_dtype=None, out=None, workspace=None, stream=None):
+    """falcon_linear_fwd on torch tensors: y = act(x weight^T + bias) + residual.
+
+    x [...,in], weight [out,in] (float32 or bfloat16; in a multiple of 16, out of 8; x may be
+    a view of a wider projection), bias [out] float32, residual [...,out] like y;
+    ``activation``: None, "silu" or "gelu".  Or both float8_e4m3fn, with ``x_scale`` [...] and
+    ``weight_scale`` [out] float32 (as ``rms_norm(..., quantize=True)`` and ``quantize_rows``
+    give them) and ``out_dtype`` bfloat16 (default) or float32.  ``pre``: whether to return the
+    activation's argument [...,out] float32, which linear_bwd needs with an activation.  ``out``: None or a tensor
+    for y, which may be the residual.  Returns (y, pre)."""
+    import torch
+    shape, need, _, lead, odt, f8, dev = _linear_shape(x, weight, activation, out_dtype)
+    N = weight.shape[0]
+    hx = _rows("x", x, x.dtype, dev)
+    full = lead + (N,)
+    _maybe("bias", bias, torch.float32, (N,), dev)
+    _maybe("residual", residual, odt, full, dev)
+    if f8 != (x_scale is not None) or f8 != (weight_scale is not None):
+        raise ValueError("x_scale, weight_scale: both for 8-bit operands, and for those only")
+    if f8:
+        _check("x_scale", x_scale, torch.float32, lead, dev)
+        _check("weight_scale", weight_scale, torch.float32, (N,), dev)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(full, dtype=odt, device=dev)
+        else:
+            _check("y", out, odt, full, dev)
+        keep = torch.empty(full, dtype=torch.float32, device=dev) if pre else None
+        ws, nbytes = _workspace(need, workspace, dev)
+        _done(lib().falcon_linear_fwd(shape, hx, _p(weight), _p(x_scale), _p(weight_scale), _p(bias), _p(residual), _p(out),
+                                      _p(keep), _p(ws), nbytes, _current(dev)), "falcon_linear_fwd")
+    return out, keep
+
+
+def linear_bwd(x, weight, dy, *, pre=None, activation=None, bias=False, dx=True, dweight=True, workspace=None, stream=None):
+    """falcon_linear_bwd on torch tensors: gradients of <dy, y> for ``linear`` of the same
+    arguments (float32 or bfloat16; the residual's gradient is dy itself).
+
+    dy [...,out] in the dtype of x (a view with dense rows will do); ``pre`` as ``linear(...,
+    pre=True)`` returned it, needed with an activation.  ``bias``: whether to return a bias's
+    gradient; ``dx``: True (allocate), a tensor to write (a view with dense rows will do) or
+    False; ``dweight``: True, a tensor or False.  Returns dict(dx, dweight, dbias): dx and
+    dweight in the dtype of x, dbias [out] float32."""
+    import torch
+    shape, _, need, lead, _, f8, dev = _linear_shape(x, weight, activation, None)
+    if f8:
+        raise TypeError("x: 8-bit operands have no backward pass")
+    N, K = weight.shape
+    hx = _rows("x", x, x.dtype, dev)
+    hdy = _rows("dy", dy, x.dtype, dev, lead + (N,))
+    if activation is not None and pre is None:
+        raise ValueError("pre: needed with an activation")
+    _maybe("pre", pre, torch.float32, lead + (N,), dev)
+    with _on(dev, stream):
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if dx is True else None if dx is False else dx
+        hdx = _NO_ROWS if dx is None else _rows("dx", dx, x.dtype, dev, x.shape)
+        dweight = torch.empty_like(weight) if dweight is True else None if dweight is False else dweight
+        _maybe("dweight", dweight, x.dtype, (N, K), dev)
+        dbias = torch.empty((N,), dtype=torch.float32, device=dev) if bias else None
+        ws, nbytes = _workspace(need, workspace, dev)
+        _done(lib().falcon_linear_bwd(shape, hx, _p(weight), _p(pre) if activation is not None else None, hdy, hdx,
+                                      _p(dweight), _p(dbias), _p(ws), nbytes, _current(dev)), "falcon_linear_bwd")
+    return dict(dx=dx, dweight=dweight, dbias=dbias)

@@ -23,7 +23,7 @@ SOURCES = ["falcon_abi.cpp", "falcon_fwd.hip", "falcon_fwd_pipe.hip", "falcon_fw
            "falcon_step.hip", "falcon_bwd.hip", "falcon_bwd_rows.hip", "falcon_segment.hip", "falcon_static.hip",
            "falcon_layer_abi.cpp", "falcon_scan.hip", "falcon_qk.hip", "falcon_attn.hip", "falcon_attn_bwd.hip",
            "falcon_block_abi.cpp", "falcon_colsum.hip", "falcon_norm.hip", "falcon_conv.hip", "falcon_ssm.hip",
-           "falcon_ssm_bwd.hip"]
+           "falcon_ssm_bwd.hip", "falcon_linear.hip"]
 ARCH = "gfx950"
 FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",

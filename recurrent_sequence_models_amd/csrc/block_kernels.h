@@ -100,4 +100,33 @@ size_t ssm_bwd_workspace(SeqMap seq, int D, int N);
 hipError_t launch_ssm_bwd(bool bf16, int N, SsmArgs a, SsmGrads o, void *ws, hipStream_t s);
 hipError_t launch_ssm_step(bool bf16, int N, SsmArgs a, hipStream_t s);
 
+// Projections.  A product out[j][i] = sum_k left(i, k) right(j, k), i < I, j < J, k < K, with its epilogue; `ld`:
+// entries between two rows of memory.
+constexpr int FALCON_SILU = 1, FALCON_GELU = 2;   // FALCON_ACT_*
+struct LinearArgs {
+  const void *left, *right;
+  int64_t ldl, ldr, ldo;
+  int I, J, K, splits;
+  void *out;
+  float *pre;                       // [J, I] or null
+  const float *scale_l, *scale_r;   // [I], [J], of 8-bit operands
+  const float *bias;                // [I] or null
+  const void *residual;             // [J, I] or null
+  float *part;                      // workspace: sums of the splits [splits, J, I]
+  int act;
+};
+struct LinearGrads {
+  const void *x, *w, *dy;           // [tokens, in], [out, in], [tokens, out]
+  const float *pre;                 // [tokens, out], with an activation
+  void *dx, *dw;                    // or null
+  float *dbias;                     // or null
+  int64_t ldx, lddy, lddx;
+  int tokens, in, out, act;
+};
+bool linear_fits(int entry_bytes, int64_t tokens, int64_t in, int64_t out);
+size_t linear_fwd_workspace(int entry_bytes, int64_t tokens, int64_t in, int64_t out);
+size_t linear_bwd_workspace(int entry_bytes, bool act, int64_t tokens, int64_t in, int64_t out);
+hipError_t launch_linear_fwd(int dtype, bool bf16_out, LinearArgs a, void *ws, hipStream_t s);
+hipError_t launch_linear_bwd(bool bf16, const LinearGrads &g, void *ws, hipStream_t s);
+
 }  // namespace falcon

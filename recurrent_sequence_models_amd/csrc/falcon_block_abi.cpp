@@ -349,3 +349,97 @@ int falcon_ssm_step(const falcon_ssm_shape_t *s, falcon_heads_t x, falcon_heads_
 }
 
 }  // extern "C"
+
+// ---- Projections -----------------------------------------------------------------------
+namespace {
+
+int check_linear(const falcon_linear_shape_t *s) {
+  if (!s || (!float_dtype(s->dtype) && s->dtype != FALCON_E4M3) || !float_dtype(s->out_dtype)) return FALCON_ERR_INVALID_ARG;
+  if (s->activation < FALCON_ACT_NONE || s->activation > FALCON_ACT_GELU) return FALCON_ERR_INVALID_ARG;
+  if (s->tokens < 1 || s->in < 1 || s->out < 1) return FALCON_ERR_INVALID_ARG;
+  if (s->dtype != FALCON_E4M3 && s->out_dtype != s->dtype) return FALCON_ERR_UNSUPPORTED;
+  if (s->in % 16 != 0 || s->out % 8 != 0 || s->in > (1 << 20) || s->out > (1 << 20)) return FALCON_ERR_UNSUPPORTED;
+  // token numbers are ints, with a tile added
+  if (s->tokens > INT32_MAX - 4096) return FALCON_ERR_UNSUPPORTED;
+  return falcon::linear_fits(esize(s->dtype), s->tokens, s->in, s->out) ? FALCON_OK : FALCON_ERR_UNSUPPORTED;
+}
+
+constexpr int64_t MOST_STEP = 1 << 23;   // bytes between two tokens: the rows of a tile, at most 256, are 32 bits apart
+
+int check_operand(falcon_heads_t t, int64_t tokens, int64_t width, int e) {
+  FALCON_TRY(check_rows(t.data, t.token_stride, tokens, width, e));
+  return t.token_stride > MOST_STEP / e ? FALCON_ERR_UNSUPPORTED : FALCON_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t falcon_linear_fwd_workspace(const falcon_linear_shape_t *s) {
+  if (check_linear(s) != FALCON_OK) return 0;
+  return falcon::linear_fwd_workspace(esize(s->dtype), s->tokens, s->in, s->out);
+}
+
+int falcon_linear_fwd(const falcon_linear_shape_t *s, falcon_heads_t x, const void *weight, const float *x_scale,
+                      const float *weight_scale, const float *bias, const void *residual, void *y, float *pre, void *ws,
+                      size_t ws_bytes, void *stream) {
+  FALCON_TRY(check_linear(s));
+  FALCON_TRY(check_operand(x, s->tokens, s->in, esize(s->dtype)));
+  FALCON_TRY(need(weight, 16));
+  const bool q8 = s->dtype == FALCON_E4M3;
+  if (q8 ? !x_scale || !weight_scale : x_scale || weight_scale) return FALCON_ERR_INVALID_ARG;
+  FALCON_TRY(maybe(x_scale, 4));
+  FALCON_TRY(maybe(weight_scale, 4));
+  FALCON_TRY(maybe(bias, 4));
+  FALCON_TRY(maybe(residual, 16));
+  FALCON_TRY(need(y, 16));
+  FALCON_TRY(maybe(pre, 16));
+  if (pre && ((const void *)pre == y || (const void *)pre == residual)) return FALCON_ERR_INVALID_ARG;
+  FALCON_TRY(check_workspace(ws, ws_bytes, falcon_linear_fwd_workspace(s)));
+  falcon::LinearArgs a{};
+  a.left = weight; a.ldl = s->in;
+  a.right = x.data; a.ldr = x.token_stride;
+  a.I = s->out; a.J = s->tokens; a.K = s->in;
+  a.out = y; a.ldo = s->out;
+  a.pre = pre;
+  a.scale_l = weight_scale; a.scale_r = x_scale;
+  a.bias = bias;
+  a.residual = residual;
+  a.act = s->activation;
+  return status_of(falcon::launch_linear_fwd(s->dtype, s->out_dtype == FALCON_BF16, a, ws, static_cast<hipStream_t>(stream)));
+}
+
+size_t falcon_linear_bwd_workspace(const falcon_linear_shape_t *s) {
+  if (check_linear(s) != FALCON_OK || s->dtype == FALCON_E4M3) return 0;
+  return falcon::linear_bwd_workspace(esize(s->dtype), s->activation != FALCON_ACT_NONE, s->tokens, s->in, s->out);
+}
+
+int falcon_linear_bwd(const falcon_linear_shape_t *s, falcon_heads_t x, const void *weight, const float *pre,
+                      falcon_heads_t d_y, falcon_heads_out_t dx, void *dweight, float *dbias, void *ws, size_t ws_bytes,
+                      void *stream) {
+  FALCON_TRY(check_linear(s));
+  if (s->dtype == FALCON_E4M3) return FALCON_ERR_UNSUPPORTED;
+  const int e = esize(s->dtype);
+  const bool act = s->activation != FALCON_ACT_NONE;
+  if (dweight) FALCON_TRY(check_operand(x, s->tokens, s->in, e));
+  if (dx.data) FALCON_TRY(need(weight, 16));
+  FALCON_TRY(act ? need(pre, 16) : FALCON_OK);
+  FALCON_TRY(check_operand(d_y, s->tokens, s->out, e));
+  if (dx.data) FALCON_TRY(check_rows(dx.data, dx.token_stride, s->tokens, s->in, e));
+  FALCON_TRY(maybe(dweight, 16));
+  FALCON_TRY(maybe(dbias, 4));
+  FALCON_TRY(check_workspace(ws, ws_bytes, falcon_linear_bwd_workspace(s)));
+  falcon::LinearGrads g{};
+  g.x = x.data; g.ldx = x.token_stride;
+  g.w = weight;
+  g.pre = pre;
+  g.dy = d_y.data; g.lddy = d_y.token_stride;
+  g.dx = dx.data; g.lddx = dx.token_stride;
+  g.dw = dweight;
+  g.dbias = dbias;
+  g.tokens = s->tokens; g.in = s->in; g.out = s->out;
+  g.act = s->activation;
+  return status_of(falcon::launch_linear_bwd(s->dtype == FALCON_BF16, g, ws, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

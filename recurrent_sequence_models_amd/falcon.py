@@ -32,7 +32,8 @@ EXPORTS = ("falcon_abi_version", "falcon_status_string", "falcon_chunk_fwd_works
            "falcon_rms_norm", "falcon_rms_norm_bwd_workspace", "falcon_rms_norm_bwd",
            "falcon_conv_fwd", "falcon_conv_bwd_workspace", "falcon_conv_bwd", "falcon_conv_step",
            "falcon_ssm_fwd_workspace", "falcon_ssm_chunks", "falcon_ssm_fwd", "falcon_ssm_bwd_workspace",
-           "falcon_ssm_bwd", "falcon_ssm_step")
+           "falcon_ssm_bwd", "falcon_ssm_step",
+           "falcon_linear_fwd_workspace", "falcon_linear_fwd", "falcon_linear_bwd_workspace", "falcon_linear_bwd")
 
 
 class Shape(ctypes.Structure):
@@ -79,6 +80,11 @@ class ConvShape(ctypes.Structure):
 class SsmShape(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("seqlen", ctypes.c_int32),
                 ("width", ctypes.c_int32), ("state", ctypes.c_int32), ("softplus", ctypes.c_int32)]
+
+
+class LinearShape(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("tokens", ctypes.c_int32), ("in_", ctypes.c_int32), ("out", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
 
 
 class Heads(ctypes.Structure):
@@ -183,6 +189,14 @@ def lib() -> ctypes.CDLL:
                                      Heads, Heads, V, Heads, V, V, V, S, V]
         L.falcon_ssm_step.restype = I
         L.falcon_ssm_step.argtypes = [P(SsmShape), Heads, Heads, V, Heads, Heads, V, Heads, V, V, V, V, V]
+        L.falcon_linear_fwd_workspace.restype = S
+        L.falcon_linear_fwd_workspace.argtypes = [P(LinearShape)]
+        L.falcon_linear_fwd.restype = I
+        L.falcon_linear_fwd.argtypes = [P(LinearShape), Heads, V, V, V, V, V, V, V, V, S, V]
+        L.falcon_linear_bwd_workspace.restype = S
+        L.falcon_linear_bwd_workspace.argtypes = [P(LinearShape)]
+        L.falcon_linear_bwd.restype = I
+        L.falcon_linear_bwd.argtypes = [P(LinearShape), Heads, V, V, Heads, Heads, V, V, V, S, V]
         _LIB = L
     return _LIB
 

@@ -14,7 +14,8 @@ def split(a, lens):
 def strided(t, more=24):
     """The same values as a view of rows `more` entries longer (a multiple of 16 bytes in every type)."""
     import torch
-    big = torch.full(t.shape[:-1] + (t.shape[-1] + more,), float("nan"), dtype=t.dtype, device=t.device)
+    none = 0x7f if t.dtype == torch.uint8 else float("nan")     # 0x7f: NaN of e4m3
+    big = torch.full(t.shape[:-1] + (t.shape[-1] + more,), none, dtype=t.dtype, device=t.device)
     big[..., :t.shape[-1]] = t
     return big[..., :t.shape[-1]]
 
