@@ -602,7 +602,7 @@ int falcon_conv_step(const falcon_conv_shape_t *shape, falcon_heads_t x, const f
  * (softplus = 0: delta_t = dt_t + dt_bias):
  *   h_t = exp(delta_t A[d][n]) h_{t-1} + delta_t x_t B_t[n]
  *   y_t = (sum_n C_t[n] h_t[n] + D[d] x_t) silu(z_t)         (z NULL: no gate)
- * B_t and C_t are shared by the channels.  A is finite; where delta_t A > 0 the state
+ * B_t and C_t are shared by the channels.  Token strides are at most 2^24 bytes.  A is finite; where delta_t A > 0 the state
  * grows, and its growth over 64 steps (where sequences are cut into segments, over a
  * segment) has to stay in fp32's range.  States, sums and delta are fp32. */
 typedef struct {

@@ -219,16 +219,22 @@ int check_ssm(const falcon_ssm_shape_t *s, bool packed, bool step) {
   return falcon::ssm_fits(seq_sizes(s->batch, s->seqlen, packed), s->width) ? FALCON_OK : FALCON_ERR_UNSUPPORTED;
 }
 
+// [tokens, width] whose tokens are at most 2^24 bytes apart: the rows of a tile, at most 64, are 32 bits apart.
+int check_near(const void *p, int64_t stride, int64_t tokens, int64_t width, int e) {
+  FALCON_TRY(check_rows(p, stride, tokens, width, e));
+  return stride > (1 << 24) / e ? FALCON_ERR_UNSUPPORTED : FALCON_OK;
+}
+
 int check_ssm_in(const falcon_ssm_shape_t *s, int64_t tokens, falcon_heads_t x, falcon_heads_t dt, const float *A,
                  falcon_heads_t B, falcon_heads_t C, const float *D, falcon_heads_t z, const float *bias) {
   const int e = esize(s->dtype);
-  FALCON_TRY(check_rows(x.data, x.token_stride, tokens, s->width, e));
-  FALCON_TRY(check_rows(dt.data, dt.token_stride, tokens, s->width, e));
+  FALCON_TRY(check_near(x.data, x.token_stride, tokens, s->width, e));
+  FALCON_TRY(check_near(dt.data, dt.token_stride, tokens, s->width, e));
   FALCON_TRY(need(A, 16));
-  FALCON_TRY(check_rows(B.data, B.token_stride, tokens, s->state, e));
-  FALCON_TRY(check_rows(C.data, C.token_stride, tokens, s->state, e));
+  FALCON_TRY(check_near(B.data, B.token_stride, tokens, s->state, e));
+  FALCON_TRY(check_near(C.data, C.token_stride, tokens, s->state, e));
   FALCON_TRY(maybe(D, 4));
-  if (z.data) FALCON_TRY(check_rows(z.data, z.token_stride, tokens, s->width, e));
+  if (z.data) FALCON_TRY(check_near(z.data, z.token_stride, tokens, s->width, e));
   return maybe(bias, 4);
 }
 
@@ -310,11 +316,11 @@ int falcon_ssm_bwd(const falcon_ssm_shape_t *s, const int32_t *cu, falcon_heads_
   FALCON_TRY(need(d_y, 16));
   FALCON_TRY(maybe(d_final, 16));
   const int e = esize(s->dtype);
-  FALCON_TRY(check_rows(dx.data, dx.token_stride, tokens, s->width, e));
-  FALCON_TRY(check_rows(ddt.data, ddt.token_stride, tokens, s->width, e));
-  FALCON_TRY(check_rows(dB.data, dB.token_stride, tokens, s->state, e));
-  FALCON_TRY(check_rows(dC.data, dC.token_stride, tokens, s->state, e));
-  if (z.data) FALCON_TRY(check_rows(dz.data, dz.token_stride, tokens, s->width, e));
+  FALCON_TRY(check_near(dx.data, dx.token_stride, tokens, s->width, e));
+  FALCON_TRY(check_near(ddt.data, ddt.token_stride, tokens, s->width, e));
+  FALCON_TRY(check_near(dB.data, dB.token_stride, tokens, s->state, e));
+  FALCON_TRY(check_near(dC.data, dC.token_stride, tokens, s->state, e));
+  if (z.data) FALCON_TRY(check_near(dz.data, dz.token_stride, tokens, s->width, e));
   FALCON_TRY(need(dA, 4));
   FALCON_TRY(maybe(dD, 4));
   FALCON_TRY(maybe(ddt_bias, 4));

@@ -20,26 +20,29 @@
 namespace falcon {
 namespace {
 
-// What a thread loads of a tile: VEC channels of one step, and two entries of B and C.
-template <typename T, int N> struct Loaded {
-  static constexpr int V = SsmTile<N>::VEC;
-  float x[V], dt[V], z[V], B[2], C[2];
-};
+constexpr int FWD_CH = 16;
+#ifndef SSM_FEW
+#define SSM_FEW 640
+#endif
+#ifndef SSM_WANT
+#define SSM_WANT 256
+#endif
 
 // MAPS: only the segment's map (end state from zero, sum of delta) is formed.
-template <typename T, int N, bool MAPS> __global__ __launch_bounds__(SSM_THR, 4) void ssm_fwd(SsmArgs a) {
-  typedef SsmTile<N> L;
-  constexpr int V = L::VEC;
-  __shared__ __align__(16) float2 step[L::TS][SSM_CH];        // (delta, delta x); then (y, -)
+template <typename T, int N, int TW, int STEPS, bool MAPS>
+__global__ __launch_bounds__((SsmTile<N, FWD_CH, TW, STEPS>::THR), (STEPS == 16 ? 3 : 4)) void ssm_fwd(SsmArgs a) {
+  typedef SsmTile<N, FWD_CH, TW, STEPS> L;
+  constexpr int V = L::VEC, BV = L::BV, CH = FWD_CH;
+  __shared__ __align__(16) float2 step[L::TS][CH];        // (delta, delta x); then (y, -)
   __shared__ __align__(16) float sB[L::TS][N], sC[L::TS][N];
-  __shared__ __align__(16) float mapP[L::TW][SSM_CH][N], mapH[L::TW][SSM_CH][N];
-  __shared__ float sumd[L::TW][SSM_CH];
-  const int groups = (a.D + SSM_CH - 1) / SSM_CH;
-  const int slots = slots_of(a.seq, a.seg), id = dealt(groups * slots);
-  if (id >= groups * slots) return;
-  const Segment g = find_segment(a.seq, a.seg, id / groups);
-  const int c0 = (id % groups) * SSM_CH;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ __align__(16) float mapP[TW][CH][N], mapH[TW][CH][N];
+  __shared__ float sumd[TW][CH];
+  const int groups = (a.D + CH - 1) / CH;
+  const SsmPlace place = ssm_place(groups, slots_of(a.seq, a.seg));
+  if (!place.any) return;
+  const Segment g = find_segment(a.seq, a.seg, place.slot);
+  const int c0 = place.group * CH;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tw = wave / L::WIDE, ch = (wave % L::WIDE) * L::CW + lane / L::P, p4 = (lane % L::P) * 4;
   const int c = c0 + ch;                      // this lane's channel
   const bool on = c < a.D;
@@ -56,9 +59,9 @@ template <typename T, int N, bool MAPS> __global__ __launch_bounds__(SSM_THR, 4)
     }
   }
   // the part of a tile that this thread loads, and of y that it stores
-  const int ls = tid / (SSM_CH / V), lc = (tid % (SSM_CH / V)) * V, lcc = c0 + lc;
+  const int ls = tid / (CH / V), lc = (tid % (CH / V)) * V, lcc = c0 + lc;
   const bool lon = lcc < a.D;
-  const int bs = tid / (N / 2), bn = (tid % (N / 2)) * 2;
+  const int bs = tid / (N / BV), bn = (tid % (N / BV)) * BV;
   float bias[V] = {}, skip[V] = {};
   if (lon) {
 #pragma unroll
@@ -67,44 +70,43 @@ template <typename T, int N, bool MAPS> __global__ __launch_bounds__(SSM_THR, 4)
       if (a.skip) skip[j] = a.skip[lcc + j];
     }
   }
-  const int chunk0 = MAPS ? 0 : first_slot(a.seq, g.n, L::TS);
-  Loaded<T, N> in;
+  const int chunk0 = MAPS ? 0 : first_slot(a.seq, g.n, SSM_CHUNK<N>);
+  Few<T, V> nx, nd, nz;                       // the next tile's entries of this thread
+  Few<T, BV> nB, nC;
   auto load = [&](int t) {
-    const int q = min(t + ls, g.t1 - 1), qb = min(t + bs, g.t1 - 1), cc = lon ? lcc : 0;
-    load_few<V>(static_cast<const T *>(a.x) + (int64_t)q * a.ldx + cc, in.x);
-    load_few<V>(static_cast<const T *>(a.dt) + (int64_t)q * a.lddt + cc, in.dt);
-    if (!MAPS && a.z) load_few<V>(static_cast<const T *>(a.z) + (int64_t)q * a.ldz + cc, in.z);
-    load_few<2>(static_cast<const T *>(a.B) + (int64_t)qb * a.ldB + bn, in.B);
-    if (!MAPS) load_few<2>(static_cast<const T *>(a.C) + (int64_t)qb * a.ldC + bn, in.C);
+    const int q = min(ls, g.t1 - 1 - t), qb = min(bs, g.t1 - 1 - t), cc = lon ? lcc : 0;
+    fetch(entry<T>(a.x, a.ldx, t, q, cc), nx);
+    fetch(entry<T>(a.dt, a.lddt, t, q, cc), nd);
+    if (!MAPS && a.z) fetch(entry<T>(a.z, a.ldz, t, q, cc), nz);
+    fetch(entry<T>(a.B, a.ldB, t, qb, bn), nB);
+    if (!MAPS) fetch(entry<T>(a.C, a.ldC, t, qb, bn), nC);
   };
   float total = 0.f;                          // MAPS: the sum of delta of this lane's channel
   if (g.any) load(g.t0);
   for (int t = g.t0; t < g.t1; t += L::TS) {
-    float x[V], z[V];
+    const Few<T, V> x = nx, z = nz;
+    const bool valid = lon && t + ls < g.t1;      // steps behind the end change nothing: delta = 0
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      x[j] = in.x[j];
-      z[j] = in.z[j];
-      float d = in.dt[j] + bias[j];
+      float d = (float)nd.v[j] + bias[j];
       if (a.softplus) d = softplus(d);
-      const bool valid = lon && t + ls < g.t1;      // steps behind the end change nothing: delta = 0
-      step[ls][lc + j] = valid ? float2{d, d * x[j]} : float2{0.f, 0.f};
+      step[ls][lc + j] = valid ? float2{d, d * (float)x.v[j]} : float2{0.f, 0.f};
     }
-    *reinterpret_cast<float2 *>(&sB[bs][bn]) = float2{in.B[0], in.B[1]};
-    if constexpr (!MAPS) *reinterpret_cast<float2 *>(&sC[bs][bn]) = float2{in.C[0], in.C[1]};
+#pragma unroll
+    for (int j = 0; j < BV; ++j) {
+      sB[bs][bn + j] = (float)nB.v[j];
+      if constexpr (!MAPS) sC[bs][bn + j] = (float)nC.v[j];
+    }
     __syncthreads();
     if (t + L::TS < g.t1) load(t + L::TS);
-    if constexpr (!MAPS) {
-      if (a.states && tw == 0 && on)
-        *reinterpret_cast<f4 *>(a.states + ((size_t)(chunk0 + (t - g.s) / L::TS) * a.D + c) * N + p4) = h;
-    }
-    const int s0 = tw * SSM_STEPS;
-    f4 dec[SSM_STEPS];
-    if constexpr (L::TW > 1 || MAPS) {
-      f4 H{0.f, 0.f, 0.f, 0.f};
+    const int s0 = tw * STEPS;
+    f4 dec[STEPS];
+    f4 run = h;                                // the state before this wave's steps
+    if constexpr (TW > 1 || MAPS) {
+      f4 H{0.f, 0.f, 0.f, 0.f}, Pm;
       float sd = 0.f;
 #pragma unroll
-      for (int s = 0; s < SSM_STEPS; ++s) {
+      for (int s = 0; s < STEPS; ++s) {
         const float2 du = step[s0 + s][ch];
         const f4 b = *reinterpret_cast<const f4 *>(&sB[s0 + s][p4]);
         sd += du.x;
@@ -114,56 +116,52 @@ template <typename T, int N, bool MAPS> __global__ __launch_bounds__(SSM_THR, 4)
           H[j] = fmaf(dec[s][j], H[j], du.y * b[j]);
         }
       }
-      f4 Pm;
 #pragma unroll
       for (int j = 0; j < 4; ++j) Pm[j] = __builtin_amdgcn_exp2f(sd * A2[j]);
       *reinterpret_cast<f4 *>(&mapP[tw][ch][p4]) = Pm;
       *reinterpret_cast<f4 *>(&mapH[tw][ch][p4]) = H;
       if (MAPS && p4 == 0) sumd[tw][ch] = sd;
       __syncthreads();
-    }
-    // the state before this wave's steps, and before the next tile
-    f4 run = h;
-    if constexpr (L::TW > 1 || MAPS) {
       f4 mine = h;
 #pragma unroll
-      for (int w = 0; w < L::TW; ++w) {
-        if (w == tw) mine = run;
-        const f4 Pm = *reinterpret_cast<const f4 *>(&mapP[w][ch][p4]), H = *reinterpret_cast<const f4 *>(&mapH[w][ch][p4]);
+      for (int w = 0; w < TW; ++w) {
+        if (w == tw) mine = h;
+        const f4 Pw = *reinterpret_cast<const f4 *>(&mapP[w][ch][p4]), Hw = *reinterpret_cast<const f4 *>(&mapH[w][ch][p4]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) run[j] = fmaf(Pm[j], run[j], H[j]);
+        for (int j = 0; j < 4; ++j) h[j] = fmaf(Pw[j], h[j], Hw[j]);
         if (MAPS) total += sumd[w][ch];
       }
-      h = run;
-      run = mine;
+      run = mine;                              // and h is the one before the next tile
     }
     if constexpr (!MAPS) {
+      if (a.states && on && (t - g.s + s0) % SSM_CHUNK<N> == 0 && t + s0 < g.t1)
+        *reinterpret_cast<f4 *>(a.states + ((size_t)(chunk0 + (t - g.s + s0) / SSM_CHUNK<N>) * a.D + c) * N + p4) = run;
 #pragma unroll
-      for (int s = 0; s < SSM_STEPS; ++s) {
+      for (int s = 0; s < STEPS; ++s) {
         const float2 du = step[s0 + s][ch];
         const f4 b = *reinterpret_cast<const f4 *>(&sB[s0 + s][p4]), cv = *reinterpret_cast<const f4 *>(&sC[s0 + s][p4]);
         float y = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float e = L::TW > 1 ? dec[s][j] : __builtin_amdgcn_exp2f(du.x * A2[j]);
+          const float e = TW > 1 ? dec[s][j] : __builtin_amdgcn_exp2f(du.x * A2[j]);
           run[j] = fmaf(e, run[j], du.y * b[j]);
           y = fmaf(cv[j], run[j], y);
         }
         y = lane_sum<L::P>(y);
         if (p4 == 0) step[s0 + s][ch].x = y;
       }
-      if constexpr (L::TW == 1) h = run;
+      if constexpr (TW == 1) h = run;
     }
     __syncthreads();
     if constexpr (!MAPS) {
-      if (lon && t + ls < g.t1) {
+      if (valid) {
         float y[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          y[j] = fmaf(skip[j], x[j], step[ls][lc + j].x);
-          if (a.z) y[j] *= z[j] * sigmoid(z[j]);
+          y[j] = fmaf(skip[j], (float)x.v[j], step[ls][lc + j].x);
+          if (a.z) y[j] *= (float)z.v[j] * sigmoid((float)z.v[j]);
         }
-        store_few<V>(static_cast<T *>(a.y) + (size_t)(t + ls) * a.D + lcc, y);
+        store_few<V>(entry<T>(a.y, a.D, t, ls, lcc), y);
       }
     }
   }
@@ -236,7 +234,7 @@ size_t align16(size_t n) { return (n + 15) / 16 * 16; }
 // Tokens of a segment: as many segments as give every compute unit two workgroups, where whole
 // sequences do not; a whole number of chunks.
 int ssm_segment(const SeqMap &q, int D) {
-  const int64_t groups = (D + SSM_CH - 1) / SSM_CH, want = 512;
+  const int64_t groups = (D + FWD_CH - 1) / FWD_CH, want = SSM_WANT;
   int64_t len;
   if (q.cu) {
     len = ((int64_t)q.T * groups + want - 1) / want;
@@ -254,10 +252,10 @@ bool ssm_segmented(const SeqMap &q, int seg) { return q.T > seg; }
 int ssm_chunk(int N) { return 1024 / N; }
 
 bool ssm_fits(SeqMap seq, int D) {
-  const int64_t groups = (D + SSM_CH - 1) / SSM_CH;
+  const int64_t groups = (D + FWD_CH - 1) / FWD_CH;
   const int64_t seg = ssm_segment(seq, D);
   const int64_t slots = seq.cu ? seq.T / seg + seq.n : (int64_t)seq.n * ((seq.T + seg - 1) / seg);
-  return slots * groups <= INT32_MAX - 64 && grid_fits(slots * groups + 8, SSM_THR);
+  return slots <= INT32_MAX - 8 && grid_fits(slots * (groups + 7) / 8 * 8 + 8, 1024);
 }
 
 size_t ssm_fwd_workspace(SeqMap seq, int D, int N) {
@@ -267,16 +265,16 @@ size_t ssm_fwd_workspace(SeqMap seq, int D, int N) {
   return 2 * align16(slots * D * N * sizeof(float)) + align16(slots * D * sizeof(float));
 }
 
-template <typename T, int N> static hipError_t fwd(SsmArgs a, void *ws, hipStream_t s) {
-  a.seg = ssm_segment(a.seq, a.D);
-  const int64_t groups = (a.D + SSM_CH - 1) / SSM_CH;
-  const unsigned grid = dealt_grid(groups * slots_of(a.seq, a.seg));
+template <typename T, int N, int TW, int STEPS> static hipError_t fwd(SsmArgs a, void *ws, hipStream_t s) {
+  constexpr int THR = SsmTile<N, FWD_CH, TW, STEPS>::THR;
+  const int groups = (a.D + FWD_CH - 1) / FWD_CH;
+  const unsigned grid = (unsigned)ssm_grid(groups, slots_of(a.seq, a.seg));
   if (ssm_segmented(a.seq, a.seg)) {
     const size_t states = align16((size_t)(slots_of(a.seq, a.seg) + 1) * a.D * N * sizeof(float));
     a.seg_map = static_cast<float *>(ws);
     a.seg_state = reinterpret_cast<float *>(static_cast<char *>(ws) + states);
     a.seg_sum = reinterpret_cast<float *>(static_cast<char *>(ws) + 2 * states);
-    hipLaunchKernelGGL((ssm_fwd<T, N, true>), dim3(grid), dim3(SSM_THR), 0, s, a);
+    hipLaunchKernelGGL((ssm_fwd<T, N, TW, STEPS, true>), dim3(grid), dim3(THR), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int rows = a.seq.n < 65535 ? a.seq.n : 65535;
@@ -284,8 +282,15 @@ template <typename T, int N> static hipError_t fwd(SsmArgs a, void *ws, hipStrea
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((ssm_fwd<T, N, false>), dim3(grid), dim3(SSM_THR), 0, s, a);
+  hipLaunchKernelGGL((ssm_fwd<T, N, TW, STEPS, false>), dim3(grid), dim3(THR), 0, s, a);
   return hipGetLastError();
+}
+
+template <typename T, int N> static hipError_t fwd(SsmArgs a, void *ws, hipStream_t s) {
+  a.seg = ssm_segment(a.seq, a.D);
+  const int64_t groups = (a.D + FWD_CH - 1) / FWD_CH;
+  if (groups * slots_of(a.seq, a.seg) < SSM_FEW) return fwd<T, N, 128 / N, (N == 64 ? 16 : 8)>(a, ws, s);
+  return fwd<T, N, 64 / N, 16>(a, ws, s);
 }
 
 hipError_t launch_ssm_fwd(bool bf16, int N, SsmArgs a, void *ws, hipStream_t s) {

@@ -46,118 +46,132 @@ template <int P> __device__ __forceinline__ void channel_sums(const f4 &b, const
   if constexpr (P <= 8) { u += dpp_mov<0x128>(u); v += dpp_mov<0x128>(v); }    // row_ror:8
 }
 
+constexpr int BWD_CH = 32;
+template <int N> using BwdTile = SsmTile<N, BWD_CH, 64 / N, 16>;
+
 // MAPS: only the segment's map (r at its start from zero behind its end, sum of delta) is formed.
-template <typename T, int N, bool MAPS> __global__ __launch_bounds__(SSM_THR, MAPS ? 4 : 2) void ssm_bwd(SsmArgs a) {
-  typedef SsmTile<N> L;
-  constexpr int V = L::VEC;
-  __shared__ __align__(16) float2 step[L::TS][SSM_CH];       // (delta, delta x); then (sum g B, sum r h A)
-  __shared__ float sgy[L::TS][SSM_CH];                       // gy; then sum C h
-  __shared__ __align__(16) float sB[L::TS][N], sC[L::TS][N];
-  __shared__ __align__(16) float mapP[L::TW][SSM_CH][N], mapG[L::TW][SSM_CH][N], mapH[MAPS ? 1 : L::TW][SSM_CH][N];
+template <typename T, int N, bool MAPS> __global__ __launch_bounds__(BwdTile<N>::THR, MAPS ? 4 : 2) void ssm_bwd(SsmArgs a) {
+  typedef BwdTile<N> L;
+  static_assert(L::TS == SSM_CHUNK<N>, "a tile starts from a state that the forward kept");
+  constexpr int V = L::VEC, BV = L::BV, CH = BWD_CH;
+  __shared__ __align__(16) f4 step[L::TS][CH];               // (delta, delta x, gy, -); then (sum g B, sum r h A log2 e, sum C h, -)
+  __shared__ __align__(16) float sBC[L::TS][2][N];
+  __shared__ __align__(16) float map[L::TW][3][CH][N];       // P, G and H of the waves' steps
   __shared__ __align__(16) float red[MAPS ? 1 : L::WIDE][L::TS][2 * N];
-  __shared__ float sumd[L::TW][SSM_CH];
-  const int groups = (a.D + SSM_CH - 1) / SSM_CH;
-  const int slots = slots_of(a.seq, a.seg), id = dealt(groups * slots);
-  if (id >= groups * slots) return;
-  const Segment g = find_segment(a.seq, a.seg, id / groups);
-  const int group = id % groups, c0 = group * SSM_CH;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int tw = wave / L::WIDE, wide = wave % L::WIDE, ch = wide * L::CW + lane / L::P, p4 = (lane % L::P) * 4;
+  __shared__ float sumd[L::TW][CH], sbias[CH], sskip[CH];
+  const int groups = (a.D + CH - 1) / CH;
+  const SsmPlace place = ssm_place(groups, slots_of(a.seq, a.seg));
+  if (!place.any) return;
+  const Segment g = find_segment(a.seq, a.seg, place.slot);
+  const int group = place.group, c0 = group * CH;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tw = wave / L::WIDE, wide = wave % L::WIDE, p = lane % L::P, p4 = p * 4, ch = wide * L::CW + lane / L::P;
   const int c = c0 + ch;
   const bool on = c < a.D;
-  const int ls = tid / (SSM_CH / V), lc = (tid % (SSM_CH / V)) * V, lcc = c0 + lc;
+  const int ls = tid / (CH / V), lc = (tid % (CH / V)) * V, lcc = c0 + lc;
   const bool lon = lcc < a.D;
   const bool empty = g.s == g.e && g.slot == first_slot(a.seq, g.n, a.seg);
   const bool first = g.t0 == g.s, lastseg = g.t1 == g.e;
   if constexpr (MAPS) {
     if (!g.any || first) return;        // nobody starts from its end
   }
-  f4 A{0.f, 0.f, 0.f, 0.f}, r{0.f, 0.f, 0.f, 0.f};
+  f4 A2{0.f, 0.f, 0.f, 0.f}, r{0.f, 0.f, 0.f, 0.f};
   if (on) {
-    A = *reinterpret_cast<const f4 *>(a.A + (size_t)c * N + p4);
+    A2 = *reinterpret_cast<const f4 *>(a.A + (size_t)c * N + p4) * SSM_LOG2E;
     if constexpr (!MAPS) {
       if (g.any && !lastseg) r = *reinterpret_cast<const f4 *>(a.seg_state + ((size_t)g.slot * a.D + c) * N + p4);
       else if ((g.any || empty) && a.d_final) r = *reinterpret_cast<const f4 *>(a.d_final + ((size_t)g.n * a.D + c) * N + p4);
     }
   }
-  const f4 A2 = A * SSM_LOG2E;
-  const int bs = tid / (N / 2), bn = (tid % (N / 2)) * 2;
-  float bias[V] = {}, skip[V] = {};
-  if (lon) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      if (a.bias) bias[j] = a.bias[lcc + j];
-      if (a.skip) skip[j] = a.skip[lcc + j];
-    }
+  const int bs = tid / (N / BV), bn = (tid % (N / BV)) * BV;
+  if (tid < CH) {
+    sbias[tid] = a.bias && c0 + tid < a.D ? a.bias[c0 + tid] : 0.f;
+    sskip[tid] = a.skip && c0 + tid < a.D ? a.skip[c0 + tid] : 0.f;
   }
+  __syncthreads();
   const int chunk0 = MAPS ? 0 : first_slot(a.seq, g.n, L::TS);
   f4 dA{0.f, 0.f, 0.f, 0.f};
   float dD[V] = {}, dbias[V] = {}, total = 0.f;
   const int64_t tokens = a.seq.tokens();
-  for (int t = g.any ? g.t0 + (g.t1 - g.t0 - 1) / L::TS * L::TS : g.t0 - 1; t >= g.t0; t -= L::TS) {
-    const int q = min(t + ls, g.t1 - 1), qb = min(t + bs, g.t1 - 1), cc = lon ? lcc : 0;
-    const bool valid = lon && t + ls < g.t1;     // steps behind the end change nothing: delta = gy = 0
-    float x[V], d[V], z[V] = {}, dy[V], gy[V], slope[V], b2[2], c2[2];
-    load_few<V>(static_cast<const T *>(a.x) + (int64_t)q * a.ldx + cc, x);
-    load_few<V>(static_cast<const T *>(a.dt) + (int64_t)q * a.lddt + cc, d);
-    if (a.z) load_few<V>(static_cast<const T *>(a.z) + (int64_t)q * a.ldz + cc, z);
-    load_few<V>(static_cast<const T *>(a.dy) + (size_t)q * a.D + cc, dy);
-    load_few<2>(static_cast<const T *>(a.B) + (int64_t)qb * a.ldB + bn, b2);
-    load_few<2>(static_cast<const T *>(a.C) + (int64_t)qb * a.ldC + bn, c2);
-    f4 hv{0.f, 0.f, 0.f, 0.f};                   // the tile's first state, then this wave's
+  Few<T, V> nx, nd, nz, ng;                   // the next tile's entries of this thread
+  Few<T, BV> nB, nC;
+  f4 nh{0.f, 0.f, 0.f, 0.f};                  // and its first state
+  auto load = [&](int t) {
+    const int q = min(ls, g.t1 - 1 - t), qb = min(bs, g.t1 - 1 - t), cc = lon ? lcc : 0;
+    fetch(entry<T>(a.x, a.ldx, t, q, cc), nx);
+    fetch(entry<T>(a.dt, a.lddt, t, q, cc), nd);
+    if (a.z) fetch(entry<T>(a.z, a.ldz, t, q, cc), nz);
+    fetch(entry<T>(a.dy, a.D, t, q, cc), ng);
+    if (!MAPS) fetch(entry<T>(a.B, a.ldB, t, qb, bn), nB);
+    fetch(entry<T>(a.C, a.ldC, t, qb, bn), nC);
     if constexpr (!MAPS) {
-      if (on) hv = *reinterpret_cast<const f4 *>(a.states + ((size_t)(chunk0 + (t - g.s) / L::TS) * a.D + c) * N + p4);
+      if (on) nh = *reinterpret_cast<const f4 *>(a.states + ((size_t)(chunk0 + (t - g.s) / L::TS) * a.D + c) * N + p4);
     }
+  };
+  const int last = g.any ? g.t0 + (g.t1 - g.t0 - 1) / L::TS * L::TS : g.t0 - 1;     // the last tile
+  if (last >= g.t0) load(last);
+  for (int t = last; t >= g.t0; t -= L::TS) {
+    const bool valid = lon && t + ls < g.t1;     // steps behind the end change nothing: delta = gy = 0
+    const Few<T, V> x = nx;
+    float d[V], slope[V], gy[V], gz[V];          // gz: dz but for its factor sum C h + D x
+    f4 hv = nh;                                  // the tile's first state, then this wave's
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      d[j] += bias[j];
+      d[j] = (float)nd.v[j] + sbias[lc + j];
       slope[j] = 1.f;
       if (a.softplus) { slope[j] = sigmoid(d[j]); d[j] = softplus(d[j]); }
-      gy[j] = a.z ? dy[j] * (z[j] * sigmoid(z[j])) : dy[j];
-      step[ls][lc + j] = valid ? float2{d[j], d[j] * x[j]} : float2{0.f, 0.f};
-      sgy[ls][lc + j] = valid ? gy[j] : 0.f;
-    }
-    *reinterpret_cast<float2 *>(&sB[bs][bn]) = float2{b2[0], b2[1]};
-    *reinterpret_cast<float2 *>(&sC[bs][bn]) = float2{c2[0], c2[1]};
-    __syncthreads();
-    const int s0 = tw * SSM_STEPS;
-    f4 dec[SSM_STEPS];
-    float sd = 0.f;
-    f4 H{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int s = 0; s < SSM_STEPS; ++s) {
-      const float2 du = step[s0 + s][ch];
-      sd += du.x;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) dec[s][j] = __builtin_amdgcn_exp2f(du.x * A2[j]);
-      if constexpr (L::TW > 1 && !MAPS) {
-        const f4 b = *reinterpret_cast<const f4 *>(&sB[s0 + s][p4]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) H[j] = fmaf(dec[s][j], H[j], du.y * b[j]);
+      gy[j] = (float)ng.v[j];
+      if (a.z) {
+        const float z = (float)nz.v[j], sg = sigmoid(z);
+        gz[j] = gy[j] * sg * fmaf(z, 1.f - sg, 1.f);
+        gy[j] *= z * sg;
       }
+      step[ls][lc + j] = valid ? f4{d[j], d[j] * (float)x.v[j], gy[j], 0.f} : f4{0.f, 0.f, 0.f, 0.f};
     }
+#pragma unroll
+    for (int j = 0; j < BV; ++j) {
+      if (!MAPS) sBC[bs][0][bn + j] = (float)nB.v[j];
+      sBC[bs][1][bn + j] = (float)nC.v[j];
+    }
+    __syncthreads();
+    if (t > g.t0) load(t - L::TS);
+    const int s0 = tw * L::STEPS;
+    f4 dec[L::STEPS];
     f4 mine = r;                                 // r behind this wave's steps
     if constexpr (L::TW > 1 || MAPS) {
-      f4 G{0.f, 0.f, 0.f, 0.f}, Pm;
+      float sd = 0.f;
+      f4 H{0.f, 0.f, 0.f, 0.f}, G{0.f, 0.f, 0.f, 0.f}, Pm;
 #pragma unroll
-      for (int s = SSM_STEPS - 1; s >= 0; --s) {
-        const float gv = sgy[s0 + s][ch];
-        const f4 cv = *reinterpret_cast<const f4 *>(&sC[s0 + s][p4]);
+      for (int s = 0; s < L::STEPS; ++s) {
+        const f4 du = step[s0 + s][ch];
+        sd += du[0];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dec[s][j] = __builtin_amdgcn_exp2f(du[0] * A2[j]);
+        if constexpr (!MAPS) {
+          const f4 b = *reinterpret_cast<const f4 *>(&sBC[s0 + s][0][p4]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) H[j] = fmaf(dec[s][j], H[j], du[1] * b[j]);
+        }
+      }
+#pragma unroll
+      for (int s = L::STEPS - 1; s >= 0; --s) {
+        const float gv = step[s0 + s][ch][2];
+        const f4 cv = *reinterpret_cast<const f4 *>(&sBC[s0 + s][1][p4]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) G[j] = dec[s][j] * fmaf(gv, cv[j], G[j]);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) Pm[j] = __builtin_amdgcn_exp2f(sd * A2[j]);
-      *reinterpret_cast<f4 *>(&mapP[tw][ch][p4]) = Pm;
-      *reinterpret_cast<f4 *>(&mapG[tw][ch][p4]) = G;
-      if constexpr (!MAPS) *reinterpret_cast<f4 *>(&mapH[tw][ch][p4]) = H;
+      *reinterpret_cast<f4 *>(&map[tw][0][ch][p4]) = Pm;
+      *reinterpret_cast<f4 *>(&map[tw][1][ch][p4]) = G;
+      if constexpr (!MAPS) *reinterpret_cast<f4 *>(&map[tw][2][ch][p4]) = H;
       if (MAPS && p4 == 0) sumd[tw][ch] = sd;
       __syncthreads();
       f4 run = r;
 #pragma unroll
       for (int w = L::TW - 1; w >= 0; --w) {
         if (w == tw) mine = run;
-        const f4 Pw = *reinterpret_cast<const f4 *>(&mapP[w][ch][p4]), Gw = *reinterpret_cast<const f4 *>(&mapG[w][ch][p4]);
+        const f4 Pw = *reinterpret_cast<const f4 *>(&map[w][0][ch][p4]), Gw = *reinterpret_cast<const f4 *>(&map[w][1][ch][p4]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) run[j] = fmaf(Pw[j], run[j], Gw[j]);
         if (MAPS) total += sumd[w][ch];
@@ -167,55 +181,67 @@ template <typename T, int N, bool MAPS> __global__ __launch_bounds__(SSM_THR, MA
 #pragma unroll
         for (int w = 0; w < L::TW - 1; ++w) {
           if (w < tw) {
-            const f4 Pw = *reinterpret_cast<const f4 *>(&mapP[w][ch][p4]), Hw = *reinterpret_cast<const f4 *>(&mapH[w][ch][p4]);
+            const f4 Pw = *reinterpret_cast<const f4 *>(&map[w][0][ch][p4]), Hw = *reinterpret_cast<const f4 *>(&map[w][2][ch][p4]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) hv[j] = fmaf(Pw[j], hv[j], Hw[j]);
           }
         }
       }
+    } else {
+#pragma unroll
+      for (int s = 0; s < L::STEPS; ++s) {
+        const float delta = step[s0 + s][ch][0];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dec[s][j] = __builtin_amdgcn_exp2f(delta * A2[j]);
+      }
     }
     if constexpr (!MAPS) {
-      f4 hp[SSM_STEPS + 1];                      // the state before every step
+      f4 hp[L::STEPS + 1];                       // the state before every step
       hp[0] = hv;
 #pragma unroll
-      for (int s = 0; s < SSM_STEPS; ++s) {
-        const float2 du = step[s0 + s][ch];
-        const f4 b = *reinterpret_cast<const f4 *>(&sB[s0 + s][p4]);
+      for (int s = 0; s < L::STEPS; ++s) {
+        const float du = step[s0 + s][ch][1];
+        const f4 b = *reinterpret_cast<const f4 *>(&sBC[s0 + s][0][p4]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) hp[s + 1][j] = fmaf(dec[s][j], hp[s][j], du.y * b[j]);
+        for (int j = 0; j < 4; ++j) hp[s + 1][j] = fmaf(dec[s][j], hp[s][j], du * b[j]);
       }
+      // what comes now reads the tile again, rather than keep it in registers
+      asm volatile("" ::: "memory");
+      // the channels' 4 (of N = 32, 64: first 4) lanes store one sum each, and a row's first lanes of two channels those of
+      // B and of C (the others the same values at the same places)
+      float *out = reinterpret_cast<float *>(&step[s0][ch]) + (p & 3);
+      const bool second = L::P < 16 && (lane / L::P) & 1;
+      float *outr = &red[wide][s0][p4 + (lane >> 4) + (second ? N : 0)];
 #pragma unroll
-      for (int s = SSM_STEPS - 1; s >= 0; --s) {
-        const float2 du = step[s0 + s][ch];
-        const float gv = sgy[s0 + s][ch];
-        const f4 b = *reinterpret_cast<const f4 *>(&sB[s0 + s][p4]), cv = *reinterpret_cast<const f4 *>(&sC[s0 + s][p4]);
+      for (int s = L::STEPS - 1; s >= 0; --s) {
+        const f4 du = step[s0 + s][ch];
+        const f4 b = *reinterpret_cast<const f4 *>(&sBC[s0 + s][0][p4]), cv = *reinterpret_cast<const f4 *>(&sBC[s0 + s][1][p4]);
         f4 gb, gc;
         float sum_b = 0.f, sum_a = 0.f, read = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float gj = fmaf(gv, cv[j], mine[j]);
-          gb[j] = gj * du.y;
-          gc[j] = gv * hp[s + 1][j];
+          const float gj = fmaf(du[2], cv[j], mine[j]);
+          gb[j] = gj * du[1];
+          gc[j] = du[2] * hp[s + 1][j];
           sum_b = fmaf(gj, b[j], sum_b);
           read = fmaf(cv[j], hp[s + 1][j], read);
           mine[j] = dec[s][j] * gj;
           const float w = mine[j] * hp[s][j];
-          sum_a = fmaf(w, A[j], sum_a);
-          dA[j] = fmaf(w, du.x, dA[j]);
+          sum_a = fmaf(w, A2[j], sum_a);
+          dA[j] = fmaf(w, du[0], dA[j]);
         }
         sum_b = lane_sum<L::P>(sum_b);
         sum_a = lane_sum<L::P>(sum_a);
         read = lane_sum<L::P>(read);
         float u, v;
         channel_sums<L::P>(gb, gc, u, v);
-        if ((lane & 15) < L::P) {
-          red[wide][s0 + s][p4 + (lane >> 4)] = u;
-          red[wide][s0 + s][N + p4 + (lane >> 4)] = v;
+        if constexpr (L::P < 16) {
+          outr[s * 2 * N] = second ? v : u;
+        } else {
+          outr[s * 2 * N] = u;
+          outr[s * 2 * N + N] = v;
         }
-        if (p4 == 0) {
-          step[s0 + s][ch] = float2{sum_b, sum_a};
-          sgy[s0 + s][ch] = read;
-        }
+        out[s * CH * 4] = (p & 3) == 0 ? sum_b : (p & 3) == 1 ? sum_a : read;
       }
       if constexpr (L::TW == 1) r = mine;
     }
@@ -225,27 +251,26 @@ template <typename T, int N, bool MAPS> __global__ __launch_bounds__(SSM_THR, MA
         float dx[V], ddt[V], dz[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const float2 s2 = step[ls][lc + j];
-          dx[j] = fmaf(s2.x, d[j], skip[j] * gy[j]);
-          ddt[j] = fmaf(s2.x, x[j], s2.y) * slope[j];
-          dD[j] = fmaf(gy[j], x[j], dD[j]);
+          const f4 sum = step[ls][lc + j];
+          const float xv = (float)x.v[j], sk = sskip[lc + j];
+          dx[j] = fmaf(sum[0], d[j], sk * gy[j]);
+          ddt[j] = fmaf(sum[0], xv, sum[1] * SSM_LN2) * slope[j];
+          dD[j] = fmaf(gy[j], xv, dD[j]);
           dbias[j] += ddt[j];
-          if (a.z) {
-            const float sg = sigmoid(z[j]);
-            dz[j] = dy[j] * fmaf(skip[j], x[j], sgy[ls][lc + j]) * (sg * fmaf(z[j], 1.f - sg, 1.f));
-          }
+          if (a.z) dz[j] = gz[j] * fmaf(sk, xv, sum[2]);
         }
-        store_few<V>(static_cast<T *>(a.dx) + (int64_t)q * a.lddx + lcc, dx);
-        store_few<V>(static_cast<T *>(a.ddt) + (int64_t)q * a.ldddt + lcc, ddt);
-        if (a.z) store_few<V>(static_cast<T *>(a.dz) + (int64_t)q * a.lddz + lcc, dz);
+        store_few<V>(entry<T>(a.dx, a.lddx, t, ls, lcc), dx);
+        store_few<V>(entry<T>(a.ddt, a.ldddt, t, ls, lcc), ddt);
+        if (a.z) store_few<V>(entry<T>(a.dz, a.lddz, t, ls, lcc), dz);
       }
       float *out = a.part_bc + ((size_t)group * tokens + t) * (2 * N);
-      for (int i = tid; i < L::TS * 2 * N; i += SSM_THR) {
-        if (t + i / (2 * N) >= g.t1) continue;
-        float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < L::WIDE; ++w) v += (&red[w][0][0])[i];
-        out[i] = v;
+      for (int k = 0; k < L::TS * 2 * N / 4 / L::THR; ++k) {
+        const int i = (k * L::THR + tid) * 4;
+        f4 v = *reinterpret_cast<const f4 *>(&red[0][0][0] + i);
+#pragma unroll
+        for (int w = 1; w < L::WIDE; ++w) v += *reinterpret_cast<const f4 *>(&red[w][0][0] + i);
+        if (t + i / (2 * N) < g.t1) *reinterpret_cast<f4 *>(out + i) = v;
       }
     }
   }
@@ -259,31 +284,24 @@ template <typename T, int N, bool MAPS> __global__ __launch_bounds__(SSM_THR, MA
       *reinterpret_cast<f4 *>(a.d_init + ((size_t)g.n * a.D + c) * N + p4) = r;
     // the segment's sums for A, D and the bias, over its waves (steps) in order; zeros without any
     __syncthreads();
-    *reinterpret_cast<f4 *>(&mapH[tw][ch][p4]) = dA;
-    float(*sums)[SSM_CH] = &sgy[0];               // dD over the steps, then dbias
-    constexpr int ROWS = L::TS;
+    *reinterpret_cast<f4 *>(&map[tw][0][ch][p4]) = dA;
 #pragma unroll
-    for (int j = 0; j < V; ++j) sums[ls][lc + j] = dD[j];
+    for (int j = 0; j < V; ++j) step[ls][lc + j] = f4{dD[j], dbias[j], 0.f, 0.f};
     __syncthreads();
     if (on && tw == 0) {
 #pragma unroll
-      for (int w = 1; w < L::TW; ++w) dA += *reinterpret_cast<const f4 *>(&mapH[w][ch][p4]);
+      for (int w = 1; w < L::TW; ++w) dA += *reinterpret_cast<const f4 *>(&map[w][0][ch][p4]);
       *reinterpret_cast<f4 *>(a.part_A + ((size_t)g.slot * a.D + c) * N + p4) = dA;
     }
-    float *out = a.part_D + (size_t)g.slot * 2 * a.D;
-    if (tid < SSM_CH && c0 + tid < a.D) {
-      float v = 0.f;
-      for (int i = 0; i < ROWS; ++i) v += sums[i][tid];
-      out[c0 + tid] = v;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < V; ++j) sums[ls][lc + j] = dbias[j];
-    __syncthreads();
-    if (tid < SSM_CH && c0 + tid < a.D) {
-      float v = 0.f;
-      for (int i = 0; i < ROWS; ++i) v += sums[i][tid];
-      out[a.D + c0 + tid] = v;
+    if (tid < CH && c0 + tid < a.D) {
+      float v = 0.f, w = 0.f;
+      for (int i = 0; i < L::TS; ++i) {
+        v += step[i][tid][0];
+        w += step[i][tid][1];
+      }
+      float *out = a.part_D + (size_t)g.slot * 2 * a.D + c0 + tid;
+      out[0] = v;
+      out[a.D] = w;
     }
   }
 }
@@ -329,7 +347,7 @@ size_t align16(size_t n) { return (n + 15) / 16 * 16; }
 struct Parts { size_t bc, A, D, map, sum, total; };
 Parts parts_of(const SeqMap &q, int D, int N) {
   const int seg = ssm_segment(q, D);
-  const size_t groups = (D + SSM_CH - 1) / SSM_CH, slots = slots_of(q, seg);
+  const size_t groups = (D + BWD_CH - 1) / BWD_CH, slots = slots_of(q, seg);
   Parts p;
   p.bc = align16(groups * q.tokens() * 2 * N * sizeof(float));
   p.A = align16(slots * D * N * sizeof(float));
@@ -355,17 +373,17 @@ template <typename T, int N> static hipError_t bwd(SsmArgs a, const SsmGrads &o,
   a.seg_state = reinterpret_cast<float *>(at += p.map);
   a.seg_sum = reinterpret_cast<float *>(at += p.map);
   a.seg = ssm_segment(a.seq, a.D);
-  const int groups = (a.D + SSM_CH - 1) / SSM_CH, slots = slots_of(a.seq, a.seg);
-  const unsigned grid = dealt_grid((int64_t)groups * slots);
+  const int groups = (a.D + BWD_CH - 1) / BWD_CH, slots = slots_of(a.seq, a.seg);
+  const unsigned grid = (unsigned)ssm_grid(groups, slots);
   hipError_t e;
   if (ssm_segmented(a.seq, a.seg)) {
-    hipLaunchKernelGGL((ssm_bwd<T, N, true>), dim3(grid), dim3(SSM_THR), 0, s, a);
+    hipLaunchKernelGGL((ssm_bwd<T, N, true>), dim3(grid), dim3(BwdTile<N>::THR), 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const int rows = a.seq.n < 65535 ? a.seq.n : 65535;
     hipLaunchKernelGGL((ssm_chain_bwd<N>), dim3((a.D * (N / 4) + 255) / 256, rows), dim3(256), 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((ssm_bwd<T, N, false>), dim3(grid), dim3(SSM_THR), 0, s, a);
+  hipLaunchKernelGGL((ssm_bwd<T, N, false>), dim3(grid), dim3(BwdTile<N>::THR), 0, s, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const int64_t sums = (int64_t)a.seq.tokens() * 2 * N / 4;
   hipLaunchKernelGGL((ssm_sum_bc<T, N>), dim3((unsigned)((sums + 255) / 256)), dim3(256), 0, s, a, groups);

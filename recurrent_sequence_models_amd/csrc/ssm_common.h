@@ -2,24 +2,27 @@
 // slots of a call's segments and chunks.
 //
 // A wave's lane holds 4 states of one channel: P = N / 4 lanes beside each other make a channel, so a
-// sum over the states is one over 4 registers and P neighbouring lanes.  A workgroup of 8 waves
-// owns CH = 32 channels: WIDE waves lie side by side over them and TW behind each other in time, each
-// with STEPS = 16 consecutive steps of a tile of TS = 16 TW.
+// sum over the states is one over 4 registers and P neighbouring lanes.  A workgroup owns CH
+// channels: WIDE waves lie side by side over them and TW behind each other in time, each
+// with STEPS consecutive steps of a tile of TS = STEPS TW.
 #pragma once
 #include "block_kernels.h"
 #include "row_io.h"
 
 namespace falcon {
 
-constexpr int SSM_THR = 512, SSM_CH = 32, SSM_STEPS = 16;
-constexpr int SSM_ALIGN = 64;      // segments are a multiple of this long: whole tiles of every N
-constexpr float SSM_LOG2E = 1.44269504088896340736f;
+constexpr int SSM_ALIGN = 64;      // segments are a multiple of this long: whole chunks of every N
+constexpr float SSM_LOG2E = 1.44269504088896340736f, SSM_LN2 = 0.69314718055994530942f;
 
-template <int N> struct SsmTile {
-  static constexpr int P = N / 4, CW = 64 / P, WIDE = SSM_CH / CW, TW = 8 / WIDE, TS = TW * SSM_STEPS;
-  static constexpr int VEC = TS * SSM_CH / SSM_THR;     // channels of a step that a thread loads: 4, 2 or 1
-  static_assert(SSM_ALIGN % TS == 0 && TS * N == 1024, "segments are whole tiles");
+template <int N, int CH_, int TW_, int STEPS_> struct SsmTile {
+  static constexpr int CH = CH_, TW = TW_, STEPS = STEPS_, P = N / 4, CW = 64 / P, WIDE = CH / CW, THR = 64 * WIDE * TW;
+  static constexpr int TS = TW * STEPS;
+  static constexpr int VEC = TS * CH / THR;     // channels of a step that a thread loads: 4, 2 or 1
+  static constexpr int BV = TS * N / THR;       // entries of B and C that it loads
+  static_assert(WIDE * CW == CH && VEC * THR == TS * CH && BV * THR == TS * N, "a tile is dealt out evenly");
 };
+// steps between the states that the forward keeps
+template <int N> constexpr int SSM_CHUNK = 1024 / N;
 
 // V consecutive entries as floats; the address is a multiple of their size together.
 template <int V> __device__ __forceinline__ void load_few(const float *p, float (&o)[V]) {
@@ -36,6 +39,24 @@ template <int V> __device__ __forceinline__ void load_few(const __bf16 *p, float
     const unsigned v = *reinterpret_cast<const unsigned *>(p);
     o[0] = __uint_as_float(v << 16); o[1] = __uint_as_float(v & 0xffff0000u);
   } else o[0] = (float)*p;
+}
+// Entries `col` on of token t + row of an array, as scalar base plus 32 bits a lane: t is the same in every lane, and
+// token strides are at most SSM_MOST_STEP bytes.
+constexpr int64_t SSM_MOST_STEP = 1 << 24;
+template <typename T> __device__ __forceinline__ const T *entry(const void *p, int64_t ld, int t, int row, int col) {
+  const char *base = static_cast<const char *>(p) + (int64_t)t * ld * (int64_t)sizeof(T);
+  return reinterpret_cast<const T *>(base + (unsigned)(row * ((int)ld * (int)sizeof(T)) + col * (int)sizeof(T)));
+}
+template <typename T> __device__ __forceinline__ T *entry(void *p, int64_t ld, int t, int row, int col) {
+  char *base = static_cast<char *>(p) + (int64_t)t * ld * (int64_t)sizeof(T);
+  return reinterpret_cast<T *>(base + (unsigned)(row * ((int)ld * (int)sizeof(T)) + col * (int)sizeof(T)));
+}
+
+// The same as it is in memory, for what is loaded long before its use.
+template <typename T, int V> struct Few { T v[V]; };
+template <typename T, int V> __device__ __forceinline__ void fetch(const T *p, Few<T, V> &o) {
+  struct alignas(sizeof(T) * V) Whole { Few<T, V> f; };
+  o = reinterpret_cast<const Whole *>(p)->f;
 }
 template <int V> __device__ __forceinline__ void store_few(float *p, const float (&v)[V]) {
   if constexpr (V == 4) *reinterpret_cast<f4 *>(p) = f4{v[0], v[1], v[2], v[3]};
@@ -99,12 +120,26 @@ __device__ __forceinline__ Segment find_segment(const SeqMap &q, int len, int sl
   return g;
 }
 
-// The workgroup's place in a grid that is dealt to the 8 dies in turn: neighbours in (segment,
-// channels) run on one die, whose cache they share lines of x and the tiles of B and C in.
-__device__ __forceinline__ int dealt(int total) {
-  const int per = (total + 7) / 8;
-  return (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
+// The workgroup's segment and channels.  Workgroups are dealt to the 8 dies in turn.  Neighbours in channels share
+// cache lines of x and the tiles of B and C, so where there are enough, a die gets an eighth of the channels, of every
+// segment (segments differ in length).
+struct SsmPlace { int slot, group; bool any; };
+constexpr int SSM_DEALT = 64;
+__host__ __device__ inline int64_t ssm_grid(int groups, int slots) {
+  return groups >= SSM_DEALT ? (int64_t)(groups + 7) / 8 * 8 * slots : (int64_t)groups * slots;
 }
-inline unsigned dealt_grid(int64_t total) { return (unsigned)((total + 7) / 8 * 8); }
+__device__ __forceinline__ SsmPlace ssm_place(int groups, int slots) {
+  SsmPlace p;
+  if (groups >= SSM_DEALT) {
+    const int per = (groups + 7) / 8, i = (int)(blockIdx.x / 8);
+    p.group = (int)(blockIdx.x % 8) * per + i % per;
+    p.slot = i / per;
+  } else {
+    p.group = (int)(blockIdx.x % groups);
+    p.slot = (int)(blockIdx.x / groups);
+  }
+  p.any = p.group < groups && p.slot < slots;
+  return p;
+}
 
 }  // namespace falcon
