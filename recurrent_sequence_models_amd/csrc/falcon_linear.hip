@@ -54,6 +54,7 @@ template <typename T> constexpr int KM = std::is_same_v<T, e4m3> ? 64 : 16;   //
 template <typename T, int ROWS, bool COLS> struct OperandTile {
   typedef Tile<T, COLS ? ROWS : KE<T>> Ti;
   static constexpr int TR = COLS ? KE<T> : ROWS;          // rows in memory
+  static constexpr int READS = COLS ? (sizeof(T) == 4 ? 8 : 2) : sizeof(T) == 2 || std::is_same_v<T, e4m3_wide> ? 1 : 2;   // of LDS, a fragment
   static constexpr int CHUNKS = TR * Ti::CPR;             // 16 bytes each
   // the operand of a product over k block b, of rows row0 .. row0 + 31
   static __device__ __forceinline__ Frag<T> frag(const uint4 *t, int row0, int b, int lane) {
@@ -126,17 +127,18 @@ template <typename T, int ROWS, bool COLS, int THR> struct Copier {
       return (unsigned)(r * ld) + c * 16;
     }
   }
-  __device__ __forceinline__ void copy(uint4 *tile, int k0, int tid) const {
-    const int wave = tid >> 6;
+  // to: the tile's LDS address, 1024 further for each wave; the tile has all its entries of k, or
+  // (copy_last) may have fewer.
+  __device__ __forceinline__ void copy(unsigned to, int k0) const {
     const char *at = base + (COLS ? k0 * ld : k0 * (int64_t)sizeof(T));
-    const int k = K - k0;
-    if (k >= KE<T>) {
 #pragma unroll
-      for (int i = 0; i < PER; ++i) copy_to_lds(at, off[i], lds_address(tile + i * THR + wave * 64));
-    } else {
+    for (int i = 0; i < PER; ++i) copy_to_lds(at, off[i], to + i * THR * 16);
+  }
+  __device__ __forceinline__ void copy_last(unsigned to, int k0, int tid) const {
+    const char *at = base + (COLS ? k0 * ld : k0 * (int64_t)sizeof(T));
+    const int k = min(K - k0, KE<T>);
 #pragma unroll
-      for (int i = 0; i < PER; ++i) copy_to_lds(at, offset(i, tid, k), lds_address(tile + i * THR + wave * 64));
-    }
+    for (int i = 0; i < PER; ++i) copy_to_lds(at, offset(i, tid, k), to + i * THR * 16);
   }
   // Zeros where a copied tile has no entries of k.  (Rows behind the last of an operand repeat it: their
   // results are not stored.)  This thread's own pieces, after copies_done().
@@ -213,7 +215,9 @@ __global__ __launch_bounds__(64 * WL * WR) void product(LinearArgs a) {
   constexpr int THR = 64 * WL * WR, FL = TL / WL / 32, FR = TR / WR / 32;
   typedef OperandTile<T, TL, LC> OL;
   typedef OperandTile<T, TR, RC> OR;
-  __shared__ __align__(16) uint4 left[2][OL::CHUNKS], right[2][OR::CHUNKS];
+  __shared__ __align__(16) uint4 lds[2 * (OL::CHUNKS + OR::CHUNKS)];
+  uint4(*left)[OL::CHUNKS] = reinterpret_cast<uint4(*)[OL::CHUNKS]>(lds);
+  uint4(*right)[OR::CHUNKS] = reinterpret_cast<uint4(*)[OR::CHUNKS]>(lds + 2 * OL::CHUNKS);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wl = wave % WL, wr = wave / WL;
   // tiles in blocks of 8 along j, dealt to the dies in runs of neighbours
   const int ti = (a.I + TL - 1) / TL, tj = (a.J + TR - 1) / TR, tiles = ti * tj;
@@ -232,50 +236,118 @@ __global__ __launch_bounds__(64 * WL * WR) void product(LinearArgs a) {
   for (int p = 0; p < FL; ++p)
 #pragma unroll
     for (int q = 0; q < FR; ++q) acc[p][q] = zero16();
-  if (s0 < s1) {
-    cl.copy(left[0], s0 * KE<T>, tid);
-    cr.copy(right[0], s0 * KE<T>, tid);
-  }
-  for (int s = s0; s < s1; ++s) {
-    const int now = (s - s0) & 1;
+  // Fragments are read one block of k ahead, between the products, into the set that the products before last have
+  // used; a step's first ones right behind the barrier that hands its tiles over, among the last products of the
+  // step before.  (8-bit fragments of a large tile are too many for two sets, and widening them takes registers too.)
+  constexpr int NB = KE<T> / KM<T>, MF = FL * FR;
+  constexpr bool AHEAD = sizeof(T) > 1 || (std::is_same_v<T, e4m3> && MF <= 4);
+  static_assert(NB % 2 == 0, "a step begins with the same set");
+  Frag<T> fl[AHEAD ? 2 : 1][FL], fr[AHEAD ? 2 : 1][FR];
+  auto read = [&](int buffer, int b) __attribute__((always_inline)) {
+    const int set = AHEAD ? b & 1 : 0;
+#pragma unroll
+    for (int p = 0; p < FL; ++p) fl[set][p] = OL::frag(left[buffer], (wl * FL + p) * 32, b, lane);
+#pragma unroll
+    for (int q = 0; q < FR; ++q) fr[set][q] = OR::frag(right[buffer], (wr * FR + q) * 32, b, lane);
+  };
+  auto multiply = [&](int b, auto half) __attribute__((always_inline)) {        // 0: all of a block's products, 1, 2: their first, second half
+    constexpr int from = half.value == 2 ? MF / 2 : 0, to = half.value == 1 ? MF / 2 : MF;
+    const int set = AHEAD ? b & 1 : 0;
+#pragma unroll
+    for (int i = from; i < to; ++i) mma(acc[i / FR][i % FR], fl[set][i / FR], fr[set][i % FR]);
+  };
+  const std::integral_constant<int, 0> all;
+  const std::integral_constant<int, 1> first;
+  const std::integral_constant<int, 2> second;
+  auto blocks = [&](int now) __attribute__((always_inline)) {                   // all blocks of a step but the last one's products
+#pragma unroll
+    for (int b = 0; b + 1 < NB; ++b) {
+      if constexpr (AHEAD) {
+        read(now, b + 1);
+        multiply(b, all);
+        // one product, then its share of the reads
+        constexpr int MI = MF * (sizeof(T) == 4 ? 8 : 1), RD = FL * OL::READS + FR * OR::READS, EACH = (RD + MI - 1) / MI;
+#pragma unroll
+        for (int i = 0; i < RD / EACH; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, EACH, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, MI - RD / EACH, 0);
+      } else {
+        read(now, b);
+        multiply(b, all);
+      }
+    }
+    if constexpr (!AHEAD) read(now, NB - 1);
+  };
+  const unsigned place = __builtin_amdgcn_readfirstlane(wave * 1024);
+  const unsigned to_l = lds_address(left) + place, to_r = lds_address(right) + place;
+  auto copy = [&](int s, int buffer) __attribute__((always_inline)) {
+    const unsigned l = to_l + buffer * (OL::CHUNKS * 16), r = to_r + buffer * (OR::CHUNKS * 16);
+    if (s + 1 < steps) {
+      cl.copy(l, s * KE<T>);
+      cr.copy(r, s * KE<T>);
+    } else {
+      cl.copy_last(l, s * KE<T>, tid);
+      cr.copy_last(r, s * KE<T>, tid);
+    }
+  };
+  // step s's tiles have arrived, and those of the step before are read no more
+  auto arrive = [&](int s, int buffer) __attribute__((always_inline)) {
     copies_done();
     if (s == steps - 1) {
-      cl.clear(left[now], s * KE<T>, tid);
-      cr.clear(right[now], s * KE<T>, tid);
+      cl.clear(left[buffer], s * KE<T>, tid);
+      cr.clear(right[buffer], s * KE<T>, tid);
     }
-    __syncthreads();       // this step's tiles are there, and the last step's are read no more
-    if (s + 1 < s1) {
-      cl.copy(left[now ^ 1], (s + 1) * KE<T>, tid);
-      cr.copy(right[now ^ 1], (s + 1) * KE<T>, tid);
+    __syncthreads();
+    if (s + 1 < s1) copy(s + 1, buffer ^ 1);
+    if constexpr (AHEAD) read(buffer, 0);
+  };
+  if (s0 < s1) {
+    copy(s0, 0);
+    arrive(s0, 0);
+    int now = 0;
+    for (int s = s0; s + 1 < s1; ++s, now ^= 1) {
+      blocks(now);
+      if constexpr (AHEAD) {
+        multiply(NB - 1, first);
+        arrive(s + 1, now ^ 1);
+        multiply(NB - 1, second);
+      } else {
+        multiply(NB - 1, all);
+        arrive(s + 1, now ^ 1);
+      }
     }
-#pragma unroll
-    for (int b = 0; b < KE<T> / KM<T>; ++b) {
-      Frag<T> fl[FL], fr[FR];
-#pragma unroll
-      for (int p = 0; p < FL; ++p) fl[p] = OL::frag(left[now], (wl * FL + p) * 32, b, lane);
-#pragma unroll
-      for (int q = 0; q < FR; ++q) fr[q] = OR::frag(right[now], (wr * FR + q) * 32, b, lane);
-#pragma unroll
-      for (int p = 0; p < FL; ++p)
-#pragma unroll
-        for (int q = 0; q < FR; ++q) mma(acc[p][q], fl[p], fr[q]);
-    }
+    blocks(now);
+    multiply(NB - 1, all);
   }
+  // A wave's results leave through its part of LDS, 32 rows (j) of 32 FL entries at a time, so that rows are read and
+  // written whole (4 entries a lane straight from the registers, 16 neighbouring bytes a row: 321 us for 287 at 16384 x
+  // 2048 x 4096).  16-byte chunk n of row j stands at place n ^ (j & 7).
+  constexpr int CI = FL * 8, RI = 64 / CI;       // chunks of a row; rows that the wave's lanes cover
+  static_assert(32 * CI * WL * WR <= 2 * (OL::CHUNKS + OR::CHUNKS), "a wave's part");
+  __syncthreads();
+  uint4 *stage = lds + wave * 32 * CI;
   const int c = lane & 31, h = lane >> 5;
 #pragma unroll
   for (int q = 0; q < FR; ++q) {
-    const int j = j0 + (wr * FR + q) * 32 + c;
-    if (j >= a.J) continue;
 #pragma unroll
     for (int p = 0; p < FL; ++p)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int i = i0 + (wl * FL + p) * 32 + 8 * e + 4 * h;
-        if (i >= a.I) continue;
-        float v[4] = {acc[p][q][4 * e], acc[p][q][4 * e + 1], acc[p][q][4 * e + 2], acc[p][q][4 * e + 3]};
-        if (a.splits > 1) store4(a.part + ((size_t)split * a.J + j) * a.I + i, v[0], v[1], v[2], v[3]);
-        else finish<O>(a, i, j, v);
+        const f4 v = {acc[p][q][4 * e], acc[p][q][4 * e + 1], acc[p][q][4 * e + 2], acc[p][q][4 * e + 3]};
+        *reinterpret_cast<f4 *>(stage + c * CI + ((8 * p + 2 * e + h) ^ (c & 7))) = v;
       }
+#pragma unroll 4
+    for (int r = 0; r < 32; r += RI) {
+      const int row = r + lane / CI, n = lane % CI;
+      const int j = j0 + (wr * FR + q) * 32 + row, i = i0 + wl * FL * 32 + 4 * n;
+      const f4 t = *reinterpret_cast<const f4 *>(stage + row * CI + (n ^ (row & 7)));
+      if (j >= a.J || i >= a.I) continue;
+      float v[4] = {t[0], t[1], t[2], t[3]};
+      if (a.splits > 1) store4(a.part + ((size_t)split * a.J + j) * a.I + i, v[0], v[1], v[2], v[3]);
+      else finish<O>(a, i, j, v);
+    }
   }
 }
 
@@ -323,17 +395,26 @@ template <typename T, typename O, int MT> __global__ __launch_bounds__(64 * FEW_
     x[m] = static_cast<const T *>(a.right) + (int64_t)min(16 * m + r, a.J - 1) * a.ldr;
     acc[m] = f4{0.f, 0.f, 0.f, 0.f};
   }
-#pragma unroll 4
-  for (int k = wave * STEP + g * E; k - g * E < a.K; k += FEW_WAVES * STEP) {
-    const bool on = k < a.K;
-    const int kk = on ? k : 0;
-    u4 p = load16(w + kk);
-    if (!on) p = u4{0, 0, 0, 0};
+  // U turns' loads in flight together
+  constexpr int U = MT == 1 ? 8 : MT == 2 ? 4 : 2, TURN = FEW_WAVES * STEP;
+  for (int k0 = wave * STEP; k0 < a.K; k0 += U * TURN) {
+    u4 p[U], q[U][MT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      u4 q = load16(x[m] + kk);
-      if (!on) q = u4{0, 0, 0, 0};
-      mma16b<T>(acc[m], p, q);
+    for (int t = 0; t < U; ++t) {
+      const int k = min(k0 + t * TURN + g * E, a.K - E);
+      p[t] = load16(w + k);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) q[t][m] = load16(x[m] + k);
+    }
+#pragma unroll
+    for (int t = 0; t < U; ++t) {
+      const bool on = k0 + t * TURN + g * E < a.K;      // behind the end: zeros for both
+      if (!on) p[t] = u4{0, 0, 0, 0};
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        if (!on) q[t][m] = u4{0, 0, 0, 0};
+        mma16b<T>(acc[m], p[t], q[t][m]);
+      }
     }
   }
 #pragma unroll
@@ -391,12 +472,15 @@ template <typename T> __global__ __launch_bounds__(256) void pre_gradient(Linear
 // ---- Launches ---------------------------------------------------------------------------
 struct Plan { bool big; int splits; int64_t tiles; };
 
-// Tiles of 256 x 256 where they fill the chip, else of 128 x 128; k is split where those leave compute units idle,
-// at 4 steps a split and 16 splits at most.
+// A compute unit holds one workgroup of 256 x 256 or two of 128 x 128; the larger tile reads less from LDS for a product
+// (16384 x 2048 -> 4096 bf16: 287 us, 299 with the smaller), the smaller one leaves less of the last round empty (16384 x
+// 768 -> 1536: 54.7 us, 58.7 with the larger; 2048 x 2048 -> 2048: 29, 51).  So rounds are counted, in tiles of 128 x
+// 128 a compute unit.  8-bit and fp32 operands take too many registers for the larger (16387 x 4096 -> 2048 e4m3:
+// 248 us, 469).  Where 128 x 128 tiles leave compute units idle, k is split, at 4 steps a split and 16 splits at most.
 Plan plan_of(int64_t I, int64_t J, int64_t K, int e) {
   Plan p;
   const int64_t large = ((I + 255) / 256) * ((J + 255) / 256), small = ((I + 127) / 128) * ((J + 127) / 128);
-  p.big = e < 4 && large >= 224;    // fp32 by columns would spill
+  p.big = e == 2 && large >= 256 && (large + 255) / 256 * 4 * 20 <= (small + 511) / 512 * 2 * 21;
   p.tiles = p.big ? large : small;
   const int64_t steps = (K * e + KB - 1) / KB;
   p.splits = 1;
@@ -414,7 +498,7 @@ template <typename T, typename O, bool LC, bool RC> hipError_t multiply(LinearAr
   a.splits = p.splits;
   a.part = static_cast<float *>(ws);
   const unsigned grid = (unsigned)((p.tiles * p.splits + 7) / 8 * 8);
-  if constexpr (sizeof(T) < 4) {
+  if constexpr (sizeof(T) == 2) {
     if (p.big) hipLaunchKernelGGL((product<T, O, LC, RC, 256, 256, 2, 4>), dim3(grid), dim3(512), 0, s, a);
   }
   if (!p.big) hipLaunchKernelGGL((product<T, O, LC, RC, 128, 128, 2, 2>), dim3(grid), dim3(256), 0, s, a);
