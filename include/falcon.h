@@ -624,7 +624,7 @@ size_t falcon_ssm_fwd_workspace(const falcon_ssm_shape_t *shape, int packed);
 /* Chunks of K = FALCON_SSM_CHUNK(N) steps that the forward keeps a state of: batch ceil(T / K),
  * or packed floor(T / K) + batch (chunk c of sequence n, which begins at token s, is number
  * floor(s / K) + n + c; some stay unused).  0 for invalid shapes. */
-int32_t falcon_ssm_chunks(const falcon_ssm_shape_t *shape, int packed);
+int falcon_ssm_chunks(const falcon_ssm_shape_t *shape, int packed);
 
 /*   cu_seqlens   NULL: x, dt, z, y are [B, T, D] and Bm, Cm [B, T, N].  Otherwise [B + 1] offsets,
  *                and they are [T, ...].

@@ -263,7 +263,7 @@ size_t falcon_ssm_fwd_workspace(const falcon_ssm_shape_t *s, int packed) {
   return falcon::ssm_fwd_workspace(seq_sizes(s->batch, s->seqlen, packed != 0), s->width, s->state);
 }
 
-int32_t falcon_ssm_chunks(const falcon_ssm_shape_t *s, int packed) {
+int falcon_ssm_chunks(const falcon_ssm_shape_t *s, int packed) {
   if (check_ssm(s, packed != 0, false) != FALCON_OK) return 0;
   const int K = falcon::ssm_chunk(s->state);
   if (packed) return s->seqlen / K + s->batch;

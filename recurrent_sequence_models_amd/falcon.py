@@ -178,7 +178,7 @@ def lib() -> ctypes.CDLL:
         L.falcon_conv_step.argtypes = [P(ConvShape), Heads, V, V, V, V, V, V]
         L.falcon_ssm_fwd_workspace.restype = S
         L.falcon_ssm_fwd_workspace.argtypes = [P(SsmShape), I]
-        L.falcon_ssm_chunks.restype = ctypes.c_int32
+        L.falcon_ssm_chunks.restype = I
         L.falcon_ssm_chunks.argtypes = [P(SsmShape), I]
         L.falcon_ssm_fwd.restype = I
         L.falcon_ssm_fwd.argtypes = [P(SsmShape), V, Heads, Heads, V, Heads, Heads, V, Heads, V, V, V, V, V, V, S, V]
