@@ -34,6 +34,8 @@ def _rows(name, t, dtype, dev, shape=None):
     """falcon_heads_t of t [..., width] (of this shape, if given): dense rows, tokens one
     stride apart (views of a wider projection are taken as they are)."""
     size = t.shape
+    if t.is_contiguous() and t.dtype is dtype and (shape is None or size == shape) and t.device == dev:
+        return Heads(t.data_ptr(), size[-1])
     if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if shape is not None and size != shape:
@@ -41,18 +43,17 @@ def _rows(name, t, dtype, dev, shape=None):
     if t.device != dev:
         raise ValueError(f"{name}: must live on {dev}")
     step = size[-1]
-    if not t.is_contiguous():
-        *strides, sd = t.stride()
-        want, ok = None, sd == 1 or size[-1] == 1
-        for n, s in zip(reversed(size[:-1]), reversed(strides)):
-            if n == 1:
-                continue
-            if want is None:
-                step = want = s
-            ok = ok and s == want
-            want = want * n
-        if not ok or step < size[-1]:
-            raise ValueError(f"{name}: rows must be dense and tokens one stride apart")
+    *strides, sd = t.stride()
+    want, ok = None, sd == 1 or size[-1] == 1
+    for n, s in zip(reversed(size[:-1]), reversed(strides)):
+        if n == 1:
+            continue
+        if want is None:
+            step = want = s
+        ok = ok and s == want
+        want = want * n
+    if not ok or step < size[-1]:
+        raise ValueError(f"{name}: rows must be dense and tokens one stride apart")
     if (step * t.element_size()) % 16:
         raise ValueError(f"{name}: the distance of two tokens must be a multiple of 16 bytes")
     return Heads(t.data_ptr(), step)

@@ -6,7 +6,8 @@
 // inputs its final one.  Backward, with d_t = dy_t act'(p_t):
 //   dx_t = sum_j w_j d_{t+W-1-j} (within the sequence),  dw_j = sum_t d_t x_{t-W+1+j},  db = sum_t d_t.
 //
-// A thread owns 16 bytes of channels and a run of consecutive tokens, and slides over them with the
+// A thread owns E neighbouring channels (16 bytes; backward 4 channels, whose sums for the weights would else
+// take the registers of half of the waves) and a run of consecutive tokens, and slides over them with the
 // last W - 1 inputs (backward: and the W unfinished gradients) in registers.  The W - 1 tokens next to
 // a run are read again, from the cache as a rule: the runs beside belong to the same workgroup.
 // In the backward pass d is formed again for the W - 1 tokens behind the run, rather than
@@ -17,10 +18,10 @@
 namespace falcon {
 namespace {
 
-constexpr int THR = 256, LANES = 16, RUNS = THR / LANES;   // lanes side by side over channels; runs of a workgroup
+constexpr int THR = 256;
+// lanes side by side over channels, and runs of a workgroup; forward and backward
+constexpr int LANES_F = 16, RUNS_F = THR / LANES_F, LANES_B = 32, RUNS_B = THR / LANES_B;
 constexpr int AHEAD = 4;                                   // tokens whose loads are in flight together
-
-template <int E> __device__ __forceinline__ float conv_at(const float (&w)[E], const float (&x)[E], int j) { return w[j] * x[j]; }
 
 // This thread's filters: w[k][j] of tap k, channel j; bias.
 template <int W, int E>
@@ -34,40 +35,39 @@ __device__ __forceinline__ void load_filters(const ConvArgs &a, int c, float (&w
 }
 
 // The W - 1 inputs before token t of sequence n, which begins at s.
-template <typename T, int W>
-__device__ __forceinline__ void load_window(const ConvArgs &a, int n, int s, int t, int c, u4 (&win)[W - 1]) {
+template <typename T, int W, int E>
+__device__ __forceinline__ void load_window(const ConvArgs &a, int n, int s, int t, int c, Few<T, E> (&win)[W - 1]) {
 #pragma unroll
   for (int i = 0; i < W - 1; ++i) {
     const int p = t - (W - 1) + i;
-    if (p >= s) win[i] = load16(static_cast<const T *>(a.x) + (int64_t)p * a.ldx + c);
-    else if (a.init) win[i] = load16(static_cast<const T *>(a.init) + ((size_t)n * (W - 1) + (p - s + W - 1)) * a.D + c);
-    else win[i] = u4{0, 0, 0, 0};
+    if (p >= s) fetch(static_cast<const T *>(a.x) + (int64_t)p * a.ldx + c, win[i]);
+    else if (a.init) fetch(static_cast<const T *>(a.init) + ((size_t)n * (W - 1) + (p - s + W - 1)) * a.D + c, win[i]);
+    else win[i] = Few<T, E>{};
   }
 }
 
 // b + sum of the window and the newest input
-template <int W, int E>
-__device__ __forceinline__ void convolve(const float (&w)[W][E], const float (&b)[E], const u4 (&win)[W - 1], const u4 &x,
-                                         float (&p)[E]) {
+template <typename T, int W, int E>
+__device__ __forceinline__ void convolve(const float (&w)[W][E], const float (&b)[E], const Few<T, E> (&win)[W - 1],
+                                         const Few<T, E> &x, float (&p)[E]) {
 #pragma unroll
   for (int j = 0; j < E; ++j) p[j] = b[j];
 #pragma unroll
   for (int k = 0; k < W; ++k) {
-    float v[E];
-    widen(k < W - 1 ? win[k < W - 1 ? k : 0] : x, v);
+    const Few<T, E> v = k < W - 1 ? win[k < W - 1 ? k : 0] : x;
 #pragma unroll
     for (int j = 0; j < E; ++j) p[j] = fmaf(w[k][j], v[j], p[j]);
   }
 }
 
-template <int W> __device__ __forceinline__ void slide(u4 (&win)[W - 1], const u4 &x) {
+template <typename T, int W, int E> __device__ __forceinline__ void slide(Few<T, E> (&win)[W - 1], const Few<T, E> &x) {
 #pragma unroll
   for (int i = 0; i + 1 < W - 1; ++i) win[i] = win[i + 1];
   win[W - 2] = x;
 }
 
 // Rows of an [n, W - 1, D] array that belong to empty sequences, copied (zeros without a source).
-template <typename T, int W>
+template <typename T, int W, int E>
 __device__ __forceinline__ void copy_empty(const ConvArgs &a, const void *from, void *to, int first, int step, int c) {
   if (!a.seq.cu || !to) return;
   for (int n = first; n < a.seq.n; n += step) {
@@ -75,19 +75,21 @@ __device__ __forceinline__ void copy_empty(const ConvArgs &a, const void *from, 
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) {
       const size_t at = ((size_t)n * (W - 1) + i) * a.D + c;
-      store16(static_cast<T *>(to) + at, from ? load16(static_cast<const T *>(from) + at) : u4{0, 0, 0, 0});
+      Few<T, E> v{};
+      if (from) fetch(static_cast<const T *>(from) + at, v);
+      put(static_cast<T *>(to) + at, v);
     }
   }
 }
 
 template <typename T, int W> __global__ __launch_bounds__(THR) void conv_fwd(ConvArgs a) {
   constexpr int E = PER16<T>;
-  const int c = (blockIdx.y * LANES + threadIdx.x % LANES) * E;
-  const int run = blockIdx.x * RUNS + threadIdx.x / LANES, total = a.seq.tokens();
+  const int c = (blockIdx.y * LANES_F + threadIdx.x % LANES_F) * E;
+  const int run = blockIdx.x * RUNS_F + threadIdx.x / LANES_F, total = a.seq.tokens();
   if (c >= a.D) return;
   float w[W][E], b[E];
   load_filters<W, E>(a, c, w, b);
-  copy_empty<T, W>(a, a.init, a.final_state, run, gridDim.x * RUNS, c);
+  copy_empty<T, W, E>(a, a.init, a.final_state, run, gridDim.x * RUNS_F, c);
   const int64_t t0 = (int64_t)run * a.run;
   if (t0 >= total) return;
   const int last = (int)min(t0 + a.run, (int64_t)total);
@@ -96,23 +98,23 @@ template <typename T, int W> __global__ __launch_bounds__(THR) void conv_fwd(Con
     const int s = a.seq.begin(n), e = a.seq.end(n), to = min(e, last);
     t = max(t, s);
     if (t >= to) continue;
-    u4 win[W - 1];
-    load_window<T, W>(a, n, s, t, c, win);
+    Few<T, E> win[W - 1];
+    load_window<T, W, E>(a, n, s, t, c, win);
     for (; t < to; t += AHEAD) {
-      u4 x[AHEAD];
+      Few<T, E> x[AHEAD];
 #pragma unroll
-      for (int i = 0; i < AHEAD; ++i) x[i] = load16(static_cast<const T *>(a.x) + (int64_t)min(t + i, to - 1) * a.ldx + c);
+      for (int i = 0; i < AHEAD; ++i) fetch(static_cast<const T *>(a.x) + (int64_t)min(t + i, to - 1) * a.ldx + c, x[i]);
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) {
         if (t + i < to) {
           float p[E];
-          convolve<W, E>(w, b, win, x[i], p);
+          convolve<T, W, E>(w, b, win, x[i], p);
           if (a.silu) {
 #pragma unroll
             for (int j = 0; j < E; ++j) p[j] *= sigmoid(p[j]);
           }
-          store16(static_cast<T *>(a.y) + (size_t)(t + i) * a.D + c, narrow(p));
-          slide<W>(win, x[i]);
+          put(static_cast<T *>(a.y) + (size_t)(t + i) * a.D + c, p);
+          slide<T, W, E>(win, x[i]);
         }
       }
     }
@@ -120,20 +122,20 @@ template <typename T, int W> __global__ __launch_bounds__(THR) void conv_fwd(Con
     if (to == e && a.final_state) {
 #pragma unroll
       for (int i = 0; i < W - 1; ++i)
-        store16(static_cast<T *>(a.final_state) + ((size_t)n * (W - 1) + i) * a.D + c, win[i]);
+        put(static_cast<T *>(a.final_state) + ((size_t)n * (W - 1) + i) * a.D + c, win[i]);
     }
   }
 }
 
 template <typename T, int W> __global__ __launch_bounds__(THR) void conv_bwd(ConvArgs a) {
-  constexpr int E = PER16<T>;
-  const int col = threadIdx.x % LANES, c = (blockIdx.y * LANES + col) * E;
-  const int run = blockIdx.x * RUNS + threadIdx.x / LANES, total = a.seq.tokens();
+  constexpr int E = 4;
+  const int col = threadIdx.x % LANES_B, c = (blockIdx.y * LANES_B + col) * E;
+  const int run = blockIdx.x * RUNS_B + threadIdx.x / LANES_B, total = a.seq.tokens();
   const bool in = c < a.D;
   float w[W][E], b[E], dw[W][E] = {}, db[E] = {};
   if (in) {
     load_filters<W, E>(a, c, w, b);
-    copy_empty<T, W>(a, a.d_final, a.d_init, run, gridDim.x * RUNS, c);
+    copy_empty<T, W, E>(a, a.d_final, a.d_init, run, gridDim.x * RUNS_B, c);
   }
   const int64_t t0 = (int64_t)run * a.run;
   const int last = (int)min(t0 + a.run, (int64_t)total);
@@ -144,31 +146,32 @@ template <typename T, int W> __global__ __launch_bounds__(THR) void conv_bwd(Con
       t = max(t, s);
       if (t >= to) continue;
       const int from = t, upto = (int)min((int64_t)to + W - 1, (int64_t)e);
-      u4 win[W - 1];
-      load_window<T, W>(a, n, s, t, c, win);
+      Few<T, E> win[W - 1];
+      load_window<T, W, E>(a, n, s, t, c, win);
       float acc[W][E] = {};      // acc[i]: the gradient of token t - (W - 1) + i so far
       // token p is finished: its gradient leaves, for the initial state where p lies before the sequence
       auto emit = [&](int p, const float (&v)[E]) {
-        if (p >= from && p < to) store16(static_cast<T *>(a.dx) + (int64_t)p * a.lddx + c, narrow(v));
+        if (p >= from && p < to) put(static_cast<T *>(a.dx) + (int64_t)p * a.lddx + c, v);
         else if (p < s && from == s && a.d_init)
-          store16(static_cast<T *>(a.d_init) + ((size_t)n * (W - 1) + (p - s + W - 1)) * a.D + c, narrow(v));
+          put(static_cast<T *>(a.d_init) + ((size_t)n * (W - 1) + (p - s + W - 1)) * a.D + c, v);
       };
       for (; t < upto; t += AHEAD) {
-        u4 x[AHEAD], g[AHEAD];
+        Few<T, E> x[AHEAD], g[AHEAD];
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
           const int q = min(t + i, upto - 1);
-          x[i] = load16(static_cast<const T *>(a.x) + (int64_t)q * a.ldx + c);
-          g[i] = load16(static_cast<const T *>(a.dy) + (size_t)q * a.D + c);
+          fetch(static_cast<const T *>(a.x) + (int64_t)q * a.ldx + c, x[i]);
+          fetch(static_cast<const T *>(a.dy) + (size_t)q * a.D + c, g[i]);
         }
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
           if (t + i < upto) {
-            float d[E], v[E];
-            widen(g[i], d);
+            float d[E];
+#pragma unroll
+            for (int j = 0; j < E; ++j) d[j] = g[i][j];
             if (a.silu) {
               float p[E];
-              convolve<W, E>(w, b, win, x[i], p);
+              convolve<T, W, E>(w, b, win, x[i], p);
 #pragma unroll
               for (int j = 0; j < E; ++j) {
                 const float sg = sigmoid(p[j]);
@@ -178,7 +181,7 @@ template <typename T, int W> __global__ __launch_bounds__(THR) void conv_bwd(Con
             if (t + i < to) {
 #pragma unroll
               for (int k = 0; k < W; ++k) {
-                widen(k < W - 1 ? win[k < W - 1 ? k : 0] : x[i], v);
+                const Few<T, E> v = k < W - 1 ? win[k < W - 1 ? k : 0] : x[i];
 #pragma unroll
                 for (int j = 0; j < E; ++j) dw[k][j] = fmaf(d[j], v[j], dw[k][j]);
               }
@@ -196,7 +199,7 @@ template <typename T, int W> __global__ __launch_bounds__(THR) void conv_bwd(Con
               for (int j = 0; j < E; ++j) acc[k][j] = acc[k + 1][j];
 #pragma unroll
             for (int j = 0; j < E; ++j) acc[W - 1][j] = 0.f;
-            slide<W>(win, x[i]);
+            slide<T, W, E>(win, x[i]);
           }
         }
       }
@@ -204,8 +207,8 @@ template <typename T, int W> __global__ __launch_bounds__(THR) void conv_bwd(Con
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) {
           if (a.d_final) {
-            float v[E];
-            widen(load16(static_cast<const T *>(a.d_final) + ((size_t)n * (W - 1) + i) * a.D + c), v);
+            Few<T, E> v;
+            fetch(static_cast<const T *>(a.d_final) + ((size_t)n * (W - 1) + i) * a.D + c, v);
 #pragma unroll
             for (int j = 0; j < E; ++j) acc[i][j] += v[j];
           }
@@ -217,19 +220,19 @@ template <typename T, int W> __global__ __launch_bounds__(THR) void conv_bwd(Con
   }
   if (!a.part) return;
   // the workgroup's sums for the weights, over its runs in order
-  __shared__ __align__(16) float sum[RUNS][LANES][E];
+  __shared__ __align__(16) float sum[RUNS_B][LANES_B][E];
   float *out = a.part + (size_t)blockIdx.x * a.D * (W + 1);
 #pragma unroll
   for (int k = 0; k <= W; ++k) {
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < E; ++j) sum[threadIdx.x / LANES][col][j] = k < W ? dw[k < W ? k : 0][j] : db[j];
+    for (int j = 0; j < E; ++j) sum[threadIdx.x / LANES_B][col][j] = k < W ? dw[k < W ? k : 0][j] : db[j];
     __syncthreads();
-    const int cc = blockIdx.y * LANES * E + threadIdx.x;
-    if (threadIdx.x < LANES * E && cc < a.D) {
+    const int cc = blockIdx.y * LANES_B * E + threadIdx.x;
+    if (threadIdx.x < LANES_B * E && cc < a.D) {
       float v = 0.f;
 #pragma unroll
-      for (int r = 0; r < RUNS; ++r) v += sum[r][threadIdx.x / E][threadIdx.x % E];
+      for (int r = 0; r < RUNS_B; ++r) v += sum[r][threadIdx.x / E][threadIdx.x % E];
       out[k < W ? (size_t)cc * W + k : (size_t)a.D * W + cc] = v;
     }
   }
@@ -241,46 +244,54 @@ template <typename T, int W> __global__ __launch_bounds__(THR) void conv_step(Co
   const int64_t i = (int64_t)blockIdx.x * THR + threadIdx.x;
   const int n = (int)(i / per), c = (int)(i - (int64_t)n * per) * E;
   if (n >= a.seq.n) return;
-  u4 win[W - 1];
-  const u4 x = load16(static_cast<const T *>(a.x) + (int64_t)n * a.ldx + c);
+  Few<T, E> win[W - 1];
+  Few<T, E> x;
+  fetch(static_cast<const T *>(a.x) + (int64_t)n * a.ldx + c, x);
   const size_t at = (size_t)n * (W - 1) * a.D + c;
 #pragma unroll
-  for (int k = 0; k < W - 1; ++k) win[k] = load16(static_cast<const T *>(a.init) + at + (size_t)k * a.D);
+  for (int k = 0; k < W - 1; ++k) fetch(static_cast<const T *>(a.init) + at + (size_t)k * a.D, win[k]);
   float w[W][E], b[E], p[E];
   load_filters<W, E>(a, c, w, b);
-  convolve<W, E>(w, b, win, x, p);
+  convolve<T, W, E>(w, b, win, x, p);
   if (a.silu) {
 #pragma unroll
     for (int j = 0; j < E; ++j) p[j] *= sigmoid(p[j]);
   }
-  store16(static_cast<T *>(a.y) + (size_t)n * a.D + c, narrow(p));
-  slide<W>(win, x);
+  put(static_cast<T *>(a.y) + (size_t)n * a.D + c, p);
+  slide<T, W, E>(win, x);
 #pragma unroll
-  for (int k = 0; k < W - 1; ++k) store16(static_cast<T *>(a.final_state) + at + (size_t)k * a.D, win[k]);
+  for (int k = 0; k < W - 1; ++k) put(static_cast<T *>(a.final_state) + at + (size_t)k * a.D, win[k]);
 }
 
-// Tokens of a run: long runs read fewer tokens twice, short ones make more workgroups.
-int run_of(SeqMap seq, int D, int E) {
-  const int64_t cols = (D + LANES * E - 1) / (LANES * E);
-  for (int run : {16, 8})
-    if (((int64_t)seq.tokens() + run * RUNS - 1) / (run * RUNS) * cols >= 512) return run;
-  return 4;
+// A pass's shape: channels of a workgroup, runs of it, and the tokens of a run.  Long runs read fewer tokens twice, short
+// ones make more workgroups.
+struct Shape {
+  int cols, runs, run;
+  dim3 grid;
+};
+Shape shape_of(SeqMap seq, int D, bool bf16, bool back) {
+  Shape s;
+  s.cols = back ? LANES_B * 4 : LANES_F * (bf16 ? 8 : 4);
+  s.runs = back ? RUNS_B : RUNS_F;
+  const int64_t wide = (D + s.cols - 1) / s.cols, tokens = seq.tokens();
+  s.run = back ? 32 : 16;
+  while (s.run > 4 && (tokens + s.run * s.runs - 1) / (s.run * s.runs) * wide < 512) s.run /= 2;
+  s.grid = dim3((unsigned)((tokens + s.run * s.runs - 1) / (s.run * s.runs)), (unsigned)wide);
+  return s;
 }
-dim3 grid_of(SeqMap seq, int D, int E) {
-  const int64_t per = (int64_t)run_of(seq, D, E) * RUNS;
-  return dim3((unsigned)((seq.tokens() + per - 1) / per), (unsigned)((D + LANES * E - 1) / (LANES * E)));
-}
-int entries(bool bf16) { return bf16 ? 8 : 4; }
 
 }  // namespace
 
 bool conv_fits(bool bf16, SeqMap seq, int D) {
-  const dim3 g = grid_of(seq, D, entries(bf16));
-  return g.y <= 65535 && grid_fits((int64_t)g.x * g.y, THR);
+  for (const bool back : {false, true}) {
+    const dim3 g = shape_of(seq, D, bf16, back).grid;
+    if (g.y > 65535 || !grid_fits((int64_t)g.x * g.y, THR)) return false;
+  }
+  return true;
 }
 
 size_t conv_bwd_workspace(bool bf16, int taps, SeqMap seq, int D) {
-  return (size_t)grid_of(seq, D, entries(bf16)).x * D * (taps + 1) * sizeof(float);
+  return (size_t)shape_of(seq, D, bf16, true).grid.x * D * (taps + 1) * sizeof(float);
 }
 
 #define FALCON_CONV(KERNEL, GRID)                                                                             \
@@ -293,24 +304,24 @@ size_t conv_bwd_workspace(bool bf16, int taps, SeqMap seq, int D) {
   else return hipErrorInvalidValue;
 
 hipError_t launch_conv_fwd(bool bf16, int taps, ConvArgs a, hipStream_t s) {
-  a.run = run_of(a.seq, a.D, entries(bf16));
-  const dim3 grid = grid_of(a.seq, a.D, entries(bf16));
-  FALCON_CONV(conv_fwd, grid)
+  const Shape p = shape_of(a.seq, a.D, bf16, false);
+  a.run = p.run;
+  FALCON_CONV(conv_fwd, p.grid)
   return hipGetLastError();
 }
 
 hipError_t launch_conv_bwd(bool bf16, int taps, ConvArgs a, float *dw, float *db, void *ws, hipStream_t s) {
-  a.run = run_of(a.seq, a.D, entries(bf16));
+  const Shape p = shape_of(a.seq, a.D, bf16, true);
+  a.run = p.run;
   a.part = dw || db ? static_cast<float *>(ws) : nullptr;
-  const dim3 grid = grid_of(a.seq, a.D, entries(bf16));
-  FALCON_CONV(conv_bwd, grid)
+  FALCON_CONV(conv_bwd, p.grid)
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.part) return e;
-  return launch_column_sum(a.part, grid.x, (int64_t)a.D * (taps + 1), dw, (int64_t)a.D * taps, db, s);
+  return launch_column_sum(a.part, p.grid.x, (int64_t)a.D * (taps + 1), dw, (int64_t)a.D * taps, db, s);
 }
 
 hipError_t launch_conv_step(bool bf16, int taps, ConvArgs a, hipStream_t s) {
-  const int64_t threads = (int64_t)a.seq.n * (a.D / entries(bf16));
+  const int64_t threads = (int64_t)a.seq.n * (a.D / (bf16 ? 8 : 4));
   const dim3 grid((unsigned)((threads + THR - 1) / THR));
   FALCON_CONV(conv_step, grid)
   return hipGetLastError();

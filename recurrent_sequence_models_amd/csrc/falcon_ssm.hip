@@ -88,14 +88,14 @@ __global__ __launch_bounds__((SsmTile<N, FWD_CH, TW, STEPS>::THR), (STEPS == 16 
     const bool valid = lon && t + ls < g.t1;      // steps behind the end change nothing: delta = 0
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      float d = (float)nd.v[j] + bias[j];
+      float d = nd[j] + bias[j];
       if (a.softplus) d = softplus(d);
-      step[ls][lc + j] = valid ? float2{d, d * (float)x.v[j]} : float2{0.f, 0.f};
+      step[ls][lc + j] = valid ? float2{d, d * x[j]} : float2{0.f, 0.f};
     }
 #pragma unroll
     for (int j = 0; j < BV; ++j) {
-      sB[bs][bn + j] = (float)nB.v[j];
-      if constexpr (!MAPS) sC[bs][bn + j] = (float)nC.v[j];
+      sB[bs][bn + j] = nB[j];
+      if constexpr (!MAPS) sC[bs][bn + j] = nC[j];
     }
     __syncthreads();
     if (t + L::TS < g.t1) load(t + L::TS);
@@ -158,8 +158,8 @@ __global__ __launch_bounds__((SsmTile<N, FWD_CH, TW, STEPS>::THR), (STEPS == 16 
         float y[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          y[j] = fmaf(skip[j], (float)x.v[j], step[ls][lc + j].x);
-          if (a.z) y[j] *= (float)z.v[j] * sigmoid((float)z.v[j]);
+          y[j] = fmaf(skip[j], x[j], step[ls][lc + j].x);
+          if (a.z) y[j] *= z[j] * sigmoid(z[j]);
         }
         store_few<V>(entry<T>(a.y, a.D, t, ls, lcc), y);
       }

@@ -117,21 +117,21 @@ template <typename T, int N, bool MAPS> __global__ __launch_bounds__(BwdTile<N>:
     f4 hv = nh;                                  // the tile's first state, then this wave's
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      d[j] = (float)nd.v[j] + sbias[lc + j];
+      d[j] = nd[j] + sbias[lc + j];
       slope[j] = 1.f;
       if (a.softplus) { slope[j] = sigmoid(d[j]); d[j] = softplus(d[j]); }
-      gy[j] = (float)ng.v[j];
+      gy[j] = ng[j];
       if (a.z) {
-        const float z = (float)nz.v[j], sg = sigmoid(z);
+        const float z = nz[j], sg = sigmoid(z);
         gz[j] = gy[j] * sg * fmaf(z, 1.f - sg, 1.f);
         gy[j] *= z * sg;
       }
-      step[ls][lc + j] = valid ? f4{d[j], d[j] * (float)x.v[j], gy[j], 0.f} : f4{0.f, 0.f, 0.f, 0.f};
+      step[ls][lc + j] = valid ? f4{d[j], d[j] * x[j], gy[j], 0.f} : f4{0.f, 0.f, 0.f, 0.f};
     }
 #pragma unroll
     for (int j = 0; j < BV; ++j) {
-      if (!MAPS) sBC[bs][0][bn + j] = (float)nB.v[j];
-      sBC[bs][1][bn + j] = (float)nC.v[j];
+      if (!MAPS) sBC[bs][0][bn + j] = nB[j];
+      sBC[bs][1][bn + j] = nC[j];
     }
     __syncthreads();
     if (t > g.t0) load(t - L::TS);
@@ -252,7 +252,7 @@ template <typename T, int N, bool MAPS> __global__ __launch_bounds__(BwdTile<N>:
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const f4 sum = step[ls][lc + j];
-          const float xv = (float)x.v[j], sk = sskip[lc + j];
+          const float xv = x[j], sk = sskip[lc + j];
           dx[j] = fmaf(sum[0], d[j], sk * gy[j]);
           ddt[j] = fmaf(sum[0], xv, sum[1] * SSM_LN2) * slope[j];
           dD[j] = fmaf(gy[j], xv, dD[j]);

@@ -46,6 +46,43 @@ template <int N> __device__ __forceinline__ void store_f32(float *p, const float
   for (int j = 0; j < N; j += 4) *reinterpret_cast<f4 *>(p + j) = f4{v[j], v[j + 1], v[j + 2], v[j + 3]};
 }
 
+// V consecutive entries as they are in memory (whole registers, or half of one), at an address that is a multiple of
+// their size together; for what is loaded long before its use.
+template <typename T, int V> struct Few {
+  static constexpr int BYTES = V * (int)sizeof(T), WORDS = BYTES < 4 ? 1 : BYTES / 4;
+  unsigned u[WORDS];
+  __device__ __forceinline__ float operator[](int j) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(u[j]);
+    return __uint_as_float(j & 1 ? u[j / 2] & 0xffff0000u : u[j / 2] << 16);
+  }
+};
+template <typename T, int V> __device__ __forceinline__ void fetch(const T *p, Few<T, V> &o) {
+  if constexpr (Few<T, V>::BYTES == 16) {
+    const u4 t = *reinterpret_cast<const u4 *>(p);
+    o.u[0] = t[0]; o.u[1] = t[1]; o.u[2] = t[2]; o.u[3] = t[3];
+  } else if constexpr (Few<T, V>::BYTES == 8) {
+    const uint2 t = *reinterpret_cast<const uint2 *>(p);
+    o.u[0] = t.x; o.u[1] = t.y;
+  } else if constexpr (Few<T, V>::BYTES == 4) {
+    o.u[0] = *reinterpret_cast<const unsigned *>(p);
+  } else {
+    static_assert(Few<T, V>::BYTES == 2, "1 to 16 bytes");
+    o.u[0] = *reinterpret_cast<const unsigned short *>(p);
+  }
+}
+template <typename T, int V> __device__ __forceinline__ void put(T *p, const Few<T, V> &o) {
+  if constexpr (Few<T, V>::BYTES == 16) *reinterpret_cast<u4 *>(p) = u4{o.u[0], o.u[1], o.u[2], o.u[3]};
+  else if constexpr (Few<T, V>::BYTES == 8) *reinterpret_cast<uint2 *>(p) = uint2{o.u[0], o.u[1]};
+  else if constexpr (Few<T, V>::BYTES == 4) *reinterpret_cast<unsigned *>(p) = o.u[0];
+  else *reinterpret_cast<unsigned short *>(p) = (unsigned short)o.u[0];
+}
+// Rounded to nearest even: the one rounding of a result held in bf16.
+__device__ __forceinline__ void put(__bf16 *p, const float (&v)[8]) { store16(p, narrow(v)); }
+__device__ __forceinline__ void put(float *p, const float (&v)[4]) { store16(p, narrow(v)); }
+__device__ __forceinline__ void put(__bf16 *p, const float (&v)[4]) {
+  *reinterpret_cast<bf4 *>(p) = __builtin_convertvector(f4{v[0], v[1], v[2], v[3]}, bf4);
+}
+
 // Sum over the 64 lanes of a wave, in each of them.
 __device__ __forceinline__ float wave_sum(float x) { return add_xor32(add_xor16(lane_sum<16>(x))); }
 // The largest of 64 lanes' unsigned values, in each of them.

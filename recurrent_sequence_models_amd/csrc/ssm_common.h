@@ -52,12 +52,6 @@ template <typename T> __device__ __forceinline__ T *entry(void *p, int64_t ld, i
   return reinterpret_cast<T *>(base + (unsigned)(row * ((int)ld * (int)sizeof(T)) + col * (int)sizeof(T)));
 }
 
-// The same as it is in memory, for what is loaded long before its use.
-template <typename T, int V> struct Few { T v[V]; };
-template <typename T, int V> __device__ __forceinline__ void fetch(const T *p, Few<T, V> &o) {
-  struct alignas(sizeof(T) * V) Whole { Few<T, V> f; };
-  o = reinterpret_cast<const Whole *>(p)->f;
-}
 template <int V> __device__ __forceinline__ void store_few(float *p, const float (&v)[V]) {
   if constexpr (V == 4) *reinterpret_cast<f4 *>(p) = f4{v[0], v[1], v[2], v[3]};
   else if constexpr (V == 2) *reinterpret_cast<float2 *>(p) = float2{v[0], v[1]};
