@@ -136,19 +136,24 @@ __global__ __launch_bounds__((SsmTile<N, FWD_CH, TW, STEPS>::THR), (STEPS == 16 
     if constexpr (!MAPS) {
       if (a.states && on && (t - g.s + s0) % SSM_CHUNK<N> == 0 && t + s0 < g.t1)
         *reinterpret_cast<f4 *>(a.states + ((size_t)(chunk0 + (t - g.s + s0) / SSM_CHUNK<N>) * a.D + c) * N + p4) = run;
+      float y[4];
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) {
         const float2 du = step[s0 + s][ch];
         const f4 b = *reinterpret_cast<const f4 *>(&sB[s0 + s][p4]), cv = *reinterpret_cast<const f4 *>(&sC[s0 + s][p4]);
-        float y = 0.f;
+        y[s & 3] = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float e = TW > 1 ? dec[s][j] : __builtin_amdgcn_exp2f(du.x * A2[j]);
           run[j] = fmaf(e, run[j], du.y * b[j]);
-          y = fmaf(cv[j], run[j], y);
+          y[s & 3] = fmaf(cv[j], run[j], y[s & 3]);
         }
-        y = lane_sum<L::P>(y);
-        if (p4 == 0) step[s0 + s][ch].x = y;
+        if constexpr (L::P == 4) {
+          if ((s & 3) == 3) step[s0 + s - 3 + p4 / 4][ch].x = quad_sums(y, p4 / 4);
+        } else {
+          const float sum = lane_sum<L::P>(y[s & 3]);
+          if (p4 == 0) step[s0 + s][ch].x = sum;
+        }
       }
       if constexpr (TW == 1) h = run;
     }

@@ -66,18 +66,25 @@ template <int V> __device__ __forceinline__ void store_few(__bf16 *p, const floa
   } else *p = (__bf16)v[0];
 }
 
-// softplus(v) = max(v, 0) + ln(1 + e), e = e^-|v| in (0, 1]; ln(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3, by
-// its series to s^15 (the next term is 2^-28 of the result): relative precision however small e is.
+// softplus(v) = max(v, 0) + ln(1 + e), e = e^-|v| in (0, 1]; ln(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3, and
+// atanh(s) = s + s q p(q), q = s^2, with p the cubic that interpolates 1/3 + q/5 + q^2/7 + .. at the Chebyshev nodes of
+// [0, 1/9] (off by 2^-25.8 of the logarithm): relative precision however small e is.
 __device__ __forceinline__ float softplus(float v) {
   const float e = __builtin_amdgcn_exp2f(-fabsf(v) * SSM_LOG2E);
   const float s = e * __builtin_amdgcn_rcpf(2.f + e), q = s * s;
-  float p = fmaf(q, 1.f / 15.f, 1.f / 13.f);
-  p = fmaf(p, q, 1.f / 11.f);
-  p = fmaf(p, q, 1.f / 9.f);
-  p = fmaf(p, q, 1.f / 7.f);
-  p = fmaf(p, q, 1.f / 5.f);
-  p = fmaf(p, q, 1.f / 3.f);
+  float p = fmaf(q, 0.13425749f, 0.141183099f);
+  p = fmaf(p, q, 0.200037803f);
+  p = fmaf(p, q, 0.333333202f);
   return fmaxf(v, 0.f) + 2.f * fmaf(p * q, s, s);
+}
+
+// The sums over a channel's 4 lanes of 4 values each: lane p gets that of y[p], by two exchanges that halve
+// the number of values (9 instructions, where 4 sums of their own take 8 and leave 4 stores).
+__device__ __forceinline__ float quad_sums(const float (&y)[4], int p) {
+  const bool odd = p & 1, high = p & 2;
+  const float u = (odd ? y[1] : y[0]) + dpp_mov<0xB1>(odd ? y[0] : y[1]);
+  const float v = (odd ? y[3] : y[2]) + dpp_mov<0xB1>(odd ? y[2] : y[3]);
+  return (high ? v : u) + dpp_mov<0x4E>(high ? u : v);
 }
 
 // A sequence's part that one workgroup runs over: tokens t0 .. t1 - 1 of sequence n, which begins at s
