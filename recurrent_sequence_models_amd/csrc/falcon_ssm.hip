@@ -8,25 +8,28 @@
 // workgroup that lie behind each other in time each compose their 16 steps first, h -> P h + H
 // with P = exp(A sum of delta), keeping the 64 decays of a lane in registers; then every wave
 // joins the maps before its own to the tile's first state and runs its steps again from there,
-// without an exponential.  So a workgroup has 4 times as many steps in flight as a plain recurrence
-// and pays 12 instructions for 4 states and a step where that pays 12 less an exchange of maps.
+// without an exponential.  So time gives 4 times the waves that the channels alone would, for 7
+// instructions a state and step (one of them the exponential) where a plain recurrence pays 5.
 //
 // Few long sequences: they are cut into segments, whose maps a pass of its own forms, and which then
 // run in parallel.
 //
-// Bound: the vector unit: per state and step one exponential and 6 multiplications and additions.
+// Bound: the vector unit: 41 instructions for 4 states and a step, with what a tile's loading, softplus, gate and joins
+// cost; busy 78 % of the time.  Measured, N = 16, bf16: 8 x 2048 x 1536 163 us (2.5e12 states a second; the bytes alone
+// would take 41 us); single tokens, 64 x 4096: 9 us (36 MB at 4.0 TB/s).
 #include "ssm_common.h"
 
 namespace falcon {
 namespace {
 
 constexpr int FWD_CH = 16;
-#ifndef SSM_FEW
-#define SSM_FEW 640
-#endif
-#ifndef SSM_WANT
-#define SSM_WANT 256
-#endif
+// Below this many workgroups, 8 waves of 8 steps each take a tile's 64 steps, instead of 4 of 16: more waves for what
+// there is, at twice the joins.  N = 16, bf16: 384 workgroups (4 x 4096 x 1536) 220 us, 257 with 4 waves; 512 (4 x 2048 x
+// 2048) 114 and 118; 768 (8 x 2048 x 1536) 186 and 163.
+constexpr int FEW_GROUPS = 640;
+// Sequences are cut where they make fewer than 256 workgroups, into 768 (1 x 16384 x 1536, 96 workgroups: 267 us with
+// the maps' pass, 311 cut for 512, 460 for 256); with 384 they are not (4 x 4096 x 1536: 220 us, 260 cut).
+int ssm_segment_fwd(const SeqMap &q, int D) { return ssm_segment(q, D, FWD_CH, 256, 768); }
 
 // MAPS: only the segment's map (end state from zero, sum of delta) is formed.
 template <typename T, int N, int TW, int STEPS, bool MAPS>
@@ -236,15 +239,16 @@ size_t align16(size_t n) { return (n + 15) / 16 * 16; }
 
 }  // namespace
 
-// Tokens of a segment: as many segments as give every compute unit two workgroups, where whole
-// sequences do not; a whole number of chunks.
-int ssm_segment(const SeqMap &q, int D) {
-  const int64_t groups = (D + FWD_CH - 1) / FWD_CH, want = SSM_WANT;
+// Tokens of a segment, a whole number of chunks.  Whole sequences, where those make `enough` workgroups (of `channels`
+// channels each); else as many segments as make `want`: forming their maps first costs half of a pass.
+int ssm_segment(const SeqMap &q, int D, int channels, int enough, int want) {
+  const int64_t groups = (D + channels - 1) / channels;
   int64_t len;
   if (q.cu) {
+    if (groups >= enough) return (q.T + SSM_ALIGN - 1) / SSM_ALIGN * SSM_ALIGN;
     len = ((int64_t)q.T * groups + want - 1) / want;
   } else {
-    const int64_t parts = want / (q.n * groups);
+    const int64_t parts = q.n * groups >= enough ? 1 : want / (q.n * groups);
     if (parts < 2) return (q.T + SSM_ALIGN - 1) / SSM_ALIGN * SSM_ALIGN;
     len = (q.T + parts - 1) / parts;
   }
@@ -258,13 +262,13 @@ int ssm_chunk(int N) { return 1024 / N; }
 
 bool ssm_fits(SeqMap seq, int D) {
   const int64_t groups = (D + FWD_CH - 1) / FWD_CH;
-  const int64_t seg = ssm_segment(seq, D);
+  const int64_t seg = ssm_segment_fwd(seq, D);
   const int64_t slots = seq.cu ? seq.T / seg + seq.n : (int64_t)seq.n * ((seq.T + seg - 1) / seg);
   return slots <= INT32_MAX - 8 && grid_fits(slots * (groups + 7) / 8 * 8 + 8, 1024);
 }
 
 size_t ssm_fwd_workspace(SeqMap seq, int D, int N) {
-  const int seg = ssm_segment(seq, D);
+  const int seg = ssm_segment_fwd(seq, D);
   if (!ssm_segmented(seq, seg)) return 0;
   const size_t slots = slots_of(seq, seg) + 1;
   return 2 * align16(slots * D * N * sizeof(float)) + align16(slots * D * sizeof(float));
@@ -292,9 +296,9 @@ template <typename T, int N, int TW, int STEPS> static hipError_t fwd(SsmArgs a,
 }
 
 template <typename T, int N> static hipError_t fwd(SsmArgs a, void *ws, hipStream_t s) {
-  a.seg = ssm_segment(a.seq, a.D);
+  a.seg = ssm_segment_fwd(a.seq, a.D);
   const int64_t groups = (a.D + FWD_CH - 1) / FWD_CH;
-  if (groups * slots_of(a.seq, a.seg) < SSM_FEW) return fwd<T, N, 128 / N, (N == 64 ? 16 : 8)>(a, ws, s);
+  if (groups * slots_of(a.seq, a.seg) < FEW_GROUPS) return fwd<T, N, 128 / N, (N == 64 ? 16 : 8)>(a, ws, s);
   return fwd<T, N, 64 / N, 16>(a, ws, s);
 }
 

@@ -16,7 +16,10 @@
 // number of lanes (16 instructions for 8 sums over 16 lanes), over the waves in LDS, and over
 // workgroups in a pass of their own, in order.
 //
-// Bound: the vector unit.
+// Bound: the vector unit: 120 instructions for 4 states and a step (67 in the way back, 27 in the maps of both
+// directions, 26 for what a tile's loading, gates and results cost).  A lane's decays and states of 16 steps take 132
+// registers, so a SIMD has two waves.  Measured, N = 16, bf16: 4 x 4096 x 1536 543 us (192 workgroups on 256 compute
+// units), and 18 us for dB and dC over the 48 groups of channels.
 #include "ssm_common.h"
 
 namespace falcon {
@@ -48,6 +51,9 @@ template <int P> __device__ __forceinline__ void channel_sums(const f4 &b, const
 
 constexpr int BWD_CH = 32;
 template <int N> using BwdTile = SsmTile<N, BWD_CH, 64 / N, 16>;
+// Sequences are cut where they make fewer than 128 workgroups, into 256 (2 x 2048 x 768: 92 us with the maps' pass, 104 cut
+// for 512; 1 x 16384 x 1536: 632 and 615).
+int segment_of(const SeqMap &q, int D) { return ssm_segment(q, D, BWD_CH, 128, 256); }
 
 // MAPS: only the segment's map (r at its start from zero behind its end, sum of delta) is formed.
 template <typename T, int N, bool MAPS> __global__ __launch_bounds__(BwdTile<N>::THR, MAPS ? 4 : 2) void ssm_bwd(SsmArgs a) {
@@ -346,7 +352,7 @@ size_t align16(size_t n) { return (n + 15) / 16 * 16; }
 
 struct Parts { size_t bc, A, D, map, sum, total; };
 Parts parts_of(const SeqMap &q, int D, int N) {
-  const int seg = ssm_segment(q, D);
+  const int seg = segment_of(q, D);
   const size_t groups = (D + BWD_CH - 1) / BWD_CH, slots = slots_of(q, seg);
   Parts p;
   p.bc = align16(groups * q.tokens() * 2 * N * sizeof(float));
@@ -372,7 +378,7 @@ template <typename T, int N> static hipError_t bwd(SsmArgs a, const SsmGrads &o,
   a.seg_map = reinterpret_cast<float *>(at += p.D);
   a.seg_state = reinterpret_cast<float *>(at += p.map);
   a.seg_sum = reinterpret_cast<float *>(at += p.map);
-  a.seg = ssm_segment(a.seq, a.D);
+  a.seg = segment_of(a.seq, a.D);
   const int groups = (a.D + BWD_CH - 1) / BWD_CH, slots = slots_of(a.seq, a.seg);
   const unsigned grid = (unsigned)ssm_grid(groups, slots);
   hipError_t e;
