@@ -11,7 +11,10 @@
 // last W - 1 inputs (backward: and the W unfinished gradients) in registers.  The W - 1 tokens next to
 // a run are read again, from the cache as a rule: the runs beside belong to the same workgroup.
 // In the backward pass d is formed again for the W - 1 tokens behind the run, rather than
-// exchanged.  Bound: HBM, x and y (backward: x, dy and dx) once.
+// exchanged.  Bound: HBM, x and y (backward: x, dy and dx) once; the backward's vector unit is half busy.
+// Measured, 4 x 4096 x 1536 bf16, 4 taps, silu: forward 25 us (101 MB at 4.0 TB/s), backward 41 us (151 MB at 3.7; 49
+// with 8 channels a thread, which leave two waves a SIMD) and 5 us to add the weights' gradients; 64 tokens x
+// 4096: 4.9 us.
 #include "block_kernels.h"
 #include "row_io.h"
 

@@ -11,7 +11,16 @@
 // kernel adds in order and finishes.  At most 64 tokens: W is what has to be read, so 16 of its rows
 // are a workgroup's, whose waves split k, without LDS tiles (8-bit operands widened to bf16 there).
 //
-// Bound: the matrix unit for many tokens, W's bytes for few.  Sums are fp32; a result is rounded once, at its end.
+// Bound: the matrix unit for many tokens, with LDS close behind (a wave's 128 x 64 takes 6 fragments for 8 products: 75 %
+// of what LDS gives at the unit's full rate, and the copies the rest), and the wait for copies that start one step
+// before their use; W's bytes for few tokens.  Measured, where a large library product reaches 1.2 to 1.34 PFLOP/s in
+// bf16 and 2.9 in e4m3:
+//   8192^3: bf16 850 us (1.29 PFLOP/s), e4m3 475 us (2.31)
+//   16384 x 2048 -> 4096 bf16, bias and silu: 244 us on one set of operands (1.13 PFLOP/s), 290 on three in turn
+//   16384 x 4096 -> 2048 e4m3, residual: 195 us (1.41 PFLOP/s); to fp32, widened: 316 us
+//   4096 x 2048 -> 2048 fp32: 280 us (123 TFLOP/s; a large fp32 product 146)
+//   16 x 2048 -> 4096 bf16: 7 us (16.8 MB at 2.4 TB/s: one wave's loads and the launch)
+// Sums are fp32; a result is rounded once, at its end.
 #include <type_traits>
 
 #include "attn_frag.h"
@@ -56,69 +65,95 @@ template <typename T, int ROWS, bool COLS> struct OperandTile {
   static constexpr int TR = COLS ? KE<T> : ROWS;          // rows in memory
   static constexpr int READS = COLS ? (sizeof(T) == 4 ? 8 : 2) : sizeof(T) == 2 || std::is_same_v<T, e4m3_wide> ? 1 : 2;   // of LDS, a fragment
   static constexpr int CHUNKS = TR * Ti::CPR;             // 16 bytes each
-  // the operand of a product over k block b, of rows row0 .. row0 + 31
-  static __device__ __forceinline__ Frag<T> frag(const uint4 *t, int row0, int b, int lane) {
-    if constexpr (!COLS) {
-      if constexpr (std::is_same_v<T, e4m3_wide>) {
-        const uint2 v = reinterpret_cast<const uint2 *>(t + Ti::place(row0 + (lane & 31), b))[lane >> 5];
-        return {widened(v.x, v.y)};
-      } else if constexpr (sizeof(T) == 1) {
-        const int row = row0 + (lane & 31), h = lane >> 5;
-        const uint4 lo = t[Ti::place(row, 4 * b + 2 * h)], hi = t[Ti::place(row, 4 * b + 2 * h + 1)];
-        return {int8v{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w}};
-      } else {
-        return Ti::rows(t, row0, b, lane);
-      }
+  // By rows: the LDS address of this lane's part of k block 0 of the 32 rows from row0, in a tile at `tile`.  Tiles are
+  // aligned to a row (128 bytes), so the swizzled chunk of another block differs in the address's low bits alone.
+  static __device__ __forceinline__ unsigned start(unsigned tile, int row0, int lane) {
+    const int row = row0 + (lane & 31), h = lane >> 5;
+    constexpr bool HALF = std::is_same_v<T, e4m3_wide>;          // 8 bytes a lane: halves of one chunk
+    const int chunk = HALF ? 0 : sizeof(T) == 2 ? h : 2 * h;
+    return tile + row * KB + ((chunk ^ Ti::swizzle(row)) << 4) + (HALF ? 8 * h : 0);
+  }
+  template <typename V> static __device__ __forceinline__ V at(unsigned address) {
+    return *(__attribute__((address_space(3))) const V *)(size_t)address;
+  }
+  // The operand of a product over k block b, of the p-th 32 rows from `start`.
+  static __device__ __forceinline__ Frag<T> frag(unsigned start, int p, int b) {
+    const int down = p * 32 * KB;
+    if constexpr (std::is_same_v<T, e4m3_wide>) {
+      typedef unsigned u2 __attribute__((ext_vector_type(2)));
+      const u2 v = at<u2>((start ^ (b << 4)) + down);
+      return {widened(v[0], v[1])};
+    } else if constexpr (sizeof(T) == 2) {
+      return {at<bf8>((start ^ (b << 5)) + down)};
+    } else if constexpr (sizeof(T) == 1) {
+      const u4 lo = at<u4>((start ^ (b << 6)) + down), hi = at<u4>((start ^ (b << 6 | 16)) + down);
+      return {int8v{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]}};
     } else {
-      // slot (h, j) = k 8 h + j, as a read by rows has it
-      const int h = lane >> 5;
-      if constexpr (sizeof(T) == 2) {
-        const int j = lane & 15, col = row0 + (lane & 16) + 4 * (j & 3);
-        Frag<__bf16> f;
+      return {at<f4>((start ^ (b << 6)) + down), at<f4>((start ^ (b << 6 | 16)) + down)};
+    }
+  }
+  // By columns: the operand of a product over k block b, of columns row0 .. row0 + 31.
+  static __device__ __forceinline__ Frag<T> frag(const uint4 *t, int row0, int b, int lane) {
+    // slot (h, j) = k 8 h + j, as a read by rows has it
+    const int h = lane >> 5;
+    if constexpr (sizeof(T) == 2) {
+      const int j = lane & 15, col = row0 + (lane & 16) + 4 * (j & 3);
+      Frag<__bf16> f;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int row = 16 * b + 8 * h + 4 * k + (j >> 2);
-          const bf4 v = ldtr(reinterpret_cast<const __bf16 *>(t + Ti::place(row, col / 8)) + (col & 7));
+      for (int k = 0; k < 2; ++k) {
+        const int row = 16 * b + 8 * h + 4 * k + (j >> 2);
+        const bf4 v = ldtr(reinterpret_cast<const __bf16 *>(t + Ti::place(row, col / 8)) + (col & 7));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) f.v[4 * k + i] = v[i];
-        }
-        return f;
-      } else {
-        const int col = row0 + (lane & 31);
-        const float *p = reinterpret_cast<const float *>(t);
-        Frag<float> f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          f.lo[i] = p[4 * Ti::place(16 * b + 8 * h + i, col / 4) + (col & 3)];
-          f.hi[i] = p[4 * Ti::place(16 * b + 8 * h + 4 + i, col / 4) + (col & 3)];
-        }
-        return f;
+        for (int i = 0; i < 4; ++i) f.v[4 * k + i] = v[i];
       }
+      return f;
+    } else {
+      const int col = row0 + (lane & 31);
+      const float *p = reinterpret_cast<const float *>(t);
+      Frag<float> f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f.lo[i] = p[4 * Ti::place(16 * b + 8 * h + i, col / 4) + (col & 3)];
+        f.hi[i] = p[4 * Ti::place(16 * b + 8 * h + 4 + i, col / 4) + (col & 3)];
+      }
+      return f;
     }
   }
 };
 
-// One thread's share in copying an operand's tiles, of THR threads.
+// One thread's share in copying an operand's tiles, of THR threads: PER pieces of 16 bytes, PR rows of memory apart.
+// Where that is a multiple of the swizzle's period, the pieces' offsets differ by the same for every thread, so one
+// register holds them all, and (by rows) a second one those of the piece in which the operand's rows end.
 template <typename T, int ROWS, bool COLS, int THR> struct Copier {
   typedef OperandTile<T, ROWS, COLS> O;
-  static constexpr int PER = O::CHUNKS / THR;
-  static_assert(O::CHUNKS % THR == 0, "whole pieces");
+  static constexpr int PER = O::CHUNKS / THR, PR = THR / O::Ti::CPR, E = 16 / (int)sizeof(T);
+  static constexpr bool SAME = PR % 16 == 0;
+  static_assert(O::CHUNKS % THR == 0 && THR % O::Ti::CPR == 0, "whole pieces");
   const char *base;       // the operand's entry (row0, k = 0) or (k = 0, row0)
   int64_t ld;             // bytes between two rows of memory
-  unsigned off[PER];
+  unsigned off[SAME ? (COLS ? 1 : 2) : PER];
   int rows, K;            // rows there are from row0; entries of k
+  int full;               // by rows: pieces whose rows all exist
   __device__ __forceinline__ Copier(const void *p, int64_t lde, int row0, int all, int K_, int tid) {
     ld = lde * (int64_t)sizeof(T);
     rows = all - row0;
     K = K_;
+    full = rows / PR;
     base = static_cast<const char *>(p) + (COLS ? row0 * (int64_t)sizeof(T) : row0 * ld);
+    if constexpr (!SAME) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) off[i] = offset(i, tid, KE<T>);
+      for (int i = 0; i < PER; ++i) off[i] = offset(i, tid, KE<T>);
+    } else {
+      off[0] = offset(0, tid, KE<T>);
+      if constexpr (!COLS) {
+        const int row = tid / O::Ti::CPR, chunk = (tid % O::Ti::CPR) ^ O::Ti::swizzle(row);
+        off[1] = (unsigned)(min(row, max(rows - full * PR, 1) - 1) * ld) + chunk * 16;
+      }
+    }
   }
   // Where piece i lies, of a tile that has k entries: places without an entry read the last one.
   __device__ __forceinline__ unsigned offset(int i, int tid, int k) const {
     const int at = i * THR + tid, row = at / O::Ti::CPR, chunk = (at % O::Ti::CPR) ^ O::Ti::swizzle(row);
-    constexpr int E = 16 / (int)sizeof(T);
     if constexpr (COLS) {
       const int r = min(row, k - 1), c = min(chunk, (rows + E - 1) / E - 1);
       return (unsigned)(r * ld) + c * 16;
@@ -132,7 +167,17 @@ template <typename T, int ROWS, bool COLS, int THR> struct Copier {
   __device__ __forceinline__ void copy(unsigned to, int k0) const {
     const char *at = base + (COLS ? k0 * ld : k0 * (int64_t)sizeof(T));
 #pragma unroll
-    for (int i = 0; i < PER; ++i) copy_to_lds(at, off[i], to + i * THR * 16);
+    for (int i = 0; i < PER; ++i) {
+      if constexpr (!SAME) {
+        copy_to_lds(at, off[i], to + i * THR * 16);
+      } else if constexpr (COLS) {
+        copy_to_lds(at + i * (PR * ld), off[0], to + i * THR * 16);
+      } else {
+        // a piece behind the rows reads the first one again
+        const bool some = i * PR < rows, whole = i < full || (!some && full > 0);
+        copy_to_lds(some ? at + i * (PR * ld) : at, whole ? off[0] : off[1], to + i * THR * 16);
+      }
+    }
   }
   __device__ __forceinline__ void copy_last(unsigned to, int k0, int tid) const {
     const char *at = base + (COLS ? k0 * ld : k0 * (int64_t)sizeof(T));
@@ -143,7 +188,6 @@ template <typename T, int ROWS, bool COLS, int THR> struct Copier {
   // Zeros where a copied tile has no entries of k.  (Rows behind the last of an operand repeat it: their
   // results are not stored.)  This thread's own pieces, after copies_done().
   __device__ __forceinline__ void clear(uint4 *tile, int k0, int tid) const {
-    constexpr int E = 16 / (int)sizeof(T);
     const int k = K - k0;
     if (k >= KE<T>) return;
 #pragma unroll
@@ -215,7 +259,7 @@ __global__ __launch_bounds__(64 * WL * WR) void product(LinearArgs a) {
   constexpr int THR = 64 * WL * WR, FL = TL / WL / 32, FR = TR / WR / 32;
   typedef OperandTile<T, TL, LC> OL;
   typedef OperandTile<T, TR, RC> OR;
-  __shared__ __align__(16) uint4 lds[2 * (OL::CHUNKS + OR::CHUNKS)];
+  __shared__ __align__(128) uint4 lds[2 * (OL::CHUNKS + OR::CHUNKS)];
   uint4(*left)[OL::CHUNKS] = reinterpret_cast<uint4(*)[OL::CHUNKS]>(lds);
   uint4(*right)[OR::CHUNKS] = reinterpret_cast<uint4(*)[OR::CHUNKS]>(lds + 2 * OL::CHUNKS);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wl = wave % WL, wr = wave / WL;
@@ -236,49 +280,40 @@ __global__ __launch_bounds__(64 * WL * WR) void product(LinearArgs a) {
   for (int p = 0; p < FL; ++p)
 #pragma unroll
     for (int q = 0; q < FR; ++q) acc[p][q] = zero16();
-  // Fragments are read one block of k ahead, between the products, into the set that the products before last have
-  // used; a step's first ones right behind the barrier that hands its tiles over, among the last products of the
-  // step before.  (8-bit fragments of a large tile are too many for two sets, and widening them takes registers too.)
-  constexpr int NB = KE<T> / KM<T>, MF = FL * FR;
-  constexpr bool AHEAD = sizeof(T) > 1 || (std::is_same_v<T, e4m3> && MF <= 4);
+  // Fragments are read one block of k ahead: the right ones into a second set, a left one over the one whose
+  // products have just been issued.
+  constexpr int NB = KE<T> / KM<T>;
   static_assert(NB % 2 == 0, "a step begins with the same set");
-  Frag<T> fl[AHEAD ? 2 : 1][FL], fr[AHEAD ? 2 : 1][FR];
-  auto read = [&](int buffer, int b) __attribute__((always_inline)) {
-    const int set = AHEAD ? b & 1 : 0;
-#pragma unroll
-    for (int p = 0; p < FL; ++p) fl[set][p] = OL::frag(left[buffer], (wl * FL + p) * 32, b, lane);
-#pragma unroll
-    for (int q = 0; q < FR; ++q) fr[set][q] = OR::frag(right[buffer], (wr * FR + q) * 32, b, lane);
+  Frag<T> fl[FL], fr[2][FR];
+  unsigned start_l = 0, start_r = 0;
+  if constexpr (!LC) start_l = OL::start(lds_address(left), wl * FL * 32, lane);
+  if constexpr (!RC) start_r = OR::start(lds_address(right), wr * FR * 32, lane);
+  auto read_left = [&](int buffer, int b, int p) __attribute__((always_inline)) {
+    if constexpr (LC) fl[p] = OL::frag(left[buffer], (wl * FL + p) * 32, b, lane);
+    else fl[p] = OL::frag(start_l + buffer * (OL::CHUNKS * 16), p, b);
   };
-  auto multiply = [&](int b, auto half) __attribute__((always_inline)) {        // 0: all of a block's products, 1, 2: their first, second half
-    constexpr int from = half.value == 2 ? MF / 2 : 0, to = half.value == 1 ? MF / 2 : MF;
-    const int set = AHEAD ? b & 1 : 0;
+  auto read_right = [&](int buffer, int b) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = from; i < to; ++i) mma(acc[i / FR][i % FR], fl[set][i / FR], fr[set][i % FR]);
+    for (int q = 0; q < FR; ++q) {
+      if constexpr (RC) fr[b & 1][q] = OR::frag(right[buffer], (wr * FR + q) * 32, b, lane);
+      else fr[b & 1][q] = OR::frag(start_r + buffer * (OR::CHUNKS * 16), q, b);
+    }
   };
-  const std::integral_constant<int, 0> all;
-  const std::integral_constant<int, 1> first;
-  const std::integral_constant<int, 2> second;
-  auto blocks = [&](int now) __attribute__((always_inline)) {                   // all blocks of a step but the last one's products
+  auto multiply = [&](int b, int p) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < FR; ++q) mma(acc[p][q], fl[p], fr[b & 1][q]);
+  };
+  auto blocks = [&](int now) __attribute__((always_inline)) {   // all blocks of a step but the last one's products
 #pragma unroll
     for (int b = 0; b + 1 < NB; ++b) {
-      if constexpr (AHEAD) {
-        read(now, b + 1);
-        multiply(b, all);
-        // one product, then its share of the reads
-        constexpr int MI = MF * (sizeof(T) == 4 ? 8 : 1), RD = FL * OL::READS + FR * OR::READS, EACH = (RD + MI - 1) / MI;
+      read_right(now, b + 1);
 #pragma unroll
-        for (int i = 0; i < RD / EACH; ++i) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x100, EACH, 0);
-        }
-        __builtin_amdgcn_sched_group_barrier(0x008, MI - RD / EACH, 0);
-      } else {
-        read(now, b);
-        multiply(b, all);
+      for (int p = 0; p < FL; ++p) {
+        multiply(b, p);
+        read_left(now, b + 1, p);
+        __builtin_amdgcn_sched_barrier(0);   // as written: the compiler would collect the reads, and need a second set
       }
     }
-    if constexpr (!AHEAD) read(now, NB - 1);
   };
   const unsigned place = __builtin_amdgcn_readfirstlane(wave * 1024);
   const unsigned to_l = lds_address(left) + place, to_r = lds_address(right) + place;
@@ -301,25 +336,32 @@ __global__ __launch_bounds__(64 * WL * WR) void product(LinearArgs a) {
     }
     __syncthreads();
     if (s + 1 < s1) copy(s + 1, buffer ^ 1);
-    if constexpr (AHEAD) read(buffer, 0);
   };
   if (s0 < s1) {
     copy(s0, 0);
     arrive(s0, 0);
+    read_right(0, 0);
+#pragma unroll
+    for (int p = 0; p < FL; ++p) read_left(0, 0, p);
     int now = 0;
     for (int s = s0; s + 1 < s1; ++s, now ^= 1) {
       blocks(now);
-      if constexpr (AHEAD) {
-        multiply(NB - 1, first);
-        arrive(s + 1, now ^ 1);
-        multiply(NB - 1, second);
-      } else {
-        multiply(NB - 1, all);
-        arrive(s + 1, now ^ 1);
+#pragma unroll
+      for (int p = 0; p < FL / 2; ++p) multiply(NB - 1, p);
+      arrive(s + 1, now ^ 1);
+      read_right(now ^ 1, 0);
+#pragma unroll
+      for (int p = 0; p < FL / 2; ++p) read_left(now ^ 1, 0, p);
+#pragma unroll
+      for (int p = FL / 2; p < FL; ++p) {
+        multiply(NB - 1, p);
+        read_left(now ^ 1, 0, p);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
     blocks(now);
-    multiply(NB - 1, all);
+#pragma unroll
+    for (int p = 0; p < FL; ++p) multiply(NB - 1, p);
   }
   // A wave's results leave through its part of LDS, 32 rows (j) of 32 FL entries at a time, so that rows are read and
   // written whole (4 entries a lane straight from the registers, 16 neighbouring bytes a row: 321 us for 287 at 16384 x
@@ -368,7 +410,7 @@ template <typename O> __global__ __launch_bounds__(256) void join(LinearArgs a) 
 // ---- Few tokens ----------------------------------------------------------------------
 // 16 rows of W a workgroup, 16 MT tokens; 8 waves take turns at 64 bytes of k.  A lane reads 16 bytes of a row:
 // the k's of its slots in a 16-wide product are the same ones for both operands.
-constexpr int FEW_WAVES = 8;
+constexpr int FEW_WAVES = 8, FEW_TOKENS = 64;
 template <typename T> __device__ __forceinline__ void mma16b(f4 &d, const u4 &a, const u4 &b) {
   if constexpr (sizeof(T) == 2) {
     d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, b), d, 0, 0, 0);
@@ -473,14 +515,14 @@ template <typename T> __global__ __launch_bounds__(256) void pre_gradient(Linear
 struct Plan { bool big; int splits; int64_t tiles; };
 
 // A compute unit holds one workgroup of 256 x 256 or two of 128 x 128; the larger tile reads less from LDS for a product
-// (16384 x 2048 -> 4096 bf16: 287 us, 299 with the smaller), the smaller one leaves less of the last round empty (16384 x
-// 768 -> 1536: 54.7 us, 58.7 with the larger; 2048 x 2048 -> 2048: 29, 51).  So rounds are counted, in tiles of 128 x
-// 128 a compute unit.  8-bit and fp32 operands take too many registers for the larger (16387 x 4096 -> 2048 e4m3:
-// 248 us, 469).  Where 128 x 128 tiles leave compute units idle, k is split, at 4 steps a split and 16 splits at most.
+// (16384 x 2048 -> 4096 bf16: 287 us, 299 with the smaller; 16384 x 4096 -> 2048 e4m3: 195, 227), the smaller one
+// leaves less of the last round empty (16384 x 768 -> 1536 bf16: 54.7 us, 58.7 with the larger; 2048 x 2048 -> 2048:
+// 29, 51).  So rounds are counted, in tiles of 128 x 128 a compute unit.  fp32 takes too many registers for the larger.
+// Where 128 x 128 tiles leave compute units idle, k is split, at 4 steps a split and 16 splits at most.
 Plan plan_of(int64_t I, int64_t J, int64_t K, int e) {
   Plan p;
   const int64_t large = ((I + 255) / 256) * ((J + 255) / 256), small = ((I + 127) / 128) * ((J + 127) / 128);
-  p.big = e == 2 && large >= 256 && (large + 255) / 256 * 4 * 20 <= (small + 511) / 512 * 2 * 21;
+  p.big = e < 4 && large >= 256 && (large + 255) / 256 * 4 * 20 <= (small + 511) / 512 * 2 * 21;
   p.tiles = p.big ? large : small;
   const int64_t steps = (K * e + KB - 1) / KB;
   p.splits = 1;
@@ -493,12 +535,15 @@ Plan plan_of(int64_t I, int64_t J, int64_t K, int e) {
   return p;
 }
 
+// The time of a plan's tiles, in rounds of the chip: 20 for tiles of 128 x 128 a compute unit.
+int64_t rounds_of(const Plan &p) { return p.big ? (p.tiles + 255) / 256 * 4 * 20 : (p.tiles * p.splits + 511) / 512 * 2 * 21; }
+
 template <typename T, typename O, bool LC, bool RC> hipError_t multiply(LinearArgs a, void *ws, hipStream_t s) {
   const Plan p = plan_of(a.I, a.J, a.K, sizeof(T));
   a.splits = p.splits;
   a.part = static_cast<float *>(ws);
   const unsigned grid = (unsigned)((p.tiles * p.splits + 7) / 8 * 8);
-  if constexpr (sizeof(T) == 2) {
+  if constexpr (sizeof(T) < 4) {
     if (p.big) hipLaunchKernelGGL((product<T, O, LC, RC, 256, 256, 2, 4>), dim3(grid), dim3(512), 0, s, a);
   }
   if (!p.big) hipLaunchKernelGGL((product<T, O, LC, RC, 128, 128, 2, 2>), dim3(grid), dim3(256), 0, s, a);
@@ -509,17 +554,36 @@ template <typename T, typename O, bool LC, bool RC> hipError_t multiply(LinearAr
   return hipGetLastError();
 }
 
-template <typename T, typename O> hipError_t fwd(const LinearArgs &a, void *ws, hipStream_t s) {
-  if constexpr (sizeof(T) == 1 && sizeof(O) == 4) {
-    if (a.J > 64) return multiply<e4m3_wide, O, false, false>(a, ws, s);
-  } else {
-    if (a.J > 64) return multiply<T, O, false, false>(a, ws, s);
-  }
+template <typename T, typename O> hipError_t few_tokens(const LinearArgs &a, hipStream_t s) {
   const dim3 grid((a.I + 15) / 16);
   if (a.J <= 16) hipLaunchKernelGGL((few<T, O, 1>), grid, dim3(64 * FEW_WAVES), 0, s, a);
   else if (a.J <= 32) hipLaunchKernelGGL((few<T, O, 2>), grid, dim3(64 * FEW_WAVES), 0, s, a);
   else hipLaunchKernelGGL((few<T, O, 4>), grid, dim3(64 * FEW_WAVES), 0, s, a);
   return hipGetLastError();
+}
+
+// Tokens that a pass of their own takes: up to 64 behind the last whole tile of 256, where that saves the others a
+// round (16387 x 4096 -> 2048 e4m3: 257 us as one pass).
+int tokens_apart(int64_t I, int64_t J, int64_t K, int e) {
+  const int rest = (int)(J % 256);
+  if (!rest || rest > FEW_TOKENS || J < 512 || K < 512) return 0;
+  return rounds_of(plan_of(I, J - rest, K, e)) < rounds_of(plan_of(I, J, K, e)) ? rest : 0;
+}
+
+template <typename T, typename O> hipError_t fwd(LinearArgs a, void *ws, hipStream_t s) {
+  typedef std::conditional_t<sizeof(T) == 1 && sizeof(O) == 4, e4m3_wide, T> Tiled;
+  if (a.J <= FEW_TOKENS) return few_tokens<T, O>(a, s);
+  const int rest = tokens_apart(a.I, a.J, a.K, sizeof(T)), most = a.J - rest;
+  a.J = most;
+  const hipError_t e = multiply<Tiled, O, false, false>(a, ws, s);
+  if (e != hipSuccess || !rest) return e;
+  a.J = rest;
+  a.right = static_cast<const T *>(a.right) + most * a.ldr;
+  a.out = static_cast<O *>(a.out) + most * a.ldo;
+  if (a.pre) a.pre += (size_t)most * a.I;
+  if (a.residual) a.residual = static_cast<const O *>(a.residual) + (size_t)most * a.I;
+  if (a.scale_r) a.scale_r += most;
+  return few_tokens<T, O>(a, s);
 }
 
 size_t align16(size_t n) { return (n + 15) / 16 * 16; }
@@ -542,7 +606,7 @@ bool linear_fits(int e, int64_t tokens, int64_t in, int64_t out) {
 }
 
 size_t linear_fwd_workspace(int e, int64_t tokens, int64_t in, int64_t out) {
-  return tokens > 64 ? part_bytes(out, tokens, in, e) : 0;
+  return tokens > FEW_TOKENS ? part_bytes(out, tokens - tokens_apart(out, tokens, in, e), in, e) : 0;
 }
 
 size_t linear_bwd_workspace(int e, bool act, int64_t tokens, int64_t in, int64_t out) {
