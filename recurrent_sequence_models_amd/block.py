@@ -59,6 +59,12 @@ def _rows(name, t, dtype, dev, shape=None):
     return Heads(t.data_ptr(), step)
 
 
+def _like(x):
+    """A new dense tensor of x's type and shape (by the quick way where x is dense)."""
+    import torch
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(tuple(x.shape))
+
+
 def _maybe(name, t, dtype, shape, dev):
     if t is not None:
         _check(name, t, dtype, shape, dev)
@@ -94,7 +100,7 @@ def _norm_fwd(x, weight, residual, norm, eps, quantize, out, scale, stream_out, 
     with _on(dev, stream):
         ydt = _f8() if quantize else x.dtype
         if out is None:
-            out = torch.empty(x.shape, dtype=ydt, device=dev)
+            out = torch.empty_like(x, dtype=ydt)
         else:
             _check("y", out, ydt, x.shape, dev)
         if residual is None:
@@ -209,7 +215,7 @@ def causal_conv(x, weight, *, bias=None, activation=None, cu_seqlens=None, init=
     _maybe("init", init, x.dtype, states, dev)
     with _on(dev, stream):
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            out = _like(x)
         else:
             _check("y", out, x.dtype, x.shape, dev)
         final = x.new_empty(states) if final is True else None if final is False else final
@@ -235,7 +241,7 @@ def causal_conv_bwd(x, weight, dy, *, bias=None, activation=None, cu_seqlens=Non
     _maybe("d_final", d_final, x.dtype, states, dev)
     with _on(dev, stream):
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            out = _like(x)
         hdx = _rows("dx", out, x.dtype, dev, x.shape)
         d_init = x.new_empty(states) if d_init is True else None if d_init is False else d_init
         _maybe("d_init", d_init, x.dtype, states, dev)
@@ -265,7 +271,7 @@ def causal_conv_step(x, weight, state, *, bias=None, activation=None, state_out=
         _check(name, t, x.dtype, (B, taps - 1, D), dev)
     with _on(dev, stream):
         if out is None:
-            out = torch.empty((B, D), dtype=x.dtype, device=dev)
+            out = _like(x)
         else:
             _check("y", out, x.dtype, x.shape, dev)
         shape, _ = _conv_plan(dt, B, 1, D, taps, _activation(activation), False)
@@ -326,7 +332,7 @@ def selective_scan(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, softplus=Tru
     _maybe("init", init, torch.float32, (n, width, N), dev)
     with _on(dev, stream):
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            out = _like(x)
         else:
             _check("y", out, x.dtype, x.shape, dev)
         final = x.new_empty((n, width, N), dtype=torch.float32) if final is True else None if final is False else final
@@ -363,7 +369,7 @@ def selective_scan_bwd(x, dt, A, B, C, dy, chunk_states, *, D=None, z=None, dt_b
     with _on(dev, stream):
         like = dict(dx=x, ddt=dt, dB=B, dC=C, dz=z)
         if out is None:
-            out = {k: torch.empty(t.shape, dtype=x.dtype, device=dev) for k, t in like.items() if t is not None}
+            out = {k: _like(t) for k, t in like.items() if t is not None}
         rows = {k: _NO_ROWS if t is None else _rows(k, out[k], x.dtype, dev, t.shape) for k, t in like.items()}
         d_init = x.new_empty(states, dtype=torch.float32) if d_init is True else None if d_init is False else d_init
         _maybe("d_init", d_init, torch.float32, states, dev)
@@ -394,7 +400,7 @@ def selective_scan_step(x, dt, A, B, C, state, *, D=None, z=None, dt_bias=None, 
         _check(name, t, torch.float32, (n, width, N), dev)
     with _on(dev, stream):
         if out is None:
-            out = torch.empty((n, width), dtype=x.dtype, device=dev)
+            out = _like(x)
         else:
             _check("y", out, x.dtype, x.shape, dev)
         shape, *_ = _ssm_plan(kind, n, 1, width, N, 1 if softplus else 0, False)
@@ -458,10 +464,10 @@ def linear(x, weight, *, bias=None, activation=None, residual=None, x_scale=None
         _check("weight_scale", weight_scale, torch.float32, (N,), dev)
     with _on(dev, stream):
         if out is None:
-            out = torch.empty(full, dtype=odt, device=dev)
+            out = x.new_empty(tuple(full), dtype=odt)
         else:
             _check("y", out, odt, full, dev)
-        keep = torch.empty(full, dtype=torch.float32, device=dev) if pre else None
+        keep = x.new_empty(tuple(full), dtype=torch.float32) if pre else None
         ws, nbytes = _workspace(need, workspace, dev)
         _done(lib().falcon_linear_fwd(shape, hx, _p(weight), _p(x_scale), _p(weight_scale), _p(bias), _p(residual), _p(out),
                                       _p(keep), _p(ws), nbytes, _current(dev)), "falcon_linear_fwd")
@@ -488,7 +494,7 @@ def linear_bwd(x, weight, dy, *, pre=None, activation=None, bias=False, dx=True,
         raise ValueError("pre: needed with an activation")
     _maybe("pre", pre, torch.float32, lead + (N,), dev)
     with _on(dev, stream):
-        dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if dx is True else None if dx is False else dx
+        dx = _like(x) if dx is True else None if dx is False else dx
         hdx = _NO_ROWS if dx is None else _rows("dx", dx, x.dtype, dev, x.shape)
         dweight = torch.empty_like(weight) if dweight is True else None if dweight is False else dweight
         _maybe("dweight", dweight, x.dtype, (N, K), dev)
