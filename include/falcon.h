@@ -515,7 +515,9 @@ int falcon_attn_bwd(const falcon_attn_shape_t *shape, const int32_t *cu_q, const
  * selective state-space scan.  Conventions as for the operators around the mixer
  * (packed sequences, gradients' types, determinism, workspaces, refusals).
  * Arrays are dense unless given as falcon_heads_t, with one head of the array's
- * width: then tokens may be further apart, as in a view of a wider projection. */
+ * width: then tokens may be further apart, as in a view of a wider projection.
+ * Outputs must not overlap inputs, but where an entry point allows it; the same pointer is
+ * FALCON_ERR_INVALID_ARG where that would be a race. */
 
 typedef enum { FALCON_ACT_NONE = 0, FALCON_ACT_SILU = 1, FALCON_ACT_GELU = 2 } falcon_activation_t;
 /* silu(p) = p / (1 + e^-p);  gelu(p) = p (1 + erf(p / sqrt 2)) / 2 */

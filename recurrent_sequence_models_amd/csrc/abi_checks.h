@@ -25,6 +25,9 @@ inline int check_workspace(const void *ws, size_t have, size_t want) {
   return maybe(ws, 16);
 }
 
+// An output that is one of the inputs where others read those late.  (Partial overlaps are the caller's to avoid.)
+inline int distinct(const void *out, const void *in) { return out && out == in ? FALCON_ERR_INVALID_ARG : FALCON_OK; }
+
 // [tokens, width] of entries of `e` bytes at a pointer with a token stride.
 inline int check_rows(const void *p, int64_t stride, int64_t tokens, int64_t width, int e) {
   if (need(p, 16) != FALCON_OK || stride < width || stride > INT64_MAX / 16 / tokens || (stride * e) % 16 != 0)

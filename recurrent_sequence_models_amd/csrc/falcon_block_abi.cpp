@@ -149,6 +149,8 @@ int falcon_conv_fwd(const falcon_conv_shape_t *s, const int32_t *cu, falcon_head
   FALCON_TRY(maybe(init, 16));
   FALCON_TRY(maybe(final_state, 16));
   FALCON_TRY(need(y, 16));
+  FALCON_TRY(distinct(final_state, init));
+  FALCON_TRY(distinct(y, x.data));
   falcon::ConvArgs a = conv_args(s, cu, x, w, bias);
   a.init = init;
   a.final_state = final_state;
@@ -175,6 +177,9 @@ int falcon_conv_bwd(const falcon_conv_shape_t *s, const int32_t *cu, falcon_head
   FALCON_TRY(maybe(dw, 4));
   FALCON_TRY(maybe(db, 4));
   FALCON_TRY(maybe(d_init, 16));
+  FALCON_TRY(distinct(d_init, d_final));
+  FALCON_TRY(distinct(dx.data, x.data));
+  FALCON_TRY(distinct(dx.data, d_y));
   if (dw || db) FALCON_TRY(check_workspace(ws, ws_bytes, falcon_conv_bwd_workspace(s, cu != nullptr)));
   falcon::ConvArgs a = conv_args(s, cu, x, w, bias);
   a.init = init;
@@ -281,6 +286,7 @@ int falcon_ssm_fwd(const falcon_ssm_shape_t *s, const int32_t *cu, falcon_heads_
   FALCON_TRY(maybe(final_state, 16));
   FALCON_TRY(need(y, 16));
   FALCON_TRY(maybe(chunk_states, 16));
+  FALCON_TRY(distinct(final_state, init));
   FALCON_TRY(check_workspace(ws, ws_bytes, falcon_ssm_fwd_workspace(s, cu != nullptr)));
   falcon::SsmArgs a = ssm_args(s, cu, x, dt, A, B, C, D, z, bias);
   a.init = init;
@@ -325,6 +331,7 @@ int falcon_ssm_bwd(const falcon_ssm_shape_t *s, const int32_t *cu, falcon_heads_
   FALCON_TRY(maybe(dD, 4));
   FALCON_TRY(maybe(ddt_bias, 4));
   FALCON_TRY(maybe(d_init, 16));
+  FALCON_TRY(distinct(d_init, d_final));
   FALCON_TRY(check_workspace(ws, ws_bytes, falcon_ssm_bwd_workspace(s, cu != nullptr)));
   falcon::SsmArgs a = ssm_args(s, cu, x, dt, A, B, C, D, z, bias);
   a.states = const_cast<float *>(chunk_states);
@@ -400,7 +407,8 @@ int falcon_linear_fwd(const falcon_linear_shape_t *s, falcon_heads_t x, const vo
   FALCON_TRY(maybe(residual, 16));
   FALCON_TRY(need(y, 16));
   FALCON_TRY(maybe(pre, 16));
-  if (pre && ((const void *)pre == y || (const void *)pre == residual)) return FALCON_ERR_INVALID_ARG;
+  for (const void *in : {x.data, (const void *)pre}) FALCON_TRY(distinct(y, in));
+  FALCON_TRY(distinct(pre, residual));
   FALCON_TRY(check_workspace(ws, ws_bytes, falcon_linear_fwd_workspace(s)));
   falcon::LinearArgs a{};
   a.left = weight; a.ldl = s->in;
@@ -434,6 +442,9 @@ int falcon_linear_bwd(const falcon_linear_shape_t *s, falcon_heads_t x, const vo
   if (dx.data) FALCON_TRY(check_rows(dx.data, dx.token_stride, s->tokens, s->in, e));
   FALCON_TRY(maybe(dweight, 16));
   FALCON_TRY(maybe(dbias, 4));
+  FALCON_TRY(distinct(dx.data, d_y.data));
+  FALCON_TRY(distinct(dx.data, x.data));
+  FALCON_TRY(distinct(dweight, weight));
   FALCON_TRY(check_workspace(ws, ws_bytes, falcon_linear_bwd_workspace(s)));
   falcon::LinearGrads g{};
   g.x = x.data; g.ldx = x.token_stride;

@@ -10,6 +10,8 @@ import pytest
 from recurrent_sequence_models_amd import falcon as F
 from test_layer_abi import INVALID, UNSUPPORTED, WORKSPACE, P, cpu_only
 
+Q = 2 * P      # another array
+
 ref = ctypes.byref
 BIG = 1 << 62
 
@@ -22,7 +24,7 @@ def shape(kind, defaults):
     return make
 
 
-def H(p=P, stride=64):
+def H(p=Q, stride=64):
     return F.Heads(p, stride)
 
 
@@ -72,7 +74,7 @@ def conv(s, cu=None, x=H(), w=P, b=P, init=None, fin=None, y=P):
     return F.lib().falcon_conv_fwd(ref(s) if s is not None else None, cu, x, w, b, init, fin, y, None)
 
 
-def conv_bwd(s, cu=None, x=H(), w=P, b=P, init=None, dy=P, df=None, dx=H(), dw=P, db=P, di=None, ws=P, n=BIG):
+def conv_bwd(s, cu=None, x=H(), w=P, b=P, init=None, dy=P, df=None, dx=H(3 * P), dw=P, db=P, di=None, ws=P, n=BIG):
     return F.lib().falcon_conv_bwd(ref(s), cu, x, w, b, init, dy, df, dx, dw, db, di, ws, n, None)
 
 
@@ -98,10 +100,10 @@ def test_conv_refusals():
     for kw in (dict(x=H(None)), dict(x=H(P + 8)), dict(x=H(P, 56)), dict(x=H(P, 65)), dict(x=H(P, 1 << 62)), dict(w=None), dict(w=P + 2),
                dict(b=P + 2), dict(init=P + 8), dict(cu=P + 2)):
         assert conv(s, **kw) == INVALID and conv_bwd(s, **kw) == INVALID, kw
-    for kw in (dict(fin=P + 8), dict(y=None), dict(y=P + 8)):
+    for kw in (dict(fin=P + 8), dict(y=None), dict(y=P + 8), dict(init=P, fin=P), dict(y=Q)):
         assert conv(s, **kw) == INVALID, kw
     for kw in (dict(dy=None), dict(df=P + 4), dict(dx=H(None)), dict(dx=H(P, 60)), dict(dw=P + 2), dict(db=P + 2), dict(di=P + 8),
-               dict(ws=P + 8)):
+               dict(ws=P + 8), dict(df=P, di=P), dict(dx=H(Q)), dict(dx=H(P))):
         assert conv_bwd(s, **kw) == INVALID, kw
     for kw in (dict(x=H(None)), dict(w=None), dict(st=None), dict(so=None), dict(so=P + 8), dict(y=None)):
         assert conv_step(s, **kw) == INVALID, kw
@@ -149,10 +151,10 @@ def test_ssm_refusals():
     for name in ("x", "dt", "B", "C", "z"):                         # 2^24 bytes between tokens
         kw = {name: H(P, (1 << 23) + 8)}
         assert ssm(s, **kw) == UNSUPPORTED and ssm_bwd(s, **kw) == UNSUPPORTED and ssm_step(s, **kw) == UNSUPPORTED, kw
-    for kw in (dict(cu=P + 2), dict(init=P + 8), dict(fin=P + 4), dict(y=None), dict(cs=P + 8)):
+    for kw in (dict(cu=P + 2), dict(init=P + 8), dict(fin=P + 4), dict(y=None), dict(cs=P + 8), dict(init=P, fin=P)):
         assert ssm(s, **kw) == INVALID, kw
     for kw in (dict(cu=P + 2), dict(cs=None), dict(dy=None), dict(df=P + 4), dict(dx=H(None)), dict(ddt=H(P, 8)), dict(dA=None), dict(dB=H(None)),
-               dict(dC=H(P, 9)), dict(dD=P + 2), dict(dz=H(None)), dict(db=P + 2), dict(di=P + 8), dict(ws=P + 8)):
+               dict(dC=H(P, 9)), dict(dD=P + 2), dict(dz=H(None)), dict(db=P + 2), dict(di=P + 8), dict(ws=P + 8), dict(df=P, di=P)):
         assert ssm_bwd(s, **kw) == INVALID, kw
     for kw in (dict(st=None), dict(so=P + 4), dict(y=None)):
         assert ssm_step(s, **kw) == INVALID, kw
@@ -181,7 +183,7 @@ def linear(s, x=H(), w=P, sx=None, sw=None, b=P, r=None, y=P, pre=None, ws=P, n=
     return F.lib().falcon_linear_fwd(ref(s) if s is not None else None, x, w, sx, sw, b, r, y, pre, ws, n, None)
 
 
-def linear_bwd(s, x=H(), w=P, pre=P, dy=H(), dx=H(), dw=P, db=P, ws=P, n=BIG):
+def linear_bwd(s, x=H(), w=P, pre=P, dy=H(), dx=H(3 * P), dw=Q, db=P, ws=P, n=BIG):
     return F.lib().falcon_linear_bwd(ref(s), x, w, pre, dy, dx, dw, db, ws, n, None)
 
 
@@ -199,7 +201,8 @@ def test_linear_refusals():
     assert linear(None) == INVALID
     s = linear_shape()
     for kw in (dict(x=H(None)), dict(x=H(P, 56)), dict(x=H(P, 65)), dict(w=None), dict(w=P + 8), dict(sx=P, sw=P), dict(sx=P), dict(b=P + 2),
-               dict(r=P + 8), dict(y=None), dict(y=P + 8), dict(pre=P + 4), dict(pre=P)):
+               dict(r=P + 8), dict(y=None), dict(y=P + 8), dict(pre=P + 4), dict(pre=P),
+               dict(y=Q), dict(r=Q, pre=Q)):
         assert linear(s, **kw) == INVALID, kw
     assert linear(s, x=H(P, (1 << 22) + 8)) == UNSUPPORTED          # 2^23 bytes between tokens
     q = linear_shape(dtype=2)
@@ -207,14 +210,14 @@ def test_linear_refusals():
         assert linear(q, **kw) == INVALID, kw
     assert linear_bwd(q) == UNSUPPORTED and L.falcon_linear_bwd_workspace(ref(q)) == 0
     for kw in (dict(x=H(None)), dict(w=None), dict(pre=None), dict(pre=P + 8), dict(dy=H(None)), dict(dy=H(P, 8)), dict(dx=H(P, 8)),
-               dict(dw=P + 8), dict(db=P + 2), dict(ws=P + 8)):
+               dict(dw=P + 8), dict(db=P + 2), dict(ws=P + 8), dict(dx=H(Q)), dict(x=H(3 * P)), dict(dw=P)):
         assert linear_bwd(s, **kw) == INVALID, kw
     assert linear_bwd(s, dy=H(P, (1 << 22) + 8)) == UNSUPPORTED
     need = L.falcon_linear_bwd_workspace(ref(s))
     assert need > 0 and linear_bwd(s, n=need - 1) == WORKSPACE and linear_bwd(s, ws=None) == WORKSPACE
     mid = linear_shape(**{"tokens": 128, "in": 2048})
     need = L.falcon_linear_fwd_workspace(ref(mid))
-    assert need > 0 and linear(mid, x=H(P, 2048), n=need - 1) == WORKSPACE and linear(mid, x=H(P, 2048), ws=None) == WORKSPACE
+    assert need > 0 and linear(mid, x=H(Q, 2048), n=need - 1) == WORKSPACE and linear(mid, x=H(Q, 2048), ws=None) == WORKSPACE
 
 
 def test_linear_workspace():

@@ -280,8 +280,17 @@ def test_past_32_bits():
         t = big[k] = torch.zeros(1, T, a[k].shape[-1], dtype=torch.bfloat16, device="cuda")
         t[:, -last:] = a[k]
     opt = dict(D=a["D"], dt_bias=a["bias"])
-    y, final, _ = rsm.selective_scan(big["x"], big["dt"], a["A"], big["B"], big["C"], **opt)
-    z, end, _ = rsm.selective_scan(a["x"], a["dt"], a["A"], a["B"], a["C"], **opt)
+    args, tail = (big["x"], big["dt"], a["A"], big["B"], big["C"]), (a["x"], a["dt"], a["A"], a["B"], a["C"])
+    y, final, states = rsm.selective_scan(*args, chunk_states=True, **opt)
+    z, end, kept = rsm.selective_scan(*tail, chunk_states=True, **opt)
     assert not y[:, :-last].any()
     torch.testing.assert_close(y[:, -last:].float(), z.float(), rtol=2 ** -7, atol=1e-5)
     torch.testing.assert_close(final, end, rtol=1e-4, atol=1e-6)
+    dy = torch.zeros_like(y)
+    dy[:, -last:] = a["dy"]
+    g, h = rsm.selective_scan_bwd(*args, dy, states, **opt), rsm.selective_scan_bwd(*tail, a["dy"], kept, **opt)
+    for k in ("dx", "ddt", "dB", "dC"):
+        # sums over up to 8192 channels: two roundings of bf16 apart, relative to the sums' size
+        size = h[k].float().abs().mean()
+        assert (g[k][:, -last:].float() - h[k].float()).abs().max() <= 2 ** -7 * h[k].float().abs().max() + 1e-3 * size, k
+    torch.testing.assert_close(g["dA"], h["dA"], rtol=1e-4, atol=1e-4)
