@@ -604,9 +604,11 @@ int falcon_conv_step(const falcon_conv_shape_t *shape, falcon_heads_t x, const f
  * (softplus = 0: delta_t = dt_t + dt_bias):
  *   h_t = exp(delta_t A[d][n]) h_{t-1} + delta_t x_t B_t[n]
  *   y_t = (sum_n C_t[n] h_t[n] + D[d] x_t) silu(z_t)         (z NULL: no gate)
- * B_t and C_t are shared by the channels.  Token strides are at most 2^24 bytes.  A is finite; where delta_t A > 0 the state
- * grows, and its growth over 64 steps (where sequences are cut into segments, over a
- * segment) has to stay in fp32's range.  States, sums and delta are fp32. */
+ * B_t and C_t are shared by the channels.  Token strides are at most 2^24 bytes.  A is
+ * finite; where delta_t A > 0 the state grows, and its growth over 64 steps (where
+ * sequences are cut into segments, over a segment) has to stay in fp32's range.  States,
+ * sums and delta are fp32.  An infinity in B or C stays in its state n; gradients of that
+ * state may be NaN where the formula's are infinite. */
 typedef struct {
   int32_t dtype;     /* falcon_dtype_t of x, dt, B, C, z, y and their gradients: F32 or BF16 */
   int32_t batch;     /* sequences, >= 1 */

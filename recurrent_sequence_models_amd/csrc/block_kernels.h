@@ -64,6 +64,7 @@ struct ConvArgs {
   int D, silu, run;              // run: tokens of a thread
 };
 bool conv_fits(bool bf16, SeqMap seq, int D);
+bool conv_step_fits(bool bf16, int n, int D);
 size_t conv_bwd_workspace(bool bf16, int taps, SeqMap seq, int D);
 hipError_t launch_conv_fwd(bool bf16, int taps, ConvArgs a, hipStream_t s);
 hipError_t launch_conv_bwd(bool bf16, int taps, ConvArgs a, float *dw, float *db, void *ws, hipStream_t s);
@@ -94,6 +95,7 @@ int ssm_chunk(int N);                             // steps between the states th
 int ssm_segment(const SeqMap &seq, int D, int channels, int enough, int want);   // tokens of a segment
 bool ssm_segmented(const SeqMap &seq, int segment);   // whether a sequence has more than one (packed: may have)
 bool ssm_fits(SeqMap seq, int D);
+bool ssm_step_fits(int n, int D, int N);
 size_t ssm_fwd_workspace(SeqMap seq, int D, int N);
 hipError_t launch_ssm_fwd(bool bf16, int N, SsmArgs a, void *ws, hipStream_t s);
 size_t ssm_bwd_workspace(SeqMap seq, int D, int N);

@@ -47,6 +47,7 @@ int falcon_rms_norm(const falcon_norm_shape_t *s, const void *x, const void *res
   FALCON_TRY(need(y, 16));
   FALCON_TRY(q8 ? need(scale, 4) : maybe(scale, 4));
   if (residual && y == stream_out) return FALCON_ERR_INVALID_ARG;
+  if (q8 && (y == x || y == residual)) return FALCON_ERR_INVALID_ARG;     // rows of another length
   falcon::NormArgs a = norm_args(s, weight);
   a.x = x;
   a.residual = residual;
@@ -109,10 +110,7 @@ int check_conv(const falcon_conv_shape_t *s, bool packed, bool step) {
   if (s->activation == FALCON_ACT_GELU || s->taps < 2 || s->taps > 4) return FALCON_ERR_UNSUPPORTED;
   if (s->width % 8 != 0 || s->width > (1 << 20)) return FALCON_ERR_UNSUPPORTED;
   const bool bf16 = s->dtype == FALCON_BF16;
-  if (step) {
-    const int64_t threads = (int64_t)s->batch * s->width * esize(s->dtype) / 16;
-    return falcon::grid_fits((threads + 255) / 256, 256) ? FALCON_OK : FALCON_ERR_UNSUPPORTED;
-  }
+  if (step) return falcon::conv_step_fits(bf16, s->batch, s->width) ? FALCON_OK : FALCON_ERR_UNSUPPORTED;
   return falcon::conv_fits(bf16, seq_sizes(s->batch, s->seqlen, packed), s->width) ? FALCON_OK : FALCON_ERR_UNSUPPORTED;
 }
 
@@ -217,10 +215,7 @@ int check_ssm(const falcon_ssm_shape_t *s, bool packed, bool step) {
   FALCON_TRY(check_seq(s->batch, step ? 1 : s->seqlen, packed));
   if (s->state != 16 && s->state != 32 && s->state != 64) return FALCON_ERR_UNSUPPORTED;
   if (s->width % 8 != 0 || s->width > (1 << 20)) return FALCON_ERR_UNSUPPORTED;
-  if (step) {
-    const int64_t threads = (int64_t)s->batch * s->width * (s->state / 4);
-    return falcon::grid_fits((threads + 255) / 256, 256) ? FALCON_OK : FALCON_ERR_UNSUPPORTED;
-  }
+  if (step) return falcon::ssm_step_fits(s->batch, s->width, s->state) ? FALCON_OK : FALCON_ERR_UNSUPPORTED;
   return falcon::ssm_fits(seq_sizes(s->batch, s->seqlen, packed), s->width) ? FALCON_OK : FALCON_ERR_UNSUPPORTED;
 }
 
@@ -287,6 +282,7 @@ int falcon_ssm_fwd(const falcon_ssm_shape_t *s, const int32_t *cu, falcon_heads_
   FALCON_TRY(need(y, 16));
   FALCON_TRY(maybe(chunk_states, 16));
   FALCON_TRY(distinct(final_state, init));
+  for (const void *in : {B.data, C.data}) FALCON_TRY(distinct(y, in));
   FALCON_TRY(check_workspace(ws, ws_bytes, falcon_ssm_fwd_workspace(s, cu != nullptr)));
   falcon::SsmArgs a = ssm_args(s, cu, x, dt, A, B, C, D, z, bias);
   a.init = init;

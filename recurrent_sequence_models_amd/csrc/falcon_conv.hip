@@ -241,12 +241,14 @@ template <typename T, int W> __global__ __launch_bounds__(THR) void conv_bwd(Con
   }
 }
 
-template <typename T, int W> __global__ __launch_bounds__(THR) void conv_step(ConvArgs a) {
+// Workgroups of one wave (64 x 4096 make 512, of 256 threads 128: fewer than compute units); those of a sequence follow
+// each other.
+constexpr int STEP_THR = 64;
+__host__ __device__ inline int step_blocks(int D, int E) { return (D / E + STEP_THR - 1) / STEP_THR; }
+template <typename T, int W> __global__ __launch_bounds__(STEP_THR) void conv_step(ConvArgs a) {
   constexpr int E = PER16<T>;
-  const int per = a.D / E;
-  const int64_t i = (int64_t)blockIdx.x * THR + threadIdx.x;
-  const int n = (int)(i / per), c = (int)(i - (int64_t)n * per) * E;
-  if (n >= a.seq.n) return;
+  const int per = step_blocks(a.D, E), n = blockIdx.x / per, c = ((blockIdx.x - n * per) * STEP_THR + threadIdx.x) * E;
+  if (c >= a.D) return;
   Few<T, E> win[W - 1];
   Few<T, E> x;
   fetch(static_cast<const T *>(a.x) + (int64_t)n * a.ldx + c, x);
@@ -285,6 +287,8 @@ Shape shape_of(SeqMap seq, int D, bool bf16, bool back) {
 
 }  // namespace
 
+bool conv_step_fits(bool bf16, int n, int D) { return grid_fits((int64_t)n * step_blocks(D, bf16 ? 8 : 4), STEP_THR); }
+
 bool conv_fits(bool bf16, SeqMap seq, int D) {
   for (const bool back : {false, true}) {
     const dim3 g = shape_of(seq, D, bf16, back).grid;
@@ -297,19 +301,19 @@ size_t conv_bwd_workspace(bool bf16, int taps, SeqMap seq, int D) {
   return (size_t)shape_of(seq, D, bf16, true).grid.x * D * (taps + 1) * sizeof(float);
 }
 
-#define FALCON_CONV(KERNEL, GRID)                                                                             \
-  if (taps == 4 && bf16) hipLaunchKernelGGL((KERNEL<__bf16, 4>), GRID, dim3(THR), 0, s, a);                   \
-  else if (taps == 4) hipLaunchKernelGGL((KERNEL<float, 4>), GRID, dim3(THR), 0, s, a);                       \
-  else if (taps == 3 && bf16) hipLaunchKernelGGL((KERNEL<__bf16, 3>), GRID, dim3(THR), 0, s, a);              \
-  else if (taps == 3) hipLaunchKernelGGL((KERNEL<float, 3>), GRID, dim3(THR), 0, s, a);                       \
-  else if (taps == 2 && bf16) hipLaunchKernelGGL((KERNEL<__bf16, 2>), GRID, dim3(THR), 0, s, a);              \
-  else if (taps == 2) hipLaunchKernelGGL((KERNEL<float, 2>), GRID, dim3(THR), 0, s, a);                       \
+#define FALCON_CONV(KERNEL, GRID, THREADS)                                                                             \
+  if (taps == 4 && bf16) hipLaunchKernelGGL((KERNEL<__bf16, 4>), GRID, dim3(THREADS), 0, s, a);                   \
+  else if (taps == 4) hipLaunchKernelGGL((KERNEL<float, 4>), GRID, dim3(THREADS), 0, s, a);                       \
+  else if (taps == 3 && bf16) hipLaunchKernelGGL((KERNEL<__bf16, 3>), GRID, dim3(THREADS), 0, s, a);              \
+  else if (taps == 3) hipLaunchKernelGGL((KERNEL<float, 3>), GRID, dim3(THREADS), 0, s, a);                       \
+  else if (taps == 2 && bf16) hipLaunchKernelGGL((KERNEL<__bf16, 2>), GRID, dim3(THREADS), 0, s, a);              \
+  else if (taps == 2) hipLaunchKernelGGL((KERNEL<float, 2>), GRID, dim3(THREADS), 0, s, a);                       \
   else return hipErrorInvalidValue;
 
 hipError_t launch_conv_fwd(bool bf16, int taps, ConvArgs a, hipStream_t s) {
   const Shape p = shape_of(a.seq, a.D, bf16, false);
   a.run = p.run;
-  FALCON_CONV(conv_fwd, p.grid)
+  FALCON_CONV(conv_fwd, p.grid, THR)
   return hipGetLastError();
 }
 
@@ -317,16 +321,15 @@ hipError_t launch_conv_bwd(bool bf16, int taps, ConvArgs a, float *dw, float *db
   const Shape p = shape_of(a.seq, a.D, bf16, true);
   a.run = p.run;
   a.part = dw || db ? static_cast<float *>(ws) : nullptr;
-  FALCON_CONV(conv_bwd, p.grid)
+  FALCON_CONV(conv_bwd, p.grid, THR)
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.part) return e;
   return launch_column_sum(a.part, p.grid.x, (int64_t)a.D * (taps + 1), dw, (int64_t)a.D * taps, db, s);
 }
 
 hipError_t launch_conv_step(bool bf16, int taps, ConvArgs a, hipStream_t s) {
-  const int64_t threads = (int64_t)a.seq.n * (a.D / (bf16 ? 8 : 4));
-  const dim3 grid((unsigned)((threads + THR - 1) / THR));
-  FALCON_CONV(conv_step, grid)
+  const dim3 grid((unsigned)a.seq.n * step_blocks(a.D, bf16 ? 8 : 4));
+  FALCON_CONV(conv_step, grid, STEP_THR)
   return hipGetLastError();
 }
 #undef FALCON_CONV

@@ -95,9 +95,10 @@ __global__ __launch_bounds__((SsmTile<N, FWD_CH, TW, STEPS>::THR), (STEPS == 16 
       if (a.softplus) d = softplus(d);
       step[ls][lc + j] = valid ? float2{d, d * x[j]} : float2{0.f, 0.f};
     }
+    const bool there = t + bs < g.t1;             // and B = 0: the last token's may be infinite
 #pragma unroll
     for (int j = 0; j < BV; ++j) {
-      sB[bs][bn + j] = nB[j];
+      sB[bs][bn + j] = there ? nB[j] : 0.f;
       if constexpr (!MAPS) sC[bs][bn + j] = nC[j];
     }
     __syncthreads();
@@ -203,11 +204,14 @@ template <int N> __global__ __launch_bounds__(256) void ssm_chain(SsmArgs a) {
   }
 }
 
-template <typename T, int N> __global__ __launch_bounds__(256) void ssm_step(SsmArgs a) {
+// Workgroups of a sequence follow each other, so its number is the same in every lane.
+constexpr int STEP_THR = 256;
+template <int N> __host__ __device__ int step_blocks(int D) { return (D * (N / 4) + STEP_THR - 1) / STEP_THR; }
+template <typename T, int N> __global__ __launch_bounds__(STEP_THR) void ssm_step(SsmArgs a) {
   constexpr int P = N / 4;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, rows = (int64_t)a.seq.n * a.D;
-  const int64_t row = min(i / P, rows - 1);           // whole waves stay for the sum over lanes
-  const int n = (int)(row / a.D), c = (int)(row - (int64_t)n * a.D), p4 = (int)(i % P) * 4;
+  const int per = step_blocks<N>(a.D), n = blockIdx.x / per, i = (blockIdx.x - n * per) * STEP_THR + threadIdx.x;
+  const int c = min(i / P, a.D - 1), p4 = i % P * 4;    // whole waves stay for the sum over lanes
+  const int64_t row = (int64_t)n * a.D + c;
   const size_t at = (size_t)row * N + p4;
   const f4 h0 = *reinterpret_cast<const f4 *>(a.init + at);
   const f4 A = *reinterpret_cast<const f4 *>(a.A + (size_t)c * N + p4);
@@ -227,7 +231,7 @@ template <typename T, int N> __global__ __launch_bounds__(256) void ssm_step(Ssm
     y = fmaf(C[j], h[j], y);
   }
   y = lane_sum<P>(y);
-  if (i / P >= rows) return;
+  if (i / P >= a.D) return;
   *reinterpret_cast<f4 *>(a.final_state + at) = h;
   if (p4) return;
   if (a.skip) y = fmaf(a.skip[c], x[0], y);
@@ -259,6 +263,8 @@ int ssm_segment(const SeqMap &q, int D, int channels, int enough, int want) {
 bool ssm_segmented(const SeqMap &q, int seg) { return q.T > seg; }
 
 int ssm_chunk(int N) { return 1024 / N; }
+
+bool ssm_step_fits(int n, int D, int N) { return grid_fits((int64_t)n * (((int64_t)D * N / 4 + STEP_THR - 1) / STEP_THR), STEP_THR); }
 
 bool ssm_fits(SeqMap seq, int D) {
   const int64_t groups = (D + FWD_CH - 1) / FWD_CH;
@@ -310,12 +316,11 @@ hipError_t launch_ssm_fwd(bool bf16, int N, SsmArgs a, void *ws, hipStream_t s) 
 }
 
 hipError_t launch_ssm_step(bool bf16, int N, SsmArgs a, hipStream_t s) {
-  const int64_t threads = (int64_t)a.seq.n * a.D * (N / 4);
-  const dim3 grid((unsigned)((threads + 255) / 256));
 #define FALCON_STEP(N_)                                                                              \
   if (N == N_) {                                                                                     \
-    if (bf16) hipLaunchKernelGGL((ssm_step<__bf16, N_>), grid, dim3(256), 0, s, a);                  \
-    else hipLaunchKernelGGL((ssm_step<float, N_>), grid, dim3(256), 0, s, a);                        \
+    const dim3 grid((unsigned)a.seq.n * step_blocks<N_>(a.D));                                       \
+    if (bf16) hipLaunchKernelGGL((ssm_step<__bf16, N_>), grid, dim3(STEP_THR), 0, s, a);             \
+    else hipLaunchKernelGGL((ssm_step<float, N_>), grid, dim3(STEP_THR), 0, s, a);                   \
     return hipGetLastError();                                                                        \
   }
   FALCON_STEP(16)

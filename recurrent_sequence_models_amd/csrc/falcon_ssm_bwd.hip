@@ -134,10 +134,11 @@ template <typename T, int N, bool MAPS> __global__ __launch_bounds__(BwdTile<N>:
       }
       step[ls][lc + j] = valid ? f4{d[j], d[j] * x[j], gy[j], 0.f} : f4{0.f, 0.f, 0.f, 0.f};
     }
+    const bool there = t + bs < g.t1;            // and B = C = 0: the last token's may be infinite
 #pragma unroll
     for (int j = 0; j < BV; ++j) {
-      if (!MAPS) sBC[bs][0][bn + j] = nB[j];
-      sBC[bs][1][bn + j] = nC[j];
+      if (!MAPS) sBC[bs][0][bn + j] = there ? nB[j] : 0.f;
+      sBC[bs][1][bn + j] = there ? nC[j] : 0.f;
     }
     __syncthreads();
     if (t > g.t0) load(t - L::TS);

@@ -58,7 +58,9 @@ def test_norm_refusals():
     for kw in (dict(x=None), dict(x=P + 8), dict(res=P + 4), dict(w=P + 4), dict(so=P + 8), dict(y=None), dict(y=P + 2),
                dict(scale=P + 2), dict(res=P, so=2 * P, y=2 * P)):
         assert norm(s, **kw) == INVALID, kw
-    assert norm(norm_shape(out=2), scale=None) == INVALID
+    assert norm(norm_shape(out=2), y=Q, scale=None) == INVALID
+    for kw in (dict(y=P), dict(y=Q, res=Q)):                        # rows of another length
+        assert norm(norm_shape(out=2), **kw) == INVALID, kw
     for kw in (dict(st=None), dict(dy=None), dict(dx=None), dict(w=P + 4), dict(ds=P + 8), dict(dw=P + 2), dict(ws=P + 8)):
         assert norm_bwd(s, **kw) == INVALID, kw
     assert norm_bwd(norm_shape(norm=0)) == UNSUPPORTED
@@ -151,7 +153,7 @@ def test_ssm_refusals():
     for name in ("x", "dt", "B", "C", "z"):                         # 2^24 bytes between tokens
         kw = {name: H(P, (1 << 23) + 8)}
         assert ssm(s, **kw) == UNSUPPORTED and ssm_bwd(s, **kw) == UNSUPPORTED and ssm_step(s, **kw) == UNSUPPORTED, kw
-    for kw in (dict(cu=P + 2), dict(init=P + 8), dict(fin=P + 4), dict(y=None), dict(cs=P + 8), dict(init=P, fin=P)):
+    for kw in (dict(cu=P + 2), dict(init=P + 8), dict(fin=P + 4), dict(y=None), dict(cs=P + 8), dict(init=P, fin=P), dict(y=Q)):
         assert ssm(s, **kw) == INVALID, kw
     for kw in (dict(cu=P + 2), dict(cs=None), dict(dy=None), dict(df=P + 4), dict(dx=H(None)), dict(ddt=H(P, 8)), dict(dA=None), dict(dB=H(None)),
                dict(dC=H(P, 9)), dict(dD=P + 2), dict(dz=H(None)), dict(db=P + 2), dict(di=P + 8), dict(ws=P + 8), dict(df=P, di=P)):

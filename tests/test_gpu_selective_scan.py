@@ -294,3 +294,38 @@ def test_past_32_bits():
         size = h[k].float().abs().mean()
         assert (g[k][:, -last:].float() - h[k].float()).abs().max() <= 2 ** -7 * h[k].float().abs().max() + 1e-3 * size, k
     torch.testing.assert_close(g["dA"], h["dA"], rtol=1e-4, atol=1e-4)
+
+
+@pytest.mark.parametrize("N", [16, 64])
+@pytest.mark.parametrize("T", [37, 600])
+def test_infinite_last_token(T, N):
+    """An infinity of a sequence's last token stays an infinity, and in its own state (backward too), where a tile ends
+    behind it."""
+    import torch
+    import recurrent_sequence_models_amd as rsm
+    a = inputs(70, (2, T), 2, 40, N, "fp32", gate=False, extras=False)
+    a = {k: v if v is None or k == "A" else v.abs() for k, v in a.items()}
+    at, rest = 3, [n for n in range(N) if n != 3]
+
+    def run(**change):
+        b = {**a, **change}
+        x = [b[k] for k in ("x", "dt", "A", "B", "C")]
+        y, final, states = rsm.selective_scan(*x, init=b["init"], chunk_states=True)
+        return y, final, rsm.selective_scan_bwd(*x, b["dy"], states, init=b["init"], d_final=b["d_final"])
+
+    inf = {k: a[k].clone() for k in ("B", "C")}
+    for v in inf.values():
+        v[:, -1, at] = float("inf")
+    y, final, g = run()
+    yb, fb, gb = run(B=inf["B"])
+    assert torch.equal(yb[:, :-1], y[:, :-1]) and torch.isposinf(yb[:, -1]).all()
+    assert torch.equal(fb[..., rest], final[..., rest]) and torch.isposinf(fb[..., at]).all()
+    for k in ("dB", "d_init"):
+        assert torch.equal(gb[k], g[k]), k
+    for k in ("dA", "dC"):
+        assert torch.equal(gb[k][..., rest], g[k][..., rest]), k
+    yc, fc, gc = run(C=inf["C"])
+    assert torch.equal(yc[:, :-1], y[:, :-1]) and torch.isposinf(yc[:, -1]).all() and torch.equal(fc, final)
+    assert torch.equal(gc["dC"], g["dC"])
+    for k in ("dA", "dB", "d_init"):
+        assert torch.equal(gc[k][..., rest], g[k][..., rest]), k
