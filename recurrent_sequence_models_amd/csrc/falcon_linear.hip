@@ -226,6 +226,14 @@ template <typename O> __device__ __forceinline__ void load4(const O *p, float (&
   }
 }
 
+// Results are not read again here, and leave the caches to the operands (16384 x 768 -> 1536 bf16 with pre: 73 us, 81 with
+// plain stores; its dx 53 and 57; 2048 -> 4096 the same).  Rounded to nearest even: the one rounding of a result.
+template <typename O> __device__ __forceinline__ void stream4(O *p, const float (&v)[4]) {
+  const f4 t = {v[0], v[1], v[2], v[3]};
+  if constexpr (sizeof(O) == 4) __builtin_nontemporal_store(t, reinterpret_cast<f4 *>(p));
+  else __builtin_nontemporal_store(__builtin_convertvector(t, bf4), reinterpret_cast<bf4 *>(p));
+}
+
 // Results i .. i + 3 of row j: scales, bias, activation, residual, and out.
 template <typename O> __device__ __forceinline__ void finish(const LinearArgs &a, int i, int j, float (&v)[4]) {
   const size_t at = (size_t)j * a.ldo + i;
@@ -238,7 +246,7 @@ template <typename O> __device__ __forceinline__ void finish(const LinearArgs &a
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] += a.bias[i + e];
   }
-  if (a.pre) store4(a.pre + (size_t)j * a.I + i, v[0], v[1], v[2], v[3]);
+  if (a.pre) stream4(a.pre + (size_t)j * a.I + i, v);
   if (a.act) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = activate(v[e], a.act);
@@ -249,7 +257,7 @@ template <typename O> __device__ __forceinline__ void finish(const LinearArgs &a
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] += r[e];
   }
-  store4(static_cast<O *>(a.out) + at, v[0], v[1], v[2], v[3]);
+  stream4(static_cast<O *>(a.out) + at, v);
 }
 
 // ---- Tiles -------------------------------------------------------------------------
