@@ -11,10 +11,13 @@
 // last W - 1 inputs (backward: and the W unfinished gradients) in registers.  The W - 1 tokens next to
 // a run are read again, from the cache as a rule: the runs beside belong to the same workgroup.
 // In the backward pass d is formed again for the W - 1 tokens behind the run, rather than
-// exchanged.  Bound: HBM, x and y (backward: x, dy and dx) once; the backward's vector unit is half busy.
-// Measured, 4 x 4096 x 1536 bf16, 4 taps, silu: forward 25 us (101 MB at 4.0 TB/s), backward 41 us (151 MB at 3.7; 49
-// with 8 channels a thread, which leave two waves a SIMD) and 5 us to add the weights' gradients; 64 tokens x
-// 4096: 4.9 us.
+// exchanged.  Blocks of tokens inside a run need no comparisons (39 us backward with them everywhere).  Bound: HBM, x and
+// y (backward: x, dy and dx) once, and backward the vector unit beside it.
+// Measured, 4 x 4096 x 1536 bf16, 4 taps, silu: forward 25 us (101 MB at 4.1 TB/s), backward 36 us (151 MB at 4.2; 42
+// with 4 waves a SIMD, which spill; 49 with 8 channels a thread, which leave two) and 5 us to add the weights'
+// gradients; 64 tokens x 4096: 3.9 us.
+#include <type_traits>
+
 #include "block_kernels.h"
 #include "row_io.h"
 
@@ -24,7 +27,7 @@ namespace {
 constexpr int THR = 256;
 // lanes side by side over channels, and runs of a workgroup; forward and backward
 constexpr int LANES_F = 16, RUNS_F = THR / LANES_F, LANES_B = 32, RUNS_B = THR / LANES_B;
-constexpr int AHEAD = 4;                                   // tokens whose loads are in flight together
+constexpr int AHEAD = 4;                                   // tokens whose loads are in flight together, W - 1 at least
 
 // This thread's filters: w[k][j] of tap k, channel j; bias.
 template <int W, int E>
@@ -103,24 +106,28 @@ template <typename T, int W> __global__ __launch_bounds__(THR) void conv_fwd(Con
     if (t >= to) continue;
     Few<T, E> win[W - 1];
     load_window<T, W, E>(a, n, s, t, c, win);
-    for (; t < to; t += AHEAD) {
+    // AHEAD tokens from t on; all of them exist, or (ends) those behind the last are left out
+    auto block = [&](auto ends) __attribute__((always_inline)) {
+      const T *from = static_cast<const T *>(a.x) + (int64_t)t * a.ldx + c;
+      T *out = static_cast<T *>(a.y) + (size_t)t * a.D + c;
       Few<T, E> x[AHEAD];
 #pragma unroll
-      for (int i = 0; i < AHEAD; ++i) fetch(static_cast<const T *>(a.x) + (int64_t)min(t + i, to - 1) * a.ldx + c, x[i]);
+      for (int i = 0; i < AHEAD; ++i) fetch(from + (decltype(ends)::value ? min(i, to - 1 - t) : i) * a.ldx, x[i]);
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) {
-        if (t + i < to) {
-          float p[E];
-          convolve<T, W, E>(w, b, win, x[i], p);
-          if (a.silu) {
+        if (decltype(ends)::value && t + i >= to) continue;
+        float p[E];
+        convolve<T, W, E>(w, b, win, x[i], p);
+        if (a.silu) {
 #pragma unroll
-            for (int j = 0; j < E; ++j) p[j] *= sigmoid(p[j]);
-          }
-          put(static_cast<T *>(a.y) + (size_t)(t + i) * a.D + c, p);
-          slide<T, W, E>(win, x[i]);
+          for (int j = 0; j < E; ++j) p[j] *= sigmoid(p[j]);
         }
+        put(out + (size_t)i * a.D, p);
+        slide<T, W, E>(win, x[i]);
       }
-    }
+    };
+    for (; t + AHEAD <= to; t += AHEAD) block(std::false_type());
+    if (t < to) block(std::true_type());
     t = to;
     if (to == e && a.final_state) {
 #pragma unroll
@@ -158,54 +165,61 @@ template <typename T, int W> __global__ __launch_bounds__(THR) void conv_bwd(Con
         else if (p < s && from == s && a.d_init)
           put(static_cast<T *>(a.d_init) + ((size_t)n * (W - 1) + (p - s + W - 1)) * a.D + c, v);
       };
-      for (; t < upto; t += AHEAD) {
+      // AHEAD tokens from t on; (ends) some may be behind the last, behind this thread's own, or finish one before those
+      auto block = [&](auto ends) __attribute__((always_inline)) {
+        constexpr bool ENDS = decltype(ends)::value;
+        const T *px = static_cast<const T *>(a.x) + (int64_t)t * a.ldx + c, *pg = static_cast<const T *>(a.dy) + (size_t)t * a.D + c;
+        T *out = static_cast<T *>(a.dx) + (int64_t)(t - (W - 1)) * a.lddx + c;
         Few<T, E> x[AHEAD], g[AHEAD];
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
-          const int q = min(t + i, upto - 1);
-          fetch(static_cast<const T *>(a.x) + (int64_t)q * a.ldx + c, x[i]);
-          fetch(static_cast<const T *>(a.dy) + (size_t)q * a.D + c, g[i]);
+          const int64_t q = ENDS ? min(i, upto - 1 - t) : i;
+          fetch(px + q * a.ldx, x[i]);
+          fetch(pg + q * a.D, g[i]);
         }
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
-          if (t + i < upto) {
-            float d[E];
+          if (ENDS && t + i >= upto) continue;
+          float d[E];
 #pragma unroll
-            for (int j = 0; j < E; ++j) d[j] = g[i][j];
-            if (a.silu) {
-              float p[E];
-              convolve<T, W, E>(w, b, win, x[i], p);
+          for (int j = 0; j < E; ++j) d[j] = g[i][j];
+          if (a.silu) {
+            float p[E];
+            convolve<T, W, E>(w, b, win, x[i], p);
 #pragma unroll
-              for (int j = 0; j < E; ++j) {
-                const float sg = sigmoid(p[j]);
-                d[j] *= sg * fmaf(p[j], 1.f - sg, 1.f);
-              }
+            for (int j = 0; j < E; ++j) {
+              const float sg = sigmoid(p[j]);
+              d[j] *= sg * fmaf(p[j], 1.f - sg, 1.f);
             }
-            if (t + i < to) {
-#pragma unroll
-              for (int k = 0; k < W; ++k) {
-                const Few<T, E> v = k < W - 1 ? win[k < W - 1 ? k : 0] : x[i];
-#pragma unroll
-                for (int j = 0; j < E; ++j) dw[k][j] = fmaf(d[j], v[j], dw[k][j]);
-              }
-#pragma unroll
-              for (int j = 0; j < E; ++j) db[j] += d[j];
-            }
-#pragma unroll
-            for (int k = 0; k < W; ++k)
-#pragma unroll
-              for (int j = 0; j < E; ++j) acc[k][j] = fmaf(w[k][j], d[j], acc[k][j]);
-            emit(t + i - (W - 1), acc[0]);
-#pragma unroll
-            for (int k = 0; k + 1 < W; ++k)
-#pragma unroll
-              for (int j = 0; j < E; ++j) acc[k][j] = acc[k + 1][j];
-#pragma unroll
-            for (int j = 0; j < E; ++j) acc[W - 1][j] = 0.f;
-            slide<T, W, E>(win, x[i]);
           }
+          if (!ENDS || t + i < to) {
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+              const Few<T, E> v = k < W - 1 ? win[k < W - 1 ? k : 0] : x[i];
+#pragma unroll
+              for (int j = 0; j < E; ++j) dw[k][j] = fmaf(d[j], v[j], dw[k][j]);
+            }
+#pragma unroll
+            for (int j = 0; j < E; ++j) db[j] += d[j];
+          }
+#pragma unroll
+          for (int k = 0; k < W; ++k)
+#pragma unroll
+            for (int j = 0; j < E; ++j) acc[k][j] = fmaf(w[k][j], d[j], acc[k][j]);
+          if constexpr (ENDS) emit(t + i - (W - 1), acc[0]);
+          else put(out + i * a.lddx, acc[0]);
+#pragma unroll
+          for (int k = 0; k + 1 < W; ++k)
+#pragma unroll
+            for (int j = 0; j < E; ++j) acc[k][j] = acc[k + 1][j];
+#pragma unroll
+          for (int j = 0; j < E; ++j) acc[W - 1][j] = 0.f;
+          slide<T, W, E>(win, x[i]);
         }
-      }
+      };
+      block(std::true_type());
+      for (t += AHEAD; t + AHEAD <= to; t += AHEAD) block(std::false_type());
+      for (; t < upto; t += AHEAD) block(std::true_type());
       if (upto == e) {           // the sequence's end: its last inputs are its final state
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) {
@@ -269,7 +283,7 @@ template <typename T, int W> __global__ __launch_bounds__(STEP_THR) void conv_st
 }
 
 // A pass's shape: channels of a workgroup, runs of it, and the tokens of a run.  Long runs read fewer tokens twice, short
-// ones make more workgroups.
+// ones make more workgroups (4 x 4096 x 1536 bf16: 25.1 and 42 us with runs twice as long, backward 54 with 16).
 struct Shape {
   int cols, runs, run;
   dim3 grid;
