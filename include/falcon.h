@@ -680,8 +680,8 @@ typedef struct {
   int32_t out_dtype;   /* falcon_dtype_t of y and residual: dtype; for E4M3 F32 or BF16 */
 } falcon_linear_shape_t;
 
-/* Bytes of workspace of the forward: the sums of workgroups that split `in`, where there are
- * few tokens but more than 64; 0 elsewhere (then workspace may be NULL) and for invalid shapes. */
+/* Bytes of workspace of the forward: the sums of workgroups that split `in`, where there are few
+ * tokens; 0 where none do (then workspace may be NULL), and for invalid shapes. */
 size_t falcon_linear_fwd_workspace(const falcon_linear_shape_t *shape);
 
 /*   x             token stride at most 2^23 bytes;  weight dense.

@@ -7,20 +7,22 @@
 // what runs along the result's rows in memory, so a lane holds 4 neighbours of a row.
 //
 // A workgroup owns a tile of the result; tiles of both operands, 128 bytes of k at a time, are copied straight
-// into LDS, swizzled, double-buffered.  Few tiles: k is split over workgroups, whose fp32 sums a second
-// kernel adds in order and finishes.  At most 64 tokens: W is what has to be read, so 16 of its rows
-// are a workgroup's, whose waves split k, without LDS tiles (8-bit operands widened to bf16 there).
+// into LDS, swizzled, one to three steps ahead.  Few tiles: they are smaller, and k is split over workgroups, whose
+// fp32 sums a second kernel adds in order and finishes.  At most 64 tokens: W is what has to be read, so (unless its rows
+// are long) 16 of them are a workgroup's, whose waves split k, without LDS tiles (8-bit operands widened to bf16 there).
 //
 // Bound: the matrix unit for many tokens, with LDS close behind (a wave's 128 x 64 takes 6 fragments for 8 products: 75 %
 // of what LDS gives at the unit's full rate, and the copies the rest), and the wait for copies that start one step
 // before their use; W's bytes for few tokens.  Measured, where a large library product reaches 1.2 to 1.34 PFLOP/s in
 // bf16 and 2.9 in e4m3:
 //   8192^3: bf16 850 us (1.29 PFLOP/s), e4m3 475 us (2.31)
-//   16384 x 2048 -> 4096 bf16, bias and silu: 244 us on one set of operands (1.13 PFLOP/s), 290 on three in turn
+//   16384 x 2048 -> 4096 bf16, bias and silu: 244 us on one set of operands (1.13 PFLOP/s), 271 on three in turn
 //   16384 x 4096 -> 2048 e4m3, residual: 195 us (1.41 PFLOP/s); to fp32, widened: 316 us
 //   4096 x 2048 -> 2048 fp32: 280 us (123 TFLOP/s; a large fp32 product 146)
+//   512 x 2048 -> 2048 bf16: 15 us (a library product 12)
 //   16 x 2048 -> 4096 bf16: 7 us (16.8 MB at 2.4 TB/s: one wave's loads and the launch)
 // Sums are fp32; a result is rounded once, at its end.
+#include <algorithm>
 #include <type_traits>
 
 #include "attn_frag.h"
@@ -261,15 +263,16 @@ template <typename O> __device__ __forceinline__ void finish(const LinearArgs &a
 }
 
 // ---- Tiles -------------------------------------------------------------------------
-// T: operands; O: results; TL, TR: tile of the result; WL, WR: waves along each.
-template <typename T, typename O, bool LC, bool RC, int TL, int TR, int WL, int WR>
+// T: operands; O: results; TL, TR: tile of the result; WL, WR: waves along each; STAGES: steps that LDS holds, all but one of
+// them on their way.
+template <typename T, typename O, bool LC, bool RC, int TL, int TR, int WL, int WR, int STAGES>
 __global__ __launch_bounds__(64 * WL * WR) void product(LinearArgs a) {
   constexpr int THR = 64 * WL * WR, FL = TL / WL / 32, FR = TR / WR / 32;
   typedef OperandTile<T, TL, LC> OL;
   typedef OperandTile<T, TR, RC> OR;
-  __shared__ __align__(128) uint4 lds[2 * (OL::CHUNKS + OR::CHUNKS)];
+  __shared__ __align__(128) uint4 lds[STAGES * (OL::CHUNKS + OR::CHUNKS)];
   uint4(*left)[OL::CHUNKS] = reinterpret_cast<uint4(*)[OL::CHUNKS]>(lds);
-  uint4(*right)[OR::CHUNKS] = reinterpret_cast<uint4(*)[OR::CHUNKS]>(lds + 2 * OL::CHUNKS);
+  uint4(*right)[OR::CHUNKS] = reinterpret_cast<uint4(*)[OR::CHUNKS]>(lds + STAGES * OL::CHUNKS);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wl = wave % WL, wr = wave / WL;
   // tiles in blocks of 8 along j, dealt to the dies in runs of neighbours
   const int ti = (a.I + TL - 1) / TL, tj = (a.J + TR - 1) / TR, tiles = ti * tj;
@@ -337,33 +340,37 @@ __global__ __launch_bounds__(64 * WL * WR) void product(LinearArgs a) {
   };
   // step s's tiles have arrived, and those of the step before are read no more
   auto arrive = [&](int s, int buffer) __attribute__((always_inline)) {
-    copies_done();
+    if (STAGES > 2 && s + STAGES - 2 < s1) copies_done_but<(STAGES - 2) * (Copier<T, TL, LC, THR>::PER + Copier<T, TR, RC, THR>::PER)>();
+    else copies_done();
     if (s == steps - 1) {
       cl.clear(left[buffer], s * KE<T>, tid);
       cr.clear(right[buffer], s * KE<T>, tid);
     }
     __syncthreads();
-    if (s + 1 < s1) copy(s + 1, buffer ^ 1);
+    if (s + STAGES - 1 < s1) copy(s + STAGES - 1, buffer ? buffer - 1 : STAGES - 1);
   };
   if (s0 < s1) {
-    copy(s0, 0);
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i)
+      if (s0 + i < s1) copy(s0 + i, i);
     arrive(s0, 0);
     read_right(0, 0);
 #pragma unroll
     for (int p = 0; p < FL; ++p) read_left(0, 0, p);
     int now = 0;
-    for (int s = s0; s + 1 < s1; ++s, now ^= 1) {
+    for (int s = s0; s + 1 < s1; ++s) {
       blocks(now);
 #pragma unroll
       for (int p = 0; p < FL / 2; ++p) multiply(NB - 1, p);
-      arrive(s + 1, now ^ 1);
-      read_right(now ^ 1, 0);
+      now = now + 1 < STAGES ? now + 1 : 0;
+      arrive(s + 1, now);
+      read_right(now, 0);
 #pragma unroll
-      for (int p = 0; p < FL / 2; ++p) read_left(now ^ 1, 0, p);
+      for (int p = 0; p < FL / 2; ++p) read_left(now, 0, p);
 #pragma unroll
       for (int p = FL / 2; p < FL; ++p) {
         multiply(NB - 1, p);
-        read_left(now ^ 1, 0, p);
+        read_left(now, 0, p);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -375,7 +382,7 @@ __global__ __launch_bounds__(64 * WL * WR) void product(LinearArgs a) {
   // written whole (4 entries a lane straight from the registers, 16 neighbouring bytes a row: 321 us for 287 at 16384 x
   // 2048 x 4096).  16-byte chunk n of row j stands at place n ^ (j & 7).
   constexpr int CI = FL * 8, RI = 64 / CI;       // chunks of a row; rows that the wave's lanes cover
-  static_assert(32 * CI * WL * WR <= 2 * (OL::CHUNKS + OR::CHUNKS), "a wave's part");
+  static_assert(32 * CI * WL * WR <= STAGES * (OL::CHUNKS + OR::CHUNKS), "a wave's part");
   __syncthreads();
   uint4 *stage = lds + wave * 32 * CI;
   const int c = lane & 31, h = lane >> 5;
@@ -520,41 +527,73 @@ template <typename T> __global__ __launch_bounds__(256) void pre_gradient(Linear
 }
 
 // ---- Launches ---------------------------------------------------------------------------
-struct Plan { bool big; int splits; int64_t tiles; };
+// Forms of a product: `few` (16 rows of the left operand a workgroup), or tiles of 64 x 64, 128 x 128 (deep: four steps in
+// LDS, one workgroup a compute unit) and 256 x 256.
+enum class Form { few, small, deep, medium, large };
+struct Plan { Form form; int splits; int64_t tiles; };
+
+int64_t over(int64_t n, int64_t d) { return (n + d - 1) / d; }
+
+// Workgroups that share a tile's k: as many as make `groups` of all, at 4 steps each and 16 at most.
+int splits_of(int64_t tiles, int64_t groups, int64_t steps) {
+  const int64_t s = std::min({groups / tiles, steps / 4, (int64_t)16});
+  return s > 1 ? (int)s : 1;
+}
 
 // A compute unit holds one workgroup of 256 x 256 or two of 128 x 128; the larger tile reads less from LDS for a product
 // (16384 x 2048 -> 4096 bf16: 287 us, 299 with the smaller; 16384 x 4096 -> 2048 e4m3: 195, 227), the smaller one
 // leaves less of the last round empty (16384 x 768 -> 1536 bf16: 54.7 us, 58.7 with the larger; 2048 x 2048 -> 2048:
 // 29, 51).  So rounds are counted, in tiles of 128 x 128 a compute unit.  fp32 takes too many registers for the larger.
-// Where 128 x 128 tiles leave compute units idle, k is split, at 4 steps a split and 16 splits at most.
-Plan plan_of(int64_t I, int64_t J, int64_t K, int e) {
-  Plan p;
-  const int64_t large = ((I + 255) / 256) * ((J + 255) / 256), small = ((I + 127) / 128) * ((J + 127) / 128);
-  p.big = e < 4 && large >= 256 && (large + 255) / 256 * 4 * 20 <= (small + 511) / 512 * 2 * 21;
-  p.tiles = p.big ? large : small;
-  const int64_t steps = (K * e + KB - 1) / KB;
-  p.splits = 1;
-  if (p.tiles < 256) {
-    int64_t s = 512 / p.tiles;
-    if (s > steps / 4) s = steps / 4;
-    if (s > 16) s = 16;
-    if (s > 1) p.splits = (int)s;
+// Where 128 x 128 tiles leave compute units idle, tiles are 64 x 64, and k is split where those do too: 512 x 2048 -> 2048
+// bf16 15.5 us, 20 in four parts of 128 x 128; 100 x 2048 -> 4096 13.5, 16.  Not over more than 48 steps a
+// workgroup: 512 x 8192 -> 2048 44.6 us, 31.8 in eight parts of 128 x 128; those for two workgroups a compute unit where
+// each has 16 steps and more (768 x 16384 -> 1536: 183 us with the rest of its backward pass, 192 for one; 100 x 8192 ->
+// 4096: 24.0 and 22.3).  One workgroup of 128 x 128 a compute unit has LDS for four steps, which are all on their way
+// (2048 x 2048 -> 2048: 27 us, 31 with two; 33 as 64 x 64).
+Plan tiles_of(int64_t I, int64_t J, int64_t K, int e) {
+  const int64_t large = over(I, 256) * over(J, 256), medium = over(I, 128) * over(J, 128), small = over(I, 64) * over(J, 64);
+  if (e < 4 && large >= 256 && over(large, 256) * 4 * 20 <= over(medium, 512) * 2 * 21) return {Form::large, 1, large};
+  const int64_t steps = over(K * e, KB);
+  if (medium < 256) {
+    const int s = splits_of(small, 256, steps);
+    if (steps / s <= 48) return {Form::small, s, small};
   }
-  return p;
+  const int s = medium < 256 ? splits_of(medium, steps * medium >= 16 * 512 ? 512 : 256, steps) : 1;
+  return {medium * s <= 256 ? Form::deep : Form::medium, s, medium};
 }
 
 // The time of a plan's tiles, in rounds of the chip: 20 for tiles of 128 x 128 a compute unit.
-int64_t rounds_of(const Plan &p) { return p.big ? (p.tiles + 255) / 256 * 4 * 20 : (p.tiles * p.splits + 511) / 512 * 2 * 21; }
+int64_t rounds_of(const Plan &p) {
+  return p.form == Form::large ? over(p.tiles, 256) * 4 * 20 : over(p.tiles * p.splits, 512) * 2 * 21;
+}
 
-template <typename T, typename O, bool LC, bool RC> hipError_t multiply(LinearArgs a, void *ws, hipStream_t s) {
-  const Plan p = plan_of(a.I, a.J, a.K, sizeof(T));
+// Few tokens take what a compute unit loads, at about 40 KB a us: 16 rows of W and the tokens (a multiple of 16) for each
+// of its workgroups of `few`, or both operands of its tiles' steps (which fp32 products hold up by a quarter, by
+// three halves in the larger tiles) and about 64 KB for the tile's beginning and the join.  16 x 2048 -> 4096 bf16: 7.5 us,
+// 9.6 in tiles; 16 x 8192 -> 2048: 17.6 and 12.1; 64 x 4096 -> 8192: 38.5 and 17.8; 24 x 4096 -> 8192 fp32: 47 and 72.
+Plan plan_of(int64_t I, int64_t J, int64_t K, int e) {
+  const Plan p = tiles_of(I, J, K, e);
+  if (J > FEW_TOKENS) return p;
+  const int64_t rows = J <= 16 ? 32 : J <= 32 ? 48 : 80, groups = over(I, 16);
+  const int64_t few = over(groups, 256) * rows * K * e, step = p.form == Form::small ? 2 * 64 * KB : 2 * 128 * KB;
+  const int64_t tiles = over(p.tiles * p.splits, 256) * (over(K * e, KB) / p.splits) * step, quarters = e < 4 ? 4 : p.form == Form::small ? 5 : 10;
+  if (p.form == Form::large || few <= tiles * quarters / 4 + 65536) return {Form::few, 1, groups};
+  return p;
+}
+
+template <typename T, typename O, bool LC, bool RC> hipError_t multiply(const Plan &p, LinearArgs a, void *ws, hipStream_t s) {
   a.splits = p.splits;
   a.part = static_cast<float *>(ws);
-  const unsigned grid = (unsigned)((p.tiles * p.splits + 7) / 8 * 8);
-  if constexpr (sizeof(T) < 4) {
-    if (p.big) hipLaunchKernelGGL((product<T, O, LC, RC, 256, 256, 2, 4>), dim3(grid), dim3(512), 0, s, a);
+  const dim3 grid((unsigned)((p.tiles * p.splits + 7) / 8 * 8));
+  if (p.form == Form::small) {
+    hipLaunchKernelGGL((product<T, O, LC, RC, 64, 64, 2, 2, 3>), grid, dim3(256), 0, s, a);
+  } else if (p.form == Form::deep) {
+    hipLaunchKernelGGL((product<T, O, LC, RC, 128, 128, 2, 2, 4>), grid, dim3(256), 0, s, a);
+  } else if (p.form == Form::medium) {
+    hipLaunchKernelGGL((product<T, O, LC, RC, 128, 128, 2, 2, 2>), grid, dim3(256), 0, s, a);
+  } else if constexpr (sizeof(T) < 4) {
+    hipLaunchKernelGGL((product<T, O, LC, RC, 256, 256, 2, 4, 2>), grid, dim3(512), 0, s, a);
   }
-  if (!p.big) hipLaunchKernelGGL((product<T, O, LC, RC, 128, 128, 2, 2>), dim3(grid), dim3(256), 0, s, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   const int64_t n = (int64_t)a.I * a.J / 4;
@@ -575,15 +614,19 @@ template <typename T, typename O> hipError_t few_tokens(const LinearArgs &a, hip
 int tokens_apart(int64_t I, int64_t J, int64_t K, int e) {
   const int rest = (int)(J % 256);
   if (!rest || rest > FEW_TOKENS || J < 512 || K < 512) return 0;
-  return rounds_of(plan_of(I, J - rest, K, e)) < rounds_of(plan_of(I, J, K, e)) ? rest : 0;
+  const Plan with = plan_of(I, J, K, e), without = plan_of(I, J - rest, K, e);
+  return with.form != Form::small && without.form != Form::small && rounds_of(without) < rounds_of(with) ? rest : 0;
 }
 
 template <typename T, typename O> hipError_t fwd(LinearArgs a, void *ws, hipStream_t s) {
   typedef std::conditional_t<sizeof(T) == 1 && sizeof(O) == 4, e4m3_wide, T> Tiled;
-  if (a.J <= FEW_TOKENS) return few_tokens<T, O>(a, s);
+  const auto pass = [&] {
+    const Plan p = plan_of(a.I, a.J, a.K, sizeof(T));
+    return p.form == Form::few ? few_tokens<T, O>(a, s) : multiply<Tiled, O, false, false>(p, a, ws, s);
+  };
   const int rest = tokens_apart(a.I, a.J, a.K, sizeof(T)), most = a.J - rest;
   a.J = most;
-  const hipError_t e = multiply<Tiled, O, false, false>(a, ws, s);
+  const hipError_t e = pass();
   if (e != hipSuccess || !rest) return e;
   a.J = rest;
   a.right = static_cast<const T *>(a.right) + most * a.ldr;
@@ -591,18 +634,15 @@ template <typename T, typename O> hipError_t fwd(LinearArgs a, void *ws, hipStre
   if (a.pre) a.pre += (size_t)most * a.I;
   if (a.residual) a.residual = static_cast<const O *>(a.residual) + (size_t)most * a.I;
   if (a.scale_r) a.scale_r += most;
-  return few_tokens<T, O>(a, s);
+  return pass();
 }
 
 size_t align16(size_t n) { return (n + 15) / 16 * 16; }
-size_t part_bytes(int64_t I, int64_t J, int64_t K, int e) {
-  const Plan p = plan_of(I, J, K, e);
-  return p.splits > 1 ? (size_t)p.splits * I * J * sizeof(float) : 0;
-}
+size_t part_bytes(const Plan &p, int64_t I, int64_t J) { return p.splits > 1 ? (size_t)p.splits * I * J * sizeof(float) : 0; }
 size_t sum_blocks(int64_t J) { return (size_t)((J + DP_RUN - 1) / DP_RUN); }
 
 bool fits(int64_t I, int64_t J, int64_t K, int e) {
-  const Plan p = plan_of(I, J, K, e);
+  const Plan p = tiles_of(I, J, K, e);
   return grid_fits(p.tiles * p.splits + 8, 512) && (p.splits == 1 || grid_fits((I * J / 4 + 255) / 256, 256));
 }
 
@@ -614,12 +654,13 @@ bool linear_fits(int e, int64_t tokens, int64_t in, int64_t out) {
 }
 
 size_t linear_fwd_workspace(int e, int64_t tokens, int64_t in, int64_t out) {
-  return tokens > FEW_TOKENS ? part_bytes(out, tokens - tokens_apart(out, tokens, in, e), in, e) : 0;
+  const int64_t rest = tokens_apart(out, tokens, in, e), most = tokens - rest;
+  return std::max(part_bytes(plan_of(out, most, in, e), out, most), rest ? part_bytes(plan_of(out, rest, in, e), out, rest) : 0);
 }
 
 size_t linear_bwd_workspace(int e, bool act, int64_t tokens, int64_t in, int64_t out) {
-  const size_t dx = part_bytes(in, tokens, out, e), dw = part_bytes(in, out, tokens, e);
-  return (act ? align16((size_t)tokens * out * e) : 0) + align16(sum_blocks(tokens) * out * sizeof(float)) + (dx > dw ? dx : dw);
+  const size_t dx = part_bytes(tiles_of(in, tokens, out, e), in, tokens), dw = part_bytes(tiles_of(in, out, tokens, e), in, out);
+  return (act ? align16((size_t)tokens * out * e) : 0) + align16(sum_blocks(tokens) * out * sizeof(float)) + std::max(dx, dw);
 }
 
 hipError_t launch_linear_fwd(int dtype, bool bf16_out, LinearArgs a, void *ws, hipStream_t s) {
@@ -661,7 +702,7 @@ template <typename T> static hipError_t bwd(const LinearGrads &g, void *ws, hipS
     a.right = d; a.ldr = ldd;
     a.I = g.in; a.J = g.tokens; a.K = g.out;
     a.out = g.dx; a.ldo = g.lddx;
-    if ((e = multiply<T, T, true, false>(a, at, s)) != hipSuccess) return e;
+    if ((e = multiply<T, T, true, false>(tiles_of(a.I, a.J, a.K, sizeof(T)), a, at, s)) != hipSuccess) return e;
   }
   if (g.dw) {            // dw[n][k] = sum over tokens of d[token][n] x[token][k]
     LinearArgs a{};
@@ -669,7 +710,7 @@ template <typename T> static hipError_t bwd(const LinearGrads &g, void *ws, hipS
     a.right = d; a.ldr = ldd;
     a.I = g.in; a.J = g.out; a.K = g.tokens;
     a.out = g.dw; a.ldo = g.in;
-    if ((e = multiply<T, T, true, true>(a, at, s)) != hipSuccess) return e;
+    if ((e = multiply<T, T, true, true>(tiles_of(a.I, a.J, a.K, sizeof(T)), a, at, s)) != hipSuccess) return e;
   }
   return hipSuccess;
 }

@@ -223,10 +223,10 @@ def test_linear_refusals():
 
 
 def test_linear_workspace():
-    """No partial sums for few tokens, nor where the tiles fill the chip."""
+    """No partial sums for few tokens on short rows, nor where the tiles fill the chip."""
     L = F.lib()
     size = lambda **kw: L.falcon_linear_fwd_workspace(ref(linear_shape(**kw)))  # noqa: E731
-    assert size(**{"tokens": 64, "in": 2048, "out": 2048}) == 0
+    assert size(**{"tokens": 16, "in": 2048, "out": 4096}) == 0
     assert size(**{"tokens": 65, "in": 2048, "out": 2048}) > 0
     assert size(**{"tokens": 16384, "in": 2048, "out": 2048}) == 0
 
