@@ -548,8 +548,9 @@ int splits_of(int64_t tiles, int64_t groups, int64_t steps) {
 // bf16 15.5 us, 20 in four parts of 128 x 128; 100 x 2048 -> 4096 13.5, 16.  Not over more than 48 steps a
 // workgroup: 512 x 8192 -> 2048 44.6 us, 31.8 in eight parts of 128 x 128; those for two workgroups a compute unit where
 // each has 16 steps and more (768 x 16384 -> 1536: 183 us with the rest of its backward pass, 192 for one; 100 x 8192 ->
-// 4096: 24.0 and 22.3).  One workgroup of 128 x 128 a compute unit has LDS for four steps, which are all on their way
-// (2048 x 2048 -> 2048: 27 us, 31 with two; 33 as 64 x 64).
+// 4096: 24.0 and 22.3).  One workgroup of 128 x 128 a compute unit has LDS for four steps, three of them on their way,
+// and 8 waves (2048 x 2048 -> 2048: 25 us, 28 with 4 waves, 31 with two steps; 33 as 64 x 64; training 2048 x 2048 -> 2048:
+// 80 and 91).
 Plan tiles_of(int64_t I, int64_t J, int64_t K, int e) {
   const int64_t large = over(I, 256) * over(J, 256), medium = over(I, 128) * over(J, 128), small = over(I, 64) * over(J, 64);
   if (e < 4 && large >= 256 && over(large, 256) * 4 * 20 <= over(medium, 512) * 2 * 21) return {Form::large, 1, large};
@@ -588,7 +589,7 @@ template <typename T, typename O, bool LC, bool RC> hipError_t multiply(const Pl
   if (p.form == Form::small) {
     hipLaunchKernelGGL((product<T, O, LC, RC, 64, 64, 2, 2, 3>), grid, dim3(256), 0, s, a);
   } else if (p.form == Form::deep) {
-    hipLaunchKernelGGL((product<T, O, LC, RC, 128, 128, 2, 2, 4>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((product<T, O, LC, RC, 128, 128, 2, 4, 4>), grid, dim3(512), 0, s, a);
   } else if (p.form == Form::medium) {
     hipLaunchKernelGGL((product<T, O, LC, RC, 128, 128, 2, 2, 2>), grid, dim3(256), 0, s, a);
   } else if constexpr (sizeof(T) < 4) {
