@@ -183,7 +183,8 @@ __global__ __launch_bounds__((SsmTile<N, FWD_CH, TW, STEPS>::THR), (STEPS == 16 
   }
 }
 
-// The states that the segments of a sequence start from, in order: thread per (channel, 4 states).
+// The states that the segments of a sequence start from, in order: thread per (channel, 4 states), which loads
+// CHAIN_AHEAD maps together.
 template <int N> __global__ __launch_bounds__(256) void ssm_chain(SsmArgs a) {
   const int per = a.D * (N / 4), i = blockIdx.x * 256 + threadIdx.x;
   if (i >= per) return;
@@ -193,13 +194,23 @@ template <int N> __global__ __launch_bounds__(256) void ssm_chain(SsmArgs a) {
     const int s = a.seq.begin(n), e = a.seq.end(n), slot = first_slot(a.seq, n, a.seg);
     f4 h{0.f, 0.f, 0.f, 0.f};
     if (a.init) h = *reinterpret_cast<const f4 *>(a.init + ((size_t)n * a.D + c) * N + p4);
-    for (int k = 0; (int64_t)s + (int64_t)(k + 1) * a.seg < e; ++k) {
-      const size_t at = ((size_t)(slot + k) * a.D + c) * N + p4;
-      const float sd = a.seg_sum[(size_t)(slot + k) * a.D + c];
-      const f4 H = *reinterpret_cast<const f4 *>(a.seg_map + at);
+    const int maps = e > s ? (e - s - 1) / a.seg : 0;      // of all segments but the last
+    for (int k0 = 0; k0 < maps; k0 += CHAIN_AHEAD) {
+      f4 H[CHAIN_AHEAD];
+      float sd[CHAIN_AHEAD];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = fmaf(__builtin_amdgcn_exp2f(sd * A2[j]), h[j], H[j]);
-      *reinterpret_cast<f4 *>(a.seg_state + at + (size_t)a.D * N) = h;
+      for (int k = 0; k < CHAIN_AHEAD; ++k) {
+        const size_t at = (size_t)(slot + min(k0 + k, maps - 1)) * a.D + c;
+        sd[k] = a.seg_sum[at];
+        H[k] = *reinterpret_cast<const f4 *>(a.seg_map + at * N + p4);
+      }
+#pragma unroll
+      for (int k = 0; k < CHAIN_AHEAD; ++k) {
+        if (k0 + k >= maps) break;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = fmaf(__builtin_amdgcn_exp2f(sd[k] * A2[j]), h[j], H[k][j]);
+        *reinterpret_cast<f4 *>(a.seg_state + ((size_t)(slot + k0 + k + 1) * a.D + c) * N + p4) = h;
+      }
     }
   }
 }

@@ -323,13 +323,22 @@ template <int N> __global__ __launch_bounds__(256) void ssm_chain_bwd(SsmArgs a)
     const int s = a.seq.begin(n), e = a.seq.end(n), slot = first_slot(a.seq, n, a.seg);
     f4 r{0.f, 0.f, 0.f, 0.f};
     if (a.d_final) r = *reinterpret_cast<const f4 *>(a.d_final + ((size_t)n * a.D + c) * N + p4);
-    for (int k = e > s ? (e - s - 1) / a.seg : 0; k > 0; --k) {
-      const size_t at = ((size_t)(slot + k) * a.D + c) * N + p4;
-      const float sd = a.seg_sum[(size_t)(slot + k) * a.D + c];
-      const f4 G = *reinterpret_cast<const f4 *>(a.seg_map + at);
+    for (int k0 = e > s ? (e - s - 1) / a.seg : 0; k0 > 0; k0 -= CHAIN_AHEAD) {
+      f4 G[CHAIN_AHEAD];
+      float sd[CHAIN_AHEAD];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) r[j] = fmaf(__builtin_amdgcn_exp2f(sd * A2[j]), r[j], G[j]);
-      *reinterpret_cast<f4 *>(a.seg_state + at - (size_t)a.D * N) = r;
+      for (int k = 0; k < CHAIN_AHEAD; ++k) {
+        const size_t at = (size_t)(slot + max(k0 - k, 1)) * a.D + c;
+        sd[k] = a.seg_sum[at];
+        G[k] = *reinterpret_cast<const f4 *>(a.seg_map + at * N + p4);
+      }
+#pragma unroll
+      for (int k = 0; k < CHAIN_AHEAD; ++k) {
+        if (k0 - k <= 0) break;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[j] = fmaf(__builtin_amdgcn_exp2f(sd[k] * A2[j]), r[j], G[k][j]);
+        *reinterpret_cast<f4 *>(a.seg_state + ((size_t)(slot + k0 - k - 1) * a.D + c) * N + p4) = r;
+      }
     }
   }
 }

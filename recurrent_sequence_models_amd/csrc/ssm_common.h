@@ -11,6 +11,7 @@
 
 namespace falcon {
 
+constexpr int CHAIN_AHEAD = 8;    // segments' maps that are on their way together
 constexpr int SSM_ALIGN = 64;      // segments are a multiple of this long: whole chunks of every N
 constexpr float SSM_LOG2E = 1.44269504088896340736f, SSM_LN2 = 0.69314718055994530942f;
 
