@@ -92,9 +92,9 @@ struct SsmArgs {
 };
 struct SsmGrads { float *dA, *dD, *dbias; };   // [D, N]; [D] or null; [D] or null
 int ssm_chunk(int N);                             // steps between the states that the forward keeps
-int ssm_segment(const SeqMap &seq, int D, int channels, int enough, int want);   // tokens of a segment
+int ssm_segment(const SeqMap &seq, int D, int channels, int enough, int want, int whole);   // tokens of a segment
 bool ssm_segmented(const SeqMap &seq, int segment);   // whether a sequence has more than one (packed: may have)
-bool ssm_fits(SeqMap seq, int D);
+bool ssm_fits(SeqMap seq, int D, int N);
 bool ssm_step_fits(int n, int D, int N);
 size_t ssm_fwd_workspace(SeqMap seq, int D, int N);
 hipError_t launch_ssm_fwd(bool bf16, int N, SsmArgs a, void *ws, hipStream_t s);

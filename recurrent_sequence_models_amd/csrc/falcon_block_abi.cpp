@@ -216,7 +216,7 @@ int check_ssm(const falcon_ssm_shape_t *s, bool packed, bool step) {
   if (s->state != 16 && s->state != 32 && s->state != 64) return FALCON_ERR_UNSUPPORTED;
   if (s->width % 8 != 0 || s->width > (1 << 20)) return FALCON_ERR_UNSUPPORTED;
   if (step) return falcon::ssm_step_fits(s->batch, s->width, s->state) ? FALCON_OK : FALCON_ERR_UNSUPPORTED;
-  return falcon::ssm_fits(seq_sizes(s->batch, s->seqlen, packed), s->width) ? FALCON_OK : FALCON_ERR_UNSUPPORTED;
+  return falcon::ssm_fits(seq_sizes(s->batch, s->seqlen, packed), s->width, s->state) ? FALCON_OK : FALCON_ERR_UNSUPPORTED;
 }
 
 // [tokens, width] whose tokens are at most 2^24 bytes apart: the rows of a tile, at most 64, are 32 bits apart.

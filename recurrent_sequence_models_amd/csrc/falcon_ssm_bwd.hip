@@ -53,7 +53,8 @@ constexpr int BWD_CH = 32;
 template <int N> using BwdTile = SsmTile<N, BWD_CH, 64 / N, 16>;
 // Sequences are cut where they make fewer than 128 workgroups, into 256 (2 x 2048 x 768: 92 us with the maps' pass, 104 cut
 // for 512; 1 x 16384 x 1536: 632 and 615).
-int segment_of(const SeqMap &q, int D) { return ssm_segment(q, D, BWD_CH, 128, 256); }
+// Up to 2048 / N tokens they are left whole (with the forward, 1 x 128 x 512: 37 us, 41 cut; 192: 48 and 42).
+int segment_of(const SeqMap &q, int D, int N) { return ssm_segment(q, D, BWD_CH, 128, 256, 2048 / N); }
 
 // MAPS: only the segment's map (r at its start from zero behind its end, sum of delta) is formed.
 template <typename T, int N, bool MAPS> __global__ __launch_bounds__(BwdTile<N>::THR, MAPS ? 4 : 2) void ssm_bwd(SsmArgs a) {
@@ -362,7 +363,7 @@ size_t align16(size_t n) { return (n + 15) / 16 * 16; }
 
 struct Parts { size_t bc, A, D, map, sum, total; };
 Parts parts_of(const SeqMap &q, int D, int N) {
-  const int seg = segment_of(q, D);
+  const int seg = segment_of(q, D, N);
   const size_t groups = (D + BWD_CH - 1) / BWD_CH, slots = slots_of(q, seg);
   Parts p;
   p.bc = align16(groups * q.tokens() * 2 * N * sizeof(float));
@@ -388,7 +389,7 @@ template <typename T, int N> static hipError_t bwd(SsmArgs a, const SsmGrads &o,
   a.seg_map = reinterpret_cast<float *>(at += p.D);
   a.seg_state = reinterpret_cast<float *>(at += p.map);
   a.seg_sum = reinterpret_cast<float *>(at += p.map);
-  a.seg = segment_of(a.seq, a.D);
+  a.seg = segment_of(a.seq, a.D, N);
   const int groups = (a.D + BWD_CH - 1) / BWD_CH, slots = slots_of(a.seq, a.seg);
   const unsigned grid = (unsigned)ssm_grid(groups, slots);
   hipError_t e;
