@@ -12,7 +12,7 @@ import ctypes
 import functools
 
 from .falcon import ConvShape, Heads, LinearShape, NormShape, SsmShape, lib
-from .layer import _check, _current, _device, _done, _dtype, _ints, _offsets, _on, _p, _workspace
+from .layer import _check, _current, _device, _done, _dtype, _ints, _offsets, _on, _p, _types, _workspace
 
 E4M3 = 2   # FALCON_E4M3
 ACTIVATIONS = {None: 0, "silu": 1, "gelu": 2}
@@ -418,25 +418,33 @@ def _linear_plan(dtype, tokens, K, N, act, out):
     return ctypes.pointer(shape), L.falcon_linear_fwd_workspace(ref), L.falcon_linear_bwd_workspace(ref)
 
 
-def _linear_shape(x, weight, activation, out_dtype):
+@functools.lru_cache(maxsize=None)
+def _linear_types(dtype, out_dtype):
+    """(C type of the operands, whether 8 bits, type of the result, its C type)."""
     import torch
-    dev = _device("x", x)
-    f8 = x.dtype is _f8()
-    kind = E4M3 if f8 else _dtype("x", x)
-    if weight.dim() != 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
-        raise ValueError(f"x, weight: shapes {tuple(x.shape)}, {tuple(weight.shape)}, expected [..., in], [out, in]")
+    f8 = dtype is _f8()
+    kind = E4M3 if f8 else _types().get(dtype)
+    if kind is None:
+        raise TypeError("x must be float32 or bfloat16, or both operands float8_e4m3fn")
     if out_dtype is None:
-        out_dtype = torch.bfloat16 if f8 else x.dtype
-    if not f8 and out_dtype is not x.dtype:
-        raise TypeError(f"out_dtype: {out_dtype}, expected {x.dtype} (only 8-bit operands have another)")
-    N, K = weight.shape
-    _check("weight", weight, x.dtype, (N, K), dev)
-    out = {torch.float32: 0, torch.bfloat16: 1}.get(out_dtype)
+        out_dtype = torch.bfloat16 if f8 else dtype
+    if not f8 and out_dtype is not dtype:
+        raise TypeError(f"out_dtype: {out_dtype}, expected {dtype} (only 8-bit operands have another)")
+    out = _types().get(out_dtype)
     if out is None:
         raise TypeError("out_dtype must be float32 or bfloat16")
-    lead = x.shape[:-1]
-    plan = _linear_plan(kind, x.numel() // max(K, 1), K, N, _activation(activation), out)
-    return *plan, lead, out_dtype, f8, dev
+    return kind, f8, out_dtype, out
+
+
+def _linear_shape(x, weight, activation, out_dtype):
+    dev = _device("x", x)
+    kind, f8, out_dtype, out = _linear_types(x.dtype, out_dtype)
+    size, (*more, K) = weight.shape, x.shape or (None,)
+    if len(size) != 2 or size[1] != K:
+        raise ValueError(f"x, weight: shapes {tuple(x.shape)}, {tuple(size)}, expected [..., in], [out, in]")
+    _check("weight", weight, x.dtype, size, dev)
+    plan = _linear_plan(kind, x.numel() // max(K, 1), K, size[0], _activation(activation), out)
+    return *plan, tuple(more), out_dtype, f8, dev
 
 
 def linear(x, weight, *, bias=None, activation=None, residual=None, x_scale=None, weight_scale=None, pre=False,
@@ -464,10 +472,10 @@ def linear(x, weight, *, bias=None, activation=None, residual=None, x_scale=None
         _check("weight_scale", weight_scale, torch.float32, (N,), dev)
     with _on(dev, stream):
         if out is None:
-            out = x.new_empty(tuple(full), dtype=odt)
+            out = x.new_empty(full, dtype=odt)
         else:
             _check("y", out, odt, full, dev)
-        keep = x.new_empty(tuple(full), dtype=torch.float32) if pre else None
+        keep = x.new_empty(full, dtype=torch.float32) if pre else None
         ws, nbytes = _workspace(need, workspace, dev)
         _done(lib().falcon_linear_fwd(shape, hx, _p(weight), _p(x_scale), _p(weight_scale), _p(bias), _p(residual), _p(out),
                                       _p(keep), _p(ws), nbytes, _current(dev)), "falcon_linear_fwd")

@@ -651,7 +651,8 @@ bool fits(int64_t I, int64_t J, int64_t K, int e) {
 }  // namespace
 
 bool linear_fits(int e, int64_t tokens, int64_t in, int64_t out) {
-  return fits(out, tokens, in, e) && fits(in, tokens, out, e) && fits(in, out, tokens, e) &&
+  return fits(out, tokens, in, e) && (tokens < 256 || fits(out, tokens / 256 * 256, in, e)) &&     // the rest apart or not
+         fits(in, tokens, out, e) && fits(in, out, tokens, e) &&
          grid_fits((int64_t)sum_blocks(tokens) * ((out * 4 + 255) / 256), 256);
 }
 

@@ -61,7 +61,14 @@ def _on(dev, stream):
         if stream.device != dev:
             raise ValueError(f"stream: must belong to {dev}")
         return torch.cuda.stream(stream)
-    return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    return _HERE if _device_now()() == dev.index else torch.cuda.device(dev)
+
+
+@functools.lru_cache(maxsize=None)
+def _device_now():
+    """The current device's index; by the short way where this torch has one."""
+    import torch
+    return getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 @functools.lru_cache(maxsize=None)
