@@ -52,9 +52,24 @@ template <int P> __device__ __forceinline__ void channel_sums(const f4 &b, const
 constexpr int BWD_CH = 32;
 template <int N> using BwdTile = SsmTile<N, BWD_CH, 64 / N, 16>;
 // Sequences are cut where they make fewer than 128 workgroups, into 256 (2 x 2048 x 768: 92 us with the maps' pass, 104 cut
-// for 512; 1 x 16384 x 1536: 632 and 615).
-// Up to 2048 / N tokens they are left whole (with the forward, 1 x 128 x 512: 37 us, 41 cut; 192: 48 and 42).
-int segment_of(const SeqMap &q, int D, int N) { return ssm_segment(q, D, BWD_CH, 128, 256, 2048 / N); }
+// for 512; 1 x 16384 x 1536: 632 and 615).  Up to 2048 / N tokens they are left whole (with the forward, 1 x 128 x 512: 37
+// us, 41 cut; 192: 48 and 42).  A compute unit holds one workgroup, so w of them, up to 4 rounds, leave the last round
+// partly empty.  There sequences are cut once, into a long segment and the rest: a unit without a long one in the last round
+// takes k rests one after the other, which are as long together.  That is worth r / (k + 1) of a sequence's tiles (2 at least)
+// and costs the rests' maps (with the forward, 4 x 4096 x 1536, w = 192: 714 us, 791 whole; 4 x 2048 x 1024, w = 128: 282,
+// 360; 3 x 500 x 1536, w = 144: 114, 118).
+int segment_of(const SeqMap &q, int D, int N) {
+  const int64_t w = (int64_t)q.n * ((D + BWD_CH - 1) / BWD_CH), rounds = (w + 255) / 256, idle = rounds * 256 - w;
+  if (!q.cu && w >= 128 && rounds <= 4 && idle) {
+    const int64_t k = (w + idle - 1) / idle;
+    if ((int64_t)q.T * rounds >= 128 * (k + 1)) return (int)((q.T * k / (k + 1) + SSM_ALIGN) / SSM_ALIGN * SSM_ALIGN);
+  }
+  return ssm_segment(q, D, BWD_CH, 128, 256, 2048 / N);
+}
+// Workgroups begin in the order of their numbers: the sequences' first segments, which are never the shorter ones, come first.
+__device__ __forceinline__ int bwd_slot(const SeqMap &q, int len, int i) {
+  return q.cu ? i : i % q.n * ((q.T + len - 1) / len) + i / q.n;
+}
 
 // MAPS: only the segment's map (r at its start from zero behind its end, sum of delta) is formed.
 template <typename T, int N, bool MAPS> __global__ __launch_bounds__(BwdTile<N>::THR, MAPS ? 4 : 2) void ssm_bwd(SsmArgs a) {
@@ -69,7 +84,7 @@ template <typename T, int N, bool MAPS> __global__ __launch_bounds__(BwdTile<N>:
   const int groups = (a.D + CH - 1) / CH;
   const SsmPlace place = ssm_place(groups, slots_of(a.seq, a.seg));
   if (!place.any) return;
-  const Segment g = find_segment(a.seq, a.seg, place.slot);
+  const Segment g = find_segment(a.seq, a.seg, bwd_slot(a.seq, a.seg, place.slot));
   const int group = place.group, c0 = group * CH;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tw = wave / L::WIDE, wide = wave % L::WIDE, p = lane % L::P, p4 = p * 4, ch = wide * L::CW + lane / L::P;

@@ -329,3 +329,27 @@ def test_infinite_last_token(T, N):
     assert torch.equal(gc["dC"], g["dC"])
     for k in ("dA", "dB", "d_init"):
         assert torch.equal(gc[k][..., rest], g[k][..., rest]), k
+
+
+@pytest.mark.parametrize("n,T,D,N", [(3, 500, 1536, 16), (4, 300, 1024, 64), (8, 330, 1536, 32)])
+def test_sequences_cut_once(n, T, D, N):
+    """Gradients where sequences are cut into a long segment and the rest, to fill the last round: those of each sequence by
+    itself."""
+    import torch
+    import recurrent_sequence_models_amd as rsm
+    a = inputs(80, (n, T), n, D, N, "bf16")
+    opt = lambda i: dict(D=a["D"], z=a["z"][i], dt_bias=a["bias"], init=a["init"][i])  # noqa: E731
+
+    def grads(i):
+        x = [a[k][i] for k in ("x", "dt")] + [a["A"]] + [a[k][i] for k in ("B", "C")]
+        _, _, states = rsm.selective_scan(*x, chunk_states=True, **opt(i))
+        return rsm.selective_scan_bwd(*x, a["dy"][i], states, d_final=a["d_final"][i], **opt(i))
+
+    g, each = grads(slice(None)), [grads(slice(i, i + 1)) for i in range(n)]
+    for k in ("dx", "ddt", "dB", "dC", "dz", "d_init"):
+        want = torch.cat([e[k] for e in each])
+        step = 2 ** -8 if want.dtype is torch.bfloat16 else 0.0       # each is rounded once, on either side of a border
+        assert ((g[k] - want).float().abs() <= 2 * step * want.float().abs() + 1e-4 * want.float().abs().max()).all(), k
+    for k in ("dA", "dD", "ddt_bias"):
+        want = sum(e[k] for e in each)
+        assert (g[k] - want).abs().max() <= 1e-4 * want.abs().max(), k
