@@ -62,13 +62,13 @@ int segment_of(const SeqMap &q, int D, int N) {
   const int64_t w = (int64_t)q.n * ((D + BWD_CH - 1) / BWD_CH), rounds = (w + 255) / 256, idle = rounds * 256 - w;
   if (!q.cu && w >= 128 && rounds <= 4 && idle) {
     const int64_t k = (w + idle - 1) / idle;
-    if ((int64_t)q.T * rounds >= 128 * (k + 1)) return (int)((q.T * k / (k + 1) + SSM_ALIGN) / SSM_ALIGN * SSM_ALIGN);
+    if ((int64_t)q.T * rounds >= 128 * (k + 1)) return (int)(((int64_t)q.T * k / (k + 1) + SSM_ALIGN) / SSM_ALIGN * SSM_ALIGN);
   }
   return ssm_segment(q, D, BWD_CH, 128, 256, 2048 / N);
 }
 // Workgroups begin in the order of their numbers: the sequences' first segments, which are never the shorter ones, come first.
 __device__ __forceinline__ int bwd_slot(const SeqMap &q, int len, int i) {
-  return q.cu ? i : i % q.n * ((q.T + len - 1) / len) + i / q.n;
+  return q.cu ? i : i % q.n * segments_of(q, len) + i / q.n;
 }
 
 // MAPS: only the segment's map (r at its start from zero behind its end, sum of delta) is formed.

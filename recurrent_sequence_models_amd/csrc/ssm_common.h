@@ -94,17 +94,18 @@ __device__ __forceinline__ float quad_sums(const float (&y)[4], int p) {
 // sequences of the same length have ceil(T / len) each.
 struct Segment { int n, slot, s, e, t0, t1; bool any; };
 
+__host__ __device__ inline int segments_of(const SeqMap &q, int len) { return (q.T - 1) / len + 1; }   // T + len may pass 2^31
 __host__ __device__ inline int slots_of(const SeqMap &q, int len) {
-  return q.cu ? q.T / len + q.n : q.n * ((q.T + len - 1) / len);
+  return q.cu ? q.T / len + q.n : q.n * segments_of(q, len);
 }
 __device__ __forceinline__ int first_slot(const SeqMap &q, int n, int len) {
-  return q.cu ? q.begin(n) / len + n : n * ((q.T + len - 1) / len);
+  return q.cu ? q.begin(n) / len + n : n * segments_of(q, len);
 }
 __device__ __forceinline__ Segment find_segment(const SeqMap &q, int len, int slot) {
   Segment g;
   g.slot = slot;
   if (!q.cu) {
-    g.n = slot / ((q.T + len - 1) / len);
+    g.n = slot / segments_of(q, len);
   } else {
     int lo = 0, more = q.n;
     while (more > 1) {
