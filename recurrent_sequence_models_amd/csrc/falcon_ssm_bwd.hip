@@ -16,10 +16,11 @@
 // number of lanes (16 instructions for 8 sums over 16 lanes), over the waves in LDS, and over
 // workgroups in a pass of their own, in order.
 //
-// Bound: the vector unit: 120 instructions for 4 states and a step (67 in the way back, 27 in the maps of both
-// directions, 26 for what a tile's loading, gates and results cost).  A lane's decays and states of 16 steps take 132
-// registers, so a SIMD has two waves.  Measured, N = 16, bf16: 4 x 4096 x 1536 543 us (192 workgroups on 256 compute
-// units), and 18 us for dB and dC over the 48 groups of channels.
+// Bound: the vector unit: 112 instructions for 4 states and a step (62 in the way back, 32 in the maps of both
+// directions and the run forward, 18 for what a tile's loading, gates and results cost), 79 % busy.  A lane's decays and
+// states of 16 steps take 132 registers, so a SIMD has two waves.  Measured, N = 16, bf16: 4 x 4096 x 1536 430 us and 45 for
+// the maps (192 sequences' workgroups on 256 compute units; 545 with whole sequences), and 18 us for dB and dC over the 48
+// groups of channels.
 #include "ssm_common.h"
 
 namespace falcon {
@@ -115,12 +116,12 @@ template <typename T, int N, bool MAPS> __global__ __launch_bounds__(BwdTile<N>:
   f4 dA{0.f, 0.f, 0.f, 0.f};
   float dD[V] = {}, dbias[V] = {}, total = 0.f;
   const int64_t tokens = a.seq.tokens();
-  Few<T, V> nx, nd, nz, ng;                   // the next tile's entries of this thread
+  Few<T, V> nx{}, nd, nz, ng;                 // the next tile's entries of this thread
   Few<T, BV> nB, nC;
   f4 nh{0.f, 0.f, 0.f, 0.f};                  // and its first state
   auto load = [&](int t) {
     const int q = min(ls, g.t1 - 1 - t), qb = min(bs, g.t1 - 1 - t), cc = lon ? lcc : 0;
-    fetch(entry<T>(a.x, a.ldx, t, q, cc), nx);
+    if constexpr (!MAPS) fetch(entry<T>(a.x, a.ldx, t, q, cc), nx);
     fetch(entry<T>(a.dt, a.lddt, t, q, cc), nd);
     if (a.z) fetch(entry<T>(a.z, a.ldz, t, q, cc), nz);
     fetch(entry<T>(a.dy, a.D, t, q, cc), ng);
