@@ -644,8 +644,8 @@ int falcon_ssm_fwd(const falcon_ssm_shape_t *shape, const int32_t *cu_seqlens, f
                    const float *dt_bias, const float *init, float *final_state, void *y, float *chunk_states,
                    void *workspace, size_t workspace_bytes, void *stream);
 
-/* Bytes of workspace of the backward: partial sums of dB and dC for every 32 channels, and of
- * the parameters' gradients. */
+/* Bytes of workspace of the backward: partial sums of dB and dC for every 32 channels and of the
+ * parameters' gradients, and the maps of segments.  0 for invalid shapes. */
 size_t falcon_ssm_bwd_workspace(const falcon_ssm_shape_t *shape, int packed);
 
 /* Gradients of <d_y, y> + <d_final, final_state>, from the chunk_states the forward wrote for

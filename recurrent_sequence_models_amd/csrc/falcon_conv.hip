@@ -168,7 +168,8 @@ template <typename T, int W> __global__ __launch_bounds__(THR) void conv_bwd(Con
       // AHEAD tokens from t on; (ends) some may be behind the last, behind this thread's own, or finish one before those
       auto block = [&](auto ends) __attribute__((always_inline)) {
         constexpr bool ENDS = decltype(ends)::value;
-        const T *px = static_cast<const T *>(a.x) + (int64_t)t * a.ldx + c, *pg = static_cast<const T *>(a.dy) + (size_t)t * a.D + c;
+        const T *px = static_cast<const T *>(a.x) + (int64_t)t * a.ldx + c;
+        const T *pg = static_cast<const T *>(a.dy) + (size_t)t * a.D + c;
         T *out = static_cast<T *>(a.dx) + (int64_t)(t - (W - 1)) * a.lddx + c;
         Few<T, E> x[AHEAD], g[AHEAD];
 #pragma unroll

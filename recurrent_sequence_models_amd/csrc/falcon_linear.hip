@@ -44,8 +44,10 @@ __device__ __forceinline__ void mma(f16v &d, const Frag<e4m3_wide> &a, const Fra
 }
 typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ bf8 widened(unsigned lo, unsigned hi) {
-  const bf2 p = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false), q = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true);
-  const bf2 r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false), t = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true);
+  const bf2 p = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false);
+  const bf2 q = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true);
+  const bf2 r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false);
+  const bf2 t = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true);
   return bf8{p[0], p[1], q[0], q[1], r[0], r[1], t[0], t[1]};
 }
 template <> struct Frag<e4m3> { int8v v; };
@@ -65,7 +67,6 @@ template <typename T> constexpr int KM = std::is_same_v<T, e4m3> ? 64 : 16;   //
 template <typename T, int ROWS, bool COLS> struct OperandTile {
   typedef Tile<T, COLS ? ROWS : KE<T>> Ti;
   static constexpr int TR = COLS ? KE<T> : ROWS;          // rows in memory
-  static constexpr int READS = COLS ? (sizeof(T) == 4 ? 8 : 2) : sizeof(T) == 2 || std::is_same_v<T, e4m3_wide> ? 1 : 2;   // of LDS, a fragment
   static constexpr int CHUNKS = TR * Ti::CPR;             // 16 bytes each
   // By rows: the LDS address of this lane's part of k block 0 of the 32 rows from row0, in a tile at `tile`.  Tiles are
   // aligned to a row (128 bytes), so the swizzled chunk of another block differs in the address's low bits alone.
@@ -212,7 +213,8 @@ __device__ __forceinline__ float slope(float p, int act) {
     return s * fmaf(p, 1.f - s, 1.f);
   }
   if (act == FALCON_GELU)
-    return 0.5f * (1.f + erff(p * 0.70710678118654752f)) + p * 0.39894228040143268f * __builtin_amdgcn_exp2f(p * p * -0.72134752044448170f);
+    return 0.5f * (1.f + erff(p * 0.70710678118654752f)) +
+           p * 0.39894228040143268f * __builtin_amdgcn_exp2f(p * p * -0.72134752044448170f);
   return 1.f;
 }
 
@@ -340,7 +342,8 @@ __global__ __launch_bounds__(64 * WL * WR) void product(LinearArgs a) {
   };
   // step s's tiles have arrived, and those of the step before are read no more
   auto arrive = [&](int s, int buffer) __attribute__((always_inline)) {
-    if (STAGES > 2 && s + STAGES - 2 < s1) copies_done_but<(STAGES - 2) * (Copier<T, TL, LC, THR>::PER + Copier<T, TR, RC, THR>::PER)>();
+    constexpr int A_STEP = Copier<T, TL, LC, THR>::PER + Copier<T, TR, RC, THR>::PER;     // copies of a thread
+    if (STAGES > 2 && s + STAGES - 2 < s1) copies_done_but<(STAGES - 2) * A_STEP>();
     else copies_done();
     if (s == steps - 1) {
       cl.clear(left[buffer], s * KE<T>, tid);
@@ -489,7 +492,8 @@ template <typename T, typename O, int MT> __global__ __launch_bounds__(64 * FEW_
 
 // ---- The gradient of the pre-activation ------------------------------------------------
 // d = dy act'(pre), rounded to the operands' type as the products take it, and the sums over tokens of the
-// unrounded d for the bias (pre is kept in fp32: rounded to bf16 it would leave 0.2 % in that sum).  Thread: 16 bytes of columns, every 16th token of a workgroup's run.
+// unrounded d for the bias (pre is kept in fp32: rounded to bf16 it would leave 0.2 % in that sum).  Thread: 16 bytes of
+// columns, every 16th token of a workgroup's run.
 constexpr int DP_LANES = 16, DP_ROWS = 256 / DP_LANES, DP_RUN = 128;
 template <typename T> __global__ __launch_bounds__(256) void pre_gradient(LinearArgs a, const void *dy, int64_t lddy, void *d) {
   constexpr int E = PER16<T>;
@@ -577,7 +581,8 @@ Plan plan_of(int64_t I, int64_t J, int64_t K, int e) {
   if (J > FEW_TOKENS) return p;
   const int64_t rows = J <= 16 ? 32 : J <= 32 ? 48 : 80, groups = over(I, 16);
   const int64_t few = over(groups, 256) * rows * K * e, step = p.form == Form::small ? 2 * 64 * KB : 2 * 128 * KB;
-  const int64_t tiles = over(p.tiles * p.splits, 256) * (over(K * e, KB) / p.splits) * step, quarters = e < 4 ? 4 : p.form == Form::small ? 5 : 10;
+  const int64_t tiles = over(p.tiles * p.splits, 256) * (over(K * e, KB) / p.splits) * step;
+  const int64_t quarters = e < 4 ? 4 : p.form == Form::small ? 5 : 10;
   if (p.form == Form::large || few <= tiles * quarters / 4 + 65536) return {Form::few, 1, groups};
   return p;
 }
@@ -591,7 +596,8 @@ template <typename T, typename O, bool LC, bool RC> hipError_t multiply(const Pl
   } else if (p.form == Form::deep) {
     hipLaunchKernelGGL((product<T, O, LC, RC, 128, 128, 2, 4, 4>), grid, dim3(512), 0, s, a);
   } else if (p.form == Form::medium) {
-    constexpr int WR = sizeof(T) < 4 ? 4 : 2;    // 4096 x 2048 -> 2048 e4m3: 24.2 us, 26.7 with 2; its training in fp32 859, 825 with 2
+    // 4096 x 2048 -> 2048 e4m3: 24.2 us, 26.7 with 2; in fp32, with its gradients, 859 and 825
+    constexpr int WR = sizeof(T) < 4 ? 4 : 2;
     hipLaunchKernelGGL((product<T, O, LC, RC, 128, 128, 2, WR, 2>), grid, dim3(128 * WR), 0, s, a);
   } else if constexpr (sizeof(T) < 4) {
     hipLaunchKernelGGL((product<T, O, LC, RC, 256, 256, 2, 4, 2>), grid, dim3(512), 0, s, a);

@@ -279,7 +279,9 @@ bool ssm_segmented(const SeqMap &q, int seg) { return q.T > seg; }
 
 int ssm_chunk(int N) { return 1024 / N; }
 
-bool ssm_step_fits(int n, int D, int N) { return grid_fits((int64_t)n * (((int64_t)D * N / 4 + STEP_THR - 1) / STEP_THR), STEP_THR); }
+bool ssm_step_fits(int n, int D, int N) {
+  return grid_fits((int64_t)n * (((int64_t)D * N / 4 + STEP_THR - 1) / STEP_THR), STEP_THR);
+}
 
 bool ssm_fits(SeqMap seq, int D, int N) {
   const int64_t groups = (D + FWD_CH - 1) / FWD_CH;

@@ -42,8 +42,7 @@ template <int V> __device__ __forceinline__ void load_few(const __bf16 *p, float
   } else o[0] = (float)*p;
 }
 // Entries `col` on of token t + row of an array, as scalar base plus 32 bits a lane: t is the same in every lane, and
-// token strides are at most SSM_MOST_STEP bytes.
-constexpr int64_t SSM_MOST_STEP = 1 << 24;
+// token strides are at most 2^24 bytes.
 template <typename T> __device__ __forceinline__ const T *entry(const void *p, int64_t ld, int t, int row, int col) {
   const char *base = static_cast<const char *>(p) + (int64_t)t * ld * (int64_t)sizeof(T);
   return reinterpret_cast<const T *>(base + (unsigned)(row * ((int)ld * (int)sizeof(T)) + col * (int)sizeof(T)));
