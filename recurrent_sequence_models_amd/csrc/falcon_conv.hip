@@ -11,11 +11,10 @@
 // last W - 1 inputs (backward: and the W unfinished gradients) in registers.  The W - 1 tokens next to
 // a run are read again, from the cache as a rule: the runs beside belong to the same workgroup.
 // In the backward pass d is formed again for the W - 1 tokens behind the run, rather than
-// exchanged.  Blocks of tokens inside a run need no comparisons (39 us backward with them everywhere).  Bound: HBM, x and
+// exchanged.  Blocks of tokens inside a run need no comparisons (backward 3 of 39 us).  Bound: HBM, x and
 // y (backward: x, dy and dx) once, and backward the vector unit beside it.
-// Measured, 4 x 4096 x 1536 bf16, 4 taps, silu: forward 25 us (101 MB at 4.1 TB/s), backward 36 us (151 MB at 4.2; 42
-// with 4 waves a SIMD, which spill; 49 with 8 channels a thread, which leave two) and 5 us to add the weights'
-// gradients; 64 tokens x 4096: 3.9 us.
+// Measured, 4 x 4096 x 1536 bf16, 4 taps, silu: forward 24 us (101 MB at 4.2 TB/s), backward 33 us (151 MB at 4.6) and 5 us
+// to add the weights' gradients; 64 tokens x 4096: 3.9 us.
 #include <type_traits>
 
 #include "block_kernels.h"
@@ -25,8 +24,9 @@ namespace falcon {
 namespace {
 
 constexpr int THR = 256;
-// lanes side by side over channels, and runs of a workgroup; forward and backward
-constexpr int LANES_F = 16, RUNS_F = THR / LANES_F, LANES_B = 32, RUNS_B = THR / LANES_B;
+// A wave's lanes lie side by side over channels, and a run is one wave's, so where it stands is the same in all of them
+// (4 x 4096 x 1536 bf16: 25 us with runs of 16 lanes, backward 36 of 32; 13 packed sequences, 9001 x 2048: 29 and 23).
+constexpr int LANES = 64, RUNS = THR / LANES;
 constexpr int AHEAD = 4;                                   // tokens whose loads are in flight together, W - 1 at least
 
 // This thread's filters: w[k][j] of tap k, channel j; bias.
@@ -90,12 +90,12 @@ __device__ __forceinline__ void copy_empty(const ConvArgs &a, const void *from, 
 
 template <typename T, int W> __global__ __launch_bounds__(THR) void conv_fwd(ConvArgs a) {
   constexpr int E = PER16<T>;
-  const int c = (blockIdx.y * LANES_F + threadIdx.x % LANES_F) * E;
-  const int run = blockIdx.x * RUNS_F + threadIdx.x / LANES_F, total = a.seq.tokens();
+  const int c = (blockIdx.y * LANES + threadIdx.x % LANES) * E;
+  const int run = blockIdx.x * RUNS + __builtin_amdgcn_readfirstlane(threadIdx.x / LANES), total = a.seq.tokens();
   if (c >= a.D) return;
   float w[W][E], b[E];
   load_filters<W, E>(a, c, w, b);
-  copy_empty<T, W, E>(a, a.init, a.final_state, run, gridDim.x * RUNS_F, c);
+  copy_empty<T, W, E>(a, a.init, a.final_state, run, gridDim.x * RUNS, c);
   const int64_t t0 = (int64_t)run * a.run;
   if (t0 >= total) return;
   const int last = (int)min(t0 + a.run, (int64_t)total);
@@ -139,13 +139,13 @@ template <typename T, int W> __global__ __launch_bounds__(THR) void conv_fwd(Con
 
 template <typename T, int W> __global__ __launch_bounds__(THR) void conv_bwd(ConvArgs a) {
   constexpr int E = 4;
-  const int col = threadIdx.x % LANES_B, c = (blockIdx.y * LANES_B + col) * E;
-  const int run = blockIdx.x * RUNS_B + threadIdx.x / LANES_B, total = a.seq.tokens();
+  const int col = threadIdx.x % LANES, c = (blockIdx.y * LANES + col) * E;
+  const int run = blockIdx.x * RUNS + __builtin_amdgcn_readfirstlane(threadIdx.x / LANES), total = a.seq.tokens();
   const bool in = c < a.D;
   float w[W][E], b[E], dw[W][E] = {}, db[E] = {};
   if (in) {
     load_filters<W, E>(a, c, w, b);
-    copy_empty<T, W, E>(a, a.d_final, a.d_init, run, gridDim.x * RUNS_B, c);
+    copy_empty<T, W, E>(a, a.d_final, a.d_init, run, gridDim.x * RUNS, c);
   }
   const int64_t t0 = (int64_t)run * a.run;
   const int last = (int)min(t0 + a.run, (int64_t)total);
@@ -238,19 +238,19 @@ template <typename T, int W> __global__ __launch_bounds__(THR) void conv_bwd(Con
   }
   if (!a.part) return;
   // the workgroup's sums for the weights, over its runs in order
-  __shared__ __align__(16) float sum[RUNS_B][LANES_B][E];
+  __shared__ __align__(16) float sum[RUNS][LANES][E];
   float *out = a.part + (size_t)blockIdx.x * a.D * (W + 1);
 #pragma unroll
   for (int k = 0; k <= W; ++k) {
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < E; ++j) sum[threadIdx.x / LANES_B][col][j] = k < W ? dw[k < W ? k : 0][j] : db[j];
+    for (int j = 0; j < E; ++j) sum[threadIdx.x / LANES][col][j] = k < W ? dw[k < W ? k : 0][j] : db[j];
     __syncthreads();
-    const int cc = blockIdx.y * LANES_B * E + threadIdx.x;
-    if (threadIdx.x < LANES_B * E && cc < a.D) {
+    const int cc = blockIdx.y * LANES * E + threadIdx.x;
+    if (threadIdx.x < LANES * E && cc < a.D) {
       float v = 0.f;
 #pragma unroll
-      for (int r = 0; r < RUNS_B; ++r) v += sum[r][threadIdx.x / E][threadIdx.x % E];
+      for (int r = 0; r < RUNS; ++r) v += sum[r][threadIdx.x / E][threadIdx.x % E];
       out[k < W ? (size_t)cc * W + k : (size_t)a.D * W + cc] = v;
     }
   }
@@ -284,15 +284,15 @@ template <typename T, int W> __global__ __launch_bounds__(STEP_THR) void conv_st
 }
 
 // A pass's shape: channels of a workgroup, runs of it, and the tokens of a run.  Long runs read fewer tokens twice, short
-// ones make more workgroups (4 x 4096 x 1536 bf16: 25.1 and 42 us with runs twice as long, backward 54 with 16).
+// ones make more workgroups (4 x 4096 x 1536 bf16, 24 and 33 us: 30 and 36 with runs half as long, 24 and 41 twice).
 struct Shape {
   int cols, runs, run;
   dim3 grid;
 };
 Shape shape_of(SeqMap seq, int D, bool bf16, bool back) {
   Shape s;
-  s.cols = back ? LANES_B * 4 : LANES_F * (bf16 ? 8 : 4);
-  s.runs = back ? RUNS_B : RUNS_F;
+  s.cols = LANES * (bf16 && !back ? 8 : 4);
+  s.runs = RUNS;
   const int64_t wide = (D + s.cols - 1) / s.cols, tokens = seq.tokens();
   s.run = back ? 32 : 16;
   while (s.run > 4 && (tokens + s.run * s.runs - 1) / (s.run * s.runs) * wide < 512) s.run /= 2;
