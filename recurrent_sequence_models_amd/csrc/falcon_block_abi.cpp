@@ -176,6 +176,7 @@ int falcon_conv_bwd(const falcon_conv_shape_t *s, const int32_t *cu, falcon_head
   FALCON_TRY(maybe(db, 4));
   FALCON_TRY(maybe(d_init, 16));
   FALCON_TRY(distinct(d_init, d_final));
+  FALCON_TRY(distinct(d_init, init));     // runs behind a sequence's first one may read it still
   FALCON_TRY(distinct(dx.data, x.data));
   FALCON_TRY(distinct(dx.data, d_y));
   if (dw || db) FALCON_TRY(check_workspace(ws, ws_bytes, falcon_conv_bwd_workspace(s, cu != nullptr)));

@@ -238,3 +238,20 @@ def test_sizes_past_32_bits():
                         (block._ssm_plan, (1, 2 ** 31, 1, 8, 16, 1, False)), (block._linear_plan, (1, 2 ** 32 + 64, 64, 64, 0, 1))):
         with pytest.raises(ValueError, match="2\\^31"):
             call(*sizes)
+
+
+# ---- The same array as input and output, where others read it late --------------------------------
+
+def at(k):
+    """The k-th of arrays that are not the same."""
+    return (k + 1) * P
+
+
+CONV = dict(x=H(at(0)), w=at(1), b=at(2), init=at(3), dy=at(4), df=at(5), dx=H(at(6)), dw=at(7), db=at(8), di=at(9), ws=at(10))
+
+
+@cpu_only
+def test_conv_bwd_initial_state_and_its_gradient():
+    """The run that owns a sequence's first token writes d_init, while runs behind it may read init still."""
+    for cu in (None, at(11)):
+        assert conv_bwd(conv_shape(), cu=cu, **{**CONV, "di": CONV["init"]}) == INVALID
