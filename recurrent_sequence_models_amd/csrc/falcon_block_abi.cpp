@@ -404,9 +404,16 @@ int falcon_linear_fwd(const falcon_linear_shape_t *s, falcon_heads_t x, const vo
   FALCON_TRY(maybe(residual, 16));
   FALCON_TRY(need(y, 16));
   FALCON_TRY(maybe(pre, 16));
-  for (const void *in : {x.data, (const void *)pre}) FALCON_TRY(distinct(y, in));
+  FALCON_TRY(distinct(y, pre));
   FALCON_TRY(distinct(pre, residual));
   FALCON_TRY(check_workspace(ws, ws_bytes, falcon_linear_fwd_workspace(s)));
+  // Workgroups store while others copy operands.  One token's bias and scales of W are read by the threads that store there.
+  for (const void *out : {(const void *)y, (const void *)pre}) {
+    for (const void *in : {x.data, weight, (const void *)x_scale}) FALCON_TRY(distinct(out, in));
+    if (s->tokens > 1) {
+      for (const void *in : {weight_scale, bias}) FALCON_TRY(distinct(out, in));
+    }
+  }
   falcon::LinearArgs a{};
   a.left = weight; a.ldl = s->in;
   a.right = x.data; a.ldr = x.token_stride;

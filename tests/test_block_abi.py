@@ -255,3 +255,19 @@ def test_conv_bwd_initial_state_and_its_gradient():
     """The run that owns a sequence's first token writes d_init, while runs behind it may read init still."""
     for cu in (None, at(11)):
         assert conv_bwd(conv_shape(), cu=cu, **{**CONV, "di": CONV["init"]}) == INVALID
+
+
+LINEAR = dict(x=H(at(0)), w=at(1), b=at(2), r=at(3), y=at(4), pre=at(5), ws=at(6))
+
+
+@cpu_only
+@pytest.mark.parametrize("out,ins", [("y", "w sx sw b"), ("pre", "x w sx sw b")])
+def test_linear_outputs_over_operands(out, ins):
+    """Workgroups store their tiles while others copy operands still, and rows while others read scales and the bias."""
+    bits, more = linear_shape(dtype=2, out_dtype=0), dict(sx=at(7), sw=at(8))
+    for name in ins.split():
+        for s, call in ((linear_shape(), LINEAR), (linear_shape(dtype=0, out_dtype=0), LINEAR), (bits, {**LINEAR, **more})):
+            if name in call:
+                p = call[name]
+                assert linear(s, **{**call, out: p.data if name == "x" else p}) == INVALID, name
+    assert linear(linear_shape(), **{**LINEAR, "pre": LINEAR["y"]}) == INVALID

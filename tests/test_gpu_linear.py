@@ -210,3 +210,14 @@ def test_past_32_bits():
     y, _ = rsm.linear(wide[:, :K], w)
     z, _ = rsm.linear(wide[:, :K].contiguous(), w)
     assert torch.equal(y, z)
+
+
+def test_one_token_over_its_bias():
+    """One token's bias may be where its result goes: the threads that read it store there."""
+    import torch
+    import recurrent_sequence_models_amd as rsm
+    for K, N in ((80, 72), (8208, 1016)):                    # 16 rows of W a workgroup, and tiles with k in parts
+        x, w, b = rand(1, K), rand(2, N, K), rand(3, N)
+        want, _ = rsm.linear(x, w, bias=b)
+        y, _ = rsm.linear(x, w, bias=b, out=b)
+        assert y is b and torch.equal(b, want)
