@@ -2,6 +2,7 @@
 #pragma once
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "falcon.h"
 #include "layer_kernels.h"
@@ -27,6 +28,12 @@ inline int check_workspace(const void *ws, size_t have, size_t want) {
 
 // An output that is one of the inputs where others read those late.  (Partial overlaps are the caller's to avoid.)
 inline int distinct(const void *out, const void *in) { return out && out == in ? FALCON_ERR_INVALID_ARG : FALCON_OK; }
+
+inline int apart(const void *out, std::initializer_list<const void *> ins) {
+  for (const void *in : ins)
+    if (distinct(out, in) != FALCON_OK) return FALCON_ERR_INVALID_ARG;
+  return FALCON_OK;
+}
 
 // [tokens, width] of entries of `e` bytes at a pointer with a token stride.
 inline int check_rows(const void *p, int64_t stride, int64_t tokens, int64_t width, int e) {

@@ -409,10 +409,8 @@ int falcon_linear_fwd(const falcon_linear_shape_t *s, falcon_heads_t x, const vo
   FALCON_TRY(check_workspace(ws, ws_bytes, falcon_linear_fwd_workspace(s)));
   // Workgroups store while others copy operands.  One token's bias and scales of W are read by the threads that store there.
   for (const void *out : {(const void *)y, (const void *)pre}) {
-    for (const void *in : {x.data, weight, (const void *)x_scale}) FALCON_TRY(distinct(out, in));
-    if (s->tokens > 1) {
-      for (const void *in : {weight_scale, bias}) FALCON_TRY(distinct(out, in));
-    }
+    FALCON_TRY(apart(out, {x.data, weight, x_scale}));
+    if (s->tokens > 1) FALCON_TRY(apart(out, {weight_scale, bias}));
   }
   falcon::LinearArgs a{};
   a.left = weight; a.ldl = s->in;
@@ -450,6 +448,10 @@ int falcon_linear_bwd(const falcon_linear_shape_t *s, falcon_heads_t x, const vo
   FALCON_TRY(distinct(dx.data, x.data));
   FALCON_TRY(distinct(dweight, weight));
   FALCON_TRY(check_workspace(ws, ws_bytes, falcon_linear_bwd_workspace(s)));
+  // dbias, dx and dweight are written in this order; a product copies its operands while others' tiles are stored
+  FALCON_TRY(distinct(dx.data, weight));
+  FALCON_TRY(apart(dweight, {x.data, d_y.data, dx.data}));
+  FALCON_TRY(apart(dbias, {x.data, d_y.data, weight, dx.data, dweight}));
   falcon::LinearGrads g{};
   g.x = x.data; g.ldx = x.token_stride;
   g.w = weight;

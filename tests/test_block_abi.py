@@ -271,3 +271,20 @@ def test_linear_outputs_over_operands(out, ins):
                 p = call[name]
                 assert linear(s, **{**call, out: p.data if name == "x" else p}) == INVALID, name
     assert linear(linear_shape(), **{**LINEAR, "pre": LINEAR["y"]}) == INVALID
+
+
+BACK = dict(x=H(at(0)), w=at(1), pre=at(2), dy=H(at(3)), dx=H(at(4)), dw=at(5), db=at(6), ws=at(7))
+
+
+@cpu_only
+@pytest.mark.parametrize("out,ins", [("dx", "w"), ("dw", "x dy"), ("db", "x w dy")])
+def test_linear_bwd_outputs_over_operands(out, ins):
+    """The products run after the bias's gradient, dx before dweight, and copy operands while tiles are stored."""
+    as_out = H if out == "dx" else (lambda p: p)
+    for name in ins.split():
+        p = BACK[name]
+        for act in (0, 1):
+            assert linear_bwd(linear_shape(activation=act), **{**BACK, out: as_out(getattr(p, "data", p))}) == INVALID, name
+    for other in {"dx", "dw", "db"} - {out}:
+        p = BACK[other]
+        assert linear_bwd(linear_shape(), **{**BACK, out: as_out(getattr(p, "data", p))}) == INVALID, other
