@@ -35,6 +35,12 @@ inline int apart(const void *out, std::initializer_list<const void *> ins) {
   return FALCON_OK;
 }
 
+// A dense output that is an input of another stride: its tokens lie where others' inputs are.  (Of the same, for what
+// is read token by token: an entry is read by the wave that writes it.)
+inline int same_rows(const void *out, const void *in, int64_t stride, int64_t tokens, int64_t width) {
+  return tokens > 1 && stride != width ? distinct(out, in) : FALCON_OK;
+}
+
 // [tokens, width] of entries of `e` bytes at a pointer with a token stride.
 inline int check_rows(const void *p, int64_t stride, int64_t tokens, int64_t width, int e) {
   if (need(p, 16) != FALCON_OK || stride < width || stride > INT64_MAX / 16 / tokens || (stride * e) % 16 != 0)

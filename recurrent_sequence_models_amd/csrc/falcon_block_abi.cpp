@@ -198,6 +198,9 @@ int falcon_conv_step(const falcon_conv_shape_t *s, falcon_heads_t x, const float
   FALCON_TRY(need(state, 16));
   FALCON_TRY(need(state_out, 16));
   FALCON_TRY(need(y, 16));
+  FALCON_TRY(apart(y, {w, bias, state, state_out}));
+  FALCON_TRY(apart(state_out, {x.data, w, bias}));
+  FALCON_TRY(same_rows(y, x.data, x.token_stride, s->batch, s->width));
   falcon::ConvArgs a = conv_args(s, nullptr, x, w, bias);
   a.init = state;
   a.final_state = state_out;
@@ -350,6 +353,9 @@ int falcon_ssm_step(const falcon_ssm_shape_t *s, falcon_heads_t x, falcon_heads_
   FALCON_TRY(need(state, 16));
   FALCON_TRY(need(state_out, 16));
   FALCON_TRY(need(y, 16));
+  FALCON_TRY(apart(y, {A, B.data, C.data, D, bias, state, state_out}));
+  FALCON_TRY(apart(state_out, {x.data, dt.data, A, B.data, C.data, D, z.data, bias}));
+  for (const falcon_heads_t &t : {x, dt, z}) FALCON_TRY(same_rows(y, t.data, t.token_stride, s->batch, s->width));
   falcon::SsmArgs a = ssm_args(s, nullptr, x, dt, A, B, C, D, z, bias);
   a.seq.T = 1;
   a.init = state;

@@ -288,3 +288,26 @@ def test_linear_bwd_outputs_over_operands(out, ins):
     for other in {"dx", "dw", "db"} - {out}:
         p = BACK[other]
         assert linear_bwd(linear_shape(), **{**BACK, out: as_out(getattr(p, "data", p))}) == INVALID, other
+
+
+CSTEP = dict(x=H(at(0)), w=at(1), b=at(2), st=at(3), so=at(4), y=at(5))
+SSTEP = dict(x=H(at(0)), dt=H(at(1)), A=at(2), B=H(at(3)), C=H(at(4)), D=at(5), z=H(at(6)), b=at(7), st=at(8), so=at(9), y=at(10))
+
+
+def refused(call, s, args, out, ins, code=INVALID):
+    for name in ins.split():
+        p = args[name]
+        assert call(s, **{**args, out: getattr(p, "data", p)}) == code, (out, name)
+
+
+@cpu_only
+def test_single_tokens_over_what_others_read():
+    """Filters, and B and C, are read for every sequence or channel; rows of another stride are other tokens' too."""
+    s, t = conv_shape(), ssm_shape()
+    refused(conv_step, s, CSTEP, "y", "w b st so")
+    refused(conv_step, s, CSTEP, "so", "x w b")
+    refused(ssm_step, t, SSTEP, "y", "A B C D b st so")
+    refused(ssm_step, t, SSTEP, "so", "x dt A B C D z b")
+    refused(conv_step, s, {**CSTEP, "x": H(at(0), 128)}, "y", "x")
+    for name in ("x", "dt", "z"):
+        refused(ssm_step, t, {**SSTEP, name: H(at(0), 128)}, "y", name)
