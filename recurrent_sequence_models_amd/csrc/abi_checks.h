@@ -35,10 +35,10 @@ inline int apart(const void *out, std::initializer_list<const void *> ins) {
   return FALCON_OK;
 }
 
-// A dense output that is an input of another stride: its tokens lie where others' inputs are.  (Of the same, for what
-// is read token by token: an entry is read by the wave that writes it.)
-inline int same_rows(const void *out, const void *in, int64_t stride, int64_t tokens, int64_t width) {
-  return tokens > 1 && stride != width ? distinct(out, in) : FALCON_OK;
+// An output that is an input of another stride: its tokens lie where others' inputs are.  (Of the same, for what is read
+// token by token: an entry is read by the wave that writes it.)
+inline int same_rows(const void *out, int64_t out_stride, const void *in, int64_t stride, int64_t tokens) {
+  return tokens > 1 && stride != out_stride ? distinct(out, in) : FALCON_OK;
 }
 
 // [tokens, width] of entries of `e` bytes at a pointer with a token stride.

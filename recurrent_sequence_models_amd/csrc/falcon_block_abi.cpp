@@ -4,6 +4,8 @@
 //
 // Host side only, as falcon_layer_abi.cpp: every argument is validated before the first HIP
 // call.
+#include <iterator>
+
 #include "abi_checks.h"
 #include "block_kernels.h"
 
@@ -200,7 +202,7 @@ int falcon_conv_step(const falcon_conv_shape_t *s, falcon_heads_t x, const float
   FALCON_TRY(need(y, 16));
   FALCON_TRY(apart(y, {w, bias, state, state_out}));
   FALCON_TRY(apart(state_out, {x.data, w, bias}));
-  FALCON_TRY(same_rows(y, x.data, x.token_stride, s->batch, s->width));
+  FALCON_TRY(same_rows(y, s->width, x.data, x.token_stride, s->batch));
   falcon::ConvArgs a = conv_args(s, nullptr, x, w, bias);
   a.init = state;
   a.final_state = state_out;
@@ -285,9 +287,12 @@ int falcon_ssm_fwd(const falcon_ssm_shape_t *s, const int32_t *cu, falcon_heads_
   FALCON_TRY(maybe(final_state, 16));
   FALCON_TRY(need(y, 16));
   FALCON_TRY(maybe(chunk_states, 16));
-  FALCON_TRY(distinct(final_state, init));
-  for (const void *in : {B.data, C.data}) FALCON_TRY(distinct(y, in));
   FALCON_TRY(check_workspace(ws, ws_bytes, falcon_ssm_fwd_workspace(s, cu != nullptr)));
+  FALCON_TRY(apart(y, {A, B.data, C.data, D, bias, init, final_state, chunk_states}));
+  FALCON_TRY(apart(final_state, {x.data, dt.data, A, B.data, C.data, D, z.data, bias, init, chunk_states}));
+  FALCON_TRY(apart(chunk_states, {x.data, dt.data, A, B.data, C.data, D, z.data, bias, init}));
+  for (const falcon_heads_t &t : {x, dt, z})
+    FALCON_TRY(same_rows(y, s->width, t.data, t.token_stride, seq_tokens(s->batch, s->seqlen, cu)));
   falcon::SsmArgs a = ssm_args(s, cu, x, dt, A, B, C, D, z, bias);
   a.init = init;
   a.final_state = final_state;
@@ -331,8 +336,18 @@ int falcon_ssm_bwd(const falcon_ssm_shape_t *s, const int32_t *cu, falcon_heads_
   FALCON_TRY(maybe(dD, 4));
   FALCON_TRY(maybe(ddt_bias, 4));
   FALCON_TRY(maybe(d_init, 16));
-  FALCON_TRY(distinct(d_init, d_final));
   FALCON_TRY(check_workspace(ws, ws_bytes, falcon_ssm_bwd_workspace(s, cu != nullptr)));
+  // A pass over the sequences writes dx, ddt, dz and d_init; those behind it, which read no inputs, the rest.
+  FALCON_TRY(apart(d_init, {x.data, dt.data, A, B.data, C.data, D, z.data, bias, chunk_states, d_y, d_final}));
+  const falcon_heads_out_t rows[] = {dx, ddt, z.data ? dz : falcon_heads_out_t{}};
+  for (const falcon_heads_out_t &o : rows) {
+    FALCON_TRY(apart(o.data, {A, B.data, C.data, D, bias, chunk_states, d_final}));
+    for (const falcon_heads_t &t : {x, dt, z}) FALCON_TRY(same_rows(o.data, o.token_stride, t.data, t.token_stride, tokens));
+    FALCON_TRY(same_rows(o.data, o.token_stride, d_y, s->width, tokens));
+  }
+  const void *outs[] = {dx.data, ddt.data, rows[2].data, dB.data, dC.data, dA, dD, ddt_bias, d_init};
+  for (const void **o = outs; o != std::end(outs); ++o)
+    for (const void **p = outs; p != o; ++p) FALCON_TRY(distinct(*o, *p));
   falcon::SsmArgs a = ssm_args(s, cu, x, dt, A, B, C, D, z, bias);
   a.states = const_cast<float *>(chunk_states);
   a.dy = d_y;
@@ -355,7 +370,7 @@ int falcon_ssm_step(const falcon_ssm_shape_t *s, falcon_heads_t x, falcon_heads_
   FALCON_TRY(need(y, 16));
   FALCON_TRY(apart(y, {A, B.data, C.data, D, bias, state, state_out}));
   FALCON_TRY(apart(state_out, {x.data, dt.data, A, B.data, C.data, D, z.data, bias}));
-  for (const falcon_heads_t &t : {x, dt, z}) FALCON_TRY(same_rows(y, t.data, t.token_stride, s->batch, s->width));
+  for (const falcon_heads_t &t : {x, dt, z}) FALCON_TRY(same_rows(y, s->width, t.data, t.token_stride, s->batch));
   falcon::SsmArgs a = ssm_args(s, nullptr, x, dt, A, B, C, D, z, bias);
   a.seq.T = 1;
   a.init = state;

@@ -311,3 +311,39 @@ def test_single_tokens_over_what_others_read():
     refused(conv_step, s, {**CSTEP, "x": H(at(0), 128)}, "y", "x")
     for name in ("x", "dt", "z"):
         refused(ssm_step, t, {**SSTEP, name: H(at(0), 128)}, "y", name)
+
+
+SCAN = dict(x=H(at(0)), dt=H(at(1)), A=at(2), B=H(at(3)), C=H(at(4)), D=at(5), z=H(at(6)), b=at(7), init=at(8), fin=at(9), y=at(10),
+            cs=at(11), ws=at(12))
+SBACK = {**{k: SCAN[k] for k in ("x", "dt", "A", "B", "C", "D", "z", "b")}, "cs": at(8), "dy": at(9), "df": at(10), "dx": H(at(11)),
+         "ddt": H(at(12)), "dA": at(13), "dB": H(at(14)), "dC": H(at(15)), "dD": at(16), "dz": H(at(17)), "db": at(18), "di": at(19),
+         "ws": at(20)}
+
+
+@cpu_only
+def test_scan_outputs_over_what_others_read():
+    """Workgroups of other channels and segments read B, C, the parameters and states late."""
+    s = ssm_shape()
+    refused(ssm, s, SCAN, "y", "A B C D b init fin cs")
+    refused(ssm, s, SCAN, "fin", "x dt A B C D z b init cs")
+    refused(ssm, s, SCAN, "cs", "x dt A B C D z b init")
+    for name in ("x", "dt", "z"):
+        refused(ssm, s, {**SCAN, name: H(at(0), 128)}, "y", name)
+
+
+@cpu_only
+def test_scan_gradients_over_what_others_read():
+    s = ssm_shape()
+    rows = ("dx", "ddt", "dz", "dB", "dC")
+    for out in rows + ("dA", "dD", "db", "di"):
+        others = [k for k in rows + ("dA", "dD", "db", "di") if k != out]
+        late = ["A", "B", "C", "D", "b", "cs", "df"] * (out in ("dx", "ddt", "dz")) + ["x", "dt", "z", "A", "B", "C", "D", "b", "cs", "dy", "df"] * (out == "di")
+        for name in others + late:
+            p = SBACK[name]
+            p = getattr(p, "data", p)
+            assert ssm_bwd(s, **{**SBACK, out: H(p) if out in rows else p}) == INVALID, (out, name)
+    for out in ("dx", "ddt", "dz"):
+        for name in ("x", "dt", "z"):
+            assert ssm_bwd(s, **{**SBACK, name: H(at(0), 128), out: H(at(0))}) == INVALID, (out, name)
+            assert ssm_bwd(s, **{**SBACK, out: H(SBACK[name].data, 128)}) == INVALID, (out, name)
+        assert ssm_bwd(s, **{**SBACK, out: H(SBACK["dy"], 128)}) == INVALID, out
