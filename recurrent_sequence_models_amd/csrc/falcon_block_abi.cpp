@@ -48,8 +48,10 @@ int falcon_rms_norm(const falcon_norm_shape_t *s, const void *x, const void *res
   FALCON_TRY(maybe(stream_out, 16));
   FALCON_TRY(need(y, 16));
   FALCON_TRY(q8 ? need(scale, 4) : maybe(scale, 4));
-  if (residual && y == stream_out) return FALCON_ERR_INVALID_ARG;
-  if (q8 && (y == x || y == residual)) return FALCON_ERR_INVALID_ARG;     // rows of another length
+  if (residual) FALCON_TRY(apart(stream_out, {weight, y}));
+  FALCON_TRY(distinct(y, weight));
+  if (q8) FALCON_TRY(apart(y, {x, residual}));                            // rows of another length
+  if (q8) FALCON_TRY(apart(scale, {x, residual, weight, residual ? stream_out : nullptr, y}));
   falcon::NormArgs a = norm_args(s, weight);
   a.x = x;
   a.residual = residual;
@@ -75,6 +77,7 @@ int falcon_rms_norm_bwd(const falcon_norm_shape_t *s, const void *stream_in, con
   FALCON_TRY(need(dx, 16));
   FALCON_TRY(maybe(dweight, 4));
   if (dweight) FALCON_TRY(check_workspace(ws, ws_bytes, falcon_rms_norm_bwd_workspace(s)));
+  FALCON_TRY(apart(dx, {weight, dweight}));
   falcon::NormArgs a = norm_args(s, weight);
   a.x = stream_in;
   a.dy = d_y;
@@ -149,8 +152,8 @@ int falcon_conv_fwd(const falcon_conv_shape_t *s, const int32_t *cu, falcon_head
   FALCON_TRY(maybe(init, 16));
   FALCON_TRY(maybe(final_state, 16));
   FALCON_TRY(need(y, 16));
-  FALCON_TRY(distinct(final_state, init));
-  FALCON_TRY(distinct(y, x.data));
+  FALCON_TRY(apart(final_state, {x.data, w, bias, init}));
+  FALCON_TRY(apart(y, {x.data, w, bias, init, final_state}));
   falcon::ConvArgs a = conv_args(s, cu, x, w, bias);
   a.init = init;
   a.final_state = final_state;
@@ -177,11 +180,12 @@ int falcon_conv_bwd(const falcon_conv_shape_t *s, const int32_t *cu, falcon_head
   FALCON_TRY(maybe(dw, 4));
   FALCON_TRY(maybe(db, 4));
   FALCON_TRY(maybe(d_init, 16));
-  FALCON_TRY(distinct(d_init, d_final));
-  FALCON_TRY(distinct(d_init, init));     // runs behind a sequence's first one may read it still
-  FALCON_TRY(distinct(dx.data, x.data));
-  FALCON_TRY(distinct(dx.data, d_y));
   if (dw || db) FALCON_TRY(check_workspace(ws, ws_bytes, falcon_conv_bwd_workspace(s, cu != nullptr)));
+  // d_init too: runs behind a sequence's first one may read the inputs before it still
+  for (const void *out : {(const void *)dx.data, (const void *)d_init})
+    FALCON_TRY(apart(out, {x.data, w, bias, init, d_y, d_final, dw, db}));
+  FALCON_TRY(distinct(dx.data, d_init));
+  FALCON_TRY(distinct(dw, db));
   falcon::ConvArgs a = conv_args(s, cu, x, w, bias);
   a.init = init;
   a.dy = d_y;

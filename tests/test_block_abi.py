@@ -347,3 +347,28 @@ def test_scan_gradients_over_what_others_read():
             assert ssm_bwd(s, **{**SBACK, name: H(at(0), 128), out: H(at(0))}) == INVALID, (out, name)
             assert ssm_bwd(s, **{**SBACK, out: H(SBACK[name].data, 128)}) == INVALID, (out, name)
         assert ssm_bwd(s, **{**SBACK, out: H(SBACK["dy"], 128)}) == INVALID, out
+
+
+@cpu_only
+def test_conv_outputs_over_what_others_read():
+    """Filters are read for every run; the states before and behind a sequence by its first and its last ones."""
+    s = conv_shape()
+    fwd = {**{k: CONV[k] for k in ("x", "w", "b", "init")}, "fin": at(4), "y": at(5)}
+    refused(conv, s, fwd, "y", "x w b init fin")
+    refused(conv, s, fwd, "fin", "x w b init")
+    for out, ins in (("dx", "x w b init dy df dw db di"), ("di", "x w b init dy df dx dw db"), ("dw", "db")):
+        for name in ins.split():
+            p = getattr(CONV[name], "data", CONV[name])
+            assert conv_bwd(s, **{**CONV, out: H(p) if out == "dx" else p}) == INVALID, (out, name)
+
+
+@cpu_only
+def test_norm_outputs_over_what_others_read():
+    """The weight is read for every row, and a row's scale may stand where another row's entries are."""
+    args = dict(x=at(0), res=at(1), w=at(2), so=at(3), y=at(4), scale=at(5))
+    for s in (norm_shape(), norm_shape(out=2)):
+        refused(norm, s, args, "y", "w so")
+        refused(norm, s, args, "so", "w")
+    refused(norm, norm_shape(out=2), args, "scale", "x res w so y")
+    back = dict(st=at(0), w=at(1), dy=at(2), ds=at(3), dx=at(4), dw=at(5), ws=at(6))
+    refused(norm_bwd, norm_shape(), back, "dx", "w dw")
