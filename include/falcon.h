@@ -529,8 +529,8 @@ typedef enum { FALCON_ACT_NONE = 0, FALCON_ACT_SILU = 1, FALCON_ACT_GELU = 2 } f
  * The norm is of the rounded stream, which the backward pass differentiates.
  * out = FALCON_E4M3: y in 8 bits, y = q scale with one fp32 scale a token,
  *   scale = max(max |y|, 1e-30) / 448, q = y / scale rounded to nearest even
- * (from the unrounded y; with norm = 0 and no weight this quantises x's rows).  A
- * row with a NaN has a NaN scale; one with an infinity (norm = 0) an infinite one.
+ * (the fp32 quotient, of the unrounded y; with norm = 0 and no weight this quantises
+ * x's rows).  A row with a NaN has a NaN scale; one with an infinity (norm = 0) an infinite one.
  * The mean of squares is formed in fp32: as in the query / key norm, entries over
  * 2^63 overflow it, and with eps = 0 a row of zeros is not finite. */
 typedef struct {

@@ -66,6 +66,26 @@ __device__ __forceinline__ void store_f8(unsigned char *p, const float (&v)[4]) 
   *reinterpret_cast<unsigned *>(p) = f8x4(v[0], v[1], v[2], v[3]);
 }
 
+// y / scale, the nearest fp32 number: by a rounded reciprocal alone, ties of the 8-bit rounding would go to either side.
+// With scale = m 2^e, y 2^-e is exact, and two corrections by the remainder of y 2^-e after q m give the quotient to the last
+// bit (Markstein's theorem: q is within a step after the first), in 6 instructions.  16387 x 768 bf16: 18.9 us, 20.1 with a
+// division an entry (17.7 by the reciprocal); 16384 x 4096 112.7 both (110.4).
+struct RowScale {
+  float m, inv, down;      // mantissa, its reciprocal, 2^-e; an infinite scale leaves zeros, and a NaN NaN
+  __device__ __forceinline__ explicit RowScale(float scale) {
+    const unsigned u = __float_as_uint(scale), e = u & 0x7f800000u;
+    m = __uint_as_float((u & 0x007fffffu) | 0x3f800000u);
+    inv = 1.f / m;
+    down = e < 0x7f800000u ? __uint_as_float(0x7f000000u - e) : 1.f / scale;
+  }
+  __device__ __forceinline__ float divide(float y) const {
+    y *= down;
+    float q = y * inv;
+    q = fmaf(fmaf(-q, m, y), inv, q);
+    return fmaf(fmaf(-q, m, y), inv, q);
+  }
+};
+
 // W waves a row, V times 16 bytes a lane.
 template <typename T, int W, int V, bool Q8> __global__ __launch_bounds__(THR) void norm_fwd(NormArgs a) {
   constexpr int E = PER16<T>, ROWS = 4 / W;
@@ -134,13 +154,14 @@ template <typename T, int W, int V, bool Q8> __global__ __launch_bounds__(THR) v
         }
       }
       top = max(row_max<W>(top, part, k + 1), __float_as_uint(LEAST));
-      const float scale = __uint_as_float(top) / F8_MAX, inv = 1.f / scale;
+      const float scale = __uint_as_float(top) / F8_MAX;
+      const RowScale by(scale);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int c = (i * W * 64 + lane) * E;
         if (c >= D) continue;
 #pragma unroll
-        for (int j = 0; j < E; ++j) y[i][j] *= inv;
+        for (int j = 0; j < E; ++j) y[i][j] = by.divide(y[i][j]);
         store_f8(static_cast<unsigned char *>(a.y) + base + c, y[i]);
       }
       if (lane == 0) a.scale[row] = scale;

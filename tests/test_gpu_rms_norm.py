@@ -175,3 +175,19 @@ def test_past_32_bits():
     h = rsm.rms_norm_bwd(x[-5:].clone(), w, alone)
     assert torch.equal(g["dx"][-5:], h["dx"])
     torch.testing.assert_close(g["dweight"], h["dweight"], rtol=1e-5, atol=1e-6)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_eight_bits_are_of_the_quotient(dtype):
+    """Rows whose scale is no power of two: every quotient of two 8-bit mantissas, rounded as the type does from the fp32
+    quotient (103.5 of a row whose largest is 138 is a tie, 336, and goes to 320)."""
+    import torch
+    import recurrent_sequence_models_amd as rsm
+    m = torch.arange(128, 256, dtype=torch.float32)
+    x = torch.cat([m[:, None], torch.cat([m * 2.0 ** -e for e in range(1, 5)]).expand(128, -1), torch.zeros(128, 7)], 1)
+    x[:, -7] = torch.where(m >= 138, 103.5, 0.0)
+    scale = m / 448
+    want = (x / scale[:, None]).to(torch.float8_e4m3fn).float()
+    q, got = rsm.quantize_rows(x.to(dict(bf16=torch.bfloat16, fp32=torch.float32)[dtype]).cuda())
+    assert torch.equal(got.cpu(), scale) and torch.equal(q.float().cpu(), want)
+    assert want[10, -7] == 320
