@@ -221,3 +221,24 @@ def test_one_token_over_its_bias():
         want, _ = rsm.linear(x, w, bias=b)
         y, _ = rsm.linear(x, w, bias=b, out=b)
         assert y is b and torch.equal(b, want)
+
+
+# of 8-bit operands to bf16: tiles of 64 with k split and whole, of 128 (deep, two a unit), of 256 with tokens apart
+@pytest.mark.parametrize("M,K,N", [(65, 2048, 264), (500, 80, 640), (2040, 272, 2040), (2050, 272, 2552), (4099, 144, 4096)])
+def test_kept_pre_activation_of_8_bits(M, K, N):
+    """The fp32 pre-activation is the sum in fp32, also where a result rounded to bf16 would not show more than 13 bits:
+    beside one large product a group's others would be dropped.  Bound: of forward(), without that."""
+    import torch
+    import recurrent_sequence_models_amd as rsm
+    g = torch.Generator(device="cuda").manual_seed(7)
+    x, w = (2 + 3 * torch.rand(n, K, generator=g, device="cuda") for n in (M, N))     # products of 2^-14 of the largest
+    x[:, ::64], w[:, ::64] = 448.0, 448.0
+    x[1::2, ::64] *= -1
+    x, w = x.to(torch.float8_e4m3fn), w.to(torch.float8_e4m3fn)
+    sx, sw, b = torch.rand(M, generator=g, device="cuda") + 0.5, torch.rand(N, generator=g, device="cuda") + 0.5, rand(3, N)
+    y, pre = rsm.linear(x, w, x_scale=sx, weight_scale=sw, bias=b, activation="silu", pre=True)
+    X, W, B = f64(x.float()) * f64(sx)[:, None], f64(w.float()) * f64(sw)[:, None], f64(b)
+    want, p = O.linear(X, W, B, "silu")
+    ep = (K + 32) * U * (np.abs(X) @ np.abs(W).T) + 4 * U * (np.abs(p) + np.abs(B))
+    check("pre", f64(pre), p, ep + TINY)
+    check("y", f64(y), want, (1.13 * ep + act_error(p, want, "silu")) * (1 + half("bf16")) + half("bf16") * np.abs(want) + TINY)
