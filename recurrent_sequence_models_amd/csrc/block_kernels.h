@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "layer_kernels.h"
+#include "seq_plan.h"
 
 namespace falcon {
 
@@ -29,27 +30,6 @@ struct NormArgs {
 size_t norm_bwd_workspace(bool bf16, int tokens, int width);
 hipError_t launch_norm_fwd(bool bf16, bool q8, NormArgs a, hipStream_t s);
 hipError_t launch_norm_bwd(bool bf16, NormArgs a, float *dw, void *ws, hipStream_t s);
-
-// The sequences of a call: n of T tokens each, or (cu != null) packed on one axis of T tokens.
-struct SeqMap {
-  const int *cu;
-  int n, T;
-  __host__ __device__ int tokens() const { return cu ? T : n * T; }
-  // token ranges, kept inside the arrays whatever the offsets hold
-  __host__ __device__ int inside(int t) const { return t < 0 ? 0 : t > T ? T : t; }
-  __host__ __device__ int begin(int i) const { return cu ? inside(cu[i]) : i * T; }
-  __host__ __device__ int end(int i) const { return cu ? inside(cu[i + 1]) : (i + 1) * T; }
-  // the largest i < n that begins at or before token t (0 if none)
-  __host__ __device__ int of(int t) const {
-    if (!cu) return t / T;
-    int lo = 0, len = n;
-    while (len > 1) {
-      const int half = len >> 1;
-      if (cu[lo + half] <= t) { lo += half; len -= half; } else { len = half; }
-    }
-    return lo;
-  }
-};
 
 // Short causal convolution.  x may have a token stride; the rest is dense.
 struct ConvArgs {
@@ -91,9 +71,6 @@ struct SsmArgs {
   int64_t lddx, ldddt, lddz, lddB, lddC;
 };
 struct SsmGrads { float *dA, *dD, *dbias; };   // [D, N]; [D] or null; [D] or null
-int ssm_chunk(int N);                             // steps between the states that the forward keeps
-int ssm_segment(const SeqMap &seq, int D, int channels, int enough, int want, int whole);   // tokens of a segment
-bool ssm_segmented(const SeqMap &seq, int segment);   // whether a sequence has more than one (packed: may have)
 bool ssm_fits(SeqMap seq, int D, int N);
 bool ssm_step_fits(int n, int D, int N);
 size_t ssm_fwd_workspace(SeqMap seq, int D, int N);

@@ -23,10 +23,10 @@
 namespace falcon {
 namespace {
 
-constexpr int THR = 256;
+constexpr int THR = CONV_THR;
 // A wave's lanes lie side by side over channels, and a run is one wave's, so where it stands is the same in all of them
 // (4 x 4096 x 1536 bf16: 25 us with runs of 16 lanes, backward 36 of 32; 13 packed sequences, 9001 x 2048: 29 and 23).
-constexpr int LANES = 64, RUNS = THR / LANES;
+constexpr int LANES = CONV_LANES, RUNS = CONV_RUNS;
 constexpr int AHEAD = 4;                                   // tokens whose loads are in flight together, W - 1 at least
 
 // This thread's filters: w[k][j] of tap k, channel j; bias.
@@ -283,21 +283,13 @@ template <typename T, int W> __global__ __launch_bounds__(STEP_THR) void conv_st
   for (int k = 0; k < W - 1; ++k) put(static_cast<T *>(a.final_state) + at + (size_t)k * a.D, win[k]);
 }
 
-// A pass's shape: channels of a workgroup, runs of it, and the tokens of a run.  Long runs read fewer tokens twice, short
-// ones make more workgroups (4 x 4096 x 1536 bf16, 24 and 33 us: 30 and 36 with runs half as long, 24 and 41 twice).
 struct Shape {
-  int cols, runs, run;
+  int run;
   dim3 grid;
 };
 Shape shape_of(SeqMap seq, int D, bool bf16, bool back) {
-  Shape s;
-  s.cols = LANES * (bf16 && !back ? 8 : 4);
-  s.runs = RUNS;
-  const int64_t wide = (D + s.cols - 1) / s.cols, tokens = seq.tokens();
-  s.run = back ? 32 : 16;
-  while (s.run > 4 && (tokens + s.run * s.runs - 1) / (s.run * s.runs) * wide < 512) s.run /= 2;
-  s.grid = dim3((unsigned)((tokens + s.run * s.runs - 1) / (s.run * s.runs)), (unsigned)wide);
-  return s;
+  const ConvPlan p = conv_plan(seq, D, bf16, back);
+  return {p.run, dim3((unsigned)p.blocks, (unsigned)p.wide)};
 }
 
 }  // namespace

@@ -27,6 +27,7 @@
 
 #include "attn_frag.h"
 #include "block_kernels.h"
+#include "linear_plan.h"
 #include "row_io.h"
 
 namespace falcon {
@@ -60,7 +61,6 @@ __device__ __forceinline__ void mma(f16v &d, const Frag<e4m3> &a, const Frag<e4m
 namespace {
 
 // ---- Operands ------------------------------------------------------------------
-constexpr int KB = 128;                                            // bytes of k that a step of the loop takes
 template <typename T> constexpr int KE = KB / (int)sizeof(T);      // entries
 template <typename T> constexpr int KM = std::is_same_v<T, e4m3> ? 64 : 16;   // entries that one mma() sums
 
@@ -429,7 +429,7 @@ template <typename O> __global__ __launch_bounds__(256) void join(LinearArgs a) 
 // ---- Few tokens ----------------------------------------------------------------------
 // 16 rows of W a workgroup, 16 MT tokens; 8 waves take turns at 64 bytes of k.  A lane reads 16 bytes of a row:
 // the k's of its slots in a 16-wide product are the same ones for both operands.
-constexpr int FEW_WAVES = 8, FEW_TOKENS = 64;
+constexpr int FEW_WAVES = 8;
 template <typename T> __device__ __forceinline__ void mma16b(f4 &d, const u4 &a, const u4 &b) {
   if constexpr (sizeof(T) == 2) {
     d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, b), d, 0, 0, 0);
@@ -532,62 +532,6 @@ template <typename T> __global__ __launch_bounds__(256) void pre_gradient(Linear
 }
 
 // ---- Launches ---------------------------------------------------------------------------
-// Forms of a product: `few` (16 rows of the left operand a workgroup), or tiles of 64 x 64, 128 x 128 (deep: four steps in
-// LDS, one workgroup a compute unit) and 256 x 256.
-enum class Form { few, small, deep, medium, large };
-struct Plan { Form form; int splits; int64_t tiles; };
-
-int64_t over(int64_t n, int64_t d) { return (n + d - 1) / d; }
-
-// Workgroups that share a tile's k: as many as make `groups` of all, at 4 steps each and 16 at most.
-int splits_of(int64_t tiles, int64_t groups, int64_t steps) {
-  const int64_t s = std::min({groups / tiles, steps / 4, (int64_t)16});
-  return s > 1 ? (int)s : 1;
-}
-
-// A compute unit holds one workgroup of 256 x 256 or two of 128 x 128; the larger tile reads less from LDS for a product
-// (16384 x 2048 -> 4096 bf16: 287 us, 299 with the smaller; 16384 x 4096 -> 2048 e4m3: 195, 227), the smaller one
-// leaves less of the last round empty (16384 x 768 -> 1536 bf16: 54.7 us, 58.7 with the larger; 2048 x 2048 -> 2048:
-// 29, 51).  So rounds are counted, in tiles of 128 x 128 a compute unit.  fp32 takes too many registers for the larger.
-// Where 128 x 128 tiles leave compute units idle, tiles are 64 x 64, and k is split where those do too: 512 x 2048 -> 2048
-// bf16 15.5 us, 20 in four parts of 128 x 128; 100 x 2048 -> 4096 13.5, 16.  Not over more than 48 steps a
-// workgroup: 512 x 8192 -> 2048 44.6 us, 31.8 in eight parts of 128 x 128; those for two workgroups a compute unit where
-// each has 16 steps and more (768 x 16384 -> 1536: 183 us with the rest of its backward pass, 192 for one; 100 x 8192 ->
-// 4096: 24.0 and 22.3).  One workgroup of 128 x 128 a compute unit has LDS for four steps, three of them on their way,
-// and 8 waves (2048 x 2048 -> 2048: 25 us, 28 with 4 waves, 31 with two steps; 33 as 64 x 64; training 2048 x 2048 -> 2048:
-// 80 and 91).
-Plan tiles_of(int64_t I, int64_t J, int64_t K, int e) {
-  const int64_t large = over(I, 256) * over(J, 256), medium = over(I, 128) * over(J, 128), small = over(I, 64) * over(J, 64);
-  if (e < 4 && large >= 256 && over(large, 256) * 4 * 20 <= over(medium, 512) * 2 * 21) return {Form::large, 1, large};
-  const int64_t steps = over(K * e, KB);
-  if (medium < 256) {
-    const int s = splits_of(small, 256, steps);
-    if (steps / s <= 48) return {Form::small, s, small};
-  }
-  const int s = medium < 256 ? splits_of(medium, steps * medium >= 16 * 512 ? 512 : 256, steps) : 1;
-  return {medium * s <= 256 ? Form::deep : Form::medium, s, medium};
-}
-
-// The time of a plan's tiles, in rounds of the chip: 20 for tiles of 128 x 128 a compute unit.
-int64_t rounds_of(const Plan &p) {
-  return p.form == Form::large ? over(p.tiles, 256) * 4 * 20 : over(p.tiles * p.splits, 512) * 2 * 21;
-}
-
-// Few tokens take what a compute unit loads, at about 40 KB a us: 16 rows of W and the tokens (a multiple of 16) for each
-// of its workgroups of `few`, or both operands of its tiles' steps (which fp32 products hold up by a quarter, by
-// three halves in the larger tiles) and about 64 KB for the tile's beginning and the join.  16 x 2048 -> 4096 bf16: 7.5 us,
-// 9.6 in tiles; 16 x 8192 -> 2048: 17.6 and 12.1; 64 x 4096 -> 8192: 38.5 and 17.8; 24 x 4096 -> 8192 fp32: 47 and 72.
-Plan plan_of(int64_t I, int64_t J, int64_t K, int e) {
-  const Plan p = tiles_of(I, J, K, e);
-  if (J > FEW_TOKENS) return p;
-  const int64_t rows = J <= 16 ? 32 : J <= 32 ? 48 : 80, groups = over(I, 16);
-  const int64_t few = over(groups, 256) * rows * K * e, step = p.form == Form::small ? 2 * 64 * KB : 2 * 128 * KB;
-  const int64_t tiles = over(p.tiles * p.splits, 256) * (over(K * e, KB) / p.splits) * step;
-  const int64_t quarters = e < 4 ? 4 : p.form == Form::small ? 5 : 10;
-  if (p.form == Form::large || few <= tiles * quarters / 4 + 65536) return {Form::few, 1, groups};
-  return p;
-}
-
 template <typename T, typename O, bool LC, bool RC> hipError_t multiply(const Plan &p, LinearArgs a, void *ws, hipStream_t s) {
   a.splits = p.splits;
   a.part = static_cast<float *>(ws);
@@ -616,15 +560,6 @@ template <typename T, typename O> hipError_t few_tokens(const LinearArgs &a, hip
   else if (a.J <= 32) hipLaunchKernelGGL((few<T, O, 2>), grid, dim3(64 * FEW_WAVES), 0, s, a);
   else hipLaunchKernelGGL((few<T, O, 4>), grid, dim3(64 * FEW_WAVES), 0, s, a);
   return hipGetLastError();
-}
-
-// Tokens that a pass of their own takes: up to 64 behind the last whole tile of 256, where that saves the others a
-// round (16387 x 4096 -> 2048 e4m3: 257 us as one pass).
-int tokens_apart(int64_t I, int64_t J, int64_t K, int e) {
-  const int rest = (int)(J % 256);
-  if (!rest || rest > FEW_TOKENS || J < 512 || K < 512) return 0;
-  const Plan with = plan_of(I, J, K, e), without = plan_of(I, J - rest, K, e);
-  return with.form != Form::small && without.form != Form::small && rounds_of(without) < rounds_of(with) ? rest : 0;
 }
 
 template <typename T, typename O> hipError_t fwd(LinearArgs a, void *ws, hipStream_t s) {

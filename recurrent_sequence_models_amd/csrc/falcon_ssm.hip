@@ -22,22 +22,11 @@
 namespace falcon {
 namespace {
 
-constexpr int FWD_CH = 16;
-// Below this many workgroups, 8 waves of 8 steps each take a tile's 64 steps, instead of 4 of 16: more waves for what
-// there is, at twice the joins.  N = 16, bf16: 384 workgroups (4 x 4096 x 1536) 220 us, 257 with 4 waves; 512 (4 x 2048 x
-// 2048) 114 and 118; 768 (8 x 2048 x 1536) 186 and 163.
-constexpr int FEW_GROUPS = 640;
-// Sequences are cut where they make fewer than 256 workgroups, into 768 (1 x 16384 x 1536, 96 workgroups: 267 us with
-// the maps' pass, 311 cut for 512, 460 for 256); with 384 they are not (4 x 4096 x 1536: 220 us, 260 cut).
-// Up to 4096 / N tokens they are left whole (1 x 192 x 512: 10.3 us, 12.8 cut; 320: 14.6 and 13.0; N = 64: 128 18.1 and 19.3,
-// 192 25.3 and 19.4).
-int ssm_segment_fwd(const SeqMap &q, int D, int N) { return ssm_segment(q, D, FWD_CH, 256, 768, 4096 / N); }
-
 // MAPS: only the segment's map (end state from zero, sum of delta) is formed.
 template <typename T, int N, int TW, int STEPS, bool MAPS>
-__global__ __launch_bounds__((SsmTile<N, FWD_CH, TW, STEPS>::THR), (STEPS == 16 ? 3 : 4)) void ssm_fwd(SsmArgs a) {
-  typedef SsmTile<N, FWD_CH, TW, STEPS> L;
-  constexpr int V = L::VEC, BV = L::BV, CH = FWD_CH;
+__global__ __launch_bounds__((SsmTile<N, SSM_FWD_CH, TW, STEPS>::THR), (STEPS == 16 ? 3 : 4)) void ssm_fwd(SsmArgs a) {
+  typedef SsmTile<N, SSM_FWD_CH, TW, STEPS> L;
+  constexpr int V = L::VEC, BV = L::BV, CH = SSM_FWD_CH;
   __shared__ __align__(16) float2 step[L::TS][CH];        // (delta, delta x); then (y, -)
   __shared__ __align__(16) float sB[L::TS][N], sC[L::TS][N];
   __shared__ __align__(16) float mapP[TW][CH][N], mapH[TW][CH][N];
@@ -256,35 +245,12 @@ size_t align16(size_t n) { return (n + 15) / 16 * 16; }
 
 }  // namespace
 
-// Tokens of a segment, a whole number of chunks.  Whole sequences, where those make `enough` workgroups (of `channels`
-// channels each) or have no more than `whole` tokens; else as many segments as make `want`, down to one tile each
-// (1 x 1000 x 512 bf16, both directions: 56 us, 89 with 256 tokens and more; 1 x 16384 x 128: 125 and 122): forming their
-// maps first costs half of a pass.
-int ssm_segment(const SeqMap &q, int D, int channels, int enough, int want, int whole) {
-  const int64_t groups = (D + channels - 1) / channels;
-  int64_t len;
-  if (q.T <= whole) return (q.T + SSM_ALIGN - 1) / SSM_ALIGN * SSM_ALIGN;
-  if (q.cu) {
-    if (groups >= enough) return (q.T + SSM_ALIGN - 1) / SSM_ALIGN * SSM_ALIGN;
-    len = ((int64_t)q.T * groups + want - 1) / want;
-  } else {
-    const int64_t parts = q.n * groups >= enough ? 1 : want / (q.n * groups);
-    if (parts < 2) return (q.T + SSM_ALIGN - 1) / SSM_ALIGN * SSM_ALIGN;
-    len = (q.T + parts - 1) / parts;
-  }
-  return (int)((len + SSM_ALIGN - 1) / SSM_ALIGN * SSM_ALIGN);
-}
-// Whether any sequence has more than one segment (packed: may have).
-bool ssm_segmented(const SeqMap &q, int seg) { return q.T > seg; }
-
-int ssm_chunk(int N) { return 1024 / N; }
-
 bool ssm_step_fits(int n, int D, int N) {
   return grid_fits((int64_t)n * (((int64_t)D * N / 4 + STEP_THR - 1) / STEP_THR), STEP_THR);
 }
 
 bool ssm_fits(SeqMap seq, int D, int N) {
-  const int64_t groups = (D + FWD_CH - 1) / FWD_CH;
+  const int64_t groups = (D + SSM_FWD_CH - 1) / SSM_FWD_CH;
   const int64_t seg = ssm_segment_fwd(seq, D, N);
   const int64_t slots = seq.cu ? seq.T / seg + seq.n : (int64_t)seq.n * ((seq.T + seg - 1) / seg);
   return slots <= INT32_MAX - 8 && grid_fits(slots * (groups + 7) / 8 * 8 + 8, 1024);
@@ -298,8 +264,8 @@ size_t ssm_fwd_workspace(SeqMap seq, int D, int N) {
 }
 
 template <typename T, int N, int TW, int STEPS> static hipError_t fwd(SsmArgs a, void *ws, hipStream_t s) {
-  constexpr int THR = SsmTile<N, FWD_CH, TW, STEPS>::THR;
-  const int groups = (a.D + FWD_CH - 1) / FWD_CH;
+  constexpr int THR = SsmTile<N, SSM_FWD_CH, TW, STEPS>::THR;
+  const int groups = (a.D + SSM_FWD_CH - 1) / SSM_FWD_CH;
   const unsigned grid = (unsigned)ssm_grid(groups, slots_of(a.seq, a.seg));
   if (ssm_segmented(a.seq, a.seg)) {
     const size_t states = align16((size_t)(slots_of(a.seq, a.seg) + 1) * a.D * N * sizeof(float));
@@ -320,8 +286,7 @@ template <typename T, int N, int TW, int STEPS> static hipError_t fwd(SsmArgs a,
 
 template <typename T, int N> static hipError_t fwd(SsmArgs a, void *ws, hipStream_t s) {
   a.seg = ssm_segment_fwd(a.seq, a.D, N);
-  const int64_t groups = (a.D + FWD_CH - 1) / FWD_CH;
-  if (groups * slots_of(a.seq, a.seg) < FEW_GROUPS) return fwd<T, N, 128 / N, (N == 64 ? 16 : 8)>(a, ws, s);
+  if (ssm_few_fwd(a.seq, a.seg, a.D)) return fwd<T, N, 128 / N, (N == 64 ? 16 : 8)>(a, ws, s);
   return fwd<T, N, 64 / N, 16>(a, ws, s);
 }
 

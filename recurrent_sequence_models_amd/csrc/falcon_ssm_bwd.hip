@@ -50,23 +50,7 @@ template <int P> __device__ __forceinline__ void channel_sums(const f4 &b, const
   if constexpr (P <= 8) { u += dpp_mov<0x128>(u); v += dpp_mov<0x128>(v); }    // row_ror:8
 }
 
-constexpr int BWD_CH = 32;
-template <int N> using BwdTile = SsmTile<N, BWD_CH, 64 / N, 16>;
-// Sequences are cut where they make fewer than 128 workgroups, into 256 (2 x 2048 x 768: 92 us with the maps' pass, 104 cut
-// for 512; 1 x 16384 x 1536: 632 and 615).  Up to 2048 / N tokens they are left whole (with the forward, 1 x 128 x 512: 37
-// us, 41 cut; 192: 48 and 42).  A compute unit holds one workgroup, so w of them, up to 4 rounds, leave the last round
-// partly empty.  There sequences are cut once, into a long segment and the rest: a unit without a long one in the last round
-// takes k rests one after the other, which are as long together.  That is worth r / (k + 1) of a sequence's tiles (2 at least)
-// and costs the rests' maps (with the forward, 4 x 4096 x 1536, w = 192: 714 us, 791 whole; 4 x 2048 x 1024, w = 128: 282,
-// 360; 3 x 500 x 1536, w = 144: 114, 118).
-int segment_of(const SeqMap &q, int D, int N) {
-  const int64_t w = (int64_t)q.n * ((D + BWD_CH - 1) / BWD_CH), rounds = (w + 255) / 256, idle = rounds * 256 - w;
-  if (!q.cu && w >= 128 && rounds <= 4 && idle) {
-    const int64_t k = (w + idle - 1) / idle;
-    if ((int64_t)q.T * rounds >= 128 * (k + 1)) return (int)(((int64_t)q.T * k / (k + 1) + SSM_ALIGN) / SSM_ALIGN * SSM_ALIGN);
-  }
-  return ssm_segment(q, D, BWD_CH, 128, 256, 2048 / N);
-}
+template <int N> using BwdTile = SsmTile<N, SSM_BWD_CH, 64 / N, 16>;
 // Workgroups begin in the order of their numbers: the sequences' first segments, which are never the shorter ones, come first.
 __device__ __forceinline__ int bwd_slot(const SeqMap &q, int len, int i) {
   return q.cu ? i : i % q.n * segments_of(q, len) + i / q.n;
@@ -76,7 +60,7 @@ __device__ __forceinline__ int bwd_slot(const SeqMap &q, int len, int i) {
 template <typename T, int N, bool MAPS> __global__ __launch_bounds__(BwdTile<N>::THR, MAPS ? 4 : 2) void ssm_bwd(SsmArgs a) {
   typedef BwdTile<N> L;
   static_assert(L::TS == SSM_CHUNK<N>, "a tile starts from a state that the forward kept");
-  constexpr int V = L::VEC, BV = L::BV, CH = BWD_CH;
+  constexpr int V = L::VEC, BV = L::BV, CH = SSM_BWD_CH;
   __shared__ __align__(16) f4 step[L::TS][CH];               // (delta, delta x, gy, -); then (sum g B, sum r h A log2 e, sum C h, -)
   __shared__ __align__(16) float sBC[L::TS][2][N];
   __shared__ __align__(16) float map[L::TW][3][CH][N];       // P, G and H of the waves' steps
@@ -379,8 +363,8 @@ size_t align16(size_t n) { return (n + 15) / 16 * 16; }
 
 struct Parts { size_t bc, A, D, map, sum, total; };
 Parts parts_of(const SeqMap &q, int D, int N) {
-  const int seg = segment_of(q, D, N);
-  const size_t groups = (D + BWD_CH - 1) / BWD_CH, slots = slots_of(q, seg);
+  const int seg = ssm_segment_bwd(q, D, N);
+  const size_t groups = (D + SSM_BWD_CH - 1) / SSM_BWD_CH, slots = slots_of(q, seg);
   Parts p;
   p.bc = align16(groups * q.tokens() * 2 * N * sizeof(float));
   p.A = align16(slots * D * N * sizeof(float));
@@ -405,8 +389,8 @@ template <typename T, int N> static hipError_t bwd(SsmArgs a, const SsmGrads &o,
   a.seg_map = reinterpret_cast<float *>(at += p.D);
   a.seg_state = reinterpret_cast<float *>(at += p.map);
   a.seg_sum = reinterpret_cast<float *>(at += p.map);
-  a.seg = segment_of(a.seq, a.D, N);
-  const int groups = (a.D + BWD_CH - 1) / BWD_CH, slots = slots_of(a.seq, a.seg);
+  a.seg = ssm_segment_bwd(a.seq, a.D, N);
+  const int groups = (a.D + SSM_BWD_CH - 1) / SSM_BWD_CH, slots = slots_of(a.seq, a.seg);
   const unsigned grid = (unsigned)ssm_grid(groups, slots);
   hipError_t e;
   if (ssm_segmented(a.seq, a.seg)) {

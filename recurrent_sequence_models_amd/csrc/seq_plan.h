@@ -1,0 +1,109 @@
+// The sequences of a call, and how the convolution and the selective scan deal them out: the rules of falcon_conv.hip,
+// falcon_ssm.hip and falcon_ssm_bwd.hip, host side only (a test can ask them).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace falcon {
+
+// The sequences of a call: n of T tokens each, or (cu != null) packed on one axis of T tokens.
+struct SeqMap {
+  const int *cu;
+  int n, T;
+  __host__ __device__ int tokens() const { return cu ? T : n * T; }
+  // token ranges, kept inside the arrays whatever the offsets hold
+  __host__ __device__ int inside(int t) const { return t < 0 ? 0 : t > T ? T : t; }
+  __host__ __device__ int begin(int i) const { return cu ? inside(cu[i]) : i * T; }
+  __host__ __device__ int end(int i) const { return cu ? inside(cu[i + 1]) : (i + 1) * T; }
+  // the largest i < n that begins at or before token t (0 if none)
+  __host__ __device__ int of(int t) const {
+    if (!cu) return t / T;
+    int lo = 0, len = n;
+    while (len > 1) {
+      const int half = len >> 1;
+      if (cu[lo + half] <= t) { lo += half; len -= half; } else { len = half; }
+    }
+    return lo;
+  }
+};
+
+// ---- Short causal convolution ---------------------------------------------------------
+constexpr int CONV_THR = 256, CONV_LANES = 64, CONV_RUNS = CONV_THR / CONV_LANES;    // threads, lanes of a run, runs
+
+// A pass of the convolution: the tokens of a run, which is a wave's, and its workgroups.  Long runs read fewer tokens twice,
+// short ones make more workgroups (4 x 4096 x 1536 bf16, 24 and 33 us: 30 and 36 with runs half as long, 24 and 41 twice).
+struct ConvPlan {
+  int run;
+  int64_t blocks, wide;      // workgroups along time and channels
+};
+inline ConvPlan conv_plan(const SeqMap &seq, int D, bool bf16, bool back) {
+  const int cols = CONV_LANES * (bf16 && !back ? 8 : 4);
+  const int64_t wide = (D + cols - 1) / cols, tokens = seq.tokens();
+  const auto blocks = [&](int run) { return (tokens + run * CONV_RUNS - 1) / (run * CONV_RUNS); };
+  int run = back ? 32 : 16;
+  while (run > 4 && blocks(run) * wide < 512) run /= 2;
+  return {run, blocks(run), wide};
+}
+
+// ---- Selective state-space scan ---------------------------------------------------------
+inline int ssm_chunk(int N) { return 1024 / N; }   // steps between the states that the forward keeps
+constexpr int SSM_ALIGN = 64;      // segments are a multiple of this long: whole chunks of every N
+
+__host__ __device__ inline int segments_of(const SeqMap &q, int len) { return (q.T - 1) / len + 1; }   // T + len may pass 2^31
+__host__ __device__ inline int slots_of(const SeqMap &q, int len) {
+  return q.cu ? q.T / len + q.n : q.n * segments_of(q, len);
+}
+
+// Tokens of a segment, a whole number of chunks.  Whole sequences, where those make `enough` workgroups (of `channels`
+// channels each) or have no more than `whole` tokens; else as many segments as make `want`, down to one tile each
+// (1 x 1000 x 512 bf16, both directions: 56 us, 89 with 256 tokens and more; 1 x 16384 x 128: 125 and 122): forming their
+// maps first costs half of a pass.
+inline int ssm_segment(const SeqMap &q, int D, int channels, int enough, int want, int whole) {
+  const int64_t groups = (D + channels - 1) / channels;
+  int64_t len;
+  if (q.T <= whole) return (q.T + SSM_ALIGN - 1) / SSM_ALIGN * SSM_ALIGN;
+  if (q.cu) {
+    if (groups >= enough) return (q.T + SSM_ALIGN - 1) / SSM_ALIGN * SSM_ALIGN;
+    len = ((int64_t)q.T * groups + want - 1) / want;
+  } else {
+    const int64_t parts = q.n * groups >= enough ? 1 : want / (q.n * groups);
+    if (parts < 2) return (q.T + SSM_ALIGN - 1) / SSM_ALIGN * SSM_ALIGN;
+    len = (q.T + parts - 1) / parts;
+  }
+  return (int)((len + SSM_ALIGN - 1) / SSM_ALIGN * SSM_ALIGN);
+}
+// Whether any sequence has more than one segment (packed: may have).
+inline bool ssm_segmented(const SeqMap &q, int seg) { return q.T > seg; }
+
+constexpr int SSM_FWD_CH = 16;      // channels of a workgroup
+// Below this many workgroups, 8 waves of 8 steps each take a tile's 64 steps, instead of 4 of 16: more waves for what
+// there is, at twice the joins.  N = 16, bf16: 384 workgroups (4 x 4096 x 1536) 220 us, 257 with 4 waves; 512 (4 x 2048 x
+// 2048) 114 and 118; 768 (8 x 2048 x 1536) 186 and 163.
+constexpr int SSM_FEW_GROUPS = 640;
+inline bool ssm_few_fwd(const SeqMap &q, int seg, int D) {
+  return (int64_t)((D + SSM_FWD_CH - 1) / SSM_FWD_CH) * slots_of(q, seg) < SSM_FEW_GROUPS;
+}
+// Sequences are cut where they make fewer than 256 workgroups, into 768 (1 x 16384 x 1536, 96 workgroups: 267 us with
+// the maps' pass, 311 cut for 512, 460 for 256); with 384 they are not (4 x 4096 x 1536: 220 us, 260 cut).
+// Up to 4096 / N tokens they are left whole (1 x 192 x 512: 10.3 us, 12.8 cut; 320: 14.6 and 13.0; N = 64: 128 18.1 and 19.3,
+// 192 25.3 and 19.4).
+inline int ssm_segment_fwd(const SeqMap &q, int D, int N) { return ssm_segment(q, D, SSM_FWD_CH, 256, 768, 4096 / N); }
+
+constexpr int SSM_BWD_CH = 32;      // channels of a workgroup
+// Sequences are cut where they make fewer than 128 workgroups, into 256 (2 x 2048 x 768: 92 us with the maps' pass, 104 cut
+// for 512; 1 x 16384 x 1536: 632 and 615).  Up to 2048 / N tokens they are left whole (with the forward, 1 x 128 x 512: 37
+// us, 41 cut; 192: 48 and 42).  A compute unit holds one workgroup, so w of them, up to 4 rounds, leave the last round
+// partly empty.  There sequences are cut once, into a long segment and the rest: a unit without a long one in the last round
+// takes k rests one after the other, which are as long together.  That is worth r / (k + 1) of a sequence's tiles (2 at least)
+// and costs the rests' maps (with the forward, 4 x 4096 x 1536, w = 192: 714 us, 791 whole; 4 x 2048 x 1024, w = 128: 282,
+// 360; 3 x 500 x 1536, w = 144: 114, 118).
+inline int ssm_segment_bwd(const SeqMap &q, int D, int N) {
+  const int64_t w = (int64_t)q.n * ((D + SSM_BWD_CH - 1) / SSM_BWD_CH), rounds = (w + 255) / 256, idle = rounds * 256 - w;
+  if (!q.cu && w >= 128 && rounds <= 4 && idle) {
+    const int64_t k = (w + idle - 1) / idle;
+    if ((int64_t)q.T * rounds >= 128 * (k + 1)) return (int)(((int64_t)q.T * k / (k + 1) + SSM_ALIGN) / SSM_ALIGN * SSM_ALIGN);
+  }
+  return ssm_segment(q, D, SSM_BWD_CH, 128, 256, 2048 / N);
+}
+
+}  // namespace falcon

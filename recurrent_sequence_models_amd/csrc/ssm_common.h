@@ -12,7 +12,6 @@
 namespace falcon {
 
 constexpr int CHAIN_AHEAD = 8;    // segments' maps that are on their way together
-constexpr int SSM_ALIGN = 64;      // segments are a multiple of this long: whole chunks of every N
 constexpr float SSM_LOG2E = 1.44269504088896340736f, SSM_LN2 = 0.69314718055994530942f;
 
 template <int N, int CH_, int TW_, int STEPS_> struct SsmTile {
@@ -93,10 +92,6 @@ __device__ __forceinline__ float quad_sums(const float (&y)[4], int p) {
 // sequences of the same length have ceil(T / len) each.
 struct Segment { int n, slot, s, e, t0, t1; bool any; };
 
-__host__ __device__ inline int segments_of(const SeqMap &q, int len) { return (q.T - 1) / len + 1; }   // T + len may pass 2^31
-__host__ __device__ inline int slots_of(const SeqMap &q, int len) {
-  return q.cu ? q.T / len + q.n : q.n * segments_of(q, len);
-}
 __device__ __forceinline__ int first_slot(const SeqMap &q, int n, int len) {
   return q.cu ? q.begin(n) / len + n : n * segments_of(q, len);
 }
