@@ -24,9 +24,6 @@ namespace falcon {
 namespace {
 
 constexpr int THR = CONV_THR;
-// A wave's lanes lie side by side over channels, and a run is one wave's, so where it stands is the same in all of them
-// (4 x 4096 x 1536 bf16: 25 us with runs of 16 lanes, backward 36 of 32; 13 packed sequences, 9001 x 2048: 29 and 23).
-constexpr int LANES = CONV_LANES, RUNS = CONV_RUNS;
 constexpr int AHEAD = 4;                                   // tokens whose loads are in flight together, W - 1 at least
 
 // This thread's filters: w[k][j] of tap k, channel j; bias.
@@ -88,10 +85,16 @@ __device__ __forceinline__ void copy_empty(const ConvArgs &a, const void *from, 
   }
 }
 
-template <typename T, int W> __global__ __launch_bounds__(THR) void conv_fwd(ConvArgs a) {
-  constexpr int E = PER16<T>;
+// The number of a thread's run, of LANES lanes each.
+template <int LANES> __device__ __forceinline__ int run_of() {
+  const int r = threadIdx.x / LANES;
+  return blockIdx.x * (THR / LANES) + (LANES == 64 ? __builtin_amdgcn_readfirstlane(r) : r);
+}
+
+template <typename T, int W, int LANES> __global__ __launch_bounds__(THR) void conv_fwd(ConvArgs a) {
+  constexpr int E = PER16<T>, RUNS = THR / LANES;
   const int c = (blockIdx.y * LANES + threadIdx.x % LANES) * E;
-  const int run = blockIdx.x * RUNS + __builtin_amdgcn_readfirstlane(threadIdx.x / LANES), total = a.seq.tokens();
+  const int run = run_of<LANES>(), total = a.seq.tokens();
   if (c >= a.D) return;
   float w[W][E], b[E];
   load_filters<W, E>(a, c, w, b);
@@ -138,9 +141,9 @@ template <typename T, int W> __global__ __launch_bounds__(THR) void conv_fwd(Con
 }
 
 template <typename T, int W> __global__ __launch_bounds__(THR) void conv_bwd(ConvArgs a) {
-  constexpr int E = 4;
+  constexpr int E = 4, LANES = CONV_WIDE, RUNS = THR / LANES;
   const int col = threadIdx.x % LANES, c = (blockIdx.y * LANES + col) * E;
-  const int run = blockIdx.x * RUNS + __builtin_amdgcn_readfirstlane(threadIdx.x / LANES), total = a.seq.tokens();
+  const int run = run_of<LANES>(), total = a.seq.tokens();
   const bool in = c < a.D;
   float w[W][E], b[E], dw[W][E] = {}, db[E] = {};
   if (in) {
@@ -283,13 +286,17 @@ template <typename T, int W> __global__ __launch_bounds__(STEP_THR) void conv_st
   for (int k = 0; k < W - 1; ++k) put(static_cast<T *>(a.final_state) + at + (size_t)k * a.D, win[k]);
 }
 
-struct Shape {
-  int run;
-  dim3 grid;
-};
-Shape shape_of(SeqMap seq, int D, bool bf16, bool back) {
-  const ConvPlan p = conv_plan(seq, D, bf16, back);
-  return {p.run, dim3((unsigned)p.blocks, (unsigned)p.wide)};
+dim3 grid_of(const ConvPlan &p) { return dim3((unsigned)p.blocks, (unsigned)p.wide); }
+
+template <typename T, int W> void fwd(const ConvPlan &p, const ConvArgs &a, hipStream_t s) {
+  if (p.lanes == CONV_NARROW) hipLaunchKernelGGL((conv_fwd<T, W, CONV_NARROW>), grid_of(p), dim3(THR), 0, s, a);
+  else hipLaunchKernelGGL((conv_fwd<T, W, CONV_WIDE>), grid_of(p), dim3(THR), 0, s, a);
+}
+template <typename T, int W> void bwd(const ConvPlan &p, const ConvArgs &a, hipStream_t s) {
+  hipLaunchKernelGGL((conv_bwd<T, W>), grid_of(p), dim3(THR), 0, s, a);
+}
+template <typename T, int W> void step(const ConvPlan &p, const ConvArgs &a, hipStream_t s) {
+  hipLaunchKernelGGL((conv_step<T, W>), grid_of(p), dim3(STEP_THR), 0, s, a);
 }
 
 }  // namespace
@@ -298,45 +305,45 @@ bool conv_step_fits(bool bf16, int n, int D) { return grid_fits((int64_t)n * ste
 
 bool conv_fits(bool bf16, SeqMap seq, int D) {
   for (const bool back : {false, true}) {
-    const dim3 g = shape_of(seq, D, bf16, back).grid;
-    if (g.y > 65535 || !grid_fits((int64_t)g.x * g.y, THR)) return false;
+    const ConvPlan p = conv_plan(seq, D, bf16, back);
+    if (p.wide > 65535 || !grid_fits(p.blocks * p.wide, THR)) return false;
   }
   return true;
 }
 
 size_t conv_bwd_workspace(bool bf16, int taps, SeqMap seq, int D) {
-  return (size_t)shape_of(seq, D, bf16, true).grid.x * D * (taps + 1) * sizeof(float);
+  return (size_t)conv_plan(seq, D, bf16, true).blocks * D * (taps + 1) * sizeof(float);
 }
 
-#define FALCON_CONV(KERNEL, GRID, THREADS)                                                                             \
-  if (taps == 4 && bf16) hipLaunchKernelGGL((KERNEL<__bf16, 4>), GRID, dim3(THREADS), 0, s, a);                   \
-  else if (taps == 4) hipLaunchKernelGGL((KERNEL<float, 4>), GRID, dim3(THREADS), 0, s, a);                       \
-  else if (taps == 3 && bf16) hipLaunchKernelGGL((KERNEL<__bf16, 3>), GRID, dim3(THREADS), 0, s, a);              \
-  else if (taps == 3) hipLaunchKernelGGL((KERNEL<float, 3>), GRID, dim3(THREADS), 0, s, a);                       \
-  else if (taps == 2 && bf16) hipLaunchKernelGGL((KERNEL<__bf16, 2>), GRID, dim3(THREADS), 0, s, a);              \
-  else if (taps == 2) hipLaunchKernelGGL((KERNEL<float, 2>), GRID, dim3(THREADS), 0, s, a);                       \
+#define FALCON_CONV(PASS)                              \
+  if (taps == 4 && bf16) PASS<__bf16, 4>(p, a, s);     \
+  else if (taps == 4) PASS<float, 4>(p, a, s);         \
+  else if (taps == 3 && bf16) PASS<__bf16, 3>(p, a, s); \
+  else if (taps == 3) PASS<float, 3>(p, a, s);         \
+  else if (taps == 2 && bf16) PASS<__bf16, 2>(p, a, s); \
+  else if (taps == 2) PASS<float, 2>(p, a, s);         \
   else return hipErrorInvalidValue;
 
 hipError_t launch_conv_fwd(bool bf16, int taps, ConvArgs a, hipStream_t s) {
-  const Shape p = shape_of(a.seq, a.D, bf16, false);
+  const ConvPlan p = conv_plan(a.seq, a.D, bf16, false);
   a.run = p.run;
-  FALCON_CONV(conv_fwd, p.grid, THR)
+  FALCON_CONV(fwd)
   return hipGetLastError();
 }
 
 hipError_t launch_conv_bwd(bool bf16, int taps, ConvArgs a, float *dw, float *db, void *ws, hipStream_t s) {
-  const Shape p = shape_of(a.seq, a.D, bf16, true);
+  const ConvPlan p = conv_plan(a.seq, a.D, bf16, true);
   a.run = p.run;
   a.part = dw || db ? static_cast<float *>(ws) : nullptr;
-  FALCON_CONV(conv_bwd, p.grid, THR)
+  FALCON_CONV(bwd)
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.part) return e;
-  return launch_column_sum(a.part, p.grid.x, (int64_t)a.D * (taps + 1), dw, (int64_t)a.D * taps, db, s);
+  return launch_column_sum(a.part, (int)p.blocks, (int64_t)a.D * (taps + 1), dw, (int64_t)a.D * taps, db, s);
 }
 
 hipError_t launch_conv_step(bool bf16, int taps, ConvArgs a, hipStream_t s) {
-  const dim3 grid((unsigned)a.seq.n * step_blocks(a.D, bf16 ? 8 : 4));
-  FALCON_CONV(conv_step, grid, STEP_THR)
+  const ConvPlan p = {STEP_THR, 1, (int64_t)a.seq.n * step_blocks(a.D, bf16 ? 8 : 4), 1};
+  FALCON_CONV(step)
   return hipGetLastError();
 }
 #undef FALCON_CONV

@@ -28,21 +28,25 @@ struct SeqMap {
 };
 
 // ---- Short causal convolution ---------------------------------------------------------
-constexpr int CONV_THR = 256, CONV_LANES = 64, CONV_RUNS = CONV_THR / CONV_LANES;    // threads, lanes of a run, runs
-
-// A pass of the convolution: the tokens of a run, which is a wave's, and its workgroups.  Long runs read fewer tokens twice,
-// short ones make more workgroups (4 x 4096 x 1536 bf16, 24 and 33 us: 30 and 36 with runs half as long, 24 and 41 twice).
+// A pass's threads, its wave's lanes that lie side by side over channels, and the tokens of a run, which is those lanes'.
+// With all 64 of a wave, where a run stands is the same in all of them (4 x 4096 x 1536 bf16: 24 us, 25 with runs of 16
+// lanes, backward 33, 36 of 32; 13 packed sequences, 9001 x 2048: 22 and 29); but forward, where 16 hold all channels, the
+// others would idle (16 x 4096 x 64 bf16: 13.3 us, 23.3 with 64 lanes; x 128: 13.2, 18.4; x 256 13.4 both; backward, 32
+// lanes would save 2 of 23).  Long runs read fewer tokens twice, short ones make more workgroups (4 x 4096 x 1536 bf16, 24
+// and 33 us: 30 and 36 with runs half as long, 24 and 41 twice).
+constexpr int CONV_THR = 256, CONV_WIDE = 64, CONV_NARROW = 16;
 struct ConvPlan {
-  int run;
+  int lanes, run;
   int64_t blocks, wide;      // workgroups along time and channels
 };
 inline ConvPlan conv_plan(const SeqMap &seq, int D, bool bf16, bool back) {
-  const int cols = CONV_LANES * (bf16 && !back ? 8 : 4);
-  const int64_t wide = (D + cols - 1) / cols, tokens = seq.tokens();
-  const auto blocks = [&](int run) { return (tokens + run * CONV_RUNS - 1) / (run * CONV_RUNS); };
+  const int each = bf16 && !back ? 8 : 4;            // channels of a lane
+  const int lanes = !back && D <= CONV_NARROW * each ? CONV_NARROW : CONV_WIDE, runs = CONV_THR / lanes;
+  const int64_t wide = (D + lanes * each - 1) / (lanes * each), tokens = seq.tokens();
+  const auto blocks = [&](int run) { return (tokens + run * runs - 1) / (run * runs); };
   int run = back ? 32 : 16;
   while (run > 4 && blocks(run) * wide < 512) run /= 2;
-  return {run, blocks(run), wide};
+  return {lanes, run, blocks(run), wide};
 }
 
 // ---- Selective state-space scan ---------------------------------------------------------

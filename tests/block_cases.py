@@ -49,3 +49,7 @@ def scan_lens(name, N):
 # The convolution with runs of 16 tokens forward and 32 backward, borders of sequences inside them.
 CONV = [("bf16", 4, "silu", 4096, [777, 0, 1, 2, 3, 1500, 0, 5, 33, 1783]), ("fp32", 3, None, 4096, [2000, 1, 1, 4, 2099]),
         ("fp32", 2, "silu", 4096, [4104]), ("bf16", 3, "silu", 4096, [17] * 242)]
+
+# Forward with 16 lanes a run, of which a wave has four, where those hold all channels: runs of 8 tokens
+CONV_NARROW = [("bf16", 4, "silu", 128, [30000, 0, 1, 2, 3, 20000, 0, 5, 33, 19956]), ("fp32", 3, None, 64, [70000]),
+               ("bf16", 2, None, 8, [5] * 14000)]

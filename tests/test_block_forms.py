@@ -7,7 +7,7 @@ import subprocess
 
 import pytest
 
-from block_cases import BACKWARD, CONV, E, FORWARD, SCAN, scan_lens
+from block_cases import BACKWARD, CONV, CONV_NARROW, E, FORWARD, SCAN, scan_lens
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "recurrent_sequence_models_amd", "csrc")
 
@@ -37,7 +37,8 @@ int main() {
       printf("%s %d", ssm_few_fwd(q, seg, D) ? "few" : "many", ssm_segmented(q, seg) ? seg : 0);
     } else if (what == 'c' && scanf("%d %d %d %d", &n, &T, &D, &e) == 4) {
       const SeqMap q{&mark, n, T};
-      printf("%d %d", conv_plan(q, D, e == 2, false).run, conv_plan(q, D, e == 2, true).run);
+      const ConvPlan f = conv_plan(q, D, e == 2, false), b = conv_plan(q, D, e == 2, true);
+      printf("%d %d %d %d", f.lanes, f.run, b.lanes, b.run);
     } else return 1;
     printf("\n");
   }
@@ -94,4 +95,9 @@ def test_scans(ask, name, N):
 
 @pytest.mark.parametrize("dtype,taps,act,D,lens", CONV)
 def test_convolution_runs(ask, dtype, taps, act, D, lens):
-    assert ask("c", len(lens), sum(lens), D, E[dtype]) == ["16", "32"]
+    assert ask("c", len(lens), sum(lens), D, E[dtype]) == ["64", "16", "64", "32"]
+
+
+@pytest.mark.parametrize("dtype,taps,act,D,lens", CONV_NARROW)
+def test_narrow_convolution(ask, dtype, taps, act, D, lens):
+    assert ask("c", len(lens), sum(lens), D, E[dtype])[:2] == ["16", "8"]

@@ -8,7 +8,7 @@ import pytest
 import test_gpu_causal_conv as conv
 import test_gpu_linear as lin
 import test_gpu_selective_scan as scan
-from block_cases import BACKWARD, CONV, FORWARD, SCAN, scan_lens
+from block_cases import BACKWARD, CONV, CONV_NARROW, FORWARD, SCAN, scan_lens
 from block_helpers import TINY, U, check, f64, half, offsets, rand, strided
 from oracle import block as O
 
@@ -101,4 +101,9 @@ def test_scan_of_many_workgroups(name, N, dtype):
 
 @pytest.mark.parametrize("dtype,taps,act,D,lens", CONV)
 def test_longest_runs_of_the_convolution(dtype, taps, act, D, lens):
+    conv.both(conv.calls(act, view=dtype == "fp32"), dtype, lens, D, taps, act, init=True, view=dtype == "fp32")
+
+
+@pytest.mark.parametrize("dtype,taps,act,D,lens", CONV_NARROW)
+def test_narrow_convolution(dtype, taps, act, D, lens):
     conv.both(conv.calls(act, view=dtype == "fp32"), dtype, lens, D, taps, act, init=True, view=dtype == "fp32")
