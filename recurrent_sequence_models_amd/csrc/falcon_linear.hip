@@ -15,10 +15,12 @@
 // of what LDS gives at the unit's full rate, and the copies the rest), and the wait for copies that start one step
 // before their use; W's bytes for few tokens.  Measured, where a large library product reaches 1.2 to 1.34 PFLOP/s in
 // bf16 and 2.9 in e4m3:
-//   8192^3: bf16 850 us (1.29 PFLOP/s), e4m3 475 us (2.31)
-//   16384 x 2048 -> 4096 bf16, bias and silu: 244 us on one set of operands (1.13 PFLOP/s), 271 on three in turn
-//   16384 x 4096 -> 2048 e4m3, residual: 195 us (1.41 PFLOP/s); to fp32, widened: 316 us
-//   4096 x 2048 -> 2048 fp32: 280 us (123 TFLOP/s; a large fp32 product 146)
+//   8192^3: bf16 850 to 870 us (1.28 PFLOP/s), e4m3 448 to 460 (2.42)
+//   16384 x 2048 -> 4096 bf16, bias and silu: 244 to 270 us on one set of operands (1.07 PFLOP/s), 264 to 286 on three
+//   in turn (the card's clock under load)
+//   16384 x 4096 -> 2048 e4m3: 130 us on one set (2.1 PFLOP/s); with residual, on three in turn 200 (1.37), to fp32 306; to
+//   fp32, widened, on one set 228
+//   4096 x 2048 -> 2048 fp32: 242 us (142 TFLOP/s; a large fp32 product 146)
 //   512 x 2048 -> 2048 bf16: 15 us (a library product 12)
 //   16 x 2048 -> 4096 bf16: 7 us (16.8 MB at 2.4 TB/s: one wave's loads and the launch)
 // Sums are fp32; a result is rounded once, at its end.
@@ -493,8 +495,11 @@ template <typename T, typename O, int MT> __global__ __launch_bounds__(64 * FEW_
 
 // ---- The gradient of the pre-activation ------------------------------------------------
 // d = dy act'(pre), rounded to the operands' type as the products take it, and the sums over tokens of the
-// unrounded d for the bias (pre is kept in fp32: rounded to bf16 it would leave 0.2 % in that sum).  Thread: 16 bytes of
-// columns, every 16th token of a workgroup's run.
+// unrounded d for the bias (pre is kept in fp32: rounded to bf16 it would leave 0.2 % in that sum).  What bf16 drops of d
+// would take a second product of dx and dW each, of the remainder: 96 of linear training's 220 us once more (16384 x 768 ->
+// 1536).  It is rounded to nearest, so it has no sign of its own that a sum over tokens or outputs would collect, and is
+// as large as the rounding of dx and dW themselves: 0.23 % of the norm off in all, 0.17 % by that alone.  Thread: 16 bytes
+// of columns, every 16th token of a workgroup's run.
 constexpr int DP_LANES = 16, DP_ROWS = 256 / DP_LANES, DP_RUN = 128;
 template <typename T> __global__ __launch_bounds__(256) void pre_gradient(LinearArgs a, const void *dy, int64_t lddy, void *d) {
   constexpr int E = PER16<T>;

@@ -14,9 +14,10 @@
 // Few long sequences: they are cut into segments, whose maps a pass of its own forms, and which then
 // run in parallel.
 //
-// Bound: the vector unit: 41 instructions for 4 states and a step, with what a tile's loading, softplus, gate and joins
-// cost; busy 78 % of the time.  Measured, N = 16, bf16: 8 x 2048 x 1536 163 us (2.5e12 states a second; the bytes alone
-// would take 41 us); single tokens, 64 x 4096: 9 us (36 MB at 4.0 TB/s).
+// Bound: the vector unit: 44 instructions (49 issue slots) for 4 states and a step, with what a tile's loading, softplus,
+// gate and joins cost; busy 91 % of the time.  Measured, bf16: 8 x 2048 x 1536, N = 16: 146 us among other work (2.8e12
+// states a second; the bytes alone would take 43 us), 160 in a row, where the card's clock is lower; 8 x 2048 x 768, N = 32:
+// 217, 64: 347; single tokens, 64 x 4096: 9 us (36 MB at 4.0 TB/s).
 #include "ssm_common.h"
 
 namespace falcon {

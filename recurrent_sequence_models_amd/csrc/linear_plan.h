@@ -24,16 +24,16 @@ inline int splits_of(int64_t tiles, int64_t groups, int64_t steps) {
 }
 
 // A compute unit holds one workgroup of 256 x 256 or two of 128 x 128; the larger tile reads less from LDS for a product
-// (16384 x 2048 -> 4096 bf16: 287 us, 299 with the smaller; 16384 x 4096 -> 2048 e4m3: 195, 227), the smaller one
-// leaves less of the last round empty (16384 x 768 -> 1536 bf16: 54.7 us, 58.7 with the larger; 2048 x 2048 -> 2048:
-// 29, 51).  So rounds are counted, in tiles of 128 x 128 a compute unit.  fp32 takes too many registers for the larger.
+// (16384 x 2048 -> 4096 bf16: 287 us, 306 with the smaller; 16384 x 4096 -> 2048 e4m3 is level, 200 and 196), the smaller
+// one leaves less of the last round empty (16384 x 768 -> 1536 bf16: 55 us, 62 with the larger; 2048 x 2048 -> 2048:
+// 28, 53).  So rounds are counted, in tiles of 128 x 128 a compute unit.  fp32 takes too many registers for the larger.
 // Where 128 x 128 tiles leave compute units idle, tiles are 64 x 64, and k is split where those do too: 512 x 2048 -> 2048
-// bf16 15.5 us, 20 in four parts of 128 x 128; 100 x 2048 -> 4096 13.5, 16.  Not over more than 48 steps a
-// workgroup: 512 x 8192 -> 2048 44.6 us, 31.8 in eight parts of 128 x 128; those for two workgroups a compute unit where
-// each has 16 steps and more (768 x 16384 -> 1536: 183 us with the rest of its backward pass, 192 for one; 100 x 8192 ->
-// 4096: 24.0 and 22.3).  One workgroup of 128 x 128 a compute unit has LDS for four steps, three of them on their way,
-// and 8 waves (2048 x 2048 -> 2048: 25 us, 28 with 4 waves, 31 with two steps; 33 as 64 x 64; training 2048 x 2048 -> 2048:
-// 80 and 91).
+// bf16 15 us, 20 in four parts of 128 x 128; 100 x 2048 -> 4096 13.5, 16.  Not over more than 48 steps a
+// workgroup: 512 x 8192 -> 2048 45 us, 32 in eight parts of 128 x 128; those for two workgroups a compute unit where
+// each has 16 steps and more, which is level with one (768 x 16384 -> 1536, training: 161 to 170 us, 159 for one; 1000 x
+// 16384 -> 512: 32.5 and 30.5; 100 x 8192 -> 4096: 22.4 and 22.9).  One workgroup of 128 x 128 a compute unit has LDS for
+// four steps, three of them on their way, and 8 waves (2048 x 2048 -> 2048: 25 us, 28 with two steps, 34 as 64 x 64;
+// training 2048 x 2048 -> 2048: 84 and 90).
 inline Plan tiles_of(int64_t I, int64_t J, int64_t K, int e) {
   const int64_t large = over(I, 256) * over(J, 256), medium = over(I, 128) * over(J, 128), small = over(I, 64) * over(J, 64);
   if (e < 4 && large >= 256 && over(large, 256) * 4 * 20 <= over(medium, 512) * 2 * 21) return {Form::large, 1, large};
@@ -54,7 +54,7 @@ inline int64_t rounds_of(const Plan &p) {
 // Few tokens take what a compute unit loads, at about 40 KB a us: 16 rows of W and the tokens (a multiple of 16) for each
 // of its workgroups of `few`, or both operands of its tiles' steps (which fp32 products hold up by a quarter, by
 // three halves in the larger tiles) and about 64 KB for the tile's beginning and the join.  16 x 2048 -> 4096 bf16: 7.5 us,
-// 9.6 in tiles; 16 x 8192 -> 2048: 17.6 and 12.1; 64 x 4096 -> 8192: 38.5 and 17.8; 24 x 4096 -> 8192 fp32: 47 and 72.
+// 9.6 in tiles; 16 x 8192 -> 2048: 17.1 and 12.7; 64 x 4096 -> 8192: 38.5 and 18; 24 x 4096 -> 8192 fp32: 47 and 50.
 inline Plan plan_of(int64_t I, int64_t J, int64_t K, int e) {
   const Plan p = tiles_of(I, J, K, e);
   if (J > FEW_TOKENS) return p;
@@ -67,7 +67,7 @@ inline Plan plan_of(int64_t I, int64_t J, int64_t K, int e) {
 }
 
 // Tokens that a pass of their own takes: up to 64 behind the last whole tile of 256, where that saves the others a
-// round (16387 x 4096 -> 2048 e4m3: 257 us as one pass).
+// round (16387 x 4096 -> 2048 e4m3: 203 us, 257 as one pass).
 inline int tokens_apart(int64_t I, int64_t J, int64_t K, int e) {
   const int rest = (int)(J % 256);
   if (!rest || rest > FEW_TOKENS || J < 512 || K < 512) return 0;

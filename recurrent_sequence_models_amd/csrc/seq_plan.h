@@ -80,15 +80,18 @@ inline int ssm_segment(const SeqMap &q, int D, int channels, int enough, int wan
 inline bool ssm_segmented(const SeqMap &q, int seg) { return q.T > seg; }
 
 constexpr int SSM_FWD_CH = 16;      // channels of a workgroup
-// Below this many workgroups, 8 waves of 8 steps each take a tile's 64 steps, instead of 4 of 16: more waves for what
-// there is, at twice the joins.  N = 16, bf16: 384 workgroups (4 x 4096 x 1536) 220 us, 257 with 4 waves; 512 (4 x 2048 x
-// 2048) 114 and 118; 768 (8 x 2048 x 1536) 186 and 163.
+// Below this many workgroups, 128 / N waves lie behind each other in time (of 8 steps each; N = 64: 16) instead of 64 / N
+// of 16 steps: more waves for what there is, at twice the joins.  bf16, N = 16, 32, 64: 384 workgroups (4 x 2048 x 1536)
+// 105, 209 and 341 us, 112, 225 and 359 with half the waves; 512 (4 x 2048 x 2048) 110, 221 and 349 us, 114, 226 and 378;
+// 768 (8 x 2048 x 1536) 165, 358 and 552 us, 146, 270 and 450.
 constexpr int SSM_FEW_GROUPS = 640;
 inline bool ssm_few_fwd(const SeqMap &q, int seg, int D) {
   return (int64_t)((D + SSM_FWD_CH - 1) / SSM_FWD_CH) * slots_of(q, seg) < SSM_FEW_GROUPS;
 }
-// Sequences are cut where they make fewer than 256 workgroups, into 768 (1 x 16384 x 1536, 96 workgroups: 267 us with
-// the maps' pass, 311 cut for 512, 460 for 256); with 384 they are not (4 x 4096 x 1536: 220 us, 260 cut).
+// Sequences are cut where they make fewer than 256 workgroups, into 768 (1 x 16384 x 1536, 96 workgroups: 237 us with
+// the maps' pass, 294 cut for 512, 386 for 256); with 384 they are not (4 x 4096 x 1536: 216 us, 218 cut).  Packed ones are
+// where the total would be, as the host does not see the offsets: 100 sequences, 5000 x 1536: 128 us, 95 uncut; with the
+// backward pass 517, of which its own cut is 42.
 // Up to 4096 / N tokens they are left whole (1 x 192 x 512: 10.3 us, 12.8 cut; 320: 14.6 and 13.0; N = 64: 128 18.1 and 19.3,
 // 192 25.3 and 19.4).
 inline int ssm_segment_fwd(const SeqMap &q, int D, int N) { return ssm_segment(q, D, SSM_FWD_CH, 256, 768, 4096 / N); }
