@@ -11,6 +11,8 @@
 
 namespace falcon {
 
+inline size_t align16(size_t n) { return (n + 15) / 16 * 16; }
+
 // out[c] = sum over i < rows of part[i][c], c < cols, in a fixed order; columns from `split` on go to
 // out2[c - split].  Either output may be null.
 hipError_t launch_column_sum(const float *part, int rows, int64_t cols, float *out, int64_t split, float *out2,

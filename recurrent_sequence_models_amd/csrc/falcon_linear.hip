@@ -592,7 +592,6 @@ template <typename T, typename O> hipError_t fwd(LinearArgs a, void *ws, hipStre
   return pass();
 }
 
-size_t align16(size_t n) { return (n + 15) / 16 * 16; }
 size_t part_bytes(const Plan &p, int64_t I, int64_t J) { return p.splits > 1 ? (size_t)p.splits * I * J * sizeof(float) : 0; }
 size_t sum_blocks(int64_t J) { return (size_t)((J + DP_RUN - 1) / DP_RUN); }
 

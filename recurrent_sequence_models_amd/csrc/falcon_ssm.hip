@@ -162,7 +162,7 @@ __global__ __launch_bounds__((SsmTile<N, SSM_FWD_CH, TW, STEPS>::THR), (STEPS ==
           y[j] = fmaf(skip[j], x[j], step[ls][lc + j].x);
           if (a.z) y[j] *= z[j] * sigmoid(z[j]);
         }
-        store_few<V>(entry<T>(a.y, a.D, t, ls, lcc), y);
+        put(entry<T>(a.y, a.D, t, ls, lcc), y);
       }
     }
   }
@@ -218,12 +218,13 @@ template <typename T, int N> __global__ __launch_bounds__(STEP_THR) void ssm_ste
   const size_t at = (size_t)row * N + p4;
   const f4 h0 = *reinterpret_cast<const f4 *>(a.init + at);
   const f4 A = *reinterpret_cast<const f4 *>(a.A + (size_t)c * N + p4);
-  float B[4], C[4], x[1], dt[1], z[1] = {0.f};
-  load_few<4>(static_cast<const T *>(a.B) + (int64_t)n * a.ldB + p4, B);
-  load_few<4>(static_cast<const T *>(a.C) + (int64_t)n * a.ldC + p4, C);
-  load_few<1>(static_cast<const T *>(a.x) + (int64_t)n * a.ldx + c, x);
-  load_few<1>(static_cast<const T *>(a.dt) + (int64_t)n * a.lddt + c, dt);
-  if (a.z) load_few<1>(static_cast<const T *>(a.z) + (int64_t)n * a.ldz + c, z);
+  Few<T, 4> B, C;
+  Few<T, 1> x, dt, z{};
+  fetch(static_cast<const T *>(a.B) + (int64_t)n * a.ldB + p4, B);
+  fetch(static_cast<const T *>(a.C) + (int64_t)n * a.ldC + p4, C);
+  fetch(static_cast<const T *>(a.x) + (int64_t)n * a.ldx + c, x);
+  fetch(static_cast<const T *>(a.dt) + (int64_t)n * a.lddt + c, dt);
+  if (a.z) fetch(static_cast<const T *>(a.z) + (int64_t)n * a.ldz + c, z);
   float d = dt[0] + (a.bias ? a.bias[c] : 0.f);
   if (a.softplus) d = softplus(d);
   f4 h;
@@ -241,8 +242,6 @@ template <typename T, int N> __global__ __launch_bounds__(STEP_THR) void ssm_ste
   if (a.z) y *= z[0] * sigmoid(z[0]);
   static_cast<T *>(a.y)[row] = (T)y;
 }
-
-size_t align16(size_t n) { return (n + 15) / 16 * 16; }
 
 }  // namespace
 

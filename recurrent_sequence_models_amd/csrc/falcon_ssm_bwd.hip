@@ -267,9 +267,9 @@ template <typename T, int N, bool MAPS> __global__ __launch_bounds__(BwdTile<N>:
           dbias[j] += ddt[j];
           if (a.z) dz[j] = gz[j] * fmaf(sk, xv, sum[2]);
         }
-        store_few<V>(entry<T>(a.dx, a.lddx, t, ls, lcc), dx);
-        store_few<V>(entry<T>(a.ddt, a.ldddt, t, ls, lcc), ddt);
-        if (a.z) store_few<V>(entry<T>(a.dz, a.lddz, t, ls, lcc), dz);
+        put(entry<T>(a.dx, a.lddx, t, ls, lcc), dx);
+        put(entry<T>(a.ddt, a.ldddt, t, ls, lcc), ddt);
+        if (a.z) put(entry<T>(a.dz, a.lddz, t, ls, lcc), dz);
       }
       float *out = a.part_bc + ((size_t)group * tokens + t) * (2 * N);
 #pragma unroll
@@ -355,11 +355,9 @@ template <typename T, int N> __global__ __launch_bounds__(256) void ssm_sum_bc(S
 #pragma unroll 4
   for (int k = 0; k < groups; ++k) s += *reinterpret_cast<const f4 *>(a.part_bc + (size_t)k * tokens * (2 * N) + i);
   const float v[4] = {s[0], s[1], s[2], s[3]};
-  if (n < N) store_few<4>(static_cast<T *>(a.dB) + t * a.lddB + n, v);
-  else store_few<4>(static_cast<T *>(a.dC) + t * a.lddC + n - N, v);
+  if (n < N) put(static_cast<T *>(a.dB) + t * a.lddB + n, v);
+  else put(static_cast<T *>(a.dC) + t * a.lddC + n - N, v);
 }
-
-size_t align16(size_t n) { return (n + 15) / 16 * 16; }
 
 struct Parts { size_t bc, A, D, map, sum, total; };
 Parts parts_of(const SeqMap &q, int D, int N) {

@@ -82,6 +82,12 @@ __device__ __forceinline__ void put(float *p, const float (&v)[4]) { store16(p, 
 __device__ __forceinline__ void put(__bf16 *p, const float (&v)[4]) {
   *reinterpret_cast<bf4 *>(p) = __builtin_convertvector(f4{v[0], v[1], v[2], v[3]}, bf4);
 }
+__device__ __forceinline__ void put(float *p, const float (&v)[2]) { *reinterpret_cast<float2 *>(p) = float2{v[0], v[1]}; }
+__device__ __forceinline__ void put(__bf16 *p, const float (&v)[2]) {
+  typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+  *reinterpret_cast<bf2 *>(p) = bf2{(__bf16)v[0], (__bf16)v[1]};
+}
+template <typename T> __device__ __forceinline__ void put(T *p, const float (&v)[1]) { *p = (T)v[0]; }
 
 // Sum over the 64 lanes of a wave, in each of them.
 __device__ __forceinline__ float wave_sum(float x) { return add_xor32(add_xor16(lane_sum<16>(x))); }

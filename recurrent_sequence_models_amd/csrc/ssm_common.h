@@ -24,22 +24,6 @@ template <int N, int CH_, int TW_, int STEPS_> struct SsmTile {
 // steps between the states that the forward keeps
 template <int N> constexpr int SSM_CHUNK = 1024 / N;
 
-// V consecutive entries as floats; the address is a multiple of their size together.
-template <int V> __device__ __forceinline__ void load_few(const float *p, float (&o)[V]) {
-  if constexpr (V == 4) { const f4 v = *reinterpret_cast<const f4 *>(p); o[0] = v[0]; o[1] = v[1]; o[2] = v[2]; o[3] = v[3]; }
-  else if constexpr (V == 2) { const float2 v = *reinterpret_cast<const float2 *>(p); o[0] = v.x; o[1] = v.y; }
-  else o[0] = *p;
-}
-template <int V> __device__ __forceinline__ void load_few(const __bf16 *p, float (&o)[V]) {
-  if constexpr (V == 4) {
-    const uint2 v = *reinterpret_cast<const uint2 *>(p);
-    o[0] = __uint_as_float(v.x << 16); o[1] = __uint_as_float(v.x & 0xffff0000u);
-    o[2] = __uint_as_float(v.y << 16); o[3] = __uint_as_float(v.y & 0xffff0000u);
-  } else if constexpr (V == 2) {
-    const unsigned v = *reinterpret_cast<const unsigned *>(p);
-    o[0] = __uint_as_float(v << 16); o[1] = __uint_as_float(v & 0xffff0000u);
-  } else o[0] = (float)*p;
-}
 // Entries `col` on of token t + row of an array, as scalar base plus 32 bits a lane: t is the same in every lane, and
 // token strides are at most 2^24 bytes.
 template <typename T> __device__ __forceinline__ const T *entry(const void *p, int64_t ld, int t, int row, int col) {
@@ -49,20 +33,6 @@ template <typename T> __device__ __forceinline__ const T *entry(const void *p, i
 template <typename T> __device__ __forceinline__ T *entry(void *p, int64_t ld, int t, int row, int col) {
   char *base = static_cast<char *>(p) + (int64_t)t * ld * (int64_t)sizeof(T);
   return reinterpret_cast<T *>(base + (unsigned)(row * ((int)ld * (int)sizeof(T)) + col * (int)sizeof(T)));
-}
-
-template <int V> __device__ __forceinline__ void store_few(float *p, const float (&v)[V]) {
-  if constexpr (V == 4) *reinterpret_cast<f4 *>(p) = f4{v[0], v[1], v[2], v[3]};
-  else if constexpr (V == 2) *reinterpret_cast<float2 *>(p) = float2{v[0], v[1]};
-  else *p = v[0];
-}
-// rounded to nearest even: the one rounding of a result held in bf16
-template <int V> __device__ __forceinline__ void store_few(__bf16 *p, const float (&v)[V]) {
-  if constexpr (V == 4) *reinterpret_cast<bf4 *>(p) = __builtin_convertvector(f4{v[0], v[1], v[2], v[3]}, bf4);
-  else if constexpr (V == 2) {
-    typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
-    *reinterpret_cast<bf2 *>(p) = bf2{(__bf16)v[0], (__bf16)v[1]};
-  } else *p = (__bf16)v[0];
 }
 
 // softplus(v) = max(v, 0) + ln(1 + e), e = e^-|v| in (0, 1]; ln(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3, and
