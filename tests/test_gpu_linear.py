@@ -5,7 +5,7 @@ Bounds, with u = 2^-24: a sum of K products is off by (K + 32) u of the sum of a
 bias add 4 u; the activations' slopes are at most 1.13 and their second derivatives at most 1; silu is off by
 (2 |p| + 10) u |y| more, gelu by 8 u |p| (1 + erf cancels); results are rounded once (half).  In the backward
 pass the products of bf16 take d rounded once (half).  The 8-bit products of the matrix unit, used for
-bf16 results (not always for up to 64 tokens), drop what lies 13 bits behind the largest product of a
+bf16 results (not always for up to 64 tokens, nor with a kept pre-activation), drop what lies 13 bits behind the largest product of a
 group: up to 2^-13 of the largest product of the row pair for each of K."""
 
 import numpy as np
@@ -19,7 +19,7 @@ pytestmark = pytest.mark.gpu
 # few tokens (1 to 64: 1, 2 and 4 blocks of 16, or tiles), tiles of 64 with k split and not, of 128; ragged in each direction
 SIZES = [(1, 16, 8), (7, 48, 24), (16, 2048, 72), (17, 176, 200), (33, 4096, 136), (64, 80, 1000), (65, 16, 8), (100, 1040, 40),
          (129, 2048, 264), (500, 64, 640), (3000, 208, 1288)]
-BIG = (4100, 144, 4000)      # 17 x 16 tiles of 256
+BIG = (4100, 144, 4000)      # 33 x 32 tiles of 128, two a compute unit; 4096 tokens on 4096 make 16 x 16 of 256
 # 256 tiles of 128; 32 and 64 of them with k in 8 parts; one in 16 (longer rows than quantize_rows takes)
 MIDDLE, LONG = [(2040, 272, 2040), (1000, 16384, 512), (1000, 8208, 1016)], (70, 100384, 72)
 # the same for dx, for dweight, and for dweight in parts
