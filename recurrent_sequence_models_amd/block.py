@@ -3,7 +3,8 @@ the residual stream with its output in 8 bits, the projections with their epilog
 short causal convolution, and the selective state-space scan.
 
 Argument marshalling only, as layer.py, whose conventions of devices, streams and
-workspaces hold here.
+workspaces hold here.  A tensor given for an output is none of the inputs or other outputs,
+unless the function's text says so (FALCON_ERR_INVALID_ARG where it would be a race).
 """
 
 from __future__ import annotations
@@ -456,7 +457,8 @@ def linear(x, weight, *, bias=None, activation=None, residual=None, x_scale=None
     ``activation``: None, "silu" or "gelu".  Or both float8_e4m3fn, with ``x_scale`` [...] and
     ``weight_scale`` [out] float32 (as ``rms_norm(..., quantize=True)`` and ``quantize_rows``
     give them) and ``out_dtype`` bfloat16 (default) or float32.  ``pre``: whether to return the
-    activation's argument [...,out] float32, which linear_bwd needs with an activation.  ``out``: None or a tensor
+    activation's argument [...,out] float32, which linear_bwd needs with an activation (8-bit
+    operands are then multiplied as bfloat16, for the fp32 sum).  ``out``: None or a tensor
     for y, which may be the residual.  Returns (y, pre)."""
     import torch
     shape, need, _, lead, odt, f8, dev = _linear_shape(x, weight, activation, out_dtype)
